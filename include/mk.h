@@ -396,6 +396,169 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
                 int cap_tasks, int32_t* sm_off_out, int32_t* sm_list_out, int cap_list,
                 int32_t* info_out);
 
+/* ==================================================================== operators
+ * Operators over several tokens of each sequence, for programs that verify drafted tokens
+ * or run prompt chunks on the cache that mk_decode_step reads: append the new nodes' keys
+ * and values (mk_qk_norm_rope), attend over the cache and the draft tree
+ * (mk_tree_attention), multiply by the routed experts' matrices (mk_expert_product), then
+ * keep the accepted path (mk_commit_nodes); mk_copy_pages copies pages for a fork.  The
+ * pages have no counterpart to them.  They need no handle and read plain (unpacked) bf16
+ * tensors.
+ *
+ * Conventions beside the ones above:
+ *   - Every pointer is a device address on the current device unless it is called a HOST
+ *     pointer.  Calls are asynchronous on `stream`, allocate nothing, synchronise nothing
+ *     and can be captured into a CUDA graph (its replays use the pointers, sizes and host
+ *     arrays of the call).
+ *   - A node is a new token of a sequence: node i of sequence b owns cache position
+ *     seq_lens[b] + i, whatever its depth in the tree.  counts[b] (NULL = n_nodes for
+ *     all) is the number of nodes of sequence b; rows of later nodes are neither read nor
+ *     written.
+ *   - status: int32[4], zeroed by the caller, or NULL (not recorded).  The first invalid
+ *     value that a kernel finds in device data is recorded there as {mk_status code,
+ *     sequence or expert, index, value}.  Invalid entries are skipped or clamped, never
+ *     followed out of bounds; the outputs of such a call are not valid.
+ *   - mk_last_error(NULL) gives the message of a refused call.
+ */
+
+/* One layer's K/V pools and the batch's page table.
+ *   k, v        bf16 [n_pages][n_kv_heads][16][head_dim], 16-byte aligned
+ *   page_table  int32[batch][max_pages]: physical page of logical page j; entries that
+ *               no position of the call falls into are not read
+ *   seq_lens    int32[batch] cached tokens; seq_lens + counts <= 16 * max_pages, else
+ *               MK_ERR_INVALID is recorded and the sequence is left out
+ * head_dim in {32, 64, 128}; batch in 1..128. */
+typedef struct mk_paged_kv {
+  void* k;
+  void* v;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  int32_t n_pages, n_kv_heads, head_dim, batch, max_pages;
+} mk_paged_kv;
+
+/* Norm of every query and key head, position rotation, and the append of the new keys and
+ * values to the cache, in one pass:
+ *   x' = R(p) (gain * x / sqrt(mean(x^2) + eps))   over each head of q and k,
+ *   R(p) rotates the pairs (i, i + head_dim/2) by p * theta^(-2i / head_dim),
+ *   p = positions[b][i], or seq_lens[b] + i when positions is NULL;
+ * a NULL gain leaves that norm out (the models of mk_create have none).  q' goes to q_out
+ * (which may be q itself, with q's strides), k' and v into the nodes' cache slots.  fp32
+ * inside (the angle in 64-bit fixed point), rounded once.
+ *   q, q_out  bf16 [batch][n_nodes][n_q_heads][head_dim]; k, v [..][n_kv_heads][..]; strides
+ *             in elements of the first three dimensions, multiples of 8; pointers 16-byte
+ *             aligned; the last dimension is contiguous
+ *   q_gain, k_gain  bf16 [head_dim] or NULL
+ *   positions int32[batch][n_nodes] or NULL; any value
+ * n_q_heads a multiple of n_kv_heads.  The pages of the nodes' slots belong to one
+ * sequence each.  A slot on a page outside [0, n_pages) is not written
+ * (MK_ERR_BAD_PAGE). */
+typedef struct mk_rope_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];
+  const void* q_gain;
+  const void* k_gain;
+  const int32_t* positions;
+  const int32_t* counts;
+  int32_t* status;
+  int32_t n_nodes, n_q_heads;
+  float eps;
+  double theta;
+} mk_rope_args;
+int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* stream);
+
+/* Attention of the nodes over the cache and one another (grouped heads: query head h reads
+ * KV head h / (n_q_heads / n_kv_heads)):
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j
+ * over the cached positions j < seq_len and the nodes that node i sees, whose K/V are
+ * already in their slots.
+ *   mask       int32 [batch][n_nodes][ceil(n_nodes / 32)]: bit a % 32 of word a / 32 of
+ *              row i = node i sees node a (itself too, if it is to); NULL = node i sees
+ *              the nodes 0..i (a prompt chunk; one node = a decode step)
+ *   window     > 0: only keys whose position is greater than p_i - window are seen;
+ *              cached key j has position j, node a the position positions[b][a] (NULL =
+ *              seq_lens[b] + a).  Positions are clamped to [seq_len, seq_len + counts - 1],
+ *              where a node's depth always lies; they matter only with a window.
+ *   q, out     bf16 [batch][n_nodes][n_q_heads][head_dim], strides in elements (multiples
+ *              of 8), 16-byte aligned, last dimension contiguous
+ *   scale      finite and >= 0
+ *   workspace  mk_tree_attention_workspace(..) bytes, 16-byte aligned, not shared with a
+ *              call that may run at the same time; its contents do not matter
+ * A row that sees no key (or only scores of -infinity) is 0.  Keys that a row does not see
+ * do not reach it whatever they hold, NaN and infinities included.  fp32 scores, softmax
+ * statistics and sums; the softmax weights are rounded to bf16 for the tensor cores.  The
+ * sums have a fixed order: equal calls give equal bits.  n_q_heads / n_kv_heads <= 128.
+ * Keys on a page outside [0, n_pages) are read from page 0 (MK_ERR_BAD_PAGE). */
+typedef struct mk_tree_args {
+  const void* q;
+  void* out;
+  int64_t q_stride[3], out_stride[3];
+  const int32_t* mask;
+  const int32_t* positions;
+  const int32_t* counts;
+  int32_t* status;
+  int32_t n_nodes, n_q_heads, window;
+  float scale;
+  void* workspace;
+  size_t workspace_bytes;
+} mk_tree_args;
+int mk_tree_attention(const mk_paged_kv* cache, const mk_tree_args* args, void* stream);
+/* Bytes of workspace that mk_tree_attention needs for these sizes on the current device
+ * (the pointers are not looked at). */
+int mk_tree_attention_workspace(const mk_paged_kv* cache, const mk_tree_args* args, size_t* bytes);
+
+/* Copy whole pages in every layer: page src[i] -> page dst[i] of k_cache and v_cache, bf16
+ * [n_layers][n_pages][n_kv_heads][16][head_dim], 16-byte aligned.  src and dst are HOST
+ * arrays, read before the call returns.  A page may be copied to several places; no page is
+ * written twice and none that is written is also read (MK_ERR_INVALID, nothing is copied),
+ * so that the order of the copies does not matter.  For the copy-on-write of a fork's last
+ * page, or to move a sequence's pages. */
+int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n_kv_heads, int head_dim,
+                  const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Keep the accepted path of a draft tree: the K/V of node accepted[b][i], at position
+ * seq_lens[b] + accepted[b][i], move to position seq_lens[b] + i in every layer, and
+ * new_lens[b] = seq_lens[b] + the number of accepted nodes (its nodes end at the first
+ * negative entry).  Every node is read before any slot of its sequence is written, so the
+ * nodes may be in any order.
+ *   cache      k, v are the whole pools [n_layers][n_pages][..]
+ *   accepted   int32[batch][max_accept], max_accept in 1..512
+ *   new_lens   int32[batch], not seq_lens itself
+ * A sequence with an entry whose slot lies beyond its page table (MK_ERR_INVALID) or on a
+ * page outside [0, n_pages) (MK_ERR_BAD_PAGE) is left as it was.  The pages that the nodes
+ * lie on belong to one sequence each. */
+int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accepted, int max_accept,
+                    int32_t* new_lens, int32_t* status, void* stream);
+
+/* Matrix products grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of `out` belong
+ * to expert e,
+ *   out[r] = x[s] W_e^T                                  s = rows[r], or r if rows is NULL
+ *   out[r] = silu(x[s] W_e^T) * (x[s] U_e^T)             when w_up (U) is given
+ * with silu(y) = y / (1 + exp(-y)).
+ *   x        bf16 [n_x][k], row stride x_stride elements (a multiple of 8)
+ *   w, w_up  bf16 [n_experts][n][k] contiguous; k a multiple of 8
+ *   offsets  int32[n_experts + 1], ascending, within [0, n_rows]; rows of `out` outside
+ *            [offsets[0], offsets[n_experts]) are not written
+ *   rows     int32[n_rows] in [0, n_x) or NULL (then n_x >= n_rows)
+ *   out      bf16 [n_rows][n], row stride out_stride elements
+ * x, w, w_up 16-byte aligned; n_experts in 1..256.  fp32 accumulation, one rounding.
+ * Offsets that descend or leave [0, n_rows] and rows outside [0, n_x) are clamped
+ * (MK_ERR_INVALID). */
+typedef struct mk_expert_args {
+  const void* x;
+  const void* w;
+  const void* w_up;
+  const int32_t* offsets;
+  const int32_t* rows;
+  void* out;
+  int32_t* status;
+  int64_t x_stride, out_stride;
+  int32_t n_x, n_rows, n_experts, n, k;
+} mk_expert_args;
+int mk_expert_product(const mk_expert_args* args, void* stream);
+
 /* Message for the last failing call on h (or the last global failure if h is
  * NULL).  The string is owned by the library. */
 const char* mk_last_error(mk_handle* h);

@@ -33,7 +33,9 @@ MK_EXPERT_BF16, MK_EXPERT_FP8, MK_WEIGHTS_FP8 = 0, 1, 2
 EXPORTS = ["mk_create", "mk_plan", "mk_decode_step", "mk_decode_steps", "mk_decode_step_host", "mk_decode_step_noalloc",
            "mk_decode_step_perop", "mk_get_status", "mk_set_fixed", "mk_set_deterministic", "mk_set_inspect", "mk_set_trace",
            "mk_plan_drop_signal", "mk_read", "mk_read_expert_fp8", "mk_read_weight_fp8", "mk_query",
-           "mk_plan_dry", "mk_last_error", "mk_destroy", "mk_version"]
+           "mk_plan_dry", "mk_last_error", "mk_destroy", "mk_version",
+           "mk_qk_norm_rope", "mk_tree_attention", "mk_tree_attention_workspace", "mk_copy_pages", "mk_commit_nodes",
+           "mk_expert_product"]
 
 
 class MkError(RuntimeError):
@@ -67,6 +69,39 @@ class mk_weights(ctypes.Structure):
 class mk_error_info(ctypes.Structure):
     _fields_ = [("code", ctypes.c_int32), ("task", ctypes.c_int32), ("counter", ctypes.c_int32),
                 ("observed", ctypes.c_int32), ("target", ctypes.c_int32), ("sm", ctypes.c_int32)]
+
+
+class mk_paged_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+_S3 = ctypes.c_int64 * 3
+
+
+class mk_rope_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", _S3), ("k_stride", _S3), ("v_stride", _S3), ("out_stride", _S3),
+                ("q_gain", ctypes.c_void_p), ("k_gain", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("status", ctypes.c_void_p), ("n_nodes", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("eps", ctypes.c_float), ("theta", ctypes.c_double)]
+
+
+class mk_tree_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_stride", _S3), ("out_stride", _S3),
+                ("mask", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("n_nodes", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class mk_expert_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("n_x", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32)]
 
 
 _lib = None
@@ -107,6 +142,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mk_destroy.argtypes = [H]
     lib.mk_destroy.restype = None
     lib.mk_version.argtypes = []
+    kv = ctypes.POINTER(mk_paged_kv)
+    lib.mk_qk_norm_rope.argtypes = [kv, ctypes.POINTER(mk_rope_args), vp]
+    lib.mk_tree_attention.argtypes = [kv, ctypes.POINTER(mk_tree_args), vp]
+    lib.mk_tree_attention_workspace.argtypes = [kv, ctypes.POINTER(mk_tree_args), ctypes.POINTER(sz)]
+    lib.mk_copy_pages.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
+    lib.mk_commit_nodes.argtypes = [kv, i32, vp, i32, vp, vp, vp]
+    lib.mk_expert_product.argtypes = [ctypes.POINTER(mk_expert_args), vp]
     for name in EXPORTS:
         if name not in ("mk_last_error", "mk_destroy"):
             getattr(lib, name).restype = ctypes.c_int

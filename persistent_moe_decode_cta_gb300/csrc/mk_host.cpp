@@ -25,6 +25,7 @@
 
 #include "mk.h"
 #include "mk_internal.h"
+#include "mk_ops.h"
 
 namespace mk {
 cudaError_t launch_pack(uint8_t* dst, const void* src_a, const void* src_b, const void* src_c,
@@ -627,6 +628,20 @@ int alloc(mk_handle* h, T** p, size_t count) {
   return MK_OK;
 }
 
+}  // namespace
+
+namespace mk {
+int op_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(nullptr, code, "%s", buf);
+}
+}  // namespace mk
+
+namespace {
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {

@@ -1,0 +1,69 @@
+// Internal interface between the host entry points of the multi-token operators
+// (mk_ops.cpp) and their kernels.  Every launch_* function returns the CUDA error of the
+// launch; argument checks are the caller's.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "mk.h"
+
+namespace mk {
+
+// sets the message of mk_last_error(NULL) and returns `code` (mk_host.cpp)
+int op_fail(int code, const char* fmt, ...);
+
+constexpr int kOpPage = 16;            // tokens per cache page
+constexpr int kOpMaxBatch = 128;       // sequences of one call (a CTA of the attention keeps their prefix sums)
+constexpr int kOpMaxExperts = 256;     // experts of one call (as mk_create)
+constexpr int kOpMaxAccept = 512;      // accepted nodes per sequence (staged in shared memory)
+constexpr int kOpMaxHalf = 64;         // head_dim / 2 at most
+
+// ------------------------------------------------------------------ qk_norm_rope
+struct RopeParams {
+  mk_paged_kv c;
+  mk_rope_args a;
+  unsigned long long turns[kOpMaxHalf];  // theta^(-2i/hd) / 2pi as a 64-bit binary fraction
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
+
+// ------------------------------------------------------------------ tree_attention
+struct TreeParams {
+  mk_paged_kv c;
+  mk_tree_args a;
+  int gs;          // query heads per KV head
+  int npt;         // nodes per 128-row tile
+  int two;         // 1: a CTA works on two row tiles at once; 0: on one, with two key streams
+  int ntp;         // row-tile groups per (sequence, KV head)
+  int words;       // mask words per node
+  int grid;        // CTAs
+  float scale_log2;
+  float* part;     // partial results: [grid][2][tiles][hd / 4][128] float4
+  float2* part_ml; // [grid][2][tiles][128] (running maximum, sum)
+};
+size_t tree_workspace_bytes(const TreeParams& p);
+cudaError_t launch_tree(TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t st);
+
+// ------------------------------------------------------------------ cache pages
+cudaError_t launch_copy_pages(uint8_t* k, uint8_t* v, int n_layers, long long layer_bytes, long long page_bytes,
+                              const int32_t* src, const int32_t* dst, int n, cudaStream_t st);
+struct CommitParams {
+  mk_paged_kv c;   // k, v: the whole pools
+  int n_layers, max_accept;
+  const int32_t* accepted;
+  int32_t* new_lens;
+  int32_t* status;
+};
+cudaError_t launch_commit(const CommitParams& p, cudaStream_t st);
+
+// ------------------------------------------------------------------ expert_product
+struct ExpertParams {
+  mk_expert_args a;
+  int grid;
+};
+cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw,
+                           const CUtensorMap& tu, cudaStream_t st);
+
+}  // namespace mk

@@ -1,0 +1,821 @@
+// Attention of several nodes per sequence over the paged cache and one another.
+//
+//   out_i = sum_j 2^(c q_i.k_j - m_i) v_j / sum_j 2^(c q_i.k_j - m_i),   c = scale / ln 2
+// in one pass over the keys, with the running maximum m_i and the running sum in fp32.
+//
+// A row is a (node, query head) pair of one KV head: row r of a tile is node r / gs, head
+// r % gs, so that the gs heads of a group share every key that is read.  A tile has 128
+// rows, the M of one tcgen05.mma; S = Q K^T and O += P V both run on the tensor cores with
+// accumulators in tensor memory, P goes back there as bf16 (A operand), and the thread that
+// owns a row (lane) keeps its maximum and sum.  Keys come in blocks of 128 (8 pages), each
+// page by its own tensor-map copy, into a ring shared by K and V.
+//
+// Two softmax warpgroups ("streams") alternate so that one's exponentials run beside the
+// other's products.  Up to 128 rows per KV head both streams work on the same rows, on
+// even and odd key blocks, and are merged at the end (two = 0); with more rows each stream
+// has a tile of its own and both use every key block that is loaded (two = 1), which halves
+// the key traffic where it would exceed what L2 delivers.
+//
+// The work is a list of units, one per (sequence, KV head, tile group, key block), cut into
+// equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  A
+// run that covers only part of an item's keys leaves (O, m, sum) in the workspace and
+// a second kernel joins the parts in order of their keys; at most a run's first and last
+// item are such.
+#include "mk_ops.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kBlk = 128;               // keys of a block
+constexpr int kTreeThreads = 320;       // two softmax warpgroups, producer warp, MMA warp
+constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P of the streams at 0 and 128, O at 256 and 384
+constexpr float kRescale = 8.f;         // the maximum may lag by 2^8 before O is rescaled
+
+template <int HD>
+struct TreeCfg {
+  static constexpr int kSpan = HD == 32 ? 64 : 128;        // swizzle span in bytes
+  static constexpr int kHalves = HD * 2 / kSpan;           // spans per row
+  static constexpr int kTile = kBlk * HD * 2;              // 128 rows
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kSmem = 1024 + 2 * kTile + kStages * kTile;
+};
+
+// ------------------------------------------------------------------ work list
+
+struct Item {          // one (sequence, KV head, tile group) and the blocks of this run
+  int b, kvh, tp;
+  int len, cnt;        // cached tokens, nodes
+  int kstart, end;     // its keys: [kstart, end)
+  int nblk;            // their blocks
+  int ja, jb;          // blocks of this run
+  int unit0;           // global index of its first unit
+};
+
+struct SeqShape {
+  int len, cnt;
+};
+
+// Length and node count of a sequence; an invalid one gets no nodes.
+__device__ __forceinline__ SeqShape seq_shape(const TreeParams& p, int b, bool record) {
+  SeqShape s;
+  s.len = __ldg(p.c.seq_lens + b);
+  s.cnt = p.a.counts ? __ldg(p.a.counts + b) : p.a.n_nodes;
+  if (s.len < 0 || s.cnt > p.a.n_nodes || (long long)s.len + s.cnt > 16ll * p.c.max_pages) {
+    if (record) op_error(p.a.status, MK_ERR_INVALID, b, s.cnt, s.len);
+    s.cnt = 0;
+  }
+  if (s.cnt < 0) s.cnt = 0;
+  return s;
+}
+
+__device__ __forceinline__ int nodes_per_group(const TreeParams& p) { return p.npt * (p.two ? 2 : 1); }
+
+// Keys [kstart, end) of tile group tp: with the causal chain a group ends at its last node;
+// a window starts at the earliest key that any of its nodes may see (on a page boundary).
+__device__ __forceinline__ void key_range(const TreeParams& p, const SeqShape& s, int tp, int& kstart, int& end) {
+  const int per = nodes_per_group(p), first = tp * per;
+  const int last = min(s.cnt, first + per) - 1;
+  end = s.len + (p.a.mask ? s.cnt : last + 1);
+  kstart = 0;
+  if (p.a.window > 0) {
+    const int pos = s.len + (p.a.mask || p.a.positions ? 0 : first);  // the earliest position of its nodes
+    kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
+  }
+}
+__device__ __forceinline__ int group_blocks(const TreeParams& p, const SeqShape& s, int tp) {
+  if (tp * nodes_per_group(p) >= s.cnt) return 0;
+  int k0, e;
+  key_range(p, s, tp, k0, e);
+  return (e - k0 + kBlk - 1) / kBlk;
+}
+// units of one KV head of a sequence
+__device__ __forceinline__ int head_units(const TreeParams& p, const SeqShape& s) {
+  if (s.cnt <= 0) return 0;
+  const int per = nodes_per_group(p), n = (s.cnt + per - 1) / per;
+  if (p.a.mask || n == 1) return n * group_blocks(p, s, 0);
+  int u = 0;
+  for (int t = 0; t < n; ++t) u += group_blocks(p, s, t);
+  return u;
+}
+
+// Inclusive prefix sums of the sequences' units into pre[0..batch] (pre[0] = 0); all
+// threads of the block.
+__device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool record) {
+  const int B = p.c.batch, nt = (int)blockDim.x;
+  if (threadIdx.x == 0) pre[0] = 0;
+  int carry = 0;
+  for (int base = 0; base < B; base += nt) {
+    const int b = base + (int)threadIdx.x;
+    int x = 0;
+    if (b < B) x = head_units(p, seq_shape(p, b, record)) * p.c.n_kv_heads;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[w] = x;
+    __syncthreads();
+    int add = carry;
+    for (int i = 0; i < w; ++i) add += warp_sums[i];
+    if (b < B) pre[b + 1] = x + add;
+    for (int i = 0; i < nt / 32; ++i) carry += warp_sums[i];
+    __syncthreads();
+  }
+}
+
+// run of CTA c of G: units [c * U / G, (c + 1) * U / G).  G <= U: every run has a unit, so the
+// parts of an item are those of consecutive CTAs.
+__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid, U); }
+__device__ __forceinline__ int run_begin(int c, int U, int G) { return (int)((long long)c * U / G); }
+__device__ __forceinline__ int run_owner(int u, int U, int G) { return (int)(((long long)(u + 1) * G - 1) / U); }
+
+// The item that unit u belongs to (its run part is filled in by the caller).
+__device__ Item locate(const TreeParams& p, const int* pre, int u) {
+  Item it;
+  int lo = 0, hi = p.c.batch - 1;  // the last b with pre[b] <= u and units of its own
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (pre[m] <= u) lo = m; else hi = m - 1;
+  }
+  it.b = lo;
+  const SeqShape s = seq_shape(p, lo, false);
+  it.len = s.len;
+  it.cnt = s.cnt;
+  const int per_head = (pre[lo + 1] - pre[lo]) / p.c.n_kv_heads;
+  int r = u - pre[lo];
+  it.kvh = r / per_head;
+  it.unit0 = pre[lo] + it.kvh * per_head;
+  r -= it.kvh * per_head;
+  if (p.a.mask) {
+    it.nblk = group_blocks(p, s, 0);
+    it.tp = r / it.nblk;
+    it.unit0 += it.tp * it.nblk;
+  } else {
+    it.tp = 0;
+    it.nblk = group_blocks(p, s, 0);
+    while (r >= it.nblk) {
+      r -= it.nblk;
+      it.unit0 += it.nblk;
+      it.nblk = group_blocks(p, s, ++it.tp);
+    }
+  }
+  key_range(p, s, it.tp, it.kstart, it.end);
+  return it;
+}
+
+// Walks the items of a run.
+struct Run {
+  int u, u1;
+  Item it;
+  __device__ __forceinline__ bool next(const TreeParams& p, const int* pre) {
+    if (u >= u1) return false;
+    it = locate(p, pre, u);
+    it.ja = u - it.unit0;
+    it.jb = min(it.nblk, it.ja + (u1 - u));
+    u += it.jb - it.ja;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ what a row sees
+
+struct Row {
+  int node;     // -1: not a row of the call
+  int pos;      // its position (clamped to [len, len + cnt - 1])
+  int lo;       // the first position inside its window
+  const int32_t* mask;
+};
+
+__device__ __forceinline__ Row make_row(const TreeParams& p, const Item& it, int node) {
+  Row r;
+  r.node = node;
+  r.pos = it.len;
+  r.lo = INT_MIN;
+  r.mask = nullptr;
+  if (node < 0) return r;
+  const long long at = (long long)it.b * p.a.n_nodes + node;
+  r.pos = it.len + node;
+  if (p.a.positions) r.pos = min(max(__ldg(p.a.positions + at), it.len), it.len + it.cnt - 1);
+  if (p.a.window > 0) r.lo = r.pos - p.a.window + 1;
+  if (p.a.mask) r.mask = p.a.mask + at * p.words;
+  return r;
+}
+
+// Bit i: the row sees key kb + i (32 keys).
+__device__ uint32_t sees32(const TreeParams& p, const Item& it, const Row& r, int kb) {
+  if (r.node < 0) return 0;
+  uint32_t bits = 0;
+  if (kb < it.len) {  // cached keys [max(lo, kb), min(len, kb + 32))
+    const int a = r.lo > kb ? r.lo - kb : 0, e = min(it.len - kb, 32);
+    if (a < e) bits = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & (0xffffffffu << a);
+  }
+  if (kb + 32 > it.len) {  // nodes a0 .. a0 + 31 (a0 > -32)
+    const int a0 = kb - it.len;
+    uint32_t nb;
+    if (r.mask) {
+      const int w = a0 >> 5, sh = a0 & 31;  // (floor)
+      const uint32_t x = w >= 0 && w < p.words ? (uint32_t)__ldg(r.mask + w) : 0u;
+      const uint32_t y = sh && w + 1 < p.words ? (uint32_t)__ldg(r.mask + w + 1) : 0u;
+      nb = __funnelshift_r(x, y, sh);
+    } else {
+      const int e = r.node - a0 + 1;  // nodes 0..node
+      nb = e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u;
+    }
+    const int e = it.cnt - a0;
+    if (e < 32) nb &= e <= 0 ? 0u : (1u << e) - 1u;
+    if (a0 < 0) nb &= 0xffffffffu << -a0;
+    if (r.lo > it.len && nb) {  // the window reaches past the cache: look at the nodes' positions
+      for (uint32_t m = nb; m; m &= m - 1) {
+        const int i = __ffs(m) - 1, a = a0 + i;
+        int pa = it.len + a;
+        if (p.a.positions)
+          pa = min(max(__ldg(p.a.positions + (long long)it.b * p.a.n_nodes + a), it.len), it.len + it.cnt - 1);
+        if (pa < r.lo) nb &= ~(1u << i);
+      }
+    }
+    bits |= nb;
+  }
+  return bits;
+}
+
+// Whether some row of the item may not see some key of the block at k0, or the block has
+// keys past the end: its scores are masked and its V checked.
+__device__ __forceinline__ bool masked_block(const TreeParams& p, const Item& it, int k0) {
+  const int per = nodes_per_group(p);
+  const int open = it.len + (p.a.mask ? 0 : it.tp * per + 1);  // keys below are seen by all rows, but for a window
+  if (k0 + kBlk > open) return true;
+  if (p.a.window > 0) {
+    const int last = p.a.mask || p.a.positions ? it.cnt : min(it.cnt, (it.tp + 1) * per);
+    return k0 < it.len + last - p.a.window;  // the latest row's window starts inside or behind
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------ shared memory
+
+struct TreeShared {
+  uint32_t tmem;
+  int abort;
+  int bad_v;             // a masked block held a V that is not finite
+  int pre[kOpMaxBatch + 1];
+  int warp_sums[kTreeThreads / 32];
+  float2 ml[kBlk];       // stream 1's (m, sum) for the merge
+  unsigned long long bars[2 * 8 + 8];
+};
+
+template <int HD>
+struct Bars {
+  uint32_t base;
+  static constexpr int S = TreeCfg<HD>::kStages;
+  __device__ uint32_t full(int s) const { return base + 8 * s; }
+  __device__ uint32_t empty(int s) const { return base + 8 * (S + s); }
+  __device__ uint32_t qfull() const { return base + 8 * (2 * S); }
+  __device__ uint32_t qempty() const { return base + 8 * (2 * S + 1); }
+  __device__ uint32_t sfull(int s) const { return base + 8 * (2 * S + 2 + s); }
+  __device__ uint32_t pready(int s) const { return base + 8 * (2 * S + 4 + s); }
+  __device__ uint32_t ofull(int s) const { return base + 8 * (2 * S + 6 + s); }
+};
+
+__device__ __forceinline__ bool nonfinite2(uint32_t u) {
+  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t u) {
+  if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+  if ((u & 0x7f800000u) == 0x7f800000u) u &= 0x0000ffffu;
+  return u;
+}
+
+// Threads t of nt: in the landed V block at `stage`, rows from `live` on become zero and
+// values that are not finite are dropped (and reported): a weight of zero times such a value
+// would otherwise reach rows that do not see the key.
+template <int HD>
+__device__ __forceinline__ void clean_v(uint8_t* stage, int live, int t, int nt, int* bad) {
+  constexpr int kVecs = TreeCfg<HD>::kSpan / 16;
+  bool seen = false;
+  for (int i = t; i < TreeCfg<HD>::kTile / 16; i += nt) {
+    uint4* a = reinterpret_cast<uint4*>(stage) + i;
+    const int row = (i / kVecs) % kBlk;
+    if (row >= live) {
+      *a = make_uint4(0, 0, 0, 0);
+    } else {
+      const uint4 x = *a;
+      if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
+        *a = make_uint4(drop_nonfinite2(x.x), drop_nonfinite2(x.y), drop_nonfinite2(x.z), drop_nonfinite2(x.w));
+        seen = true;
+      }
+    }
+  }
+  if (seen) *reinterpret_cast<volatile int*>(bad) = 1;
+}
+
+__device__ __forceinline__ int page_of(const TreeParams& p, int b, int key, bool record) {
+  const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + key / kOpPage);
+  if (page >= 0 && page < p.c.n_pages) return page;
+  if (record) op_error(p.a.status, MK_ERR_BAD_PAGE, b, key / kOpPage, page);
+  return 0;
+}
+
+// What clean_v dropped, for 16 columns of a row: p_j * v_j of the keys that the row sees.
+// Only after a masked block held such values (never with finite caches): plain loads.
+template <int HD>
+__device__ __noinline__ void add_nonfinite(const TreeParams& p, const Item& it, const Row& r, const uint16_t* q, float m, int c0,
+                                           int j0, int jstep, float* o) {
+  const uint16_t* K = static_cast<const uint16_t*>(p.c.k);
+  const uint16_t* V = static_cast<const uint16_t*>(p.c.v);
+  for (int j = it.ja + j0; j < it.jb; j += jstep) {
+    const int k0 = it.kstart + j * kBlk;
+    if (!masked_block(p, it, k0)) continue;
+    for (int w = 0; w < kBlk / 32; ++w) {
+      for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
+        const int key = k0 + 32 * w + __ffs(bits) - 1;
+        const long long at = (((long long)page_of(p, it.b, key, false) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
+        float weight = -1.f;
+        for (int c = 0; c < 16; ++c) {
+          const float v = bf16_to_f(V[at + c0 + c]);
+          if (fabsf(v) <= 3.4e38f) continue;
+          if (weight < 0.f) {
+            float s = 0.f;
+            for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
+            weight = ex2(s * p.scale_log2 - m);
+          }
+          o[c] += weight * v;
+        }
+      }
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tq,
+                const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  using C = TreeCfg<HD>;
+  extern __shared__ uint8_t raw[];
+  __shared__ TreeShared sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* const gbase = raw + (base - smem_u32(raw));
+  const uint32_t q_s = base, ring = base + 2 * C::kTile;
+  uint8_t* const ring_g = gbase + 2 * C::kTile;
+  float* const exch = reinterpret_cast<float*>(gbase + C::kTile);  // two = 0: the second Q tile is free
+  Bars<HD> bars{smem_u32(sh.bars)};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &sh.abort;
+  __shared__ unsigned long long merge_bar;  // the two warpgroups meet here
+  const uint32_t mbar = smem_u32(&merge_bar);
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    sh.bad_v = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bars.full(s), 1);
+      mbar_init(bars.empty(s), 1);
+    }
+    mbar_init(bars.qfull(), 1);
+    mbar_init(bars.qempty(), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bars.sfull(s), 1);
+      mbar_init(bars.pready(s), 128);
+      mbar_init(bars.ofull(s), 1);
+    }
+    mbar_init(mbar, 256);
+    fence_proxy_async_smem();
+  }
+  scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
+  const int U = sh.pre[p.c.batch];
+  const int G = run_count(p, U);
+  if ((int)blockIdx.x >= G) return;  // (the whole CTA)
+  const int u0 = run_begin(blockIdx.x, U, G), u1 = run_begin(blockIdx.x + 1, U, G);
+  if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const bool two = p.two != 0;
+  Run run{u0, u1, {}};
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- producer
+    // lane = (page of the block) + 8 * (span of the row): one copy per lane
+    uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
+    const int pg = lane & 7, half = lane >> 3;
+    bool ok = true;
+    while (ok && run.next(p, sh.pre)) {
+      const Item& it = run.it;
+      const int rows = p.npt * p.gs;
+      // this lane's page of the next block is looked up one block ahead
+      int key = it.kstart + it.ja * kBlk + pg * kOpPage;
+      int next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
+      for (int j = it.ja; ok && j < it.jb; ++j) {
+        const int k0 = it.kstart + j * kBlk;
+        const int live = min(kBlk / kOpPage, (it.end - k0 + kOpPage - 1) / kOpPage);
+        const int row = (next_page * p.c.n_kv_heads + it.kvh) * kOpPage;
+        key = k0 + kBlk + pg * kOpPage;
+        if (j + 1 < it.jb) next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int s = fill % C::kStages;
+          const uint32_t ph = (fill / C::kStages) & 1;
+          if (!(ok = op_wait(bars.empty(s), ph ^ 1, abort, p.a.status, 1))) break;
+          if (lane == 0) mbar_expect_tx(bars.full(s), (uint32_t)live * kOpPage * HD * 2);
+          __syncwarp();
+          if (pg < live && half < C::kHalves)
+            op_tma_2d(ring + s * C::kTile + half * (kBlk * C::kSpan) + pg * (kOpPage * C::kSpan), kv ? &tv : &tk,
+                      half * (C::kSpan / 2), row, bars.full(s));
+          ++fill;
+          if (kv == 0 && j == it.ja) {  // the item's queries, once the last item's products have read theirs
+            if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
+            ++qphase;
+            const int tiles = two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1;
+            if (lane == 0) {
+              mbar_expect_tx(bars.qfull(), (uint32_t)(tiles * rows * HD * 2));
+              for (int t = 0; t < tiles; ++t)
+                for (int h = 0; h < C::kHalves; ++h)
+                  op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), it.kvh * p.gs,
+                            it.tp * nodes_per_group(p) + t * p.npt, it.b, bars.qfull());
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    // an abandoned run leaves copies in flight: wait for them (bounded)
+    if (*abort) {
+      const uint32_t n = min(fill, (uint32_t)C::kStages);
+      for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(bars.full(f % C::kStages), (f / C::kStages) & 1, 10000000ll);
+      if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMA issue
+    constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
+    constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
+    constexpr uint32_t kSbo = 8 * C::kSpan;
+    uint32_t used = 0;                  // ring slots of earlier items
+    uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
+    bool ok = true;
+    while (ok && run.next(p, sh.pre)) {
+      const int nb = run.it.jb - run.it.ja;
+      const int steps = two ? 2 * nb : nb;
+      if (!(ok = op_wait(bars.qfull(), nq & 1, abort, p.a.status, 3))) break;
+      tc_fence_after();
+      ++nq;
+      // step t: stream t & 1, block t >> 1 (two) or t
+      auto issue_s = [&](int t) -> bool {
+        const int st = t & 1, blk = two ? t >> 1 : t;
+        const uint32_t slot = used + 2 * blk, s = slot % C::kStages;
+        if (!op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 4)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a = q_s + (two ? st : 0) * C::kTile, b = ring + s * C::kTile;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan;
+            umma_bf16(tmem + kTmemS + 128 * st, umma_sdesc_sw(a + off, 16, kSbo, C::kSpan),
+                      umma_sdesc_sw(b + off, 16, kSbo, C::kSpan), idesc_s, kk > 0);
+          }
+          umma_commit(bars.sfull(st));
+          if (!two || st == 1) umma_commit(bars.empty(s));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = issue_s(0) && (steps < 2 || issue_s(1));
+      for (int t = 0; ok && t < steps; ++t) {
+        const int st = t & 1, blk = two ? t >> 1 : t;
+        const uint32_t slot = used + 2 * blk + 1, s = slot % C::kStages;
+        if (!(ok = op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 5))) break;
+        if (!(ok = op_wait(bars.pready(st), np[st] & 1, abort, p.a.status, 6))) break;
+        ++np[st];
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t b = ring + s * C::kTile;
+          const bool first = two ? blk == 0 : blk == st;
+#pragma unroll
+          for (int kk = 0; kk < kBlk / 16; ++kk)
+            umma_bf16_ta(tmem + kTmemO + 128 * st, tmem + kTmemS + 128 * st + 8 * kk,
+                         umma_sdesc_sw(b + kk * 16 * C::kSpan, kBlk * C::kSpan, kSbo, C::kSpan), idesc_o, !first || kk > 0);
+          if (!two || st == 1) umma_commit(bars.empty(s));
+          if (t + 2 >= steps) umma_commit(bars.ofull(st));
+        }
+        __syncwarp();
+        if (t + 2 < steps) {
+          ok = issue_s(t + 2);
+        } else if (t + 1 == steps && lane == 0) {
+          umma_commit(bars.qempty());
+        }
+      }
+      used += 2 * nb;
+    }
+    if (*abort) {  // let the products in flight end before the memory goes
+      if (lane == 0) umma_commit(bars.ofull(0));
+      __syncwarp();
+      const uint64_t t0 = gtime();
+      while ((long long)(gtime() - t0) < 10000000ll) {}
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax streams
+    const int st = warp >> 2;                       // 0 or 1
+    const int row = (int)threadIdx.x & 127;         // = lane of tensor memory
+    const uint32_t tS = tmem + kTmemS + 128 * st + ((uint32_t)(warp & 3) << 21);
+    const uint32_t tO = tmem + kTmemO + 128 * st + ((uint32_t)(warp & 3) << 21);
+    uint32_t ns = 0, no = 0, used = 0, nm = 0;      // S tiles, finished items, ring slots, meetings
+    bool ok = true;
+    auto meet = [&]() -> bool {                     // all 256 threads of the two streams
+      mbar_arrive(mbar);
+      const bool r = op_wait(mbar, nm & 1, abort, p.a.status, 7);
+      ++nm;
+      return r;
+    };
+    while (ok && run.next(p, sh.pre)) {
+      const Item& it = run.it;
+      const int nb = it.jb - it.ja;
+      const int tile = two ? st : 0;
+      const int node_in = row / p.gs;
+      int node = it.tp * nodes_per_group(p) + tile * p.npt + node_in;
+      if (node_in >= p.npt || node >= it.cnt) node = -1;
+      const Row r = make_row(p, it, node);
+      float m = -INFINITY, l = 0.f;
+      const int b0 = two ? 0 : st, bstep = two ? 1 : 2;
+      for (int blk = b0; ok && blk < nb; blk += bstep) {
+        const int k0 = it.kstart + (it.ja + blk) * kBlk;
+        const bool masked = masked_block(p, it, k0);
+        uint32_t vis[4];
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = sees32(p, it, r, k0 + 32 * w);
+          const uint32_t slot = used + 2 * blk + 1, s = slot % C::kStages;
+          if (!(ok = op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 8))) break;
+          const int live = it.end - k0;
+          clean_v<HD>(ring_g + s * C::kTile, live, two ? (int)threadIdx.x : row, two ? 256 : 128, &sh.bad_v);
+          fence_proxy_async_smem();
+          if (two && !(ok = meet())) break;
+        }
+        if (!(ok = op_wait(bars.sfull(st), ns & 1, abort, p.a.status, 9))) break;
+        ++ns;
+        tc_fence_after();
+        uint32_t s[kBlk];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait32(s + 32 * i);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < kBlk; ++i)
+            if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kBlk; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const float mnew = fmaxf(m, top);
+        const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = mnew == m ? 1.f : ex2(m - mnew);
+          if (blk != b0) {
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
+              tmem_wait16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(tO + c, o);
+            }
+          }
+          l *= f;
+          m = mnew;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kBlk / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = ex2(fmaf(__uint_as_float(s[32 * c + 2 * i]), p.scale_log2, -mm));
+            const float b = ex2(fmaf(__uint_as_float(s[32 * c + 2 * i + 1]), p.scale_log2, -mm));
+            sum[(2 * i) & 3] += a;
+            sum[(2 * i + 1) & 3] += b;
+            pk[i] = pack_bf16(a, b);
+          }
+          tmem_st16(tS + 16 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bars.pready(st));
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ the item's result
+      const bool had = nb > b0;  // this stream had a block
+      if (had) {
+        if (!(ok = op_wait(bars.ofull(st), no & 1, abort, p.a.status, 10))) break;
+        ++no;
+        tc_fence_after();
+      }
+      used += 2 * nb;
+      const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
+      const bool whole = nb == it.nblk;
+      const uint16_t* qrow = nullptr;
+      uint16_t* dst = nullptr;
+      if (node >= 0) {
+        const int head = it.kvh * p.gs + row % p.gs;
+        qrow = static_cast<const uint16_t*>(p.a.q) + it.b * p.a.q_stride[0] + node * p.a.q_stride[1] + head * p.a.q_stride[2];
+        dst = static_cast<uint16_t*>(p.a.out) + it.b * p.a.out_stride[0] + node * p.a.out_stride[1] + head * p.a.out_stride[2];
+      }
+      // partial results: first item of the run in slot 0, a later (so last) one in slot 1
+      const int slot = it.unit0 + it.ja == u0 ? 0 : 1;
+      const long long pt = ((long long)blockIdx.x * 2 + slot) * (two ? 2 : 1) + tile;
+      float4* part = reinterpret_cast<float4*>(p.part) + pt * (HD / 4) * kBlk + row;
+      float w0 = 1.f, w1 = 0.f;  // weights of the two streams' sums
+      if (!two) {
+        if (st == 1) sh.ml[row] = make_float2(m, l);
+        if (!(ok = meet())) break;
+        if (st == 0) {
+          const float2 o = sh.ml[row];
+          const float top = fmaxf(m, o.x), t = top == -INFINITY ? 0.f : top;
+          w0 = ex2(m - t);
+          w1 = ex2(o.x - t);
+          l = l * w0 + o.y * w1;
+          m = top;
+        }
+      }
+      const bool other = nb > 1;  // stream 1 had a block (two = 0)
+      if (st == 0 || two) {
+        if (!whole && node >= 0) p.part_ml[pt * kBlk + row] = make_float2(m, l);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int h = 0; ok && h < 2; ++h) {  // halves of the columns
+#pragma unroll 1
+        for (int c = h * (HD / 2); c < (h + 1) * (HD / 2); c += 16) {
+          if (!two && st == 0) break;
+          uint32_t u[16];
+          float o[16];
+          if (had) {
+            tmem_ld16(tO + c, u);
+            tmem_wait16(u);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = had ? __uint_as_float(u[i]) : 0.f;
+          if (fix && had && node >= 0) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, b0, bstep, o);
+          if (!two) {  // stream 1 hands its columns over
+            if (had) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) exch[(c - h * (HD / 2) + i) * kBlk + row] = o[i];
+            }
+          } else if (node >= 0) {
+            if (whole) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+              *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) part[(c / 4 + i) * kBlk] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        if (two) continue;
+        if (!(ok = meet())) break;
+        if (st == 0) {
+#pragma unroll 1
+          for (int c = h * (HD / 2); c < (h + 1) * (HD / 2); c += 16) {
+            uint32_t u[16];
+            float o[16];
+            tmem_ld16(tO + c, u);
+            tmem_wait16(u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * w0;
+            // (m is the merged maximum here, to which the scaled sums are relative)
+            if (fix && node >= 0) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, b0, bstep, o);
+            if (other) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] += w1 * exch[(c - h * (HD / 2) + i) * kBlk + row];
+            }
+            if (node >= 0) {
+              if (whole) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+                *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[(c / 4 + i) * kBlk] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+            }
+          }
+        }
+        if (!(ok = meet())) break;
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ joining the parts
+// One block per (item, row tile, 32 rows, 16 columns): thread = (row, 4 columns).
+constexpr int kJoinThreads = 128;
+
+template <int HD>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ int pre[kOpMaxBatch + 1];
+  __shared__ int warp_sums[kJoinThreads / 32];
+  pdl_wait();
+  scan_units(p, pre, warp_sums, false);
+  const int U = pre[p.c.batch];
+  const int tiles = p.two ? 2 : 1;
+  int i = blockIdx.x;
+  const int rowq = i & 3;
+  i >>= 2;
+  const int tile = i % tiles;
+  i /= tiles;
+  const int tp = i % p.ntp;
+  i /= p.ntp;
+  const int kvh = i % p.c.n_kv_heads, b = i / p.c.n_kv_heads;
+  const SeqShape s = seq_shape(p, b, false);
+  const int nblk = group_blocks(p, s, tp);
+  if (nblk == 0) return;
+  int g0 = pre[b] + kvh * ((pre[b + 1] - pre[b]) / p.c.n_kv_heads);
+  if (p.a.mask)
+    g0 += tp * nblk;
+  else
+    for (int t = 0; t < tp; ++t) g0 += group_blocks(p, s, t);
+  const int G = run_count(p, U);
+  const int c0 = run_owner(g0, U, G), c1 = run_owner(g0 + nblk - 1, U, G);
+  if (c0 == c1) return;  // written whole
+  const int row = rowq * 32 + (threadIdx.x & 31), c4 = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int node_in = row / p.gs, node = tp * nodes_per_group(p) + tile * p.npt + node_in;
+  if (node_in >= p.npt || node >= s.cnt) return;
+  // a CTA's slot 0 holds the item that its run starts in: every part but, maybe, the first
+  const int slot0 = run_begin(c0, U, G) >= g0 ? 0 : 1;
+  auto part_of = [&](int c) -> long long { return ((long long)c * 2 + (c == c0 ? slot0 : 0)) * tiles + tile; };
+  float m = -INFINITY;
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(&p.part_ml[part_of(c) * kBlk + row].x));
+  const float mm = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const long long pt = part_of(c);
+    const float2 ml = __ldcg(p.part_ml + pt * kBlk + row);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part) + (pt * (HD / 4) + c4) * kBlk + row);
+    const float w = ex2(ml.x - mm);
+    l += w * ml.y;
+    o.x += w * x.x;
+    o.y += w * x.y;
+    o.z += w * x.z;
+    o.w += w * x.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* dst = static_cast<uint16_t*>(p.a.out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] +
+                  (long long)(kvh * p.gs + row % p.gs) * p.a.out_stride[2] + 4 * c4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
+template <int HD>
+cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                      cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<HD>::kSmem);
+  if (e != cudaSuccess) return e;
+  tree_kernel<HD><<<p.grid, kTreeThreads, TreeCfg<HD>::kSmem, st>>>(p, tq, tk, tv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.c.batch * p.c.n_kv_heads * p.ntp * (p.two ? 2 : 1) * 4), HD / 16);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<HD>, p);
+}
+
+}  // namespace
+
+size_t tree_workspace_bytes(const TreeParams& p) {
+  const size_t tiles = (size_t)p.grid * 2 * (p.two ? 2 : 1);
+  return tiles * kBlk * ((size_t)p.c.head_dim * 4 + sizeof(float2));
+}
+
+cudaError_t launch_tree(TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t st) {
+  const size_t tiles = (size_t)p.grid * 2 * (p.two ? 2 : 1);
+  p.part = static_cast<float*>(p.a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part + tiles * kBlk * p.c.head_dim);
+  if (p.c.head_dim == 128) return launch_hd<128>(p, tq, tk, tv, st);
+  if (p.c.head_dim == 64) return launch_hd<64>(p, tq, tk, tv, st);
+  return launch_hd<32>(p, tq, tk, tv, st);
+}
+
+}  // namespace mk
