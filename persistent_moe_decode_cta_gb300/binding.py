@@ -142,13 +142,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mk_destroy.argtypes = [H]
     lib.mk_destroy.restype = None
     lib.mk_version.argtypes = []
-    kv = ctypes.POINTER(mk_paged_kv)
-    lib.mk_qk_norm_rope.argtypes = [kv, ctypes.POINTER(mk_rope_args), vp]
-    lib.mk_tree_attention.argtypes = [kv, ctypes.POINTER(mk_tree_args), vp]
-    lib.mk_tree_attention_workspace.argtypes = [kv, ctypes.POINTER(mk_tree_args), ctypes.POINTER(sz)]
+    # (structs as void*: ops.py passes them packed)
+    lib.mk_qk_norm_rope.argtypes = [vp, vp, vp]
+    lib.mk_tree_attention.argtypes = [vp, vp, vp]
+    lib.mk_tree_attention_workspace.argtypes = [vp, vp, ctypes.POINTER(sz)]
     lib.mk_copy_pages.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
-    lib.mk_commit_nodes.argtypes = [kv, i32, vp, i32, vp, vp, vp]
-    lib.mk_expert_product.argtypes = [ctypes.POINTER(mk_expert_args), vp]
+    lib.mk_commit_nodes.argtypes = [vp, i32, vp, i32, vp, vp, vp]
+    lib.mk_expert_product.argtypes = [vp, vp]
     for name in EXPORTS:
         if name not in ("mk_last_error", "mk_destroy"):
             getattr(lib, name).restype = ctypes.c_int

@@ -123,7 +123,8 @@ cudaError_t launch_copy_pages(uint8_t* k, uint8_t* v, int n_layers, long long la
 cudaError_t launch_commit(const CommitParams& p, cudaStream_t st) {
   const size_t smem = ((2 * (size_t)p.max_accept * 4 + 15) & ~(size_t)15) + (size_t)p.max_accept * p.c.head_dim * 2;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(commit_kernel, kOpMaxAccept * (2 * 4 + 2 * 2 * kOpMaxHalf), done);  // the most of any call
     if (e != cudaSuccess) return e;
   }
   commit_kernel<<<dim3((unsigned)(p.c.batch * p.c.n_kv_heads), (unsigned)p.n_layers, 2), kCommitThreads, smem, st>>>(p);

@@ -12,8 +12,11 @@
 // One persistent CTA per SM walks the tiles in order of (expert, row tile, weight block), so
 // that CTAs that run together share rows and, across row tiles, weights in L2.  Warp roles:
 // producer (weights through a 3-D map whose rows stop at the expert's last; rows through a
-// plain map, or four at a time through gather copies when `rows` is given), MMA issue, and
-// four epilogue warps that transpose through shared memory to store whole output rows.
+// plain map), MMA issue, four epilogue warps that transpose through shared memory to store
+// whole output rows and, when `rows` is given, four warps that fetch the named rows with
+// 16-byte asynchronous copies straight into the swizzled layout.  (Tensor-map gather copies
+// of four rows at a time were tried for that: 566 us against 224 us for rows that lie in
+// order, 4096 tokens x top-8 of 128 experts, 2048 -> 768 with SwiGLU.)
 // Accumulation is fp32; the result is rounded once.
 #include "mk_ops.cuh"
 
@@ -21,6 +24,8 @@ namespace mk {
 namespace {
 
 constexpr int kExpThreads = 192;   // producer, MMA, four epilogue warps
+constexpr int kGatherThreads = 128;  // ... and four gather warps when rows are named
+constexpr int kGatherLag = 2;      // stages whose copies a gather thread has in flight beside the newest
 constexpr int kTileW = 128;        // weight rows of a block
 constexpr int kTileR = 128;        // rows of a tile
 constexpr int kTileK = 64;         // columns of a stage: one 128-byte swizzle span
@@ -40,7 +45,7 @@ struct ExpShared {
   uint32_t tmem;
   int abort;
   int pre[kOpMaxExperts + 1];   // prefix sums of the experts' row tiles
-  int warp_sums[kExpThreads / 32];
+  int warp_sums[(kExpThreads + kGatherThreads) / 32];
   unsigned long long bars[2 * kExpStages + 5];
 };
 
@@ -52,7 +57,7 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, bool r
 }
 
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
-  const int E = p.a.n_experts, nt = kExpThreads;
+  const int E = p.a.n_experts, nt = (int)blockDim.x;
   if (threadIdx.x == 0) sh.pre[0] = 0;
   int carry = 0;
   for (int base = 0; base < E; base += nt) {
@@ -99,7 +104,7 @@ __device__ __forceinline__ ExpTile find_tile(const ExpertParams& p, const int* p
 __device__ __forceinline__ float silu(float y) { return y / (1.f + __expf(-y)); }
 
 template <bool GLU>
-__global__ void __launch_bounds__(kExpThreads, 1)
+__global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     expert_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ CUtensorMap tx,
                   const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tu) {
   extern __shared__ uint8_t raw[];
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   if (threadIdx.x == 0) {
     sh.abort = 0;
     for (int s = 0; s < kExpStages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), p.a.rows ? 1 + kGatherThreads : 1);
       mbar_init(empty(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -148,17 +153,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
       const bool second = GLU || x.w0 + kTileW < p.a.n;
       const int boxes = (x.nr + kBoxR - 1) / kBoxR;
-      const uint32_t bytes = (second ? 2 : 1) * kBytesW + (p.a.rows ? (x.nr + 3) / 4 * 4 : boxes * kBoxR) * (kTileK * 2);
-      int g[4] = {0, 0, 0, 0};  // lane's four gathered rows
-      if (p.a.rows) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = x.r0 + min(4 * lane + i, x.nr - 1);
-          const int s = __ldg(p.a.rows + r);
-          g[i] = min(max(s, 0), p.a.n_x - 1);
-          if (g[i] != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, r, s);
-        }
-      }
+      const uint32_t bytes = (second ? 2 : 1) * kBytesW + (p.a.rows ? 0 : boxes * kBoxR * (kTileK * 2));
       for (int ks = 0; ks < ksteps; ++ks, ++fill) {
         const int s = fill % kExpStages;
         if (!(ok = op_wait(empty(s), ((fill / kExpStages) & 1) ^ 1, abort, p.a.status, 1))) break;
@@ -167,18 +162,56 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         __syncwarp();
         if (lane == 0) op_tma_3d(st, &tw, ks * kTileK, x.w0, x.e, full(s));
         if (lane == 1 && second) op_tma_3d(st + kBytesW, GLU ? &tu : &tw, ks * kTileK, GLU ? x.w0 : x.w0 + kTileW, x.e, full(s));
-        const uint32_t xs = st + 2 * kBytesW;
-        if (p.a.rows) {
-          if (4 * lane < x.nr) op_tma_gather4(xs + lane * 4 * kTileK * 2, &tx, ks * kTileK, g[0], g[1], g[2], g[3], full(s));
-        } else if (lane < boxes) {
-          op_tma_2d(xs + lane * kBoxR * kTileK * 2, &tx, ks * kTileK, x.r0 + lane * kBoxR, full(s));
-        }
+        if (!p.a.rows && lane < boxes)
+          op_tma_2d(st + 2 * kBytesW + lane * kBoxR * kTileK * 2, &tx, ks * kTileK, x.r0 + lane * kBoxR, full(s));
       }
     }
     if (*abort) {  // an abandoned run leaves copies in flight: wait for them (bounded)
       const uint32_t n = min(fill, (uint32_t)kExpStages);
       for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(full(f % kExpStages), (f / kExpStages) & 1, 10000000ll);
     }
+  } else if (warp >= kExpThreads / 32) {
+    // ---------------------------------------------------------------- gather
+    // eight threads a row (128 bytes of a stage), 16 rows at a time; a stage is handed over
+    // two stages later, when its copies have landed
+    const int t128 = (int)threadIdx.x - kExpThreads, chunk = t128 & 7, row0 = t128 >> 3;
+    const uint32_t swz = (uint32_t)(chunk ^ (row0 & 7)) * 16;  // (16 j keeps the low three bits of the row)
+    uint32_t fill = 0;
+    bool ok = true;
+    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
+      const uint16_t* src[kTileR / 16];
+#pragma unroll
+      for (int j = 0; j < kTileR / 16; ++j) {
+        const int i = row0 + 16 * j;
+        int r = 0;
+        if (i < x.nr) {
+          const int s = __ldg(p.a.rows + x.r0 + i);
+          r = min(max(s, 0), p.a.n_x - 1);
+          if (r != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, x.r0 + i, s);
+        }
+        src[j] = static_cast<const uint16_t*>(p.a.x) + r * p.a.x_stride + 8 * chunk;
+      }
+      for (int ks = 0; ks < ksteps; ++ks, ++fill) {
+        const int s = fill % kExpStages;
+        if (!(ok = op_wait(empty(s), ((fill / kExpStages) & 1) ^ 1, abort, p.a.status, 6))) break;
+        const uint32_t dst = base + s * kExpStage + 2 * kBytesW + row0 * (kTileK * 2) + swz;
+        const int bytes = ks * kTileK + 8 * chunk < p.a.k ? 16 : 0;  // (0: zeros)
+#pragma unroll
+        for (int j = 0; j < kTileR / 16; ++j)
+          if (row0 + 16 * j < x.nr) op_cp16(dst + j * 16 * kTileK * 2, bytes ? src[j] + ks * kTileK : src[j], bytes);
+        op_cp_commit();
+        if (fill >= kGatherLag) {
+          op_cp_wait<kGatherLag>();
+          fence_proxy_async_smem();
+          mbar_arrive(full((fill - kGatherLag) % kExpStages));
+        }
+      }
+    }
+    op_cp_wait<0>();
+    fence_proxy_async_smem();
+    if (ok)
+      for (uint32_t f = fill > kGatherLag ? fill - kGatherLag : 0; f < fill; ++f) mbar_arrive(full(f % kExpStages));
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
     uint32_t used = 0, nt = 0;
@@ -279,13 +312,19 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 
 }  // namespace
 
+template <bool GLU>
+static cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& tu,
+                              cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
+  if (e != cudaSuccess) return e;
+  expert_kernel<GLU><<<p.grid, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tw, tu);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& tu,
                            cudaStream_t st) {
-  auto* kernel = p.a.w_up ? expert_kernel<true> : expert_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpSmem);
-  if (e != cudaSuccess) return e;
-  kernel<<<p.grid, kExpThreads, kExpSmem, st>>>(p, tx, tw, tu);
-  return cudaGetLastError();
+  return p.a.w_up ? launch_glu<true>(p, tx, tw, tu, st) : launch_glu<false>(p, tx, tw, tu, st);
 }
 
 }  // namespace mk

@@ -134,8 +134,21 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
   p.c = *cache;
   p.a = *args;
   const int half = cache->head_dim / 2;
-  for (int i = 0; i < half; ++i)  // turns per position, as a fraction of 2^64
-    p.turns[i] = (unsigned long long)std::ldexp(std::pow(args->theta, -(double)i / half) / (2 * M_PI), 64);
+  // turns per position, as a fraction of 2^64 (the last theta's table is kept: 64 powers take
+  // as long as the launch)
+  struct Turns {
+    double theta = 0;
+    int half = 0;
+    unsigned long long t[kOpMaxHalf];
+  };
+  static thread_local Turns table;
+  if (table.theta != args->theta || table.half != half) {
+    for (int i = 0; i < half; ++i)
+      table.t[i] = (unsigned long long)std::ldexp(std::pow(args->theta, -(double)i / half) / (2 * M_PI), 64);
+    table.theta = args->theta;
+    table.half = half;
+  }
+  std::copy(table.t, table.t + half, p.turns);
   return cuda_error(launch_rope(p, static_cast<cudaStream_t>(stream)), "qk_norm_rope launch");
 }
 
@@ -269,7 +282,7 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   CUtensorMap tx, tw, tu;
   cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n_x};
   cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
-  cuuint32_t xb[2] = {64, a->rows ? 1u : 32u};
+  cuuint32_t xb[2] = {64, 32};
   r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
   cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, (cuuint64_t)a->n_experts};
   cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};

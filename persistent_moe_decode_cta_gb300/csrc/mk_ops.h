@@ -3,6 +3,7 @@
 // launch; argument checks are the caller's.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -13,6 +14,19 @@ namespace mk {
 
 // sets the message of mk_last_error(NULL) and returns `code` (mk_host.cpp)
 int op_fail(int code, const char* fmt, ...);
+
+// Allow `kernel` that much dynamic shared memory, once per device (`done`: a bit per device).
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 constexpr int kOpPage = 16;            // tokens per cache page
 constexpr int kOpMaxBatch = 128;       // sequences of one call (a CTA of the attention keeps their prefix sums)

@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 template <int HD>
 cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(tree_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<HD>::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(tree_kernel<HD>, TreeCfg<HD>::kSmem, done);
   if (e != cudaSuccess) return e;
   tree_kernel<HD><<<p.grid, kTreeThreads, TreeCfg<HD>::kSmem, st>>>(p, tq, tk, tv);
   e = cudaGetLastError();

@@ -276,7 +276,8 @@ def test_workspace_contents_do_not_matter(lens, n):
     import ctypes
     a = setup((8, 2, 64), lens, n, tree=False)
     want = ops.tree_attention(**a)
-    kv, b, _, _ = ops._kv(a["k_cache"], a["v_cache"], a["page_table"], a["seq_lens"], a["q"].device)
+    kv = B.mk_paged_kv(a["k_cache"].data_ptr(), a["v_cache"].data_ptr(), a["page_table"].data_ptr(), a["seq_lens"].data_ptr(),
+                       a["k_cache"].shape[0], 2, 64, len(lens), a["page_table"].shape[1])
     out = torch.zeros_like(a["q"])
     s = B._S3(*a["q"].stride()[:3])
     args = B.mk_tree_args(a["q"].data_ptr(), out.data_ptr(), s, s, None, None, None, None, n, 8, 0, 64 ** -0.5)

@@ -94,6 +94,18 @@ def test_expert_arguments(over, code):
     assert B.load_library().mk_expert_product(ctypes.byref(experts(**over)), None) == code
 
 
+def test_packed_structs_have_the_layout_of_the_header():
+    for packed, struct in ((ops._KV, B.mk_paged_kv), (ops._ROPE, B.mk_rope_args), (ops._TREE, B.mk_tree_args), (ops._EXPERT, B.mk_expert_args)):
+        assert packed.size == ctypes.sizeof(struct)
+        fields = [getattr(struct, n).size // (8 if n.endswith("_stride") and t is B._S3 else getattr(struct, n).size) for n, t in struct._fields_]
+        values = list(range(1, 1 + sum(fields)))
+        got = struct.from_buffer_copy(packed.pack(*values))
+        flat = []
+        for n, t in struct._fields_:
+            flat += list(getattr(got, n)) if t is B._S3 else [getattr(got, n)]
+        assert flat == values
+
+
 def test_no_rows_is_no_work():
     assert B.load_library().mk_expert_product(ctypes.byref(experts(n_rows=0)), None) == B.MK_OK
 
