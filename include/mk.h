@@ -427,7 +427,7 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  *               no position of the call falls into are not read
  *   seq_lens    int32[batch] cached tokens; seq_lens + counts <= 16 * max_pages, else
  *               MK_ERR_INVALID is recorded and the sequence is left out
- * head_dim in {32, 64, 128}; batch in 1..128. */
+ * head_dim in {32, 64, 128}; batch in 1..65535. */
 typedef struct mk_paged_kv {
   void* k;
   void* v;

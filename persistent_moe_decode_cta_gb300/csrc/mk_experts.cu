@@ -215,25 +215,26 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
     uint32_t used = 0, nt = 0;
+    const uint32_t tm = uniform(tmem);
+    const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, second weights, rows
     bool ok = true;
     for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++nt) {
       const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
-      const bool second = GLU || x.w0 + kTileW < p.a.n;
-      const uint32_t idesc = umma_idesc_bf16(kTileW, (x.nr + 15) / 16 * 16);
-      const uint32_t a = nt & 1, acc = tmem + 256 * a;
+      const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
+      const uint32_t idesc = umma_idesc_bf16(kTileW, (uniform(x.nr) + 15) / 16 * 16);
+      const uint32_t a = nt & 1, acc = tm + 256 * a;
       if (!(ok = op_wait(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
       tc_fence_after();
       for (int ks = 0; ks < ksteps; ++ks, ++used) {
         const int s = used % kExpStages;
         if (!(ok = op_wait(full(s), (used / kExpStages) & 1, abort, p.a.status, 3))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t st = base + s * kExpStage;
+        if (elect_one()) {
+          const uint64_t d = d0 + s * (kExpStage / 16);
 #pragma unroll
           for (int kk = 0; kk < kTileK / 16; ++kk) {
-            const uint64_t b = umma_sdesc_sw(st + 2 * kBytesW + 32 * kk, 16, 1024, 128);
-            umma_bf16(acc, umma_sdesc_sw(st + 32 * kk, 16, 1024, 128), b, idesc, ks > 0 || kk > 0);
-            if (second) umma_bf16(acc + 128, umma_sdesc_sw(st + kBytesW + 32 * kk, 16, 1024, 128), b, idesc, ks > 0 || kk > 0);
+            umma_bf16(acc, d + 2 * kk, d + 2 * kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
+            if (second) umma_bf16(acc + 128, d + kBytesW / 16 + 2 * kk, d + 2 * kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
           }
           umma_commit(empty(s));
           if (ks == ksteps - 1) umma_commit(afull(a));

@@ -104,6 +104,7 @@ int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   p.npt = std::min(fit, a->n_nodes);
   const int per = p.npt * (p.two ? 2 : 1);
   p.ntp = (a->n_nodes + per - 1) / per;
+  p.team = p.ntp <= 8 ? p.ntp : 1;
   p.words = (a->n_nodes + 31) / 32;
   const double units = (double)c->batch * c->n_kv_heads * p.ntp * ((double)c->max_pages / 8 + 1);
   if (units >= 2147483647.0 || (double)c->batch * c->n_kv_heads * p.ntp * 8 >= 2147483647.0)

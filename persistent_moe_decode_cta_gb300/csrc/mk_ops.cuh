@@ -69,6 +69,7 @@ __device__ __forceinline__ void op_cp_wait() {
 //   K-major:  rows of `span` bytes, 8-row groups `sbo` bytes apart (lbo unused).
 //   MN-major: `span` bytes along MN, 8 K-rows a group, K groups `sbo` bytes apart, the next
 //             span along MN `lbo` bytes away.
+//   A step along K inside the span, or to another tile, is an addition to the low word.
 __device__ __forceinline__ uint64_t umma_sdesc_sw(uint32_t addr, uint32_t lbo, uint32_t sbo, int span) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)(span == 128 ? 2 : 4) << 61);
@@ -128,6 +129,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// One lane of a converged warp, chosen so that the compiler knows that there is one: under
+// it the operands of tcgen05.mma stay in uniform registers (under `lane == 0` each MMA cost
+// about 140 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// v, equal in all lanes, as a value that the compiler knows to be so
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Programmatic dependent launch: the next kernel of the stream may start its prologue /
 // wait until every earlier kernel's memory is visible.

@@ -29,7 +29,7 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& do
 }
 
 constexpr int kOpPage = 16;            // tokens per cache page
-constexpr int kOpMaxBatch = 128;       // sequences of one call (a CTA of the attention keeps their prefix sums)
+constexpr int kOpMaxBatch = 65535;     // sequences of one call
 constexpr int kOpMaxExperts = 256;     // experts of one call (as mk_create)
 constexpr int kOpMaxAccept = 512;      // accepted nodes per sequence (staged in shared memory)
 constexpr int kOpMaxHalf = 64;         // head_dim / 2 at most
@@ -50,6 +50,7 @@ struct TreeParams {
   int npt;         // nodes per 128-row tile
   int two;         // 1: a CTA works on two row tiles at once; 0: on one, with two key streams
   int ntp;         // row-tile groups per (sequence, KV head)
+  int team;        // tile groups that walk a run of keys together
   int words;       // mask words per node
   int grid;        // CTAs
   float scale_log2;

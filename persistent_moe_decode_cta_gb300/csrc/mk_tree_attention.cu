@@ -16,18 +16,24 @@
 // has a tile of its own and both use every key block that is loaded (two = 1), which halves
 // the key traffic where it would exceed what L2 delivers.
 //
-// The work is a list of units, one per (sequence, KV head, tile group, key block), cut into
-// equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  A
-// run that covers only part of an item's keys leaves (O, m, sum) in the workspace and
-// a second kernel joins the parts in order of their keys; at most a run's first and last
-// item are such.
+// The work is a list of units, one per (sequence, tile group, KV head, key block), cut into
+// equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  (Up
+// to 8 tile groups form a team instead: each run is walked by one CTA per group at the same
+// time, so that the keys come from HBM once and from L2 for the others.)  A run that covers
+// only part of an item's keys leaves (O, m, sum) in the workspace and a second kernel joins
+// the parts in order of their keys; at most a run's first and last item are such.
 #include "mk_ops.cuh"
 
 namespace mk {
 namespace {
 
 constexpr int kBlk = 128;               // keys of a block
-constexpr int kTreeThreads = 320;       // two softmax warpgroups, producer warp, MMA warp
+constexpr int kTreeThreads = 384;       // two softmax warpgroups; a producer, an MMA and two idle warps
+// Registers per thread: 168 at launch (384 threads of 65,536 / 384), of which the third
+// warpgroup gives up what the softmax warpgroups take on (a row's 128 scores are kept in
+// registers): 2 * 128 * 216 + 128 * 72 = 384 * 168.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kTreeThreads * kLaunchRegs, "register split");
 constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P of the streams at 0 and 128, O at 256 and 384
 constexpr float kRescale = 8.f;         // the maximum may lag by 2^8 before O is rescaled
 
@@ -36,8 +42,7 @@ struct TreeCfg {
   static constexpr int kSpan = HD == 32 ? 64 : 128;        // swizzle span in bytes
   static constexpr int kHalves = HD * 2 / kSpan;           // spans per row
   static constexpr int kTile = kBlk * HD * 2;              // 128 rows
-  static constexpr int kStages = HD == 128 ? 5 : 8;
-  static constexpr int kSmem = 1024 + 2 * kTile + kStages * kTile;
+  static constexpr int kSlots = HD == 128 ? 7 : 10;        // query tiles and ring stages together
 };
 
 // ------------------------------------------------------------------ work list
@@ -70,111 +75,109 @@ __device__ __forceinline__ SeqShape seq_shape(const TreeParams& p, int b, bool r
 
 __device__ __forceinline__ int nodes_per_group(const TreeParams& p) { return p.npt * (p.two ? 2 : 1); }
 
-// Keys [kstart, end) of tile group tp: with the causal chain a group ends at its last node;
-// a window starts at the earliest key that any of its nodes may see (on a page boundary).
-__device__ __forceinline__ void key_range(const TreeParams& p, const SeqShape& s, int tp, int& kstart, int& end) {
+// An entry of the work list: the tile groups [tp, tp + team) of sequence b.  All of them
+// start at the same key; with the causal chain each ends at its own last node.  A window starts
+// at the earliest key that any of their nodes may see (on a page boundary).
+struct Entry {
+  int b, tp;           // first tile group
+  SeqShape s;
+  int kstart, nblk;    // blocks of the longest
+};
+
+// end of the keys of tile group tp (0 if it has no nodes)
+__device__ __forceinline__ int group_end(const TreeParams& p, const SeqShape& s, int tp) {
   const int per = nodes_per_group(p), first = tp * per;
-  const int last = min(s.cnt, first + per) - 1;
-  end = s.len + (p.a.mask ? s.cnt : last + 1);
-  kstart = 0;
+  if (first >= s.cnt) return 0;
+  return s.len + (p.a.mask ? s.cnt : min(s.cnt, first + per));
+}
+
+__device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool record) {
+  Entry x;
+  const int groups = (p.ntp + p.team - 1) / p.team;
+  x.b = e / groups;
+  x.tp = (e - x.b * groups) * p.team;
+  x.s = seq_shape(p, x.b, record);
+  x.kstart = x.nblk = 0;
+  const int per = nodes_per_group(p), first = x.tp * per;
+  if (first >= x.s.cnt) return x;
+  const int end = group_end(p, x.s, min(x.tp + p.team, (x.s.cnt + per - 1) / per) - 1);
   if (p.a.window > 0) {
-    const int pos = s.len + (p.a.mask || p.a.positions ? 0 : first);  // the earliest position of its nodes
-    kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
+    const int pos = x.s.len + (p.a.mask || p.a.positions ? 0 : first);  // the earliest position of its nodes
+    x.kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
   }
-}
-__device__ __forceinline__ int group_blocks(const TreeParams& p, const SeqShape& s, int tp) {
-  if (tp * nodes_per_group(p) >= s.cnt) return 0;
-  int k0, e;
-  key_range(p, s, tp, k0, e);
-  return (e - k0 + kBlk - 1) / kBlk;
-}
-// units of one KV head of a sequence
-__device__ __forceinline__ int head_units(const TreeParams& p, const SeqShape& s) {
-  if (s.cnt <= 0) return 0;
-  const int per = nodes_per_group(p), n = (s.cnt + per - 1) / per;
-  if (p.a.mask || n == 1) return n * group_blocks(p, s, 0);
-  int u = 0;
-  for (int t = 0; t < n; ++t) u += group_blocks(p, s, t);
-  return u;
+  x.nblk = (end - x.kstart + kBlk - 1) / kBlk;
+  return x;
 }
 
-// Inclusive prefix sums of the sequences' units into pre[0..batch] (pre[0] = 0); all
-// threads of the block.
+__device__ __forceinline__ int num_entries(const TreeParams& p) { return p.c.batch * ((p.ntp + p.team - 1) / p.team); }
+
+constexpr int kScan = 128;  // threads that add up the work list
+
+// Prefix sums of the entries' units: thread i < kScan owns entries [i * chunk, (i + 1) *
+// chunk), pre[i] is the number of units before them, pre[kScan] that of all.
 __device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool record) {
-  const int B = p.c.batch, nt = (int)blockDim.x;
-  if (threadIdx.x == 0) pre[0] = 0;
-  int carry = 0;
-  for (int base = 0; base < B; base += nt) {
-    const int b = base + (int)threadIdx.x;
-    int x = 0;
-    if (b < B) x = head_units(p, seq_shape(p, b, record)) * p.c.n_kv_heads;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int E = num_entries(p), chunk = (E + kScan - 1) / kScan;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = 0;
+  if (threadIdx.x < kScan)
+    for (int e = (int)threadIdx.x * chunk; e < min(E, ((int)threadIdx.x + 1) * chunk); ++e)
+      x += make_entry(p, e, record).nblk * p.c.n_kv_heads;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[w] = x;
-    __syncthreads();
-    int add = carry;
-    for (int i = 0; i < w; ++i) add += warp_sums[i];
-    if (b < B) pre[b + 1] = x + add;
-    for (int i = 0; i < nt / 32; ++i) carry += warp_sums[i];
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  if (lane == 31 && w < kScan / 32) warp_sums[w] = x;
+  __syncthreads();
+  if (threadIdx.x < kScan) {
+    for (int i = 0; i < w; ++i) x += warp_sums[i];
+    pre[threadIdx.x + 1] = x;
+  }
+  if (threadIdx.x == 0) pre[0] = 0;
+  __syncthreads();
 }
 
-// run of CTA c of G: units [c * U / G, (c + 1) * U / G).  G <= U: every run has a unit, so the
-// parts of an item are those of consecutive CTAs.
-__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid, U); }
+// run of team g of G: units [g * U / G, (g + 1) * U / G).  G <= U: every run has a unit, so the
+// parts of an item are those of consecutive teams.
+__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid / p.team, U); }
 __device__ __forceinline__ int run_begin(int c, int U, int G) { return (int)((long long)c * U / G); }
 __device__ __forceinline__ int run_owner(int u, int U, int G) { return (int)(((long long)(u + 1) * G - 1) / U); }
 
-// The item that unit u belongs to (its run part is filled in by the caller).
-__device__ Item locate(const TreeParams& p, const int* pre, int u) {
-  Item it;
-  int lo = 0, hi = p.c.batch - 1;  // the last b with pre[b] <= u and units of its own
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (pre[m] <= u) lo = m; else hi = m - 1;
-  }
-  it.b = lo;
-  const SeqShape s = seq_shape(p, lo, false);
-  it.len = s.len;
-  it.cnt = s.cnt;
-  const int per_head = (pre[lo + 1] - pre[lo]) / p.c.n_kv_heads;
-  int r = u - pre[lo];
-  it.kvh = r / per_head;
-  it.unit0 = pre[lo] + it.kvh * per_head;
-  r -= it.kvh * per_head;
-  if (p.a.mask) {
-    it.nblk = group_blocks(p, s, 0);
-    it.tp = r / it.nblk;
-    it.unit0 += it.tp * it.nblk;
-  } else {
-    it.tp = 0;
-    it.nblk = group_blocks(p, s, 0);
-    while (r >= it.nblk) {
-      r -= it.nblk;
-      it.unit0 += it.nblk;
-      it.nblk = group_blocks(p, s, ++it.tp);
-    }
-  }
-  key_range(p, s, it.tp, it.kstart, it.end);
-  return it;
-}
-
-// Walks the items of a run.
+// Walks the items of a run for tile group `member` of its team.
 struct Run {
-  int u, u1;
+  int u, u1, member;
   Item it;
+  // the next item with blocks of this group in the run
   __device__ __forceinline__ bool next(const TreeParams& p, const int* pre) {
-    if (u >= u1) return false;
-    it = locate(p, pre, u);
-    it.ja = u - it.unit0;
-    it.jb = min(it.nblk, it.ja + (u1 - u));
-    u += it.jb - it.ja;
-    return true;
+    while (u < u1) {
+      int lo = 0, hi = kScan - 1;  // the last chunk that starts at or before u (so it has units)
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (pre[m] <= u) lo = m; else hi = m - 1;
+      }
+      const int chunk = (num_entries(p) + kScan - 1) / kScan;
+      int e = lo * chunk, first = pre[lo];
+      Entry x = make_entry(p, e, false);
+      while (u >= first + x.nblk * p.c.n_kv_heads) {
+        first += x.nblk * p.c.n_kv_heads;
+        x = make_entry(p, ++e, false);
+      }
+      it.b = x.b;
+      it.tp = x.tp + member;
+      it.len = x.s.len;
+      it.cnt = x.s.cnt;
+      it.kvh = (u - first) / x.nblk;
+      it.unit0 = first + it.kvh * x.nblk;
+      it.kstart = x.kstart;
+      it.end = group_end(p, x.s, it.tp);
+      it.nblk = max(0, it.end - it.kstart + kBlk - 1) / kBlk;
+      it.ja = u - it.unit0;
+      const int stop = min(x.nblk, it.ja + (u1 - u));
+      u = it.unit0 + stop;
+      it.jb = min(stop, it.nblk);
+      if (it.ja < it.jb) return true;
+    }
+    return false;
   }
 };
 
@@ -196,8 +199,10 @@ __device__ __forceinline__ Row make_row(const TreeParams& p, const Item& it, int
   if (node < 0) return r;
   const long long at = (long long)it.b * p.a.n_nodes + node;
   r.pos = it.len + node;
-  if (p.a.positions) r.pos = min(max(__ldg(p.a.positions + at), it.len), it.len + it.cnt - 1);
-  if (p.a.window > 0) r.lo = r.pos - p.a.window + 1;
+  if (p.a.window > 0) {
+    if (p.a.positions) r.pos = min(max(__ldg(p.a.positions + at), it.len), it.len + it.cnt - 1);
+    r.lo = r.pos - p.a.window + 1;
+  }
   if (p.a.mask) r.mask = p.a.mask + at * p.words;
   return r;
 }
@@ -258,23 +263,28 @@ struct TreeShared {
   uint32_t tmem;
   int abort;
   int bad_v;             // a masked block held a V that is not finite
-  int pre[kOpMaxBatch + 1];
-  int warp_sums[kTreeThreads / 32];
-  float2 ml[kBlk];       // stream 1's (m, sum) for the merge
-  unsigned long long bars[2 * 8 + 8];
+  int pre[kScan + 1];
+  int warp_sums[kScan / 32];
+  float2 ml[2][kBlk];    // the streams' (m, sum) for the merge
+  unsigned long long bars[2 * 9 + 9];
 };
 
 template <int HD>
+struct TreeSmem {
+  static constexpr int kBytes = TreeCfg<HD>::kSlots * TreeCfg<HD>::kTile + (int)sizeof(TreeShared);
+  static_assert(kBytes <= 232448, "exceeds the 227 KB per-block shared memory limit");
+};
+
 struct Bars {
   uint32_t base;
-  static constexpr int S = TreeCfg<HD>::kStages;
   __device__ uint32_t full(int s) const { return base + 8 * s; }
-  __device__ uint32_t empty(int s) const { return base + 8 * (S + s); }
-  __device__ uint32_t qfull() const { return base + 8 * (2 * S); }
-  __device__ uint32_t qempty() const { return base + 8 * (2 * S + 1); }
-  __device__ uint32_t sfull(int s) const { return base + 8 * (2 * S + 2 + s); }
-  __device__ uint32_t pready(int s) const { return base + 8 * (2 * S + 4 + s); }
-  __device__ uint32_t ofull(int s) const { return base + 8 * (2 * S + 6 + s); }
+  __device__ uint32_t empty(int s) const { return base + 8 * (9 + s); }
+  __device__ uint32_t qfull() const { return base + 8 * 18; }
+  __device__ uint32_t qempty() const { return base + 8 * 19; }
+  __device__ uint32_t sfull(int s) const { return base + 8 * (20 + s); }
+  __device__ uint32_t pready(int s) const { return base + 8 * (22 + s); }
+  __device__ uint32_t ofull(int s) const { return base + 8 * (24 + s); }
+  __device__ uint32_t meet() const { return base + 8 * 26; }
 };
 
 __device__ __forceinline__ bool nonfinite2(uint32_t u) {
@@ -320,10 +330,10 @@ __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key, bool
 // Only after a masked block held such values (never with finite caches): plain loads.
 template <int HD>
 __device__ __noinline__ void add_nonfinite(const TreeParams& p, const Item& it, const Row& r, const uint16_t* q, float m, int c0,
-                                           int j0, int jstep, float* o) {
+                                           float* o) {
   const uint16_t* K = static_cast<const uint16_t*>(p.c.k);
   const uint16_t* V = static_cast<const uint16_t*>(p.c.v);
-  for (int j = it.ja + j0; j < it.jb; j += jstep) {
+  for (int j = it.ja; j < it.jb; ++j) {
     const int k0 = it.kstart + j * kBlk;
     if (!masked_block(p, it, k0)) continue;
     for (int w = 0; w < kBlk / 32; ++w) {
@@ -346,29 +356,78 @@ __device__ __noinline__ void add_nonfinite(const TreeParams& p, const Item& it, 
   }
 }
 
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Store 16 columns of a row: the result (one 32-byte sector), or the row's part of it (a
+// float4 per 4 columns, rows side by side).
+__device__ __forceinline__ void put16(const float (&o)[16], bool whole, float inv, uint16_t* dst, float4* part, int c) {
+  if (whole) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+    *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) __stcg(part + (c / 4 + i) * kBlk, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tq,
                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = TreeCfg<HD>;
-  extern __shared__ uint8_t raw[];
-  __shared__ TreeShared sh;
-  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  uint8_t* const gbase = raw + (base - smem_u32(raw));
-  const uint32_t q_s = base, ring = base + 2 * C::kTile;
-  uint8_t* const ring_g = gbase + 2 * C::kTile;
-  float* const exch = reinterpret_cast<float*>(gbase + C::kTile);  // two = 0: the second Q tile is free
-  Bars<HD> bars{smem_u32(sh.bars)};
+  // (no static shared memory: the tiles start at its first byte, which is aligned to 1024)
+  extern __shared__ __align__(1024) uint8_t raw[];
+  TreeShared& sh = *reinterpret_cast<TreeShared*>(raw + C::kSlots * C::kTile);
+  const uint32_t base = smem_u32(raw);
+  if (base & 1023u) {
+    if (threadIdx.x == 0) op_error(p.a.status, MK_ERR_UNSUPPORTED, -1, (int)base, 0);
+    return;
+  }
+  const bool two = p.two != 0;
+  const int stages = C::kSlots - (two ? 2 : 1);
+  const uint32_t q_s = base, ring = base + (two ? 2 : 1) * C::kTile;
+  uint8_t* const ring_g = raw + (ring - base);
+  const Bars bars{smem_u32(sh.bars)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
-  __shared__ unsigned long long merge_bar;  // the two warpgroups meet here
-  const uint32_t mbar = smem_u32(&merge_bar);
 
   pdl_trigger();
+  if (warp == 8 && lane < 3) {
+    const CUtensorMap* tm = lane == 0 ? &tk : lane == 1 ? &tv : &tq;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
   if (threadIdx.x == 0) {
     sh.abort = 0;
     sh.bad_v = 0;
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 1);
     }
@@ -379,153 +438,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(bars.pready(s), 128);
       mbar_init(bars.ofull(s), 1);
     }
-    mbar_init(mbar, 256);
+    mbar_init(bars.meet(), 256);
     fence_proxy_async_smem();
   }
-  scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
-  const int U = sh.pre[p.c.batch];
-  const int G = run_count(p, U);
-  if ((int)blockIdx.x >= G) return;  // (the whole CTA)
-  const int u0 = run_begin(blockIdx.x, U, G), u1 = run_begin(blockIdx.x + 1, U, G);
-  if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
   tc_fence_before();
-  __syncthreads();
+  scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const bool two = p.two != 0;
-  Run run{u0, u1, {}};
+  const int U = sh.pre[kScan];
+  const int G = run_count(p, U), team = (int)blockIdx.x / p.team;
+  if (team >= G) {  // (the whole CTA)
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int u0 = run_begin(team, U, G);
+  Run run{u0, run_begin(team + 1, U, G), (int)blockIdx.x % p.team, {}};
 
-  if (warp == 8) {
-    // ---------------------------------------------------------------- producer
-    // lane = (page of the block) + 8 * (span of the row): one copy per lane
-    uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
-    const int pg = lane & 7, half = lane >> 3;
-    bool ok = true;
-    while (ok && run.next(p, sh.pre)) {
-      const Item& it = run.it;
-      const int rows = p.npt * p.gs;
-      // this lane's page of the next block is looked up one block ahead
-      int key = it.kstart + it.ja * kBlk + pg * kOpPage;
-      int next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
-      for (int j = it.ja; ok && j < it.jb; ++j) {
-        const int k0 = it.kstart + j * kBlk;
-        const int live = min(kBlk / kOpPage, (it.end - k0 + kOpPage - 1) / kOpPage);
-        const int row = (next_page * p.c.n_kv_heads + it.kvh) * kOpPage;
-        key = k0 + kBlk + pg * kOpPage;
-        if (j + 1 < it.jb) next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
-        for (int kv = 0; kv < 2; ++kv) {
-          const int s = fill % C::kStages;
-          const uint32_t ph = (fill / C::kStages) & 1;
-          if (!(ok = op_wait(bars.empty(s), ph ^ 1, abort, p.a.status, 1))) break;
-          if (lane == 0) mbar_expect_tx(bars.full(s), (uint32_t)live * kOpPage * HD * 2);
-          __syncwarp();
-          if (pg < live && half < C::kHalves)
-            op_tma_2d(ring + s * C::kTile + half * (kBlk * C::kSpan) + pg * (kOpPage * C::kSpan), kv ? &tv : &tk,
-                      half * (C::kSpan / 2), row, bars.full(s));
-          ++fill;
-          if (kv == 0 && j == it.ja) {  // the item's queries, once the last item's products have read theirs
-            if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
-            ++qphase;
-            const int tiles = two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1;
-            if (lane == 0) {
-              mbar_expect_tx(bars.qfull(), (uint32_t)(tiles * rows * HD * 2));
-              for (int t = 0; t < tiles; ++t)
-                for (int h = 0; h < C::kHalves; ++h)
-                  op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), it.kvh * p.gs,
-                            it.tp * nodes_per_group(p) + t * p.npt, it.b, bars.qfull());
-            }
-            __syncwarp();
-          }
-        }
-      }
-    }
-    // an abandoned run leaves copies in flight: wait for them (bounded)
-    if (*abort) {
-      const uint32_t n = min(fill, (uint32_t)C::kStages);
-      for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(bars.full(f % C::kStages), (f / C::kStages) & 1, 10000000ll);
-      if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
-    }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMA issue
-    constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
-    constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
-    constexpr uint32_t kSbo = 8 * C::kSpan;
-    uint32_t used = 0;                  // ring slots of earlier items
-    uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
-    bool ok = true;
-    while (ok && run.next(p, sh.pre)) {
-      const int nb = run.it.jb - run.it.ja;
-      const int steps = two ? 2 * nb : nb;
-      if (!(ok = op_wait(bars.qfull(), nq & 1, abort, p.a.status, 3))) break;
-      tc_fence_after();
-      ++nq;
-      // step t: stream t & 1, block t >> 1 (two) or t
-      auto issue_s = [&](int t) -> bool {
-        const int st = t & 1, blk = two ? t >> 1 : t;
-        const uint32_t slot = used + 2 * blk, s = slot % C::kStages;
-        if (!op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 4)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a = q_s + (two ? st : 0) * C::kTile, b = ring + s * C::kTile;
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan;
-            umma_bf16(tmem + kTmemS + 128 * st, umma_sdesc_sw(a + off, 16, kSbo, C::kSpan),
-                      umma_sdesc_sw(b + off, 16, kSbo, C::kSpan), idesc_s, kk > 0);
-          }
-          umma_commit(bars.sfull(st));
-          if (!two || st == 1) umma_commit(bars.empty(s));
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = issue_s(0) && (steps < 2 || issue_s(1));
-      for (int t = 0; ok && t < steps; ++t) {
-        const int st = t & 1, blk = two ? t >> 1 : t;
-        const uint32_t slot = used + 2 * blk + 1, s = slot % C::kStages;
-        if (!(ok = op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 5))) break;
-        if (!(ok = op_wait(bars.pready(st), np[st] & 1, abort, p.a.status, 6))) break;
-        ++np[st];
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t b = ring + s * C::kTile;
-          const bool first = two ? blk == 0 : blk == st;
-#pragma unroll
-          for (int kk = 0; kk < kBlk / 16; ++kk)
-            umma_bf16_ta(tmem + kTmemO + 128 * st, tmem + kTmemS + 128 * st + 8 * kk,
-                         umma_sdesc_sw(b + kk * 16 * C::kSpan, kBlk * C::kSpan, kSbo, C::kSpan), idesc_o, !first || kk > 0);
-          if (!two || st == 1) umma_commit(bars.empty(s));
-          if (t + 2 >= steps) umma_commit(bars.ofull(st));
-        }
-        __syncwarp();
-        if (t + 2 < steps) {
-          ok = issue_s(t + 2);
-        } else if (t + 1 == steps && lane == 0) {
-          umma_commit(bars.qempty());
-        }
-      }
-      used += 2 * nb;
-    }
-    if (*abort) {  // let the products in flight end before the memory goes
-      if (lane == 0) umma_commit(bars.ofull(0));
-      __syncwarp();
-      const uint64_t t0 = gtime();
-      while ((long long)(gtime() - t0) < 10000000ll) {}
-    }
-  } else {
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------------------------------------------------------- softmax streams
     const int st = warp >> 2;                       // 0 or 1
     const int row = (int)threadIdx.x & 127;         // = lane of tensor memory
-    const uint32_t tS = tmem + kTmemS + 128 * st + ((uint32_t)(warp & 3) << 21);
-    const uint32_t tO = tmem + kTmemO + 128 * st + ((uint32_t)(warp & 3) << 21);
-    uint32_t ns = 0, no = 0, used = 0, nm = 0;      // S tiles, finished items, ring slots, meetings
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t tS = tmem + kTmemS + 128 * st + lanes;
+    const uint32_t tO = tmem + kTmemO + lanes;      // of stream 0; stream 1's is 128 columns on
+    uint32_t ns = 0, no[2] = {0, 0}, used = 0, nm = 0;  // S tiles, finished items per stream, ring slots, meetings
     bool ok = true;
     auto meet = [&]() -> bool {                     // all 256 threads of the two streams
-      mbar_arrive(mbar);
-      const bool r = op_wait(mbar, nm & 1, abort, p.a.status, 7);
-      ++nm;
-      return r;
+      mbar_arrive(bars.meet());
+      return op_wait(bars.meet(), nm++ & 1, abort, p.a.status, 7);
     };
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     while (ok && run.next(p, sh.pre)) {
       const Item& it = run.it;
       const int nb = it.jb - it.ja;
@@ -534,6 +477,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       int node = it.tp * nodes_per_group(p) + tile * p.npt + node_in;
       if (node_in >= p.npt || node >= it.cnt) node = -1;
       const Row r = make_row(p, it, node);
+      const bool warp_live = __any_sync(0xffffffffu, node >= 0);
       float m = -INFINITY, l = 0.f;
       const int b0 = two ? 0 : st, bstep = two ? 1 : 2;
       for (int blk = b0; ok && blk < nb; blk += bstep) {
@@ -543,78 +487,74 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (masked) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] = sees32(p, it, r, k0 + 32 * w);
-          const uint32_t slot = used + 2 * blk + 1, s = slot % C::kStages;
-          if (!(ok = op_wait(bars.full(s), (slot / C::kStages) & 1, abort, p.a.status, 8))) break;
-          const int live = it.end - k0;
-          clean_v<HD>(ring_g + s * C::kTile, live, two ? (int)threadIdx.x : row, two ? 256 : 128, &sh.bad_v);
+          const uint32_t slot = used + 2 * blk + 1, s = slot % stages;
+          if (!(ok = op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 8))) break;
+          clean_v<HD>(ring_g + s * C::kTile, it.end - k0, two ? (int)threadIdx.x : row, two ? 256 : 128, &sh.bad_v);
           fence_proxy_async_smem();
           if (two && !(ok = meet())) break;
         }
         if (!(ok = op_wait(bars.sfull(st), ns & 1, abort, p.a.status, 9))) break;
         ++ns;
         tc_fence_after();
-        uint32_t s[kBlk];
+        if (warp_live) {
+          uint32_t s[kBlk];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
+          for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait32(s + 32 * i);
-        if (masked) {
+          for (int i = 0; i < 4; ++i) tmem_wait32(s + 32 * i);
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < kBlk; ++i)
-            if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int i = 0; i < kBlk; ++i)
+              if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kBlk; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        const float mnew = fmaxf(m, top);
-        const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = mnew == m ? 1.f : ex2(m - mnew);
-          if (blk != b0) {
+          for (int i = 0; i < kBlk; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          const float mnew = fmaxf(m, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * p.scale_log2);
+          const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = mnew == m ? 1.f : ex2(m - mnew);
+            if (blk != b0) {
+#pragma unroll 1
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + 128 * st + c, o);
+                tmem_wait16(o);
 #pragma unroll
-            for (int c = 0; c < HD; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tO + c, o);
-              tmem_wait16(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(tO + c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(tO + 128 * st + c, o);
+              }
             }
+            l *= f;
+            m = mnew;
           }
-          l *= f;
-          m = mnew;
-        }
-        const float mm = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mm = m == -INFINITY ? 0.f : m;
+          const uint64_t neg = pack2(-mm, -mm);
+          uint64_t sum[2] = {0, 0};  // (two pairs of zeros)
 #pragma unroll
-        for (int c = 0; c < kBlk / 32; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < kBlk / 32; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = ex2(fmaf(__uint_as_float(s[32 * c + 2 * i]), p.scale_log2, -mm));
-            const float b = ex2(fmaf(__uint_as_float(s[32 * c + 2 * i + 1]), p.scale_log2, -mm));
-            sum[(2 * i) & 3] += a;
-            sum[(2 * i + 1) & 3] += b;
-            pk[i] = pack_bf16(a, b);
+            for (int i = 0; i < 16; ++i) {
+              const int j = 32 * c + 2 * i;
+              float2 x = unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2, neg));
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum[i & 1] = add2(sum[i & 1], pack2(x.x, x.y));
+              pk[i] = pack_bf16(x.x, x.y);
+            }
+            tmem_st16(tS + 16 * c, pk);
           }
-          tmem_st16(tS + 16 * c, pk);
+          const float2 total = unpack2(add2(sum[0], sum[1]));
+          l += total.x + total.y;
+          tmem_wait_st();
+          tc_fence_before();
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
         mbar_arrive(bars.pready(st));
       }
       if (!ok) break;
       // ------------------------------------------------------------ the item's result
-      const bool had = nb > b0;  // this stream had a block
-      if (had) {
-        if (!(ok = op_wait(bars.ofull(st), no & 1, abort, p.a.status, 10))) break;
-        ++no;
-        tc_fence_after();
-      }
       used += 2 * nb;
-      const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
       const bool whole = nb == it.nblk;
       const uint16_t* qrow = nullptr;
       uint16_t* dst = nullptr;
@@ -627,90 +567,183 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int slot = it.unit0 + it.ja == u0 ? 0 : 1;
       const long long pt = ((long long)blockIdx.x * 2 + slot) * (two ? 2 : 1) + tile;
       float4* part = reinterpret_cast<float4*>(p.part) + pt * (HD / 4) * kBlk + row;
-      float w0 = 1.f, w1 = 0.f;  // weights of the two streams' sums
-      if (!two) {
-        if (st == 1) sh.ml[row] = make_float2(m, l);
-        if (!(ok = meet())) break;
-        if (st == 0) {
-          const float2 o = sh.ml[row];
-          const float top = fmaxf(m, o.x), t = top == -INFINITY ? 0.f : top;
-          w0 = ex2(m - t);
-          w1 = ex2(o.x - t);
-          l = l * w0 + o.y * w1;
-          m = top;
-        }
-      }
-      const bool other = nb > 1;  // stream 1 had a block (two = 0)
-      if (st == 0 || two) {
+      if (two) {
+        if (!(ok = op_wait(bars.ofull(st), no[st] & 1, abort, p.a.status, 10))) break;
+        ++no[st];
+        tc_fence_after();
+        const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
         if (!whole && node >= 0) p.part_ml[pt * kBlk + row] = make_float2(m, l);
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (warp_live) {
 #pragma unroll 1
-      for (int h = 0; ok && h < 2; ++h) {  // halves of the columns
-#pragma unroll 1
-        for (int c = h * (HD / 2); c < (h + 1) * (HD / 2); c += 16) {
-          if (!two && st == 0) break;
-          uint32_t u[16];
-          float o[16];
-          if (had) {
-            tmem_ld16(tO + c, u);
-            tmem_wait16(u);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = had ? __uint_as_float(u[i]) : 0.f;
-          if (fix && had && node >= 0) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, b0, bstep, o);
-          if (!two) {  // stream 1 hands its columns over
-            if (had) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) exch[(c - h * (HD / 2) + i) * kBlk + row] = o[i];
-            }
-          } else if (node >= 0) {
-            if (whole) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-              *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[(c / 4 + i) * kBlk] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-          }
-        }
-        if (two) continue;
-        if (!(ok = meet())) break;
-        if (st == 0) {
-#pragma unroll 1
-          for (int c = h * (HD / 2); c < (h + 1) * (HD / 2); c += 16) {
+          for (int c = 0; c < HD; c += 16) {
             uint32_t u[16];
             float o[16];
-            tmem_ld16(tO + c, u);
+            tmem_ld16(tO + 128 * st + c, u);
             tmem_wait16(u);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * w0;
-            // (m is the merged maximum here, to which the scaled sums are relative)
-            if (fix && node >= 0) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, b0, bstep, o);
-            if (other) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] += w1 * exch[(c - h * (HD / 2) + i) * kBlk + row];
-            }
+            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]);
             if (node >= 0) {
-              if (whole) {
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-                *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[(c / 4 + i) * kBlk] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              }
+              if (fix) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, o);
+              put16(o, whole, inv, dst, part, c);
             }
           }
         }
+        tc_fence_before();
+      } else {
+        // The streams' rows lie in the same lanes: each warpgroup joins one half of the columns
+        // of both sums.
+        sh.ml[st][row] = make_float2(m, l);
+        if (!(ok = meet())) break;
+        const float2 a = sh.ml[0][row], b = sh.ml[1][row];
+        const float top = fmaxf(a.x, b.x), mm = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2(a.x - mm), w1 = ex2(b.x - mm);
+        l = a.y * w0 + b.y * w1;
+        const bool other = nb > 1;  // stream 1 had a block
+        if (!(ok = op_wait(bars.ofull(0), no[0]++ & 1, abort, p.a.status, 10))) break;
+        if (other && !(ok = op_wait(bars.ofull(1), no[1]++ & 1, abort, p.a.status, 11))) break;
+        tc_fence_after();
+        const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
+        if (!whole && node >= 0 && st == 0) p.part_ml[pt * kBlk + row] = make_float2(top, l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = st * (HD / 2); c < (st + 1) * (HD / 2); c += 16) {
+            uint32_t u[16], v[16];
+            float o[16];
+            tmem_ld16(tO + c, u);
+            if (other) tmem_ld16(tO + 128 + c, v);
+            tmem_wait16(u);
+            tmem_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = w0 * __uint_as_float(u[i]) + (other ? w1 * __uint_as_float(v[i]) : 0.f);
+            if (node >= 0) {
+              if (fix) add_nonfinite<HD>(p, it, r, qrow, mm, c, o);
+              put16(o, whole, inv, dst, part, c);
+            }
+          }
+        }
+        tc_fence_before();
         if (!(ok = meet())) break;
       }
-      tc_fence_before();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ---------------------------------------------------------------- producer
+      // lane = (page of the block) + 8 * (span of the row): one copy per lane
+      uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
+      const int pg = lane & 7, half = lane >> 3;
+      bool ok = true;
+      while (ok && run.next(p, sh.pre)) {
+        const Item& it = run.it;
+        const int rows = p.npt * p.gs;
+        // this lane's page of the next block is looked up one block ahead
+        int key = it.kstart + it.ja * kBlk + pg * kOpPage;
+        int next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
+        for (int j = it.ja; ok && j < it.jb; ++j) {
+          const int k0 = it.kstart + j * kBlk;
+          const int live = min(kBlk / kOpPage, (it.end - k0 + kOpPage - 1) / kOpPage);
+          const int row = (next_page * p.c.n_kv_heads + it.kvh) * kOpPage;
+          key = k0 + kBlk + pg * kOpPage;
+          if (j + 1 < it.jb) next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
+          for (int kv = 0; kv < 2; ++kv) {
+            const int s = fill % stages;
+            const uint32_t ph = (fill / stages) & 1;
+            if (!(ok = op_wait(bars.empty(s), ph ^ 1, abort, p.a.status, 1))) break;
+            if (lane == 0) mbar_expect_tx(bars.full(s), (uint32_t)live * kOpPage * HD * 2);
+            __syncwarp();
+            if (pg < live && half < C::kHalves)
+              op_tma_2d(ring + s * C::kTile + half * (kBlk * C::kSpan) + pg * (kOpPage * C::kSpan), kv ? &tv : &tk,
+                        half * (C::kSpan / 2), row, bars.full(s));
+            ++fill;
+            if (kv == 0 && j == it.ja) {  // the item's queries, once the last item's products have read theirs
+              if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
+              ++qphase;
+              const int tiles = two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1;
+              if (lane == 0) {
+                mbar_expect_tx(bars.qfull(), (uint32_t)(tiles * rows * HD * 2));
+                for (int t = 0; t < tiles; ++t)
+                  for (int h = 0; h < C::kHalves; ++h)
+                    op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), it.kvh * p.gs,
+                              it.tp * nodes_per_group(p) + t * p.npt, it.b, bars.qfull());
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      // an abandoned run leaves copies in flight: wait for them (bounded)
+      if (*abort) {
+        const uint32_t n = min(fill, (uint32_t)stages);
+        for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(bars.full(f % stages), (f / stages) & 1, 10000000ll);
+        if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMA issue
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
+      constexpr uint32_t kSbo = 8 * C::kSpan;
+      uint32_t used = 0;                  // ring slots of earlier items
+      uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
+      const uint32_t tm = uniform(tmem);
+      // descriptors of the first query tile and ring stage; a tile further is kTile / 16 more
+      const uint64_t dq = umma_sdesc_sw(q_s, 16, kSbo, C::kSpan), dk = umma_sdesc_sw(ring, 16, kSbo, C::kSpan);
+      const uint64_t dv = umma_sdesc_sw(ring, kBlk * C::kSpan, kSbo, C::kSpan);
+      bool ok = true;
+      while (ok && run.next(p, sh.pre)) {
+        const int nb = (int)uniform((uint32_t)(run.it.jb - run.it.ja));
+        const int steps = two ? 2 * nb : nb;
+        if (!(ok = op_wait(bars.qfull(), nq & 1, abort, p.a.status, 3))) break;
+        tc_fence_after();
+        ++nq;
+        // step t: stream t & 1, block t >> 1 (two) or t
+        auto issue_s = [&](int t) -> bool {
+          const uint32_t st = t & 1, slot = used + 2 * (two ? t >> 1 : t), s = slot % stages;
+          if (!op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 4)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t a = dq + (two ? st : 0) * (C::kTile / 16), b = dk + s * (C::kTile / 16);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint32_t off = ((kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan) / 16;
+              umma_bf16(tm + kTmemS + 128 * st, a + off, b + off, idesc_s, kk > 0);
+            }
+            umma_commit(bars.sfull(st));
+            if (!two || st == 1) umma_commit(bars.empty(s));
+          }
+          __syncwarp();
+          return true;
+        };
+        ok = issue_s(0) && (steps < 2 || issue_s(1));
+        for (int t = 0; ok && t < steps; ++t) {
+          const uint32_t st = t & 1, blk = two ? t >> 1 : t;
+          const uint32_t slot = used + 2 * blk + 1, s = slot % stages;
+          if (!(ok = op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 5))) break;
+          if (!(ok = op_wait(bars.pready(st), (st ? np[1] : np[0]) & 1, abort, p.a.status, 6))) break;
+          if (st) ++np[1]; else ++np[0];
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t b = dv + s * (C::kTile / 16);
+            const bool first = two ? blk == 0 : blk == st;
+#pragma unroll
+            for (int kk = 0; kk < kBlk / 16; ++kk)
+              umma_bf16_ta(tm + kTmemO + 128 * st, tm + kTmemS + 128 * st + 8 * kk, b + kk * C::kSpan, idesc_o, !first || kk > 0);
+            if (!two || st == 1) umma_commit(bars.empty(s));
+            if (t + 2 >= steps) umma_commit(bars.ofull(st));
+            if (t + 1 == steps) umma_commit(bars.qempty());
+          }
+          __syncwarp();
+          if (t + 2 < steps) ok = issue_s(t + 2);
+        }
+        used += 2 * nb;
+      }
+      if (*abort) {  // let the products in flight end before the memory goes
+        if (elect_one()) umma_commit(bars.ofull(0));
+        __syncwarp();
+        const uint64_t t0 = gtime();
+        while ((long long)(gtime() - t0) < 10000000ll) {}
+      }
     }
   }
   tc_fence_before();
@@ -724,14 +757,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // ------------------------------------------------------------------ joining the parts
 // One block per (item, row tile, 32 rows, 16 columns): thread = (row, 4 columns).
 constexpr int kJoinThreads = 128;
+static_assert(kJoinThreads >= kScan, "the join adds up the work list too");
 
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ int pre[kOpMaxBatch + 1];
-  __shared__ int warp_sums[kJoinThreads / 32];
-  pdl_wait();
+  __shared__ int pre[kScan + 1];
+  __shared__ int warp_sums[kScan / 32];
+  // (the inputs of the work list are older than the kernel before this one)
   scan_units(p, pre, warp_sums, false);
-  const int U = pre[p.c.batch];
+  pdl_wait();
+  const int U = pre[kScan];
   const int tiles = p.two ? 2 : 1;
   int i = blockIdx.x;
   const int rowq = i & 3;
@@ -741,23 +776,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int tp = i % p.ntp;
   i /= p.ntp;
   const int kvh = i % p.c.n_kv_heads, b = i / p.c.n_kv_heads;
-  const SeqShape s = seq_shape(p, b, false);
-  const int nblk = group_blocks(p, s, tp);
-  if (nblk == 0) return;
-  int g0 = pre[b] + kvh * ((pre[b + 1] - pre[b]) / p.c.n_kv_heads);
-  if (p.a.mask)
-    g0 += tp * nblk;
-  else
-    for (int t = 0; t < tp; ++t) g0 += group_blocks(p, s, t);
+  const int member = tp % p.team, e = b * ((p.ntp + p.team - 1) / p.team) + tp / p.team;
+  const int chunk = (num_entries(p) + kScan - 1) / kScan;
+  int g0 = pre[e / chunk];
+  for (int x = e / chunk * chunk; x < e; ++x) g0 += make_entry(p, x, false).nblk * p.c.n_kv_heads;
+  const Entry x = make_entry(p, e, false);
+  const SeqShape s = x.s;
+  const int end = group_end(p, s, tp);
+  if (end == 0) return;
+  g0 += kvh * x.nblk;
+  const int nblk = (end - x.kstart + kBlk - 1) / kBlk;
   const int G = run_count(p, U);
   const int c0 = run_owner(g0, U, G), c1 = run_owner(g0 + nblk - 1, U, G);
   if (c0 == c1) return;  // written whole
   const int row = rowq * 32 + (threadIdx.x & 31), c4 = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int node_in = row / p.gs, node = tp * nodes_per_group(p) + tile * p.npt + node_in;
   if (node_in >= p.npt || node >= s.cnt) return;
-  // a CTA's slot 0 holds the item that its run starts in: every part but, maybe, the first
+  // slot 0 holds the item that a run starts in: every part but, maybe, the first
   const int slot0 = run_begin(c0, U, G) >= g0 ? 0 : 1;
-  auto part_of = [&](int c) -> long long { return ((long long)c * 2 + (c == c0 ? slot0 : 0)) * tiles + tile; };
+  auto part_of = [&](int c) -> long long { return (((long long)c * p.team + member) * 2 + (c == c0 ? slot0 : 0)) * tiles + tile; };
   float m = -INFINITY;
   for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(&p.part_ml[part_of(c) * kBlk + row].x));
   const float mm = m == -INFINITY ? 0.f : m;
@@ -785,9 +822,18 @@ template <int HD>
 cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(tree_kernel<HD>, TreeCfg<HD>::kSmem, done);
+  static std::atomic<int> regs{0};
+  cudaError_t e = allow_smem(tree_kernel<HD>, TreeSmem<HD>::kBytes, done);
   if (e != cudaSuccess) return e;
-  tree_kernel<HD><<<p.grid, kTreeThreads, TreeCfg<HD>::kSmem, st>>>(p, tq, tk, tv);
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    // the softmax warpgroups would wait for ever for registers that the launch does not hold
+    cudaFuncAttributes at = {};
+    e = cudaFuncGetAttributes(&at, tree_kernel<HD>);
+    if (e != cudaSuccess) return e;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < kLaunchRegs) return cudaErrorLaunchOutOfResources;
+  tree_kernel<HD><<<p.grid, kTreeThreads, TreeSmem<HD>::kBytes, st>>>(p, tq, tk, tv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -43,7 +43,7 @@ def experts(**over):
     return B.mk_expert_args(**a)
 
 
-CACHE = [(dict(head_dim=48), UNS), (dict(head_dim=256), UNS), (dict(batch=0), INV), (dict(batch=129), INV), (dict(n_kv_heads=0), INV),
+CACHE = [(dict(head_dim=48), UNS), (dict(head_dim=256), UNS), (dict(batch=0), INV), (dict(batch=65536), INV), (dict(n_kv_heads=0), INV),
          (dict(max_pages=0), INV), (dict(n_pages=0), INV), (dict(n_pages=1 << 27), INV), (dict(k=None), INV), (dict(v=P + 8), INV),
          (dict(page_table=None), INV), (dict(seq_lens=None), INV)]
 
