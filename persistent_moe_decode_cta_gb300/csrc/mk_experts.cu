@@ -29,7 +29,7 @@ constexpr int kGatherLag = 2;      // stages whose copies a gather thread has in
 constexpr int kTileW = 128;        // weight rows of a block
 constexpr int kTileR = 128;        // rows of a tile
 constexpr int kTileK = 64;         // columns of a stage: one 128-byte swizzle span
-constexpr int kBoxR = 32;          // rows per copy of x
+constexpr int kBoxR = 32;          // rows per copy of x (one copy of 128 if more than two would be needed)
 constexpr int kExpStages = 4;
 constexpr int kBytesW = kTileW * kTileK * 2, kBytesR = kTileR * kTileK * 2;
 constexpr int kExpStage = 2 * kBytesW + kBytesR;
@@ -106,7 +106,8 @@ __device__ __forceinline__ float silu(float y) { return y / (1.f + __expf(-y)); 
 template <bool GLU>
 __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     expert_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ CUtensorMap tx,
-                  const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tu) {
+                  const __grid_constant__ CUtensorMap tx128, const __grid_constant__ CUtensorMap tw,
+                  const __grid_constant__ CUtensorMap tu) {
   extern __shared__ uint8_t raw[];
   __shared__ ExpShared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -151,19 +152,26 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     bool ok = true;
     for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
-      const bool second = GLU || x.w0 + kTileW < p.a.n;
-      const int boxes = (x.nr + kBoxR - 1) / kBoxR;
-      const uint32_t bytes = (second ? 2 : 1) * kBytesW + (p.a.rows ? 0 : boxes * kBoxR * (kTileK * 2));
+      const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
+      const int e = (int)uniform(x.e), w0 = (int)uniform(x.w0), r0 = (int)uniform(x.r0), nr = (int)uniform(x.nr);
+      const uint32_t xrows = p.a.rows ? 0 : nr <= kBoxR ? kBoxR : nr <= 2 * kBoxR ? 2 * kBoxR : kTileR;
+      const uint32_t bytes = (second ? 2 : 1) * kBytesW + xrows * (kTileK * 2);
       for (int ks = 0; ks < ksteps; ++ks, ++fill) {
         const int s = fill % kExpStages;
         if (!(ok = op_wait(empty(s), ((fill / kExpStages) & 1) ^ 1, abort, p.a.status, 1))) break;
-        const uint32_t st = base + s * kExpStage;
-        if (lane == 0) mbar_expect_tx(full(s), bytes);
+        if (elect_one()) {
+          const uint32_t st = base + s * kExpStage;
+          mbar_expect_tx(full(s), bytes);
+          op_tma_3d(st, &tw, ks * kTileK, w0, e, full(s));
+          if (second) op_tma_3d(st + kBytesW, GLU ? &tu : &tw, ks * kTileK, GLU ? w0 : w0 + kTileW, e, full(s));
+          if (xrows == kTileR) {
+            op_tma_2d(st + 2 * kBytesW, &tx128, ks * kTileK, r0, full(s));
+          } else if (xrows) {
+            op_tma_2d(st + 2 * kBytesW, &tx, ks * kTileK, r0, full(s));
+            if (xrows > kBoxR) op_tma_2d(st + 2 * kBytesW + kBoxR * kTileK * 2, &tx, ks * kTileK, r0 + kBoxR, full(s));
+          }
+        }
         __syncwarp();
-        if (lane == 0) op_tma_3d(st, &tw, ks * kTileK, x.w0, x.e, full(s));
-        if (lane == 1 && second) op_tma_3d(st + kBytesW, GLU ? &tu : &tw, ks * kTileK, GLU ? x.w0 : x.w0 + kTileW, x.e, full(s));
-        if (!p.a.rows && lane < boxes)
-          op_tma_2d(st + 2 * kBytesW + lane * kBoxR * kTileK * 2, &tx, ks * kTileK, x.r0 + lane * kBoxR, full(s));
       }
     }
     if (*abort) {  // an abandoned run leaves copies in flight: wait for them (bounded)
@@ -314,18 +322,18 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
 }  // namespace
 
 template <bool GLU>
-static cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& tu,
+static cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw, const CUtensorMap& tu,
                               cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
   if (e != cudaSuccess) return e;
-  expert_kernel<GLU><<<p.grid, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tw, tu);
+  expert_kernel<GLU><<<p.grid, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tx128, tw, tu);
   return cudaGetLastError();
 }
 
-cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& tu,
+cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw, const CUtensorMap& tu,
                            cudaStream_t st) {
-  return p.a.w_up ? launch_glu<true>(p, tx, tw, tu, st) : launch_glu<false>(p, tx, tw, tu, st);
+  return p.a.w_up ? launch_glu<true>(p, tx, tx128, tw, tu, st) : launch_glu<false>(p, tx, tx128, tw, tu, st);
 }
 
 }  // namespace mk

@@ -196,11 +196,12 @@ int mk_tree_attention(const mk_paged_kv* cache, const mk_tree_args* args, void* 
   }
   cuuint32_t qb[4] = {(cuuint32_t)span, (cuuint32_t)p.gs, (cuuint32_t)p.npt, 1};
   r = encode(&tq, args->q, 4, qd, qs, qb, sw);
-  cuuint64_t kd[2] = {(cuuint64_t)hd, (cuuint64_t)cache->n_pages * cache->n_kv_heads * kOpPage};
-  cuuint64_t ks[1] = {(cuuint64_t)hd * 2};
-  cuuint32_t kb[2] = {(cuuint32_t)span, kOpPage};
-  if (!r) r = encode(&tk, cache->k, 2, kd, ks, kb, sw);
-  if (!r) r = encode(&tv, cache->v, 2, kd, ks, kb, sw);
+  // keys: column in the span, row of a group of 8, span, group (a page of a head is two groups)
+  cuuint64_t kd[4] = {(cuuint64_t)span, 8, (cuuint64_t)hd / span, (cuuint64_t)cache->n_pages * cache->n_kv_heads * (kOpPage / 8)};
+  cuuint64_t ks[3] = {(cuuint64_t)hd * 2, (cuuint64_t)span * 2, (cuuint64_t)hd * 16};
+  cuuint32_t kb[4] = {(cuuint32_t)span, 8, (cuuint32_t)(hd / span), kOpPage / 8};
+  if (!r) r = encode(&tk, cache->k, 4, kd, ks, kb, sw);
+  if (!r) r = encode(&tv, cache->v, 4, kd, ks, kb, sw);
   if (r) return r;
   return cuda_error(launch_tree(p, tq, tk, tv, static_cast<cudaStream_t>(stream)), "tree_attention launch");
 }
@@ -280,18 +281,20 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   p.a = *a;
   int r = num_sms(&p.grid);
   if (r) return r;
-  CUtensorMap tx, tw, tu;
+  CUtensorMap tx, tx128, tw, tu;
   cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n_x};
   cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
   cuuint32_t xb[2] = {64, 32};
+  cuuint32_t xb128[2] = {64, 128};
   r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = encode(&tx128, a->x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
   cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, (cuuint64_t)a->n_experts};
   cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
   cuuint32_t wb[3] = {64, 128, 1};
   if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!r) r = encode(&tu, a->w_up ? a->w_up : a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (r) return r;
-  return cuda_error(launch_experts(p, tx, tw, tu, static_cast<cudaStream_t>(stream)), "expert_product launch");
+  return cuda_error(launch_experts(p, tx, tx128, tw, tu, static_cast<cudaStream_t>(stream)), "expert_product launch");
 }
 
 }  // extern "C"

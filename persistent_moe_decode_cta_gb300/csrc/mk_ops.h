@@ -78,7 +78,7 @@ struct ExpertParams {
   mk_expert_args a;
   int grid;
 };
-cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tw,
+cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                            const CUtensorMap& tu, cudaStream_t st);
 
 }  // namespace mk

@@ -37,12 +37,20 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kTreeThreads * kLaunchReg
 constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P of the streams at 0 and 128, O at 256 and 384
 constexpr float kRescale = 8.f;         // the maximum may lag by 2^8 before O is rescaled
 
+// Shared-memory layout of a tile of 128 rows: groups of 8 rows, of each group the spans one
+// behind the other, of each span 8 swizzled lines.  A page (16 rows) is then one contiguous
+// piece that one copy fills, and a group is kGroup bytes from the next in every page.
 template <int HD>
 struct TreeCfg {
   static constexpr int kSpan = HD == 32 ? 64 : 128;        // swizzle span in bytes
   static constexpr int kHalves = HD * 2 / kSpan;           // spans per row
+  static constexpr int kGroup = 8 * HD * 2;                // 8 rows
   static constexpr int kTile = kBlk * HD * 2;              // 128 rows
   static constexpr int kSlots = HD == 128 ? 7 : 10;        // query tiles and ring stages together
+  // the row that 16-byte piece i of a tile belongs to
+  __host__ __device__ static constexpr int row_of(int i) { return i / (kGroup / 16) * 8 + i / (kSpan / 16) % 8; }
+  // byte offset of column 16 kk of a tile's first row group
+  __host__ __device__ static constexpr int column16(int kk) { return (kk * 32 / kSpan) * (8 * kSpan) + (kk * 32) % kSpan; }
 };
 
 // ------------------------------------------------------------------ work list
@@ -296,27 +304,39 @@ __device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t u) {
   return u;
 }
 
-// Threads t of nt: in the landed V block at `stage`, rows from `live` on become zero and
+// Threads t of NT: in the landed V block at `stage`, rows from `live` on become zero and
 // values that are not finite are dropped (and reported): a weight of zero times such a value
-// would otherwise reach rows that do not see the key.
-template <int HD>
-__device__ __forceinline__ void clean_v(uint8_t* stage, int live, int t, int nt, int* bad) {
-  constexpr int kVecs = TreeCfg<HD>::kSpan / 16;
-  bool seen = false;
-  for (int i = t; i < TreeCfg<HD>::kTile / 16; i += nt) {
-    uint4* a = reinterpret_cast<uint4*>(stage) + i;
-    const int row = (i / kVecs) % kBlk;
-    if (row >= live) {
-      *a = make_uint4(0, 0, 0, 0);
-    } else {
-      const uint4 x = *a;
-      if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
-        *a = make_uint4(drop_nonfinite2(x.x), drop_nonfinite2(x.y), drop_nonfinite2(x.z), drop_nonfinite2(x.w));
-        seen = true;
+// would otherwise reach rows that do not see the key.  The loads of a thread go out together.
+template <int HD, int NT>
+__device__ __forceinline__ void clean_v(uint8_t* stage, int live, int t, int* bad) {
+  using C = TreeCfg<HD>;
+  constexpr int kVecs = C::kTile / 16 / NT, kBatch = kVecs < 8 ? kVecs : 8;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kVecs; i0 += kBatch) {
+    uint4 x[kBatch];
+    uint4* at[kBatch];
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      at[i] = reinterpret_cast<uint4*>(stage) + (i0 + i) * NT + t;
+      x[i] = *at[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (C::row_of((i0 + i) * NT + t) >= live) {
+        *at[i] = make_uint4(0, 0, 0, 0);
+      } else if (nonfinite2(x[i].x) || nonfinite2(x[i].y) || nonfinite2(x[i].z) || nonfinite2(x[i].w)) {
+        any |= 1u << i;
       }
     }
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (any >> i & 1u)
+          *at[i] = make_uint4(drop_nonfinite2(x[i].x), drop_nonfinite2(x[i].y), drop_nonfinite2(x[i].z), drop_nonfinite2(x[i].w));
+      *reinterpret_cast<volatile int*>(bad) = 1;
+    }
   }
-  if (seen) *reinterpret_cast<volatile int*>(bad) = 1;
 }
 
 __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key, bool record) {
@@ -326,13 +346,13 @@ __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key, bool
   return 0;
 }
 
-// What clean_v dropped, for 16 columns of a row: p_j * v_j of the keys that the row sees.
-// Only after a masked block held such values (never with finite caches): plain loads.
+// What clean_v dropped from column c of a row: p_j * v_j of the keys that the row sees.  Only
+// after a masked block held such values (never with finite caches): plain loads.
 template <int HD>
-__device__ __noinline__ void add_nonfinite(const TreeParams& p, const Item& it, const Row& r, const uint16_t* q, float m, int c0,
-                                           float* o) {
+__device__ __noinline__ float nonfinite_part(const TreeParams& p, const Item& it, const Row& r, const uint16_t* q, float m, int c) {
   const uint16_t* K = static_cast<const uint16_t*>(p.c.k);
   const uint16_t* V = static_cast<const uint16_t*>(p.c.v);
+  float o = 0.f;
   for (int j = it.ja; j < it.jb; ++j) {
     const int k0 = it.kstart + j * kBlk;
     if (!masked_block(p, it, k0)) continue;
@@ -340,20 +360,15 @@ __device__ __noinline__ void add_nonfinite(const TreeParams& p, const Item& it, 
       for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
         const int key = k0 + 32 * w + __ffs(bits) - 1;
         const long long at = (((long long)page_of(p, it.b, key, false) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
-        float weight = -1.f;
-        for (int c = 0; c < 16; ++c) {
-          const float v = bf16_to_f(V[at + c0 + c]);
-          if (fabsf(v) <= 3.4e38f) continue;
-          if (weight < 0.f) {
-            float s = 0.f;
-            for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
-            weight = ex2(s * p.scale_log2 - m);
-          }
-          o[c] += weight * v;
-        }
+        const float v = bf16_to_f(V[at + c]);
+        if (fabsf(v) <= 3.4e38f) continue;
+        float s = 0.f;
+        for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
+        o += ex2(s * p.scale_log2 - m) * v;
       }
     }
   }
+  return o;
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -489,7 +504,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int w = 0; w < 4; ++w) vis[w] = sees32(p, it, r, k0 + 32 * w);
           const uint32_t slot = used + 2 * blk + 1, s = slot % stages;
           if (!(ok = op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 8))) break;
-          clean_v<HD>(ring_g + s * C::kTile, it.end - k0, two ? (int)threadIdx.x : row, two ? 256 : 128, &sh.bad_v);
+          if (two)
+            clean_v<HD, 256>(ring_g + s * C::kTile, it.end - k0, (int)threadIdx.x, &sh.bad_v);
+          else
+            clean_v<HD, 128>(ring_g + s * C::kTile, it.end - k0, row, &sh.bad_v);
           fence_proxy_async_smem();
           if (two && !(ok = meet())) break;
         }
@@ -584,7 +602,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]);
             if (node >= 0) {
-              if (fix) add_nonfinite<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c, o);
+              if (fix) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c + i);
+              }
               put16(o, whole, inv, dst, part, c);
             }
           }
@@ -618,7 +639,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = w0 * __uint_as_float(u[i]) + (other ? w1 * __uint_as_float(v[i]) : 0.f);
             if (node >= 0) {
-              if (fix) add_nonfinite<HD>(p, it, r, qrow, mm, c, o);
+              if (fix) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, mm, c + i);
+              }
               put16(o, whole, inv, dst, part, c);
             }
           }
@@ -631,38 +655,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
       // ---------------------------------------------------------------- producer
-      // lane = (page of the block) + 8 * (span of the row): one copy per lane
+      // lane i < 8 looks up page i of the next block while this one's copies are issued
       uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
-      const int pg = lane & 7, half = lane >> 3;
       bool ok = true;
+      auto look_up = [&](const Item& it, int j) -> int {  // first row group of lane's page of block j
+        const int key = it.kstart + j * kBlk + lane * kOpPage;
+        const int page = lane < 8 && key < it.end ? page_of(p, it.b, key, true) : 0;
+        return (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);
+      };
       while (ok && run.next(p, sh.pre)) {
         const Item& it = run.it;
-        const int rows = p.npt * p.gs;
-        // this lane's page of the next block is looked up one block ahead
-        int key = it.kstart + it.ja * kBlk + pg * kOpPage;
-        int next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
+        const uint32_t rows = p.npt * p.gs;
+        int page = look_up(it, it.ja);
         for (int j = it.ja; ok && j < it.jb; ++j) {
-          const int k0 = it.kstart + j * kBlk;
-          const int live = min(kBlk / kOpPage, (it.end - k0 + kOpPage - 1) / kOpPage);
-          const int row = (next_page * p.c.n_kv_heads + it.kvh) * kOpPage;
-          key = k0 + kBlk + pg * kOpPage;
-          if (j + 1 < it.jb) next_page = key < it.end && lane < 8 * C::kHalves ? page_of(p, it.b, key, half == 0) : 0;
-          for (int kv = 0; kv < 2; ++kv) {
-            const int s = fill % stages;
-            const uint32_t ph = (fill / stages) & 1;
-            if (!(ok = op_wait(bars.empty(s), ph ^ 1, abort, p.a.status, 1))) break;
-            if (lane == 0) mbar_expect_tx(bars.full(s), (uint32_t)live * kOpPage * HD * 2);
+          const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
+          uint32_t group[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, page, i);
+          if (j + 1 < it.jb) page = look_up(it, j + 1);
+          for (int kv = 0; kv < 2; ++kv, ++fill) {
+            const uint32_t s = fill % stages;
+            if (!(ok = op_wait(bars.empty(s), ((fill / stages) & 1) ^ 1, abort, p.a.status, 1))) break;
+            if (elect_one()) {
+              const uint32_t dst = ring + s * C::kTile, bar = bars.full(s);
+              mbar_expect_tx(bar, live * kOpPage * HD * 2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
+            }
             __syncwarp();
-            if (pg < live && half < C::kHalves)
-              op_tma_2d(ring + s * C::kTile + half * (kBlk * C::kSpan) + pg * (kOpPage * C::kSpan), kv ? &tv : &tk,
-                        half * (C::kSpan / 2), row, bars.full(s));
-            ++fill;
             if (kv == 0 && j == it.ja) {  // the item's queries, once the last item's products have read theirs
               if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
               ++qphase;
               const int tiles = two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1;
-              if (lane == 0) {
-                mbar_expect_tx(bars.qfull(), (uint32_t)(tiles * rows * HD * 2));
+              if (elect_one()) {
+                mbar_expect_tx(bars.qfull(), (uint32_t)tiles * rows * HD * 2);
                 for (int t = 0; t < tiles; ++t)
                   for (int h = 0; h < C::kHalves; ++h)
                     op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), it.kvh * p.gs,
@@ -683,13 +710,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---------------------------------------------------------------- MMA issue
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
       constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
-      constexpr uint32_t kSbo = 8 * C::kSpan;
+      // queries: spans of 128 rows one behind the other (one copy each); keys: see TreeCfg
       uint32_t used = 0;                  // ring slots of earlier items
       uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
       const uint32_t tm = uniform(tmem);
       // descriptors of the first query tile and ring stage; a tile further is kTile / 16 more
-      const uint64_t dq = umma_sdesc_sw(q_s, 16, kSbo, C::kSpan), dk = umma_sdesc_sw(ring, 16, kSbo, C::kSpan);
-      const uint64_t dv = umma_sdesc_sw(ring, kBlk * C::kSpan, kSbo, C::kSpan);
+      const uint64_t dq = umma_sdesc_sw(q_s, 16, 8 * C::kSpan, C::kSpan), dk = umma_sdesc_sw(ring, 16, C::kGroup, C::kSpan);
+      const uint64_t dv = umma_sdesc_sw(ring, 8 * C::kSpan, C::kGroup, C::kSpan);
       bool ok = true;
       while (ok && run.next(p, sh.pre)) {
         const int nb = (int)uniform((uint32_t)(run.it.jb - run.it.ja));
@@ -707,7 +734,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
               const uint32_t off = ((kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan) / 16;
-              umma_bf16(tm + kTmemS + 128 * st, a + off, b + off, idesc_s, kk > 0);
+              umma_bf16(tm + kTmemS + 128 * st, a + off, b + C::column16(kk) / 16, idesc_s, kk > 0);
             }
             umma_commit(bars.sfull(st));
             if (!two || st == 1) umma_commit(bars.empty(s));
@@ -728,7 +755,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const bool first = two ? blk == 0 : blk == st;
 #pragma unroll
             for (int kk = 0; kk < kBlk / 16; ++kk)
-              umma_bf16_ta(tm + kTmemO + 128 * st, tm + kTmemS + 128 * st + 8 * kk, b + kk * C::kSpan, idesc_o, !first || kk > 0);
+              umma_bf16_ta(tm + kTmemO + 128 * st, tm + kTmemS + 128 * st + 8 * kk, b + kk * (2 * C::kGroup / 16), idesc_o, !first || kk > 0);
             if (!two || st == 1) umma_commit(bars.empty(s));
             if (t + 2 >= steps) umma_commit(bars.ofull(st));
             if (t + 1 == steps) umma_commit(bars.qempty());
