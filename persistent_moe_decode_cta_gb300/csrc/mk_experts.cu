@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
   scan_experts(p, sh);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
-  const long long tiles = (long long)sh.pre[p.a.n_experts] * wblocks;
-  if (blockIdx.x >= tiles) return;  // (the whole CTA)
+  const int tiles = (int)uniform(sh.pre[p.a.n_experts]) * wblocks;  // (below 2^31: checked by the host)
+  if ((int)blockIdx.x >= tiles) return;  // (the whole CTA)
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
   tc_fence_before();
   __syncthreads();
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     // ---------------------------------------------------------------- producer
     uint32_t fill = 0;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
+    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
+      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
       const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
       const int e = (int)uniform(x.e), w0 = (int)uniform(x.w0), r0 = (int)uniform(x.r0), nr = (int)uniform(x.nr);
       const uint32_t xrows = p.a.rows ? 0 : nr <= kBoxR ? kBoxR : nr <= 2 * kBoxR ? 2 * kBoxR : kTileR;
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     const uint32_t swz = (uint32_t)(chunk ^ (row0 & 7)) * 16;  // (16 j keeps the low three bits of the row)
     uint32_t fill = 0;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
+    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
+      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
       const uint16_t* src[kTileR / 16];
 #pragma unroll
       for (int j = 0; j < kTileR / 16; ++j) {
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     const uint32_t tm = uniform(tmem);
     const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, second weights, rows
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++nt) {
-      const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
+    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x, ++nt) {
+      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
       const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
       const uint32_t idesc = umma_idesc_bf16(kTileW, (uniform(x.nr) + 15) / 16 * 16);
       const uint32_t a = nt & 1, acc = tm + 256 * a;
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
     // whole 16-byte pieces of an output row where its address allows them
     const bool wide = p.a.n % 8 == 0 && p.a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.a.out) & 15) == 0;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++nt) {
-      const ExpTile x = find_tile(p, sh.pre, (int)t, wblocks, kStep);
+    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x, ++nt) {
+      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
       const uint32_t a = nt & 1;
       const uint32_t acc = tmem + 256 * a + ((uint32_t)q << 21);
       if (!(ok = op_wait(afull(a), (nt >> 1) & 1, abort, p.a.status, 4))) break;

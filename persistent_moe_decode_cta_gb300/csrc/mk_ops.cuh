@@ -19,23 +19,25 @@ __device__ __forceinline__ void op_error(int32_t* st, int code, int where, int i
 
 constexpr long long kOpWaitNs = 2000000000ll;  // limit of every barrier wait
 
-// Bounded wait of a whole warp that also gives up once another thread of the CTA has:
-// false in all lanes then (they stay converged for the .aligned instructions that follow).
+// Bounded wait of a whole warp that also gives up once another thread of the CTA has.  Every
+// branch goes by a vote, so that the lanes stay converged (for the .aligned instructions that
+// follow) and the compiler knows it.
 __device__ __forceinline__ bool op_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = gtime();
-    while (!(ok = mbar_try_wait(bar, parity))) {
-      if (*abort) break;
-      if ((long long)(gtime() - t0) > kOpWaitNs) {
-        *abort = 1;
-        op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
-        break;
-      }
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = gtime();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, (long long)(gtime() - t0) > kOpWaitNs)) {
+      *abort = 1;
+      op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, ok);
+  return true;
 }
+
+// v, equal in all lanes, as a value that the compiler knows to be so
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void op_tma_2d(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
   asm volatile(
@@ -130,16 +132,25 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One lane of a converged warp, chosen so that the compiler knows that there is one: under
-// it the operands of tcgen05.mma stay in uniform registers (under `lane == 0` each MMA cost
-// about 140 cycles to issue).
+// One lane of a converged warp, chosen so that the compiler knows that there is one.
+// tcgen05.mma and the tensor-map copies take uniform registers: where the warp's control flow
+// or the operands are not known to be uniform, each costs 100 to 140 cycles to issue.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
-// v, equal in all lanes, as a value that the compiler knows to be so
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Slot of a ring and the parity of its next phase, counted without divisions.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void advance(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 // Programmatic dependent launch: the next kernel of the stream may start its prologue /
 // wait until every earlier kernel's memory is visible.

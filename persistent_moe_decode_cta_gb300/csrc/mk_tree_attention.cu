@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return;
   }
   const bool two = p.two != 0;
-  const int stages = C::kSlots - (two ? 2 : 1);
+  const uint32_t stages = C::kSlots - (two ? 2 : 1);
   const uint32_t q_s = base, ring = base + (two ? 2 : 1) * C::kTile;
   uint8_t* const ring_g = raw + (ring - base);
   const Bars bars{smem_u32(sh.bars)};
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (threadIdx.x == 0) {
     sh.abort = 0;
     sh.bad_v = 0;
-    for (int s = 0; s < stages; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 1);
     }
@@ -484,9 +484,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       return op_wait(bars.meet(), nm++ & 1, abort, p.a.status, 7);
     };
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    while (ok && run.next(p, sh.pre)) {
+    while (ok && uniform(run.next(p, sh.pre))) {
       const Item& it = run.it;
-      const int nb = it.jb - it.ja;
+      const int nb = (int)uniform(it.jb - it.ja);
       const int tile = two ? st : 0;
       const int node_in = row / p.gs;
       int node = it.tp * nodes_per_group(p) + tile * p.npt + node_in;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int b0 = two ? 0 : st, bstep = two ? 1 : 2;
       for (int blk = b0; ok && blk < nb; blk += bstep) {
         const int k0 = it.kstart + (it.ja + blk) * kBlk;
-        const bool masked = masked_block(p, it, k0);
+        const bool masked = uniform(masked_block(p, it, k0));
         uint32_t vis[4];
         if (masked) {
 #pragma unroll
@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------------------------- producer
       // lane i < 8 looks up page i of the next block while this one's copies are issued
+      Ring put;
       uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
       bool ok = true;
       auto look_up = [&](const Item& it, int j) -> int {  // first row group of lane's page of block j
@@ -663,19 +664,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int page = lane < 8 && key < it.end ? page_of(p, it.b, key, true) : 0;
         return (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);
       };
-      while (ok && run.next(p, sh.pre)) {
+      while (ok && uniform(run.next(p, sh.pre))) {
         const Item& it = run.it;
+        const int blocks = (int)uniform(run.it.jb - run.it.ja);
         const uint32_t rows = p.npt * p.gs;
         int page = look_up(it, it.ja);
-        for (int j = it.ja; ok && j < it.jb; ++j) {
+        for (int blk = 0; ok && blk < blocks; ++blk) {
+          const int j = it.ja + blk;
           const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
           uint32_t group[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, page, i);
-          if (j + 1 < it.jb) page = look_up(it, j + 1);
-          for (int kv = 0; kv < 2; ++kv, ++fill) {
-            const uint32_t s = fill % stages;
-            if (!(ok = op_wait(bars.empty(s), ((fill / stages) & 1) ^ 1, abort, p.a.status, 1))) break;
+          if (blk + 1 < blocks) page = look_up(it, j + 1);
+          for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(stages)) {
+            const uint32_t s = put.slot;
+            if (!(ok = op_wait(bars.empty(s), put.phase ^ 1, abort, p.a.status, 1))) break;
             if (elect_one()) {
               const uint32_t dst = ring + s * C::kTile, bar = bars.full(s);
               mbar_expect_tx(bar, live * kOpPage * HD * 2);
@@ -684,16 +687,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
             }
             __syncwarp();
-            if (kv == 0 && j == it.ja) {  // the item's queries, once the last item's products have read theirs
+            if (kv == 0 && blk == 0) {  // the item's queries, once the last item's products have read theirs
               if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
               ++qphase;
-              const int tiles = two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1;
+              const uint32_t tiles = uniform(two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1);
+              const int head = (int)uniform(it.kvh * p.gs), node = (int)uniform(it.tp * nodes_per_group(p)), seq = (int)uniform(it.b);
               if (elect_one()) {
-                mbar_expect_tx(bars.qfull(), (uint32_t)tiles * rows * HD * 2);
-                for (int t = 0; t < tiles; ++t)
+                mbar_expect_tx(bars.qfull(), tiles * rows * HD * 2);
+                for (uint32_t t = 0; t < tiles; ++t)
                   for (int h = 0; h < C::kHalves; ++h)
-                    op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), it.kvh * p.gs,
-                              it.tp * nodes_per_group(p) + t * p.npt, it.b, bars.qfull());
+                    op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), head,
+                              node + (int)t * p.npt, seq, bars.qfull());
               }
               __syncwarp();
             }
@@ -711,14 +715,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
       constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
       // queries: spans of 128 rows one behind the other (one copy each); keys: see TreeCfg
-      uint32_t used = 0;                  // ring slots of earlier items
+      Ring k_at, v_at;                    // slots of the next K and V block (every second slot each)
+      v_at.advance(stages);
+      auto skip2 = [&](Ring& r) {
+        r.advance(stages);
+        r.advance(stages);
+      };
       uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
       const uint32_t tm = uniform(tmem);
       // descriptors of the first query tile and ring stage; a tile further is kTile / 16 more
       const uint64_t dq = umma_sdesc_sw(q_s, 16, 8 * C::kSpan, C::kSpan), dk = umma_sdesc_sw(ring, 16, C::kGroup, C::kSpan);
       const uint64_t dv = umma_sdesc_sw(ring, 8 * C::kSpan, C::kGroup, C::kSpan);
       bool ok = true;
-      while (ok && run.next(p, sh.pre)) {
+      while (ok && uniform(run.next(p, sh.pre))) {
         const int nb = (int)uniform((uint32_t)(run.it.jb - run.it.ja));
         const int steps = two ? 2 * nb : nb;
         if (!(ok = op_wait(bars.qfull(), nq & 1, abort, p.a.status, 3))) break;
@@ -726,8 +735,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ++nq;
         // step t: stream t & 1, block t >> 1 (two) or t
         auto issue_s = [&](int t) -> bool {
-          const uint32_t st = t & 1, slot = used + 2 * (two ? t >> 1 : t), s = slot % stages;
-          if (!op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 4)) return false;
+          const uint32_t st = t & 1, s = uniform(k_at.slot);
+          if (!op_wait(bars.full(s), k_at.phase, abort, p.a.status, 4)) return false;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t a = dq + (two ? st : 0) * (C::kTile / 16), b = dk + s * (C::kTile / 16);
@@ -740,13 +749,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (!two || st == 1) umma_commit(bars.empty(s));
           }
           __syncwarp();
+          if (!two || st == 1) skip2(k_at);
           return true;
         };
         ok = issue_s(0) && (steps < 2 || issue_s(1));
         for (int t = 0; ok && t < steps; ++t) {
           const uint32_t st = t & 1, blk = two ? t >> 1 : t;
-          const uint32_t slot = used + 2 * blk + 1, s = slot % stages;
-          if (!(ok = op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 5))) break;
+          const uint32_t s = uniform(v_at.slot);
+          if (!(ok = op_wait(bars.full(s), v_at.phase, abort, p.a.status, 5))) break;
           if (!(ok = op_wait(bars.pready(st), (st ? np[1] : np[0]) & 1, abort, p.a.status, 6))) break;
           if (st) ++np[1]; else ++np[0];
           tc_fence_after();
@@ -761,9 +771,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (t + 1 == steps) umma_commit(bars.qempty());
           }
           __syncwarp();
+          if (!two || st == 1) skip2(v_at);
           if (t + 2 < steps) ok = issue_s(t + 2);
         }
-        used += 2 * nb;
       }
       if (*abort) {  // let the products in flight end before the memory goes
         if (elect_one()) umma_commit(bars.ofull(0));
