@@ -36,6 +36,21 @@ __device__ __forceinline__ bool op_wait(uint32_t bar, uint32_t parity, volatile 
   return true;
 }
 
+// The same for one thread.
+__device__ __forceinline__ bool op_wait1(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = gtime();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if ((long long)(gtime() - t0) > kOpWaitNs) {
+      *abort = 1;
+      op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
+      return false;
+    }
+  }
+  return true;
+}
+
 // v, equal in all lanes, as a value that the compiler knows to be so
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 

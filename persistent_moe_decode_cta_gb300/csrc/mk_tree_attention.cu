@@ -12,9 +12,19 @@
 //
 // Two softmax warpgroups ("streams") alternate so that one's exponentials run beside the
 // other's products.  Up to 128 rows per KV head both streams work on the same rows, on
-// even and odd key blocks, and are merged at the end (two = 0); with more rows each stream
-// has a tile of its own and both use every key block that is loaded (two = 1), which halves
-// the key traffic where it would exceed what L2 delivers.
+// even and odd key blocks, and are merged at the end (TWO = false); with more rows each
+// stream has a tile of its own and both use every key block that is loaded (TWO = true),
+// which halves the key traffic where it would exceed what L2 delivers.  A stream takes a block
+// in two halves of 64 keys with an S/P buffer each: S of the next half is computed while the
+// softmax of this one runs, so that a stream never waits for its own products.  S and P V
+// are issued by a warp each: the tensor pipe queues too few products to cover a warp's waits
+// between two groups (8 products of 64 cycles cost 514 cycles alone, 700 with two waits and
+// two commits), and so one warp's overhead is the other's time.
+//
+// Keys that a row does not see get a score of -infinity.  Blocks with such keys have their V
+// cleaned in shared memory by a further warp (rows past the end and values that are not
+// finite become zero, since 0 * NaN would reach every row); what was dropped is added by plain
+// loads at the end, for the rows that do see it.
 //
 // The work is a list of units, one per (sequence, tile group, KV head, key block), cut into
 // equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  (Up
@@ -24,17 +34,15 @@
 // the parts in order of their keys; at most a run's first and last item are such.
 #include "mk_ops.cuh"
 
+#include <type_traits>
+
 namespace mk {
 namespace {
 
 constexpr int kBlk = 128;               // keys of a block
-constexpr int kTreeThreads = 384;       // two softmax warpgroups; a producer, an MMA and two idle warps
-// Registers per thread: 168 at launch (384 threads of 65,536 / 384), of which the third
-// warpgroup gives up what the softmax warpgroups take on (a row's 128 scores are kept in
-// registers): 2 * 128 * 216 + 128 * 72 = 384 * 168.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kTreeThreads * kLaunchRegs, "register split");
-constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P of the streams at 0 and 128, O at 256 and 384
+constexpr int kHalf = 64;               // keys of a softmax step
+constexpr int kTreeThreads = 384;       // two softmax warpgroups; copy, S, P V and cleaning warps
+constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P halves of the streams from 0 and 128, O from 256 and 384
 constexpr float kRescale = 8.f;         // the maximum may lag by 2^8 before O is rescaled
 
 // Shared-memory layout of a tile of 128 rows: groups of 8 rows, of each group the spans one
@@ -148,24 +156,34 @@ __device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool r
 // run of team g of G: units [g * U / G, (g + 1) * U / G).  G <= U: every run has a unit, so the
 // parts of an item are those of consecutive teams.
 __device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid / p.team, U); }
-__device__ __forceinline__ int run_begin(int c, int U, int G) { return (int)((long long)c * U / G); }
-__device__ __forceinline__ int run_owner(int u, int U, int G) { return (int)(((long long)(u + 1) * G - 1) / U); }
+__device__ __forceinline__ int run_begin(int g, int U, int G) { return g * (U / G) + g * (U % G) / G; }
+__device__ __forceinline__ int run_owner(int u, int U, int G) {  // the g with run_begin(g) <= u < run_begin(g + 1)
+  int g = min(G - 1, (int)((float)(u + 1) * G / U));
+  while (g > 0 && run_begin(g, U, G) > u) --g;
+  while (g + 1 < G && run_begin(g + 1, U, G) <= u) ++g;
+  return g;
+}
 
 // Walks the items of a run for tile group `member` of its team.
 struct Run {
   int u, u1, member;
+  int e, first;        // the entry that unit u lies in or behind, and its first unit
+  Entry x;
   Item it;
+
+  __device__ __forceinline__ void start(const TreeParams& p, const int* pre) {
+    int lo = 0, hi = kScan - 1;  // the last chunk that starts at or before u (so it has units)
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (pre[m] <= u) lo = m; else hi = m - 1;
+    }
+    e = lo * ((num_entries(p) + kScan - 1) / kScan);
+    first = pre[lo];
+    x = make_entry(p, e, false);
+  }
   // the next item with blocks of this group in the run
-  __device__ __forceinline__ bool next(const TreeParams& p, const int* pre) {
+  __device__ __forceinline__ bool next(const TreeParams& p) {
     while (u < u1) {
-      int lo = 0, hi = kScan - 1;  // the last chunk that starts at or before u (so it has units)
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (pre[m] <= u) lo = m; else hi = m - 1;
-      }
-      const int chunk = (num_entries(p) + kScan - 1) / kScan;
-      int e = lo * chunk, first = pre[lo];
-      Entry x = make_entry(p, e, false);
       while (u >= first + x.nblk * p.c.n_kv_heads) {
         first += x.nblk * p.c.n_kv_heads;
         x = make_entry(p, ++e, false);
@@ -267,6 +285,7 @@ __device__ __forceinline__ bool masked_block(const TreeParams& p, const Item& it
 
 // ------------------------------------------------------------------ shared memory
 
+constexpr int kMaxStages = 9;
 struct TreeShared {
   uint32_t tmem;
   int abort;
@@ -274,7 +293,7 @@ struct TreeShared {
   int pre[kScan + 1];
   int warp_sums[kScan / 32];
   float2 ml[2][kBlk];    // the streams' (m, sum) for the merge
-  unsigned long long bars[2 * 9 + 9];
+  unsigned long long bars[4 * kMaxStages + 17];
 };
 
 template <int HD>
@@ -283,16 +302,24 @@ struct TreeSmem {
   static_assert(kBytes <= 232448, "exceeds the 227 KB per-block shared memory limit");
 };
 
+// Key block i of the CTA's run (i modulo the ring's slots) has barriers of its own for its K,
+// its V and its cleaned V: whoever waits for one has seen, or knows done, its previous use, so
+// that the parity of a phase says which one it is.  (A slot's fills alternate between K and V when
+// the number of slots is odd, and nobody sees them all but the producer.)
 struct Bars {
   uint32_t base;
-  __device__ uint32_t full(int s) const { return base + 8 * s; }
-  __device__ uint32_t empty(int s) const { return base + 8 * (9 + s); }
-  __device__ uint32_t qfull() const { return base + 8 * 18; }
-  __device__ uint32_t qempty() const { return base + 8 * 19; }
-  __device__ uint32_t sfull(int s) const { return base + 8 * (20 + s); }
-  __device__ uint32_t pready(int s) const { return base + 8 * (22 + s); }
-  __device__ uint32_t ofull(int s) const { return base + 8 * (24 + s); }
-  __device__ uint32_t meet() const { return base + 8 * 26; }
+  __device__ __forceinline__ uint32_t kfull(uint32_t i) const { return base + 8 * i; }                     // copied
+  __device__ __forceinline__ uint32_t vfull(uint32_t i) const { return base + 8 * (kMaxStages + i); }
+  __device__ __forceinline__ uint32_t clean(uint32_t i) const { return base + 8 * (2 * kMaxStages + i); }  // V fit for use
+  __device__ __forceinline__ uint32_t empty(uint32_t s) const { return base + 8 * (3 * kMaxStages + s); }  // slot s read
+  __device__ __forceinline__ uint32_t one(int i) const { return base + 8 * (4 * kMaxStages + i); }
+  __device__ __forceinline__ uint32_t qfull() const { return one(0); }
+  __device__ __forceinline__ uint32_t qempty() const { return one(1); }
+  __device__ __forceinline__ uint32_t meet() const { return one(2); }
+  __device__ __forceinline__ uint32_t sfull(uint32_t st, uint32_t h) const { return one(3 + 2 * st + h); }   // S of a half
+  __device__ __forceinline__ uint32_t pready(uint32_t st, uint32_t h) const { return one(7 + 2 * st + h); }  // P of a half
+  __device__ __forceinline__ uint32_t pvdone(uint32_t st, uint32_t h) const { return one(11 + 2 * st + h); } // its product P V
+  __device__ __forceinline__ uint32_t ofull(uint32_t st) const { return one(15 + st); }                      // an item's last one
 };
 
 __device__ __forceinline__ bool nonfinite2(uint32_t u) {
@@ -412,11 +439,18 @@ __device__ __forceinline__ void put16(const float (&o)[16], bool whole, float in
   }
 }
 
-template <int HD>
+// Halves of block `blk` of the run part that hold keys before the end.
+__device__ __forceinline__ int block_halves(const Item& it, int blk) {
+  return it.end - it.kstart - (it.ja + blk) * kBlk > kHalf ? 2 : 1;
+}
+
+template <int HD, bool TWO>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tq,
                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = TreeCfg<HD>;
+  constexpr uint32_t kStages = C::kSlots - (TWO ? 2 : 1);
+  static_assert(kStages <= kMaxStages, "barriers");
   // (no static shared memory: the tiles start at its first byte, which is aligned to 1024)
   extern __shared__ __align__(1024) uint8_t raw[];
   TreeShared& sh = *reinterpret_cast<TreeShared*>(raw + C::kSlots * C::kTile);
@@ -425,9 +459,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (threadIdx.x == 0) op_error(p.a.status, MK_ERR_UNSUPPORTED, -1, (int)base, 0);
     return;
   }
-  const bool two = p.two != 0;
-  const uint32_t stages = C::kSlots - (two ? 2 : 1);
-  const uint32_t q_s = base, ring = base + (two ? 2 : 1) * C::kTile;
+  const uint32_t q_s = base, ring = base + (TWO ? 2 : 1) * C::kTile;
   uint8_t* const ring_g = raw + (ring - base);
   const Bars bars{smem_u32(sh.bars)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -438,141 +470,147 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const CUtensorMap* tm = lane == 0 ? &tk : lane == 1 ? &tv : &tq;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
   }
-  if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
-  if (threadIdx.x == 0) {
+  if (warp == 11) tmem_alloc(smem_u32(&sh.tmem), 512);
+  if (threadIdx.x == 128) {
     sh.abort = 0;
     sh.bad_v = 0;
-    for (uint32_t s = 0; s < stages; ++s) {
-      mbar_init(bars.full(s), 1);
+    for (uint32_t s = 0; s < kStages; ++s) {
+      mbar_init(bars.kfull(s), 1);
+      mbar_init(bars.vfull(s), 1);
       mbar_init(bars.empty(s), 1);
+      mbar_init(bars.clean(s), 32);
     }
     mbar_init(bars.qfull(), 1);
     mbar_init(bars.qempty(), 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bars.sfull(s), 1);
-      mbar_init(bars.pready(s), 128);
-      mbar_init(bars.ofull(s), 1);
-    }
     mbar_init(bars.meet(), 256);
+    for (uint32_t st = 0; st < 2; ++st) {
+      mbar_init(bars.ofull(st), 1);
+      for (uint32_t h = 0; h < 2; ++h) {
+        mbar_init(bars.sfull(st, h), 1);
+        mbar_init(bars.pvdone(st, h), 1);
+        mbar_init(bars.pready(st, h), 128);
+      }
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
   scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = uniform(sh.tmem);
   const int U = sh.pre[kScan];
   const int G = run_count(p, U), team = (int)blockIdx.x / p.team;
   if (team >= G) {  // (the whole CTA)
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 11) tmem_dealloc(tmem, 512);
     return;
   }
-  const int u0 = run_begin(team, U, G);
-  Run run{u0, run_begin(team + 1, U, G), (int)blockIdx.x % p.team, {}};
+  Run run;
+  run.u = run_begin(team, U, G);
+  run.u1 = run_begin(team + 1, U, G);
+  run.member = (int)blockIdx.x % p.team;
+  const int u0 = run.u;
+  run.start(p, sh.pre);
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------------------------------------------------------- softmax streams
-    const int st = warp >> 2;                       // 0 or 1
+    const uint32_t st = (uint32_t)warp >> 2;        // 0 or 1
     const int row = (int)threadIdx.x & 127;         // = lane of tensor memory
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t tS = tmem + kTmemS + 128 * st + lanes;
     const uint32_t tO = tmem + kTmemO + lanes;      // of stream 0; stream 1's is 128 columns on
-    uint32_t ns = 0, no[2] = {0, 0}, used = 0, nm = 0;  // S tiles, finished items per stream, ring slots, meetings
+    uint32_t ns[2] = {0, 0}, nm = 0;                // phases: S of either half, meetings
+    uint32_t no[2] = {0, 0};                        // items of the streams
     bool ok = true;
     auto meet = [&]() -> bool {                     // all 256 threads of the two streams
       mbar_arrive(bars.meet());
       return op_wait(bars.meet(), nm++ & 1, abort, p.a.status, 7);
     };
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    while (ok && uniform(run.next(p, sh.pre))) {
+    while (ok && uniform(run.next(p))) {
       const Item& it = run.it;
       const int nb = (int)uniform(it.jb - it.ja);
-      const int tile = two ? st : 0;
+      const int tile = TWO ? (int)st : 0;
       const int node_in = row / p.gs;
       int node = it.tp * nodes_per_group(p) + tile * p.npt + node_in;
       if (node_in >= p.npt || node >= it.cnt) node = -1;
       const Row r = make_row(p, it, node);
       const bool warp_live = __any_sync(0xffffffffu, node >= 0);
       float m = -INFINITY, l = 0.f;
-      const int b0 = two ? 0 : st, bstep = two ? 1 : 2;
-      for (int blk = b0; ok && blk < nb; blk += bstep) {
+      uint32_t steps = 0;                           // of this stream and item
+      for (int blk = TWO ? 0 : (int)st; ok && blk < nb; blk += TWO ? 1 : 2) {
         const int k0 = it.kstart + (it.ja + blk) * kBlk;
         const bool masked = uniform(masked_block(p, it, k0));
-        uint32_t vis[4];
-        if (masked) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) vis[w] = sees32(p, it, r, k0 + 32 * w);
-          const uint32_t slot = used + 2 * blk + 1, s = slot % stages;
-          if (!(ok = op_wait(bars.full(s), (slot / stages) & 1, abort, p.a.status, 8))) break;
-          if (two)
-            clean_v<HD, 256>(ring_g + s * C::kTile, it.end - k0, (int)threadIdx.x, &sh.bad_v);
-          else
-            clean_v<HD, 128>(ring_g + s * C::kTile, it.end - k0, row, &sh.bad_v);
-          fence_proxy_async_smem();
-          if (two && !(ok = meet())) break;
-        }
-        if (!(ok = op_wait(bars.sfull(st), ns & 1, abort, p.a.status, 9))) break;
-        ++ns;
-        tc_fence_after();
-        if (warp_live) {
-          uint32_t s[kBlk];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_wait32(s + 32 * i);
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < kBlk; ++i)
-              if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < kBlk; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          const float mnew = fmaxf(m, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * p.scale_log2);
-          const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = mnew == m ? 1.f : ex2(m - mnew);
-            if (blk != b0) {
+        const int halves = (int)uniform(block_halves(it, blk));
 #pragma unroll 1
-              for (int c = 0; c < HD; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(tO + 128 * st + c, o);
-                tmem_wait16(o);
+        for (int h = 0; h < halves; ++h, ++steps) {
+          uint32_t vis[2] = {0, 0};
+          if (masked) {
+            vis[0] = sees32(p, it, r, k0 + kHalf * h);
+            vis[1] = sees32(p, it, r, k0 + kHalf * h + 32);
+          }
+          if (!(ok = op_wait(bars.sfull(st, h), (h ? ns[1]++ : ns[0]++) & 1, abort, p.a.status, 9))) break;
+          tc_fence_after();
+          if (warp_live) {
+            const uint32_t tSh = tS + kHalf * h;
+            uint32_t s[kHalf];
+            tmem_ld32(tSh, s);
+            tmem_ld32(tSh + 32, s + 32);
+            tmem_wait32(s);
+            tmem_wait32(s + 32);
+            if (masked) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(tO + 128 * st + c, o);
+              for (int i = 0; i < kHalf; ++i)
+                if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            const float mnew = fmaxf(m, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * p.scale_log2);
+            const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
+            if (__any_sync(0xffffffffu, grow)) {
+              const float f = mnew == m ? 1.f : ex2(m - mnew);
+              if (steps > 0) {  // once the product before this one, of the other half, has ended
+                if (!(ok = op_wait(bars.pvdone(st, h ^ 1), ((h ? ns[0] : ns[1]) - 1) & 1, abort, p.a.status, 8))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 128 * st + c, o);
+                  tmem_wait16(o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st16(tO + 128 * st + c, o);
+                }
               }
+              l *= f;
+              m = mnew;
             }
-            l *= f;
-            m = mnew;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          const uint64_t neg = pack2(-mm, -mm);
-          uint64_t sum[2] = {0, 0};  // (two pairs of zeros)
+            const float mm = m == -INFINITY ? 0.f : m;
+            const uint64_t neg = pack2(-mm, -mm);
+            uint64_t sum[2] = {0, 0};  // (two pairs of zeros)
 #pragma unroll
-          for (int c = 0; c < kBlk / 32; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < kHalf / 32; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = 32 * c + 2 * i;
-              float2 x = unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2, neg));
-              x.x = ex2(x.x);
-              x.y = ex2(x.y);
-              sum[i & 1] = add2(sum[i & 1], pack2(x.x, x.y));
-              pk[i] = pack_bf16(x.x, x.y);
+              for (int i = 0; i < 16; ++i) {
+                const int j = 32 * c + 2 * i;
+                float2 x = unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2, neg));
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[i & 1] = add2(sum[i & 1], pack2(x.x, x.y));
+                pk[i] = pack_bf16(x.x, x.y);
+              }
+              tmem_st16(tSh + 16 * c, pk);
             }
-            tmem_st16(tS + 16 * c, pk);
+            const float2 total = unpack2(add2(sum[0], sum[1]));
+            l += total.x + total.y;
+            tmem_wait_st();
+            tc_fence_before();
           }
-          const float2 total = unpack2(add2(sum[0], sum[1]));
-          l += total.x + total.y;
-          tmem_wait_st();
-          tc_fence_before();
+          mbar_arrive(bars.pready(st, h));
         }
-        mbar_arrive(bars.pready(st));
       }
       if (!ok) break;
       // ------------------------------------------------------------ the item's result
-      used += 2 * nb;
       const bool whole = nb == it.nblk;
       const uint16_t* qrow = nullptr;
       uint16_t* dst = nullptr;
@@ -583,209 +621,236 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       // partial results: first item of the run in slot 0, a later (so last) one in slot 1
       const int slot = it.unit0 + it.ja == u0 ? 0 : 1;
-      const long long pt = ((long long)blockIdx.x * 2 + slot) * (two ? 2 : 1) + tile;
+      const long long pt = ((long long)blockIdx.x * 2 + slot) * (TWO ? 2 : 1) + tile;
       float4* part = reinterpret_cast<float4*>(p.part) + pt * (HD / 4) * kBlk + row;
-      if (two) {
-        if (!(ok = op_wait(bars.ofull(st), no[st] & 1, abort, p.a.status, 10))) break;
-        ++no[st];
-        tc_fence_after();
-        const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
-        if (!whole && node >= 0) p.part_ml[pt * kBlk + row] = make_float2(m, l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (warp_live) {
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 16) {
-            uint32_t u[16];
-            float o[16];
-            tmem_ld16(tO + 128 * st + c, u);
-            tmem_wait16(u);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]);
-            if (node >= 0) {
-              if (fix) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, m == -INFINITY ? 0.f : m, c + i);
-              }
-              put16(o, whole, inv, dst, part, c);
-            }
-          }
-        }
-        tc_fence_before();
+      float w0 = 1.f, w1 = 0.f;      // weights of the streams' sums (TWO: of this one's)
+      bool other = false;            // stream 1 had a block (TWO = false)
+      if (TWO) {
+        if (!(ok = op_wait(bars.ofull(st), no[0]++ & 1, abort, p.a.status, 10))) break;
       } else {
         // The streams' rows lie in the same lanes: each warpgroup joins one half of the columns
         // of both sums.
         sh.ml[st][row] = make_float2(m, l);
         if (!(ok = meet())) break;
         const float2 a = sh.ml[0][row], b = sh.ml[1][row];
-        const float top = fmaxf(a.x, b.x), mm = top == -INFINITY ? 0.f : top;
-        const float w0 = ex2(a.x - mm), w1 = ex2(b.x - mm);
+        m = fmaxf(a.x, b.x);
+        const float mm = m == -INFINITY ? 0.f : m;
+        w0 = ex2(a.x - mm);
+        w1 = ex2(b.x - mm);
         l = a.y * w0 + b.y * w1;
-        const bool other = nb > 1;  // stream 1 had a block
+        other = nb > 1;
         if (!(ok = op_wait(bars.ofull(0), no[0]++ & 1, abort, p.a.status, 10))) break;
         if (other && !(ok = op_wait(bars.ofull(1), no[1]++ & 1, abort, p.a.status, 11))) break;
-        tc_fence_after();
-        const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
-        if (!whole && node >= 0 && st == 0) p.part_ml[pt * kBlk + row] = make_float2(top, l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (warp_live) {
+      }
+      tc_fence_after();
+      const bool fix = *reinterpret_cast<volatile int*>(&sh.bad_v) != 0;
+      const float mm = m == -INFINITY ? 0.f : m;
+      if (!whole && node >= 0 && (TWO || st == 0)) p.part_ml[pt * kBlk + row] = make_float2(m, l);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (warp_live) {
+        const int c0 = TWO ? 0 : (int)st * (HD / 2), c1 = TWO ? HD : c0 + HD / 2;
+        const uint32_t own = tO + (TWO ? 128 * st : 0);
 #pragma unroll 1
-          for (int c = st * (HD / 2); c < (st + 1) * (HD / 2); c += 16) {
-            uint32_t u[16], v[16];
-            float o[16];
-            tmem_ld16(tO + c, u);
-            if (other) tmem_ld16(tO + 128 + c, v);
-            tmem_wait16(u);
-            tmem_wait16(v);
+        for (int c = c0; c < c1; c += 16) {
+          uint32_t u[16], v[16];
+          float o[16];
+          tmem_ld16(own + c, u);
+          if (other) tmem_ld16(tO + 128 + c, v);
+          tmem_wait16(u);
+          tmem_wait16(v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = w0 * __uint_as_float(u[i]) + (other ? w1 * __uint_as_float(v[i]) : 0.f);
-            if (node >= 0) {
-              if (fix) {
+          for (int i = 0; i < 16; ++i) {
+            o[i] = __uint_as_float(u[i]);
+            if (!TWO) o[i] = w0 * o[i] + (other ? w1 * __uint_as_float(v[i]) : 0.f);
+          }
+          if (node >= 0) {
+            if (fix) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, mm, c + i);
-              }
-              put16(o, whole, inv, dst, part, c);
+              for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, mm, c + i);
             }
+            put16(o, whole, inv, dst, part, c);
           }
         }
-        tc_fence_before();
-        if (!(ok = meet())) break;
       }
+      tc_fence_before();
+      if (!TWO && !(ok = meet())) break;
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
-      // ---------------------------------------------------------------- producer
-      // lane i < 8 looks up page i of the next block while this one's copies are issued
-      Ring put;
-      uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
-      bool ok = true;
-      auto look_up = [&](const Item& it, int j) -> int {  // first row group of lane's page of block j
-        const int key = it.kstart + j * kBlk + lane * kOpPage;
-        const int page = lane < 8 && key < it.end ? page_of(p, it.b, key, true) : 0;
-        return (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);
-      };
-      while (ok && uniform(run.next(p, sh.pre))) {
-        const Item& it = run.it;
-        const int blocks = (int)uniform(run.it.jb - run.it.ja);
-        const uint32_t rows = p.npt * p.gs;
-        int page = look_up(it, it.ja);
-        for (int blk = 0; ok && blk < blocks; ++blk) {
-          const int j = it.ja + blk;
-          const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
-          uint32_t group[8];
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- producer
+    // lane i < 8 looks up page i of the next block while this one's copies are issued
+    Ring put, block;                // ring slots; blocks
+    uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
+    bool ok = true;
+    auto look_up = [&](const Item& it, int j) -> int {  // first row group of lane's page of block j
+      const int key = it.kstart + j * kBlk + lane * kOpPage;
+      const int page = lane < 8 && key < it.end ? page_of(p, it.b, key, true) : 0;
+      return (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);
+    };
+    while (ok && uniform(run.next(p))) {
+      const Item& it = run.it;
+      const int blocks = (int)uniform(it.jb - it.ja);
+      const uint32_t rows = p.npt * p.gs;
+      int page = look_up(it, it.ja);
+      for (int blk = 0; ok && blk < blocks; ++blk) {
+        const int j = it.ja + blk;
+        const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
+        uint32_t group[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, page, i);
-          if (blk + 1 < blocks) page = look_up(it, j + 1);
-          for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(stages)) {
-            const uint32_t s = put.slot;
-            if (!(ok = op_wait(bars.empty(s), put.phase ^ 1, abort, p.a.status, 1))) break;
+        for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, page, i);
+        if (blk + 1 < blocks) page = look_up(it, j + 1);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(kStages)) {
+          const uint32_t s = put.slot;
+          if (!(ok = op_wait(bars.empty(s), put.phase ^ 1, abort, p.a.status, 1))) break;
+          if (elect_one()) {
+            const uint32_t dst = ring + s * C::kTile, bar = kv ? bars.vfull(block.slot) : bars.kfull(block.slot);
+            mbar_expect_tx(bar, live * kOpPage * HD * 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
+          }
+          __syncwarp();
+          if (kv == 0 && blk == 0) {  // the item's queries, once the last item's products have read theirs
+            if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
+            ++qphase;
+            const uint32_t tiles = uniform(TWO && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1);
+            const int head = (int)uniform(it.kvh * p.gs), node = (int)uniform(it.tp * nodes_per_group(p)), seq = (int)uniform(it.b);
             if (elect_one()) {
-              const uint32_t dst = ring + s * C::kTile, bar = bars.full(s);
-              mbar_expect_tx(bar, live * kOpPage * HD * 2);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
+              mbar_expect_tx(bars.qfull(), tiles * rows * HD * 2);
+              for (uint32_t t = 0; t < tiles; ++t)
+                for (int h = 0; h < C::kHalves; ++h)
+                  op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), head,
+                            node + (int)t * p.npt, seq, bars.qfull());
             }
             __syncwarp();
-            if (kv == 0 && blk == 0) {  // the item's queries, once the last item's products have read theirs
-              if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
-              ++qphase;
-              const uint32_t tiles = uniform(two && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1);
-              const int head = (int)uniform(it.kvh * p.gs), node = (int)uniform(it.tp * nodes_per_group(p)), seq = (int)uniform(it.b);
-              if (elect_one()) {
-                mbar_expect_tx(bars.qfull(), tiles * rows * HD * 2);
-                for (uint32_t t = 0; t < tiles; ++t)
-                  for (int h = 0; h < C::kHalves; ++h)
-                    op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), head,
-                              node + (int)t * p.npt, seq, bars.qfull());
-              }
-              __syncwarp();
-            }
           }
         }
+        block.advance(kStages);
       }
-      // an abandoned run leaves copies in flight: wait for them (bounded)
-      if (*abort) {
-        const uint32_t n = min(fill, (uint32_t)stages);
-        for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(bars.full(f % stages), (f / stages) & 1, 10000000ll);
-        if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
-      }
-    } else if (warp == 9) {
-      // ---------------------------------------------------------------- MMA issue
-      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kBlk);
-      constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
-      // queries: spans of 128 rows one behind the other (one copy each); keys: see TreeCfg
-      Ring k_at, v_at;                    // slots of the next K and V block (every second slot each)
-      v_at.advance(stages);
-      auto skip2 = [&](Ring& r) {
-        r.advance(stages);
-        r.advance(stages);
-      };
-      uint32_t np[2] = {0, 0}, nq = 0;    // P tiles received per stream, items
-      const uint32_t tm = uniform(tmem);
-      // descriptors of the first query tile and ring stage; a tile further is kTile / 16 more
+    }
+    // an abandoned run leaves copies in flight: wait for them (bounded)
+    if (*abort) {
+      const uint32_t n = min(fill, kStages);
+      for (uint32_t f = fill - n; f < fill; ++f)
+        mbar_wait(f & 1 ? bars.vfull(f / 2 % kStages) : bars.kfull(f / 2 % kStages), (f / 2 / kStages) & 1, 10000000ll);
+      if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
+    }
+  } else if (warp == 9 || warp == 10) {
+    // ---------------------------------------------------------------- S = Q K^T (warp 9), O += P V (warp 10)
+    // Both walk the streams' halves in turn, in one thread.  queries: spans of 128 rows one behind the
+    // other (one copy each); keys: see TreeCfg.  The second half of a key block and the next tile are
+    // additions to the descriptors.
+    constexpr uint32_t idesc_s = umma_idesc_bf16(128, kHalf);
+    constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
+    constexpr uint32_t kHalfOff = kHalf / 8 * C::kGroup / 16, kTileOff = C::kTile / 16;
+    if (elect_one()) {
+      const bool pv = warp == 10;
       const uint64_t dq = umma_sdesc_sw(q_s, 16, 8 * C::kSpan, C::kSpan), dk = umma_sdesc_sw(ring, 16, C::kGroup, C::kSpan);
       const uint64_t dv = umma_sdesc_sw(ring, 8 * C::kSpan, C::kGroup, C::kSpan);
+      uint32_t used[2][2] = {{0, 0}, {0, 0}}, nq = 0;  // uses of the streams' halves, items
+      uint32_t item = 0;                               // ring slots of earlier items
       bool ok = true;
-      while (ok && uniform(run.next(p, sh.pre))) {
-        const int nb = (int)uniform((uint32_t)(run.it.jb - run.it.ja));
-        const int steps = two ? 2 * nb : nb;
-        if (!(ok = op_wait(bars.qfull(), nq & 1, abort, p.a.status, 3))) break;
-        tc_fence_after();
-        ++nq;
-        // step t: stream t & 1, block t >> 1 (two) or t
-        auto issue_s = [&](int t) -> bool {
-          const uint32_t st = t & 1, s = uniform(k_at.slot);
-          if (!op_wait(bars.full(s), k_at.phase, abort, p.a.status, 4)) return false;
+      while (ok && run.next(p)) {
+        const Item& it = run.it;
+        const int nb = it.jb - it.ja;
+        const int last_halves = block_halves(it, nb - 1);
+        if (!pv) {
+          if (!(ok = op_wait1(bars.qfull(), nq++ & 1, abort, p.a.status, 3))) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint64_t a = dq + (two ? st : 0) * (C::kTile / 16), b = dk + s * (C::kTile / 16);
+        }
+        int blk[2] = {0, TWO ? 0 : 1};                 // next half of the streams: its block,
+        int half[2] = {0, 0};
+        Ring slot[2], count[2];                        // the block's slot in the ring, and the block
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint32_t a = item + (TWO ? 0 : 2 * st);
+          slot[st].slot = a % kStages;
+          slot[st].phase = a / kStages & 1;
+          if (pv) slot[st].advance(kStages);
+          count[st].slot = a / 2 % kStages;
+          count[st].phase = a / 2 / kStages & 1;
+        }
+        auto step = [&](auto stream) -> bool {
+          constexpr uint32_t st = decltype(stream)::value;
+          const uint32_t s = slot[st].slot;
+          const uint32_t h = half[st];
+          const uint32_t n = h ? used[st][1]++ : used[st][0]++;
+          const bool done = h == 1 || (blk[st] + 1 == nb && last_halves == 1);  // the block's last half
+          const uint32_t sp = tmem + kTmemS + 128 * st + kHalf * h;
+          if (!pv) {
+            if (h == 0 && !op_wait1(bars.kfull(count[st].slot), count[st].phase, abort, p.a.status, 4)) return false;
+            if (n > 0 && !op_wait1(bars.pvdone(st, h), (n - 1) & 1, abort, p.a.status, 5)) return false;  // P of the last use
+            tc_fence_after();
+            const uint64_t a = dq + (TWO ? st : 0) * kTileOff, b = dk + s * kTileOff + h * kHalfOff;
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
               const uint32_t off = ((kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan) / 16;
-              umma_bf16(tm + kTmemS + 128 * st, a + off, b + C::column16(kk) / 16, idesc_s, kk > 0);
+              umma_bf16(sp, a + off, b + C::column16(kk) / 16, idesc_s, kk > 0);
             }
-            umma_commit(bars.sfull(st));
-            if (!two || st == 1) umma_commit(bars.empty(s));
+            umma_commit(bars.sfull(st, h));
+          } else {
+            if (h == 0 && !op_wait1(bars.clean(count[st].slot), count[st].phase, abort, p.a.status, 6)) return false;
+            if (!op_wait1(bars.pready(st, h), n & 1, abort, p.a.status, 13)) return false;
+            tc_fence_after();
+            const uint64_t b = dv + s * kTileOff + h * kHalfOff;
+            const bool first = h == 0 && blk[st] == (TWO ? 0 : (int)st);
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              umma_bf16_ta(tmem + kTmemO + 128 * st, sp + 8 * kk, b + kk * (2 * C::kGroup / 16), idesc_o, !first || kk > 0);
+            umma_commit(bars.pvdone(st, h));
+            if (done && blk[st] + (TWO ? 1 : 2) >= nb) umma_commit(bars.ofull(st));
           }
-          __syncwarp();
-          if (!two || st == 1) skip2(k_at);
+          if (!done) {
+            half[st] = 1;
+            return true;
+          }
+          if (!TWO || st == 1) umma_commit(bars.empty(s));
+          half[st] = 0;
+          blk[st] += TWO ? 1 : 2;
+#pragma unroll
+          for (int i = 0; i < (TWO ? 2 : 4); ++i) slot[st].advance(kStages);
+#pragma unroll
+          for (int i = 0; i < (TWO ? 1 : 2); ++i) count[st].advance(kStages);
           return true;
         };
-        ok = issue_s(0) && (steps < 2 || issue_s(1));
-        for (int t = 0; ok && t < steps; ++t) {
-          const uint32_t st = t & 1, blk = two ? t >> 1 : t;
-          const uint32_t s = uniform(v_at.slot);
-          if (!(ok = op_wait(bars.full(s), v_at.phase, abort, p.a.status, 5))) break;
-          if (!(ok = op_wait(bars.pready(st), (st ? np[1] : np[0]) & 1, abort, p.a.status, 6))) break;
-          if (st) ++np[1]; else ++np[0];
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t b = dv + s * (C::kTile / 16);
-            const bool first = two ? blk == 0 : blk == st;
-#pragma unroll
-            for (int kk = 0; kk < kBlk / 16; ++kk)
-              umma_bf16_ta(tm + kTmemO + 128 * st, tm + kTmemS + 128 * st + 8 * kk, b + kk * (2 * C::kGroup / 16), idesc_o, !first || kk > 0);
-            if (!two || st == 1) umma_commit(bars.empty(s));
-            if (t + 2 >= steps) umma_commit(bars.ofull(st));
-            if (t + 1 == steps) umma_commit(bars.qempty());
-          }
-          __syncwarp();
-          if (!two || st == 1) skip2(v_at);
-          if (t + 2 < steps) ok = issue_s(t + 2);
+        while (ok && (blk[0] < nb || blk[1] < nb)) {
+          if (blk[0] < nb) ok = step(std::integral_constant<uint32_t, 0>{});
+          if (ok && blk[1] < nb) ok = step(std::integral_constant<uint32_t, 1>{});
         }
+        if (ok && !pv) umma_commit(bars.qempty());
+        item += 2 * nb;
       }
-      if (*abort) {  // let the products in flight end before the memory goes
-        if (elect_one()) umma_commit(bars.ofull(0));
-        __syncwarp();
-        const uint64_t t0 = gtime();
-        while ((long long)(gtime() - t0) < 10000000ll) {}
+    }
+    __syncwarp();
+    if (*abort) {  // let the products in flight end before the memory goes
+      const uint64_t t0 = gtime();
+      while ((long long)(gtime() - t0) < 10000000ll) {}
+    }
+  } else {
+    // ---------------------------------------------------------------- cleaning
+    Ring at, block;       // V's ring slot, block
+    at.advance(kStages);
+    bool ok = true;
+    while (ok && uniform(run.next(p))) {
+      const Item& it = run.it;
+      const int nb = (int)uniform(it.jb - it.ja);
+      for (int blk = 0; blk < nb; ++blk) {
+        const int k0 = it.kstart + (it.ja + blk) * kBlk;
+        if (!(ok = op_wait(bars.vfull(block.slot), block.phase, abort, p.a.status, 12))) break;
+        if (uniform(masked_block(p, it, k0))) {
+          clean_v<HD, 32>(ring_g + at.slot * C::kTile, it.end - k0, lane, &sh.bad_v);
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(bars.clean(block.slot));
+        block.advance(kStages);
+        at.advance(kStages);
+        at.advance(kStages);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 11) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -855,23 +920,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
+template <int HD, bool TWO>
+cudaError_t launch_one(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(tree_kernel<HD, TWO>, TreeSmem<HD>::kBytes, done);
+  if (e != cudaSuccess) return e;
+  tree_kernel<HD, TWO><<<p.grid, kTreeThreads, TreeSmem<HD>::kBytes, st>>>(p, tq, tk, tv);
+  return cudaGetLastError();
+}
+
 template <int HD>
 cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  static std::atomic<int> regs{0};
-  cudaError_t e = allow_smem(tree_kernel<HD>, TreeSmem<HD>::kBytes, done);
-  if (e != cudaSuccess) return e;
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    // the softmax warpgroups would wait for ever for registers that the launch does not hold
-    cudaFuncAttributes at = {};
-    e = cudaFuncGetAttributes(&at, tree_kernel<HD>);
-    if (e != cudaSuccess) return e;
-    regs.store(at.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) < kLaunchRegs) return cudaErrorLaunchOutOfResources;
-  tree_kernel<HD><<<p.grid, kTreeThreads, TreeSmem<HD>::kBytes, st>>>(p, tq, tk, tv);
-  e = cudaGetLastError();
+  const cudaError_t e = p.two ? launch_one<HD, true>(p, tq, tk, tv, st) : launch_one<HD, false>(p, tq, tk, tv, st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.c.batch * p.c.n_kv_heads * p.ntp * (p.two ? 2 : 1) * 4), HD / 16);
