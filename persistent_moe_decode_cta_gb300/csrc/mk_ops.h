@@ -56,6 +56,7 @@ struct TreeParams {
   float scale_log2;
   float* part;     // partial results: [grid][2][tiles][hd / 4][128] float4
   float2* part_ml; // [grid][2][tiles][128] (running maximum, sum)
+  int* table;      // prefix sums of the work list, written for the join
 };
 size_t tree_workspace_bytes(const TreeParams& p);
 cudaError_t launch_tree(TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -155,7 +155,8 @@ __device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool r
 
 // run of team g of G: units [g * U / G, (g + 1) * U / G).  G <= U: every run has a unit, so the
 // parts of an item are those of consecutive teams.
-__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid / p.team, U); }
+// (One tile: two blocks a run, where there are so few, since its two streams take one each.)
+__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid / p.team, p.two ? U : (U + 1) / 2); }
 __device__ __forceinline__ int run_begin(int g, int U, int G) { return g * (U / G) + g * (U % G) / G; }
 __device__ __forceinline__ int run_owner(int u, int U, int G) {  // the g with run_begin(g) <= u < run_begin(g + 1)
   int g = min(G - 1, (int)((float)(u + 1) * G / U));
@@ -366,11 +367,9 @@ __device__ __forceinline__ void clean_v(uint8_t* stage, int live, int t, int* ba
   }
 }
 
-__device__ __forceinline__ int page_of(const TreeParams& p, int b, int key, bool record) {
+__device__ __forceinline__ int page_of(const TreeParams& p, int b, int key) {
   const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + key / kOpPage);
-  if (page >= 0 && page < p.c.n_pages) return page;
-  if (record) op_error(p.a.status, MK_ERR_BAD_PAGE, b, key / kOpPage, page);
-  return 0;
+  return page >= 0 && page < p.c.n_pages ? page : 0;
 }
 
 // What clean_v dropped from column c of a row: p_j * v_j of the keys that the row sees.  Only
@@ -386,7 +385,7 @@ __device__ __noinline__ float nonfinite_part(const TreeParams& p, const Item& it
     for (int w = 0; w < kBlk / 32; ++w) {
       for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
         const int key = k0 + 32 * w + __ffs(bits) - 1;
-        const long long at = (((long long)page_of(p, it.b, key, false) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
+        const long long at = (((long long)page_of(p, it.b, key) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
         const float v = bf16_to_f(V[at + c]);
         if (fabsf(v) <= 3.4e38f) continue;
         float s = 0.f;
@@ -497,6 +496,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
+  if (blockIdx.x == 0 && threadIdx.x <= kScan) p.table[threadIdx.x] = sh.pre[threadIdx.x];  // for the join
   const int U = sh.pre[kScan];
   const int G = run_count(p, U), team = (int)blockIdx.x / p.team;
   if (team >= G) {  // (the whole CTA)
@@ -677,27 +677,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- producer
-    // lane i < 8 looks up page i of the next block while this one's copies are issued
+    // lane i < 8 looks up page i of a block; the table is read two blocks ahead and not looked at
+    // before it is needed, so that its latency is nobody's
     Ring put, block;                // ring slots; blocks
     uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
     bool ok = true;
-    auto look_up = [&](const Item& it, int j) -> int {  // first row group of lane's page of block j
-      const int key = it.kstart + j * kBlk + lane * kOpPage;
-      const int page = lane < 8 && key < it.end ? page_of(p, it.b, key, true) : 0;
-      return (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);
+    auto look_up = [&](const Item& it, int j) -> int {
+      const int at = (it.kstart + j * kBlk) / kOpPage + lane;
+      return lane < 8 && at * kOpPage < it.end ? __ldg(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
     };
     while (ok && uniform(run.next(p))) {
       const Item& it = run.it;
       const int blocks = (int)uniform(it.jb - it.ja);
       const uint32_t rows = p.npt * p.gs;
-      int page = look_up(it, it.ja);
+      int page1 = look_up(it, it.ja), page2 = look_up(it, it.ja + 1);
       for (int blk = 0; ok && blk < blocks; ++blk) {
         const int j = it.ja + blk;
         const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
+        int page = page1;
+        page1 = page2;
+        page2 = look_up(it, j + 2);
+        if (page < 0 || page >= p.c.n_pages) {
+          op_error(p.a.status, MK_ERR_BAD_PAGE, it.b, (it.kstart + j * kBlk) / kOpPage + lane, page);
+          page = 0;
+        }
+        __syncwarp();
+        const int first = (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);  // its first row group
         uint32_t group[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, page, i);
-        if (blk + 1 < blocks) page = look_up(it, j + 1);
+        for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, first, i);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(kStages)) {
           const uint32_t s = put.slot;
@@ -857,67 +865,128 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ------------------------------------------------------------------ joining the parts
-// One block per (item, row tile, 32 rows, 16 columns): thread = (row, 4 columns).
-constexpr int kJoinThreads = 128;
-static_assert(kJoinThreads >= kScan, "the join adds up the work list too");
+// A block joins (row, 4 columns) pieces of one row tile of an item, rows side by side as the
+// parts have them.  Few items have many parts each (38 at batch 1 with 4 KV heads): GROUPS = 4
+// groups of threads share them and meet in shared memory, a piece per thread.  Many items have
+// fewer than nine: GROUPS = 1, four pieces per thread.
+constexpr int kJoinThreads = 256;
+template <int GROUPS>
+constexpr int kJoinPieces = GROUPS == 1 ? 4 : 1;  // per thread
 
-template <int HD>
+template <int HD, int GROUPS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ int pre[kScan + 1];
-  __shared__ int warp_sums[kScan / 32];
-  // (the inputs of the work list are older than the kernel before this one)
-  scan_units(p, pre, warp_sums, false);
-  pdl_wait();
-  const int U = pre[kScan];
-  const int tiles = p.two ? 2 : 1;
+  constexpr int kSide = kJoinThreads / GROUPS, kN = kJoinPieces<GROUPS>;
+  __shared__ float4 s_o[GROUPS][kSide];
+  __shared__ float2 s_ml[GROUPS][kSide];
+  const int tiles = p.two ? 2 : 1, rows = p.npt * p.gs;
   int i = blockIdx.x;
-  const int rowq = i & 3;
-  i >>= 2;
   const int tile = i % tiles;
   i /= tiles;
   const int tp = i % p.ntp;
   i /= p.ntp;
   const int kvh = i % p.c.n_kv_heads, b = i / p.c.n_kv_heads;
+  const int group = threadIdx.x / kSide, side = threadIdx.x % kSide;
   const int member = tp % p.team, e = b * ((p.ntp + p.team - 1) / p.team) + tp / p.team;
-  const int chunk = (num_entries(p) + kScan - 1) / kScan;
-  int g0 = pre[e / chunk];
-  for (int x = e / chunk * chunk; x < e; ++x) g0 += make_entry(p, x, false).nblk * p.c.n_kv_heads;
+  // (the inputs of the work list are older than the kernel before this one)
   const Entry x = make_entry(p, e, false);
-  const SeqShape s = x.s;
-  const int end = group_end(p, s, tp);
+  const int end = group_end(p, x.s, tp), nblk = (end - x.kstart + kBlk - 1) / kBlk;
+  const int chunk = (num_entries(p) + kScan - 1) / kScan;
+  int g0 = kvh * x.nblk;
+  for (int y = e / chunk * chunk; y < e; ++y) g0 += make_entry(p, y, false).nblk * p.c.n_kv_heads;
+  pdl_wait();
   if (end == 0) return;
-  g0 += kvh * x.nblk;
-  const int nblk = (end - x.kstart + kBlk - 1) / kBlk;
+  const int U = __ldcg(p.table + kScan);
+  g0 += __ldcg(p.table + e / chunk);
   const int G = run_count(p, U);
-  const int c0 = run_owner(g0, U, G), c1 = run_owner(g0 + nblk - 1, U, G);
-  if (c0 == c1) return;  // written whole
-  const int row = rowq * 32 + (threadIdx.x & 31), c4 = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int node_in = row / p.gs, node = tp * nodes_per_group(p) + tile * p.npt + node_in;
-  if (node_in >= p.npt || node >= s.cnt) return;
+  const int r0 = run_owner(g0, U, G), r1 = run_owner(g0 + nblk - 1, U, G);
+  if (r0 == r1) return;  // written whole
   // slot 0 holds the item that a run starts in: every part but, maybe, the first
-  const int slot0 = run_begin(c0, U, G) >= g0 ? 0 : 1;
-  auto part_of = [&](int c) -> long long { return (((long long)c * p.team + member) * 2 + (c == c0 ? slot0 : 0)) * tiles + tile; };
-  float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(&p.part_ml[part_of(c) * kBlk + row].x));
-  const float mm = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const long long pt = part_of(c);
-    const float2 ml = __ldcg(p.part_ml + pt * kBlk + row);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part) + (pt * (HD / 4) + c4) * kBlk + row);
-    const float w = ex2(ml.x - mm);
-    l += w * ml.y;
-    o.x += w * x.x;
-    o.y += w * x.y;
-    o.z += w * x.z;
-    o.w += w * x.w;
+  const int slot0 = run_begin(r0, U, G) >= g0 ? 0 : 1;
+  auto part_of = [&](int r) -> long long { return (((long long)r * p.team + member) * 2 + (r == r0 ? slot0 : 0)) * tiles + tile; };
+  int row[kN], c4[kN];
+  bool live[kN];
+  float m[kN], l[kN];
+  float4 o[kN];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    const int at = (blockIdx.y * kN + n) * kSide + side;
+    c4[n] = at / rows;
+    row[n] = at - c4[n] * rows;
+    live[n] = c4[n] < HD / 4 && tp * nodes_per_group(p) + tile * p.npt + row[n] / p.gs < x.s.cnt;
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+    o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = static_cast<uint16_t*>(p.a.out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] +
-                  (long long)(kvh * p.gs + row % p.gs) * p.a.out_stride[2] + 4 * c4;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  constexpr int kBatch = GROUPS == 1 ? 2 : 4;  // parts whose loads go out together
+  for (int r = r0 + group; r <= r1; r += GROUPS * kBatch) {
+    float2 ml[kBatch][kN];
+    float4 y[kBatch][kN];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = min(r + k * GROUPS, r1);
+      const long long pt = part_of(q);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        ml[k][n] = make_float2(-INFINITY, 0.f);
+        y[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live[n] && r + k * GROUPS <= r1) {
+          ml[k][n] = __ldcg(p.part_ml + pt * kBlk + row[n]);
+          y[k][n] = __ldcg(reinterpret_cast<const float4*>(p.part) + (pt * (HD / 4) + c4[n]) * kBlk + row[n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float top = m[n];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k][n].x);
+      const float mm = top == -INFINITY ? 0.f : top, f = ex2(m[n] - mm);
+      m[n] = top;
+      l[n] *= f;
+      o[n] = make_float4(o[n].x * f, o[n].y * f, o[n].z * f, o[n].w * f);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = ex2(ml[k][n].x - mm);
+        l[n] += w * ml[k][n].y;
+        o[n].x += w * y[k][n].x;
+        o[n].y += w * y[k][n].y;
+        o[n].z += w * y[k][n].z;
+        o[n].w += w * y[k][n].w;
+      }
+    }
+  }
+  if (GROUPS > 1) {
+    s_o[group][side] = o[0];
+    s_ml[group][side] = make_float2(m[0], l[0]);
+    __syncthreads();
+    if (group) return;
+    float top = m[0];
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) top = fmaxf(top, s_ml[k][side].x);
+    const float mm = top == -INFINITY ? 0.f : top;
+    l[0] = 0.f;
+    o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      const float2 ml = s_ml[k][side];
+      const float4 y = s_o[k][side];
+      const float w = ex2(ml.x - mm);
+      l[0] += w * ml.y;
+      o[0].x += w * y.x;
+      o[0].y += w * y.y;
+      o[0].z += w * y.z;
+      o[0].w += w * y.w;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    if (!live[n]) continue;
+    const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
+    const int node = tp * nodes_per_group(p) + tile * p.npt + row[n] / p.gs;
+    uint16_t* dst = static_cast<uint16_t*>(p.a.out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] +
+                    (long long)(kvh * p.gs + row[n] % p.gs) * p.a.out_stride[2] + 4 * c4[n];
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[n].x * inv, o[n].y * inv), pack_bf16(o[n].z * inv, o[n].w * inv));
+  }
 }
 
 template <int HD, bool TWO>
@@ -935,8 +1004,11 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
                       cudaStream_t st) {
   const cudaError_t e = p.two ? launch_one<HD, true>(p, tq, tk, tv, st) : launch_one<HD, false>(p, tq, tk, tv, st);
   if (e != cudaSuccess) return e;
+  const long long heads = (long long)p.c.batch * p.c.n_kv_heads * p.ntp;
+  const bool many = 8 * heads > p.grid;  // up to 9 parts an item
+  const int pieces = many ? kJoinThreads * kJoinPieces<1> : kJoinThreads / 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.c.batch * p.c.n_kv_heads * p.ntp * (p.two ? 2 : 1) * 4), HD / 16);
+  cfg.gridDim = dim3((unsigned)(heads * (p.two ? 2 : 1)), (unsigned)((p.npt * p.gs * (HD / 4) + pieces - 1) / pieces));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at = {};
@@ -944,14 +1016,14 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<HD>, p);
+  return many ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1>, p) : cudaLaunchKernelEx(&cfg, join_kernel<HD, 4>, p);
 }
 
 }  // namespace
 
 size_t tree_workspace_bytes(const TreeParams& p) {
   const size_t tiles = (size_t)p.grid * 2 * (p.two ? 2 : 1);
-  return tiles * kBlk * ((size_t)p.c.head_dim * 4 + sizeof(float2));
+  return tiles * kBlk * ((size_t)p.c.head_dim * 4 + sizeof(float2)) + (kScan + 1) * sizeof(int);
 }
 
 cudaError_t launch_tree(TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -959,6 +1031,7 @@ cudaError_t launch_tree(TreeParams& p, const CUtensorMap& tq, const CUtensorMap&
   const size_t tiles = (size_t)p.grid * 2 * (p.two ? 2 : 1);
   p.part = static_cast<float*>(p.a.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + tiles * kBlk * p.c.head_dim);
+  p.table = reinterpret_cast<int*>(p.part_ml + tiles * kBlk);
   if (p.c.head_dim == 128) return launch_hd<128>(p, tq, tk, tv, st);
   if (p.c.head_dim == 64) return launch_hd<64>(p, tq, tk, tv, st);
   return launch_hd<32>(p, tq, tk, tv, st);
