@@ -51,6 +51,19 @@ __device__ __forceinline__ bool op_wait1(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool op_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // v, equal in all lanes, as a value that the compiler knows to be so
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 

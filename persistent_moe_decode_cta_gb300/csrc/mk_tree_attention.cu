@@ -14,15 +14,17 @@
 // other's products.  Up to 128 rows per KV head both streams work on the same rows, on
 // even and odd key blocks, and are merged at the end (TWO = false); with more rows each
 // stream has a tile of its own and both use every key block that is loaded (TWO = true),
-// which halves the key traffic where it would exceed what L2 delivers.  A stream takes a block
-// in two halves of 64 keys with an S/P buffer each: S of the next half is computed while the
-// softmax of this one runs, so that a stream never waits for its own products.  S and P V
-// are issued by a warp each: the tensor pipe queues too few products to cover a warp's waits
-// between two groups (8 products of 64 cycles cost 514 cycles alone, 700 with two waits and
-// two commits), and so one warp's overhead is the other's time.
+// which halves the key traffic where it would exceed what L2 delivers.
+//
+// One thread issues all products.  TWO = true is bound by them: P V of a block and S of the
+// stream's next one go out behind one wait (32 products of 64 cycles a pair of blocks; the queue
+// does not cover the 60 to 75 cycles of each wait).  TWO = false is bound by the copies: a
+// stream takes a block in two halves with an S/P buffer each, and S of a block is computed as soon
+// as its K is there, whatever the softmax is at, so that the slots of the ring are free again early
+// (with whole blocks: 122 us instead of 106 for 16 nodes at 32K of 8 sequences).
 //
 // Keys that a row does not see get a score of -infinity.  Blocks with such keys have their V
-// cleaned in shared memory by a further warp (rows past the end and values that are not
+// cleaned in shared memory by two further warps (rows past the end and values that are not
 // finite become zero, since 0 * NaN would reach every row); what was dropped is added by plain
 // loads at the end, for the rows that do see it.
 //
@@ -40,9 +42,9 @@ namespace mk {
 namespace {
 
 constexpr int kBlk = 128;               // keys of a block
-constexpr int kHalf = 64;               // keys of a softmax step
-constexpr int kTreeThreads = 384;       // two softmax warpgroups; copy, S, P V and cleaning warps
-constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P halves of the streams from 0 and 128, O from 256 and 384
+constexpr int kTreeThreads = 384;       // two softmax warpgroups; a copy, a product and two cleaning warps
+constexpr int kCleaners = 64;
+constexpr int kTmemS = 0, kTmemO = 256;  // columns: S/P of the streams at 0 and 128, O at 256 and 384
 constexpr float kRescale = 8.f;         // the maximum may lag by 2^8 before O is rescaled
 
 // Shared-memory layout of a tile of 128 rows: groups of 8 rows, of each group the spans one
@@ -182,8 +184,9 @@ struct Run {
     first = pre[lo];
     x = make_entry(p, e, false);
   }
-  // the next item with blocks of this group in the run
-  __device__ __forceinline__ bool next(const TreeParams& p) {
+  // The next item with blocks of this group in the run.  (One copy for all roles: an inlined
+  // one per role, rarely run, costs thousands of cycles of instruction fetches each time.)
+  __device__ __noinline__ bool next(const TreeParams& p) {
     while (u < u1) {
       while (u >= first + x.nblk * p.c.n_kv_heads) {
         first += x.nblk * p.c.n_kv_heads;
@@ -235,7 +238,7 @@ __device__ __forceinline__ Row make_row(const TreeParams& p, const Item& it, int
 }
 
 // Bit i: the row sees key kb + i (32 keys).
-__device__ uint32_t sees32(const TreeParams& p, const Item& it, const Row& r, int kb) {
+__device__ __noinline__ uint32_t sees32(const TreeParams& p, const Item& it, const Row& r, int kb) {
   if (r.node < 0) return 0;
   uint32_t bits = 0;
   if (kb < it.len) {  // cached keys [max(lo, kb), min(len, kb + 32))
@@ -294,7 +297,7 @@ struct TreeShared {
   int pre[kScan + 1];
   int warp_sums[kScan / 32];
   float2 ml[2][kBlk];    // the streams' (m, sum) for the merge
-  unsigned long long bars[4 * kMaxStages + 17];
+  unsigned long long bars[3 * kMaxStages + 17];
 };
 
 template <int HD>
@@ -303,24 +306,24 @@ struct TreeSmem {
   static_assert(kBytes <= 232448, "exceeds the 227 KB per-block shared memory limit");
 };
 
-// Key block i of the CTA's run (i modulo the ring's slots) has barriers of its own for its K,
-// its V and its cleaned V: whoever waits for one has seen, or knows done, its previous use, so
-// that the parity of a phase says which one it is.  (A slot's fills alternate between K and V when
-// the number of slots is odd, and nobody sees them all but the producer.)
+// Key block i of the CTA's run (i modulo the ring's slots) has barriers of its own for its K and
+// its V: whoever waits for one has seen, or knows done, its previous use, so that the parity
+// of a phase says which one it is.  (A slot's fills alternate between K and V when the number
+// of slots is odd, and nobody sees them all but the producer.)
 struct Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t kfull(uint32_t i) const { return base + 8 * i; }                     // copied
   __device__ __forceinline__ uint32_t vfull(uint32_t i) const { return base + 8 * (kMaxStages + i); }
-  __device__ __forceinline__ uint32_t clean(uint32_t i) const { return base + 8 * (2 * kMaxStages + i); }  // V fit for use
-  __device__ __forceinline__ uint32_t empty(uint32_t s) const { return base + 8 * (3 * kMaxStages + s); }  // slot s read
-  __device__ __forceinline__ uint32_t one(int i) const { return base + 8 * (4 * kMaxStages + i); }
+  __device__ __forceinline__ uint32_t empty(uint32_t s) const { return base + 8 * (2 * kMaxStages + s); }  // slot s read
+  __device__ __forceinline__ uint32_t one(int i) const { return base + 8 * (3 * kMaxStages + i); }
   __device__ __forceinline__ uint32_t qfull() const { return one(0); }
   __device__ __forceinline__ uint32_t qempty() const { return one(1); }
   __device__ __forceinline__ uint32_t meet() const { return one(2); }
-  __device__ __forceinline__ uint32_t sfull(uint32_t st, uint32_t h) const { return one(3 + 2 * st + h); }   // S of a half
-  __device__ __forceinline__ uint32_t pready(uint32_t st, uint32_t h) const { return one(7 + 2 * st + h); }  // P of a half
-  __device__ __forceinline__ uint32_t pvdone(uint32_t st, uint32_t h) const { return one(11 + 2 * st + h); } // its product P V
-  __device__ __forceinline__ uint32_t ofull(uint32_t st) const { return one(15 + st); }                      // an item's last one
+  // (TWO = false: per half h of a block)
+  __device__ __forceinline__ uint32_t sfull(uint32_t st, uint32_t h) const { return one(3 + 2 * st + h); }   // S computed
+  __device__ __forceinline__ uint32_t pready(uint32_t st, uint32_t h) const { return one(7 + 2 * st + h); }  // P written (h = 0: V fit for use)
+  __device__ __forceinline__ uint32_t pvdone(uint32_t st, uint32_t h) const { return one(11 + 2 * st + h); } // its P V (TWO = false)
+  __device__ __forceinline__ uint32_t ofull(uint32_t st) const { return one(15 + st); }                      // an item's last P V
 };
 
 __device__ __forceinline__ bool nonfinite2(uint32_t u) {
@@ -334,35 +337,37 @@ __device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t u) {
 
 // Threads t of NT: in the landed V block at `stage`, rows from `live` on become zero and
 // values that are not finite are dropped (and reported): a weight of zero times such a value
-// would otherwise reach rows that do not see the key.  The loads of a thread go out together.
+// would otherwise reach rows that do not see the key.  Sixteen bytes at a time, eight loads
+// together; an exponent of all ones carries into the sign's place when one is added to it.
 template <int HD, int NT>
-__device__ __forceinline__ void clean_v(uint8_t* stage, int live, int t, int* bad) {
+__device__ __noinline__ void clean_v(uint8_t* stage, int live, int t, int* bad) {
   using C = TreeCfg<HD>;
-  constexpr int kVecs = C::kTile / 16 / NT, kBatch = kVecs < 8 ? kVecs : 8;
+  constexpr int kVecs = C::kTile / 16 / NT, kBatch = 8;
+  static_assert(kVecs % kBatch == 0, "batches");
+  uint4* const at = reinterpret_cast<uint4*>(stage) + t;
 #pragma unroll 1
   for (int i0 = 0; i0 < kVecs; i0 += kBatch) {
     uint4 x[kBatch];
-    uint4* at[kBatch];
     uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      at[i] = reinterpret_cast<uint4*>(stage) + (i0 + i) * NT + t;
-      x[i] = *at[i];
-    }
+    for (int i = 0; i < kBatch; ++i) x[i] = at[(i0 + i) * NT];
+    auto carry = [](uint32_t u) { return (u & 0x7f807f80u) + 0x00800080u; };
 #pragma unroll
+    for (int i = 0; i < kBatch; ++i) any |= carry(x[i].x) | carry(x[i].y) | carry(x[i].z) | carry(x[i].w);
+    const bool past = C::row_of((i0 + kBatch - 1) * NT + NT - 1) >= live;  // (rows ascend along the tile)
+    if (!past && !(any & 0x80008000u)) continue;
+#pragma unroll 1
     for (int i = 0; i < kBatch; ++i) {
+      uint4 y = at[(i0 + i) * NT];
       if (C::row_of((i0 + i) * NT + t) >= live) {
-        *at[i] = make_uint4(0, 0, 0, 0);
-      } else if (nonfinite2(x[i].x) || nonfinite2(x[i].y) || nonfinite2(x[i].z) || nonfinite2(x[i].w)) {
-        any |= 1u << i;
+        y = make_uint4(0, 0, 0, 0);
+      } else if (nonfinite2(y.x) || nonfinite2(y.y) || nonfinite2(y.z) || nonfinite2(y.w)) {
+        y = make_uint4(drop_nonfinite2(y.x), drop_nonfinite2(y.y), drop_nonfinite2(y.z), drop_nonfinite2(y.w));
+        *reinterpret_cast<volatile int*>(bad) = 1;
+      } else {
+        continue;
       }
-    }
-    if (any) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (any >> i & 1u)
-          *at[i] = make_uint4(drop_nonfinite2(x[i].x), drop_nonfinite2(x[i].y), drop_nonfinite2(x[i].z), drop_nonfinite2(x[i].w));
-      *reinterpret_cast<volatile int*>(bad) = 1;
+      at[(i0 + i) * NT] = y;
     }
   }
 }
@@ -430,17 +435,18 @@ __device__ __forceinline__ void put16(const float (&o)[16], bool whole, float in
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-    *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {  // (a lane's row is a line of its own: one access, not two)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    } else {
+      *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) __stcg(part + (c / 4 + i) * kBlk, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
   }
-}
-
-// Halves of block `blk` of the run part that hold keys before the end.
-__device__ __forceinline__ int block_halves(const Item& it, int blk) {
-  return it.end - it.kstart - (it.ja + blk) * kBlk > kHalf ? 2 : 1;
 }
 
 template <int HD, bool TWO>
@@ -449,6 +455,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = TreeCfg<HD>;
   constexpr uint32_t kStages = C::kSlots - (TWO ? 2 : 1);
+  constexpr int kParts = TWO ? 2 : 1;  // halves of a block that a softmax step takes
   static_assert(kStages <= kMaxStages, "barriers");
   // (no static shared memory: the tiles start at its first byte, which is aligned to 1024)
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -477,7 +484,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(bars.kfull(s), 1);
       mbar_init(bars.vfull(s), 1);
       mbar_init(bars.empty(s), 1);
-      mbar_init(bars.clean(s), 32);
     }
     mbar_init(bars.qfull(), 1);
     mbar_init(bars.qempty(), 1);
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (uint32_t h = 0; h < 2; ++h) {
         mbar_init(bars.sfull(st, h), 1);
         mbar_init(bars.pvdone(st, h), 1);
-        mbar_init(bars.pready(st, h), 128);
+        mbar_init(bars.pready(st, h), h ? 128 : 128 + kCleaners);
       }
     }
     fence_proxy_async_smem();
@@ -517,7 +523,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t tS = tmem + kTmemS + 128 * st + lanes;
     const uint32_t tO = tmem + kTmemO + lanes;      // of stream 0; stream 1's is 128 columns on
-    uint32_t ns[2] = {0, 0}, nm = 0;                // phases: S of either half, meetings
+    uint32_t ns = 0, nm = 0;                        // blocks of the stream, meetings
     uint32_t no[2] = {0, 0};                        // items of the streams
     bool ok = true;
     auto meet = [&]() -> bool {                     // all 256 threads of the two streams
@@ -535,41 +541,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const Row r = make_row(p, it, node);
       const bool warp_live = __any_sync(0xffffffffu, node >= 0);
       float m = -INFINITY, l = 0.f;
-      uint32_t steps = 0;                           // of this stream and item
-      for (int blk = TWO ? 0 : (int)st; ok && blk < nb; blk += TWO ? 1 : 2) {
+      const int b0 = TWO ? 0 : (int)st;
+      for (int blk = b0; ok && blk < nb; blk += TWO ? 1 : 2) {
         const int k0 = it.kstart + (it.ja + blk) * kBlk;
         const bool masked = uniform(masked_block(p, it, k0));
-        const int halves = (int)uniform(block_halves(it, blk));
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h, ++steps) {
-          uint32_t vis[2] = {0, 0};
+        for (uint32_t h = 0; h < 2 / kParts; ++h) {
+          constexpr int kW = kBlk / 2 * kParts;  // keys of a step
+          uint32_t vis[kW / 32];
           if (masked) {
-            vis[0] = sees32(p, it, r, k0 + kHalf * h);
-            vis[1] = sees32(p, it, r, k0 + kHalf * h + 32);
+#pragma unroll
+            for (int w = 0; w < kW / 32; ++w) vis[w] = sees32(p, it, r, k0 + kW * (int)h + 32 * w);
           }
-          if (!(ok = op_wait(bars.sfull(st, h), (h ? ns[1]++ : ns[0]++) & 1, abort, p.a.status, 9))) break;
+          if (!(ok = op_wait(bars.sfull(st, h), ns & 1, abort, p.a.status, 9))) break;
           tc_fence_after();
           if (warp_live) {
-            const uint32_t tSh = tS + kHalf * h;
-            uint32_t s[kHalf];
-            tmem_ld32(tSh, s);
-            tmem_ld32(tSh + 32, s + 32);
-            tmem_wait32(s);
-            tmem_wait32(s + 32);
+            const uint32_t tSh = tS + kW * h;
+            uint32_t s[kW];
+#pragma unroll
+            for (int i = 0; i < kW / 32; ++i) tmem_ld32(tSh + 32 * i, s + 32 * i);
+#pragma unroll
+            for (int i = 0; i < kW / 32; ++i) tmem_wait32(s + 32 * i);
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < kHalf; ++i)
+              for (int i = 0; i < kW; ++i)
                 if (!(vis[i >> 5] >> (i & 31) & 1u)) s[i] = 0xff800000u;
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            for (int i = 0; i < kW; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             const float mnew = fmaxf(m, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * p.scale_log2);
             const bool grow = node >= 0 && mnew > m + kRescale;  // (also the first finite maximum)
             if (__any_sync(0xffffffffu, grow)) {
               const float f = mnew == m ? 1.f : ex2(m - mnew);
-              if (steps > 0) {  // once the product before this one, of the other half, has ended
-                if (!(ok = op_wait(bars.pvdone(st, h ^ 1), ((h ? ns[0] : ns[1]) - 1) & 1, abort, p.a.status, 8))) break;
+              if (blk != b0 || h) {
+                // once the last P V has ended (TWO: S came after it)
+                if (!TWO && !(ok = op_wait(bars.pvdone(st, h ^ 1), (ns - (h ^ 1)) & 1, abort, p.a.status, 8))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 16) {
@@ -586,9 +593,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             const float mm = m == -INFINITY ? 0.f : m;
             const uint64_t neg = pack2(-mm, -mm);
-            uint64_t sum[2] = {0, 0};  // (two pairs of zeros)
+            uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)
 #pragma unroll
-            for (int c = 0; c < kHalf / 32; ++c) {
+            for (int c = 0; c < kW / 32; ++c) {
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -596,18 +603,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 float2 x = unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2, neg));
                 x.x = ex2(x.x);
                 x.y = ex2(x.y);
-                sum[i & 1] = add2(sum[i & 1], pack2(x.x, x.y));
+                sum[i & 3] = add2(sum[i & 3], pack2(x.x, x.y));
                 pk[i] = pack_bf16(x.x, x.y);
               }
               tmem_st16(tSh + 16 * c, pk);
             }
-            const float2 total = unpack2(add2(sum[0], sum[1]));
+            const float2 total = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
             l += total.x + total.y;
             tmem_wait_st();
             tc_fence_before();
           }
           mbar_arrive(bars.pready(st, h));
         }
+        ++ns;
       }
       if (!ok) break;
       // ------------------------------------------------------------ the item's result
@@ -675,184 +683,238 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       tc_fence_before();
       if (!TWO && !(ok = meet())) break;
     }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- producer
-    // lane i < 8 looks up page i of a block; the table is read two blocks ahead and not looked at
-    // before it is needed, so that its latency is nobody's
-    Ring put, block;                // ring slots; blocks
-    uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
-    bool ok = true;
-    auto look_up = [&](const Item& it, int j) -> int {
-      const int at = (it.kstart + j * kBlk) / kOpPage + lane;
-      return lane < 8 && at * kOpPage < it.end ? __ldg(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
-    };
-    while (ok && uniform(run.next(p))) {
-      const Item& it = run.it;
-      const int blocks = (int)uniform(it.jb - it.ja);
-      const uint32_t rows = p.npt * p.gs;
-      int page1 = look_up(it, it.ja), page2 = look_up(it, it.ja + 1);
-      for (int blk = 0; ok && blk < blocks; ++blk) {
-        const int j = it.ja + blk;
-        const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
-        int page = page1;
-        page1 = page2;
-        page2 = look_up(it, j + 2);
-        if (page < 0 || page >= p.c.n_pages) {
-          op_error(p.a.status, MK_ERR_BAD_PAGE, it.b, (it.kstart + j * kBlk) / kOpPage + lane, page);
-          page = 0;
-        }
-        __syncwarp();
-        const int first = (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);  // its first row group
-        uint32_t group[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, first, i);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(kStages)) {
-          const uint32_t s = put.slot;
-          if (!(ok = op_wait(bars.empty(s), put.phase ^ 1, abort, p.a.status, 1))) break;
-          if (elect_one()) {
-            const uint32_t dst = ring + s * C::kTile, bar = kv ? bars.vfull(block.slot) : bars.kfull(block.slot);
-            mbar_expect_tx(bar, live * kOpPage * HD * 2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
+  } else {
+    if (warp == 8) {
+      // ---------------------------------------------------------------- producer
+      // lane i < 8 looks up page i of a block; the table is read two blocks ahead and not looked at
+      // before it is needed, so that its latency is nobody's
+      Ring put, block;                // ring slots; blocks
+      uint32_t fill = 0, qphase = 0;  // ring slots filled; Q loads done
+      bool ok = true;
+      auto look_up = [&](const Item& it, int j) -> int {
+        const int at = (it.kstart + j * kBlk) / kOpPage + lane;
+        return lane < 8 && at * kOpPage < it.end ? __ldg(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
+      };
+      while (ok && uniform(run.next(p))) {
+        const Item& it = run.it;
+        const int blocks = (int)uniform(it.jb - it.ja);
+        const uint32_t rows = p.npt * p.gs;
+        int page1 = look_up(it, it.ja), page2 = look_up(it, it.ja + 1);
+        for (int blk = 0; ok && blk < blocks; ++blk) {
+          const int j = it.ja + blk;
+          const uint32_t live = uniform(min(kBlk / kOpPage, (it.end - it.kstart - j * kBlk + kOpPage - 1) / kOpPage));
+          int page = page1;
+          page1 = page2;
+          page2 = look_up(it, j + 2);
+          if (page < 0 || page >= p.c.n_pages) {
+            op_error(p.a.status, MK_ERR_BAD_PAGE, it.b, (it.kstart + j * kBlk) / kOpPage + lane, page);
+            page = 0;
           }
           __syncwarp();
-          if (kv == 0 && blk == 0) {  // the item's queries, once the last item's products have read theirs
-            if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
-            ++qphase;
-            const uint32_t tiles = uniform(TWO && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1);
-            const int head = (int)uniform(it.kvh * p.gs), node = (int)uniform(it.tp * nodes_per_group(p)), seq = (int)uniform(it.b);
+          const int first = (page * p.c.n_kv_heads + it.kvh) * (kOpPage / 8);  // its first row group
+          uint32_t group[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) group[i] = __shfl_sync(0xffffffffu, first, i);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++fill, put.advance(kStages)) {
+            const uint32_t s = put.slot;
+            if (!(ok = op_wait(bars.empty(s), put.phase ^ 1, abort, p.a.status, 1))) break;
             if (elect_one()) {
-              mbar_expect_tx(bars.qfull(), tiles * rows * HD * 2);
-              for (uint32_t t = 0; t < tiles; ++t)
-                for (int h = 0; h < C::kHalves; ++h)
-                  op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), head,
-                            node + (int)t * p.npt, seq, bars.qfull());
+              const uint32_t dst = ring + s * C::kTile, bar = kv ? bars.vfull(block.slot) : bars.kfull(block.slot);
+              mbar_expect_tx(bar, live * kOpPage * HD * 2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < live) op_tma_4d(dst + i * (kOpPage * HD * 2), kv ? &tv : &tk, 0, 0, 0, (int)group[i], bar);
             }
             __syncwarp();
-          }
-        }
-        block.advance(kStages);
-      }
-    }
-    // an abandoned run leaves copies in flight: wait for them (bounded)
-    if (*abort) {
-      const uint32_t n = min(fill, kStages);
-      for (uint32_t f = fill - n; f < fill; ++f)
-        mbar_wait(f & 1 ? bars.vfull(f / 2 % kStages) : bars.kfull(f / 2 % kStages), (f / 2 / kStages) & 1, 10000000ll);
-      if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
-    }
-  } else if (warp == 9 || warp == 10) {
-    // ---------------------------------------------------------------- S = Q K^T (warp 9), O += P V (warp 10)
-    // Both walk the streams' halves in turn, in one thread.  queries: spans of 128 rows one behind the
-    // other (one copy each); keys: see TreeCfg.  The second half of a key block and the next tile are
-    // additions to the descriptors.
-    constexpr uint32_t idesc_s = umma_idesc_bf16(128, kHalf);
-    constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
-    constexpr uint32_t kHalfOff = kHalf / 8 * C::kGroup / 16, kTileOff = C::kTile / 16;
-    if (elect_one()) {
-      const bool pv = warp == 10;
-      const uint64_t dq = umma_sdesc_sw(q_s, 16, 8 * C::kSpan, C::kSpan), dk = umma_sdesc_sw(ring, 16, C::kGroup, C::kSpan);
-      const uint64_t dv = umma_sdesc_sw(ring, 8 * C::kSpan, C::kGroup, C::kSpan);
-      uint32_t used[2][2] = {{0, 0}, {0, 0}}, nq = 0;  // uses of the streams' halves, items
-      uint32_t item = 0;                               // ring slots of earlier items
-      bool ok = true;
-      while (ok && run.next(p)) {
-        const Item& it = run.it;
-        const int nb = it.jb - it.ja;
-        const int last_halves = block_halves(it, nb - 1);
-        if (!pv) {
-          if (!(ok = op_wait1(bars.qfull(), nq++ & 1, abort, p.a.status, 3))) break;
-          tc_fence_after();
-        }
-        int blk[2] = {0, TWO ? 0 : 1};                 // next half of the streams: its block,
-        int half[2] = {0, 0};
-        Ring slot[2], count[2];                        // the block's slot in the ring, and the block
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const uint32_t a = item + (TWO ? 0 : 2 * st);
-          slot[st].slot = a % kStages;
-          slot[st].phase = a / kStages & 1;
-          if (pv) slot[st].advance(kStages);
-          count[st].slot = a / 2 % kStages;
-          count[st].phase = a / 2 / kStages & 1;
-        }
-        auto step = [&](auto stream) -> bool {
-          constexpr uint32_t st = decltype(stream)::value;
-          const uint32_t s = slot[st].slot;
-          const uint32_t h = half[st];
-          const uint32_t n = h ? used[st][1]++ : used[st][0]++;
-          const bool done = h == 1 || (blk[st] + 1 == nb && last_halves == 1);  // the block's last half
-          const uint32_t sp = tmem + kTmemS + 128 * st + kHalf * h;
-          if (!pv) {
-            if (h == 0 && !op_wait1(bars.kfull(count[st].slot), count[st].phase, abort, p.a.status, 4)) return false;
-            if (n > 0 && !op_wait1(bars.pvdone(st, h), (n - 1) & 1, abort, p.a.status, 5)) return false;  // P of the last use
-            tc_fence_after();
-            const uint64_t a = dq + (TWO ? st : 0) * kTileOff, b = dk + s * kTileOff + h * kHalfOff;
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t off = ((kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan) / 16;
-              umma_bf16(sp, a + off, b + C::column16(kk) / 16, idesc_s, kk > 0);
+            if (kv == 0 && blk == 0) {  // the item's queries, once the last item's products have read theirs
+              if (!(ok = op_wait(bars.qempty(), (qphase & 1) ^ 1, abort, p.a.status, 2))) break;
+              ++qphase;
+              const uint32_t tiles = uniform(TWO && (it.tp * 2 + 1) * p.npt < it.cnt ? 2 : 1);
+              const int head = (int)uniform(it.kvh * p.gs), node = (int)uniform(it.tp * nodes_per_group(p)), seq = (int)uniform(it.b);
+              if (elect_one()) {
+                mbar_expect_tx(bars.qfull(), tiles * rows * HD * 2);
+                for (uint32_t t = 0; t < tiles; ++t)
+                  for (int h = 0; h < C::kHalves; ++h)
+                    op_tma_4d(q_s + t * C::kTile + h * (kBlk * C::kSpan), &tq, h * (C::kSpan / 2), head,
+                              node + (int)t * p.npt, seq, bars.qfull());
+              }
+              __syncwarp();
             }
-            umma_commit(bars.sfull(st, h));
-          } else {
-            if (h == 0 && !op_wait1(bars.clean(count[st].slot), count[st].phase, abort, p.a.status, 6)) return false;
-            if (!op_wait1(bars.pready(st, h), n & 1, abort, p.a.status, 13)) return false;
-            tc_fence_after();
-            const uint64_t b = dv + s * kTileOff + h * kHalfOff;
-            const bool first = h == 0 && blk[st] == (TWO ? 0 : (int)st);
-#pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-              umma_bf16_ta(tmem + kTmemO + 128 * st, sp + 8 * kk, b + kk * (2 * C::kGroup / 16), idesc_o, !first || kk > 0);
-            umma_commit(bars.pvdone(st, h));
-            if (done && blk[st] + (TWO ? 1 : 2) >= nb) umma_commit(bars.ofull(st));
           }
-          if (!done) {
-            half[st] = 1;
-            return true;
-          }
-          if (!TWO || st == 1) umma_commit(bars.empty(s));
-          half[st] = 0;
-          blk[st] += TWO ? 1 : 2;
-#pragma unroll
-          for (int i = 0; i < (TWO ? 2 : 4); ++i) slot[st].advance(kStages);
-#pragma unroll
-          for (int i = 0; i < (TWO ? 1 : 2); ++i) count[st].advance(kStages);
-          return true;
-        };
-        while (ok && (blk[0] < nb || blk[1] < nb)) {
-          if (blk[0] < nb) ok = step(std::integral_constant<uint32_t, 0>{});
-          if (ok && blk[1] < nb) ok = step(std::integral_constant<uint32_t, 1>{});
+          block.advance(kStages);
         }
-        if (ok && !pv) umma_commit(bars.qempty());
-        item += 2 * nb;
       }
-    }
-    __syncwarp();
-    if (*abort) {  // let the products in flight end before the memory goes
-      const uint64_t t0 = gtime();
-      while ((long long)(gtime() - t0) < 10000000ll) {}
-    }
-  } else {
-    // ---------------------------------------------------------------- cleaning
-    Ring at, block;       // V's ring slot, block
-    at.advance(kStages);
-    bool ok = true;
-    while (ok && uniform(run.next(p))) {
-      const Item& it = run.it;
-      const int nb = (int)uniform(it.jb - it.ja);
-      for (int blk = 0; blk < nb; ++blk) {
-        const int k0 = it.kstart + (it.ja + blk) * kBlk;
-        if (!(ok = op_wait(bars.vfull(block.slot), block.phase, abort, p.a.status, 12))) break;
-        if (uniform(masked_block(p, it, k0))) {
-          clean_v<HD, 32>(ring_g + at.slot * C::kTile, it.end - k0, lane, &sh.bad_v);
-          fence_proxy_async_smem();
+      // an abandoned run leaves copies in flight: wait for them (bounded)
+      if (*abort) {
+        const uint32_t n = min(fill, kStages);
+        for (uint32_t f = fill - n; f < fill; ++f)
+          mbar_wait(f & 1 ? bars.vfull(f / 2 % kStages) : bars.kfull(f / 2 % kStages), (f / 2 / kStages) & 1, 10000000ll);
+        if (qphase) mbar_wait(bars.qfull(), (qphase - 1) & 1, 10000000ll);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- products
+      // Products execute in the order of their issue: S may be issued into a buffer as soon as the
+      // P V that reads its old P is.  Queries: spans of 128 rows one behind the other (one copy
+      // each); keys: see TreeCfg.
+      constexpr int kW = kBlk / 2 * kParts;
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kW);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_bmn(128, HD);
+      constexpr uint32_t kTileOff = C::kTile / 16;
+      if (elect_one()) {
+        const uint64_t dq = umma_sdesc_sw(q_s, 16, 8 * C::kSpan, C::kSpan), dk = umma_sdesc_sw(ring, 16, C::kGroup, C::kSpan);
+        const uint64_t dv = umma_sdesc_sw(ring, 8 * C::kSpan, C::kGroup, C::kSpan);
+        uint32_t nq = 0;                  // items
+        bool ok = true;
+        // S of half h (or all) of the K block in `slot`, done with it if `last`
+        auto issue_s = [&](uint32_t st, uint32_t h, uint32_t slot, bool last) {
+          const uint64_t a = dq + (TWO ? st : 0) * kTileOff, b = dk + slot * kTileOff + h * (kW / 8 * C::kGroup / 16);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = ((kk * 32 / C::kSpan) * (kBlk * C::kSpan) + (kk * 32) % C::kSpan) / 16;
+            umma_bf16(tmem + kTmemS + 128 * st + kW * h, a + off, b + C::column16(kk) / 16, idesc_s, kk > 0);
+          }
+          umma_commit(bars.sfull(st, h));
+          if (last) umma_commit(bars.empty(slot));
+        };
+        auto issue_pv = [&](uint32_t st, uint32_t h, uint32_t slot, bool first, bool last) {
+          tc_fence_after();
+          const uint64_t b = dv + slot * kTileOff + h * (kW / 8 * C::kGroup / 16);
+          const uint32_t o = tmem + kTmemO + 128 * st, sp = tmem + kTmemS + 128 * st + kW * h;
+#pragma unroll
+          for (int kk = 0; kk < kW / 16; ++kk)
+            umma_bf16_ta(o, sp + 8 * kk, b + kk * (2 * C::kGroup / 16), idesc_o, !first || kk > 0);
+          if (!TWO) umma_commit(bars.pvdone(st, h));
+          if (last) umma_commit(bars.empty(slot));
+        };
+        Ring ks, vs, kb;                  // slots of the next K and V block, and K's count
+        vs.advance(kStages);
+        uint32_t np[2] = {0, 0};          // blocks of the streams whose P V is issued
+        Ring vst[2];                      // (TWO = false) the V slots of the streams' next blocks
+        while (ok && run.next(p)) {
+          const int nb = run.it.jb - run.it.ja;
+          if (!(ok = op_wait1(bars.qfull(), nq++ & 1, abort, p.a.status, 3))) break;
+          if (TWO) {
+            auto next_s = [&](uint32_t st) {
+              issue_s(st, 0, ks.slot, st == 1);
+              if (st == 1) {
+                ks.advance(kStages);
+                ks.advance(kStages);
+                kb.advance(kStages);
+              }
+            };
+            if (!(ok = op_wait1(bars.kfull(kb.slot), kb.phase, abort, p.a.status, 4))) break;
+            tc_fence_after();
+            next_s(0);
+            next_s(1);
+            for (int blk = 0; ok && blk < nb; ++blk) {
+              const uint32_t ph = np[0]++ & 1;
+#pragma unroll
+              for (uint32_t st = 0; st < 2; ++st) {
+                // P is written, V clean and the next K there: see the cleaners
+                if (!ok || !(ok = op_wait1(bars.pready(st, 0), ph, abort, p.a.status, 5))) break;
+                issue_pv(st, 0, vs.slot, blk == 0, st == 1);
+                if (blk + 1 < nb)
+                  next_s(st);
+                else
+                  umma_commit(bars.ofull(st));
+              }
+              vs.advance(kStages);
+              vs.advance(kStages);
+            }
+          } else {
+            // whatever is ready: S by block and half, P V of either stream by its blocks and halves
+            int qb = 0, pb[2] = {0, 1};
+            uint32_t qh = 0, ph[2] = {0, 0};
+            vst[0] = vst[1] = vs;
+            vst[1].advance(kStages);
+            vst[1].advance(kStages);
+            uint64_t since = gtime();
+            while (pb[0] < nb || pb[1] < nb) {
+              bool moved = false;
+              // (its buffer is free when the stream is past the block before, or past this half of it)
+              const uint32_t qs = qb & 1;
+              const int at = qs ? pb[1] : pb[0];
+              if (qb < nb && (at == qb || (at + 2 == qb && (qs ? ph[1] : ph[0]) > qh)) &&
+                  (qh == 1 || op_test(bars.kfull(kb.slot), kb.phase))) {
+                tc_fence_after();
+                issue_s(qs, qh, ks.slot, qh == 1);
+                if (qh == 1) {
+                  ks.advance(kStages);
+                  ks.advance(kStages);
+                  kb.advance(kStages);
+                  ++qb;
+                }
+                qh ^= 1;
+                moved = true;
+              }
+#pragma unroll
+              for (uint32_t st = 0; st < 2; ++st) {
+                if (pb[st] >= nb || !op_test(bars.pready(st, ph[st]), np[st] & 1)) continue;
+                issue_pv(st, ph[st], vst[st].slot, pb[st] == (int)st && ph[st] == 0, ph[st] == 1);
+                if (ph[st] == 1) {
+                  if (pb[st] + 2 >= nb) umma_commit(bars.ofull(st));
+                  pb[st] += 2;
+                  ++np[st];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) vst[st].advance(kStages);
+                }
+                ph[st] ^= 1;
+                moved = true;
+              }
+              if (moved) {
+                since = gtime();
+              } else if (*abort || (long long)(gtime() - since) > kOpWaitNs) {
+                if (!*abort) op_error(p.a.status, MK_ERR_TIMEOUT, (int)blockIdx.x, 6, qb);
+                *abort = 1;
+                ok = false;
+                break;
+              }
+            }
+            // the next item's first V: behind this one's last
+            for (int i = 0; i < (2 * nb) % (int)kStages; ++i) vs.advance(kStages);
+          }
+          if (ok) umma_commit(bars.qempty());
         }
-        mbar_arrive(bars.clean(block.slot));
-        block.advance(kStages);
-        at.advance(kStages);
-        at.advance(kStages);
+      }
+      __syncwarp();
+      if (*abort) {  // let the products in flight end before the memory goes
+        const uint64_t t0 = gtime();
+        while ((long long)(gtime() - t0) < 10000000ll) {}
+      }
+    } else {
+      // ---------------------------------------------------------------- cleaning
+      // Arrives with a block's P on `pready` once its V is fit for use, at most one phase ahead.
+      // (TWO: and once the next K is there, so that the product thread has one wait a step.)
+      Ring at, block;       // V's ring slot, block
+      at.advance(kStages);
+      uint32_t n[2] = {0, 0};
+      bool ok = true;
+      auto arrive = [&](uint32_t st, uint32_t k) -> bool {
+        if (k > 0 && !op_wait(bars.pready(st, 0), (k - 1) & 1, abort, p.a.status, 13)) return false;
+        mbar_arrive(bars.pready(st, 0));
+        return true;
+      };
+      while (ok && uniform(run.next(p))) {
+        const Item& it = run.it;
+        const int nb = (int)uniform(it.jb - it.ja);
+        for (int blk = 0; ok && blk < nb; ++blk) {
+          const int k0 = it.kstart + (it.ja + blk) * kBlk;
+          if (!(ok = op_wait(bars.vfull(block.slot), block.phase, abort, p.a.status, 12))) break;
+          if (uniform(masked_block(p, it, k0))) {
+            clean_v<HD, kCleaners>(ring_g + at.slot * C::kTile, it.end - k0, (int)threadIdx.x - (kTreeThreads - kCleaners), &sh.bad_v);
+            fence_proxy_async_smem();
+          }
+          block.advance(kStages);
+          at.advance(kStages);
+          at.advance(kStages);
+          if (TWO) {
+            if (blk + 1 < nb && !(ok = op_wait(bars.kfull(block.slot), block.phase, abort, p.a.status, 14))) break;
+            ok = arrive(0, n[0]++) && arrive(1, n[1]++);
+          } else {
+            ok = blk & 1 ? arrive(1, n[1]++) : arrive(0, n[0]++);
+          }
+        }
       }
     }
   }
