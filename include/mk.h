@@ -412,8 +412,8 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  *     arrays of the call).
  *   - A node is a new token of a sequence: node i of sequence b owns cache position
  *     seq_lens[b] + i, whatever its depth in the tree.  counts[b] (NULL = n_nodes for
- *     all) is the number of nodes of sequence b; rows of later nodes are neither read nor
- *     written.
+ *     all) is the number of nodes of sequence b; rows of later nodes are not written, and
+ *     what they hold does not matter.
  *   - status: int32[4], zeroed by the caller, or NULL (not recorded).  The first invalid
  *     value that a kernel finds in device data is recorded there as {mk_status code,
  *     sequence or expert, index, value}.  Invalid entries are skipped or clamped, never

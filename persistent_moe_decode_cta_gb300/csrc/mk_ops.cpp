@@ -127,6 +127,8 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
   if (!r) r = check_rows("v", args->v, args->v_stride, dk);
   if (!r) r = check_rows("q_out", args->q_out, args->out_stride, dq);
   if (r) return r;
+  if ((long long)cache->batch * args->n_nodes >= 0x7fffffffll - (1 << 20))
+    return op_fail(MK_ERR_UNSUPPORTED, "batch x n_nodes does not fit 31 bits");
   if ((args->q_gain && !aligned16(args->q_gain)) || (args->k_gain && !aligned16(args->k_gain)))
     return op_fail(MK_ERR_INVALID, "gains must be 16-byte aligned");
   if (!(args->theta >= 1.0) || !std::isfinite(args->theta)) return op_fail(MK_ERR_INVALID, "theta must be finite and >= 1");

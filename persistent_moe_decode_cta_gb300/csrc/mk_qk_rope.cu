@@ -4,8 +4,8 @@
 // (i, i + hd/2) by p * theta^(-2i/hd).  A slot of hd/16 lanes holds a head: lane j the
 // values 8j..8j+7 of each half (two 16-byte loads), so that a pair never leaves its
 // lane and the mean is a shuffle over hd/16 lanes.  V heads are copied by the same slots.
-// A token's cosines and sines are computed once, into shared memory, while its heads'
-// loads are in flight.  The angle's fraction of a turn is exact in 64-bit fixed point
+// A token's cosines and sines are computed once, into shared memory, while the loads of its
+// heads are in flight.  The angle's fraction of a turn is exact in 64-bit fixed point
 // (position * turns, modulo 1), so that positions of any size keep fp32 accuracy.
 // Everything is fp32; each result is rounded to bf16 once.
 #include "mk_ops.cuh"
@@ -13,148 +13,176 @@
 namespace mk {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxThreads = 512;
 
 struct Head8 {  // values 8j..8j+7 of the lower and of the upper half of a head
   uint4 lo, hi;
 };
 
-__device__ __forceinline__ void widen(uint4 u, float (&x)[8]) {
+// two pairs of floats
+__device__ __forceinline__ void widen(uint4 u, uint64_t (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = bf16x2_to_f2(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    x[i] = pack2(f.x, f.y);
   }
 }
-__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint32_t narrow2(uint64_t x) {
+  const float2 f = unpack2(x);
+  return pack_bf16(f.x, f.y);
+}
+__device__ __forceinline__ uint4 narrow(const uint64_t (&x)[4]) {
+  return make_uint4(narrow2(x[0]), narrow2(x[1]), narrow2(x[2]), narrow2(x[3]));
 }
 
-// HD / 16 lanes a head; `tpb` tokens a block.
-template <int HD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, int tpb) {
+// HD / 16 lanes a head, `slots` lanes of a token's heads in this block (blockIdx.y: which),
+// `side` tokens side by side and P behind one another, whose loads all go out before the
+// cosines are computed.
+template <int HD, int P>
+__global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const __grid_constant__ RopeParams p, int slots, int side) {
   constexpr int LPH = HD / 16;
-  __shared__ float2 cs[8 * (HD / 2)];  // [token of the block][HD / 2] (cos, sin)
+  // per token of the block, piece i of four angles and lane: cosines and sines of angles 8 lane + 2 i and
+  // 2 i + 1, so that the lanes of a head read side by side
+  extern __shared__ float4 cs[];
   const int n = p.a.n_nodes;
-  const long long tokens = (long long)p.c.batch * n;
-  const long long t0 = (long long)blockIdx.x * tpb;
-  const int heads = p.a.n_q_heads + 2 * p.c.n_kv_heads;
-  const int slots = heads * LPH;  // per token
-  const uint16_t* q = static_cast<const uint16_t*>(p.a.q);
-  const uint16_t* k = static_cast<const uint16_t*>(p.a.k);
-  const uint16_t* v = static_cast<const uint16_t*>(p.a.v);
+  const int tokens = p.c.batch * n;  // (below 2^31: checked by the host)
+  const int t0 = (int)blockIdx.x * side * P;
+  const int tl = (int)threadIdx.x / slots, r = (int)threadIdx.x - tl * slots + (int)blockIdx.y * slots;
+  const int head = r / LPH, lane = r % LPH;
+  const int hq = p.a.n_q_heads, hkv = p.c.n_kv_heads;
+  const bool mine = tl < side && head < hq + 2 * hkv;
+  const int kind = head < hq ? 0 : head < hq + hkv ? 1 : 2;
+  const int hk = kind == 0 ? head : head - hq - (kind == 2 ? hkv : 0);
+  const int64_t* stride = kind == 0 ? p.a.q_stride : kind == 1 ? p.a.k_stride : p.a.v_stride;
+  const uint16_t* src = static_cast<const uint16_t*>(kind == 0 ? p.a.q : kind == 1 ? p.a.k : p.a.v) + hk * stride[2] + 8 * lane;
 
-  // cosines and sines of the block's tokens
-  for (int i = threadIdx.x; i < tpb * (HD / 2); i += kRopeThreads) {
-    const long long t = t0 + i / (HD / 2);
+  Head8 h[P];
+  uint16_t* dst[P];
+  int b = (t0 + tl) / n, node = t0 + tl - b * n - side;
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const int t = t0 + k * side + tl;
+    for (node += side; node >= n; node -= n) ++b;
+    dst[k] = nullptr;
+    h[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (!mine || t >= tokens) continue;
+    const uint16_t* x = src + b * stride[0] + node * stride[1];
+    h[k].lo = __ldcs(reinterpret_cast<const uint4*>(x));
+    h[k].hi = __ldcs(reinterpret_cast<const uint4*>(x + HD / 2));
+    const int cnt = p.a.counts ? __ldg(p.a.counts + b) : n;
+    if (node >= cnt) continue;
+    if (kind == 0) {
+      dst[k] = static_cast<uint16_t*>(p.a.q_out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] + hk * p.a.out_stride[2] + 8 * lane;
+      continue;
+    }
+    const int len = __ldg(p.c.seq_lens + b);
+    const long long at = (long long)len + node;
+    if (len < 0 || cnt > n || (long long)len + cnt > 16ll * p.c.max_pages) {
+      op_error(p.a.status, MK_ERR_INVALID, b, node, len);
+      continue;
+    }
+    const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + at / kOpPage);
+    if (page < 0 || page >= p.c.n_pages)
+      op_error(p.a.status, MK_ERR_BAD_PAGE, b, (int)(at / kOpPage), page);
+    else
+      dst[k] = static_cast<uint16_t*>(kind == 1 ? p.c.k : p.c.v) +
+               (((long long)page * hkv + hk) * kOpPage + at % kOpPage) * HD + 8 * lane;
+  }
+  uint64_t gl[4], gh[4];
+  const void* gain = kind == 0 ? p.a.q_gain : p.a.k_gain;
+  const bool norm = kind != 2 && gain != nullptr;
+  if (norm) {
+    widen(__ldg(reinterpret_cast<const uint4*>(gain) + lane), gl);
+    widen(__ldg(reinterpret_cast<const uint4*>(gain) + LPH + lane), gh);
+  }
+
+  for (int i = threadIdx.x; i < side * P * (HD / 2); i += (int)blockDim.x) {
+    const int t = t0 + i / (HD / 2);
     if (t >= tokens) break;
-    const int b = (int)(t / n), node = (int)(t - (long long)b * n);
-    const int pos = p.a.positions ? __ldg(p.a.positions + t) : __ldg(p.c.seq_lens + b) + node;
+    const int pos = p.a.positions ? __ldg(p.a.positions + t) : __ldg(p.c.seq_lens + t / n) + t % n;
     const unsigned long long u = (unsigned long long)(long long)pos * p.turns[i % (HD / 2)];
     float s, c;
     sincospif((float)(int)(u >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns = signed fraction * 2^-31
-    cs[i] = make_float2(c, s);
+    const int f = i % (HD / 2);
+    float2* out = reinterpret_cast<float2*>(cs + (i / (HD / 2)) * (HD / 4) + (f / 2 % 4) * LPH + f / 8);  // (cos, cos), (sin, sin)
+    reinterpret_cast<float*>(out)[f % 2] = c;
+    reinterpret_cast<float*>(out)[2 + f % 2] = s;
   }
   __syncthreads();
 
-  // whole groups of LPH lanes take part in the shuffles: the loop bound is rounded up to warps
-  const int total = tpb * slots;
-  for (int base = 0; base < total; base += kRopeThreads) {
-    const int s = base + (int)threadIdx.x;
-    const int tl = s / slots, r = s - tl * slots;
-    const int head = r / LPH, lane = r % LPH;
-    const long long t = t0 + tl;
-    const int b = (int)(t / n), node = (int)(t - (long long)b * n);
-    bool live = s < total && t < tokens;
-    int len = 0, cnt = 0;
-    if (live) {
-      len = __ldg(p.c.seq_lens + b);
-      cnt = p.a.counts ? __ldg(p.a.counts + b) : n;
-      live = node < cnt;
-    }
-    const int kind = head < p.a.n_q_heads ? 0 : head < p.a.n_q_heads + p.c.n_kv_heads ? 1 : 2;
-    const int hk = head - p.a.n_q_heads - (kind == 2 ? p.c.n_kv_heads : 0);
-    Head8 h = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (live) {
-      const uint16_t* src =
-          kind == 0 ? q + b * p.a.q_stride[0] + node * p.a.q_stride[1] + head * p.a.q_stride[2]
-          : kind == 1 ? k + b * p.a.k_stride[0] + node * p.a.k_stride[1] + hk * p.a.k_stride[2]
-                      : v + b * p.a.v_stride[0] + node * p.a.v_stride[1] + hk * p.a.v_stride[2];
-      h.lo = *reinterpret_cast<const uint4*>(src + 8 * lane);
-      h.hi = *reinterpret_cast<const uint4*>(src + HD / 2 + 8 * lane);
-    }
-    uint16_t* dst = nullptr;
-    if (live && kind == 0) {
-      dst = static_cast<uint16_t*>(p.a.q_out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] + head * p.a.out_stride[2];
-    } else if (live) {
-      const long long at = (long long)len + node;
-      if (len < 0 || cnt > n || (long long)len + cnt > 16ll * p.c.max_pages) {
-        op_error(p.a.status, MK_ERR_INVALID, b, node, len);
-      } else {
-        const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + at / kOpPage);
-        if (page < 0 || page >= p.c.n_pages)
-          op_error(p.a.status, MK_ERR_BAD_PAGE, b, (int)(at / kOpPage), page);
-        else
-          dst = static_cast<uint16_t*>(kind == 1 ? p.c.k : p.c.v) +
-                (((long long)page * p.c.n_kv_heads + hk) * kOpPage + at % kOpPage) * HD;
-      }
-    }
-    const void* gain = kind == 0 ? p.a.q_gain : p.a.k_gain;
-    float lo[8], hi[8];
-    widen(h.lo, lo);
-    widen(h.hi, hi);
-    float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
+  for (int k = 0; k < P; ++k) {
+    uint64_t lo[4], hi[4];
+    widen(h[k].lo, lo);
+    widen(h[k].hi, hi);
+    uint64_t sq = mul2(lo[0], lo[0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i) sq = fma2(lo[i], lo[i], sq);
+      sq = fma2(hi[i], hi[i], sq);
+    }
+    const float2 sum = unpack2(sq);
+    float ss = sum.x + sum.y;
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!dst) continue;
+    if (!dst[k]) continue;
     if (kind != 2) {
-      if (gain) {
+      if (norm) {
         const float rs = rsqrtf(ss * (1.f / HD) + p.a.eps);
-        float g[8];
-        widen(__ldg(reinterpret_cast<const uint4*>(gain) + lane), g);
+        const uint64_t r2 = pack2(rs, rs);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] *= rs * g[i];
-        widen(__ldg(reinterpret_cast<const uint4*>(gain) + LPH + lane), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hi[i] *= rs * g[i];
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = mul2(lo[i], mul2(r2, gl[i]));
+          hi[i] = mul2(hi[i], mul2(r2, gh[i]));
+        }
       }
-      const float2* c = cs + tl * (HD / 2) + 8 * lane;
+      const float4* c = cs + (k * side + tl) * (HD / 4) + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = c[i];
-        const float a = lo[i], d = hi[i];
-        lo[i] = a * w.x - d * w.y;
-        hi[i] = d * w.x + a * w.y;
+      for (int i = 0; i < 4; ++i) {
+        const float4 w = c[i * LPH];
+        const uint64_t co = pack2(w.x, w.y), si = pack2(w.z, w.w), ms = pack2(-w.z, -w.w);
+        const uint64_t a = lo[i], d = hi[i];
+        lo[i] = fma2(a, co, mul2(d, ms));
+        hi[i] = fma2(d, co, mul2(a, si));
       }
-      h.lo = narrow(lo);
-      h.hi = narrow(hi);
+      h[k].lo = narrow(lo);
+      h[k].hi = narrow(hi);
     }
-    *reinterpret_cast<uint4*>(dst + 8 * lane) = h.lo;
-    *reinterpret_cast<uint4*>(dst + HD / 2 + 8 * lane) = h.hi;
+    *reinterpret_cast<uint4*>(dst[k]) = h[k].lo;
+    *reinterpret_cast<uint4*>(dst[k] + HD / 2) = h[k].hi;
   }
+}
+
+template <int HD>
+cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
+  const int all = (p.a.n_q_heads + 2 * p.c.n_kv_heads) * (HD / 16);
+  const int ny = (all + kRopeMaxThreads - 1) / kRopeMaxThreads;
+  // lanes of a token in one block: whole heads
+  const int slots = ((all + ny - 1) / ny + HD / 16 - 1) / (HD / 16) * (HD / 16);
+  const int side = slots < 256 ? 256 / slots : 1;  // small models: several tokens fill a block
+  const int threads = (slots * side + 31) / 32 * 32;
+  const long long tokens = (long long)p.c.batch * p.a.n_nodes;
+  // Two tokens behind one another keep more loads in flight at the same occupancy (8002 tokens
+  // of 32 + 2 * 4 heads of 128, 164 MB: 35.8 us; 37.0 with two and half the blocks), one where there
+  // are too few to fill the SMs.
+  const bool two = tokens >= 2ll * side * 152 * 8;
+  const int per = side * (two ? 2 : 1);
+  const dim3 grid((unsigned)((tokens + per - 1) / per), (unsigned)ny);
+  const size_t smem = (size_t)per * (HD / 4) * sizeof(float4);
+  if (two)
+    rope_kernel<HD, 2><<<grid, threads, smem, st>>>(p, slots, side);
+  else
+    rope_kernel<HD, 1><<<grid, threads, smem, st>>>(p, slots, side);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t st) {
-  const int hd = p.c.head_dim;
-  const int slots = (p.a.n_q_heads + 2 * p.c.n_kv_heads) * (hd / 16);
-  // small models: several tokens fill a block (at most 8: the shared cosines)
-  int tpb = kRopeThreads / slots;
-  tpb = tpb < 1 ? 1 : tpb > 8 ? 8 : tpb;
-  const long long tokens = (long long)p.c.batch * p.a.n_nodes;
-  const unsigned grid = (unsigned)((tokens + tpb - 1) / tpb);
-  if (hd == 128)
-    rope_kernel<128><<<grid, kRopeThreads, 0, st>>>(p, tpb);
-  else if (hd == 64)
-    rope_kernel<64><<<grid, kRopeThreads, 0, st>>>(p, tpb);
-  else
-    rope_kernel<32><<<grid, kRopeThreads, 0, st>>>(p, tpb);
-  return cudaGetLastError();
+  if (p.c.head_dim == 128) return launch_hd<128>(p, st);
+  if (p.c.head_dim == 64) return launch_hd<64>(p, st);
+  return launch_hd<32>(p, st);
 }
 
 }  // namespace mk
