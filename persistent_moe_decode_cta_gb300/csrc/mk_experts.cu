@@ -1,53 +1,146 @@
 // Matrix products grouped by expert:  out[r] = x[rows[r]] W_e^T  for the rows r of expert e,
 // or silu(x W_e^T) * (x U_e^T) with two weight sets.
 //
-// The weights are the M side of the tcgen05 products and the rows the N side: a tile is two
-// blocks of 128 weight rows (the gate and the up rows of the same 128 outputs, or 256
-// outputs of a single product) times up to 128 rows of one expert.  So a ragged group costs
-// what its rows cost (N in steps of 16), an expert with few rows is one pass over its
-// weights, and gate and up of an output meet in the same thread of the epilogue.  Two
-// accumulators of 128 columns, double buffered, fill tensor memory: a tile's epilogue
-// runs beside the next tile's products.
+// The weights are the M side of the tcgen05 products and the rows the N side, so that a
+// ragged group costs what its rows cost (N in steps of 32) and an expert with few rows is one
+// pass over its weights.  Two CTAs of a cluster share a product of M = 256 (cta_group::2): each
+// holds 128 rows of weights and half of the rows, and the pair reads both halves.  A tile is
+//   256 outputs, or with two weight sets 128 outputs (each CTA: 64 gate and 64 up rows), times
+//   up to 256 rows of one expert;
+// per 64 columns a CTA copies 16 KB of weights and at most 16 KB of rows for 512 cycles of
+// products, which shared memory and L2 can take.  (One CTA with 128 x 128 products moves 112 KB
+// through 128 bytes a cycle for the same work.  4096 tokens x top-8 of 128 experts, 2048 -> 768
+// with SwiGLU and named rows: 223 us with one, 189 us with two; 16384 tokens: 694 and 560 us.)
+// Two accumulators of 256 columns fill tensor memory: a tile's epilogue runs beside the next
+// tile's products.
 //
-// One persistent CTA per SM walks the tiles in order of (expert, row tile, weight block), so
-// that CTAs that run together share rows and, across row tiles, weights in L2.  Warp roles:
-// producer (weights through a 3-D map whose rows stop at the expert's last; rows through a
-// plain map), MMA issue, four epilogue warps that transpose through shared memory to store
-// whole output rows and, when `rows` is given, four warps that fetch the named rows with
-// 16-byte asynchronous copies straight into the swizzled layout.  (Tensor-map gather copies
-// of four rows at a time were tried for that: 566 us against 224 us for rows that lie in
-// order, 4096 tokens x top-8 of 128 experts, 2048 -> 768 with SwiGLU.)
+// One persistent cluster per two SMs walks the tiles in order of (expert, row tile, weight
+// block), so that clusters that run together share rows and, across row tiles, weights in
+// L2.  Warp roles of a CTA: producer (weights through a 3-D map whose rows stop at the expert's
+// last; rows through a plain map), product issue (the first CTA's), four epilogue warps that
+// exchange gate and up and transpose through shared memory to store whole output rows and, when
+// `rows` is given, four warps that fetch the named rows with 16-byte asynchronous copies
+// straight into the swizzled layout.  (Tensor-map gather copies of four rows at a time were tried
+// for that: 566 us against 224 us for rows that lie in order.  So was a prefetch of the weights
+// into L2 10 stages ahead of the ring: 154 us against 131 for 8 rows an expert.)
 // Accumulation is fp32; the result is rounded once.
 #include "mk_ops.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kExpThreads = 192;   // producer, MMA, four epilogue warps
+constexpr int kExpThreads = 192;     // producer, product issue, four epilogue warps
 constexpr int kGatherThreads = 128;  // ... and four gather warps when rows are named
-constexpr int kGatherLag = 2;      // stages whose copies a gather thread has in flight beside the newest
-constexpr int kTileW = 128;        // weight rows of a block
-constexpr int kTileR = 128;        // rows of a tile
-constexpr int kTileK = 64;         // columns of a stage: one 128-byte swizzle span
-constexpr int kBoxR = 32;          // rows per copy of x (one copy of 128 if more than two would be needed)
-constexpr int kExpStages = 4;
-constexpr int kBytesW = kTileW * kTileK * 2, kBytesR = kTileR * kTileK * 2;
-constexpr int kExpStage = 2 * kBytesW + kBytesR;
-constexpr int kExpOut = kTileR * kTileW * 2;  // a block's results, row by row
-constexpr int kExpSmem = 1024 + kExpStages * kExpStage + kExpOut;
+constexpr int kTileW = 128;          // weight rows of a CTA
+constexpr int kTileR = 256;          // rows of a tile, half of them in either CTA
+constexpr int kTileK = 64;           // columns of a stage: one 128-byte swizzle span
+constexpr int kBoxR = 32;            // rows per copy of x (one copy of 128 if more than two would be needed)
+constexpr int kBytesW = kTileW * kTileK * 2;
+// The ring: a stage has 16 KB of weights and room for 32, 64 or 128 rows, as many as the largest
+// expert of the call needs: 9, 8 or 6 stages.  (With 6 throughout, 8 rows an expert: 136 us.)
+constexpr int kRingBytes = 6 * (kBytesW + kTileR / 2 * kTileK * 2);
+constexpr int kMaxExpStages = 9;
+constexpr int kChunk = 32;           // rows of an epilogue step
+// per epilogue warp a chunk's results; per pair of warps two buffers of gate / up values in fp32
+constexpr int kExpSmem = 1024 + kRingBytes + 4 * kChunk * 32 * 2 + 2 * 2 * kChunk * 32 * 4;
+static_assert(kExpSmem + 2304 <= 232448, "exceeds the 227 KB per-block shared memory limit");
 
 struct ExpTile {
-  int e, r0, nr;   // expert, first row, rows (<= 128)
-  int w0;          // first weight row
+  int e, r0, nr;   // expert, first row, rows (<= 256)
+  int w0;          // first output
 };
 
 struct ExpShared {
   uint32_t tmem;
   int abort;
+  int most;                     // rows of the largest expert
   int pre[kOpMaxExperts + 1];   // prefix sums of the experts' row tiles
   int warp_sums[(kExpThreads + kGatherThreads) / 32];
-  unsigned long long bars[2 * kExpStages + 5];
+  unsigned long long bars[3 * kMaxExpStages + 4];
 };
+
+// ---- cluster primitives
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of the first CTA's copy of a shared variable
+__device__ __forceinline__ uint32_t map_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same without the order of this CTA's other accesses against the cluster, which costs about
+// 2000 cycles (a whole stage's products take 512): for an arrival that publishes nothing but rows
+// in this CTA's own shared memory, seen complete by the caller and passed to the async proxy,
+// where this CTA's tensor core reads them.
+__device__ __forceinline__ void arrive_cluster_own(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait of one thread for what both CTAs do.
+__device__ __forceinline__ bool wait_cluster1(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = gtime();
+  while (!try_wait_cluster(bar, parity)) {
+    if (*abort) return false;
+    if ((long long)(gtime() - t0) > kOpWaitNs) {
+      *abort = 1;
+      op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
+      return false;
+    }
+  }
+  return true;
+}
+// copies into this CTA that complete on a barrier of either
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+               "r"(accumulate ? 1u : 0u)
+               : "memory");
+}
+// arrive on the barrier at this address in both CTAs once the products issued so far have ended
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((uint16_t)3)
+               : "memory");
+}
 
 __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, bool record, int& lo, int& hi) {
   const int a = __ldg(p.a.offsets + e), b = __ldg(p.a.offsets + e + 1);
@@ -58,7 +151,8 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, bool r
 
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
-  if (threadIdx.x == 0) sh.pre[0] = 0;
+  if (threadIdx.x == 0) sh.pre[0] = sh.most = 0;
+  __syncthreads();
   int carry = 0;
   for (int base = 0; base < E; base += nt) {
     const int e = base + (int)threadIdx.x;
@@ -67,6 +161,7 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
       int lo, hi;
       expert_rows(p, e, blockIdx.x == 0, lo, hi);
       x = (hi - lo + kTileR - 1) / kTileR;
+      if (hi > lo) atomicMax(&sh.most, hi - lo);
     }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -84,255 +179,291 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
   }
 }
 
-__device__ __forceinline__ ExpTile find_tile(const ExpertParams& p, const int* pre, int t, int wblocks, int wstep) {
-  ExpTile x;
+// The tile that this cluster takes in turn k (false: none)
+__device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& sh, int k, int tiles, int wblocks, int wstep, ExpTile& x) {
+  const int t = k * ((int)gridDim.x / 2) + (int)blockIdx.x / 2;
+  if (t >= tiles) return false;
   const int rt = t / wblocks;
   int lo = 0, hi = p.a.n_experts - 1;
   while (lo < hi) {
     const int m = (lo + hi + 1) >> 1;
-    if (pre[m] <= rt) lo = m; else hi = m - 1;
+    if (sh.pre[m] <= rt) lo = m; else hi = m - 1;
   }
   x.e = lo;
   x.w0 = (t - rt * wblocks) * wstep;
   int a, b;
   expert_rows(p, lo, false, a, b);
-  x.r0 = a + (rt - pre[lo]) * kTileR;
-  x.nr = min(kTileR, b - x.r0);
-  return x;
+  // the expert's rows in equal tiles
+  const int mine = sh.pre[lo + 1] - sh.pre[lo], per = (b - a + mine - 1) / mine;
+  x.r0 = a + (rt - sh.pre[lo]) * per;
+  x.nr = min(per, b - x.r0);
+  return true;
 }
 
-__device__ __forceinline__ float silu(float y) { return y / (1.f + __expf(-y)); }
+__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
 template <bool GLU>
-__global__ void __launch_bounds__(kExpThreads + kGatherThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGatherThreads, 1)
     expert_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ CUtensorMap tx,
                   const __grid_constant__ CUtensorMap tx128, const __grid_constant__ CUtensorMap tw,
                   const __grid_constant__ CUtensorMap tu) {
   extern __shared__ uint8_t raw[];
   __shared__ ExpShared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  uint8_t* const out_g = raw + (base - smem_u32(raw)) + kExpStages * kExpStage;
+  uint8_t* const epi_g = raw + (base - smem_u32(raw)) + kRingBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
   volatile int* abort = &sh.abort;
   const uint32_t bars = smem_u32(sh.bars);
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (kExpStages + s); };
-  auto afull = [&](int a) { return bars + 8 * (2 * kExpStages + a); };      // accumulators written
-  auto aempty = [&](int a) { return bars + 8 * (2 * kExpStages + 2 + a); };  // ... and read
-  const uint32_t emeet = bars + 8 * (2 * kExpStages + 4);                    // the epilogue warps meet
+  auto full = [&](uint32_t s) { return bars + 8 * s; };                            // (used in the first CTA only)
+  auto empty = [&](uint32_t s) { return bars + 8 * (kMaxExpStages + s); };
+  auto afull = [&](uint32_t a) { return bars + 8 * (2 * kMaxExpStages + a); };        // accumulators written
+  auto aempty = [&](uint32_t a) { return bars + 8 * (2 * kMaxExpStages + 2 + a); };   // ... and read by both (first CTA only)
+  auto gathered = [&](uint32_t s) { return bars + 8 * (2 * kMaxExpStages + 4 + s); }; // this CTA's named rows
 
   if (threadIdx.x == 0) {
     sh.abort = 0;
-    for (int s = 0; s < kExpStages; ++s) {
-      mbar_init(full(s), p.a.rows ? 1 + kGatherThreads : 1);
+    for (int s = 0; s < kMaxExpStages; ++s) {
+      mbar_init(full(s), p.a.rows ? 2 : 1);  // the copies; the second CTA's named rows
       mbar_init(empty(s), 1);
+      mbar_init(gathered(s), kGatherThreads);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(afull(a), 1);
-      mbar_init(aempty(a), 128);
+      mbar_init(aempty(a), 2 * 4);
     }
-    mbar_init(emeet, 128);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
+  if (warp == 0 && lane < 4) {
+    const CUtensorMap* tm = lane == 0 ? &tx : lane == 1 ? &tx128 : lane == 2 ? &tw : &tu;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&sh.tmem), 512);
   scan_experts(p, sh);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the barriers of both CTAs are there
+  tc_fence_after();
+  const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
   const int tiles = (int)uniform(sh.pre[p.a.n_experts]) * wblocks;  // (below 2^31: checked by the host)
-  if ((int)blockIdx.x >= tiles) return;  // (the whole CTA)
-  if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   const int ksteps = (p.a.k + kTileK - 1) / kTileK;
+  const uint32_t most = uniform(min(sh.most, kTileR)), room = most <= 64 ? 32 : most <= 128 ? 64 : 128;  // rows of a stage
+  const uint32_t stage_bytes = kBytesW + room * kTileK * 2, stages = room == 32 ? 9 : room == 64 ? 8 : 6;
+  auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, x)); };
+  auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, x); };  // (one thread)
+  ExpTile x;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     uint32_t fill = 0;
+    Ring at;
     bool ok = true;
-    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
-      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
-      const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
-      const int e = (int)uniform(x.e), w0 = (int)uniform(x.w0), r0 = (int)uniform(x.r0), nr = (int)uniform(x.nr);
-      const uint32_t xrows = p.a.rows ? 0 : nr <= kBoxR ? kBoxR : nr <= 2 * kBoxR ? 2 * kBoxR : kTileR;
-      const uint32_t bytes = (second ? 2 : 1) * kBytesW + xrows * (kTileK * 2);
-      for (int ks = 0; ks < ksteps; ++ks, ++fill) {
-        const int s = fill % kExpStages;
-        if (!(ok = op_wait(empty(s), ((fill / kExpStages) & 1) ^ 1, abort, p.a.status, 1))) break;
+    const int half = GLU ? kTileW / 2 : kTileW;  // weight rows per copy
+    for (int t = 0; ok && tile(t, x); ++t) {
+      const int e = (int)uniform(x.e), nr = (int)uniform(x.nr);
+      const int w = (int)uniform(x.w0) + (int)rank * half, n2 = (nr + 31) / 32 * 16;  // rows of this CTA
+      const int r = (int)uniform(x.r0) + (int)rank * n2;
+      const uint32_t xrows = p.a.rows ? 0 : n2 <= kBoxR ? kBoxR : n2 <= 2 * kBoxR ? 2 * kBoxR : kTileR / 2;
+      const uint32_t bytes = 2 * (kBytesW + xrows * (kTileK * 2));  // of both CTAs
+      for (int ks = 0; ks < ksteps; ++ks, ++fill, at.advance(stages)) {
+        const uint32_t s = at.slot;
+        if (!(ok = op_wait(empty(s), at.phase ^ 1, abort, p.a.status, 1))) break;
         if (elect_one()) {
-          const uint32_t st = base + s * kExpStage;
-          mbar_expect_tx(full(s), bytes);
-          op_tma_3d(st, &tw, ks * kTileK, w0, e, full(s));
-          if (second) op_tma_3d(st + kBytesW, GLU ? &tu : &tw, ks * kTileK, GLU ? w0 : w0 + kTileW, e, full(s));
-          if (xrows == kTileR) {
-            op_tma_2d(st + 2 * kBytesW, &tx128, ks * kTileK, r0, full(s));
+          const uint32_t st = base + s * stage_bytes, bar = map_leader(full(s));
+          if (rank == 0) mbar_expect_tx(full(s), bytes);
+          tma_pair_3d(st, &tw, ks * kTileK, w, e, bar);
+          if (GLU) tma_pair_3d(st + kBytesW / 2, &tu, ks * kTileK, w, e, bar);
+          if (xrows == kTileR / 2) {
+            tma_pair_2d(st + kBytesW, &tx128, ks * kTileK, r, bar);
           } else if (xrows) {
-            op_tma_2d(st + 2 * kBytesW, &tx, ks * kTileK, r0, full(s));
-            if (xrows > kBoxR) op_tma_2d(st + 2 * kBytesW + kBoxR * kTileK * 2, &tx, ks * kTileK, r0 + kBoxR, full(s));
+            tma_pair_2d(st + kBytesW, &tx, ks * kTileK, r, bar);
+            if (xrows > kBoxR) tma_pair_2d(st + kBytesW + kBoxR * kTileK * 2, &tx, ks * kTileK, r + kBoxR, bar);
           }
         }
         __syncwarp();
       }
     }
-    if (*abort) {  // an abandoned run leaves copies in flight: wait for them (bounded)
-      const uint32_t n = min(fill, (uint32_t)kExpStages);
-      for (uint32_t f = fill - n; f < fill; ++f) mbar_wait(full(f % kExpStages), (f / kExpStages) & 1, 10000000ll);
+    // an abandoned run leaves copies in flight: give them time to land
+    if (*abort) {
+      const uint64_t s0 = gtime();
+      while ((long long)(gtime() - s0) < 10000000ll) {}
     }
   } else if (warp >= kExpThreads / 32) {
     // ---------------------------------------------------------------- gather
-    // eight threads a row (128 bytes of a stage), 16 rows at a time; a stage is handed over
-    // two stages later, when its copies have landed
+    // eight threads a row (128 bytes of a stage), 16 rows at a time; the copies report themselves
     const int t128 = (int)threadIdx.x - kExpThreads, chunk = t128 & 7, row0 = t128 >> 3;
     const uint32_t swz = (uint32_t)(chunk ^ (row0 & 7)) * 16;  // (16 j keeps the low three bits of the row)
-    uint32_t fill = 0;
+    constexpr int kRows = kTileR / 2 / 16;
+    Ring at;
     bool ok = true;
-    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
-      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
-      const uint16_t* src[kTileR / 16];
+    for (int t = 0; ok && tile(t, x); ++t) {
+      const int n2 = (x.nr + 31) / 32 * 16, first = (int)rank * n2, mine = min(n2, x.nr - first);  // (may be < 0)
+      const uint16_t* src[kRows];
 #pragma unroll
-      for (int j = 0; j < kTileR / 16; ++j) {
+      for (int j = 0; j < kRows; ++j) {
         const int i = row0 + 16 * j;
         int r = 0;
-        if (i < x.nr) {
-          const int s = __ldg(p.a.rows + x.r0 + i);
+        if (i < mine) {
+          const int s = __ldg(p.a.rows + x.r0 + first + i);
           r = min(max(s, 0), p.a.n_x - 1);
-          if (r != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, x.r0 + i, s);
+          if (r != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, x.r0 + first + i, s);
         }
         src[j] = static_cast<const uint16_t*>(p.a.x) + r * p.a.x_stride + 8 * chunk;
       }
-      for (int ks = 0; ks < ksteps; ++ks, ++fill) {
-        const int s = fill % kExpStages;
-        if (!(ok = op_wait(empty(s), ((fill / kExpStages) & 1) ^ 1, abort, p.a.status, 6))) break;
-        const uint32_t dst = base + s * kExpStage + 2 * kBytesW + row0 * (kTileK * 2) + swz;
+      for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
+        if (!(ok = op_wait(empty(at.slot), at.phase ^ 1, abort, p.a.status, 6))) break;
+        const uint32_t dst = base + at.slot * stage_bytes + kBytesW + row0 * (kTileK * 2) + swz;
         const int bytes = ks * kTileK + 8 * chunk < p.a.k ? 16 : 0;  // (0: zeros)
 #pragma unroll
-        for (int j = 0; j < kTileR / 16; ++j)
-          if (row0 + 16 * j < x.nr) op_cp16(dst + j * 16 * kTileK * 2, bytes ? src[j] + ks * kTileK : src[j], bytes);
-        op_cp_commit();
-        if (fill >= kGatherLag) {
-          op_cp_wait<kGatherLag>();
-          fence_proxy_async_smem();
-          mbar_arrive(full((fill - kGatherLag) % kExpStages));
-        }
+        for (int j = 0; j < kRows; ++j)
+          if (row0 + 16 * j < mine) op_cp16(dst + j * 16 * kTileK * 2, bytes ? src[j] + ks * kTileK : src[j], bytes);
+        op_cp_arrive(gathered(at.slot));
       }
     }
-    op_cp_wait<0>();
-    fence_proxy_async_smem();
-    if (ok)
-      for (uint32_t f = fill > kGatherLag ? fill - kGatherLag : 0; f < fill; ++f) mbar_arrive(full(f % kExpStages));
+    op_cp_wait_all();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issue
-    uint32_t used = 0, nt = 0;
-    const uint32_t tm = uniform(tmem);
-    const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, second weights, rows
-    bool ok = true;
-    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x, ++nt) {
-      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
-      const bool second = GLU || uniform(x.w0 + kTileW < p.a.n);
-      const uint32_t idesc = umma_idesc_bf16(kTileW, (uniform(x.nr) + 15) / 16 * 16);
-      const uint32_t a = nt & 1, acc = tm + 256 * a;
-      if (!(ok = op_wait(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
-      tc_fence_after();
-      for (int ks = 0; ks < ksteps; ++ks, ++used) {
-        const int s = used % kExpStages;
-        if (!(ok = op_wait(full(s), (used / kExpStages) & 1, abort, p.a.status, 3))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t d = d0 + s * (kExpStage / 16);
-#pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk) {
-            umma_bf16(acc, d + 2 * kk, d + 2 * kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
-            if (second) umma_bf16(acc + 128, d + kBytesW / 16 + 2 * kk, d + 2 * kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
+    // ---------------------------------------------------------------- product issue (first CTA)
+    if (rank != 0) {
+      // This thread reports the second CTA's gathered stages, made visible to the products.
+      if (p.a.rows && elect_one()) {
+        Ring at;
+        bool ok = true;
+        for (int t = 0; ok && tile1(t, x); ++t)
+          for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
+            if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 7))) break;
+            fence_proxy_async_smem();
+            arrive_cluster_own(map_leader(full(at.slot)));
           }
-          umma_commit(empty(s));
-          if (ks == ksteps - 1) umma_commit(afull(a));
+      }
+    } else if (elect_one()) {
+      uint32_t nt = 0;
+      Ring at;
+      const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, rows
+      bool ok = true;
+      for (int t = 0; ok && tile1(t, x); ++t, ++nt) {
+        const uint32_t idesc = umma_idesc_bf16(2 * kTileW, (x.nr + 31) / 32 * 32);
+        const uint32_t a = nt & 1, acc = tmem + kTileR * a;
+        if (!(ok = wait_cluster1(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
+        for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
+          if (!(ok = wait_cluster1(full(at.slot), at.phase, abort, p.a.status, 3))) break;
+          if (p.a.rows) {
+            if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 8))) break;
+            fence_proxy_async_smem();
+          }
+          tc_fence_after();
+          const uint64_t d = d0 + at.slot * (stage_bytes / 16);
+#pragma unroll
+          for (int kk = 0; kk < kTileK / 16; ++kk)
+            umma_bf16_pair(acc, d + 2 * kk, d + kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
+          umma_commit_pair(empty(at.slot));
         }
-        __syncwarp();
+        if (ok) umma_commit_pair(afull(a));
       }
     }
+    __syncwarp();
     if (*abort) {  // let the products in flight end before the memory goes
-      const uint64_t t0 = gtime();
-      while ((long long)(gtime() - t0) < 10000000ll) {}
+      const uint64_t s0 = gtime();
+      while ((long long)(gtime() - s0) < 10000000ll) {}
     }
   } else {
     // ---------------------------------------------------------------- epilogue
+    // A warp has 32 weight rows (lanes) and takes 32 rows of x at a time; it turns its piece of the
+    // result in shared memory of its own and stores 64 bytes of every row.  With two weight sets
+    // warps 0 and 1 have gate rows and warps 2 and 3 the up rows of the same outputs: each side of
+    // a pair gets the other's values for half of the rows.  (A wait that gives up is not followed
+    // by an exit: the pair keeps meeting, and every later wait returns at once.)
     const int q = warp & 3;               // lanes 32 q .. of tensor memory
-    const int col = 32 * q + lane;        // weight row of the block
-    uint32_t nt = 0, nm = 0;
-    auto meet = [&]() -> bool {           // all four warps, bounded like every wait
-      mbar_arrive(emeet);
-      return op_wait(emeet, nm++ & 1, abort, p.a.status, 5);
-    };
-    uint16_t* const stage = reinterpret_cast<uint16_t*>(out_g);
+    uint32_t nt = 0, nc = 0;
+    constexpr int kTake = GLU ? kChunk / 2 : kChunk;  // rows that this warp stores of a chunk
+    const bool up = GLU && q >= 2;
+    const int o = GLU ? 32 * (q & 1) : 32 * q;        // first output of this warp in the CTA's
     // whole 16-byte pieces of an output row where its address allows them
     const bool wide = p.a.n % 8 == 0 && p.a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.a.out) & 15) == 0;
-    bool ok = true;
-    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x, ++nt) {
-      const ExpTile x = find_tile(p, sh.pre, t, wblocks, kStep);
+    uint16_t* const stage = reinterpret_cast<uint16_t*>(epi_g) + q * kChunk * 32;
+    float* const exch_g = reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + (q & 1) * kChunk * 32;
+    for (int t = 0; tile(t, x); ++t, ++nt) {
       const uint32_t a = nt & 1;
-      const uint32_t acc = tmem + 256 * a + ((uint32_t)q << 21);
-      if (!(ok = op_wait(afull(a), (nt >> 1) & 1, abort, p.a.status, 4))) break;
+      const uint32_t acc = tmem + kTileR * a + ((uint32_t)q << 21);
+      const int w0 = x.w0 + (int)rank * (GLU ? kTileW / 2 : kTileW) + o, width = min(32, p.a.n - w0);  // (<= 0: nothing to store)
+      op_wait(afull(a), (nt >> 1) & 1, abort, p.a.status, 4);
       tc_fence_after();
+      uint32_t u[kChunk];
+      tmem_ld32(acc, u);
 #pragma unroll 1
-      for (int blk = 0; ok && blk < (GLU ? 1 : 2); ++blk) {
-        const int w0 = x.w0 + blk * kTileW;
-        if (w0 >= p.a.n) break;
-        for (int c = 0; c < x.nr; c += 16) {
-          uint32_t u[16];
-          tmem_ld16(acc + 128 * blk + c, u);
-          tmem_wait16(u);
-          if (GLU) {
-            uint32_t v[16];
-            tmem_ld16(acc + 128 + c, v);
-            tmem_wait16(v);
+      for (int c = 0; c < x.nr; c += kChunk, ++nc) {
+        float v[kTake];
+        tmem_wait32(u);
+        if (GLU) {
+          float* const exch = exch_g + (nc & 1) * 2 * kChunk * 32;
+          // [row][lane]: the first 16 rows from the up warp to the gate warp, the others the other way
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(silu(__uint_as_float(u[i])) * __uint_as_float(v[i]));
-          }
+          for (int i = 0; i < 16; ++i) exch[((up ? 0 : 16) + i) * 32 + lane] = __uint_as_float(up ? u[i] : u[16 + i]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) stage[(c + i) * kTileW + col] = to_bf16(__uint_as_float(u[i]));
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(up ? u[16 + i] : u[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTake; ++i) v[i] = __uint_as_float(u[i]);
         }
-        if (GLU || blk == 1 || w0 + kTileW >= p.a.n) {
+        const bool last = c + kChunk >= x.nr;
+        if (last) {  // read: the next products may overwrite it
           tc_fence_before();
-          mbar_arrive(aempty(a));
+          __syncwarp();
+          if (lane == 0) arrive_cluster(map_leader(aempty(a)));
+        } else {
+          tmem_ld32(acc + c + kChunk, u);
         }
-        if (!(ok = meet())) break;
-        const int tid = (int)threadIdx.x - 64, width = min(kTileW, p.a.n - w0);
-        uint16_t* out = static_cast<uint16_t*>(p.a.out) + w0;
+        if (GLU) {
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + (q & 1)) : "memory");
+          const float* const exch = exch_g + (nc & 1) * 2 * kChunk * 32;
+#pragma unroll
+          for (int i = 0; i < kTake; ++i) {
+            const float y = exch[((up ? 16 : 0) + i) * 32 + lane];
+            v[i] = up ? silu(y) * v[i] : silu(v[i]) * y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTake; ++i) stage[i * 32 + lane] = to_bf16(v[i]);
+        __syncwarp();
+        const int r0 = c + (up ? kTake : 0), rows = min(kTake, x.nr - r0);
+        uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (x.r0 + r0) * p.a.out_stride + w0;
         if (wide) {
-          const int c8 = tid & 15;
-          if (8 * c8 < width)
-            for (int r = tid >> 4; r < x.nr; r += 8)
-              *reinterpret_cast<uint4*>(out + (x.r0 + r) * p.a.out_stride + 8 * c8) =
-                  *reinterpret_cast<const uint4*>(stage + r * kTileW + 8 * c8);
-        } else if (tid < width) {
-          for (int r = 0; r < x.nr; ++r) out[(x.r0 + r) * p.a.out_stride + tid] = stage[r * kTileW + tid];
+          if (8 * (lane & 3) < width)
+            for (int r = lane >> 2; r < rows; r += 8)
+              *reinterpret_cast<uint4*>(out + r * p.a.out_stride + 8 * (lane & 3)) =
+                  *reinterpret_cast<const uint4*>(stage + r * 32 + 8 * (lane & 3));
+        } else if (lane < width) {
+          for (int r = 0; r < rows; ++r) out[r * p.a.out_stride + lane] = stage[r * 32 + lane];
         }
-        ok = meet();
+        __syncwarp();
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may signal it or read its half
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
+}
+
+template <bool GLU>
+cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
+                       const CUtensorMap& tu, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
+  if (e != cudaSuccess) return e;
+  expert_kernel<GLU><<<p.grid / 2 * 2, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tx128, tw, tu);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-template <bool GLU>
-static cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw, const CUtensorMap& tu,
-                              cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
-  if (e != cudaSuccess) return e;
-  expert_kernel<GLU><<<p.grid, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tx128, tw, tu);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw, const CUtensorMap& tu,
-                           cudaStream_t st) {
+cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
+                           const CUtensorMap& tu, cudaStream_t st) {
   return p.a.w_up ? launch_glu<true>(p, tx, tx128, tw, tu, st) : launch_glu<false>(p, tx, tx128, tw, tu, st);
 }
 

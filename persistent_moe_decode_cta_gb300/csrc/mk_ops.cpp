@@ -292,7 +292,7 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   if (!r) r = encode(&tx128, a->x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
   cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, (cuuint64_t)a->n_experts};
   cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
-  cuuint32_t wb[3] = {64, 128, 1};
+  cuuint32_t wb[3] = {64, a->w_up ? 64u : 128u, 1};
   if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!r) r = encode(&tu, a->w_up ? a->w_up : a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (r) return r;

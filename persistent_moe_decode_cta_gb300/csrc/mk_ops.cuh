@@ -89,11 +89,11 @@ __device__ __forceinline__ void op_tma_4d(uint32_t dst, const CUtensorMap* tm, i
 __device__ __forceinline__ void op_cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void op_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void op_cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// arrive on the barrier (one of its expected arrivals) once this thread's copies so far have landed
+__device__ __forceinline__ void op_cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void op_cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Shared-memory matrix descriptor of a swizzled operand (span 128 or 64 bytes).
 //   K-major:  rows of `span` bytes, 8-row groups `sbo` bytes apart (lbo unused).

@@ -19,7 +19,7 @@ struct Head8 {  // values 8j..8j+7 of the lower and of the upper half of a head
   uint4 lo, hi;
 };
 
-// two pairs of floats
+// four pairs of floats
 __device__ __forceinline__ void widen(uint4 u, uint64_t (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -164,7 +164,7 @@ cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
   const int threads = (slots * side + 31) / 32 * 32;
   const long long tokens = (long long)p.c.batch * p.a.n_nodes;
   // Two tokens behind one another keep more loads in flight at the same occupancy (8002 tokens
-  // of 32 + 2 * 4 heads of 128, 164 MB: 35.8 us; 37.0 with two and half the blocks), one where there
+  // of 32 + 2 * 4 heads of 128, 164 MB: 35.8 us; 37.0 with four and half the blocks), one where there
   // are too few to fill the SMs.
   const bool two = tokens >= 2ll * side * 152 * 8;
   const int per = side * (two ? 2 : 1);
