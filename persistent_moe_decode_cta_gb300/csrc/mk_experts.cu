@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         const uint32_t a = nt & 1, acc = tmem + kTileR * a;
         if (!(ok = wait_cluster1(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
         for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
-          if (!(ok = wait_cluster1(full(at.slot), at.phase, abort, p.a.status, 3))) break;
+          if (!(ok = op_wait1(full(at.slot), at.phase, abort, p.a.status, 3))) break;
           if (p.a.rows) {
             if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 8))) break;
             fence_proxy_async_smem();
