@@ -2,7 +2,9 @@
 
 Four builds of the megakernel (default, deterministic, two tensor-core variants), the
 multi-token operators and the host planner/ABI compile in parallel, then link into
-persistent_moe_decode_cta_gb300/libmk.so with the CUDA runtime linked statically.  Usable as `python -m persistent_moe_decode_cta_gb300.build`.
+persistent_moe_decode_cta_gb300/libmk.so with the CUDA runtime linked statically.  Beside it,
+_ops.so is the Python module that checks and marshals tensors for the operators (against the
+installed torch; it finds libmk.so by its own directory).  Usable as `python -m persistent_moe_decode_cta_gb300.build`.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmk.so")
+MODULE = os.path.join(PKG, "_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["mk_kernel.cu", "mk_kernel_det.cu", "mk_kernel_umma.cu", "mk_kernel_umma_ffn.cu",
            "mk_tree_attention.cu", "mk_experts.cu", "mk_qk_rope.cu", "mk_cache_pages.cu", "mk_ops.cpp", "mk_host.cpp"]
@@ -38,6 +41,20 @@ def _flags(extra_ptxas=False):
     return f
 
 
+def _module_command(out: str, obj: bool):
+    """g++ for the Python module: its object, or the link of it."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    if obj:
+        inc = [os.path.join(home, "include"), sysconfig.get_paths()["include"], "/usr/local/cuda/include", os.path.join(ROOT, "include")]
+        abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+        return [cxx, "-O2", "-std=c++17", "-fPIC", abi, *["-I" + i for i in inc], "-c", os.path.join(CSRC, "ops_module.cpp"), "-o", out]
+    return [cxx, "-shared", "-o", out, os.path.join(OUT_DIR, "ops_module.cpp.o"), "-L" + PKG, "-l:libmk.so", "-L" + os.path.join(home, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     nvcc = nvcc_path()
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -49,6 +66,8 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         cmds.append([nvcc, *lang, *_flags(ptxas_info and src.endswith(".cu")), "-c",
                      os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
+
+    cmds.append(_module_command(os.path.join(OUT_DIR, "ops_module.cpp.o"), True))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -66,6 +85,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + " ".join(link) + "\n" + r.stdout + r.stderr)
     os.replace(LIB + ".tmp", LIB)
+    r = subprocess.run(_module_command(MODULE + ".tmp", False), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    os.replace(MODULE + ".tmp", MODULE)
     return LIB
 
 

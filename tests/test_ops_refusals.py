@@ -94,18 +94,6 @@ def test_expert_arguments(over, code):
     assert B.load_library().mk_expert_product(ctypes.byref(experts(**over)), None) == code
 
 
-def test_packed_structs_have_the_layout_of_the_header():
-    for packed, struct in ((ops._KV, B.mk_paged_kv), (ops._ROPE, B.mk_rope_args), (ops._TREE, B.mk_tree_args), (ops._EXPERT, B.mk_expert_args)):
-        assert packed.size == ctypes.sizeof(struct)
-        fields = [getattr(struct, n).size // (8 if n.endswith("_stride") and t is B._S3 else getattr(struct, n).size) for n, t in struct._fields_]
-        values = list(range(1, 1 + sum(fields)))
-        got = struct.from_buffer_copy(packed.pack(*values))
-        flat = []
-        for n, t in struct._fields_:
-            flat += list(getattr(got, n)) if t is B._S3 else [getattr(got, n)]
-        assert flat == values
-
-
 def test_no_rows_is_no_work():
     assert B.load_library().mk_expert_product(ctypes.byref(experts(n_rows=0)), None) == B.MK_OK
 
@@ -146,6 +134,26 @@ def test_tensors_on_the_host_are_refused():
                  lambda: ops.expert_product(x, x, x), lambda: ops.expert_product(x=None, w=x, offsets=x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_native_module_loads_and_checks():
+    m = ops._native()
+    x = torch.zeros(1, 1, 2, 32, dtype=torch.bfloat16)
+    for call, n in ((m.qk_norm_rope, 15), (m.tree_attention, 12), (m.copy_pages, 4), (m.commit_nodes, 7), (m.expert_product, 7)):
+        with pytest.raises(TypeError, match="arguments"):
+            call(x)
+        with pytest.raises(ValueError, match="must be a tensor"):
+            call(*[None] * n)
+        with pytest.raises(ValueError, match="dimensions|CUDA"):
+            call(*[x] * n)
+    for ids in ([0.5], ["1"], [2 ** 31], [True, None]):
+        with pytest.raises(ValueError):
+            m.copy_pages(torch.zeros(1, 1, 1, 16, 32, dtype=torch.bfloat16), x, ids, ids)
+    with pytest.raises(ValueError):
+        ops._page_ids(np.zeros((2, 2), np.int32), "src")
+    with pytest.raises(ValueError):
+        ops._page_ids(np.zeros(2, np.float32), "src")
+    assert ops._page_ids(torch.tensor([3, 4], dtype=torch.int32), "src") == [3, 4] and ops._page_ids(np.zeros(0), "src") == []
 
 
 def test_tree_mask():
