@@ -377,29 +377,40 @@ __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key) {
   return page >= 0 && page < p.c.n_pages ? page : 0;
 }
 
-// What clean_v dropped from column c of a row: p_j * v_j of the keys that the row sees.  Only
-// after a masked block held such values (never with finite caches): plain loads.
+// What clean_v dropped from columns [c0, c1) of a row: p_j * v_j of the keys that the row sees, in
+// place of the stored sum (which no finite part of it can change).  Only after a masked block held such
+// values (never with finite caches): plain loads.
 template <int HD>
-__device__ __noinline__ float nonfinite_part(const TreeParams& p, const Item& it, const Row& r, const uint16_t* q, float m, int c) {
+__device__ __noinline__ void put_nonfinite(const TreeParams& p, const Item& it, const Row& r, int head, float m, float inv, int c0,
+                                           int c1, uint16_t* dst, float4* part) {
+  const uint16_t* q = static_cast<const uint16_t*>(p.a.q) + it.b * p.a.q_stride[0] + r.node * p.a.q_stride[1] + head * p.a.q_stride[2];
   const uint16_t* K = static_cast<const uint16_t*>(p.c.k);
   const uint16_t* V = static_cast<const uint16_t*>(p.c.v);
-  float o = 0.f;
-  for (int j = it.ja; j < it.jb; ++j) {
-    const int k0 = it.kstart + j * kBlk;
-    if (!masked_block(p, it, k0)) continue;
-    for (int w = 0; w < kBlk / 32; ++w) {
-      for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
-        const int key = k0 + 32 * w + __ffs(bits) - 1;
-        const long long at = (((long long)page_of(p, it.b, key) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
-        const float v = bf16_to_f(V[at + c]);
-        if (fabsf(v) <= 3.4e38f) continue;
-        float s = 0.f;
-        for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
-        o += ex2(s * p.scale_log2 - m) * v;
+  for (int c = c0; c < c1; ++c) {
+    float o = 0.f;
+    bool any = false;
+    for (int j = it.ja; j < it.jb; ++j) {
+      const int k0 = it.kstart + j * kBlk;
+      if (!masked_block(p, it, k0)) continue;
+      for (int w = 0; w < kBlk / 32; ++w) {
+        for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
+          const int key = k0 + 32 * w + __ffs(bits) - 1;
+          const long long at = (((long long)page_of(p, it.b, key) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
+          const float v = bf16_to_f(V[at + c]);
+          if (fabsf(v) <= 3.4e38f) continue;
+          float s = 0.f;
+          for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
+          o += ex2(s * p.scale_log2 - m) * v;
+          any = true;
+        }
       }
     }
+    if (!any) continue;
+    if (dst)
+      dst[c] = to_bf16(o * inv);
+    else
+      reinterpret_cast<float*>(part + (c / 4) * kBlk)[c % 4] = o;
   }
-  return o;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -600,13 +611,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!ok) break;
       // ------------------------------------------------------------ the item's result
       const bool whole = nb == it.nblk;
-      const uint16_t* qrow = nullptr;
-      uint16_t* dst = nullptr;
-      if (node >= 0) {
-        const int head = it.kvh * p.gs + row % p.gs;
-        qrow = static_cast<const uint16_t*>(p.a.q) + it.b * p.a.q_stride[0] + node * p.a.q_stride[1] + head * p.a.q_stride[2];
-        dst = static_cast<uint16_t*>(p.a.out) + it.b * p.a.out_stride[0] + node * p.a.out_stride[1] + head * p.a.out_stride[2];
-      }
+      const int head = it.kvh * p.gs + (row - node_in * p.gs);
+      uint16_t* const dst = static_cast<uint16_t*>(p.a.out) + it.b * p.a.out_stride[0] + node * p.a.out_stride[1] + head * p.a.out_stride[2];
       // partial results: first item of the run in slot 0, a later (so last) one in slot 1
       const int slot = it.unit0 + it.ja == u0 ? 0 : 1;
       const long long pt = ((long long)blockIdx.x * 2 + slot) * (TWO ? 2 : 1) + tile;
@@ -651,14 +657,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             o[i] = __uint_as_float(u[i]);
             if (!TWO) o[i] = w0 * o[i] + (other ? w1 * __uint_as_float(v[i]) : 0.f);
           }
-          if (node >= 0) {
-            if (fix) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] += nonfinite_part<HD>(p, it, r, qrow, mm, c + i);
-            }
-            put16(o, whole, inv, dst, part, c);
-          }
+          if (node >= 0) put16(o, whole, inv, dst, part, c);
         }
+        if (fix && node >= 0) put_nonfinite<HD>(p, it, r, head, mm, inv, c0, c1, whole ? dst : nullptr, part);
       }
       tc_fence_before();
       if (!TWO && !(ok = meet())) break;
@@ -910,14 +911,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // A block joins (row, 4 columns) pieces of one row tile of an item, rows side by side as the
 // parts have them.  Few items have many parts each (38 at batch 1 with 4 KV heads): GROUPS = 4
 // groups of threads share them and meet in shared memory, a piece per thread.  Many items have
-// fewer than nine: GROUPS = 1, four pieces per thread.
+// fewer than nine: GROUPS = 1, and four pieces per thread where that still leaves every SM its blocks.
 constexpr int kJoinThreads = 256;
-template <int GROUPS>
-constexpr int kJoinPieces = GROUPS == 1 ? 4 : 1;  // per thread
 
-template <int HD, int GROUPS>
+template <int HD, int GROUPS, int PIECES>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int kSide = kJoinThreads / GROUPS, kN = kJoinPieces<GROUPS>;
+  constexpr int kSide = kJoinThreads / GROUPS, kN = PIECES;
   __shared__ float4 s_o[GROUPS][kSide];
   __shared__ float2 s_ml[GROUPS][kSide];
   const int tiles = p.two ? 2 : 1, rows = p.npt * p.gs;
@@ -959,7 +958,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     l[n] = 0.f;
     o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  constexpr int kBatch = GROUPS == 1 ? 2 : 4;  // parts whose loads go out together
+  constexpr int kBatch = PIECES > 1 ? 2 : 4;  // parts whose loads go out together
   for (int r = r0 + group; r <= r1; r += GROUPS * kBatch) {
     float2 ml[kBatch][kN];
     float4 y[kBatch][kN];
@@ -1048,7 +1047,9 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
   if (e != cudaSuccess) return e;
   const long long heads = (long long)p.c.batch * p.c.n_kv_heads * p.ntp;
   const bool many = 8 * heads > p.grid;  // up to 9 parts an item
-  const int pieces = many ? kJoinThreads * kJoinPieces<1> : kJoinThreads / 4;
+  const long long all = heads * (p.two ? 2 : 1) * p.npt * p.gs * (HD / 4);  // pieces of all items
+  const bool four = many && all > 4ll * kJoinThreads * p.grid * 4;
+  const int pieces = four ? 4 * kJoinThreads : many ? kJoinThreads : kJoinThreads / 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(heads * (p.two ? 2 : 1)), (unsigned)((p.npt * p.gs * (HD / 4) + pieces - 1) / pieces));
   cfg.blockDim = dim3(kJoinThreads);
@@ -1058,7 +1059,9 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1>, p) : cudaLaunchKernelEx(&cfg, join_kernel<HD, 4>, p);
+  return four ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1, 4>, p)
+         : many ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1, 1>, p)
+                : cudaLaunchKernelEx(&cfg, join_kernel<HD, 4, 1>, p);
 }
 
 }  // namespace
