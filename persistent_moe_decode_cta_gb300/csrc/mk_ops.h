@@ -50,6 +50,7 @@ struct TreeParams {
   int npt;         // nodes per 128-row tile
   int two;         // 1: a CTA works on two row tiles at once; 0: on one, with two key streams
   int ntp;         // row-tile groups per (sequence, KV head)
+  int pad;         // units that an item counts for beside its key blocks
   int team;        // tile groups that walk a run of keys together
   int words;       // mask words per node
   int grid;        // CTAs

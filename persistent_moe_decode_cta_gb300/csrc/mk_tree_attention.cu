@@ -71,7 +71,7 @@ struct Item {          // one (sequence, KV head, tile group) and the blocks of 
   int kstart, end;     // its keys: [kstart, end)
   int nblk;            // their blocks
   int ja, jb;          // blocks of this run
-  int unit0;           // global index of its first unit
+  int unit0;           // global index of its first unit (of p.pad without a block)
 };
 
 struct SeqShape {
@@ -100,6 +100,7 @@ struct Entry {
   int b, tp;           // first tile group
   SeqShape s;
   int kstart, nblk;    // blocks of the longest
+  int units;           // per KV head: the blocks, and p.pad for what an item costs beside them
 };
 
 // end of the keys of tile group tp (0 if it has no nodes)
@@ -115,7 +116,7 @@ __device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool rec
   x.b = e / groups;
   x.tp = (e - x.b * groups) * p.team;
   x.s = seq_shape(p, x.b, record);
-  x.kstart = x.nblk = 0;
+  x.kstart = x.nblk = x.units = 0;
   const int per = nodes_per_group(p), first = x.tp * per;
   if (first >= x.s.cnt) return x;
   const int end = group_end(p, x.s, min(x.tp + p.team, (x.s.cnt + per - 1) / per) - 1);
@@ -124,6 +125,7 @@ __device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool rec
     x.kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
   }
   x.nblk = (end - x.kstart + kBlk - 1) / kBlk;
+  x.units = x.nblk + p.pad;
   return x;
 }
 
@@ -139,7 +141,7 @@ __device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool r
   int x = 0;
   if (threadIdx.x < kScan)
     for (int e = (int)threadIdx.x * chunk; e < min(E, ((int)threadIdx.x + 1) * chunk); ++e)
-      x += make_entry(p, e, record).nblk * p.c.n_kv_heads;
+      x += make_entry(p, e, record).units * p.c.n_kv_heads;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -188,23 +190,23 @@ struct Run {
   // one per role, rarely run, costs thousands of cycles of instruction fetches each time.)
   __device__ __noinline__ bool next(const TreeParams& p) {
     while (u < u1) {
-      while (u >= first + x.nblk * p.c.n_kv_heads) {
-        first += x.nblk * p.c.n_kv_heads;
+      while (u >= first + x.units * p.c.n_kv_heads) {
+        first += x.units * p.c.n_kv_heads;
         x = make_entry(p, ++e, false);
       }
       it.b = x.b;
       it.tp = x.tp + member;
       it.len = x.s.len;
       it.cnt = x.s.cnt;
-      it.kvh = (u - first) / x.nblk;
-      it.unit0 = first + it.kvh * x.nblk;
+      it.kvh = (u - first) / x.units;
+      it.unit0 = first + it.kvh * x.units;
       it.kstart = x.kstart;
       it.end = group_end(p, x.s, it.tp);
       it.nblk = max(0, it.end - it.kstart + kBlk - 1) / kBlk;
-      it.ja = u - it.unit0;
-      const int stop = min(x.nblk, it.ja + (u1 - u));
+      const int start = u - it.unit0, stop = min(x.units, start + (u1 - u));
       u = it.unit0 + stop;
-      it.jb = min(stop, it.nblk);
+      it.ja = max(0, start - p.pad);
+      it.jb = min(stop - p.pad, it.nblk);
       if (it.ja < it.jb) return true;
     }
     return false;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int head = it.kvh * p.gs + (row - node_in * p.gs);
       uint16_t* const dst = static_cast<uint16_t*>(p.a.out) + it.b * p.a.out_stride[0] + node * p.a.out_stride[1] + head * p.a.out_stride[2];
       // partial results: first item of the run in slot 0, a later (so last) one in slot 1
-      const int slot = it.unit0 + it.ja == u0 ? 0 : 1;
+      const int slot = u0 >= it.unit0 ? 0 : 1;
       const long long pt = ((long long)blockIdx.x * 2 + slot) * (TWO ? 2 : 1) + tile;
       float4* part = reinterpret_cast<float4*>(p.part) + pt * (HD / 4) * kBlk + row;
       float w0 = 1.f, w1 = 0.f;      // weights of the streams' sums (TWO: of this one's)
@@ -932,14 +934,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const Entry x = make_entry(p, e, false);
   const int end = group_end(p, x.s, tp), nblk = (end - x.kstart + kBlk - 1) / kBlk;
   const int chunk = (num_entries(p) + kScan - 1) / kScan;
-  int g0 = kvh * x.nblk;
-  for (int y = e / chunk * chunk; y < e; ++y) g0 += make_entry(p, y, false).nblk * p.c.n_kv_heads;
+  int g0 = kvh * x.units;
+  for (int y = e / chunk * chunk; y < e; ++y) g0 += make_entry(p, y, false).units * p.c.n_kv_heads;
   pdl_wait();
   if (end == 0) return;
   const int U = __ldcg(p.table + kScan);
   g0 += __ldcg(p.table + e / chunk);
   const int G = run_count(p, U);
-  const int r0 = run_owner(g0, U, G), r1 = run_owner(g0 + nblk - 1, U, G);
+  const int r0 = run_owner(g0 + p.pad, U, G), r1 = run_owner(g0 + p.pad + nblk - 1, U, G);
   if (r0 == r1) return;  // written whole
   // slot 0 holds the item that a run starts in: every part but, maybe, the first
   const int slot0 = run_begin(r0, U, G) >= g0 ? 0 : 1;

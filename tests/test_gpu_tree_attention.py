@@ -96,6 +96,17 @@ def test_windows(heads, window, tree):
     check(setup(heads, [0, 40, 700], 75, tree, counts=[75, 20, 75]), window)
 
 
+@pytest.mark.parametrize("window", [0, 100])
+def test_more_items_than_runs(window):
+    """Work lists with several items a run: many sequences, many groups of nodes."""
+    lens = [(37 * i * i) % 400 for i in range(60)]
+    check(setup((8, 4, 64), lens, 3, counts=[i % 4 for i in range(60)]), window)
+    check(setup((8, 4, 32), lens, 40, tree=False, counts=[(7 * i) % 41 for i in range(60)]), window)
+    check(setup((32, 8, 128), lens[:40], 45), window)
+    check(setup((16, 4, 64), [0, 777], 1500, tree=False, counts=[1500, 1301]), window)
+    check(setup((8, 1, 128), [40], 3001, tree=False), window)
+
+
 def test_long_context_is_split_and_joined():
     check(setup((32, 4, 128), [20011], 3))
     check(setup((32, 4, 128), [9000], 64))
