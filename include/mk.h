@@ -416,7 +416,8 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  *     what they hold does not matter.
  *   - status: int32[4], zeroed by the caller, or NULL (not recorded).  The first invalid
  *     value that a kernel finds in device data is recorded there as {mk_status code,
- *     sequence or expert, index, value}.  Invalid entries are skipped or clamped, never
+ *     sequence or expert, index, value} (MK_ERR_TIMEOUT: {code, CTA, wait, ..}: an internal
+ *     wait of more than 2 s was given up).  Invalid entries are skipped or clamped, never
  *     followed out of bounds; the outputs of such a call are not valid.
  *   - mk_last_error(NULL) gives the message of a refused call.
  */
@@ -482,14 +483,16 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
  *              seq_lens[b] + a).  Positions are clamped to [seq_len, seq_len + counts - 1],
  *              where a node's depth always lies; they matter only with a window.
  *   q, out     bf16 [batch][n_nodes][n_q_heads][head_dim], strides in elements (multiples
- *              of 8), 16-byte aligned, last dimension contiguous
- *   scale      finite and >= 0
+ *              of 8), 16-byte aligned, last dimension contiguous; out does not overlap q
+ *   scale      finite and >= 0 (times log2 e too)
  *   workspace  mk_tree_attention_workspace(..) bytes, 16-byte aligned, not shared with a
  *              call that may run at the same time; its contents do not matter
  * A row that sees no key (or only scores of -infinity) is 0.  Keys that a row does not see
  * do not reach it whatever they hold, NaN and infinities included.  fp32 scores, softmax
  * statistics and sums; the softmax weights are rounded to bf16 for the tensor cores.  The
- * sums have a fixed order: equal calls give equal bits.  n_q_heads / n_kv_heads <= 128.
+ * sums have a fixed order: equal calls give equal bits.  n_q_heads / n_kv_heads <= 128;
+ * batch times the groups of nodes (up to 8 groups count as one; a group has 2 * (128 / (n_q_heads /
+ * n_kv_heads)) nodes) <= 65536.
  * Keys on a page outside [0, n_pages) are read from page 0 (MK_ERR_BAD_PAGE). */
 typedef struct mk_tree_args {
   const void* q;
@@ -525,7 +528,7 @@ int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n
  * nodes may be in any order.
  *   cache      k, v are the whole pools [n_layers][n_pages][..]
  *   accepted   int32[batch][max_accept], max_accept in 1..512
- *   new_lens   int32[batch], not seq_lens itself
+ *   new_lens   int32[batch], not seq_lens itself nor a part of it
  * A sequence with an entry whose slot lies beyond its page table (MK_ERR_INVALID) or on a
  * page outside [0, n_pages) (MK_ERR_BAD_PAGE) is left as it was.  The pages that the nodes
  * lie on belong to one sequence each. */
@@ -542,7 +545,7 @@ int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accep
  *   offsets  int32[n_experts + 1], ascending, within [0, n_rows]; rows of `out` outside
  *            [offsets[0], offsets[n_experts]) are not written
  *   rows     int32[n_rows] in [0, n_x) or NULL (then n_x >= n_rows)
- *   out      bf16 [n_rows][n], row stride out_stride elements
+ *   out      bf16 [n_rows][n], row stride out_stride elements; it does not overlap x
  * x, w, w_up 16-byte aligned; n_experts in 1..256.  fp32 accumulation, one rounding.
  * Offsets that descend or leave [0, n_rows] and rows outside [0, n_x) are clamped
  * (MK_ERR_INVALID). */

@@ -109,6 +109,9 @@ int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   const double units = (double)c->batch * c->n_kv_heads * p.ntp * ((double)c->max_pages / 8 + 8);
   if (units >= 2147483647.0 || (double)c->batch * c->n_kv_heads * p.ntp * 8 >= 2147483647.0)
     return op_fail(MK_ERR_UNSUPPORTED, "batch x heads x nodes x keys exceeds 2^31 work units");
+  // (every CTA adds up the work list, 128 entries at a time)
+  if ((long long)c->batch * ((p.ntp + p.team - 1) / p.team) > kOpMaxEntries)
+    return op_fail(MK_ERR_UNSUPPORTED, "batch x groups of nodes: %lld > %d", (long long)c->batch * ((p.ntp + p.team - 1) / p.team), kOpMaxEntries);
   const int rc = num_sms(&p.grid);
   if (rc) return rc;
   // Where runs hold several items, what an item costs beside its blocks (queries, masked blocks, results)
@@ -180,7 +183,7 @@ int mk_tree_attention(const mk_paged_kv* cache, const mk_tree_args* args, void* 
   if (!r) r = check_rows("out", args->out, args->out_stride, dq);
   if (r) return r;
   if (args->out == args->q) return op_fail(MK_ERR_INVALID, "out must not be q");
-  if (!(args->scale >= 0.f) || !std::isfinite(args->scale)) return op_fail(MK_ERR_INVALID, "scale must be finite and >= 0");
+  if (!(args->scale >= 0.f) || !std::isfinite(args->scale * 1.4426950408889634f)) return op_fail(MK_ERR_INVALID, "scale must be finite and >= 0");
   if (args->window < 0) return op_fail(MK_ERR_INVALID, "window %d < 0", args->window);
   if (!args->workspace || !aligned16(args->workspace)) return op_fail(MK_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
   TreeParams p{};
@@ -283,7 +286,7 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
     return op_fail(MK_ERR_INVALID, "x_stride %lld: need a multiple of 8, at least k", (long long)a->x_stride);
   if (a->out_stride < a->n) return op_fail(MK_ERR_INVALID, "out_stride %lld < n", (long long)a->out_stride);
   const long long step = a->w_up ? 128 : 256;
-  if (((long long)a->n_rows / 128 + a->n_experts) * ((a->n + step - 1) / step) >= 0x7fffffffll)
+  if (((long long)a->n_rows / 128 + a->n_experts) * ((a->n + step - 1) / step) >= 0x7fffffffll - 1024)
     return op_fail(MK_ERR_UNSUPPORTED, "more than 2^31 tiles");
   ExpertParams p{};
   p.a = *a;

@@ -30,6 +30,7 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& do
 
 constexpr int kOpPage = 16;            // tokens per cache page
 constexpr int kOpMaxBatch = 65535;     // sequences of one call
+constexpr int kOpMaxEntries = 65536;   // of the attention's work list: sequences x groups of nodes
 constexpr int kOpMaxExperts = 256;     // experts of one call (as mk_create)
 constexpr int kOpMaxAccept = 512;      // accepted nodes per sequence (staged in shared memory)
 constexpr int kOpMaxHalf = 64;         // head_dim / 2 at most

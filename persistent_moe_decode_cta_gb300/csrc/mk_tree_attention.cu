@@ -25,7 +25,7 @@
 //
 // Keys that a row does not see get a score of -infinity.  Blocks with such keys have their V
 // cleaned in shared memory by two further warps (rows past the end and values that are not
-// finite become zero, since 0 * NaN would reach every row); what was dropped is added by plain
+// finite become zero, since 0 * NaN would reach every row); what was dropped is added with plain
 // loads at the end, for the rows that do see it.
 //
 // The work is a list of units, one per (sequence, tile group, KV head, key block), cut into
@@ -379,39 +379,53 @@ __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key) {
   return page >= 0 && page < p.c.n_pages ? page : 0;
 }
 
-// What clean_v dropped from columns [c0, c1) of a row: p_j * v_j of the keys that the row sees, in
-// place of the stored sum (which no finite part of it can change).  Only after a masked block held such
-// values (never with finite caches): plain loads.
+// What clean_v dropped from columns [c0, c1) of a row: p_j * v_j of the keys that the row sees, added
+// to the stored values (in any order and precision: each is an infinity or NaN, and so is the sum).
+// Only after a masked block held such values (never with finite caches): plain loads.
 template <int HD>
 __device__ __noinline__ void put_nonfinite(const TreeParams& p, const Item& it, const Row& r, int head, float m, float inv, int c0,
                                            int c1, uint16_t* dst, float4* part) {
   const uint16_t* q = static_cast<const uint16_t*>(p.a.q) + it.b * p.a.q_stride[0] + r.node * p.a.q_stride[1] + head * p.a.q_stride[2];
   const uint16_t* K = static_cast<const uint16_t*>(p.c.k);
   const uint16_t* V = static_cast<const uint16_t*>(p.c.v);
-  for (int c = c0; c < c1; ++c) {
-    float o = 0.f;
-    bool any = false;
-    for (int j = it.ja; j < it.jb; ++j) {
-      const int k0 = it.kstart + j * kBlk;
-      if (!masked_block(p, it, k0)) continue;
-      for (int w = 0; w < kBlk / 32; ++w) {
-        for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
-          const int key = k0 + 32 * w + __ffs(bits) - 1;
-          const long long at = (((long long)page_of(p, it.b, key) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
+  for (int j = it.ja; j < it.jb; ++j) {
+    const int k0 = it.kstart + j * kBlk;
+    if (!masked_block(p, it, k0)) continue;
+    for (int w = 0; w < kBlk / 32; ++w) {
+      for (uint32_t bits = sees32(p, it, r, k0 + 32 * w); bits; bits &= bits - 1) {
+        const int key = k0 + 32 * w + __ffs(bits) - 1;
+        const long long at = (((long long)page_of(p, it.b, key) * p.c.n_kv_heads + it.kvh) * kOpPage + key % kOpPage) * HD;
+        uint32_t any = 0;
+#pragma unroll
+        for (int c = 0; c < HD; c += 8) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(V + at + c));
+          any |= (uint32_t)(nonfinite2(v.x) || nonfinite2(v.y) || nonfinite2(v.z) || nonfinite2(v.w)) << (c / 8);
+        }
+        if (!any) continue;
+        float s = 0.f;
+        for (int d = 0; d < HD; d += 8) {
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(q + d)), b = __ldg(reinterpret_cast<const uint4*>(K + at + d));
+          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2_to_f2(x[i]), g = bf16x2_to_f2(y[i]);
+            s += f.x * g.x + f.y * g.y;
+          }
+        }
+        const float weight = ex2(s * p.scale_log2 - m);
+        for (int c = c0; c < c1; ++c) {
+          if (!(any >> (c / 8) & 1u)) continue;
           const float v = bf16_to_f(V[at + c]);
           if (fabsf(v) <= 3.4e38f) continue;
-          float s = 0.f;
-          for (int d = 0; d < HD; ++d) s += bf16_to_f(q[d]) * bf16_to_f(K[at + d]);
-          o += ex2(s * p.scale_log2 - m) * v;
-          any = true;
+          if (dst) {
+            dst[c] = to_bf16(bf16_to_f(dst[c]) + weight * v * inv);
+          } else {
+            float* o = reinterpret_cast<float*>(part + (c / 4) * kBlk) + c % 4;
+            __stcg(o, __ldcg(o) + weight * v);
+          }
         }
       }
     }
-    if (!any) continue;
-    if (dst)
-      dst[c] = to_bf16(o * inv);
-    else
-      reinterpret_cast<float*>(part + (c / 4) * kBlk)[c % 4] = o;
   }
 }
 
@@ -456,6 +470,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const uint32_t base = smem_u32(raw);
   if (base & 1023u) {
     if (threadIdx.x == 0) op_error(p.a.status, MK_ERR_UNSUPPORTED, -1, (int)base, 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.table[kScan] = 0;
     return;
   }
   const uint32_t q_s = base, ring = base + (TWO ? 2 : 1) * C::kTile;
@@ -939,6 +954,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   pdl_wait();
   if (end == 0) return;
   const int U = __ldcg(p.table + kScan);
+  if (U <= 0) return;
   g0 += __ldcg(p.table + e / chunk);
   const int G = run_count(p, U);
   const int r0 = run_owner(g0 + p.pad, U, G), r1 = run_owner(g0 + p.pad + nblk - 1, U, G);
@@ -1047,6 +1063,7 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
                       cudaStream_t st) {
   const cudaError_t e = p.two ? launch_one<HD, true>(p, tq, tk, tv, st) : launch_one<HD, false>(p, tq, tk, tv, st);
   if (e != cudaSuccess) return e;
+  if (p.c.max_pages <= kBlk / kOpPage) return cudaSuccess;  // items of one block: nothing is split
   const long long heads = (long long)p.c.batch * p.c.n_kv_heads * p.ntp;
   const bool many = 8 * heads > p.grid;  // up to 9 parts an item
   const long long all = heads * (p.two ? 2 : 1) * p.npt * p.gs * (HD / 4);  // pieces of all items

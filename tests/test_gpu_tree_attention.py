@@ -186,6 +186,27 @@ def test_masked_values_do_not_leak():
             check(a, window=50)
 
 
+@pytest.mark.parametrize("heads", LAYOUTS)
+@pytest.mark.parametrize("n,length", [(6, 300), (60, 300), (6, 3000), (60, 3000)])
+def test_infinities_of_masked_and_unmasked_blocks_add(heads, n, length):
+    """Infinities of a cached key (in a block that every row sees) and of nodes that some rows see."""
+    hkv, hd = heads[1], heads[2]
+    a = setup(heads, [length], n)
+    i = torch.arange(n, device="cuda")
+    seen = (i[:, None] == i) | (i == 0) | ((i == 2) & (i[:, None] % 2 == 0)) | ((i == 4) & (i[:, None] % 3 == 0))
+    words = torch.zeros(n, a["mask"].shape[2], dtype=torch.int64, device="cuda")
+    for x in range(n):
+        words[:, x // 32] += seen[:, x].long() << (x % 32)
+    a["mask"][0] = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+    for at, values in ((10, (-math.inf, NAN, math.inf)), (length + 2, (math.inf, math.inf, 1.0, -math.inf)),
+                       (length + 4, (1.0, 1.0, -math.inf, 1.0, math.inf))):
+        row = torch.zeros(1, hkv, hd, dtype=torch.bfloat16, device="cuda")
+        row[:, :, :len(values)] = torch.tensor(values, dtype=torch.bfloat16)
+        R.put(a["v_cache"], a["page_table"], 0, torch.tensor([at], device="cuda"), row)
+    out = check(a)
+    assert torch.isnan(out[0, 2, :, 0]).all() and (out[0, 1, :, 0] == -math.inf).all() and torch.isnan(out[0, :, :, 1]).all()
+
+
 def test_positions_are_clamped_to_the_sequence():
     a = setup((8, 2, 32), [100], 6)
     for lo in (-1000, 2 ** 31 - 1):

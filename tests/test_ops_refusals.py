@@ -71,7 +71,7 @@ def test_rope_arguments(over, code):
 @pytest.mark.parametrize("over,code", [
     (dict(q=None), INV), (dict(out=None), INV), (dict(out=P), INV), (dict(q=P + 2), INV), (dict(n_nodes=0), INV),
     (dict(n_nodes=1 << 30), INV), (dict(n_q_heads=9), INV), (dict(n_q_heads=2 * 129), UNS), (dict(window=-1), INV),
-    (dict(scale=-0.1), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(workspace=None), INV),
+    (dict(scale=-0.1), INV), (dict(scale=3e38), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(workspace=None), INV),
     (dict(workspace=P + 8), INV), (dict(q_stride=B._S3(1024, 512, 60)), INV), (dict(out_stride=B._S3(1024, 0, 64)), INV)])
 def test_tree_arguments(over, code):
     a = tree(**over)
@@ -83,6 +83,8 @@ def test_tree_work_is_bounded():
     n = ctypes.c_size_t()
     assert B.load_library().mk_tree_attention_workspace(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) == UNS
     assert B.load_library().mk_tree_attention_workspace(ctypes.byref(c), ctypes.byref(a), None) == INV
+    c, a = kv(batch=100), tree(n_nodes=1 << 16)                 # 102400 groups of 64 nodes
+    assert B.load_library().mk_tree_attention_workspace(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) == UNS
 
 
 @pytest.mark.parametrize("over,code", [
