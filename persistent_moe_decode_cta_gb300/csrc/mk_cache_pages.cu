@@ -25,9 +25,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
   uint4* dst = pool + (long long)pairs.dst[pair] * page_vecs;
   const int i0 = part * kCopyThreads * kCopyVecs + threadIdx.x;
   uint4 x[kCopyVecs];
+  pdl_wait();
+  pdl_trigger();
 #pragma unroll
   for (int j = 0; j < kCopyVecs; ++j)
-    if (i0 + j * kCopyThreads < page_vecs) x[j] = __ldcs(src + i0 + j * kCopyThreads);
+    if (i0 + j * kCopyThreads < page_vecs) x[j] = op_ld16_once(src + i0 + j * kCopyThreads);
 #pragma unroll
   for (int j = 0; j < kCopyVecs; ++j)
     if (i0 + j * kCopyThreads < page_vecs) __stcs(dst + i0 + j * kCopyThreads, x[j]);
@@ -43,9 +45,8 @@ cudaError_t copy_some(uint8_t* k, uint8_t* v, int n_layers, long long layer_byte
   }
   const int vecs = (int)(page_bytes / 16);
   const int parts = (vecs + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs);
-  copy_pages_kernel<N><<<dim3((unsigned)(n * parts), (unsigned)n_layers, 2), kCopyThreads, 0, st>>>(
-      pairs, reinterpret_cast<uint4*>(k), reinterpret_cast<uint4*>(v), layer_bytes / 16, vecs, parts);
-  return cudaGetLastError();
+  return launch_early(copy_pages_kernel<N>, dim3((unsigned)(n * parts), (unsigned)n_layers, 2), kCopyThreads, 0, st, pairs,
+                      reinterpret_cast<uint4*>(k), reinterpret_cast<uint4*>(v), layer_bytes / 16, vecs, parts);
 }
 
 constexpr int kCommitThreads = 128;
@@ -61,25 +62,27 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_con
   int* to = from + p.max_accept;                    // ... and of its new place
   uint4* rows = reinterpret_cast<uint4*>(raw + ((2 * p.max_accept * 4 + 15) & ~15));
   const int b = blockIdx.x / p.c.n_kv_heads, kvh = blockIdx.x - b * p.c.n_kv_heads;
-  const int len = __ldg(p.c.seq_lens + b);
+  pdl_wait();
+  pdl_trigger();
+  const int len = op_ld(p.c.seq_lens + b);
   const int32_t* acc = p.accepted + (long long)b * p.max_accept;
   if (threadIdx.x == 0) s_count = p.max_accept;
   __syncthreads();
   for (int i = threadIdx.x; i < p.max_accept; i += kCommitThreads)
-    if (__ldg(acc + i) < 0) atomicMin(&s_count, i);
+    if (op_ld(acc + i) < 0) atomicMin(&s_count, i);
   __syncthreads();
   const int count = s_count;
   int bad = 0;
   const int32_t* table = p.c.page_table + (long long)b * p.c.max_pages;
   for (int i = threadIdx.x; i < 2 * count; i += kCommitThreads) {
-    const int a = i < count ? __ldg(acc + i) : i - count;
+    const int a = i < count ? op_ld(acc + i) : i - count;
     const long long at = (long long)len + a;
     if (len < 0 || at >= 16ll * p.c.max_pages) {
       op_error(p.status, MK_ERR_INVALID, b, a, len);
       bad = 1;
       continue;
     }
-    const int page = __ldg(table + at / kOpPage);
+    const int page = op_ld(table + at / kOpPage);
     if (page < 0 || page >= p.c.n_pages) {
       op_error(p.status, MK_ERR_BAD_PAGE, b, (int)(at / kOpPage), page);
       bad = 1;
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_con
   uint4* pool = static_cast<uint4*>(blockIdx.z ? p.c.v : p.c.k) + (long long)blockIdx.y * layer_vecs;
   for (int i = threadIdx.x; i < count * vecs; i += kCommitThreads) {
     const int r = i / vecs, c = i - r * vecs;
-    const int slot = (int)(((long long)len + __ldg(acc + r)) % kOpPage);
+    const int slot = (int)(((long long)len + op_ld(acc + r)) % kOpPage);
     rows[i] = pool[((long long)(from[r] + kvh) * kOpPage + slot) * vecs + c];
   }
   __syncthreads();
@@ -127,8 +130,7 @@ cudaError_t launch_commit(const CommitParams& p, cudaStream_t st) {
     const cudaError_t e = allow_smem(commit_kernel, kOpMaxAccept * (2 * 4 + 2 * 2 * kOpMaxHalf), done);  // the most of any call
     if (e != cudaSuccess) return e;
   }
-  commit_kernel<<<dim3((unsigned)(p.c.batch * p.c.n_kv_heads), (unsigned)p.n_layers, 2), kCommitThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(commit_kernel, dim3((unsigned)(p.c.batch * p.c.n_kv_heads), (unsigned)p.n_layers, 2), kCommitThreads, smem, st, p);
 }
 
 }  // namespace mk

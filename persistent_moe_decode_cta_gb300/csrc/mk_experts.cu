@@ -143,7 +143,7 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
 }
 
 __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, bool record, int& lo, int& hi) {
-  const int a = __ldg(p.a.offsets + e), b = __ldg(p.a.offsets + e + 1);
+  const int a = op_ld(p.a.offsets + e), b = op_ld(p.a.offsets + e + 1);
   lo = min(max(a, 0), p.a.n_rows);
   hi = min(max(b, lo), p.a.n_rows);
   if (record && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
@@ -240,6 +240,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+  pdl_wait();
+  pdl_trigger();
   scan_experts(p, sh);
   tc_fence_before();
   __syncthreads();
@@ -307,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         const int i = row0 + 16 * j;
         int r = 0;
         if (i < mine) {
-          const int s = __ldg(p.a.rows + x.r0 + first + i);
+          const int s = op_ld(p.a.rows + x.r0 + first + i);
           r = min(max(s, 0), p.a.n_x - 1);
           if (r != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, x.r0 + first + i, s);
         }
@@ -456,8 +458,8 @@ cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUten
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
   if (e != cudaSuccess) return e;
-  expert_kernel<GLU><<<p.grid / 2 * 2, kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st>>>(p, tx, tx128, tw, tu);
-  return cudaGetLastError();
+  return launch_early(expert_kernel<GLU>, dim3((unsigned)(p.grid / 2 * 2)), kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st,
+                      p, tx, tx128, tw, tu);
 }
 
 }  // namespace

@@ -196,8 +196,27 @@ struct Ring {
 };
 
 // Programmatic dependent launch: the next kernel of the stream may start its prologue /
-// wait until every earlier kernel's memory is visible.
+// wait until every earlier kernel's memory is visible.  Every thread block of every operator
+// waits before it touches global memory, so that "every earlier kernel" holds along a chain.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Loads that stay behind a pdl_wait (a load through the read-only path is free to move before it).
+__device__ __forceinline__ int op_ld(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 op_ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// ... of values that are read once
+__device__ __forceinline__ uint4 op_ld16_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 }  // namespace mk

@@ -28,6 +28,23 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& do
   return e;
 }
 
+// Launch `kernel` so that its prologue may run beside the end of the kernel before it on the
+// stream (griddepcontrol.wait in the kernel is where it waits for that one).
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kOpPage = 16;            // tokens per cache page
 constexpr int kOpMaxBatch = 65535;     // sequences of one call
 constexpr int kOpMaxEntries = 65536;   // of the attention's work list: sequences x groups of nodes

@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const __grid_c
   const int64_t* stride = kind == 0 ? p.a.q_stride : kind == 1 ? p.a.k_stride : p.a.v_stride;
   const uint16_t* src = static_cast<const uint16_t*>(kind == 0 ? p.a.q : kind == 1 ? p.a.k : p.a.v) + hk * stride[2] + 8 * lane;
 
+  pdl_wait();
+  pdl_trigger();
   Head8 h[P];
   uint16_t* dst[P];
   int b = (t0 + tl) / n, node = t0 + tl - b * n - side;
@@ -68,21 +70,21 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const __grid_c
     h[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (!mine || t >= tokens) continue;
     const uint16_t* x = src + b * stride[0] + node * stride[1];
-    h[k].lo = __ldcs(reinterpret_cast<const uint4*>(x));
-    h[k].hi = __ldcs(reinterpret_cast<const uint4*>(x + HD / 2));
-    const int cnt = p.a.counts ? __ldg(p.a.counts + b) : n;
+    h[k].lo = op_ld16_once(x);
+    h[k].hi = op_ld16_once(x + HD / 2);
+    const int cnt = p.a.counts ? op_ld(p.a.counts + b) : n;
     if (node >= cnt) continue;
     if (kind == 0) {
       dst[k] = static_cast<uint16_t*>(p.a.q_out) + b * p.a.out_stride[0] + node * p.a.out_stride[1] + hk * p.a.out_stride[2] + 8 * lane;
       continue;
     }
-    const int len = __ldg(p.c.seq_lens + b);
+    const int len = op_ld(p.c.seq_lens + b);
     const long long at = (long long)len + node;
     if (len < 0 || cnt > n || (long long)len + cnt > 16ll * p.c.max_pages) {
       op_error(p.a.status, MK_ERR_INVALID, b, node, len);
       continue;
     }
-    const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + at / kOpPage);
+    const int page = op_ld(p.c.page_table + (long long)b * p.c.max_pages + at / kOpPage);
     if (page < 0 || page >= p.c.n_pages)
       op_error(p.a.status, MK_ERR_BAD_PAGE, b, (int)(at / kOpPage), page);
     else
@@ -93,14 +95,14 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const __grid_c
   const void* gain = kind == 0 ? p.a.q_gain : p.a.k_gain;
   const bool norm = kind != 2 && gain != nullptr;
   if (norm) {
-    widen(__ldg(reinterpret_cast<const uint4*>(gain) + lane), gl);
-    widen(__ldg(reinterpret_cast<const uint4*>(gain) + LPH + lane), gh);
+    widen(op_ld16(static_cast<const uint4*>(gain) + lane), gl);
+    widen(op_ld16(static_cast<const uint4*>(gain) + LPH + lane), gh);
   }
 
   for (int i = threadIdx.x; i < side * P * (HD / 2); i += (int)blockDim.x) {
     const int t = t0 + i / (HD / 2);
     if (t >= tokens) break;
-    const int pos = p.a.positions ? __ldg(p.a.positions + t) : __ldg(p.c.seq_lens + t / n) + t % n;
+    const int pos = p.a.positions ? op_ld(p.a.positions + t) : op_ld(p.c.seq_lens + t / n) + t % n;
     const unsigned long long u = (unsigned long long)(long long)pos * p.turns[i % (HD / 2)];
     float s, c;
     sincospif((float)(int)(u >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns = signed fraction * 2^-31
@@ -170,11 +172,7 @@ cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
   const int per = side * (two ? 2 : 1);
   const dim3 grid((unsigned)((tokens + per - 1) / per), (unsigned)ny);
   const size_t smem = (size_t)per * (HD / 4) * sizeof(float4);
-  if (two)
-    rope_kernel<HD, 2><<<grid, threads, smem, st>>>(p, slots, side);
-  else
-    rope_kernel<HD, 1><<<grid, threads, smem, st>>>(p, slots, side);
-  return cudaGetLastError();
+  return launch_early(two ? rope_kernel<HD, 2> : rope_kernel<HD, 1>, grid, threads, smem, st, p, slots, side);
 }
 
 }  // namespace

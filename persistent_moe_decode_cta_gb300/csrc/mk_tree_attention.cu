@@ -81,8 +81,8 @@ struct SeqShape {
 // Length and node count of a sequence; an invalid one gets no nodes.
 __device__ __forceinline__ SeqShape seq_shape(const TreeParams& p, int b, bool record) {
   SeqShape s;
-  s.len = __ldg(p.c.seq_lens + b);
-  s.cnt = p.a.counts ? __ldg(p.a.counts + b) : p.a.n_nodes;
+  s.len = op_ld(p.c.seq_lens + b);
+  s.cnt = p.a.counts ? op_ld(p.a.counts + b) : p.a.n_nodes;
   if (s.len < 0 || s.cnt > p.a.n_nodes || (long long)s.len + s.cnt > 16ll * p.c.max_pages) {
     if (record) op_error(p.a.status, MK_ERR_INVALID, b, s.cnt, s.len);
     s.cnt = 0;
@@ -232,7 +232,7 @@ __device__ __forceinline__ Row make_row(const TreeParams& p, const Item& it, int
   const long long at = (long long)it.b * p.a.n_nodes + node;
   r.pos = it.len + node;
   if (p.a.window > 0) {
-    if (p.a.positions) r.pos = min(max(__ldg(p.a.positions + at), it.len), it.len + it.cnt - 1);
+    if (p.a.positions) r.pos = min(max(op_ld(p.a.positions + at), it.len), it.len + it.cnt - 1);
     r.lo = r.pos - p.a.window + 1;
   }
   if (p.a.mask) r.mask = p.a.mask + at * p.words;
@@ -252,8 +252,8 @@ __device__ __noinline__ uint32_t sees32(const TreeParams& p, const Item& it, con
     uint32_t nb;
     if (r.mask) {
       const int w = a0 >> 5, sh = a0 & 31;  // (floor)
-      const uint32_t x = w >= 0 && w < p.words ? (uint32_t)__ldg(r.mask + w) : 0u;
-      const uint32_t y = sh && w + 1 < p.words ? (uint32_t)__ldg(r.mask + w + 1) : 0u;
+      const uint32_t x = w >= 0 && w < p.words ? (uint32_t)op_ld(r.mask + w) : 0u;
+      const uint32_t y = sh && w + 1 < p.words ? (uint32_t)op_ld(r.mask + w + 1) : 0u;
       nb = __funnelshift_r(x, y, sh);
     } else {
       const int e = r.node - a0 + 1;  // nodes 0..node
@@ -267,7 +267,7 @@ __device__ __noinline__ uint32_t sees32(const TreeParams& p, const Item& it, con
         const int i = __ffs(m) - 1, a = a0 + i;
         int pa = it.len + a;
         if (p.a.positions)
-          pa = min(max(__ldg(p.a.positions + (long long)it.b * p.a.n_nodes + a), it.len), it.len + it.cnt - 1);
+          pa = min(max(op_ld(p.a.positions + (long long)it.b * p.a.n_nodes + a), it.len), it.len + it.cnt - 1);
         if (pa < r.lo) nb &= ~(1u << i);
       }
     }
@@ -375,7 +375,7 @@ __device__ __noinline__ void clean_v(uint8_t* stage, int live, int t, int* bad) 
 }
 
 __device__ __forceinline__ int page_of(const TreeParams& p, int b, int key) {
-  const int page = __ldg(p.c.page_table + (long long)b * p.c.max_pages + key / kOpPage);
+  const int page = op_ld(p.c.page_table + (long long)b * p.c.max_pages + key / kOpPage);
   return page >= 0 && page < p.c.n_pages ? page : 0;
 }
 
@@ -398,13 +398,13 @@ __device__ __noinline__ void put_nonfinite(const TreeParams& p, const Item& it, 
         uint32_t any = 0;
 #pragma unroll
         for (int c = 0; c < HD; c += 8) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(V + at + c));
+          const uint4 v = op_ld16(V + at + c);
           any |= (uint32_t)(nonfinite2(v.x) || nonfinite2(v.y) || nonfinite2(v.z) || nonfinite2(v.w)) << (c / 8);
         }
         if (!any) continue;
         float s = 0.f;
         for (int d = 0; d < HD; d += 8) {
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(q + d)), b = __ldg(reinterpret_cast<const uint4*>(K + at + d));
+          const uint4 a = op_ld16(q + d), b = op_ld16(K + at + d);
           const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -418,10 +418,11 @@ __device__ __noinline__ void put_nonfinite(const TreeParams& p, const Item& it, 
           const float v = bf16_to_f(V[at + c]);
           if (fabsf(v) <= 3.4e38f) continue;
           if (dst) {
-            dst[c] = to_bf16(bf16_to_f(dst[c]) + weight * v * inv);
+            volatile uint16_t* o = dst + c;
+            *o = to_bf16(bf16_to_f(*o) + weight * v * inv);
           } else {
-            float* o = reinterpret_cast<float*>(part + (c / 4) * kBlk) + c % 4;
-            __stcg(o, __ldcg(o) + weight * v);
+            volatile float* o = reinterpret_cast<float*>(part + (c / 4) * kBlk) + c % 4;
+            *o = *o + weight * v;
           }
         }
       }
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   TreeShared& sh = *reinterpret_cast<TreeShared*>(raw + C::kSlots * C::kTile);
   const uint32_t base = smem_u32(raw);
   if (base & 1023u) {
+    pdl_wait();
     if (threadIdx.x == 0) op_error(p.a.status, MK_ERR_UNSUPPORTED, -1, (int)base, 0);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.table[kScan] = 0;
     return;
@@ -479,7 +481,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
 
-  pdl_trigger();
   if (warp == 8 && lane < 3) {
     const CUtensorMap* tm = lane == 0 ? &tk : lane == 1 ? &tv : &tq;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
@@ -507,6 +508,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     fence_proxy_async_smem();
   }
   tc_fence_before();
+  // (the join, which reads the work list's inputs at once, starts only when they are final)
+  pdl_wait();
+  pdl_trigger();
   scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
@@ -691,7 +695,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       bool ok = true;
       auto look_up = [&](const Item& it, int j) -> int {
         const int at = (it.kstart + j * kBlk) / kOpPage + lane;
-        return lane < 8 && at * kOpPage < it.end ? __ldg(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
+        return lane < 8 && at * kOpPage < it.end ? op_ld(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
       };
       while (ok && uniform(run.next(p))) {
         const Item& it = run.it;
@@ -952,10 +956,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   int g0 = kvh * x.units;
   for (int y = e / chunk * chunk; y < e; ++y) g0 += make_entry(p, y, false).units * p.c.n_kv_heads;
   pdl_wait();
+  pdl_trigger();
   if (end == 0) return;
-  const int U = __ldcg(p.table + kScan);
+  const int U = op_ld(p.table + kScan);
   if (U <= 0) return;
-  g0 += __ldcg(p.table + e / chunk);
+  g0 += op_ld(p.table + e / chunk);
   const int G = run_count(p, U);
   const int r0 = run_owner(g0 + p.pad, U, G), r1 = run_owner(g0 + p.pad + nblk - 1, U, G);
   if (r0 == r1) return;  // written whole
@@ -989,8 +994,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         ml[k][n] = make_float2(-INFINITY, 0.f);
         y[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live[n] && r + k * GROUPS <= r1) {
-          ml[k][n] = __ldcg(p.part_ml + pt * kBlk + row[n]);
-          y[k][n] = __ldcg(reinterpret_cast<const float4*>(p.part) + (pt * (HD / 4) + c4[n]) * kBlk + row[n]);
+          ml[k][n] = p.part_ml[pt * kBlk + row[n]];
+          const uint4 u = op_ld16_once(reinterpret_cast<const float4*>(p.part) + (pt * (HD / 4) + c4[n]) * kBlk + row[n]);
+          y[k][n] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
         }
       }
     }
@@ -1054,8 +1060,7 @@ cudaError_t launch_one(const TreeParams& p, const CUtensorMap& tq, const CUtenso
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(tree_kernel<HD, TWO>, TreeSmem<HD>::kBytes, done);
   if (e != cudaSuccess) return e;
-  tree_kernel<HD, TWO><<<p.grid, kTreeThreads, TreeSmem<HD>::kBytes, st>>>(p, tq, tk, tv);
-  return cudaGetLastError();
+  return launch_early(tree_kernel<HD, TWO>, dim3((unsigned)p.grid), kTreeThreads, TreeSmem<HD>::kBytes, st, p, tq, tk, tv);
 }
 
 template <int HD>
@@ -1069,18 +1074,8 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
   const long long all = heads * (p.two ? 2 : 1) * p.npt * p.gs * (HD / 4);  // pieces of all items
   const bool four = many && all > 4ll * kJoinThreads * p.grid * 4;
   const int pieces = four ? 4 * kJoinThreads : many ? kJoinThreads : kJoinThreads / 4;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(heads * (p.two ? 2 : 1)), (unsigned)((p.npt * p.gs * (HD / 4) + pieces - 1) / pieces));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return four ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1, 4>, p)
-         : many ? cudaLaunchKernelEx(&cfg, join_kernel<HD, 1, 1>, p)
-                : cudaLaunchKernelEx(&cfg, join_kernel<HD, 4, 1>, p);
+  const dim3 grid((unsigned)(heads * (p.two ? 2 : 1)), (unsigned)((p.npt * p.gs * (HD / 4) + pieces - 1) / pieces));
+  return launch_early(four ? join_kernel<HD, 1, 4> : many ? join_kernel<HD, 1, 1> : join_kernel<HD, 4, 1>, grid, kJoinThreads, 0, st, p);
 }
 
 }  // namespace
