@@ -10,6 +10,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/core/GradMode.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -293,6 +294,13 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// Whether the tensor is on the current device (None: no CUDA tensor).
+PyObject* is_here(PyObject*, PyObject* o) {
+  if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda()) Py_RETURN_NONE;
+  int dev = -1;
+  return PyBool_FromLong(cudaGetDevice(&dev) == cudaSuccess && dev == THPVariable_Unpack(o).get_device());
+}
+
 PyObject* setup(PyObject*, PyObject* check) {
   Py_INCREF(check);
   Py_XSETREF(g_check, check);
@@ -306,7 +314,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<qk_norm_rope, 15>("qk_norm_rope"), method<tree_attention, 12>("tree_attention"),
                          method<copy_pages, 4>("copy_pages"),      method<commit_nodes, 7>("commit_nodes"),
-                         method<expert_product, 7>("expert_product"), {"setup", setup, METH_O, nullptr},
+                         method<expert_product, 7>("expert_product"), {"is_here", is_here, METH_O, nullptr},
+                         {"setup", setup, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -58,11 +58,11 @@ def _operator(fn):
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         first = args[0] if args else kw.get(lead)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        here = (_module or _native()).is_here(first)
+        if here is None:
             raise ValueError(f"{lead} must be a CUDA tensor")
-        dev = first.get_device()
-        if dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
+        if not here:
+            with torch.cuda.device(first.get_device()):
                 return call(*args, stream=stream, **kw)
         if stream is None:
             return fn(*args, **kw)
