@@ -70,6 +70,8 @@ struct TreeParams {
   int ntp;         // row-tile groups per (sequence, KV head)
   int pad;         // units that an item counts for beside its key blocks
   int team;        // tile groups that walk a run of keys together
+  int teams;       // such teams in the grid
+  int groups;      // entries of the work list per sequence
   int words;       // mask words per node
   int grid;        // CTAs
   float scale_log2;

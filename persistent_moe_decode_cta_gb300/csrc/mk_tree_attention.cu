@@ -112,14 +112,13 @@ __device__ __forceinline__ int group_end(const TreeParams& p, const SeqShape& s,
 
 __device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool record) {
   Entry x;
-  const int groups = (p.ntp + p.team - 1) / p.team;
-  x.b = e / groups;
-  x.tp = (e - x.b * groups) * p.team;
+  x.b = p.groups == 1 ? e : e / p.groups;
+  x.tp = (e - x.b * p.groups) * p.team;
   x.s = seq_shape(p, x.b, record);
   x.kstart = x.nblk = x.units = 0;
   const int per = nodes_per_group(p), first = x.tp * per;
   if (first >= x.s.cnt) return x;
-  const int end = group_end(p, x.s, min(x.tp + p.team, (x.s.cnt + per - 1) / per) - 1);
+  const int end = x.s.len + (p.a.mask ? x.s.cnt : min(x.s.cnt, first + p.team * per));  // of its last group with nodes
   if (p.a.window > 0) {
     const int pos = x.s.len + (p.a.mask || p.a.positions ? 0 : first);  // the earliest position of its nodes
     x.kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
@@ -129,9 +128,10 @@ __device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool rec
   return x;
 }
 
-__device__ __forceinline__ int num_entries(const TreeParams& p) { return p.c.batch * ((p.ntp + p.team - 1) / p.team); }
+__device__ __forceinline__ int num_entries(const TreeParams& p) { return p.c.batch * p.groups; }
 
 constexpr int kScan = 128;  // threads that add up the work list
+constexpr int kJoinThreads = 256;
 
 // Prefix sums of the entries' units: thread i < kScan owns entries [i * chunk, (i + 1) *
 // chunk), pre[i] is the number of units before them, pre[kScan] that of all.
@@ -157,17 +157,10 @@ __device__ void scan_units(const TreeParams& p, int* pre, int* warp_sums, bool r
   __syncthreads();
 }
 
-// run of team g of G: units [g * U / G, (g + 1) * U / G).  G <= U: every run has a unit, so the
-// parts of an item are those of consecutive teams.
-// (One tile: two blocks a run, where there are so few, since its two streams take one each.)
-__device__ __forceinline__ int run_count(const TreeParams& p, int U) { return min(p.grid / p.team, p.two ? U : (U + 1) / 2); }
-__device__ __forceinline__ int run_begin(int g, int U, int G) { return g * (U / G) + g * (U % G) / G; }
-__device__ __forceinline__ int run_owner(int u, int U, int G) {  // the g with run_begin(g) <= u < run_begin(g + 1)
-  int g = min(G - 1, (int)((float)(u + 1) * G / U));
-  while (g > 0 && run_begin(g, U, G) > u) --g;
-  while (g + 1 < G && run_begin(g + 1, U, G) <= u) ++g;
-  return g;
-}
+// Units of a run: run g, of team g, is [g * n, (g + 1) * n) up to U, so the parts of an item are those
+// of consecutive teams.  (The longest run is what an even split would have, and the owner of a unit is
+// one division away.  One tile: at least two blocks a run, since its two streams take one each.)
+__device__ __forceinline__ int run_units(const TreeParams& p, int U) { return max((U + p.teams - 1) / p.teams, p.two ? 1 : 2); }
 
 // Walks the items of a run for tile group `member` of its team.
 struct Run {
@@ -177,11 +170,9 @@ struct Run {
   Item it;
 
   __device__ __forceinline__ void start(const TreeParams& p, const int* pre) {
-    int lo = 0, hi = kScan - 1;  // the last chunk that starts at or before u (so it has units)
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (pre[m] <= u) lo = m; else hi = m - 1;
-    }
+    int lo = -1;  // the last chunk that starts at or before u (so it has units)
+#pragma unroll
+    for (int i = 0; i < kScan; i += 32) lo += __popc(__ballot_sync(0xffffffffu, pre[i + (threadIdx.x & 31)] <= u));
     e = lo * ((num_entries(p) + kScan - 1) / kScan);
     first = pre[lo];
     x = make_entry(p, e, false);
@@ -514,17 +505,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
-  if (blockIdx.x == 0 && threadIdx.x <= kScan) p.table[threadIdx.x] = sh.pre[threadIdx.x];  // for the join
-  const int U = sh.pre[kScan];
-  const int G = run_count(p, U), team = (int)blockIdx.x / p.team;
-  if (team >= G) {  // (the whole CTA)
+  if (blockIdx.x == 0 && threadIdx.x <= kScan && num_entries(p) > kJoinThreads) p.table[threadIdx.x] = sh.pre[threadIdx.x];
+  const int U = sh.pre[kScan], n = run_units(p, U);
+  const int team = p.team == 1 ? (int)blockIdx.x : (int)blockIdx.x / p.team;
+  if (team >= p.teams || team * n >= U) {  // (the whole CTA)
     if (warp == 11) tmem_dealloc(tmem, 512);
     return;
   }
   Run run;
-  run.u = run_begin(team, U, G);
-  run.u1 = run_begin(team + 1, U, G);
-  run.member = (int)blockIdx.x % p.team;
+  run.u = team * n;
+  run.u1 = min(U, run.u + n);
+  run.member = (int)blockIdx.x - team * p.team;
   const int u0 = run.u;
   run.start(p, sh.pre);
 
@@ -933,50 +924,78 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // parts have them.  Few items have many parts each (38 at batch 1 with 4 KV heads): GROUPS = 4
 // groups of threads share them and meet in shared memory, a piece per thread.  Many items have
 // fewer than nine: GROUPS = 1, and four pieces per thread where that still leaves every SM its blocks.
-constexpr int kJoinThreads = 256;
+// What a block joins is known before the parts are there: it adds up a work list of up to 256 entries
+// itself while it waits for them (the first kernel's sums, read afterwards, cost 2 us of the 16 that 8 nodes
+// at 2K of one sequence take).
 
 template <int HD, int GROUPS, int PIECES>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
   constexpr int kSide = kJoinThreads / GROUPS, kN = PIECES;
   __shared__ float4 s_o[GROUPS][kSide];
   __shared__ float2 s_ml[GROUPS][kSide];
+  __shared__ int s_units[2][kJoinThreads / 32];
   const int tiles = p.two ? 2 : 1, rows = p.npt * p.gs;
   int i = blockIdx.x;
-  const int tile = i % tiles;
-  i /= tiles;
+  const int tile = p.two ? i & 1 : 0;
+  i = p.two ? i >> 1 : i;
   const int tp = i % p.ntp;
   i /= p.ntp;
   const int kvh = i % p.c.n_kv_heads, b = i / p.c.n_kv_heads;
   const int group = threadIdx.x / kSide, side = threadIdx.x % kSide;
-  const int member = tp % p.team, e = b * ((p.ntp + p.team - 1) / p.team) + tp / p.team;
+  const int member = tp % p.team, e = b * p.groups + tp / p.team, E = num_entries(p);
   // (the inputs of the work list are older than the kernel before this one)
   const Entry x = make_entry(p, e, false);
   const int end = group_end(p, x.s, tp), nblk = (end - x.kstart + kBlk - 1) / kBlk;
-  const int chunk = (num_entries(p) + kScan - 1) / kScan;
-  int g0 = kvh * x.units;
-  for (int y = e / chunk * chunk; y < e; ++y) g0 += make_entry(p, y, false).units * p.c.n_kv_heads;
-  pdl_wait();
-  pdl_trigger();
-  if (end == 0) return;
-  const int U = op_ld(p.table + kScan);
-  if (U <= 0) return;
-  g0 += op_ld(p.table + e / chunk);
-  const int G = run_count(p, U);
-  const int r0 = run_owner(g0 + p.pad, U, G), r1 = run_owner(g0 + p.pad + nblk - 1, U, G);
-  if (r0 == r1) return;  // written whole
-  // slot 0 holds the item that a run starts in: every part but, maybe, the first
-  const int slot0 = run_begin(r0, U, G) >= g0 ? 0 : 1;
-  auto part_of = [&](int r) -> long long { return (((long long)r * p.team + member) * 2 + (r == r0 ? slot0 : 0)) * tiles + tile; };
   int row[kN], c4[kN];
   bool live[kN];
-  float m[kN], l[kN];
-  float4 o[kN];
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     const int at = (blockIdx.y * kN + n) * kSide + side;
     c4[n] = at / rows;
     row[n] = at - c4[n] * rows;
     live[n] = c4[n] < HD / 4 && tp * nodes_per_group(p) + tile * p.npt + row[n] / p.gs < x.s.cnt;
+  }
+  int U = 0, before = 0;  // units of the list, and of the entries before this one
+  if (E <= kJoinThreads) {
+    if (threadIdx.x < E) U = make_entry(p, (int)threadIdx.x, false).units * p.c.n_kv_heads;
+    if (threadIdx.x < e) before = U;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      U += __shfl_xor_sync(0xffffffffu, U, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+      s_units[0][threadIdx.x >> 5] = U;
+      s_units[1][threadIdx.x >> 5] = before;
+    }
+    __syncthreads();
+    U = before = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      U += s_units[0][w];
+      before += s_units[1][w];
+    }
+    pdl_wait();
+    pdl_trigger();
+  } else {
+    const int chunk = (E + kScan - 1) / kScan;
+    for (int y = e / chunk * chunk; y < e; ++y) before += make_entry(p, y, false).units * p.c.n_kv_heads;
+    pdl_wait();
+    pdl_trigger();
+    U = op_ld(p.table + kScan);
+    before += op_ld(p.table + e / chunk);
+  }
+  if (end == 0 || U <= 0) return;
+  const int n_run = run_units(p, U), g0 = before + kvh * x.units;
+  const int r0 = (g0 + p.pad) / n_run, r1 = (g0 + p.pad + nblk - 1) / n_run;
+  if (r0 == r1) return;  // written whole
+  // slot 0 holds the item that a run starts in: every part but, maybe, the first
+  const int slot0 = r0 * n_run >= g0 ? 0 : 1;
+  auto part_of = [&](int r) -> long long { return (((long long)r * p.team + member) * 2 + (r == r0 ? slot0 : 0)) * tiles + tile; };
+  float m[kN], l[kN];
+  float4 o[kN];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
     m[n] = -INFINITY;
     l[n] = 0.f;
     o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
