@@ -43,8 +43,6 @@ constexpr int kMaxExpStages = 9;
 constexpr int kChunk = 32;           // rows of an epilogue step
 // per epilogue warp a chunk's results; per pair of warps two buffers of gate / up values in fp32
 constexpr int kExpSmem = 1024 + kRingBytes + 4 * kChunk * 32 * 2 + 2 * 2 * kChunk * 32 * 4;
-static_assert(kExpSmem + 2304 <= 232448, "exceeds the 227 KB per-block shared memory limit");
-
 struct ExpTile {
   int e, r0, nr;   // expert, first row, rows (<= 256)
   int w0;          // first output
@@ -55,9 +53,12 @@ struct ExpShared {
   int abort;
   int most;                     // rows of the largest expert
   int pre[kOpMaxExperts + 1];   // prefix sums of the experts' row tiles
+  int2 rows[kOpMaxExperts];     // the experts' rows [x, y)
   int warp_sums[(kExpThreads + kGatherThreads) / 32];
   unsigned long long bars[3 * kMaxExpStages + 4];
 };
+
+static_assert(kExpSmem + sizeof(ExpShared) <= 232448, "exceeds the 227 KB per-block shared memory limit");
 
 // ---- cluster primitives
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -142,24 +143,23 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
                : "memory");
 }
 
-__device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, bool record, int& lo, int& hi) {
+__device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& lo, int& hi) {
   const int a = op_ld(p.a.offsets + e), b = op_ld(p.a.offsets + e + 1);
   lo = min(max(a, 0), p.a.n_rows);
   hi = min(max(b, lo), p.a.n_rows);
-  if (record && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
+  if (blockIdx.x == 0 && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
 }
 
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
-  if (threadIdx.x == 0) sh.pre[0] = sh.most = 0;
-  __syncthreads();
   int carry = 0;
   for (int base = 0; base < E; base += nt) {
     const int e = base + (int)threadIdx.x;
     int x = 0;
     if (e < E) {
       int lo, hi;
-      expert_rows(p, e, blockIdx.x == 0, lo, hi);
+      expert_rows(p, e, lo, hi);
+      sh.rows[e] = make_int2(lo, hi);
       x = (hi - lo + kTileR - 1) / kTileR;
       if (hi > lo) atomicMax(&sh.most, hi - lo);
     }
@@ -184,19 +184,17 @@ __device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& s
   const int t = k * ((int)gridDim.x / 2) + (int)blockIdx.x / 2;
   if (t >= tiles) return false;
   const int rt = t / wblocks;
-  int lo = 0, hi = p.a.n_experts - 1;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (sh.pre[m] <= rt) lo = m; else hi = m - 1;
-  }
+  int lo = 0;
+#pragma unroll
+  for (int step = kOpMaxExperts / 2; step > 0; step >>= 1)
+    if (lo + step < p.a.n_experts && sh.pre[lo + step] <= rt) lo += step;
   x.e = lo;
   x.w0 = (t - rt * wblocks) * wstep;
-  int a, b;
-  expert_rows(p, lo, false, a, b);
   // the expert's rows in equal tiles
-  const int mine = sh.pre[lo + 1] - sh.pre[lo], per = (b - a + mine - 1) / mine;
-  x.r0 = a + (rt - sh.pre[lo]) * per;
-  x.nr = min(per, b - x.r0);
+  const int2 r = sh.rows[lo];
+  const int mine = sh.pre[lo + 1] - sh.pre[lo], per = mine == 1 ? r.y - r.x : (r.y - r.x + mine - 1) / mine;
+  x.r0 = r.x + (rt - sh.pre[lo]) * per;
+  x.nr = min(per, r.y - x.r0);
   return true;
 }
 
@@ -222,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   auto gathered = [&](uint32_t s) { return bars + 8 * (2 * kMaxExpStages + 4 + s); }; // this CTA's named rows
 
   if (threadIdx.x == 0) {
-    sh.abort = 0;
+    sh.abort = sh.pre[0] = sh.most = 0;
     for (int s = 0; s < kMaxExpStages; ++s) {
       mbar_init(full(s), p.a.rows ? 2 : 1);  // the copies; the second CTA's named rows
       mbar_init(empty(s), 1);
@@ -240,13 +238,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // the barriers of both CTAs are there
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
   scan_experts(p, sh);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // the barriers of both CTAs are there
-  tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;

@@ -62,6 +62,8 @@ def commit_ref(k, v, table, lens, accepted):
     (2, 2, 32, [15, 16, 0], [[0, 2, 5], [1, -1, 4], [-1, 0, 0]]),           # ends at the first negative entry
     (3, 3, 64, [30, 1], [[5, 3, 4, 0], [2, 2, 2, 2]]),                      # any order, the same node twice
     (48, 4, 128, [100, 7, 3, 0, 1, 2, 5, 9], [[0, 3, 7, 12, 40]] * 8),
+    (38, 6, 32, [100, 7, 3, 0, 1, 2, 5, 9], [[0, 3, 7, 12, 40]] * 8),       # blocks of 4 heads and of 2
+    (48, 5, 64, [100, 7, 3, 0, 1, 2, 5, 9], [[9, -1, 2]] * 8),
     (1, 1, 128, [9], [list(range(1, 513))]),                                # the longest path, a shift by one
     (1, 1, 32, [9], [list(range(511, -1, -1))]),
 ])
