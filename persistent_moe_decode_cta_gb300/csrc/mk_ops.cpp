@@ -106,7 +106,7 @@ int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   p.ntp = (a->n_nodes + per - 1) / per;
   p.team = p.ntp <= 8 ? p.ntp : 1;
   p.words = (a->n_nodes + 31) / 32;
-  const double units = (double)c->batch * c->n_kv_heads * p.ntp * ((double)c->max_pages / 8 + 8);
+  const double units = (double)c->batch * c->n_kv_heads * p.ntp * ((double)c->max_pages / 8 + 2 + kItemUnits);
   if (units >= 1073741824.0 || (double)c->batch * c->n_kv_heads * p.ntp * 8 >= 1073741824.0)
     return op_fail(MK_ERR_UNSUPPORTED, "batch x heads x nodes x keys exceeds 2^30 work units");
   // (every CTA adds up the work list, 128 entries at a time)
@@ -116,10 +116,6 @@ int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   const int rc = num_sms(&p.grid);
   if (rc) return rc;
   p.teams = std::max(1, p.grid / p.team);
-  // Where runs hold several items, what an item costs beside its blocks (queries, masked blocks, results)
-  // counts too: the short items of a prompt's first nodes are many to a run.
-  const long long items = (long long)c->batch * c->n_kv_heads * p.ntp / p.team;
-  p.pad = items > p.teams ? (p.two ? 6 : 3) : 0;
   return MK_OK;
 }
 

@@ -48,6 +48,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 constexpr int kOpPage = 16;            // tokens per cache page
 constexpr int kOpMaxBatch = 65535;     // sequences of one call
 constexpr int kOpMaxEntries = 65536;   // of the attention's work list: sequences x groups of nodes
+constexpr int kItemUnits = 6;          // of the attention's work list: what an item counts for beside its key blocks
 constexpr int kOpMaxExperts = 256;     // experts of one call (as mk_create)
 constexpr int kOpMaxAccept = 512;      // accepted nodes per sequence (staged in shared memory)
 constexpr int kOpMaxHalf = 64;         // head_dim / 2 at most
@@ -68,7 +69,6 @@ struct TreeParams {
   int npt;         // nodes per 128-row tile
   int two;         // 1: a CTA works on two row tiles at once; 0: on one, with two key streams
   int ntp;         // row-tile groups per (sequence, KV head)
-  int pad;         // units that an item counts for beside its key blocks
   int team;        // tile groups that walk a run of keys together
   int teams;       // such teams in the grid
   int groups;      // entries of the work list per sequence

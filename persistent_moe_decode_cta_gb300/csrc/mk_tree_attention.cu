@@ -21,7 +21,7 @@
 // does not cover the 60 to 75 cycles of each wait).  TWO = false is bound by the copies: a
 // stream takes a block in two halves with an S/P buffer each, and S of a block is computed as soon
 // as its K is there, whatever the softmax is at, so that the slots of the ring are free again early
-// (with whole blocks: 122 us instead of 106 for 16 nodes at 32K of 8 sequences).
+// (16 nodes at 32K of 8 sequences: 106 us, with whole blocks 122).
 //
 // Keys that a row does not see get a score of -infinity.  Blocks with such keys have their V
 // cleaned in shared memory by two further warps (rows past the end and values that are not
@@ -29,7 +29,12 @@
 // loads at the end, for the rows that do see it.
 //
 // The work is a list of units, one per (sequence, tile group, KV head, key block), cut into
-// equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  (Up
+// equal runs, one per CTA: ragged batches and single long sequences fill all SMs alike.  An item, the
+// keys of one KV head for one tile group, counts for six units more: a run that starts one pays for its
+// queries, the empty pipeline and one more result.  (Without them the 31 of 152 CTAs whose run holds a
+// border of 8 sequences' items end 8 us after the others: 58.4 us against 51.3 for 16 nodes of 8 ragged
+// sequences, 18.6 against 15.7 for one node at 8K, 332 against 152 for a prompt of 4096, whose first items
+// are short.  3 to 8 are within 3% of one another.)  (Up
 // to 8 tile groups form a team instead: each run is walked by one CTA per group at the same
 // time, so that the keys come from HBM once and from L2 for the others.)  A run that covers
 // only part of an item's keys leaves (O, m, sum) in the workspace and a second kernel joins
@@ -71,7 +76,7 @@ struct Item {          // one (sequence, KV head, tile group) and the blocks of 
   int kstart, end;     // its keys: [kstart, end)
   int nblk;            // their blocks
   int ja, jb;          // blocks of this run
-  int unit0;           // global index of its first unit (of p.pad without a block)
+  int unit0;           // global index of its first unit
 };
 
 struct SeqShape {
@@ -100,7 +105,7 @@ struct Entry {
   int b, tp;           // first tile group
   SeqShape s;
   int kstart, nblk;    // blocks of the longest
-  int units;           // per KV head: the blocks, and p.pad for what an item costs beside them
+  int units;           // per KV head: the blocks and kItemUnits
 };
 
 // end of the keys of tile group tp (0 if it has no nodes)
@@ -124,7 +129,7 @@ __device__ __forceinline__ Entry make_entry(const TreeParams& p, int e, bool rec
     x.kstart = max(0, pos - p.a.window + 1) & ~(kOpPage - 1);
   }
   x.nblk = (end - x.kstart + kBlk - 1) / kBlk;
-  x.units = x.nblk + p.pad;
+  x.units = x.nblk + kItemUnits;
   return x;
 }
 
@@ -196,8 +201,8 @@ struct Run {
       it.nblk = max(0, it.end - it.kstart + kBlk - 1) / kBlk;
       const int start = u - it.unit0, stop = min(x.units, start + (u1 - u));
       u = it.unit0 + stop;
-      it.ja = max(0, start - p.pad);
-      it.jb = min(stop - p.pad, it.nblk);
+      it.ja = max(0, start - kItemUnits);
+      it.jb = min(stop - kItemUnits, it.nblk);
       if (it.ja < it.jb) return true;
     }
     return false;
@@ -987,7 +992,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
   if (end == 0 || U <= 0) return;
   const int n_run = run_units(p, U), g0 = before + kvh * x.units;
-  const int r0 = (g0 + p.pad) / n_run, r1 = (g0 + p.pad + nblk - 1) / n_run;
+  const int r0 = (g0 + kItemUnits) / n_run, r1 = (g0 + kItemUnits + nblk - 1) / n_run;
   if (r0 == r1) return;  // written whole
   // slot 0 holds the item that a run starts in: every part but, maybe, the first
   const int slot0 = r0 * n_run >= g0 ? 0 : 1;
