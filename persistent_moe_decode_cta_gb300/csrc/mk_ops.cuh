@@ -81,6 +81,12 @@ __device__ __forceinline__ void op_cp16(uint32_t dst, const void* src, int bytes
 __device__ __forceinline__ void op_cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void op_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all of this thread's groups but the last N have landed
+template <int N>
+__device__ __forceinline__ void op_cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void op_cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Shared-memory matrix descriptor of a swizzled operand (span 128 or 64 bytes).

@@ -59,6 +59,13 @@ def test_lengths(n):
     check((32, 4, 128), [0, 1, 16, 4097], n)
 
 
+@pytest.mark.parametrize("heads,lens,n", [((32, 4, 128), [3, 40], 1001), ((16, 4, 64), [0], 6000), ((8, 2, 32), [5] * 1300, 5),
+                                          ((3, 3, 128), [1] * 2500, 1)])
+def test_many_tokens_behind_one_another(heads, lens, n):
+    counts = [n - (i % 3 if n > 1 else 0) for i in range(len(lens))]
+    check(heads, lens, n, counts=counts if n < 100 else None, in_place=n > 2000, packed=n <= 2000)
+
+
 def test_no_norm_unpacked_in_place():
     check((16, 4, 64), [3, 40], 9, norm=False, packed=False, in_place=True)
     check((32, 4, 128), [3, 40], 9, in_place=True)
