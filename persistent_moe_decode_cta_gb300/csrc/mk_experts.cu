@@ -48,6 +48,8 @@ struct ExpTile {
   int w0;          // first output
 };
 
+constexpr int kTileNotes = 16;  // more than the ring holds tiles
+
 struct ExpShared {
   uint32_t tmem;
   int abort;
@@ -55,6 +57,7 @@ struct ExpShared {
   int pre[kOpMaxExperts + 1];   // prefix sums of the experts' row tiles
   int2 rows[kOpMaxExperts];     // the experts' rows [x, y)
   int warp_sums[(kExpThreads + kGatherThreads) / 32];
+  int rows_of[kTileNotes];      // rows of the tiles under way
   unsigned long long bars[3 * kMaxExpStages + 4];
 };
 
@@ -254,25 +257,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   const uint32_t stage_bytes = kBytesW + room * kTileK * 2, stages = room == 32 ? 9 : room == 64 ? 8 : 6;
   auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, x)); };
   auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, x); };  // (one thread)
+  const int clusters = (int)gridDim.x / 2, mine = (tiles - (int)blockIdx.x / 2 + clusters - 1) / clusters;  // tiles of this cluster
   ExpTile x;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    uint32_t fill = 0;
-    Ring at;
-    bool ok = true;
-    const int half = GLU ? kTileW / 2 : kTileW;  // weight rows per copy
-    for (int t = 0; ok && tile(t, x); ++t) {
-      const int e = (int)uniform(x.e), nr = (int)uniform(x.nr);
-      const int w = (int)uniform(x.w0) + (int)rank * half, n2 = (nr + 31) / 32 * 16;  // rows of this CTA
-      const int r = (int)uniform(x.r0) + (int)rank * n2;
-      const uint32_t xrows = p.a.rows ? 0 : n2 <= kBoxR ? kBoxR : n2 <= 2 * kBoxR ? 2 * kBoxR : kTileR / 2;
-      const uint32_t bytes = 2 * (kBytesW + xrows * (kTileK * 2));  // of both CTAs
-      for (int ks = 0; ks < ksteps; ++ks, ++fill, at.advance(stages)) {
-        const uint32_t s = at.slot;
-        if (!(ok = op_wait(empty(s), at.phase ^ 1, abort, p.a.status, 1))) break;
-        if (elect_one()) {
-          const uint32_t st = base + s * stage_bytes, bar = map_leader(full(s));
+    if (elect_one()) {
+      Ring at;
+      bool ok = true;
+      const int half = GLU ? kTileW / 2 : kTileW;  // weight rows per copy
+      const uint32_t lead = map_leader(bars);
+      // (the next tile is looked up while this one's stages are under way)
+      bool more = tile1(0, x);
+      for (int t = 0; ok && more; ++t) {
+        const int e = x.e, n2 = (x.nr + 31) / 32 * 16;  // rows of this CTA
+        const int w = x.w0 + (int)rank * half, r = x.r0 + (int)rank * n2;
+        const uint32_t xrows = p.a.rows ? 0 : n2 <= kBoxR ? kBoxR : n2 <= 2 * kBoxR ? 2 * kBoxR : kTileR / 2;
+        const uint32_t bytes = 2 * (kBytesW + xrows * (kTileK * 2));  // of both CTAs
+        sh.rows_of[t % kTileNotes] = x.nr;  // for the products, which wait for these copies
+        for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
+          const uint32_t s = at.slot;
+          if (!(ok = op_wait1(empty(s), at.phase ^ 1, abort, p.a.status, 1))) break;
+          const uint32_t st = base + s * stage_bytes, bar = lead + 8 * s;
           if (rank == 0) mbar_expect_tx(full(s), bytes);
           tma_pair_3d(st, &tw, ks * kTileK, w, e, bar);
           if (GLU) tma_pair_3d(st + kBytesW / 2, &tu, ks * kTileK, w, e, bar);
@@ -282,10 +288,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
             tma_pair_2d(st + kBytesW, &tx, ks * kTileK, r, bar);
             if (xrows > kBoxR) tma_pair_2d(st + kBytesW + kBoxR * kTileK * 2, &tx, ks * kTileK, r + kBoxR, bar);
           }
+          if (ks == 0) more = tile1(t + 1, x);
         }
-        __syncwarp();
       }
     }
+    __syncwarp();
     // an abandoned run leaves copies in flight: give them time to land
     if (*abort) {
       const uint64_t s0 = gtime();
@@ -299,28 +306,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     constexpr int kRows = kTileR / 2 / 16;
     Ring at;
     bool ok = true;
-    for (int t = 0; ok && tile(t, x); ++t) {
-      const int n2 = (x.nr + 31) / 32 * 16, first = (int)rank * n2, mine = min(n2, x.nr - first);  // (may be < 0)
+    // A tile's row numbers are read a tile ahead: the ring covers 2600 cycles, less than the numbers and
+    // the first rows take one after the other (4096 tokens: 193 us, 2000 to 7000 cycles of every 21000 lost).
+    int first, count, names[kRows];
+    auto look_up = [&](int t) -> bool {
+      if (!tile(t, x)) return false;
+      const int n2 = (x.nr + 31) / 32 * 16;
+      first = x.r0 + (int)rank * n2;
+      count = min(n2, x.nr - (int)rank * n2);  // (may be < 0)
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) names[j] = row0 + 16 * j < count ? op_ld(p.a.rows + first + row0 + 16 * j) : 0;
+      return true;
+    };
+    bool more = look_up(0);
+    for (int t = 0; ok && more; ++t) {
       const uint16_t* src[kRows];
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
-        const int i = row0 + 16 * j;
-        int r = 0;
-        if (i < mine) {
-          const int s = op_ld(p.a.rows + x.r0 + first + i);
-          r = min(max(s, 0), p.a.n_x - 1);
-          if (r != s && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, x.r0 + first + i, s);
-        }
+        const int r = min(max(names[j], 0), p.a.n_x - 1);
+        if (r != names[j] && x.w0 == 0) op_error(p.a.status, MK_ERR_INVALID, x.e, first + row0 + 16 * j, names[j]);
         src[j] = static_cast<const uint16_t*>(p.a.x) + r * p.a.x_stride + 8 * chunk;
       }
+      const int rows_now = count;
       for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
         if (!(ok = op_wait(empty(at.slot), at.phase ^ 1, abort, p.a.status, 6))) break;
         const uint32_t dst = base + at.slot * stage_bytes + kBytesW + row0 * (kTileK * 2) + swz;
         const int bytes = ks * kTileK + 8 * chunk < p.a.k ? 16 : 0;  // (0: zeros)
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
-          if (row0 + 16 * j < mine) op_cp16(dst + j * 16 * kTileK * 2, bytes ? src[j] + ks * kTileK : src[j], bytes);
+          if (row0 + 16 * j < rows_now) op_cp16(dst + j * 16 * kTileK * 2, bytes ? src[j] + ks * kTileK : src[j], bytes);
         op_cp_arrive(gathered(at.slot));
+        if (ks == 0) more = look_up(t + 1);
       }
     }
     op_cp_wait_all();
@@ -331,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       if (p.a.rows && elect_one()) {
         Ring at;
         bool ok = true;
-        for (int t = 0; ok && tile1(t, x); ++t)
+        for (int t = 0; ok && t < mine; ++t)
           for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
             if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 7))) break;
             fence_proxy_async_smem();
@@ -343,8 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       Ring at;
       const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, rows
       bool ok = true;
-      for (int t = 0; ok && tile1(t, x); ++t, ++nt) {
-        const uint32_t idesc = umma_idesc_bf16(2 * kTileW, (x.nr + 31) / 32 * 32);
+      for (; ok && (int)nt < mine; ++nt) {
+        uint32_t idesc = 0;
         const uint32_t a = nt & 1, acc = tmem + kTileR * a;
         if (!(ok = wait_cluster1(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
         for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
@@ -354,6 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
             fence_proxy_async_smem();
           }
           tc_fence_after();
+          if (ks == 0) idesc = umma_idesc_bf16(2 * kTileW, (*(volatile int*)&sh.rows_of[nt % kTileNotes] + 31) / 32 * 32);
           const uint64_t d = d0 + at.slot * (stage_bytes / 16);
 #pragma unroll
           for (int kk = 0; kk < kTileK / 16; ++kk)
