@@ -15,7 +15,8 @@ struct PagePairs {
   int32_t src[N], dst[N];
 };
 
-// One block per (pair, layer, K or V, 16 KB of the page).
+// One block per (pair, layer, K or V, 16 KB of the page).  HBM bounds it: 512 pages of 48 layers (1.6 GB
+// moved) 231 us, 7.0 TB/s; 8 pages 4.2 us.
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ PagePairs<N> pairs, uint4* k, uint4* v,
                                                                   long long layer_vecs, int page_vecs, int parts) {
@@ -53,7 +54,8 @@ constexpr int kCommitThreads = 128;
 
 // One block per (sequence, KV head, layer, K or V).  The accepted rows of its slice are
 // staged in shared memory, all of them before the first is written back, so that the path
-// may name the nodes in any order.
+// may name the nodes in any order.  A chain of loads (path, page table, rows) bounds it: 8 sequences of 48
+// layers 6.7 us.
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_constant__ CommitParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int s_count;
