@@ -186,6 +186,12 @@ struct Run {
     first = pre[lo];
     x = make_entry(p, e, false);
   }
+  // (up to 32 entries: lane i knows the units before entry i)
+  __device__ __forceinline__ void start_short(const TreeParams& p, int before) {
+    e = __popc(__ballot_sync(0xffffffffu, before <= u)) - 1;
+    first = __shfl_sync(0xffffffffu, before, e);
+    x = make_entry(p, e, false);
+  }
   // The next item with blocks of this group in the run.  (One copy for all roles: an inlined
   // one per role, rarely run, costs thousands of cycles of instruction fetches each time.)
   __device__ __noinline__ bool next(const TreeParams& p) {
@@ -508,14 +514,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     fence_proxy_async_smem();
   }
   tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(sh.tmem);
   // (the join, which reads the work list's inputs at once, starts only when they are final)
   pdl_wait();
   pdl_trigger();
-  scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
-  tc_fence_after();
-  const uint32_t tmem = uniform(sh.tmem);
-  if (blockIdx.x == 0 && threadIdx.x <= kScan && num_entries(p) > kJoinThreads) p.table[threadIdx.x] = sh.pre[threadIdx.x];
-  const int U = sh.pre[kScan], n = run_units(p, U);
+  // The units before each entry.  Up to 32 entries every warp adds them up by itself, without a barrier.
+  const int E = num_entries(p);
+  int U, before = 0;
+  if (E <= 32) {
+    int own = 0;
+    if (lane < E) own = make_entry(p, lane, blockIdx.x == 0 && warp == 0).units * p.c.n_kv_heads;
+    U = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, U, o);
+      if (lane >= o) U += y;
+    }
+    before = U - own;
+    U = __shfl_sync(0xffffffffu, U, 31);
+  } else {
+    scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
+    if (blockIdx.x == 0 && threadIdx.x <= kScan && E > kJoinThreads) p.table[threadIdx.x] = sh.pre[threadIdx.x];
+    U = sh.pre[kScan];
+  }
+  const int n = run_units(p, U);
   const int team = p.team == 1 ? (int)blockIdx.x : (int)blockIdx.x / p.team;
   if (team >= p.teams || team * n >= U) {  // (the whole CTA)
     if (warp == 11) tmem_dealloc(tmem, 512);
@@ -525,8 +549,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   run.u = team * n;
   run.u1 = min(U, run.u + n);
   run.member = (int)blockIdx.x - team * p.team;
+  if (E <= 32)
+    run.start_short(p, before);
+  else
+    run.start(p, sh.pre);
   const int u0 = run.u;
-  run.start(p, sh.pre);
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax streams
