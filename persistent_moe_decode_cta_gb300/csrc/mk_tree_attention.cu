@@ -302,8 +302,7 @@ struct TreeShared {
   uint32_t tmem;
   int abort;
   int bad_v;             // a masked block held a V that is not finite
-  int pre[kScan + 1];
-  int warp_sums[kScan / 32];
+  Run runs[4];           // of the copy, product and cleaning warps
   float2 ml[2][kBlk];    // the streams' (m, sum) for the merge
   unsigned long long bars[3 * kMaxStages + 17];
 };
@@ -522,6 +521,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   pdl_trigger();
   // The units before each entry.  Up to 32 entries every warp adds them up by itself, without a barrier.
   const int E = num_entries(p);
+  int* const pre = reinterpret_cast<int*>(raw);  // (where the queries go afterwards)
   int U, before = 0;
   if (E <= 32) {
     int own = 0;
@@ -535,9 +535,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     before = U - own;
     U = __shfl_sync(0xffffffffu, U, 31);
   } else {
-    scan_units(p, sh.pre, sh.warp_sums, blockIdx.x == 0);
-    if (blockIdx.x == 0 && threadIdx.x <= kScan && E > kJoinThreads) p.table[threadIdx.x] = sh.pre[threadIdx.x];
-    U = sh.pre[kScan];
+    scan_units(p, pre, pre + kScan + 1, blockIdx.x == 0);
+    if (blockIdx.x == 0 && threadIdx.x <= kScan && E > kJoinThreads) p.table[threadIdx.x] = pre[threadIdx.x];
+    U = pre[kScan];
   }
   const int n = run_units(p, U);
   const int team = p.team == 1 ? (int)blockIdx.x : (int)blockIdx.x / p.team;
@@ -545,15 +545,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp == 11) tmem_dealloc(tmem, 512);
     return;
   }
-  Run run;
-  run.u = team * n;
-  run.u1 = min(U, run.u + n);
-  run.member = (int)blockIdx.x - team * p.team;
-  if (E <= 32)
-    run.start_short(p, before);
-  else
-    run.start(p, sh.pre);
-  const int u0 = run.u;
+  Run begin;
+  begin.u = team * n;
+  begin.u1 = min(U, begin.u + n);
+  begin.member = (int)blockIdx.x - team * p.team;
+  if (E <= 32) {
+    begin.start_short(p, before);
+  } else {
+    begin.start(p, pre);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+  const int u0 = begin.u;
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax streams
@@ -570,6 +573,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       return op_wait(bars.meet(), nm++ & 1, abort, p.a.status, 7);
     };
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    Run run = begin;
     while (ok && uniform(run.next(p))) {
       const Item& it = run.it;
       const int nb = (int)uniform(it.jb - it.ja);
@@ -713,6 +717,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!TWO && !(ok = meet())) break;
     }
   } else {
+    // (a walk in local memory costs 2000 cycles: what shared memory leaves of L1 does not hold it)
+    Run& run = sh.runs[warp - 8];
+    if (lane == 0) run = begin;
+    __syncwarp();
+    auto next = [&]() -> bool {
+      bool more = false;
+      __syncwarp();
+      if (lane == 0) more = run.next(p);
+      __syncwarp();
+      return uniform(more);
+    };
     if (warp == 8) {
       // ---------------------------------------------------------------- producer
       // lane i < 8 looks up page i of a block; the table is read two blocks ahead and not looked at
@@ -724,8 +739,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int at = (it.kstart + j * kBlk) / kOpPage + lane;
         return lane < 8 && at * kOpPage < it.end ? op_ld(p.c.page_table + (long long)it.b * p.c.max_pages + at) : 0;
       };
-      while (ok && uniform(run.next(p))) {
-        const Item& it = run.it;
+      while (ok && next()) {
+        const Item it = run.it;
         const int blocks = (int)uniform(it.jb - it.ja);
         const uint32_t rows = p.npt * p.gs;
         int page1 = look_up(it, it.ja), page2 = look_up(it, it.ja + 1);
@@ -924,8 +939,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_arrive(bars.pready(st, 0));
         return true;
       };
-      while (ok && uniform(run.next(p))) {
-        const Item& it = run.it;
+      while (ok && next()) {
+        const Item it = run.it;
         const int nb = (int)uniform(it.jb - it.ja);
         for (int blk = 0; ok && blk < nb; ++blk) {
           const int k0 = it.kstart + (it.ja + blk) * kBlk;
