@@ -86,6 +86,12 @@ def test_all_rows_to_one_expert_and_none():
     check([0, 0], 128, 128, pad=4)
 
 
+@pytest.mark.parametrize("glu,gather,rows", [(False, None, 150), (True, 77, 150), (False, 500, 6)])
+def test_many_tiles_of_few_columns(glu, gather, rows):
+    """A cluster has more tiles under way than the ring has stages (64 columns: one stage a tile)."""
+    check([rows + i % 7 for i in range(64)], 4096 + 40, 64, glu=glu, gather=gather)
+
+
 def test_pages_scale_shapes():
     g = torch.Generator().manual_seed(3)
     sizes = torch.bincount(torch.randint(0, 128, (1024,), generator=g), minlength=128).tolist()
