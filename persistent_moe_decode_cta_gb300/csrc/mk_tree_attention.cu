@@ -40,9 +40,9 @@
 // only part of an item's keys leaves (O, m, sum) in the workspace and a second kernel joins
 // the parts in order of their keys; at most a run's first and last item are such.
 //
-// Measured, 32 query heads and 4 KV heads of 128: 16 nodes at 32K of 8 sequences 97 us (5.6 TB/s), 64 nodes
-// 194 us (1.42 PFLOP/s), 2001 nodes of a chunk at 8K 221 us (1.37 PFLOP/s), one node at 8K of one sequence
-// 15.9 us, 8 nodes at 2K of the small model 11.7 us (latencies).
+// Measured, 32 query heads and 4 KV heads of 128: 16 nodes at 32K of 8 sequences 96 us (5.6 TB/s), 64 nodes
+// 196 us (1.41 PFLOP/s), 2001 nodes of a chunk at 8K 222 us (1.36 PFLOP/s), one node at 8K of one sequence
+// 15.0 us, 8 nodes at 2K of the small model 11.3 us (latencies).
 #include "mk_ops.cuh"
 
 #include <type_traits>
