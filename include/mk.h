@@ -490,9 +490,10 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
  * A row that sees no key (or only scores of -infinity) is 0.  Keys that a row does not see
  * do not reach it whatever they hold, NaN and infinities included.  fp32 scores, softmax
  * statistics and sums; the softmax weights are rounded to bf16 for the tensor cores.  The
- * sums have a fixed order: equal calls give equal bits.  n_q_heads / n_kv_heads <= 128;
- * batch times the groups of nodes (up to 8 groups count as one; a group has 2 * (128 / (n_q_heads /
- * n_kv_heads)) nodes) <= 65536.
+ * sums have a fixed order: equal calls give equal bits.
+ * MK_ERR_UNSUPPORTED: n_q_heads / n_kv_heads > 128; more than 65536 (sequence, group of nodes)
+ * pairs, where a group has 2 * (128 / (n_q_heads / n_kv_heads)) nodes and up to 8 groups of a
+ * sequence count as one; more than 2^30 (sequence, KV head, group, 128 keys) units.
  * Keys on a page outside [0, n_pages) are read from page 0 (MK_ERR_BAD_PAGE). */
 typedef struct mk_tree_args {
   const void* q;

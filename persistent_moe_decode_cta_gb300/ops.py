@@ -121,7 +121,6 @@ def qk_norm_rope(q, k, v, k_cache, v_cache, page_table, seq_lens, *, theta, q_ga
                                   counts, out, status)
 
 
-
 @_operator
 def tree_attention(q, k_cache, v_cache, page_table, seq_lens, *, mask=None, positions=None, counts=None, window=0,
                    scale=None, out=None, status=None):
@@ -133,7 +132,6 @@ def tree_attention(q, k_cache, v_cache, page_table, seq_lens, *, mask=None, posi
     `out` (not q); nodes from counts[b] on are left as they are."""
     return _native().tree_attention(q, k_cache, v_cache, page_table, seq_lens, mask, positions, counts, window, scale, out,
                                     status)
-
 
 
 def _page_ids(ids, name):
@@ -158,7 +156,6 @@ def copy_pages(k_cache, v_cache, src, dst):
     _native().copy_pages(k_cache, v_cache, _page_ids(src, "src"), _page_ids(dst, "dst"))
 
 
-
 @_operator
 def commit_nodes(k_cache, v_cache, page_table, seq_lens, accepted, *, out=None, status=None):
     """Keep the accepted path of a draft: in every layer of the pools [n_layers, ..] the K/V
@@ -166,7 +163,6 @@ def commit_nodes(k_cache, v_cache, page_table, seq_lens, accepted, *, out=None, 
     position seq_lens[b] + i.  Returns the new lengths, int32 [batch] (`out`, not
     seq_lens)."""
     return _native().commit_nodes(k_cache, v_cache, page_table, seq_lens, accepted, out, status)
-
 
 
 @_operator
