@@ -73,3 +73,54 @@ def test_captured_on_first_use():
     run = subprocess.run([sys.executable, "-c", FIRST.format(tests=here, root=os.path.dirname(here))], capture_output=True,
                          text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.split()[-1] == "equal", run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("heads,d,lens", [((8, 2, 32), 256, [5, 60, 700]), ((32, 4, 128), 512, [0, 3000])])
+def test_chain_of_dependent_calls(heads, d, lens):
+    """Each call reads what the one before it wrote, while their launches overlap: step by step with a
+    synchronisation behind every call, back to back, and captured, the bits are the same."""
+    hq, hkv, hd = heads
+    g = R.gen(11)
+    b, n = len(lens), 12
+    k, v, table, sl = R.cache(g, lens, 4 * n, hkv, hd, layers=2)
+    q, kn, vn = R.bf16(g, b, n, hq, hd), R.bf16(g, b, n, hkv, hd), R.bf16(g, b, n, hkv, hd)
+    w = R.bf16(g, 3, d, hq * hd, std=0.05)
+    back = R.bf16(g, 3, hq * hd, d, std=0.05)
+    offsets = torch.tensor([0, 7, 7, b * n], dtype=torch.int32, device="cuda")
+    acc = torch.tensor([[1, 3, 6, 7, -1]] * b, dtype=torch.int32, device="cuda")
+    k0, v0 = k.clone(), v.clone()
+    torch.cuda.synchronize()
+
+    def run(pause):
+        x, lengths = q, sl
+        for _ in range(3):
+            for layer in range(2):
+                x = ops.qk_norm_rope(x, kn, vn, k[layer], v[layer], table, lengths, theta=1e4)
+                pause()
+                x = ops.tree_attention(x, k[layer], v[layer], table, lengths)
+                pause()
+                h = ops.expert_product(x.view(b * n, hq * hd), w, offsets)
+                pause()
+                x = ops.expert_product(h, back, offsets).view(b, n, hq, hd)
+                pause()
+            lengths = ops.commit_nodes(k, v, table, lengths, acc)
+            pause()
+        return x, lengths
+
+    def reset():
+        k.copy_(k0), v.copy_(v0)
+
+    x, lengths = run(torch.cuda.synchronize)
+    want = [t.clone() for t in (x, lengths, k, v)]
+    assert torch.isfinite(x).all() and (lengths == sl + 12).all()
+    for _ in range(10):
+        reset()
+        x, lengths = run(lambda: None)
+        assert all(torch.equal(a, c) for a, c in zip(want, (x, lengths, k, v)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x, lengths = run(lambda: None)
+    for _ in range(10):
+        reset()
+        graph.replay()
+        assert all(torch.equal(a, c) for a, c in zip(want, (x, lengths, k, v)))
