@@ -516,7 +516,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
-  // (the join, which reads the work list's inputs at once, starts only when they are final)
   pdl_wait();
   pdl_trigger();
   // The units before each entry.  Up to 32 entries every warp adds them up by itself, without a barrier.
@@ -975,9 +974,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // parts have them.  Few items have many parts each (38 at batch 1 with 4 KV heads): GROUPS = 4
 // groups of threads share them and meet in shared memory, a piece per thread.  Many items have
 // fewer than nine: GROUPS = 1, and four pieces per thread where that still leaves every SM its blocks.
-// What a block joins is known before the parts are there: it adds up a work list of up to 256 entries
-// itself while it waits for them (the first kernel's sums, read afterwards, cost 2 us of the 16 that 8 nodes
-// at 2K of one sequence take).
+// A block adds up a work list of up to 256 entries itself; the lengths are read behind the wait like
+// everything else: that the first kernel's blocks had waited before they triggered makes them final, not
+// visible to this kernel.
 
 template <int HD, int GROUPS, int PIECES>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
@@ -994,7 +993,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int kvh = i % p.c.n_kv_heads, b = i / p.c.n_kv_heads;
   const int group = threadIdx.x / kSide, side = threadIdx.x % kSide;
   const int member = tp % p.team, e = b * p.groups + tp / p.team, E = num_entries(p);
-  // (the inputs of the work list are older than the kernel before this one)
+  pdl_wait();
+  pdl_trigger();
   const Entry x = make_entry(p, e, false);
   const int end = group_end(p, x.s, tp), nblk = (end - x.kstart + kBlk - 1) / kBlk;
   int row[kN], c4[kN];
@@ -1026,13 +1026,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       U += s_units[0][w];
       before += s_units[1][w];
     }
-    pdl_wait();
-    pdl_trigger();
   } else {
     const int chunk = (E + kScan - 1) / kScan;
     for (int y = e / chunk * chunk; y < e; ++y) before += make_entry(p, y, false).units * p.c.n_kv_heads;
-    pdl_wait();
-    pdl_trigger();
     U = op_ld(p.table + kScan);
     before += op_ld(p.table + e / chunk);
   }

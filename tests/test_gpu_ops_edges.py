@@ -1,0 +1,37 @@
+"""Calls of the multi-token operators that the documentation allows and that lie at the edge of
+what a program makes: inputs written just before the call, positions of siblings in a prompt
+chunk, long lists of sequences, many heads."""
+import pytest
+import torch
+
+import ops_ref as R
+from persistent_moe_decode_cta_gb300 import ops
+from test_gpu_tree_attention import setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("heads,n", [((8, 2, 32), 3), ((32, 4, 128), 40)])
+def test_lengths_written_just_before_the_call(heads, n):
+    """The kernels of a call, launched before the copies of its lengths and counts have ended, all work with the
+    new ones: other lengths every time split the items elsewhere."""
+    a = setup(heads, [3000, 700, 1], n, counts=[n, n, n])
+    sets = [([3000, 700, 1], [n, n, n]), ([5, 690, 0], [n - 1, n, 1]), ([1700, 0, 1], [1, n, n]), ([2999, 128, 1], [n, 0, 2])]
+    sets = [tuple(torch.tensor(x, dtype=torch.int32, device="cuda") for x in s) for s in sets]
+    out = torch.zeros_like(a["q"])
+
+    def call(i):
+        a["seq_lens"].copy_(sets[i][0])
+        a["counts"].copy_(sets[i][1])
+        return ops.tree_attention(**a, out=out)
+
+    want = []
+    for i in range(4):
+        call(i)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    got = [call(i % 4).clone() for i in range(40)]
+    # (rows of no node keep what the call before has left there: compared where a node is)
+    for i, x in enumerate(got):
+        for b, m in enumerate(sets[i % 4][1].tolist()):
+            assert torch.equal(x[b, :m], want[i % 4][b, :m]), (i, b)

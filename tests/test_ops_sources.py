@@ -1,0 +1,66 @@
+"""Orders in memory that the multi-token operators rely on, looked up in their sources: an
+access that comes too early shows no wrong result on most runs, so no call can test for it."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "persistent_moe_decode_cta_gb300", "csrc")
+KERNELS = ["mk_tree_attention.cu", "mk_experts.cu", "mk_qk_rope.cu", "mk_cache_pages.cu"]
+
+
+def source(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def body(text, at):
+    """From the first opening brace behind `at` to the one that closes it."""
+    start = text.index("{", at)
+    depth = 0
+    for i in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i + 1]
+    raise AssertionError("unbalanced braces")
+
+
+def kernels(name):
+    """(name, body) of the __global__ functions of a file."""
+    text = source(name)
+    out = []
+    for m in re.finditer(r"__global__", text):
+        head = re.compile(r"(\w+)\s*\((?:[^()]|\([^()]*\))*\)\s*\{").search(text, re.compile(r"__launch_bounds__\([^()]*\)").search(text, m.end()).end())
+        out.append((head.group(1), body(text, head.end() - 1)))
+    return out
+
+
+def readers(name):
+    """Device functions of a file that read global memory, by themselves or through another one."""
+    text = source(name)
+    bodies = {m.group(1): body(text, m.end() - 1)
+              for m in re.finditer(r"__device__[^;{}()]*?\b(\w+)\s*\((?:[^()]|\([^()]*\))*\)\s*(?:const\s*)?\{", text)}
+    found = {"op_ld", "op_ld16", "op_ld16_once", "op_cp16", "op_error"}
+    while True:
+        more = {f for f, b in bodies.items() if f not in found and any(re.search(rf"\b{g}\s*\(", b) for g in found)}
+        if not more:
+            return found
+        found |= more
+
+
+def test_the_readers_are_found():
+    assert {"seq_shape", "make_entry", "scan_units", "make_row"} <= readers("mk_tree_attention.cu")
+    assert {"expert_rows", "scan_experts"} <= readers("mk_experts.cu")
+    assert [[k for k, _ in kernels(f)] for f in KERNELS] == [["tree_kernel", "join_kernel"], ["expert_kernel"], ["rope_kernel"],
+                                                             ["copy_pages_kernel", "commit_kernel"]]
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_kernels_wait_for_earlier_ones_before_they_read(name):
+    """A kernel that is launched early sees what earlier kernels wrote behind its own wait, not before."""
+    reads = re.compile(r"\b(" + "|".join(sorted(readers(name))) + r")\s*\(|->\s*\w+\s*\[")
+    for kernel, text in kernels(name):
+        wait = text.index("pdl_wait()")
+        early = reads.search(text[:wait])
+        assert early is None, f"{kernel}: {early.group(0)} before the wait"
+        assert "pdl_trigger()" not in text[:wait], kernel
