@@ -85,13 +85,28 @@ __device__ __forceinline__ uint32_t map_leader(uint32_t addr) {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same without the order of this CTA's other accesses against the cluster, which costs about
-// 2000 cycles (a whole stage's products take 512): for an arrival that publishes nothing but rows
-// in this CTA's own shared memory, seen complete by the caller and passed to the async proxy,
-// where this CTA's tensor core reads them.
-__device__ __forceinline__ void arrive_cluster_own(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// The same for a thread that publishes only shared memory of its CTA (rows that it has seen complete): a
+// release of everything costs about 2000 cycles (a whole stage's products take 512), one restricted to
+// shared memory does not wait for accesses to global memory.
+__device__ __forceinline__ void arrive_cluster_smem(uint32_t bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A barrier that the other CTA arrives on is waited for at the scope of the cluster.
+// For shared memory: the products' reads of a stage, or the rows and weights of both.
+__device__ __forceinline__ bool try_wait_stage(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return ok != 0;
+}
+// For the accumulators.
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -103,13 +118,28 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
-// Bounded wait of one thread for what both CTAs do.
-__device__ __forceinline__ bool wait_cluster1(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
-  if (try_wait_cluster(bar, parity)) return true;
+// Bounded waits of one thread and of a whole warp, as op_wait1 and op_wait.
+template <bool (*TRY)(uint32_t, uint32_t)>
+__device__ __forceinline__ bool wait_pair1(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
+  if (TRY(bar, parity)) return true;
   const uint64_t t0 = gtime();
-  while (!try_wait_cluster(bar, parity)) {
+  while (!TRY(bar, parity)) {
     if (*abort) return false;
     if ((long long)(gtime() - t0) > kOpWaitNs) {
+      *abort = 1;
+      op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
+      return false;
+    }
+  }
+  return true;
+}
+template <bool (*TRY)(uint32_t, uint32_t)>
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status, int tag) {
+  if (__all_sync(0xffffffffu, TRY(bar, parity))) return true;
+  const uint64_t t0 = gtime();
+  while (!__all_sync(0xffffffffu, TRY(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, (long long)(gtime() - t0) > kOpWaitNs)) {
       *abort = 1;
       op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, tag, (int)parity);
       return false;
@@ -281,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         sh.rows_of[t % kTileNotes] = x.nr;  // for the products, which wait for these copies
         for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
           const uint32_t s = at.slot;
-          if (!(ok = op_wait1(empty(s), at.phase ^ 1, abort, p.a.status, 1))) break;
+          if (!(ok = wait_pair1<try_wait_stage>(empty(s), at.phase ^ 1, abort, p.a.status, 1))) break;
           const uint32_t st = base + s * stage_bytes, bar = lead + 8 * s;
           if (rank == 0) mbar_expect_tx(full(s), bytes);
           tma_pair_3d(st, &tw, ks * kTileK, w, e, bar);
@@ -333,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       }
       const int rows_now = count;
       for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
-        if (!(ok = op_wait(empty(at.slot), at.phase ^ 1, abort, p.a.status, 6))) break;
+        if (!(ok = wait_pair<try_wait_stage>(empty(at.slot), at.phase ^ 1, abort, p.a.status, 6))) break;
         const uint32_t dst = base + at.slot * stage_bytes + kBytesW + row0 * (kTileK * 2) + swz;
         const int bytes = ks * kTileK + 8 * chunk < p.a.k ? 16 : 0;  // (0: zeros)
 #pragma unroll
@@ -355,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
           for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
             if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 7))) break;
             fence_proxy_async_smem();
-            arrive_cluster_own(map_leader(full(at.slot)));
+            arrive_cluster_smem(map_leader(full(at.slot)));
           }
       }
     } else if (elect_one()) {
@@ -366,9 +396,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       for (; ok && (int)nt < mine; ++nt) {
         uint32_t idesc = 0;
         const uint32_t a = nt & 1, acc = tmem + kTileR * a;
-        if (!(ok = wait_cluster1(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
+        if (!(ok = wait_pair1<try_wait_cluster>(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
         for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
-          if (!(ok = op_wait1(full(at.slot), at.phase, abort, p.a.status, 3))) break;
+          if (!(ok = wait_pair1<try_wait_stage>(full(at.slot), at.phase, abort, p.a.status, 3))) break;
           if (p.a.rows) {
             if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 8))) break;
             fence_proxy_async_smem();
@@ -409,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       const uint32_t a = nt & 1;
       const uint32_t acc = tmem + kTileR * a + ((uint32_t)q << 21);
       const int w0 = x.w0 + (int)rank * (GLU ? kTileW / 2 : kTileW) + o, width = min(32, p.a.n - w0);  // (<= 0: nothing to store)
-      op_wait(afull(a), (nt >> 1) & 1, abort, p.a.status, 4);
+      wait_pair<try_wait_cluster>(afull(a), (nt >> 1) & 1, abort, p.a.status, 4);
       tc_fence_after();
       uint32_t u[kChunk];
       tmem_ld32(acc, u);

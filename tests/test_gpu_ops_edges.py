@@ -35,3 +35,19 @@ def test_lengths_written_just_before_the_call(heads, n):
     for i, x in enumerate(got):
         for b, m in enumerate(sets[i % 4][1].tolist()):
             assert torch.equal(x[b, :m], want[i % 4][b, :m]), (i, b)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("sizes,n,k", [([300, 0, 129, 5, 256, 1000], 384, 1024), ([700] * 16, 768, 256), ([3, 9, 1, 0, 30] * 8, 512, 2048)])
+def test_named_rows_equal_rows_in_order(sizes, n, k, glu):
+    """Both CTAs of a pair fetch named rows themselves; the bits are those of rows that lie in order."""
+    g = R.gen(len(sizes))
+    e, total = len(sizes), sum(sizes)
+    offsets = torch.tensor([0] + sizes, device="cuda").cumsum(0).to(torch.int32)
+    x = R.bf16(g, 611, k)
+    w, u = R.bf16(g, e, n, k, std=0.05), R.bf16(g, e, n, k, std=0.05) if glu else None
+    for _ in range(8):
+        rows = torch.randint(0, 611, (total,), generator=g, device="cuda").to(torch.int32)
+        want = ops.expert_product(x[rows.long()], w, offsets, w_up=u)
+        for _ in range(4):
+            assert torch.equal(ops.expert_product(x, w, offsets, w_up=u, rows=rows), want)

@@ -64,3 +64,17 @@ def test_kernels_wait_for_earlier_ones_before_they_read(name):
         early = reads.search(text[:wait])
         assert early is None, f"{kernel}: {early.group(0)} before the wait"
         assert "pdl_trigger()" not in text[:wait], kernel
+
+
+def test_the_pair_meets_at_cluster_scope():
+    """Arrivals on the other CTA's barriers, and waits for barriers that it arrives on, order at the
+    scope of the cluster (at that of the CTA they would order nothing between the two)."""
+    text = source("mk_experts.cu")
+    arrivals = re.findall(r"mbarrier\.arrive\.[\w.:]*shared::cluster\S*", text)
+    assert len(arrivals) >= 2 and all(".cluster.shared::cluster" in a for a in arrivals), arrivals
+    assert set(re.findall(r"\bop_wait1?\(\s*(\w+)", text)) == {"gathered"}   # the CTA's own
+    waits = re.findall(r"mbarrier\.try_wait\.parity\.[\w.:]+", text)
+    assert waits and all(".cluster." in w for w in waits), waits
+    assert len(re.findall(r"fence\.acquire\.sync_restrict::shared::cluster\.cluster", text)) == sum(".relaxed." in w for w in waits)
+    for m in re.finditer(r"mbarrier\.arrive\.relaxed\.cluster", text):   # a release in front of it
+        assert re.search(r"fence\.release\.\S*cluster;[^}]*$", text[:m.start()])
