@@ -286,7 +286,10 @@ __device__ __noinline__ uint32_t sees32(const TreeParams& p, const Item& it, con
 // keys past the end: its scores are masked and its V checked.
 __device__ __forceinline__ bool masked_block(const TreeParams& p, const Item& it, int k0) {
   const int per = nodes_per_group(p);
-  const int open = it.len + (p.a.mask ? 0 : it.tp * per + 1);  // keys below are seen by all rows, but for a window
+  // keys below `open` are seen by all rows, but for a window that leaves their slots behind (with
+  // positions of their own, nodes may be behind it whatever their slots are)
+  const bool chain = !p.a.mask && !(p.a.window > 0 && p.a.positions);
+  const int open = it.len + (chain ? it.tp * per + 1 : 0);
   if (k0 + kBlk > open) return true;
   if (p.a.window > 0) {
     const int last = p.a.mask || p.a.positions ? it.cnt : min(it.cnt, (it.tp + 1) * per);

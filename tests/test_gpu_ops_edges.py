@@ -6,7 +6,7 @@ import torch
 
 import ops_ref as R
 from persistent_moe_decode_cta_gb300 import ops
-from test_gpu_tree_attention import setup
+from test_gpu_tree_attention import LAYOUTS, check, setup
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,19 @@ def test_named_rows_equal_rows_in_order(sizes, n, k, glu):
         want = ops.expert_product(x[rows.long()], w, offsets, w_up=u)
         for _ in range(4):
             assert torch.equal(ops.expert_product(x, w, offsets, w_up=u, rows=rows), want)
+
+
+@pytest.mark.parametrize("heads", LAYOUTS + [(6, 6, 64), (128, 1, 32)])
+@pytest.mark.parametrize("window", [1, 40, 300])
+def test_window_and_positions_of_a_chain(heads, window):
+    """Without a mask, positions of the nodes that do not ascend one by one: a node's key leaves the window by its
+    position, whatever its slot is."""
+    for n, lens, counts in ((500, [70, 0], [500, 431]), (131, [300], None)):
+        a = setup(heads, lens, n, tree=False, counts=counts)
+        g = R.gen(window)
+        start = a["seq_lens"][:, None]
+        node = torch.arange(n, device="cuda")
+        for depth in (torch.zeros_like(node), node // 2, node.flip(0), torch.randint(0, n, (n,), generator=g, device="cuda"),
+                      torch.where(node < n // 2, 0, n - 1)):
+            a["positions"] = (start + depth).to(torch.int32)
+            check(a, window)
