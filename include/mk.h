@@ -414,7 +414,8 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  *     seq_lens[b] + i, whatever its depth in the tree.  counts[b] (NULL = n_nodes for
  *     all) is the number of nodes of sequence b; rows of later nodes are not written, and
  *     what they hold does not matter.
- *   - status: int32[4], zeroed by the caller, or NULL (not recorded).  The first invalid
+ *   - status: int32[4], zeroed by the caller, or NULL for the device's own record
+ *     (mk_op_status).  The first invalid
  *     value that a kernel finds in device data is recorded there as {mk_status code,
  *     sequence or expert, index, value} (MK_ERR_TIMEOUT: {code, CTA, wait, ..}: an internal
  *     wait of more than 2 s was given up).  Invalid entries are skipped or clamped, never
@@ -562,6 +563,12 @@ typedef struct mk_expert_args {
   int32_t n_x, n_rows, n_experts, n, k;
 } mk_expert_args;
 int mk_expert_product(const mk_expert_args* args, void* stream);
+
+/* The current device's own record, of the calls whose status was NULL: copied to status_out
+ * (HOST int32[4], zeros where nothing was recorded) and, if something was, cleared.
+ * Synchronises `stream`; calls on other streams count once the caller knows that they have
+ * ended.  Not during a capture. */
+int mk_op_status(int32_t* status_out, void* stream);
 
 /* Message for the last failing call on h (or the last global failure if h is
  * NULL).  The string is owned by the library. */

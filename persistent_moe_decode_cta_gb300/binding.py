@@ -35,7 +35,7 @@ EXPORTS = ["mk_create", "mk_plan", "mk_decode_step", "mk_decode_steps", "mk_deco
            "mk_plan_drop_signal", "mk_read", "mk_read_expert_fp8", "mk_read_weight_fp8", "mk_query",
            "mk_plan_dry", "mk_last_error", "mk_destroy", "mk_version",
            "mk_qk_norm_rope", "mk_tree_attention", "mk_tree_attention_workspace", "mk_copy_pages", "mk_commit_nodes",
-           "mk_expert_product"]
+           "mk_expert_product", "mk_op_status"]
 
 
 class MkError(RuntimeError):
@@ -149,6 +149,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mk_copy_pages.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
     lib.mk_commit_nodes.argtypes = [vp, i32, vp, i32, vp, vp, vp]
     lib.mk_expert_product.argtypes = [vp, vp]
+    lib.mk_op_status.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
     for name in EXPORTS:
         if name not in ("mk_last_error", "mk_destroy"):
             getattr(lib, name).restype = ctypes.c_int

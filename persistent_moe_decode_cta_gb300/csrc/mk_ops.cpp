@@ -89,6 +89,11 @@ int check_rows(const char* name, const void* ptr, const int64_t* stride, const i
   return MK_OK;
 }
 
+// where a call records what its kernels find wrong: the caller's record or the device's own
+int set_record(int32_t*& status) {
+  return status ? (int)MK_OK : cuda_error(op_record(&status), "error record");
+}
+
 // the tile shape of mk_tree_attention for these sizes (device: the SM count)
 int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
@@ -159,6 +164,8 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
     table.half = half;
   }
   std::copy(table.t, table.t + half, p.turns);
+  r = set_record(p.a.status);
+  if (r) return r;
   return cuda_error(launch_rope(p, static_cast<cudaStream_t>(stream)), "qk_norm_rope launch");
 }
 
@@ -211,6 +218,7 @@ int mk_tree_attention(const mk_paged_kv* cache, const mk_tree_args* args, void* 
   cuuint32_t kb[4] = {(cuuint32_t)span, 8, (cuuint32_t)(hd / span), kOpPage / 8};
   if (!r) r = encode(&tk, cache->k, 4, kd, ks, kb, sw);
   if (!r) r = encode(&tv, cache->v, 4, kd, ks, kb, sw);
+  if (!r) r = set_record(p.a.status);
   if (r) return r;
   return cuda_error(launch_tree(p, tq, tk, tv, static_cast<cudaStream_t>(stream)), "tree_attention launch");
 }
@@ -252,7 +260,7 @@ int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n
 
 int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accepted, int max_accept, int32_t* new_lens,
                     int32_t* status, void* stream) {
-  const int r = check_cache(cache, true);
+  int r = check_cache(cache, true);
   if (r) return r;
   if (n_layers < 1 || n_layers > 65535) return op_fail(MK_ERR_INVALID, "n_layers %d not in [1, 65535]", n_layers);
   if (!accepted || !new_lens) return op_fail(MK_ERR_INVALID, "NULL pointer");
@@ -265,6 +273,8 @@ int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accep
   p.accepted = accepted;
   p.new_lens = new_lens;
   p.status = status;
+  r = set_record(p.status);
+  if (r) return r;
   return cuda_error(launch_commit(p, static_cast<cudaStream_t>(stream)), "commit_nodes launch");
 }
 
@@ -302,8 +312,24 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   cuuint32_t wb[3] = {64, a->w_up ? 64u : 128u, 1};
   if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!r) r = encode(&tu, a->w_up ? a->w_up : a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = set_record(p.a.status);
   if (r) return r;
   return cuda_error(launch_experts(p, tx, tx128, tw, tu, static_cast<cudaStream_t>(stream)), "expert_product launch");
+}
+
+int mk_op_status(int32_t* status_out, void* stream) {
+  if (!status_out) return op_fail(MK_ERR_INVALID, "status_out is NULL");
+  const auto st = static_cast<cudaStream_t>(stream);
+  int32_t* record = nullptr;
+  int r = set_record(record);
+  if (r) return r;
+  r = cuda_error(cudaMemcpyAsync(status_out, record, 4 * sizeof(int32_t), cudaMemcpyDeviceToHost, st), "error record");
+  if (!r) r = cuda_error(cudaStreamSynchronize(st), "error record");
+  if (!r && status_out[0]) {
+    r = cuda_error(cudaMemsetAsync(record, 0, 4 * sizeof(int32_t), st), "error record");
+    if (!r) r = cuda_error(cudaStreamSynchronize(st), "error record");
+  }
+  return r;
 }
 
 }  // extern "C"

@@ -53,6 +53,9 @@ constexpr int kOpMaxExperts = 256;     // experts of one call (as mk_create)
 constexpr int kOpMaxAccept = 512;      // accepted nodes per sequence (staged in shared memory)
 constexpr int kOpMaxHalf = 64;         // head_dim / 2 at most
 
+// The current device's own error record, int32[4] (mk_cache_pages.cu).
+cudaError_t op_record(int32_t** record);
+
 // ------------------------------------------------------------------ qk_norm_rope
 struct RopeParams {
   mk_paged_kv c;

@@ -12,8 +12,9 @@ the operators are defined; a wrong tensor raises ValueError, a call that the lib
 refuses raises `binding.MkError`.  Like the library's calls they are asynchronous, on the
 current stream of the tensors' device or on `stream` (a torch stream or a raw pointer), and
 can be captured into a CUDA graph.  What a kernel finds wrong in device data (a page id, an
-offset) goes to `status`, an int32[4] CUDA tensor from `new_status`, if one is given;
-`check_status` reads it.  None of them has a backward pass.
+offset, or a wait of its own that ran out) goes to `status`, an int32[4] CUDA tensor from
+`new_status`, or without one to the device's own record; `check_status` reads either.  None of
+them has a backward pass.
 
 Shapes: k_cache, v_cache bf16 [n_pages, n_kv_heads, 16, head_dim] (one layer) or
 [n_layers, n_pages, n_kv_heads, 16, head_dim] (whole pools); page_table int32
@@ -21,6 +22,7 @@ Shapes: k_cache, v_cache bf16 [n_pages, n_kv_heads, 16, head_dim] (one layer) or
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import inspect
 
@@ -81,11 +83,19 @@ def new_status(device="cuda"):
     return torch.zeros(4, dtype=_I32, device=device)
 
 
-def check_status(status):
-    """Read and clear an error record (synchronising); raises MkError for a recorded error."""
-    code, where, index, value = status.tolist()
+def check_status(status=None):
+    """Read and clear an error record (synchronising); raises MkError for a recorded error.
+    None: the current device's own record, of all calls so far that were given no `status`."""
+    if status is None:
+        torch.cuda.synchronize()
+        found = (ctypes.c_int32 * 4)()
+        B._check(B.load_library().mk_op_status(found, torch.cuda.current_stream().cuda_stream))
+        code, where, index, value = found
+    else:
+        code, where, index, value = status.tolist()
     if code:
-        status.zero_()
+        if status is not None:
+            status.zero_()
         raise B.MkError(code, f"recorded by a kernel: sequence, expert or CTA {where}, index {index}, value {value}")
 
 

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import ops_ref as R
+from persistent_moe_decode_cta_gb300 import binding as B
 from persistent_moe_decode_cta_gb300 import ops
 from test_gpu_tree_attention import LAYOUTS, check, setup
 
@@ -67,3 +68,42 @@ def test_window_and_positions_of_a_chain(heads, window):
                       torch.where(node < n // 2, 0, n - 1)):
             a["positions"] = (start + depth).to(torch.int32)
             check(a, window)
+
+
+def test_what_is_found_without_a_status_is_recorded():
+    """A call that is given no record leaves what it finds in the device's own."""
+    g = R.gen(8)
+    k, v, table, sl = R.cache(g, [20, 3], 4, 2, 32, layers=1)
+    q = R.bf16(g, 2, 4, 4, 32)
+    kn = R.bf16(g, 2, 4, 2, 32)
+    x, w = R.bf16(g, 8, 64), R.bf16(g, 2, 40, 64)
+    keep = table.clone()
+    bad = keep.clone()
+    bad[1, 0] = k.shape[1]
+    table.copy_(bad)
+    calls = [(B.MK_ERR_BAD_PAGE, 1, lambda **s: ops.qk_norm_rope(q, kn, kn, k[0], v[0], table, sl, theta=1e4, **s)),
+             (B.MK_ERR_BAD_PAGE, 1, lambda **s: ops.tree_attention(q, k[0], v[0], table, sl, **s)),
+             (B.MK_ERR_BAD_PAGE, 1, lambda **s: ops.commit_nodes(k, v, table, sl, torch.ones_like(sl)[:, None], **s)),
+             (B.MK_ERR_INVALID, 0, lambda **s: ops.expert_product(x, w, torch.tensor([-1, 2, 8], dtype=torch.int32, device="cuda"), **s))]
+    ops.check_status()
+    for code, where, call in calls:
+        call()
+        with pytest.raises(B.MkError, match=f"expert or CTA {where},") as e:
+            ops.check_status()
+        assert e.value.code == code
+        ops.check_status()      # cleared
+        status = ops.new_status()
+        call(status=status)
+        ops.check_status()      # the caller's record, not the device's
+        with pytest.raises(B.MkError):
+            ops.check_status(status)
+    graph = torch.cuda.CUDAGraph()
+    table.copy_(keep)
+    with torch.cuda.graph(graph):
+        calls[1][2]()
+    graph.replay()
+    ops.check_status()
+    table.copy_(bad)
+    graph.replay()
+    with pytest.raises(B.MkError):
+        ops.check_status()
