@@ -4,10 +4,11 @@ Four builds of the megakernel (default, deterministic, two tensor-core variants)
 multi-token operators and the host planner/ABI compile in parallel, then link into
 persistent_moe_decode_cta_gb300/libmk.so with the CUDA runtime linked statically.  Beside it,
 _ops.so is the Python module that checks and marshals tensors for the operators (against the
-installed torch; it finds libmk.so by its own directory).  Usable as `python -m persistent_moe_decode_cta_gb300.build`.
+installed torch, and left out where there is none; it finds libmk.so by its own directory).  Usable as `python -m persistent_moe_decode_cta_gb300.build`.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -67,13 +68,17 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                      os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
 
-    cmds.append(_module_command(os.path.join(OUT_DIR, "ops_module.cpp.o"), True))
+    with_module = importlib.util.find_spec("torch") is not None
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with ThreadPoolExecutor(len(cmds)) as ex:
+    def module_object():
+        return run(_module_command(os.path.join(OUT_DIR, "ops_module.cpp.o"), True))
+
+    with ThreadPoolExecutor(len(cmds) + 1) as ex:
+        module = ex.submit(module_object) if with_module else None
         results = list(ex.map(run, cmds))
     for cmd, r in results:
         if verbose or ptxas_info:
@@ -85,9 +90,15 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + " ".join(link) + "\n" + r.stdout + r.stderr)
     os.replace(LIB + ".tmp", LIB)
-    r = subprocess.run(_module_command(MODULE + ".tmp", False), capture_output=True, text=True)
+    # (the library is in place whatever becomes of the module)
+    if not with_module:
+        sys.stderr.write("torch is not installed: _ops.so, which ops.py needs, is left out\n")
+        return LIB
+    cmd, r = module.result()
+    if r.returncode == 0:
+        cmd, r = run(_module_command(MODULE + ".tmp", False))
     if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+        raise RuntimeError("the Python module failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(MODULE + ".tmp", MODULE)
     return LIB
 

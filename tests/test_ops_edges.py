@@ -3,6 +3,8 @@ import os
 import subprocess
 import sys
 
+import pytest
+
 from persistent_moe_decode_cta_gb300 import binding as B
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -28,3 +30,38 @@ def test_the_package_alone_imports_no_torch():
               "from persistent_moe_decode_cta_gb300 import *\n"
               "print(ops.__name__)")
     assert out.split() == ["persistent_moe_decode_cta_gb300.ops"]
+
+
+COMPILER = """#!{python}
+import sys
+
+import pytest
+open(sys.argv[sys.argv.index("-o") + 1], "w").write("built")
+"""
+
+BUILD = """
+import os, sys
+if {block}:
+    class NoTorch:
+        def find_spec(self, name, path=None, target=None):
+            if name.split(".")[0] == "torch":
+                raise ModuleNotFoundError(name)
+    import importlib.util
+    found = importlib.util.find_spec
+    importlib.util.find_spec = lambda name, *a: None if name == "torch" else found(name, *a)
+    sys.meta_path.insert(0, NoTorch())
+from persistent_moe_decode_cta_gb300 import build as b
+b.OUT_DIR, b.LIB, b.MODULE = (os.path.join({out!r}, x) for x in ("_build", "libmk.so", "_ops.so"))
+b.build()
+print(*sorted(x for x in os.listdir({out!r}) if x.endswith(".so")))
+"""
+
+
+@pytest.mark.parametrize("block", [True, False])
+def test_the_library_is_built_without_torch(tmp_path, block):
+    """(With a compiler that only writes its output: which files are asked for.)"""
+    fake = tmp_path / "compiler"
+    fake.write_text(COMPILER.format(python=sys.executable))
+    fake.chmod(0o755)
+    out = run(BUILD.format(block=block, out=str(tmp_path)), NVCC=str(fake), CXX=str(fake))
+    assert out.split() == (["libmk.so"] if block else ["_ops.so", "libmk.so"])
