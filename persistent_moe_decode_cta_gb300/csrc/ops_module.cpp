@@ -49,12 +49,14 @@ const at::Tensor& shaped(PyObject* o, const char* name, int64_t dims) {
 }
 
 void check(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int dev) {
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, and this operator has no backward pass");
+  if (t._fw_grad(0).defined())  // (forward-mode derivatives have one level, 0)
+    refuse(std::string(name) + " carries a forward-mode tangent, and this operator has no derivative");
   if (!t.is_cuda() || t.get_device() != dev)
     refuse(std::string(name) + " must be a CUDA tensor on device " + std::to_string(dev) + ", not on " + t.device().str());
   if (t.scalar_type() != type) refuse(std::string(name) + " must be " + toString(type) + ", not " + toString(t.scalar_type()));
   if (t.sizes() != shape) refuse(std::string(name) + " has shape " + show(t.sizes()) + ", needs " + show(shape));
-  if (t.requires_grad() && c10::GradMode::is_enabled())
-    refuse(std::string(name) + " requires a gradient, and this operator has no backward pass");
 }
 
 // address of a contiguous operand

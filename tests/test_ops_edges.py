@@ -4,8 +4,11 @@ import subprocess
 import sys
 
 import pytest
+import torch
+import torch.autograd.forward_ad as forward
 
 from persistent_moe_decode_cta_gb300 import binding as B
+from persistent_moe_decode_cta_gb300 import ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -36,6 +39,8 @@ COMPILER = """#!{python}
 import sys
 
 import pytest
+import torch
+import torch.autograd.forward_ad as forward
 open(sys.argv[sys.argv.index("-o") + 1], "w").write("built")
 """
 
@@ -65,3 +70,17 @@ def test_the_library_is_built_without_torch(tmp_path, block):
     fake.chmod(0o755)
     out = run(BUILD.format(block=block, out=str(tmp_path)), NVCC=str(fake), CXX=str(fake))
     assert out.split() == (["libmk.so"] if block else ["_ops.so", "libmk.so"])
+
+
+def test_tensors_that_carry_derivatives_are_refused():
+    """A gradient that would be wanted, and a forward-mode tangent that would be dropped."""
+    m = ops._native()
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with forward.dual_level():
+        dual = forward.make_dual(x, torch.ones_like(x))
+        with pytest.raises(ValueError, match="x carries a forward-mode tangent"):
+            m.expert_product(dual, x[None], x, None, None, None, None)
+    with pytest.raises(ValueError, match="x requires a gradient"):
+        m.expert_product(x.clone().requires_grad_(), x[None], x, None, None, None, None)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"), torch.no_grad():
+        m.expert_product(x.clone().requires_grad_(), x[None], x, None, None, None, None)
