@@ -244,6 +244,7 @@ PyObject* commit_nodes(PyObject* const* a) {
   const at::Tensor out = a[5] == Py_None ? fresh({c.batch}, k, at::kInt, false) : tensor(a[5], "out");
   int32_t* lens = need<int32_t>(out, "out", at::kInt, {c.batch}, dev);
   int32_t* status = optional<int32_t>(a[6], "status", at::kInt, {4}, dev);
+  if (c.batch == 0) return wrap(out);
   return finish(mk_commit_nodes(&c, size32(k.size(0), "the number of layers"), accepted, size32(acc.size(1), "max_accept"), lens,
                                 status, stream(dev)),
                 wrap(out));

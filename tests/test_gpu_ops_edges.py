@@ -107,3 +107,20 @@ def test_what_is_found_without_a_status_is_recorded():
     graph.replay()
     with pytest.raises(B.MkError):
         ops.check_status()
+
+
+def test_an_empty_batch_is_no_work():
+    """No sequence: every operator on the cache returns without one."""
+    g = R.gen(2)
+    k, v = R.bf16(g, 2, 4, 2, 16, 32), R.bf16(g, 2, 4, 2, 16, 32)
+    k0, v0 = k.clone(), v.clone()
+    table = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q, kn = R.bf16(g, 0, 5, 4, 32), R.bf16(g, 0, 5, 2, 32)
+    assert ops.qk_norm_rope(q, kn, kn, k[0], v[0], table, lens, theta=1e4).shape == q.shape
+    assert ops.tree_attention(q, k[0], v[0], table, lens).shape == q.shape
+    new = ops.commit_nodes(k, v, table, lens, torch.zeros(0, 4, dtype=torch.int32, device="cuda"))
+    assert new.shape == (0,) and new.dtype == torch.int32
+    ops.copy_pages(k, v, [], [])
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    ops.check_status()
