@@ -424,7 +424,8 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  */
 
 /* One layer's K/V pools and the batch's page table.
- *   k, v        bf16 [n_pages][n_kv_heads][16][head_dim], 16-byte aligned
+ *   k, v        bf16 [n_pages][n_kv_heads][16][head_dim], 16-byte aligned; they do not overlap
+ *               where a call writes them
  *   page_table  int32[batch][max_pages]: physical page of logical page j; entries that
  *               no position of the call falls into are not read
  *   seq_lens    int32[batch] cached tokens; seq_lens + counts <= 16 * max_pages, else

@@ -72,6 +72,15 @@ int check_cache(const mk_paged_kv* c, bool pointers) {
   return MK_OK;
 }
 
+// K and V of `layers` layers in memory of their own: an operator that writes both would write one
+// twice, in any order
+int check_apart(const mk_paged_kv* c, long long layers) {
+  const uintptr_t k = reinterpret_cast<uintptr_t>(c->k), v = reinterpret_cast<uintptr_t>(c->v);
+  const unsigned long long bytes = (unsigned long long)layers * c->n_pages * c->n_kv_heads * kOpPage * c->head_dim * 2;
+  if ((k < v ? v - k : k - v) < bytes) return op_fail(MK_ERR_INVALID, "the K and V pools overlap");
+  return MK_OK;
+}
+
 int check_heads(const mk_paged_kv* c, int n_nodes, int n_q_heads) {
   if (n_nodes < 1 || n_nodes > (1 << 24)) return op_fail(MK_ERR_INVALID, "n_nodes %d not in [1, 2^24]", n_nodes);
   if (n_q_heads < 1 || n_q_heads % c->n_kv_heads) return op_fail(MK_ERR_INVALID, "n_q_heads %d not a multiple of n_kv_heads %d", n_q_heads, c->n_kv_heads);
@@ -145,6 +154,8 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
     return op_fail(MK_ERR_INVALID, "gains must be 16-byte aligned");
   if (!(args->theta >= 1.0) || !std::isfinite(args->theta)) return op_fail(MK_ERR_INVALID, "theta must be finite and >= 1");
   if (!(args->eps >= 0.f) || !std::isfinite(args->eps)) return op_fail(MK_ERR_INVALID, "eps must be finite and >= 0");
+  r = check_apart(cache, 1);
+  if (r) return r;
   RopeParams p{};
   p.c = *cache;
   p.a = *args;
@@ -230,7 +241,7 @@ int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n
   c.n_kv_heads = n_kv_heads;
   c.head_dim = head_dim;
   c.batch = c.max_pages = 1;
-  const int r = check_cache(&c, false);
+  int r = check_cache(&c, false);
   if (r) return r;
   if (!k_cache || !v_cache) return op_fail(MK_ERR_INVALID, "NULL cache pointer");
   if (!aligned16(k_cache) || !aligned16(v_cache)) return op_fail(MK_ERR_INVALID, "K/V pools must be 16-byte aligned");
@@ -252,6 +263,10 @@ int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n
   } catch (const std::bad_alloc&) {
     return op_fail(MK_ERR_OOM, "host memory for %d page ids", n);
   }
+  c.k = k_cache;
+  c.v = v_cache;
+  if (k_cache != v_cache) r = check_apart(&c, n_layers);  // (the same copies twice do no harm)
+  if (r) return r;
   const long long page = (long long)n_kv_heads * kOpPage * head_dim * 2;
   return cuda_error(launch_copy_pages(static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), n_layers, page * n_pages,
                                       page, src, dst, n, static_cast<cudaStream_t>(stream)),
@@ -266,6 +281,8 @@ int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accep
   if (!accepted || !new_lens) return op_fail(MK_ERR_INVALID, "NULL pointer");
   if (new_lens == cache->seq_lens) return op_fail(MK_ERR_INVALID, "new_lens must not be seq_lens");
   if (max_accept < 1 || max_accept > kOpMaxAccept) return op_fail(MK_ERR_INVALID, "max_accept %d not in [1, %d]", max_accept, kOpMaxAccept);
+  r = check_apart(cache, n_layers);
+  if (r) return r;
   CommitParams p{};
   p.c = *cache;
   p.n_layers = n_layers;

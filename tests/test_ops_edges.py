@@ -1,15 +1,19 @@
 """Calls at the edge of the multi-token operators' entry points that need no GPU."""
+import ctypes
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 import torch.autograd.forward_ad as forward
 
 from persistent_moe_decode_cta_gb300 import binding as B
 from persistent_moe_decode_cta_gb300 import ops
+import test_ops_refusals as R
 
+P = R.P
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -84,3 +88,21 @@ def test_tensors_that_carry_derivatives_are_refused():
         m.expert_product(x.clone().requires_grad_(), x[None], x, None, None, None, None)
     with pytest.raises(ValueError, match="x must be a CUDA tensor"), torch.no_grad():
         m.expert_product(x.clone().requires_grad_(), x[None], x, None, None, None, None)
+
+
+@pytest.mark.parametrize("shift", [0, 16, 40959, 40960])
+def test_pools_that_overlap_are_not_written(shift):
+    """K and V of one layer are 40960 bytes here, of three 122880."""
+    lib = B.load_library()
+    pages = np.array([0, 1], np.int32)
+
+    def refused(rc):
+        return rc == B.MK_ERR_INVALID and b"overlap" in lib.mk_last_error(None)
+
+    for k, v in ((P, P + shift // 16 * 16), (P + shift // 16 * 16, P)):
+        one = R.kv(k=k, v=v)
+        if shift < 40960:    # (what is not refused would follow the made-up addresses where there is a GPU)
+            assert refused(lib.mk_qk_norm_rope(ctypes.byref(one), ctypes.byref(R.rope()), None))
+        assert refused(lib.mk_commit_nodes(ctypes.byref(one), 3, P, 4, 1 << 40, None, None))
+        if shift:    # (the same pool twice: the same copies twice)
+            assert refused(lib.mk_copy_pages(k, v, 3, 10, 2, 64, pages[:1].ctypes.data, pages[1:].ctypes.data, 1, None))
