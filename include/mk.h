@@ -531,7 +531,7 @@ int mk_copy_pages(void* k_cache, void* v_cache, int n_layers, int n_pages, int n
  * nodes may be in any order.
  *   cache      k, v are the whole pools [n_layers][n_pages][..]
  *   accepted   int32[batch][max_accept], max_accept in 1..512
- *   new_lens   int32[batch], not seq_lens itself nor a part of it
+ *   new_lens   int32[batch], not a part of seq_lens, accepted or page_table
  * A sequence with an entry whose slot lies beyond its page table (MK_ERR_INVALID) or on a
  * page outside [0, n_pages) (MK_ERR_BAD_PAGE) is left as it was.  The pages that the nodes
  * lie on belong to one sequence each. */

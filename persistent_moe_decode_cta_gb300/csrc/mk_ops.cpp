@@ -279,8 +279,15 @@ int mk_commit_nodes(const mk_paged_kv* cache, int n_layers, const int32_t* accep
   if (r) return r;
   if (n_layers < 1 || n_layers > 65535) return op_fail(MK_ERR_INVALID, "n_layers %d not in [1, 65535]", n_layers);
   if (!accepted || !new_lens) return op_fail(MK_ERR_INVALID, "NULL pointer");
-  if (new_lens == cache->seq_lens) return op_fail(MK_ERR_INVALID, "new_lens must not be seq_lens");
   if (max_accept < 1 || max_accept > kOpMaxAccept) return op_fail(MK_ERR_INVALID, "max_accept %d not in [1, %d]", max_accept, kOpMaxAccept);
+  // (a sequence's length is written while other blocks may still have to read)
+  const auto overlaps = [&](const int32_t* p, long long n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(new_lens), b = reinterpret_cast<uintptr_t>(p);
+    return a < b + n * 4 && b < a + cache->batch * 4ll;
+  };
+  if (overlaps(cache->seq_lens, cache->batch)) return op_fail(MK_ERR_INVALID, "new_lens must not be seq_lens nor a part of it");
+  if (overlaps(accepted, (long long)cache->batch * max_accept) || overlaps(cache->page_table, (long long)cache->batch * cache->max_pages))
+    return op_fail(MK_ERR_INVALID, "new_lens must not be a part of accepted or of the page table");
   r = check_apart(cache, n_layers);
   if (r) return r;
   CommitParams p{};

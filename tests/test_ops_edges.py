@@ -106,3 +106,14 @@ def test_pools_that_overlap_are_not_written(shift):
         assert refused(lib.mk_commit_nodes(ctypes.byref(one), 3, P, 4, 1 << 40, None, None))
         if shift:    # (the same pool twice: the same copies twice)
             assert refused(lib.mk_copy_pages(k, v, 3, 10, 2, 64, pages[:1].ctypes.data, pages[1:].ctypes.data, 1, None))
+
+
+@pytest.mark.parametrize("lens,table,accepted,new", [
+    (0, 4096, 8192, 0), (0, 4096, 8192, 4), (4, 4096, 8192, 0), (0, 4096, 8192, 4096), (0, 4096, 8192, 4096 + 28), (0, 4096, 8192, 4092),
+    (0, 4096, 8192, 8192), (0, 4096, 8192, 8192 + 20), (0, 4096, 8192, 8188)])
+def test_new_lengths_are_no_part_of_what_is_read(lens, table, accepted, new):
+    """Two sequences, tables of 4 pages, paths of 3 nodes; offsets in bytes."""
+    c = R.kv(k=P, v=1 << 40, seq_lens=P + lens, page_table=P + table)
+    lib = B.load_library()
+    assert lib.mk_commit_nodes(ctypes.byref(c), 1, P + accepted, 3, P + new, None, None) == B.MK_ERR_INVALID
+    assert b"new_lens" in lib.mk_last_error(None)
