@@ -69,6 +69,8 @@ def _operator(fn):
         if stream is None:
             return fn(*args, **kw)
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=first.device)
+        if s.device != first.device:
+            raise ValueError(f"{lead} is on {first.device}, the stream on {s.device}")
         with torch.cuda.stream(s):
             out = fn(*args, **kw)
         for t in (*args, *kw.values()):

@@ -1,4 +1,5 @@
 """Calls at the edge of the multi-token operators' entry points that need no GPU."""
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -117,3 +118,62 @@ def test_new_lengths_are_no_part_of_what_is_read(lens, table, accepted, new):
     lib = B.load_library()
     assert lib.mk_commit_nodes(ctypes.byref(c), 1, P + accepted, 3, P + new, None, None) == B.MK_ERR_INVALID
     assert b"new_lens" in lib.mk_last_error(None)
+
+
+class Devices:
+    """Two devices that are not there: which one is current, where calls run, what they keep."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.streams, self.ran, self.kept = 0, [], [], []
+        monkeypatch.setattr(ops, "_module", self)
+        monkeypatch.setattr(torch.cuda, "device", lambda d: self.entered("now", d))
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: self.entered("streams", self.streams + [s]))
+        monkeypatch.setattr(torch.cuda, "Stream", self.Stream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: self.Stream(device, raw))
+
+    class Stream:
+        def __init__(self, device, raw=None):
+            self.device, self.raw = torch.device(device), raw
+
+    @contextlib.contextmanager
+    def entered(self, name, value):
+        before = getattr(self, name)
+        setattr(self, name, value)
+        try:
+            yield
+        finally:
+            setattr(self, name, before)
+
+    def is_here(self, t):
+        return t.get_device() == self.now
+
+    def copy_pages(self, k, *_):
+        self.ran.append((self.now, [s.raw or s for s in self.streams]))
+
+    def tensor(self, index):
+        kept = self.kept
+
+        class Tensor(torch.Tensor):
+            device = torch.device("cuda", index)
+            is_cuda = True
+
+            def get_device(self):
+                return index
+
+            def record_stream(self, s):
+                kept.append(s.raw or s)
+        return torch.zeros(1).as_subclass(Tensor)
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    d = Devices(monkeypatch)
+    k = d.tensor(1)
+    ops.copy_pages(k, k, [0], [1])
+    assert d.ran == [(1, [])] and d.now == 0 and not d.kept
+    s = d.Stream("cuda:1")
+    ops.copy_pages(k, k, [0], [1], stream=s)
+    ops.copy_pages(k, k, [0], [1], stream=77)            # a raw pointer: a stream of the tensors' device
+    assert d.ran[1:] == [(1, [s]), (1, [77])] and d.kept == [s, s, 77, 77] and d.now == 0
+    with pytest.raises(ValueError, match="k_cache is on cuda:1, the stream on cuda:0"):
+        ops.copy_pages(k, k, [0], [1], stream=d.Stream("cuda:0"))
+    assert len(d.ran) == 3 and d.now == 0
