@@ -176,8 +176,10 @@ int mk_qk_norm_rope(const mk_paged_kv* cache, const mk_rope_args* args, void* st
   }
   std::copy(table.t, table.t + half, p.turns);
   r = set_record(p.a.status);
+  int sms = 0;
+  if (!r) r = num_sms(&sms);
   if (r) return r;
-  return cuda_error(launch_rope(p, static_cast<cudaStream_t>(stream)), "qk_norm_rope launch");
+  return cuda_error(launch_rope(p, sms, static_cast<cudaStream_t>(stream)), "qk_norm_rope launch");
 }
 
 int mk_tree_attention_workspace(const mk_paged_kv* cache, const mk_tree_args* args, size_t* bytes) {

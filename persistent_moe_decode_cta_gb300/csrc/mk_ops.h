@@ -62,7 +62,7 @@ struct RopeParams {
   mk_rope_args a;
   unsigned long long turns[kOpMaxHalf];  // theta^(-2i/hd) / 2pi as a 64-bit binary fraction
 };
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
+cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ tree_attention
 struct TreeParams {

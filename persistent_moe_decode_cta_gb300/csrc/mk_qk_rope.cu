@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const __grid_c
 }
 
 template <int HD>
-cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
+cudaError_t launch_hd(const RopeParams& p, int sms, cudaStream_t st) {
   const int all = (p.a.n_q_heads + 2 * p.c.n_kv_heads) * (HD / 16);
   const int ny = (all + kRopeMaxThreads - 1) / kRopeMaxThreads;
   // lanes of a token in one block: whole heads
@@ -194,7 +194,7 @@ cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
   // Tokens behind one another: as few as fill the SMs (1024 threads each) in whole rounds of blocks
   // (8002 tokens of 32 + 2 * 4 heads of 128, 164 MB: two rounds of 9 tokens 30.8 us, 5.3 TB/s; one of 18 34.6;
   // 16 tokens, 1.1 rounds, 43.2; two tokens a block in registers, without the copies ahead, 35.7)
-  const long long round = 152ll * (2 * kRopeMaxThreads / threads) * side;
+  const long long round = (long long)sms * (2 * kRopeMaxThreads / threads) * side;
   const int most = (int)std::min<long long>(kRopeMost, kRopeSmem / (side * HD * 4));
   const long long rounds = (tokens * ny + round * most - 1) / (round * most);
   const int P = (int)((tokens * ny + round * rounds - 1) / (round * rounds)), per = side * P;
@@ -205,10 +205,10 @@ cudaError_t launch_hd(const RopeParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t st) {
-  if (p.c.head_dim == 128) return launch_hd<128>(p, st);
-  if (p.c.head_dim == 64) return launch_hd<64>(p, st);
-  return launch_hd<32>(p, st);
+cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t st) {
+  if (p.c.head_dim == 128) return launch_hd<128>(p, sms, st);
+  if (p.c.head_dim == 64) return launch_hd<64>(p, sms, st);
+  return launch_hd<32>(p, sms, st);
 }
 
 }  // namespace mk

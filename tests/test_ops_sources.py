@@ -78,3 +78,8 @@ def test_the_pair_meets_at_cluster_scope():
     assert len(re.findall(r"fence\.acquire\.sync_restrict::shared::cluster\.cluster", text)) == sum(".relaxed." in w for w in waits)
     for m in re.finditer(r"mbarrier\.arrive\.relaxed\.cluster", text):   # a release in front of it
         assert re.search(r"fence\.release\.\S*cluster;[^}]*$", text[:m.start()])
+
+
+@pytest.mark.parametrize("name", KERNELS + ["mk_ops.cpp", "mk_ops.h"])
+def test_launches_ask_the_device_for_its_sms(name):
+    assert not re.search(r"\b(148|152)(u|l|ll)?\b", source(name)), "a number of SMs, written down"
