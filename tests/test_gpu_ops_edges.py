@@ -7,6 +7,8 @@ import torch
 import ops_ref as R
 from persistent_moe_decode_cta_gb300 import binding as B
 from persistent_moe_decode_cta_gb300 import ops
+import test_gpu_qk_rope as Rope
+from test_gpu_experts import reference
 from test_gpu_tree_attention import LAYOUTS, check, setup
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +126,109 @@ def test_an_empty_batch_is_no_work():
     ops.copy_pages(k, v, [], [])
     assert torch.equal(k, k0) and torch.equal(v, v0)
     ops.check_status()
+
+
+@pytest.mark.parametrize("heads,n", [((64, 8, 128), 3), ((64, 8, 128), 700), ((256, 128, 32), 5), ((96, 96, 64), 40), ((400, 4, 128), 9)])
+def test_rotation_of_many_heads(heads, n):
+    """More heads than the threads of a block: several blocks share a token."""
+    Rope.check(heads, [3, 40], n, counts=[n, n - 1])
+    Rope.check(heads, [0], n, norm=False, packed=False, in_place=True)
+
+
+@pytest.mark.parametrize("layers,pages,hkv,hd,n", [(2, 40, 8, 128, 15), (3, 20, 9, 128, 7), (1, 10, 33, 128, 5), (2, 90, 40, 64, 41)])
+def test_copies_of_large_pages(layers, pages, hkv, hd, n):
+    """Pages above 16 KB: several blocks a page, the last of them with less than the others."""
+    g = R.gen(pages)
+    k, v = (R.bf16(g, layers, pages, hkv, 16, hd) for _ in range(2))
+    ids = torch.randperm(pages, generator=g, device="cuda").tolist()
+    src, dst = ids[:n], ids[n:2 * n]
+    ek, ev = k.clone(), v.clone()
+    ek[:, dst] = k[:, src]
+    ev[:, dst] = v[:, src]
+    ops.copy_pages(k, v, src, dst)
+    assert torch.equal(k, ek) and torch.equal(v, ev)
+
+
+def ragged(batch, far):
+    """Short lengths, some of them zero, and `far` sequences of several thousand keys, the last among them."""
+    lens = [(53 * i * i) % 190 * (i % 5 != 0) for i in range(batch)]
+    for i in range(far):
+        lens[batch - 1 - i * (batch // far)] = 2500 + 1300 * i
+    return lens
+
+
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("heads,n,batch", [((4, 1, 32), 2, 128), ((4, 1, 32), 2, 129), ((4, 2, 64), 3, 256), ((4, 2, 64), 3, 257),
+                                           ((4, 1, 32), 70, 300), ((2, 1, 128), 1, 1000), ((8, 2, 32), 2, 1000)])
+def test_long_lists_of_sequences(heads, n, batch, window):
+    """Work lists of more than one entry a thread, and of more than the join adds up itself."""
+    counts = [0 if i % 7 == 3 else 1 + i % n for i in range(batch)]
+    check(setup(heads, ragged(batch, 4), n, counts=counts), window)
+    check(setup(heads, ragged(batch, 1), n, tree=False, counts=counts), window)
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+def test_long_chunks(window):
+    """A chunk whose groups of nodes are more than 256 entries, beside a short one."""
+    check(setup((8, 1, 32), [100], 8300, tree=False), window)
+    check(setup((16, 1, 32), [40, 3], 2100, tree=False, counts=[2099, 1300]), window)
+
+
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("offsets,rows,owner", [
+    ([0, 9, 12], None, [0] * 8), ([-3, 2, 8], None, [0] * 2 + [1] * 6), ([4, 2, 8], None, [None] * 2 + [1] * 6),
+    ([2 ** 31 - 1, -2 ** 31, 5], None, [1] * 5 + [None] * 3), ([0, 4, 8], [0, 1, 2, 3, 4, 5, 6, 8], [0] * 4 + [1] * 4),
+    ([0, 4, 8], [0, 1, -2 ** 31, 3, 4, 2 ** 31 - 1, 6, 7], [0] * 4 + [1] * 4)])
+def test_bad_offsets_and_rows_stay_inside(offsets, rows, owner, named):
+    """Beyond the error: rows that belong to an expert are those of the clamped numbers, all others as they were."""
+    g = R.gen(5)
+    x, w = R.bf16(g, 8, 64), R.bf16(g, 2, 40, 64)
+    base = torch.full((24, 40), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = base[8:16]
+    if rows is None and named:
+        rows = list(range(8))
+    r = None if rows is None else torch.tensor(rows, dtype=torch.int32, device="cuda")
+    status = ops.new_status()
+    ops.expert_product(x, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), rows=r, out=out, status=status)
+    with pytest.raises(B.MkError) as e:
+        ops.check_status(status)
+    assert e.value.code == B.MK_ERR_INVALID
+    ends = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    at = torch.arange(8, device="cuda") if rows is None else torch.tensor(rows, device="cuda").clamp(0, 7)
+    want, bound = zip(*(reference(x[at], w[i:i + 1], ends, None, None) for i in range(2)))
+    for i, e in enumerate(owner):
+        if e is None:
+            assert bool((out[i] == 3.0).all())
+        else:
+            R.assert_close(out[i], want[e][i], bound[e][i], f"row {i}")
+    assert bool((base[:8] == 3.0).all() and (base[16:] == 3.0).all())
+
+
+@pytest.mark.parametrize("n", [3, 70])
+@pytest.mark.parametrize("heads", LAYOUTS)
+def test_bad_pages_and_lengths_of_one_sequence(heads, n):
+    """A bad page is read as page 0, a sequence of a bad length left out; the other sequence has its bits."""
+    a = setup(heads, [900, 433], n)
+    a["k_cache"].nan_to_num_(nan=0.5), a["v_cache"].nan_to_num_(nan=0.5)
+    fine = ops.tree_attention(**a)
+    table, status = a["page_table"], ops.new_status()
+    keep = table.clone()
+    table[0, 1] = 0
+    zero = ops.tree_attention(**a)
+    for bad in (-1, a["k_cache"].shape[0], 2 ** 31 - 1, -2 ** 31):
+        table[0, 1] = bad
+        got = ops.tree_attention(**a, status=status)
+        assert torch.equal(got, zero) and torch.equal(got[1], fine[1])
+        with pytest.raises(B.MkError, match="MK_ERR_BAD_PAGE"):
+            ops.check_status(status)
+    table.copy_(keep)
+    for length, count in ((-1, n), (16 * table.shape[1] - n + 1, n), (900, n + 1), (2 ** 31 - 1, n), (0, 2 ** 31 - 1)):
+        bad = dict(a, seq_lens=torch.tensor([length, 433], dtype=torch.int32, device="cuda"),
+                   counts=torch.tensor([count, n], dtype=torch.int32, device="cuda"))
+        out = torch.full_like(a["q"], 5.0)
+        ops.tree_attention(**bad, out=out, status=status)
+        assert bool((out[0] == 5.0).all())
+        want, bound = R.attention(a["q"], a["k_cache"], a["v_cache"], table, a["seq_lens"], a["mask"], a["positions"])
+        R.assert_close(out[1], want[1], bound[1])
+        with pytest.raises(B.MkError, match="MK_ERR_INVALID"):
+            ops.check_status(status)
