@@ -232,3 +232,28 @@ def test_bad_pages_and_lengths_of_one_sequence(heads, n):
         R.assert_close(out[1], want[1], bound[1])
         with pytest.raises(B.MkError, match="MK_ERR_INVALID"):
             ops.check_status(status)
+
+
+def test_pages_whose_offsets_pass_32_bits():
+    """The same tokens in a pool of 40 pages and in the last pages of pools of 10 GB a layer: equal bits."""
+    g = R.gen(12)
+    far, pages, hkv, hd, n, lens = 600_000, 40, 4, 128, 9, [300, 77]
+    small = [R.bf16(g, 2, pages, hkv, 16, hd) for _ in range(2)]
+    large = [torch.empty(2, far, hkv, 16, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for a, b in zip(small, large):
+        b[:, far - pages:] = a
+    table = torch.randperm(pages, generator=g, device="cuda")[:pages // 2 * 2].view(2, -1).to(torch.int32)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q, kn, vn = R.bf16(g, 2, n, 32, hd), R.bf16(g, 2, n, hkv, hd), R.bf16(g, 2, n, hkv, hd)
+    acc = torch.tensor([[1, 4, 8], [0, 2, -1]], dtype=torch.int32, device="cuda")
+    src, dst = table[0, :5].tolist(), table[1, -5:].tolist()
+    got = []
+    for (k, v), first in ((small, 0), (large, far - pages)):
+        t = table + first
+        r = [ops.qk_norm_rope(q, kn, vn, k[l], v[l], t, sl, theta=1e6) for l in range(2)]
+        r += [ops.tree_attention(r[l], k[l], v[l], t, sl) for l in range(2)]
+        r.append(ops.commit_nodes(k, v, t, sl, acc))
+        ops.copy_pages(k, v, [first + p for p in src], [first + p for p in dst])
+        got.append(r + [k[:, first:first + pages].clone(), v[:, first:first + pages].clone()])
+    ops.check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
