@@ -142,7 +142,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mk_destroy.argtypes = [H]
     lib.mk_destroy.restype = None
     lib.mk_version.argtypes = []
-    # (structs as void*: ops.py passes them packed)
+    # (structs as void*; ops.py goes through the module _ops, which fills them itself)
     lib.mk_qk_norm_rope.argtypes = [vp, vp, vp]
     lib.mk_tree_attention.argtypes = [vp, vp, vp]
     lib.mk_tree_attention_workspace.argtypes = [vp, vp, ctypes.POINTER(sz)]

@@ -26,8 +26,9 @@
 // into L2 10 stages ahead of the ring: 154 us against 131 for 8 rows an expert.)
 // Accumulation is fp32; the result is rounded once.
 //
-// Measured: 4096 tokens as above 175 us (1.18 PFLOP/s and 5.0 TB/s: both bound it), 128 tokens 122 us
-// (6.6 TB/s), the down products (768 -> 2048) of 2 tokens 12.7 us, of which weights stream for 5.5.
+// Measured in a graph: 4096 tokens as above 177 to 180 us (1.15 PFLOP/s and 4.9 TB/s: both bound it; called back
+// to back 190 to 200, the clock falls under the power cap), 128 tokens 123 us (6.6 TB/s), the down products
+// (768 -> 2048) of 2 tokens 12.7 us, of which weights stream for 5.5, of 4096 tokens 108 us.
 #include "mk_ops.cuh"
 
 namespace mk {

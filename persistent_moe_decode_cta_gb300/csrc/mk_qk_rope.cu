@@ -17,7 +17,7 @@ namespace mk {
 namespace {
 
 constexpr int kRopeMaxThreads = 512;
-constexpr int kRopeMost = 12;            // tokens behind one another in a block, at most
+constexpr int kRopeMost = 12;            // tokens behind one another in a block, at most (8002 tokens 31.0 us; 6: 31.4, 24: 33.6)
 constexpr int kRopeSmem = 16 * 1024;     // ... and of their angles
 
 struct Head8 {  // values 8j..8j+7 of the lower and of the upper half of a head

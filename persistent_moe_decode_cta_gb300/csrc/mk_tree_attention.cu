@@ -7,7 +7,9 @@
 // r % gs, so that the gs heads of a group share every key that is read.  A tile has 128
 // rows, the M of one tcgen05.mma; S = Q K^T and O += P V both run on the tensor cores with
 // accumulators in tensor memory, P goes back there as bf16 (A operand), and the thread that
-// owns a row (lane) keeps its maximum and sum.  Keys come in blocks of 128 (8 pages), each
+// owns a row (lane) keeps its maximum and sum.  (P and V of one product have one type, and V is
+// bf16: each weight is rounded to 8 bits, in the sum it keeps its 24.  Against float64 the results are
+// 0.0021 to 0.0024 off, relative; their own rounding alone is 0.0017.)  Keys come in blocks of 128 (8 pages), each
 // page by its own tensor-map copy, into a ring shared by K and V.
 //
 // Two softmax warpgroups ("streams") alternate so that one's exponentials run beside the
@@ -34,15 +36,15 @@
 // queries, the empty pipeline and one more result.  (Without them the 31 of 152 CTAs whose run holds a
 // border of 8 sequences' items end 8 us after the others: 58.4 us against 51.3 for 16 nodes of 8 ragged
 // sequences, 18.6 against 15.7 for one node at 8K, 332 against 152 for a prompt of 4096, whose first items
-// are short.  3 to 8 are within 3% of one another.)  (Up
+// are short, when that was changed.  3 to 8 are within 3% of one another.)  (Up
 // to 8 tile groups form a team instead: each run is walked by one CTA per group at the same
 // time, so that the keys come from HBM once and from L2 for the others.)  A run that covers
 // only part of an item's keys leaves (O, m, sum) in the workspace and a second kernel joins
 // the parts in order of their keys; at most a run's first and last item are such.
 //
-// Measured, 32 query heads and 4 KV heads of 128: 16 nodes at 32K of 8 sequences 96 us (5.6 TB/s), 64 nodes
-// 196 us (1.41 PFLOP/s), 2001 nodes of a chunk at 8K 222 us (1.36 PFLOP/s), one node at 8K of one sequence
-// 15.0 us, 8 nodes at 2K of the small model 11.3 us (latencies).
+// Measured, 32 query heads and 4 KV heads of 128: 16 nodes at 32K of 8 sequences 97 us (5.6 TB/s), 64 nodes
+// 198 us (1.39 PFLOP/s), 2001 nodes of a chunk at 8K 224 us (1.34 PFLOP/s), one node at 8K of one sequence
+// 16.7 us, 8 nodes at 2K of the small model 12.7 us (latencies).
 #include "mk_ops.cuh"
 
 #include <type_traits>
@@ -979,7 +981,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // fewer than nine: GROUPS = 1, and four pieces per thread where that still leaves every SM its blocks.
 // A block adds up a work list of up to 256 entries itself; the lengths are read behind the wait like
 // everything else: that the first kernel's blocks had waited before they triggered makes them final, not
-// visible to this kernel.
+// visible to this kernel.  (Read in front of the wait they saved 1.2 us of the 12.7 that 8 nodes at 2K of one
+// sequence take.)
 
 template <int HD, int GROUPS, int PIECES>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p) {
@@ -1139,7 +1142,12 @@ cudaError_t launch_hd(const TreeParams& p, const CUtensorMap& tq, const CUtensor
   if (e != cudaSuccess) return e;
   if (p.c.max_pages <= kBlk / kOpPage) return cudaSuccess;  // items of one block: nothing is split
   const long long heads = (long long)p.c.batch * p.c.n_kv_heads * p.ntp;
-  const bool many = 8 * heads > p.grid;  // up to 9 parts an item
+  // One group of threads where an item has up to 9 parts (512 nodes of 8 sequences 145 us, with four groups
+  // 355; 16 nodes at 32K of 8 sequences 97.0, 103.4), four where it has more (one node at 8K of one sequence
+  // 16.7 us, with one group 23.0).  Four pieces a thread where that leaves every SM four blocks (chunk of 2001 at
+  // 8K 224 us, with one piece 240; prompt of 4096 155, 185), else one (8 ragged sequences of 16 nodes 58.0, with
+  // four 60.5).
+  const bool many = 8 * heads > p.grid;
   const long long all = heads * (p.two ? 2 : 1) * p.npt * p.gs * (HD / 4);  // pieces of all items
   const bool four = many && all > 4ll * kJoinThreads * p.grid * 4;
   const int pieces = four ? 4 * kJoinThreads : many ? kJoinThreads : kJoinThreads / 4;
