@@ -162,10 +162,15 @@ def measured_peaks():
 NOMINAL_HBM_GBS = 7900.0  # GB300 HBM3e, spec sheet
 
 
+# what the decode step is built from (its plan is the host's; the operators beside it have no part in it)
+STEP_SOURCES = ("mk_device.cuh", "mk_host.cpp", "mk_internal.h", "mk_kernel.cu", "mk_kernel_det.cu", "mk_kernel_umma.cu",
+                "mk_kernel_umma_ffn.cu")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "persistent_moe_decode_cta_gb300", "csrc")
-    for n in sorted(os.listdir(csrc)):
+    for n in STEP_SOURCES:
         with open(os.path.join(csrc, n), "rb") as f:
             h.update(n.encode() + f.read())
     return h.hexdigest()[:16]
