@@ -401,8 +401,9 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  * or run prompt chunks on the cache that mk_decode_step reads: append the new nodes' keys
  * and values (mk_qk_norm_rope), attend over the cache and the draft tree
  * (mk_tree_attention), multiply by the routed experts' matrices (mk_expert_product), then
- * keep the accepted path (mk_commit_nodes); mk_copy_pages copies pages for a fork.  The
- * pages have no counterpart to them.  They need no handle and read plain (unpacked) bf16
+ * keep the accepted path (mk_commit_nodes); mk_copy_pages copies pages for a fork.  mk_linear
+ * has the projections and the LM head, mk_moe_layer the routed layer of a few tokens as a whole,
+ * and mk_verify_nodes decides which drafted tokens are accepted.  The pages have no counterpart to them.  They need no handle and read plain (unpacked) bf16
  * tensors.
  *
  * Conventions beside the ones above:
@@ -564,6 +565,111 @@ typedef struct mk_expert_args {
   int32_t n_x, n_rows, n_experts, n, k;
 } mk_expert_args;
 int mk_expert_product(const mk_expert_args* args, void* stream);
+
+/* Products with an epilogue, of the layers' projections (QKV, attention output, dense FFN) and
+ * the LM head over several tokens:
+ *   out = act(x W^T + bias) + residual
+ *   x         bf16 [m][k], row stride x_stride elements (a multiple of 8)
+ *   w         bf16 [n][k] contiguous; k a multiple of 8; x and w 16-byte aligned
+ *   bias      bf16 [n] or NULL
+ *   residual  bf16 [m][n], row stride residual_stride elements, or NULL
+ *   out       [m][n], row stride out_stride elements: bf16, or float32 when out_float is not 0.  It may
+ *             be the residual itself (same address, stride and type); it overlaps nothing else
+ *   activation  MK_ACT_NONE, _RELU, _SILU (y / (1 + exp(-y))), _GELU (y/2 (1 + erf(y / sqrt 2))) or
+ *             _GELU_TANH (y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))))
+ * fp32 accumulation in a fixed order (equal calls give equal bits), one rounding. */
+enum { MK_ACT_NONE = 0, MK_ACT_RELU = 1, MK_ACT_SILU = 2, MK_ACT_GELU = 3, MK_ACT_GELU_TANH = 4 };
+typedef struct mk_linear_args {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* out;
+  int32_t* status;
+  int64_t x_stride, residual_stride, out_stride;
+  int32_t m, n, k, activation, out_float;
+} mk_linear_args;
+int mk_linear(const mk_linear_args* args, void* stream);
+
+/* The whole routed layer of a few tokens (n_tokens <= 256; more go through mk_expert_product):
+ *   s = x Wr^T;  ids = the top_k largest s, ties to the lower expert;  c = softmax of those s
+ *   out = residual + sum_j c_j Wd[ids_j] (silu(Wg[ids_j] x) * (Wu[ids_j] x))
+ *   x, residual, out  bf16 [n_tokens][d_model], row strides in elements (x: a multiple of 8); residual may
+ *             be NULL, and out may be the residual itself (same address and stride); out overlaps nothing else
+ *   router    bf16 [n_experts][d_model]
+ *   w_gate, w_up  bf16 [n_experts][d_ff][d_model];  w_down  bf16 [n_experts][d_model][d_ff]
+ *             x, router and the weights 16-byte aligned, d_model and d_ff multiples of 8
+ *   ids, weights  int32, float32 [n_tokens][top_k] or NULL: where the selection and c go, in order of s
+ *   workspace mk_moe_layer_workspace(..) bytes, 16-byte aligned, not shared with a call that may run at
+ *             the same time; its contents do not matter
+ * The scores are sums of exact products good to 2^-40 of the sum of their sizes, so that the selection is that of the
+ * formula.  A NaN score counts as the largest.  c times the product of gate and up is rounded to bf16, everything else is
+ * fp32 until the one rounding of out.  The sums have a fixed order: equal calls give equal bits.
+ * n_experts in 1..256, top_k in 1..min(16, n_experts). */
+typedef struct mk_moe_args {
+  const void* x;
+  const void* router;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* residual;
+  void* out;
+  int32_t* ids;
+  float* weights;
+  int32_t* status;
+  int64_t x_stride, residual_stride, out_stride;
+  int32_t n_tokens, d_model, d_ff, n_experts, top_k;
+  void* workspace;
+  size_t workspace_bytes;
+} mk_moe_args;
+int mk_moe_layer(const mk_moe_args* args, void* stream);
+int mk_moe_layer_workspace(const mk_moe_args* args, size_t* bytes);
+
+/* Which drafted nodes the target model accepts, from given random numbers, and its next token.
+ * Node 0 of a sequence is its last sampled token (not yet cached; always kept), the nodes i > 0 a tree of
+ * drafted tokens with parents[b][i] < i.  logits[b][i] are the target's for the token after node i.
+ *   p = softmax(logits[b][v] / temperature[b]); temperature 0: 1 at the largest logit (the lowest index of
+ *   equal ones)
+ * From v = 0 on, the children of v in order of their index: child i with token x is accepted, and becomes v, if
+ *   uniforms[b][i] * q(x) < p(x),          q = draft_probs[b][v]: what the children were drawn from, one
+ *                                          by one; draft_probs NULL: q is 1 at x
+ * else p <- (p - q)+ / sum (p - q)+, or p as it is where that is empty.  Where no child is accepted, next_tokens[b]
+ * is the lowest index at which the running sum of p exceeds uniforms[b][0] times the whole sum.  The accepted tokens and
+ * the next one together are distributed as the target's own.
+ *   logits    [batch][n_nodes][vocab] bf16, or float32 when logits_float is not 0; strides in elements of the
+ *             first two dimensions; -infinity excludes a token
+ *   draft_probs  float32 [batch][n_nodes][vocab], strides likewise, values in [0, 1] (others are clamped), or NULL
+ *   tokens, parents  int32 [batch][n_nodes]; parents NULL: a chain.  parents[b][0] and tokens[b][0] are not read
+ *   uniforms  float32 [batch][n_nodes] in [0, 1)
+ *   temperature  float32 [batch], >= 0, or NULL (1)
+ *   counts    int32 [batch]: nodes of each sequence, in 1..n_nodes, or NULL (n_nodes for all)
+ *   accepted  int32 [batch][n_nodes]: the accepted nodes, 0 first, then -1 (mk_commit_nodes' argument)
+ *   next_tokens  int32 [batch]; neither output overlaps an input
+ *   workspace mk_verify_nodes_workspace(..) bytes, 16-byte aligned, not shared with a call that may run at
+ *             the same time; its contents do not matter
+ * The sums that a token is drawn from are exact sums of 64-bit integers (each probability to 2^-40 of itself or 2^-44 of
+ * the largest), so neither the split of the work nor the order changes a result.
+ * vocab in 1..262144, n_nodes in 1..512 (as mk_commit_nodes).  A row of p without a finite largest logit or with a NaN, a count,
+ * parent, token, temperature or uniform out of its range is recorded (MK_ERR_INVALID; sequence, node, value); such a child is
+ * passed over, a sequence whose count, temperature or p is bad ends there with next_tokens[b] = -1. */
+typedef struct mk_verify_args {
+  const void* logits;
+  const float* draft_probs;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* uniforms;
+  const float* temperature;
+  const int32_t* counts;
+  int32_t* accepted;
+  int32_t* next_tokens;
+  int32_t* status;
+  int64_t logits_stride[2], draft_stride[2];
+  int32_t batch, n_nodes, vocab, logits_float;
+  void* workspace;
+  size_t workspace_bytes;
+} mk_verify_args;
+int mk_verify_nodes(const mk_verify_args* args, void* stream);
+int mk_verify_nodes_workspace(const mk_verify_args* args, size_t* bytes);
 
 /* The current device's own record, of the calls whose status was NULL: copied to status_out
  * (HOST int32[4], zeros where nothing was recorded) and, if something was, cleared.

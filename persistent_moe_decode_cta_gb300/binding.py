@@ -25,6 +25,7 @@ MK_READ_HIDDEN, MK_READ_ROUTES, MK_READ_ROUTE_W, MK_READ_ACTIVE = 1, 2, 3, 4
 MK_READ_SEQ_LENS, MK_READ_COUNTERS, MK_READ_ROUTER_LOGITS, MK_READ_TRACE_COUNT = 5, 6, 7, 8
 MK_READ_FINAL_COUNTERS, MK_READ_FINAL_QUEUES, MK_READ_TASKS = 9, 10, 11
 MK_EXPERT_BF16, MK_EXPERT_FP8, MK_WEIGHTS_FP8 = 0, 1, 2
+MK_ACT_NONE, MK_ACT_RELU, MK_ACT_SILU, MK_ACT_GELU, MK_ACT_GELU_TANH = range(5)
 (MK_Q_NUM_SMS, MK_Q_NUM_TASKS, MK_Q_NUM_COUNTERS, MK_Q_PACKED_BYTES, MK_Q_MAX_ACTIVE,
  MK_Q_SPLIT_PAGES, MK_Q_SMEM_BYTES, MK_Q_PEROP_LAUNCHES, MK_Q_THREADS, MK_Q_STAGE_BYTES,
  MK_Q_NUM_STAGES, MK_Q_TENSOR_CORES) = range(1, 13)
@@ -35,7 +36,8 @@ EXPORTS = ["mk_create", "mk_plan", "mk_decode_step", "mk_decode_steps", "mk_deco
            "mk_plan_drop_signal", "mk_read", "mk_read_expert_fp8", "mk_read_weight_fp8", "mk_query",
            "mk_plan_dry", "mk_last_error", "mk_destroy", "mk_version",
            "mk_qk_norm_rope", "mk_tree_attention", "mk_tree_attention_workspace", "mk_copy_pages", "mk_commit_nodes",
-           "mk_expert_product", "mk_op_status"]
+           "mk_expert_product", "mk_linear", "mk_moe_layer", "mk_moe_layer_workspace", "mk_verify_nodes",
+           "mk_verify_nodes_workspace", "mk_op_status"]
 
 
 class MkError(RuntimeError):
@@ -104,6 +106,34 @@ class mk_expert_args(ctypes.Structure):
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32)]
 
 
+class mk_linear_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("status", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("activation", ctypes.c_int32), ("out_float", ctypes.c_int32)]
+
+
+class mk_moe_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("router", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("status", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("n_tokens", ctypes.c_int32),
+                ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_S2 = ctypes.c_int64 * 2
+
+
+class mk_verify_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p), ("uniforms", ctypes.c_void_p), ("temperature", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("accepted", ctypes.c_void_p), ("next_tokens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("logits_stride", _S2), ("draft_stride", _S2), ("batch", ctypes.c_int32),
+                ("n_nodes", ctypes.c_int32), ("vocab", ctypes.c_int32), ("logits_float", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -149,6 +179,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mk_copy_pages.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
     lib.mk_commit_nodes.argtypes = [vp, i32, vp, i32, vp, vp, vp]
     lib.mk_expert_product.argtypes = [vp, vp]
+    lib.mk_linear.argtypes = [vp, vp]
+    lib.mk_moe_layer.argtypes = [vp, vp]
+    lib.mk_moe_layer_workspace.argtypes = [vp, ctypes.POINTER(sz)]
+    lib.mk_verify_nodes.argtypes = [vp, vp]
+    lib.mk_verify_nodes_workspace.argtypes = [vp, ctypes.POINTER(sz)]
     lib.mk_op_status.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
     for name in EXPORTS:
         if name not in ("mk_last_error", "mk_destroy"):

@@ -1,5 +1,6 @@
 // Matrix products grouped by expert:  out[r] = x[rows[r]] W_e^T  for the rows r of expert e,
-// or silu(x W_e^T) * (x U_e^T) with two weight sets.
+// or silu(x W_e^T) * (x U_e^T) with two weight sets.  And, with one expert that has every row, products with
+// an epilogue:  out = act(x W^T + bias) + residual.
 //
 // The weights are the M side of the tcgen05 products and the rows the N side, so that a
 // ragged group costs what its rows cost (N in steps of 32) and an expert with few rows is one
@@ -30,6 +31,7 @@
 // to back 190 to 200, the clock falls under the power cap), 128 tokens 123 us (6.6 TB/s), the down products
 // (768 -> 2048) of 2 tokens 12.7 us, of which weights stream for 5.5, of 4096 tokens 108 us.
 #include "mk_ops.cuh"
+#include "mk_linear.cuh"
 
 namespace mk {
 namespace {
@@ -188,6 +190,8 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& l
   if (blockIdx.x == 0 && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
 }
 
+// (EPI: one expert with every row)
+template <bool EPI>
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
   int carry = 0;
@@ -195,8 +199,8 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
     const int e = base + (int)threadIdx.x;
     int x = 0;
     if (e < E) {
-      int lo, hi;
-      expert_rows(p, e, lo, hi);
+      int lo = 0, hi = p.a.n_rows;
+      if (!EPI) expert_rows(p, e, lo, hi);
       sh.rows[e] = make_int2(lo, hi);
       x = (hi - lo + kTileR - 1) / kTileR;
       if (hi > lo) atomicMax(&sh.most, hi - lo);
@@ -238,11 +242,11 @@ __device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& s
 
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-template <bool GLU>
+template <bool GLU, bool EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGatherThreads, 1)
     expert_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ CUtensorMap tx,
                   const __grid_constant__ CUtensorMap tx128, const __grid_constant__ CUtensorMap tw,
-                  const __grid_constant__ CUtensorMap tu) {
+                  const __grid_constant__ CUtensorMap tu, const __grid_constant__ LinearEpi epi) {
   extern __shared__ uint8_t raw[];
   __shared__ ExpShared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -282,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  scan_experts(p, sh);
+  scan_experts<EPI>(p, sh);
   const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
@@ -444,8 +448,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       tc_fence_after();
       uint32_t u[kChunk];
       tmem_ld32(acc, u);
+      if (EPI) {
 #pragma unroll 1
-      for (int c = 0; c < x.nr; c += kChunk, ++nc) {
+        for (int c = 0; c < x.nr; c += kChunk) {
+          float v[kChunk];
+          tmem_wait32(u);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(u[i]);
+          if (c + kChunk >= x.nr) {  // read: the next products may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_leader(aempty(a)));
+          } else {
+            tmem_ld32(acc + c + kChunk, u);
+          }
+          linear_store(p.a, epi, v, x.r0 + c, min(kChunk, x.nr - c), w0, width,
+                       reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + q * kChunk * 32, lane);
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; !EPI && c < x.nr; c += kChunk, ++nc) {
         float v[kTake];
         tmem_wait32(u);
         if (GLU) {
@@ -502,21 +524,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   }
 }
 
-template <bool GLU>
-cudaError_t launch_glu(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
-                       const CUtensorMap& tu, cudaStream_t st) {
+template <bool GLU, bool EPI>
+cudaError_t launch_kind(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
+                        const CUtensorMap& tu, const LinearEpi& epi, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(expert_kernel<GLU>, kExpSmem, done);
+  const cudaError_t e = allow_smem(expert_kernel<GLU, EPI>, kExpSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_early(expert_kernel<GLU>, dim3((unsigned)(p.grid / 2 * 2)), kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem, st,
-                      p, tx, tx128, tw, tu);
+  return launch_early(expert_kernel<GLU, EPI>, dim3((unsigned)(p.grid / 2 * 2)), kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem,
+                      st, p, tx, tx128, tw, tu, epi);
 }
 
 }  // namespace
 
 cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                            const CUtensorMap& tu, cudaStream_t st) {
-  return p.a.w_up ? launch_glu<true>(p, tx, tx128, tw, tu, st) : launch_glu<false>(p, tx, tx128, tw, tu, st);
+  const LinearEpi none{};
+  return p.a.w_up ? launch_kind<true, false>(p, tx, tx128, tw, tu, none, st) : launch_kind<false, false>(p, tx, tx128, tw, tu, none, st);
+}
+
+cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, const CUtensorMap& tx, const CUtensorMap& tx128,
+                                const CUtensorMap& tw, cudaStream_t st) {
+  return launch_kind<false, true>(p, tx, tx128, tw, tw, epi, st);
 }
 
 }  // namespace mk

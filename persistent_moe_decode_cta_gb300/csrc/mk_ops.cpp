@@ -133,6 +133,44 @@ int tree_shape(const mk_paged_kv* c, const mk_tree_args* a, TreeParams& p) {
   return MK_OK;
 }
 
+// A [rows][width] operand in memory, in bytes, and whether two of them share any.
+struct Rows {
+  uintptr_t at;
+  unsigned long long rows, width, stride;
+};
+Rows rows_of(const void* p, long long rows, long long width, long long stride, int size) {
+  return {reinterpret_cast<uintptr_t>(p), (unsigned long long)rows, (unsigned long long)width * size, (unsigned long long)stride * size};
+}
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.rows || !b.rows || !a.width || !b.width) return false;
+  const uintptr_t a1 = a.at + (a.rows - 1) * a.stride + a.width, b1 = b.at + (b.rows - 1) * b.stride + b.width;
+  if (a1 <= b.at || b1 <= a.at) return false;
+  if (a.rows == 1 || b.rows == 1 || a.stride != b.stride) return true;
+  // columns of the same rows (two halves of one tensor) may lie between one another
+  const unsigned long long d = b.at >= a.at ? (b.at - a.at) % a.stride : (a.stride - (a.at - b.at) % a.stride) % a.stride;
+  return !(a.width <= d && d + b.width <= a.stride);
+}
+
+int check_moe(const mk_moe_args* a) {
+  if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
+  if (a->n_tokens < 0) return op_fail(MK_ERR_INVALID, "n_tokens %d < 0", a->n_tokens);
+  if (a->n_tokens > kMoeTokens) return op_fail(MK_ERR_UNSUPPORTED, "n_tokens %d > %d (mk_expert_product takes more)", a->n_tokens, kMoeTokens);
+  if (a->n_experts < 1 || a->n_experts > kOpMaxExperts) return op_fail(MK_ERR_INVALID, "n_experts %d not in [1, %d]", a->n_experts, kOpMaxExperts);
+  if (a->top_k < 1 || a->top_k > kMoeTopK || a->top_k > a->n_experts)
+    return op_fail(MK_ERR_INVALID, "top_k %d not in [1, min(%d, n_experts)]", a->top_k, kMoeTopK);
+  if (a->d_model < 8 || a->d_model % 8 || a->d_model > (1 << 16) || a->d_ff < 8 || a->d_ff % 8 || a->d_ff > (1 << 16))
+    return op_fail(MK_ERR_UNSUPPORTED, "d_model %d and d_ff %d must be multiples of 8 in [8, 65536]", a->d_model, a->d_ff);
+  return MK_OK;
+}
+
+int check_verify(const mk_verify_args* a) {
+  if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
+  if (a->batch < 0 || a->batch > kOpMaxBatch) return op_fail(MK_ERR_INVALID, "batch %d not in [0, %d]", a->batch, kOpMaxBatch);
+  if (a->n_nodes < 1 || a->n_nodes > kOpMaxAccept) return op_fail(MK_ERR_INVALID, "n_nodes %d not in [1, %d]", a->n_nodes, kOpMaxAccept);
+  if (a->vocab < 1 || a->vocab > kVerifyVocab) return op_fail(MK_ERR_INVALID, "vocab %d not in [1, %d]", a->vocab, kVerifyVocab);
+  return MK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -341,6 +379,169 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   if (!r) r = set_record(p.a.status);
   if (r) return r;
   return cuda_error(launch_experts(p, tx, tx128, tw, tu, static_cast<cudaStream_t>(stream)), "expert_product launch");
+}
+
+int mk_linear(const mk_linear_args* a, void* stream) {
+  if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
+  if (a->m < 0 || a->m > (1 << 28)) return op_fail(MK_ERR_INVALID, "m %d not in [0, 2^28]", a->m);
+  if (a->n < 1 || a->n > (1 << 24)) return op_fail(MK_ERR_INVALID, "n %d not in [1, 2^24]", a->n);
+  if (a->k < 8 || a->k % 8 || a->k > (1 << 24)) return op_fail(MK_ERR_UNSUPPORTED, "k %d is not a positive multiple of 8", a->k);
+  if (a->activation < MK_ACT_NONE || a->activation > MK_ACT_GELU_TANH) return op_fail(MK_ERR_INVALID, "activation %d is not known", a->activation);
+  if (a->m == 0) return MK_OK;
+  if (!a->x || !a->w || !a->out) return op_fail(MK_ERR_INVALID, "NULL pointer");
+  if (!aligned16(a->x) || !aligned16(a->w)) return op_fail(MK_ERR_INVALID, "x and w must be 16-byte aligned");
+  if (a->x_stride < a->k || a->x_stride % 8 || a->x_stride >= (1ll << 38))
+    return op_fail(MK_ERR_INVALID, "x_stride %lld: need a multiple of 8, at least k", (long long)a->x_stride);
+  if (a->out_stride < a->n || a->out_stride >= (1ll << 38)) return op_fail(MK_ERR_INVALID, "out_stride %lld < n", (long long)a->out_stride);
+  if (a->residual && (a->residual_stride < a->n || a->residual_stride >= (1ll << 38)))
+    return op_fail(MK_ERR_INVALID, "residual_stride %lld < n", (long long)a->residual_stride);
+  const int size = a->out_float ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(a->out) % size || reinterpret_cast<uintptr_t>(a->bias) % 2 || reinterpret_cast<uintptr_t>(a->residual) % 2)
+    return op_fail(MK_ERR_INVALID, "out, bias and residual must be aligned to their values");
+  if (((long long)a->m / 128 + 1) * (((long long)a->n + 255) / 256) >= 0x7fffffffll - 1024)
+    return op_fail(MK_ERR_UNSUPPORTED, "more than 2^31 tiles");
+  const Rows out = rows_of(a->out, a->m, a->n, a->out_stride, size);
+  if (overlap(out, rows_of(a->x, a->m, a->k, a->x_stride, 2)) || overlap(out, rows_of(a->w, a->n, a->k, a->k, 2)) ||
+      (a->bias && overlap(out, rows_of(a->bias, 1, a->n, a->n, 2))))
+    return op_fail(MK_ERR_INVALID, "out overlaps x, w or bias");
+  if (a->residual && !(a->residual == a->out && !a->out_float && (a->m == 1 || a->residual_stride == a->out_stride)) &&
+      overlap(out, rows_of(a->residual, a->m, a->n, a->residual_stride, 2)))
+    return op_fail(MK_ERR_INVALID, "out overlaps the residual without being it");
+  ExpertParams p{};
+  p.a.x = a->x;
+  p.a.w = a->w;
+  p.a.out = a->out;
+  p.a.status = a->status;
+  p.a.x_stride = a->x_stride;
+  p.a.out_stride = a->out_stride;
+  p.a.n_x = p.a.n_rows = a->m;
+  p.a.n_experts = 1;
+  p.a.n = a->n;
+  p.a.k = a->k;
+  LinearEpi epi{};
+  epi.bias = static_cast<const uint16_t*>(a->bias);
+  epi.residual = static_cast<const uint16_t*>(a->residual);
+  epi.residual_stride = a->residual_stride;
+  epi.act = a->activation;
+  epi.out_float = a->out_float != 0;
+  epi.vec = a->n % 4 == 0 && a->out_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a->out) % (4 * size) == 0 &&
+            (!a->residual || (a->residual_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a->residual) % 8 == 0));
+  int r = num_sms(&p.grid);
+  if (r) return r;
+  CUtensorMap tx, tx128, tw;
+  cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->m};
+  cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
+  cuuint32_t xb[2] = {64, 32};
+  cuuint32_t xb128[2] = {64, 128};
+  r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = encode(&tx128, a->x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
+  cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, 1};
+  cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
+  cuuint32_t wb[3] = {64, 128, 1};
+  if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = set_record(p.a.status);
+  if (r) return r;
+  return cuda_error(launch_linear_pairs(p, epi, tx, tx128, tw, static_cast<cudaStream_t>(stream)), "linear launch");
+}
+
+int mk_moe_layer_workspace(const mk_moe_args* a, size_t* bytes) {
+  if (!bytes) return op_fail(MK_ERR_INVALID, "bytes is NULL");
+  const int r = check_moe(a);
+  if (r) return r;
+  *bytes = moe_workspace_bytes(*a);
+  return MK_OK;
+}
+
+int mk_moe_layer(const mk_moe_args* a, void* stream) {
+  int r = check_moe(a);
+  if (r) return r;
+  if (a->n_tokens == 0) return MK_OK;
+  if (!a->x || !a->router || !a->w_gate || !a->w_up || !a->w_down || !a->out) return op_fail(MK_ERR_INVALID, "NULL pointer");
+  if (!aligned16(a->x) || !aligned16(a->router) || !aligned16(a->w_gate) || !aligned16(a->w_up) || !aligned16(a->w_down))
+    return op_fail(MK_ERR_INVALID, "x, router and the weights must be 16-byte aligned");
+  if (a->x_stride < a->d_model || a->x_stride % 8 || a->x_stride >= (1ll << 38))
+    return op_fail(MK_ERR_INVALID, "x_stride %lld: need a multiple of 8, at least d_model", (long long)a->x_stride);
+  if (a->out_stride < a->d_model || a->out_stride >= (1ll << 38)) return op_fail(MK_ERR_INVALID, "out_stride %lld < d_model", (long long)a->out_stride);
+  if (a->residual && (a->residual_stride < a->d_model || a->residual_stride >= (1ll << 38)))
+    return op_fail(MK_ERR_INVALID, "residual_stride %lld < d_model", (long long)a->residual_stride);
+  if (reinterpret_cast<uintptr_t>(a->out) % 2 || reinterpret_cast<uintptr_t>(a->residual) % 2 || reinterpret_cast<uintptr_t>(a->ids) % 4 ||
+      reinterpret_cast<uintptr_t>(a->weights) % 4)
+    return op_fail(MK_ERR_INVALID, "out, residual, ids and weights must be aligned to their values");
+  const long long t = a->n_tokens, d = a->d_model, f = a->d_ff, e = a->n_experts, tk = t * a->top_k;
+  const size_t need = moe_workspace_bytes(*a);
+  if (!a->workspace || !aligned16(a->workspace)) return op_fail(MK_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
+  if (a->workspace_bytes < need) return op_fail(MK_ERR_INVALID, "workspace has %zu bytes, needs %zu", a->workspace_bytes, need);
+  // what is written, and what is read or written beside it
+  const Rows writes[4] = {rows_of(a->out, t, d, a->out_stride, 2), rows_of(a->ids, a->ids ? 1 : 0, tk, tk, 4),
+                          rows_of(a->weights, a->weights ? 1 : 0, tk, tk, 4), rows_of(a->workspace, 1, (long long)need, (long long)need, 1)};
+  const Rows reads[6] = {rows_of(a->x, t, d, a->x_stride, 2),       rows_of(a->router, e, d, d, 2),
+                         rows_of(a->w_gate, e * f, d, d, 2),        rows_of(a->w_up, e * f, d, d, 2),
+                         rows_of(a->w_down, e * d, f, f, 2),        rows_of(a->residual, a->residual ? t : 0, d, a->residual_stride, 2)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 6; ++j) {
+      const bool same = i == 0 && j == 5 && a->residual == a->out && (t == 1 || a->residual_stride == a->out_stride);
+      if (!same && overlap(writes[i], reads[j])) return op_fail(MK_ERR_INVALID, "an output or the workspace overlaps an input");
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(writes[i], writes[j])) return op_fail(MK_ERR_INVALID, "outputs and workspace overlap");
+  }
+  MoeParams p{};
+  p.a = *a;
+  r = num_sms(&p.grid);
+  if (!r) r = set_record(p.a.status);
+  if (r) return r;
+  return cuda_error(launch_moe(p, static_cast<cudaStream_t>(stream)), "moe_layer launch");
+}
+
+int mk_verify_nodes_workspace(const mk_verify_args* a, size_t* bytes) {
+  if (!bytes) return op_fail(MK_ERR_INVALID, "bytes is NULL");
+  const int r = check_verify(a);
+  if (r) return r;
+  *bytes = verify_workspace_bytes(*a);
+  return MK_OK;
+}
+
+int mk_verify_nodes(const mk_verify_args* a, void* stream) {
+  int r = check_verify(a);
+  if (r) return r;
+  if (a->batch == 0) return MK_OK;
+  if (!a->logits || !a->tokens || !a->uniforms || !a->accepted || !a->next_tokens) return op_fail(MK_ERR_INVALID, "NULL pointer");
+  const int size = a->logits_float ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(a->logits) % size || reinterpret_cast<uintptr_t>(a->draft_probs) % 4)
+    return op_fail(MK_ERR_INVALID, "logits and draft_probs must be aligned to their values");
+  const long long b = a->batch, n = a->n_nodes, v = a->vocab, dims[2] = {b, n};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t least = i ? v : 1, s = a->logits_stride[i], q = a->draft_stride[i];
+    if (dims[i] > 1 && (s < least || s >= (1ll << 38))) return op_fail(MK_ERR_INVALID, "logits: stride %lld of dimension %d", (long long)s, i);
+    if (a->draft_probs && dims[i] > 1 && (q < least || q >= (1ll << 38)))
+      return op_fail(MK_ERR_INVALID, "draft_probs: stride %lld of dimension %d", (long long)q, i);
+  }
+  const size_t need = verify_workspace_bytes(*a);
+  if (!a->workspace || !aligned16(a->workspace)) return op_fail(MK_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
+  if (a->workspace_bytes < need) return op_fail(MK_ERR_INVALID, "workspace has %zu bytes, needs %zu", a->workspace_bytes, need);
+  const Rows writes[3] = {rows_of(a->accepted, 1, b * n, b * n, 4), rows_of(a->next_tokens, 1, b, b, 4),
+                          rows_of(a->workspace, 1, (long long)need, (long long)need, 1)};
+  const long long span = (b - 1) * (b > 1 ? a->logits_stride[0] : 0) + (n - 1) * (n > 1 ? a->logits_stride[1] : 0) + v;
+  const long long qspan = (b - 1) * (b > 1 ? a->draft_stride[0] : 0) + (n - 1) * (n > 1 ? a->draft_stride[1] : 0) + v;
+  const Rows reads[7] = {rows_of(a->logits, 1, span, span, size),
+                         rows_of(a->draft_probs, a->draft_probs ? 1 : 0, qspan, qspan, 4),
+                         rows_of(a->tokens, 1, b * n, b * n, 4),
+                         rows_of(a->parents, a->parents ? 1 : 0, b * n, b * n, 4),
+                         rows_of(a->uniforms, 1, b * n, b * n, 4),
+                         rows_of(a->temperature, a->temperature ? 1 : 0, b, b, 4),
+                         rows_of(a->counts, a->counts ? 1 : 0, b, b, 4)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& x : reads)
+      if (overlap(writes[i], x)) return op_fail(MK_ERR_INVALID, "an output or the workspace overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(writes[i], writes[j])) return op_fail(MK_ERR_INVALID, "outputs and workspace overlap");
+  }
+  VerifyParams p{};
+  p.a = *a;
+  r = num_sms(&p.grid);
+  if (!r) r = set_record(p.a.status);
+  if (r) return r;
+  return cuda_error(launch_verify(p, static_cast<cudaStream_t>(stream)), "verify_nodes launch");
 }
 
 int mk_op_status(int32_t* status_out, void* stream) {

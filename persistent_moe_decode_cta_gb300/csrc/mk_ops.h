@@ -45,6 +45,25 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters of `ctas` blocks.
+template <class... P, class... A>
+cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int ctas, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kOpPage = 16;            // tokens per cache page
 constexpr int kOpMaxBatch = 65535;     // sequences of one call
 constexpr int kOpMaxEntries = 65536;   // of the attention's work list: sequences x groups of nodes
@@ -105,5 +124,43 @@ struct ExpertParams {
 };
 cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                            const CUtensorMap& tu, cudaStream_t st);
+
+// ------------------------------------------------------------------ linear
+// One expert that has every row, and what happens to its results.  (mk_experts.cu)
+struct LinearEpi {
+  const uint16_t* bias;      // [n] or NULL
+  const uint16_t* residual;  // [m][n] or NULL
+  int64_t residual_stride;
+  int act, out_float;
+  int vec;                   // residual and out can be read and written four values at a time
+};
+cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, const CUtensorMap& tx, const CUtensorMap& tx128,
+                                const CUtensorMap& tw, cudaStream_t st);
+
+// ------------------------------------------------------------------ moe_layer
+constexpr int kMoeTokens = 256;   // tokens of one call
+constexpr int kMoeTopK = 16;
+struct MoeParams {
+  mk_moe_args a;
+  int grid;          // CTAs of the products
+  int rounds, width; // output columns of a CTA: `rounds` blocks of `width` at most
+  int32_t* ids;      // the caller's or the workspace's
+  float* weights;
+  uint16_t* h;       // [tokens * top_k][d_ff] bf16: c * silu(gate) * up
+  uint32_t* sync;    // counters, zeroed by the router
+};
+size_t moe_workspace_bytes(const mk_moe_args& a);
+cudaError_t launch_moe(const MoeParams& p, cudaStream_t st);
+
+// ------------------------------------------------------------------ verify_nodes
+constexpr int kVerifyVocab = 1 << 18;
+struct VerifyParams {
+  mk_verify_args a;
+  int grid;        // SMs
+  float4* parts;   // [batch][n_nodes][pieces] (largest, sum, index of the largest) of a piece of a row
+  int pieces;
+};
+size_t verify_workspace_bytes(const mk_verify_args& a);
+cudaError_t launch_verify(VerifyParams& p, cudaStream_t st);
 
 }  // namespace mk

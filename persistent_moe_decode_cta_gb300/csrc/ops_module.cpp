@@ -75,9 +75,9 @@ T* optional(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef 
   return o == Py_None ? nullptr : need<T>(o, name, type, shape, dev);
 }
 
-// address of a bf16 operand whose last dimension is contiguous; strides of the others
-void* rows(const at::Tensor& t, const char* name, at::IntArrayRef shape, int dev, int64_t* stride) {
-  check(t, name, at::kBFloat16, shape, dev);
+// address of an operand whose last dimension is contiguous; strides of the others
+void* rows(const at::Tensor& t, const char* name, at::IntArrayRef shape, int dev, int64_t* stride, at::ScalarType type = at::kBFloat16) {
+  check(t, name, type, shape, dev);
   const int64_t last = t.dim() - 1;
   if (t.stride(last) != 1 && shape[last] != 1) refuse(std::string(name) + ": the last dimension must be contiguous");
   for (int64_t i = 0; i < last; ++i) stride[i] = t.stride(i);
@@ -281,6 +281,123 @@ PyObject* expert_product(PyObject* const* a) {
   return finish(n_rows == 0 ? (int)MK_OK : mk_expert_product(&r, stream(dev)), wrap(out));
 }
 
+// bf16 or float32
+bool is_float(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
+    refuse(std::string(name) + " must be BFloat16 or Float, not " + toString(t.scalar_type()));
+  return t.scalar_type() == at::kFloat;
+}
+// stride of the rows of a matrix (one row has none)
+int64_t row_stride(const int64_t* stride, int64_t rows, int64_t width) { return rows > 1 ? stride[0] : width; }
+
+// x, w, bias, activation, residual, out, wide (None: out's type, or bf16), status
+PyObject* linear(PyObject* const* a) {
+  const at::Tensor& x = shaped(a[0], "x", 2);
+  const int dev = (int)x.get_device();
+  const at::Tensor& w = shaped(a[1], "w", 2);
+  const int64_t m = x.size(0), k = x.size(1), n = w.size(0);
+  mk_linear_args r{};
+  int64_t stride[1];
+  r.x = rows(x, "x", {m, k}, dev, stride);
+  r.x_stride = row_stride(stride, m, k);
+  r.w = need(w, "w", at::kBFloat16, {n, k}, dev);
+  r.bias = optional(a[2], "bias", at::kBFloat16, {n}, dev);
+  r.activation = whole(a[3], "activation");
+  if (a[4] != Py_None) {
+    r.residual = rows(tensor(a[4], "residual"), "residual", {m, n}, dev, stride);
+    r.residual_stride = row_stride(stride, m, n);
+  }
+  at::Tensor out;
+  if (a[5] == Py_None) {
+    r.out_float = a[6] == Py_True;
+    out = fresh({m, n}, x, r.out_float ? at::kFloat : at::kBFloat16, false);
+  } else {
+    out = shaped(a[5], "out", 2);
+    r.out_float = is_float(out, "out");
+    if (a[6] != Py_None && (a[6] == Py_True) != (r.out_float != 0)) refuse("out has another dtype than the one asked for");
+  }
+  r.out = rows(out, "out", {m, n}, dev, stride, r.out_float ? at::kFloat : at::kBFloat16);
+  r.out_stride = row_stride(stride, m, n);
+  r.status = optional<int32_t>(a[7], "status", at::kInt, {4}, dev);
+  r.m = size32(m, "m");
+  r.n = size32(n, "n");
+  r.k = size32(k, "k");
+  return finish(mk_linear(&r, stream(dev)), wrap(out));
+}
+
+// x, router, w_gate, w_up, w_down, top_k, residual, ids, weights, out, status
+PyObject* moe_layer(PyObject* const* a) {
+  const at::Tensor& x = shaped(a[0], "x", 2);
+  const int dev = (int)x.get_device();
+  const at::Tensor& gate = shaped(a[2], "w_gate", 3);
+  const int64_t t = x.size(0), e = gate.size(0), f = gate.size(1), d = gate.size(2);
+  mk_moe_args r{};
+  int64_t stride[1];
+  r.x = rows(x, "x", {t, d}, dev, stride);
+  r.x_stride = row_stride(stride, t, d);
+  r.router = need(a[1], "router", at::kBFloat16, {e, d}, dev);
+  r.w_gate = need(gate, "w_gate", at::kBFloat16, {e, f, d}, dev);
+  r.w_up = need(a[3], "w_up", at::kBFloat16, {e, f, d}, dev);
+  r.w_down = need(a[4], "w_down", at::kBFloat16, {e, d, f}, dev);
+  r.top_k = whole(a[5], "top_k");
+  if (a[6] != Py_None) {
+    r.residual = rows(tensor(a[6], "residual"), "residual", {t, d}, dev, stride);
+    r.residual_stride = row_stride(stride, t, d);
+  }
+  r.ids = optional<int32_t>(a[7], "ids", at::kInt, {t, r.top_k}, dev);
+  r.weights = optional<float>(a[8], "weights", at::kFloat, {t, r.top_k}, dev);
+  const at::Tensor out = a[9] == Py_None ? fresh({t, d}, x, at::kBFloat16, false) : tensor(a[9], "out");
+  r.out = rows(out, "out", {t, d}, dev, stride);
+  r.out_stride = row_stride(stride, t, d);
+  r.status = optional<int32_t>(a[10], "status", at::kInt, {4}, dev);
+  r.n_tokens = size32(t, "the number of tokens");
+  r.d_model = size32(d, "d_model");
+  r.d_ff = size32(f, "d_ff");
+  r.n_experts = size32(e, "the number of experts");
+  const int rc = mk_moe_layer_workspace(&r, &r.workspace_bytes);
+  if (rc != MK_OK) return finish(rc, nullptr);
+  if (t == 0) return wrap(out);
+  const at::Tensor work = fresh({(int64_t)r.workspace_bytes}, x, at::kByte, false);
+  r.workspace = work.data_ptr();
+  return finish(mk_moe_layer(&r, stream(dev)), wrap(out));
+}
+
+// logits, tokens, uniforms, parents, draft_probs, temperature, counts, accepted, next_tokens, status
+PyObject* verify_nodes(PyObject* const* a) {
+  const at::Tensor& logits = shaped(a[0], "logits", 3);
+  const int dev = (int)logits.get_device();
+  const int64_t b = logits.size(0), n = logits.size(1), v = logits.size(2);
+  mk_verify_args r{};
+  r.logits_float = is_float(logits, "logits");
+  r.logits = rows(logits, "logits", {b, n, v}, dev, r.logits_stride, r.logits_float ? at::kFloat : at::kBFloat16);
+  r.tokens = need<int32_t>(a[1], "tokens", at::kInt, {b, n}, dev);
+  r.uniforms = need<float>(a[2], "uniforms", at::kFloat, {b, n}, dev);
+  r.parents = optional<int32_t>(a[3], "parents", at::kInt, {b, n}, dev);
+  if (a[4] != Py_None)
+    r.draft_probs = static_cast<const float*>(rows(tensor(a[4], "draft_probs"), "draft_probs", {b, n, v}, dev, r.draft_stride, at::kFloat));
+  r.temperature = optional<float>(a[5], "temperature", at::kFloat, {b}, dev);
+  r.counts = optional<int32_t>(a[6], "counts", at::kInt, {b}, dev);
+  const at::Tensor accepted = a[7] == Py_None ? fresh({b, n}, logits, at::kInt, false) : tensor(a[7], "accepted");
+  const at::Tensor next = a[8] == Py_None ? fresh({b}, logits, at::kInt, false) : tensor(a[8], "next_tokens");
+  r.accepted = need<int32_t>(accepted, "accepted", at::kInt, {b, n}, dev);
+  r.next_tokens = need<int32_t>(next, "next_tokens", at::kInt, {b}, dev);
+  r.status = optional<int32_t>(a[9], "status", at::kInt, {4}, dev);
+  r.batch = size32(b, "the batch");
+  r.n_nodes = size32(n, "the number of nodes");
+  r.vocab = size32(v, "the vocabulary");
+  int rc = mk_verify_nodes_workspace(&r, &r.workspace_bytes);
+  if (rc == MK_OK && b > 0) {
+    const at::Tensor work = fresh({(int64_t)r.workspace_bytes}, logits, at::kByte, false);
+    r.workspace = work.data_ptr();
+    rc = mk_verify_nodes(&r, stream(dev));
+  }
+  if (rc != MK_OK) return finish(rc, nullptr);
+  PyObject *first = wrap(accepted), *second = wrap(next), *both = first && second ? PyTuple_Pack(2, first, second) : nullptr;
+  Py_XDECREF(first);
+  Py_XDECREF(second);
+  return both;
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -317,7 +434,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<qk_norm_rope, 15>("qk_norm_rope"), method<tree_attention, 12>("tree_attention"),
                          method<copy_pages, 4>("copy_pages"),      method<commit_nodes, 7>("commit_nodes"),
-                         method<expert_product, 7>("expert_product"), {"is_here", is_here, METH_O, nullptr},
+                         method<expert_product, 7>("expert_product"), method<linear, 8>("linear"),
+                         method<moe_layer, 11>("moe_layer"),       method<verify_nodes, 10>("verify_nodes"), {"is_here", is_here, METH_O, nullptr},
                          {"setup", setup, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

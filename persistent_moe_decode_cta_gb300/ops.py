@@ -4,7 +4,9 @@ They are what a program needs around the decode step to verify drafted tokens or
 prompt chunks: append the new nodes' keys and values to the paged cache
 (`qk_norm_rope`), attend over the cache and the draft tree (`tree_attention`), multiply by
 the routed experts' matrices (`expert_product`), keep the accepted path
-(`commit_nodes`) and copy pages for a fork (`copy_pages`).  A *node* is a new token; node i
+(`commit_nodes`) and copy pages for a fork (`copy_pages`); the projections and the LM head
+(`linear`), the routed layer of a few tokens as a whole (`moe_layer`), and the decision which
+drafted tokens are accepted (`verify_nodes`).  A *node* is a new token; node i
 of sequence b owns cache position seq_lens[b] + i whatever its depth in the tree.
 
 The functions check and marshal torch tensors for the entry points of include/mk.h, where
@@ -186,3 +188,42 @@ def expert_product(x, w, offsets, *, w_up=None, rows=None, out=None, status=None
     [n_rows, n]; rows that belong to no expert are left as they are (uninitialised in a new
     result)."""
     return _native().expert_product(x, w, offsets, w_up, rows, out, status)
+
+
+_ACTIVATIONS = {None: B.MK_ACT_NONE, "relu": B.MK_ACT_RELU, "silu": B.MK_ACT_SILU, "gelu": B.MK_ACT_GELU, "gelu_tanh": B.MK_ACT_GELU_TANH}
+_WIDE = {None: None, torch.bfloat16: False, torch.float32: True}
+
+
+@_operator
+def linear(x, w, *, bias=None, activation=None, residual=None, dtype=None, out=None, status=None):
+    """act(x @ w.T + bias) + residual.  x bf16 [m, k] and residual bf16 [m, n] (rows may be strided), w bf16 [n, k],
+    bias bf16 [n]; activation None, "relu", "silu", "gelu" (erf) or "gelu_tanh".  Returns [m, n] of `dtype`, bf16
+    (default) or float32 (an LM head's logits); `out` may be strided, and the residual itself."""
+    if not isinstance(activation, (str, type(None))) or activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(a for a in _ACTIVATIONS if a)} or None, not {activation!r}")
+    if dtype not in _WIDE:
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, not {dtype!r}")
+    return _native().linear(x, w, bias, _ACTIVATIONS[activation], residual, out, _WIDE[dtype], status)
+
+
+@_operator
+def moe_layer(x, router, w_gate, w_up, w_down, top_k, *, residual=None, ids=None, weights=None, out=None, status=None):
+    """The routed layer of up to 256 tokens as a whole: residual + sum over a token's top_k experts of its softmax weight
+    times w_down[e] @ (silu(w_gate[e] @ x) * (w_up[e] @ x)).  x, residual bf16 [n, d_model] (rows may be strided), router bf16
+    [n_experts, d_model], w_gate and w_up bf16 [n_experts, d_ff, d_model], w_down bf16 [n_experts, d_model, d_ff].  The
+    selection goes to `ids` and `weights` (int32, float32 [n, top_k], largest score first) where given.  Returns bf16
+    [n, d_model]; `out` may be the residual itself."""
+    return _native().moe_layer(x, router, w_gate, w_up, w_down, top_k, residual, ids, weights, out, status)
+
+
+@_operator
+def verify_nodes(logits, tokens, uniforms, *, parents=None, draft_probs=None, temperature=None, counts=None, accepted=None,
+                 next_tokens=None, status=None):
+    """Which drafted nodes the target model accepts, and its next token: (accepted, next_tokens).  Node 0 of a sequence is its
+    last sampled token, the others a tree of drafted tokens (parents[b, i] < i; None: a chain).  logits [batch, n, vocab] (bf16
+    or float32, last dimension contiguous) are the target's for the token after each node, draft_probs float32 [batch, n, vocab]
+    what each node's children were drawn from (None: they were not drawn, but proposed), uniforms float32 [batch, n] random
+    numbers in [0, 1): entry i decides on node i, entry 0 draws the next token.  temperature float32 [batch] (None: 1; 0: the
+    largest logit).  accepted int32 [batch, n] holds the path from node 0, ended by -1, as `commit_nodes` takes it;
+    next_tokens int32 [batch]."""
+    return _native().verify_nodes(logits, tokens, uniforms, parents, draft_probs, temperature, counts, accepted, next_tokens, status)

@@ -1,0 +1,170 @@
+"""mk_moe_layer against float64: selection, weights, both products and their sum."""
+import pytest
+import torch
+
+import more_ops_ref as M
+import ops_ref as R
+from persistent_moe_decode_cta_gb300 import binding as B
+from persistent_moe_decode_cta_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(g, e, d, f):
+    return (R.bf16(g, e, d, std=0.05), R.bf16(g, e, f, d, std=d ** -0.5), R.bf16(g, e, f, d, std=d ** -0.5), R.bf16(g, e, d, f, std=f ** -0.5))
+
+
+def check(t, e, k, d, f, residual=True, x_extra=0, r_extra=0, out_extra=0, seed=0, spoil=None, in_place=False):
+    g = R.gen(seed)
+    x = R.bf16(g, t, d + x_extra)[:, :d]
+    router, gate, up, down = weights(g, e, d, f)
+    if spoil:
+        spoil(x, router)
+    r = R.bf16(g, t, d + r_extra) if residual else None
+    res = None if r is None else r[:, :d]
+    want, bound, ids, c = M.moe(x, router, gate, up, down, k, res)
+    got_ids = torch.full((t, k), -7, dtype=torch.int32, device="cuda")
+    got_c = torch.zeros(t, k, device="cuda")
+    whole = r if in_place else torch.full((t, d + out_extra), 3.0, dtype=torch.bfloat16, device="cuda")
+    before = whole.clone()
+    status = ops.new_status()
+    ops.moe_layer(x, router, gate, up, down, k, residual=res, ids=got_ids, weights=got_c, out=whole[:, :d], status=status)
+    ops.check_status(status)
+    assert torch.equal(got_ids.long(), ids)
+    assert float((got_c.double() - c).abs().max()) <= 2.0 ** -20
+    R.assert_close(whole[:, :d], want, bound, f"{t} tokens")
+    assert torch.equal(whole[:, d:], before[:, d:])
+    if not in_place:
+        again = ops.moe_layer(x, router, gate, up, down, k, residual=res)
+        assert torch.equal(again, whole[:, :d])
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 7, 8, 9, 16, 31, 33, 64, 65, 100, 128, 129, 255, 256])
+def test_tokens(t):
+    check(t, 8, 2, 256, 128, residual=t % 2 == 0)
+
+
+@pytest.mark.parametrize("t", [1, 5, 20, 100])
+@pytest.mark.parametrize("e,k,d,f", [(1, 1, 8, 8), (3, 3, 64, 72), (5, 2, 136, 40), (33, 4, 1024, 512), (256, 16, 128, 64), (40, 16, 72, 200),
+                                     (16, 1, 2568, 24), (7, 5, 520, 1032)])
+def test_sizes(t, e, k, d, f):
+    check(t, e, k, d, f)
+
+
+@pytest.mark.parametrize("t", [1, 16, 128, 250])
+def test_pages_scale(t):
+    check(t, 128, 8, 2048, 768)
+
+
+@pytest.mark.parametrize("t", [3, 30, 200])
+@pytest.mark.parametrize("x_extra,r_extra,out_extra", [(8, 0, 0), (0, 3, 0), (0, 0, 5), (16, 7, 9)])
+def test_strides(t, x_extra, r_extra, out_extra):
+    check(t, 12, 3, 192, 64, x_extra=x_extra, r_extra=r_extra, out_extra=out_extra)
+
+
+@pytest.mark.parametrize("t", [1, 8, 40, 256])
+def test_the_residual_in_place(t):
+    check(t, 8, 2, 256, 128, in_place=True)
+    check(t, 8, 2, 256, 128, in_place=True, r_extra=11)
+
+
+@pytest.mark.parametrize("t", [1, 8, 64, 256])
+def test_every_token_to_the_same_experts(t):
+    """One expert's rows fill several tiles, others have none."""
+    def same(x, router):
+        x[:] = x[:1]
+    check(t, 24, 3, 256, 128, spoil=same)
+
+
+@pytest.mark.parametrize("t", [1, 6, 50])
+def test_equal_scores_go_to_the_lower_expert(t):
+    def equal(x, router):
+        router[3:] = router[3]
+    check(t, 40, 4, 128, 64, spoil=equal)
+
+    def nothing(x, router):
+        router[:] = 0
+    check(t, 40, 4, 128, 64, spoil=nothing)
+
+
+def test_scores_that_differ_in_their_last_bits():
+    """Two experts' scores differ by 2^-30 of the sum of their terms' sizes: an fp32 sum cannot tell them apart."""
+    d = 512
+    x = torch.ones(4, d, dtype=torch.bfloat16, device="cuda")
+    x[:, 1::2] = -1
+    router = torch.zeros(6, d, dtype=torch.bfloat16, device="cuda")
+    router[:, :] = torch.linspace(100, 200, d // 2, device="cuda").repeat_interleave(2).to(torch.bfloat16)   # (pairs cancel)
+    for e in range(6):
+        router[e, 2 * e] = router[e, 2 * e]
+        router[e, -1] = 0
+        x[:, -1] = 0
+        router[e, -2] = 2.0 ** -14 * (1 + (5 * e) % 6)
+    x[:, -2] = 1
+    g = R.gen(8)
+    _, gate, up, down = weights(g, 6, d, 64)
+    ids = torch.zeros(4, 3, dtype=torch.int32, device="cuda")
+    ops.moe_layer(x, router, gate, up, down, 3, ids=ids)
+    want, _ = M.select(M.scores(x, router), 3)
+    assert torch.equal(ids.long(), want) and len(set(want[0].tolist())) == 3 and want[0].tolist() != [0, 1, 2]
+
+
+def test_scores_that_are_not_finite():
+    """A NaN score is the largest; the outputs of such a token are NaN, those of others are as ever."""
+    g = R.gen(9)
+    x, (router, gate, up, down) = R.bf16(g, 5, 64), weights(g, 8, 64, 32)
+    x[1, 3] = float("nan")
+    x[2, 4] = float("inf")
+    ids = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    y = ops.moe_layer(x, router, gate, up, down, 2, ids=ids)
+    assert ids.min() >= 0 and ids.max() < 8 and (ids[:, 0] != ids[:, 1]).all()
+    assert torch.isnan(y[1:3]).all()
+    fine = [0, 3, 4]
+    want, bound, want_ids, _ = M.moe(x[fine], router, gate, up, down, 2)
+    assert torch.equal(ids[fine].long(), want_ids)
+    R.assert_close(y[fine], want, bound)
+
+
+def test_no_tokens():
+    g = R.gen(10)
+    router, gate, up, down = weights(g, 4, 64, 32)
+    assert ops.moe_layer(router[:0], router, gate, up, down, 2).shape == (0, 64)
+
+
+def test_one_row_more_than_the_layer_takes():
+    g = R.gen(11)
+    router, gate, up, down = weights(g, 4, 64, 32)
+    with pytest.raises(B.MkError) as e:
+        ops.moe_layer(R.bf16(g, 257, 64), router, gate, up, down, 2)
+    assert e.value.code == B.MK_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("t", [1, 20, 200])
+def test_captured_replay(t):
+    g = R.gen(12)
+    x, (router, gate, up, down) = R.bf16(g, t, 128), weights(g, 16, 128, 64)
+    out = torch.zeros(t, 128, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.moe_layer(x, router, gate, up, down, 4, residual=x, out=out)
+    x.copy_(R.bf16(g, t, 128))
+    for _ in range(3):
+        graph.replay()
+        want, bound, _, _ = M.moe(x, router, gate, up, down, 4, x)
+        R.assert_close(out, want, bound)
+
+
+def test_many_calls_side_by_side():
+    """Calls that share the GPU: a wait for the first product never waits for a CTA that cannot start."""
+    g = R.gen(13)
+    jobs = []
+    for i, t in enumerate((1, 8, 30, 128, 256, 2)):
+        w = weights(g, 32, 512, 256)
+        jobs.append((R.bf16(g, t, 512), w))
+    want = [ops.moe_layer(x, *w, 4) for x, w in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(30):
+        got = [ops.moe_layer(x, *w, 4, stream=s) for (x, w), s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    ops.check_status()
