@@ -605,7 +605,7 @@ int mk_linear(const mk_linear_args* args, void* stream);
  * The scores are sums of exact products good to 2^-40 of the sum of their sizes, so that the selection is that of the
  * formula.  A NaN score counts as the largest.  c times the product of gate and up is rounded to bf16, everything else is
  * fp32 until the one rounding of out.  The sums have a fixed order: equal calls give equal bits.
- * n_experts in 1..256, top_k in 1..min(16, n_experts). */
+ * n_experts in 1..256, top_k in 1..min(16, n_experts), d_model up to 8192, d_ff up to 65536. */
 typedef struct mk_moe_args {
   const void* x;
   const void* router;

@@ -5,17 +5,17 @@
 // added up.
 //
 // With few tokens every selected expert's weights are read for a handful of rows: HBM bounds it, and the products only have to
-// keep up.  So the weights go straight from HBM to the lane that multiplies them, without barriers or a shared ring: each
-// warp has a ring of its own, filled by 16-byte asynchronous copies, and every lane reads back what it copied itself.
-// (m16n8k16 wants pairs of k apart from one another in a lane; since the order of k does not matter to a sum, a lane's 16 bytes
-// in a row count as four such pairs, for weights and rows alike.)  The warps split k; their parts of a result meet in
-// shared memory and are added in the order of the warps.
+// keep up.  Every warp has a ring of its own that it fills itself, with tensor-map copies of 8 rows by 64 columns (no barrier
+// between warps), and multiplies with m16n8k16: with 8 rows an expert a tcgen05 tile would be empty but for a sixteenth.  The
+// warps split k; their parts of a result meet in shared memory and are added in the order of the warps.
 //
 // First product: a unit is 8 outputs of an expert (8 gate and 8 up rows of weights: one 16-row tile) for up to 8 NT of its
-// rows.  The list of units is cut into as many equal runs as there are CTAs, and a CTA claims a run when it starts, so that a
-// wait for the first product never waits for a CTA that has yet to start.  Second product: a CTA has up to 16 output
-// columns and goes through all experts with them, so that the sum over a token's experts stays in the CTA, in the order
-// of the experts: no partial results leave it.
+// rows, which stay in shared memory for all units of the expert.  The list of units is cut into as many equal runs as there are
+// CTAs, and a CTA claims a run when it starts, so that a wait for the first product never waits for a CTA that has yet to
+// start.  Second product: a CTA has up to 16 output columns and goes through all experts with them, so that the sum over a
+// token's experts stays in the CTA, in the order of the experts: no partial results leave it.
+#include <algorithm>
+
 #include "mk_ops.cuh"
 
 namespace mk {
@@ -150,301 +150,284 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
 
 // ------------------------------------------------------------------------------------------- layer
 constexpr int kLayerThreads = 256, kLayerWarps = kLayerThreads / 32;
-constexpr int kStepK = 64;  // columns of a step: two 16-byte pieces a lane and row
-
-template <int NT>
-constexpr int kSlots = NT == 1 ? 8 : NT == 2 ? 5 : 3;  // of a warp's ring
-template <int NT>
-constexpr int kSlotBytes = (4 + 2 * NT) * 32 * 16;
+constexpr int kStepK = 64;       // columns of a step: one 128-byte swizzle span
+constexpr int kTileBytes = 2048; // weights of a step: 16 rows
+constexpr int kMaxSlots = 10;    // of a warp's ring
 constexpr int kAccPitch = 20;
 
-template <int NT>
-struct LayerSmem {  // offsets in dynamic shared memory
-  int red, list, weight, acc, ent, total;
-  __host__ __device__ LayerSmem(int tokens, int entries) {
-    red = kLayerWarps * kSlots<NT> * kSlotBytes<NT>;
-    list = red + 2 * kLayerWarps * NT * 32 * 16;            // (the token masks lie here before the first results)
+struct LayerShared {
+  int off[kOpMaxExperts + 1];       // first row of every expert in the list
+  int act[kOpMaxExperts];           // experts that have rows
+  int tile_pre[kOpMaxExperts + 1];  // row tiles before each of them
+  int n_act, run, next, abort;
+  int warp_rows[8], warp_tiles[8], warp_act[8];
+  unsigned long long bars[kLayerWarps][kMaxSlots];
+};
+
+// offsets in dynamic shared memory, behind the warps' rings; the same on host and device
+struct LayerSmem {
+  int warp_bytes, red, list, weight, acc, total;
+  __host__ __device__ LayerSmem(int nt, bool direct, int slots, int d, int tokens, int top_k) {
+    const int entries = tokens * top_k, mine = ((d + kStepK - 1) / kStepK + kLayerWarps - 1) / kLayerWarps;
+    warp_bytes = slots * kTileBytes + (slots > mine ? slots : mine) * nt * 1024;  // weights, rows
+    red = kLayerWarps * warp_bytes;
+    list = red + 2 * kLayerWarps * nt * 32 * 16;  // (the token masks lie here before the first results)
     weight = list + (entries * 2 + 15) / 16 * 16;
-    acc = weight + (entries * 4 + 15) / 16 * 16;
-    ent = acc + tokens * kAccPitch * 4;
-    total = ent + (NT == 1 ? kOpMaxExperts * 8 * 2 : 0);
+    acc = weight + (direct ? entries * 8 : entries) * 4;  // (direct: of every active expert and token)
+    acc = (acc + 15) / 16 * 16;
+    total = acc + tokens * kAccPitch * 4 + 1024;
   }
 };
 
-struct LayerShared {
-  int off[kOpMaxExperts + 1];    // first row of every expert in the list
-  int act[kOpMaxExperts];        // experts that have rows
-  int pre[kOpMaxExperts + 1];    // units before each of them
-  int tile_pre[kOpMaxExperts + 1];
-  int n_act, run, next;
-};
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// acquire-free copies of a box of a matrix
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+               : "memory");
 }
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 __device__ __forceinline__ float moe_silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-template <int NT>
-__global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_constant__ MoeParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
+// NT: row tiles of 8 that share a pass over the weights.  DIRECT (up to 8 tokens): a tile's rows are the tokens, with zeros for
+// those that have not selected the expert, so that the second product adds its experts up in registers.
+template <int NT, bool DIRECT>
+__global__ void __launch_bounds__(kLayerThreads, 1)
+    layer_kernel(const __grid_constant__ MoeParams p, const __grid_constant__ CUtensorMap tgate, const __grid_constant__ CUtensorMap tup,
+                 const __grid_constant__ CUtensorMap tdown, const __grid_constant__ CUtensorMap th) {
+  extern __shared__ uint8_t raw_[];
   __shared__ LayerShared sh;
-  constexpr int S = kSlots<NT>;
-  constexpr bool kDirect = NT == 1;  // second product: a tile's rows are the tokens, and its sums stay in registers
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int T = p.a.n_tokens, K = p.a.top_k, E = p.a.n_experts, d = p.a.d_model, f = p.a.d_ff, entries = T * K;
-  const LayerSmem<NT> at(T, entries);
+  const int tid = threadIdx.x, warp = (int)uniform(threadIdx.x >> 5), lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int T = p.a.n_tokens, K = p.a.top_k, E = p.a.n_experts, d = p.a.d_model, f = p.a.d_ff, entries = T * K, S = p.slots;
+  const LayerSmem at(NT, DIRECT, S, d, T, K);
+  const uint32_t base = (smem_u32(raw_) + 1023u) & ~1023u;
+  uint8_t* const raw = raw_ + (base - smem_u32(raw_));
   float4* const red = reinterpret_cast<float4*>(raw + at.red);
   uint32_t* const mask = reinterpret_cast<uint32_t*>(raw + at.red);
-  uint16_t* const list = reinterpret_cast<uint16_t*>(raw + at.list);  // token << 4 | slot, by expert, then token
-  float* const weight = reinterpret_cast<float*>(raw + at.weight);    // ... and its weight
+  uint16_t* const list = reinterpret_cast<uint16_t*>(raw + at.list);  // token of every row, by expert, then token
+  float* const weight = reinterpret_cast<float*>(raw + at.weight);    // ... and its weight (DIRECT: [active expert][8])
   float* const acc = reinterpret_cast<float*>(raw + at.acc);
-  int16_t* const ent = reinterpret_cast<int16_t*>(raw + at.ent);      // [active expert][token]: its row of h, or -1
   const int words = (T + 31) / 32;
+  const uint32_t bars = smem_u32(sh.bars[warp]);
 
+  if (tid == 0) {
+    for (int w = 0; w < kLayerWarps; ++w)
+      for (int s = 0; s < S; ++s) mbar_init(smem_u32(&sh.bars[w][s]), 1);
+    fence_proxy_async_smem();
+    sh.abort = 0;
+    sh.next = -1;
+  }
+  if (tid >= 32 && tid < 36) {
+    const CUtensorMap* tm = tid == 32 ? &tgate : tid == 33 ? &tup : tid == 34 ? &tdown : &th;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+  }
   for (int i = tid; i < E * words; i += kLayerThreads) mask[i] = 0;
-  if (kDirect)
-    for (int i = tid; i < kOpMaxExperts * 8; i += kLayerThreads) ent[i] = -1;
+  if (DIRECT)
+    for (int i = tid; i < entries * 8; i += kLayerThreads) weight[i] = -1.f;
   for (int i = tid; i < T * kAccPitch; i += kLayerThreads) acc[i] = 0.f;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   // ---------------------------------------------------------------- who has which rows
-  if (tid == 0) {
-    sh.run = (int)atomicAdd(p.sync, 1u);
-    sh.next = -1;
-  }
+  if (tid == 0) sh.run = (int)atomicAdd(p.sync, 1u);
+  int my_id = 0;
+  float my_weight = 0.f;
+  if (tid < entries) my_id = op_ld(p.ids + tid), my_weight = op_ldf(p.weights + tid);
   for (int i = tid; i < entries; i += kLayerThreads) {
     const int t = i / K;
-    atomicOr(mask + op_ld(p.ids + i) * words + (t >> 5), 1u << (t & 31));
+    atomicOr(mask + (i == tid ? my_id : op_ld(p.ids + i)) * words + (t >> 5), 1u << (t & 31));
   }
   __syncthreads();
-  if (warp == 0) {
-    // (one warp: the experts in order, 32 at a time)
-    int rows = 0, tiles = 0, active = 0;
-    for (int base = 0; base < E; base += 32) {
-      const int e = base + lane;
-      int n = 0;
-      if (e < E)
-        for (int w = 0; w < words; ++w) n += __popc(mask[e * words + w]);
-      const int k = (n + 8 * NT - 1) / (8 * NT);
-      int r = n, c = k;
+  {  // (one expert a thread)
+    const int e = tid;
+    int n = 0;
+    if (e < E)
+      for (int w = 0; w < words; ++w) n += __popc(mask[e * words + w]);
+    const int k = DIRECT ? (n > 0) : (n + 8 * NT - 1) / (8 * NT);
+    int r = n, c = k;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, c, o);
-        if (lane >= o) r += a, c += b;
-      }
-      const unsigned some = __ballot_sync(0xffffffffu, n > 0);
-      const int idx = active + __popc(some & ((1u << lane) - 1));
-      if (e < E) sh.off[e] = rows + r - n;
-      if (n > 0) {
-        sh.act[idx] = e;
-        sh.tile_pre[idx] = tiles + c - k;
-      }
-      rows += __shfl_sync(0xffffffffu, r, 31);
-      tiles += __shfl_sync(0xffffffffu, c, 31);
-      active += __popc(some);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) r += a, c += b;
     }
-    if (lane == 0) {
-      sh.off[E] = rows;
-      sh.tile_pre[active] = tiles;
-      sh.n_act = active;
+    const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+    if (lane == 31) sh.warp_rows[warp] = r, sh.warp_tiles[warp] = c, sh.warp_act[warp] = __popc(some);
+    __syncthreads();
+    int rows = 0, tiles = 0, active = 0;
+    for (int w = 0; w < warp; ++w) rows += sh.warp_rows[w], tiles += sh.warp_tiles[w], active += sh.warp_act[w];
+    const int idx = active + __popc(some & ((1u << lane) - 1));
+    if (e < E) sh.off[e] = rows + r - n;
+    if (n > 0) sh.act[idx] = e, sh.tile_pre[idx] = tiles + c - k;
+    if (tid == kLayerThreads - 1) {
+      sh.off[E] = rows + r;
+      sh.n_act = active + __popc(some);
+      sh.tile_pre[sh.n_act] = tiles + c;
     }
   }
   __syncthreads();
-  const int A = sh.n_act, groups = f / 8;
+  const int A = (int)uniform(sh.n_act), groups = f / 8;
   for (int i = tid; i < entries; i += kLayerThreads) {
-    const int t = i / K, e = op_ld(p.ids + i);
-    int r = sh.off[e];
-    for (int w = 0; w < (t >> 5); ++w) r += __popc(mask[e * words + w]);
-    r += __popc(mask[e * words + (t >> 5)] & ((1u << (t & 31)) - 1));
-    list[r] = (uint16_t)(t << 4 | (i - t * K));
-    weight[r] = op_ldf(p.weights + i);
-    if (kDirect) {
+    const int t = i / K, e = i == tid ? my_id : op_ld(p.ids + i);
+    const float c = i == tid ? my_weight : op_ldf(p.weights + i);
+    if (DIRECT) {
       int lo = 0;  // the expert's place among the active ones
 #pragma unroll
       for (int step = kOpMaxExperts / 2; step; step >>= 1)
         if (lo + step < A && sh.act[lo + step] <= e) lo += step;
-      ent[lo * 8 + t] = (int16_t)i;
+      weight[lo * 8 + t] = c;
+    } else {
+      int r = sh.off[e];
+      for (int w = 0; w < (t >> 5); ++w) r += __popc(mask[e * words + w]);
+      r += __popc(mask[e * words + (t >> 5)] & ((1u << (t & 31)) - 1));
+      list[r] = (uint16_t)t;
+      weight[r] = c;
     }
   }
   __syncthreads();
-  const long long units = (long long)sh.tile_pre[A] * groups;
-  const int runs = (int)gridDim.x;
+  const long long units = (long long)uniform(sh.tile_pre[A]) * groups;
+  const int runs = (int)gridDim.x, steps_up = (d + kStepK - 1) / kStepK, steps_down = (f + kStepK - 1) / kStepK;
 
   // ---------------------------------------------------------------- the warp's ring
-  const uint32_t ring = smem_u32(raw) + warp * (S * kSlotBytes<NT>) + lane * 16;
-  const uint8_t* const ring_g = raw + warp * (S * kSlotBytes<NT>) + lane * 16;
-  uint32_t put = 0, get = 0;  // slots, modulo S
-  auto bump = [](uint32_t& s) { s = s + 1 == (uint32_t)S ? 0u : s + 1; };
+  const uint32_t tiles_at = base + warp * at.warp_bytes, rows_at = tiles_at + S * kTileBytes;
+  Ring get;
+  uint32_t put = 0;
+  // where a lane reads its part of a step: 16 rows of weights, 8 rows of x or h (swizzled 128-byte rows)
+  const uint32_t r8 = lane & 7, m4 = lane >> 3;
+  const uint32_t a_at = (m4 & 1) * 1024 + r8 * 128, a_x = ((m4 >> 1) ^ r8) << 4, b_at = r8 * 128 + ((m4 ^ r8) << 4);
 
   // ---------------------------------------------------------------- first product
-  struct Up {             // a place in the list of units
-    int left;             // units of the run from here on, this one included
-    int a, g, tile, tiles, e, n;   // active expert, group of outputs, row tile (of tiles), the expert, its rows
+  // A unit: 8 outputs of an expert for one of its row tiles; the units of a tile follow one another.
+  struct Up {
+    int left;          // units of the run from here on, this one included
+    int a, tile, grp;  // active expert, row tile among all, group of outputs
+    int end;           // the expert's last row tile + 1
   };
-  auto up_at = [&](long long u, int left) {
-    Up c;
-    c.left = left;
-    if (left <= 0) return c;
+  auto up_begin = [&](int r) {
+    const long long u0 = r * units / runs, u1 = (r + 1) * units / runs;
+    Up c{(int)(u1 - u0), 0, 0, 0, 0};
+    if (c.left <= 0) return c;
+    c.tile = (int)(u0 / groups);
+    c.grp = (int)(u0 - (long long)c.tile * groups);
     int lo = 0;
 #pragma unroll
     for (int step = kOpMaxExperts / 2; step; step >>= 1)
-      if (lo + step < A && (long long)sh.tile_pre[lo + step] * groups <= u) lo += step;
+      if (lo + step < A && sh.tile_pre[lo + step] <= c.tile) lo += step;
     c.a = lo;
-    c.e = sh.act[lo];
-    c.n = sh.off[c.e + 1] - sh.off[c.e];
-    c.tiles = sh.tile_pre[lo + 1] - sh.tile_pre[lo];
-    const int rem = (int)(u - (long long)sh.tile_pre[lo] * groups);
-    c.g = rem / c.tiles;
-    c.tile = rem - c.g * c.tiles;
+    c.end = sh.tile_pre[lo + 1];
     return c;
   };
   auto up_next = [&](Up& c) {
-    if (--c.left <= 0) return;
-    if (++c.tile < c.tiles) return;
-    c.tile = 0;
-    if (++c.g < groups) return;
-    c.g = 0;
-    ++c.a;
-    c.e = sh.act[c.a];
-    c.n = sh.off[c.e + 1] - sh.off[c.e];
-    c.tiles = sh.tile_pre[c.a + 1] - sh.tile_pre[c.a];
-  };
-  const int steps_up = (d + kStepK - 1) / kStepK, steps_down = (f + kStepK - 1) / kStepK;
-  const uint16_t *a0 = nullptr, *a1 = nullptr, *rows[NT];  // where the lane's pieces come from (the issuing side's)
-  auto up_rows = [&](const Up& c) {
-    const long long r = ((long long)c.e * f + 8 * c.g + g) * d;
-    a0 = static_cast<const uint16_t*>(p.a.w_gate) + r;
-    a1 = static_cast<const uint16_t*>(p.a.w_up) + r;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int n = (c.tile * NT + j) * 8 + g;
-      rows[j] = n < c.n ? static_cast<const uint16_t*>(p.a.x) + (list[sh.off[c.e] + n] >> 4) * p.a.x_stride : nullptr;
-    }
-  };
-  auto copy = [&](uint32_t dst, const uint16_t* row, int k, int width) {
-    cp16(dst, k < width ? row + k : row, k < width ? 16 : 0);
-    cp16(dst + 512, k + 32 < width ? row + k + 32 : row, k + 32 < width ? 16 : 0);
+    --c.left;
+    if (++c.grp < groups) return;
+    c.grp = 0;
+    if (++c.tile < c.end || c.left <= 0) return;
+    c.end = sh.tile_pre[++c.a + 1];
   };
   Up is{}, cs{};   // issuing and consuming sides
-  int istep = warp;
-  auto run_begin = [&](int r) {
-    const long long u0 = r * units / runs, u1 = (r + 1) * units / runs;
-    cs = is = up_at(u0, (int)(u1 - u0));
-    istep = warp;
-    if (is.left > 0) up_rows(is);
-  };
+  int istep = warp, irow = 0;
 
   // ---------------------------------------------------------------- second product
-  // Blocks of output columns, this CTA's one after another; per block the active experts' tiles, of each the steps.  With
-  // kDirect the steps of all experts form one list that the warps deal out, else the warps deal out those of a tile.
+  // Blocks of output columns, this CTA's one after another; per block the row tiles of the active experts, of each the steps.
+  // DIRECT: the warps deal out the steps of all experts as one list, else those of every tile.
   struct Down {
-    int block, a, tile, s;
-    bool more;
+    int block, a, tile, end, s;
   };
   const int blocks = (d + p.width - 1) / p.width;
-  auto down_fit = [&](Down& c) {  // the next place at or behind this one that has a step for this warp
-    while (c.block < blocks) {
-      if (c.s < steps_down) return;
-      if (kDirect) {
+  auto down_fit = [&](Down& c) {  // to the next step of this warp, if this is none
+    while (c.s >= steps_down) {
+      if (DIRECT) {
         c.s -= steps_down;
         ++c.a;
       } else {
         c.s = warp;
-        if (++c.tile >= sh.tile_pre[c.a + 1] - sh.tile_pre[c.a]) c.tile = 0, ++c.a;
-        if (c.s >= steps_down && c.a < A) continue;
+        if (++c.tile == c.end) {
+          ++c.a;
+          if (c.a < A) c.end = sh.tile_pre[c.a + 1];
+        }
       }
       if (c.a >= A) {
         c.block += (int)gridDim.x;
+        if (c.block >= blocks) return;
         c.a = c.tile = 0;
+        c.end = sh.tile_pre[1];
         c.s = warp;
-        if (c.s >= steps_down && !kDirect) c.block = blocks;  // (a warp without steps)
       }
     }
   };
   auto down_begin = [&]() {
-    Down c{(int)blockIdx.x, 0, 0, warp, true};
-    if (!kDirect && warp >= steps_down) c.block = blocks;
-    down_fit(c);
+    Down c{(int)blockIdx.x, 0, 0, (int)uniform(sh.tile_pre[1]), warp};
+    if (!DIRECT && warp >= steps_down) c.block = blocks;  // (a warp without steps)
+    if (c.block < blocks) down_fit(c);
     return c;
   };
-  auto down_next = [&](Down& c) {
-    c.s += kLayerWarps;
-    down_fit(c);
-  };
-  auto down_weights = [&](const Down& c, uint32_t slot) {
-    const int c0 = c.block * p.width, wide = min(p.width, d - c0), k = c.s * kStepK + 8 * q;
-    const uint16_t* const w = static_cast<const uint16_t*>(p.a.w_down) + ((long long)sh.act[c.a] * d + c0 + g) * f;
-    const uint32_t dst = ring + slot * kSlotBytes<NT>;
-    if (g < wide) copy(dst, w, k, f);
-    if (g + 8 < wide) copy(dst + 1024, w + 8ll * f, k, f);
-  };
-  auto down_rows = [&](const Down& c, uint32_t slot) {
-    const int k = c.s * kStepK + 8 * q;
-    const uint32_t dst = ring + slot * kSlotBytes<NT> + 2048;
-    if (kDirect) {
-      const int i = ent[c.a * 8 + g];
-      const uint16_t* const row = p.h + (long long)max(i, 0) * f;
-      cp16(dst, i >= 0 && k < f ? row + k : row, i >= 0 && k < f ? 16 : 0);
-      cp16(dst + 512, i >= 0 && k + 32 < f ? row + k + 32 : row, i >= 0 && k + 32 < f ? 16 : 0);
-    } else {
-      const int e = sh.act[c.a], o = sh.off[e], n = sh.off[e + 1] - o;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int r = (c.tile * NT + j) * 8 + g;
-        if (r < n) {
-          const int x = list[o + r];
-          copy(dst + j * 1024, p.h + (long long)((x >> 4) * K + (x & 15)) * f, k, f);
-        }
-      }
-    }
-  };
-  Down id = down_begin(), first_down = id;
-  int ahead = 0;  // steps of the second product whose weights are under way
+  Down id = down_begin(), ib = id;  // weights, rows
+  int ahead = 0;                    // steps of the second product whose weights are under way and whose rows are not
+  const uint32_t down_bytes = p.width * 128 + NT * 1024;
 
-  // ---------------------------------------------------------------- issue one step of what comes next
+  auto issue_weights = [&]() {
+    if (elect_one()) {
+      const uint32_t bar = bars + 8 * put, dst = tiles_at + put * kTileBytes;
+      mbar_expect_tx(bar, down_bytes);
+      tma_box(dst, &tdown, id.s * kStepK, sh.act[id.a] * d + id.block * p.width, bar);
+    }
+    __syncwarp();
+    put = put + 1 == (uint32_t)S ? 0 : put + 1;
+    id.s += kLayerWarps;
+    down_fit(id);
+  };
+  auto issue_rows = [&](uint32_t slot) {
+    if (elect_one())
+      tma_box(rows_at + slot * NT * 1024, &th, ib.s * kStepK, DIRECT ? ib.a * 8 : sh.off[sh.act[ib.a]] + (ib.tile - sh.tile_pre[ib.a]) * NT * 8,
+              bars + 8 * slot);
+    __syncwarp();
+    ib.s += kLayerWarps;
+    down_fit(ib);
+  };
   int next_run = -1;  // -1: not known yet
-  auto issue_first = [&]() {
-    if (is.left > 0 && istep < steps_up) {
-      const int k = istep * kStepK + 8 * q;
-      const uint32_t dst = ring + put * kSlotBytes<NT>;
-      copy(dst, a0, k, d);
-      copy(dst + 1024, a1, k, d);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (rows[j]) copy(dst + 2048 + j * 1024, rows[j], k, d);
-      bump(put);
+  // (at most S steps are under way: a slot is filled again once its step has been multiplied)
+  auto issue_next = [&]() {
+    if (is.left > 0) {
+      if (istep >= steps_up) return;  // (a warp without steps)
+      if (elect_one()) {
+        const uint32_t bar = bars + 8 * put, dst = tiles_at + put * kTileBytes;
+        mbar_expect_tx(bar, kTileBytes);
+        tma_box(dst, &tgate, istep * kStepK, irow, bar);
+        tma_box(dst + 1024, &tup, istep * kStepK, irow, bar);
+      }
+      __syncwarp();
+      put = put + 1 == (uint32_t)S ? 0 : put + 1;
       istep += kLayerWarps;
       if (istep >= steps_up) {
         istep = warp;
         up_next(is);
-        if (is.left > 0) up_rows(is);
+        if (is.left > 0) irow = sh.act[is.a] * f + 8 * is.grp;
       }
     } else if (next_run >= runs && id.block < blocks && ahead < S) {
-      down_weights(id, put);
-      bump(put);
-      down_next(id);
+      issue_weights();
       ++ahead;
     }
-    op_cp_commit();
   };
 
   float sum[NT][4];
-  auto multiply = [&](int nt) {
-    const uint8_t* const s = ring_g + get * kSlotBytes<NT>;
-    const uint4 g0 = *reinterpret_cast<const uint4*>(s), g1 = *reinterpret_cast<const uint4*>(s + 512);
-    const uint4 u0 = *reinterpret_cast<const uint4*>(s + 1024), u1 = *reinterpret_cast<const uint4*>(s + 1536);
+  auto multiply = [&](uint32_t rows, int nt) {
+    op_wait(bars + 8 * get.slot, get.phase, &sh.abort, p.a.status, 2);
+    const uint32_t tile = tiles_at + get.slot * kTileBytes + a_at;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j >= nt) break;
-      const uint4 b0 = *reinterpret_cast<const uint4*>(s + 2048 + j * 1024), b1 = *reinterpret_cast<const uint4*>(s + 2560 + j * 1024);
-      mma_bf16(sum[j], g0.x, u0.x, g0.y, u0.y, b0.x, b0.y);
-      mma_bf16(sum[j], g0.z, u0.z, g0.w, u0.w, b0.z, b0.w);
-      mma_bf16(sum[j], g1.x, u1.x, g1.y, u1.y, b1.x, b1.y);
-      mma_bf16(sum[j], g1.z, u1.z, g1.w, u1.w, b1.z, b1.w);
+    for (int half = 0; half < 2; ++half) {
+      uint32_t a[8];
+      ldsm_x4(tile + (a_x ^ (half << 6)), a[0], a[1], a[2], a[3]);
+      ldsm_x4(tile + (a_x ^ (half << 6 | 32)), a[4], a[5], a[6], a[7]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j >= nt) break;
+        uint32_t b[4];
+        ldsm_x4(rows + j * 1024 + (b_at ^ (half << 6)), b[0], b[1], b[2], b[3]);
+        mma_bf16(sum[j], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_bf16(sum[j], a[4], a[5], a[6], a[7], b[2], b[3]);
+      }
     }
-    bump(get);
+    __syncwarp();
+    get.advance(S);
   };
   auto clear = [&]() {
 #pragma unroll
@@ -466,37 +449,60 @@ __global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_co
       if (j < nt) red[((buf * kLayerWarps + warp) * NT + j) * 32 + lane] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
     __syncthreads();
   };
+  // this warp's steps of the rows of a tile (n of them from the list's first on; DIRECT: of all tokens)
+  auto load_rows = [&](int first, int n) {
+    uint32_t dst = rows_at;
+    for (int s = warp; s < steps_up; s += kLayerWarps, dst += NT * 1024) {
+      const int k = s * kStepK + 8 * (int)r8;
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        const int r = (int)m4 + 4 * i;
+        if (r < n) {
+          const int t = DIRECT ? r : list[first + r];
+          const uint16_t* const row = static_cast<const uint16_t*>(p.a.x) + t * p.a.x_stride;
+          op_cp16(dst + r * 128 + ((r8 ^ (r & 7)) << 4), k < d ? row + k : row, k < d ? 16 : 0);
+        }
+      }
+    }
+    op_cp_wait_all();
+    __syncwarp();
+  };
 
-  // (the ring is at most S steps ahead: a slot is filled again after its step has been multiplied, by the lane that read it)
-  int buf = 0;
+  int buf = 0, have = -1;  // the tile whose rows are there
   long long made = 0;
-  for (int run = sh.run; run < runs;) {
-    run_begin(run);
+  for (int run = (int)uniform(sh.run); run < runs;) {
+    cs = is = up_begin(run);
+    istep = warp;
+    if (is.left > 0) irow = sh.act[is.a] * f + 8 * is.grp;
     next_run = -1;
     const int all = cs.left, middle = all / 2;
-    for (int i = 0; i < S - 1; ++i) issue_first();
+    for (int i = 0; i < S; ++i) issue_next();
     while (cs.left > 0) {
-      if (tid == 0 && all - cs.left == middle) sh.next = (int)atomicAdd(p.sync, 1u);
-      const int nt = min(NT, (cs.n - cs.tile * NT * 8 + 7) / 8);
+      if (tid == 0 && all - cs.left == middle) *(volatile int*)&sh.next = (int)atomicAdd(p.sync, 1u);
+      const int e = sh.act[cs.a], first = sh.off[e] + (DIRECT ? 0 : (cs.tile - sh.tile_pre[cs.a]) * NT * 8);
+      const int n = DIRECT ? T : min(sh.off[e + 1] - first, NT * 8), nt = (n + 7) / 8;
+      if (DIRECT ? have < 0 : have != cs.tile) load_rows(first, n);
+      have = cs.tile;
       clear();
-      for (int s = warp; s < steps_up; s += kLayerWarps) {
-        issue_first();
-        op_cp_wait<S - 1>();
-        multiply(nt);
+      uint32_t rows = rows_at;
+      for (int s = warp; s < steps_up; s += kLayerWarps, rows += NT * 1024) {
+        multiply(rows, nt);
+        issue_next();
       }
       hand_in(buf, nt);
       next_run = (int)uniform((uint32_t)*(volatile int*)&sh.next);
       const int j = (warp - cs.left) & (kLayerWarps - 1);
       if (j < nt) {
         const float4 y = add_up(buf, j);
-        const int r0 = (cs.tile * NT + j) * 8 + 2 * q, o = sh.off[cs.e];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (r0 + i < cs.n) {
-            const int x = list[o + r0 + i];
-            const float gate = i ? y.y : y.x, up = i ? y.w : y.z;
-            p.h[(long long)((x >> 4) * K + (x & 15)) * f + 8 * cs.g + g] = to_bf16(weight[o + r0 + i] * (moe_silu(gate) * up));
+        for (int i = 0; i < 2; ++i) {
+          const int r = j * 8 + 2 * q + i;
+          if (r < n) {
+            const float gate = i ? y.y : y.x, up = i ? y.w : y.z, c = weight[DIRECT ? cs.a * 8 + r : first + r];
+            // (c < 0: the token has not selected the expert, and its product does not count, whatever it is)
+            p.h[(long long)(DIRECT ? cs.a * 8 + r : first + r) * f + 8 * cs.grp + g] = c < 0.f ? (uint16_t)0 : to_bf16(c * (moe_silu(gate) * up));
           }
+        }
       }
       buf ^= 1;
       up_next(cs);
@@ -504,19 +510,14 @@ __global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_co
     }
     // (a run without units has claimed nothing more)
     if (all == 0 && tid == 0) sh.next = (int)atomicAdd(p.sync, 1u);
-    op_cp_wait_all();
     __syncthreads();
-    run = next_run = sh.next;
+    run = next_run = (int)uniform(sh.next);
     __syncthreads();
     if (tid == 0) sh.next = -1;
   }
   // ---------------------------------------------------------------- hand over
-  for (; ahead < S && id.block < blocks; ++ahead) {
-    down_weights(id, put);
-    bump(put);
-    down_next(id);
-  }
-  op_cp_commit();
+  for (; ahead < S && id.block < blocks; ++ahead) issue_weights();
+  fence_async_global();  // (the results are read by tensor-map copies)
   __syncthreads();
   if (tid == 0) {
     __threadfence();
@@ -529,41 +530,27 @@ __global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_co
       }
   }
   __syncthreads();
+  fence_async_global();
   {
-    Down c = first_down;
-    uint32_t slot = get;
+    uint32_t slot = get.slot;
     for (int i = 0; i < ahead; ++i) {
-      down_rows(c, slot);
-      bump(slot);
-      down_next(c);
+      issue_rows(slot);
+      slot = slot + 1 == (uint32_t)S ? 0 : slot + 1;
     }
-    op_cp_commit();
-    op_cp_wait_all();
   }
-  auto issue_second = [&]() {
-    if (id.block < blocks) {
-      down_weights(id, put);
-      down_rows(id, put);
-      bump(put);
-      down_next(id);
-    }
-    op_cp_commit();
-  };
-  int ready = ahead;  // steps that are known to be there
   auto take = [&](int nt) {
-    if (ready > 0) {
-      --ready;
-    } else {
-      op_cp_wait<S - 1>();
+    multiply(rows_at + get.slot * NT * 1024, nt);
+    if (id.block < blocks) {
+      const uint32_t slot = put;
+      issue_weights();
+      issue_rows(slot);
     }
-    multiply(nt);
-    issue_second();
   };
 
   for (int block = blockIdx.x; block < blocks; block += (int)gridDim.x) {
     const int c0 = block * p.width, wide = min(p.width, d - c0);
     clear();
-    if (kDirect) {
+    if (DIRECT) {
       const int n = A * steps_down;
       for (int s = warp; s < n; s += kLayerWarps) take(1);
       hand_in(buf, 1);
@@ -579,20 +566,20 @@ __global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_co
       buf ^= 1;
     } else {
       for (int a = 0; a < A; ++a) {
-        const int e = sh.act[a], o = sh.off[e], n = sh.off[e + 1] - o, tiles = sh.tile_pre[a + 1] - sh.tile_pre[a];
-        for (int tile = 0; tile < tiles; ++tile) {
-          const int nt = min(NT, (n - tile * NT * 8 + 7) / 8);
+        const int e = sh.act[a], last = sh.off[e + 1];
+        for (int first = sh.off[e], turn = a; first < last; first += NT * 8, ++turn) {
+          const int n = min(last - first, NT * 8), nt = (n + 7) / 8;
           clear();
           for (int s = warp; s < steps_down; s += kLayerWarps) take(nt);
           hand_in(buf, nt);
-          const int j = (warp - a) & (kLayerWarps - 1);
+          const int j = (warp - turn) & (kLayerWarps - 1);
           if (j < nt) {
             const float4 y = add_up(buf, j);
             const float v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = (tile * NT + j) * 8 + 2 * q + (i & 1);
-              if (r < n) acc[(list[o + r] >> 4) * kAccPitch + g + 8 * (i >> 1)] += v[i];
+              const int r = j * 8 + 2 * q + (i & 1);
+              if (r < n) acc[list[first + r] * kAccPitch + g + 8 * (i >> 1)] += v[i];
             }
           }
           buf ^= 1;
@@ -611,17 +598,10 @@ __global__ void __launch_bounds__(kLayerThreads, 1) layer_kernel(const __grid_co
     }
     __syncthreads();
   }
-  op_cp_wait_all();
-}
-
-template <int NT>
-cudaError_t launch_layer(const MoeParams& p, cudaStream_t st) {
-  const int smem = LayerSmem<NT>(p.a.n_tokens, p.a.n_tokens * p.a.top_k).total;
-  constexpr int kMost = NT == 1 ? 8 : NT == 2 ? 64 : kMoeTokens;  // tokens of this form
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(layer_kernel<NT>, LayerSmem<NT>(kMost, kMost * kMoeTopK).total, done);
-  if (e != cudaSuccess) return e;
-  return launch_early(layer_kernel<NT>, dim3((unsigned)p.grid), kLayerThreads, (size_t)smem, st, p);
+  if (sh.abort) {  // an abandoned run leaves copies in flight: give them time to land
+    const uint64_t s0 = gtime();
+    while ((long long)(gtime() - s0) < 10000000ll) {}
+  }
 }
 
 template <int TT>
@@ -631,34 +611,69 @@ cudaError_t launch_router(const MoeParams& p, cudaStream_t st) {
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
+constexpr int kMostSmem = 232448 - ((int)sizeof(LayerShared) + 127) / 128 * 128;
+
+// slots of a warp's ring that fit: as many as there is room for
+int layer_slots(const mk_moe_args& a, int nt, bool direct) {
+  for (int s = kMaxSlots; s >= 2; --s)
+    if (LayerSmem(nt, direct, s, a.d_model, a.n_tokens, a.top_k).total <= kMostSmem) return s;
+  return 0;
+}
+
+template <int NT, bool DIRECT>
+cudaError_t launch_layer(const MoeParams& p, const MoeMaps& m, cudaStream_t st) {
+  const int smem = LayerSmem(NT, DIRECT, p.slots, p.a.d_model, p.a.n_tokens, p.a.top_k).total;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(layer_kernel<NT, DIRECT>, kMostSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_early(layer_kernel<NT, DIRECT>, dim3((unsigned)p.grid), kLayerThreads, (size_t)smem, st, p, m.gate, m.up, m.down, m.h);
+}
+
 }  // namespace
+
+long long moe_h_rows(const mk_moe_args& a) {
+  const long long entries = (long long)a.n_tokens * a.top_k;
+  return a.n_tokens <= kMoeDirect ? 8 * std::min<long long>(a.n_experts, entries) : entries;
+}
 
 size_t moe_workspace_bytes(const mk_moe_args& a) {
   const size_t entries = (size_t)a.n_tokens * a.top_k;
-  return 16 + 2 * align16(entries * 4) + align16(entries * a.d_ff * 2);
+  return 16 + 2 * align16(entries * 4) + (size_t)moe_h_rows(a) * a.d_ff * 2;
 }
 
-cudaError_t launch_moe(const MoeParams& args, cudaStream_t st) {
-  MoeParams p = args;
-  const size_t entries = (size_t)p.a.n_tokens * p.a.top_k;
-  uint8_t* at = static_cast<uint8_t*>(p.a.workspace);
+int moe_shape(MoeParams& p) {
+  const mk_moe_args& a = p.a;
+  const size_t entries = (size_t)a.n_tokens * a.top_k;
+  uint8_t* at = static_cast<uint8_t*>(a.workspace);
   p.sync = reinterpret_cast<uint32_t*>(at);
   at += 16;
-  p.ids = p.a.ids ? p.a.ids : reinterpret_cast<int32_t*>(at);
+  p.ids = a.ids ? a.ids : reinterpret_cast<int32_t*>(at);
   at += align16(entries * 4);
-  p.weights = p.a.weights ? p.a.weights : reinterpret_cast<float*>(at);
+  p.weights = a.weights ? a.weights : reinterpret_cast<float*>(at);
   at += align16(entries * 4);
   p.h = reinterpret_cast<uint16_t*>(at);
   // output columns: 16 at most, in blocks of equal width over all CTAs
-  p.rounds = (p.a.d_model + 16 * p.grid - 1) / (16 * p.grid);
-  p.width = (p.a.d_model + p.rounds * p.grid - 1) / (p.rounds * p.grid);
+  const int rounds = (a.d_model + 16 * p.grid - 1) / (16 * p.grid);
+  p.width = (a.d_model + rounds * p.grid - 1) / (rounds * p.grid);
+  // rows of a tile: what most experts have
+  const double mean = (double)entries / a.n_experts;
+  p.direct = a.n_tokens <= kMoeDirect;
+  p.nt = p.direct || mean <= 3 ? 1 : mean <= 10 ? 2 : 4;
+  while ((p.slots = layer_slots(a, p.nt, p.direct)) < 4 && p.nt > 1) p.nt /= 2;
+  return p.slots;
+}
+
+cudaError_t launch_moe(const MoeParams& p, const MoeMaps& m, cudaStream_t st) {
   const int t = p.a.n_tokens, clusters = 2 * p.grid / kRouterCtas;
   cudaError_t e = t <= clusters       ? launch_router<1>(p, st)
                   : t <= 2 * clusters ? launch_router<2>(p, st)
                   : t <= 4 * clusters ? launch_router<4>(p, st)
                                       : launch_router<8>(p, st);
   if (e != cudaSuccess) return e;
-  return t <= 8 ? launch_layer<1>(p, st) : t <= 64 ? launch_layer<2>(p, st) : launch_layer<4>(p, st);
+  return p.direct    ? launch_layer<1, true>(p, m, st)
+         : p.nt == 1 ? launch_layer<1, false>(p, m, st)
+         : p.nt == 2 ? launch_layer<2, false>(p, m, st)
+                     : launch_layer<4, false>(p, m, st);
 }
 
 }  // namespace mk

@@ -158,8 +158,8 @@ int check_moe(const mk_moe_args* a) {
   if (a->n_experts < 1 || a->n_experts > kOpMaxExperts) return op_fail(MK_ERR_INVALID, "n_experts %d not in [1, %d]", a->n_experts, kOpMaxExperts);
   if (a->top_k < 1 || a->top_k > kMoeTopK || a->top_k > a->n_experts)
     return op_fail(MK_ERR_INVALID, "top_k %d not in [1, min(%d, n_experts)]", a->top_k, kMoeTopK);
-  if (a->d_model < 8 || a->d_model % 8 || a->d_model > (1 << 16) || a->d_ff < 8 || a->d_ff % 8 || a->d_ff > (1 << 16))
-    return op_fail(MK_ERR_UNSUPPORTED, "d_model %d and d_ff %d must be multiples of 8 in [8, 65536]", a->d_model, a->d_ff);
+  if (a->d_model < 8 || a->d_model % 8 || a->d_model > kMoeWidest || a->d_ff < 8 || a->d_ff % 8 || a->d_ff > (1 << 16))
+    return op_fail(MK_ERR_UNSUPPORTED, "d_model %d and d_ff %d must be multiples of 8, up to %d and 65536", a->d_model, a->d_ff, kMoeWidest);
   return MK_OK;
 }
 
@@ -488,9 +488,22 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
   MoeParams p{};
   p.a = *a;
   r = num_sms(&p.grid);
+  if (r) return r;
+  if (!moe_shape(p)) return op_fail(MK_ERR_UNSUPPORTED, "d_model %d with %d tokens does not fit shared memory", a->d_model, a->n_tokens);
+  MoeMaps m;
+  const auto matrix = [&](CUtensorMap* tm, const void* base, long long rows, long long cols, int high) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)high};
+    return encode(tm, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  r = matrix(&m.gate, a->w_gate, e * f, d, 8);
+  if (!r) r = matrix(&m.up, a->w_up, e * f, d, 8);
+  if (!r) r = matrix(&m.down, a->w_down, e * d, f, p.width);
+  if (!r) r = matrix(&m.h, p.h, moe_h_rows(*a), f, 8 * p.nt);
   if (!r) r = set_record(p.a.status);
   if (r) return r;
-  return cuda_error(launch_moe(p, static_cast<cudaStream_t>(stream)), "moe_layer launch");
+  return cuda_error(launch_moe(p, m, static_cast<cudaStream_t>(stream)), "moe_layer launch");
 }
 
 int mk_verify_nodes_workspace(const mk_verify_args* a, size_t* bytes) {

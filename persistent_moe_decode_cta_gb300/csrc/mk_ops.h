@@ -28,6 +28,19 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& do
   return e;
 }
 
+// Allow `kernel` clusters of more than 8 blocks, likewise.
+template <class K>
+cudaError_t allow_wide_clusters(K* kernel, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Launch `kernel` so that its prologue may run beside the end of the kernel before it on the
 // stream (griddepcontrol.wait in the kernel is where it waits for that one).
 template <class... P, class... A>
@@ -140,17 +153,26 @@ cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, con
 // ------------------------------------------------------------------ moe_layer
 constexpr int kMoeTokens = 256;   // tokens of one call
 constexpr int kMoeTopK = 16;
+constexpr int kMoeDirect = 8;     // up to here a tile's rows are the tokens
+constexpr int kMoeWidest = 8192;  // d_model: a tile's rows stay in shared memory
 struct MoeParams {
   mk_moe_args a;
   int grid;          // CTAs of the products
-  int rounds, width; // output columns of a CTA: `rounds` blocks of `width` at most
+  int width;         // output columns of a CTA's block
+  int nt, slots;     // row tiles of a pass, slots of a warp's ring
+  bool direct;
   int32_t* ids;      // the caller's or the workspace's
   float* weights;
-  uint16_t* h;       // [tokens * top_k][d_ff] bf16: c * silu(gate) * up
+  uint16_t* h;       // [moe_h_rows][d_ff] bf16: c * silu(gate) * up
   uint32_t* sync;    // counters, zeroed by the router
 };
+struct MoeMaps {
+  CUtensorMap gate, up, down, h;
+};
 size_t moe_workspace_bytes(const mk_moe_args& a);
-cudaError_t launch_moe(const MoeParams& p, cudaStream_t st);
+long long moe_h_rows(const mk_moe_args& a);
+int moe_shape(MoeParams& p);  // fills what follows `grid`; 0: it does not fit
+cudaError_t launch_moe(const MoeParams& p, const MoeMaps& m, cudaStream_t st);
 
 // ------------------------------------------------------------------ verify_nodes
 constexpr int kVerifyVocab = 1 << 18;

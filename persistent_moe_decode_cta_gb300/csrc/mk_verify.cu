@@ -22,6 +22,9 @@ constexpr int kWalkThreads = 512, kWalkWarps = kWalkThreads / 32;
 constexpr int kWalkCtas = 16;              // of a cluster at most
 constexpr int kFixed = 44;                 // fraction bits of an exponential
 constexpr int kBlock = 128;                // elements that a warp takes at a time: four a lane
+constexpr int kWarpBlocks = 12;            // ... of a row at most: in registers while they are under way
+constexpr int kCtaBlocks = 180;            // blocks whose exponentials fit a CTA's shared memory
+static_assert(kCtaBlocks <= kWarpBlocks * kWalkWarps, "");
 
 __device__ __forceinline__ float load_logit(const void* p, long long at, bool f32) {
   return f32 ? op_ldf(static_cast<const float*>(p) + at) : bf16_to_f(op_ld2(static_cast<const uint16_t*>(p) + at));
@@ -53,11 +56,18 @@ __device__ __forceinline__ const void* logit_row(const mk_verify_args& a, int b,
                         : static_cast<const void*>(static_cast<const uint16_t*>(a.logits) + at);
 }
 
-// log2(e) / temperature; a temperature of 0 (the largest logit alone counts) reads as 1 here
-__device__ __forceinline__ double heat(const mk_verify_args& a, int b, float* t) {
-  *t = a.temperature ? op_ldf(a.temperature + b) : 1.f;
-  return 1.4426950408889634074 / (*t > 0.f ? (double)*t : 1.0);
-}
+// log2(e) / temperature as a sum of two floats, to 2^-46; a temperature of 0 (the largest logit alone counts) reads as 1 here
+struct Heat {
+  float t, hi, lo;
+  __device__ __forceinline__ explicit Heat(float temperature) : t(temperature) {
+    const float x = t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 1.f;
+    const float r = 1.f / x, e = fmaf(-r, x, 1.f) * r;  // 1 / x = r + e
+    constexpr float kH = 1.44269502162933349609375f, kL = 1.92596299112661746887e-8f;
+    hi = __fmul_rn(kH, r);
+    lo = fmaf(kH, r, -hi) + fmaf(kH, e, kL * r);
+  }
+};
+__device__ __forceinline__ float temperature(const mk_verify_args& a, int b) { return a.temperature ? op_ldf(a.temperature + b) : 1.f; }
 __device__ __forceinline__ int node_count(const mk_verify_args& a, int b) { return a.counts ? op_ld(a.counts + b) : a.n_nodes; }
 
 // -------------------------------------------------------------------------------------------- rows
@@ -75,8 +85,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const bool f32 = p.a.logits_float != 0;
   const void* row = logit_row(p.a, b, node);
   const bool wide = is_wide(row, f32);
-  float t;
-  const float beta = (float)fmin(heat(p.a, b, &t), 1e30);
+  const float beta = Heat(temperature(p.a, b)).hi;
   const int base = piece * (kRowThreads * 4 * ITER) + 4 * threadIdx.x;
   float4 v[ITER];
 #pragma unroll
@@ -116,16 +125,30 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------------------------- exponentials
-// 2^(i/256), i = -128 .. 128, in units of 2^-52 and as a sum of two floats (exp2 of a double is good to 2^-52)
-constexpr int kTable = 257;
+// 2^(i/256), i = -128 .. 128, in units of 2^-52 and as a sum of two floats
+constexpr int kPowers = 257;
 struct __align__(16) Power {
   unsigned long long fix;
   float hi, lo;
 };
+struct Powers {
+  Power v[kPowers];
+  constexpr Powers() : v() {
+    for (int i = 0; i < kPowers; ++i) {
+      const double x = (i - 128) / 256.0 * 0.69314718055994530942;
+      double y = 1;
+      for (int k = 18; k > 0; --k) y = 1 + x / k * y;  // the exponential series
+      v[i].fix = (unsigned long long)(y * 4503599627370496.0 + 0.5);
+      v[i].hi = (float)y;
+      v[i].lo = (float)(y - (double)v[i].hi);
+    }
+  }
+};
+__device__ const Powers powers = Powers();
 
 struct Exp {
   float top;        // the row's largest logit
-  float bh, bl;     // log2(e) / T as a sum of two floats
+  float bh, bl;     // log2(e) / T
   const Power* table;
   // exp((l - top) / T) in units of 2^-44, for finite l <= top, to 2^-41 of itself; 0 for anything else.
   __device__ __forceinline__ unsigned long long operator()(float l) const {
@@ -173,18 +196,20 @@ struct Cut {
 };
 
 // -------------------------------------------------------------------------------------------- walk
-struct Node {
+struct __align__(16) Node {
   int parent, token;   // parent -1: not a child of anything
+  int first, next;     // its first child, its parent's next child; -1: none
   float u;             // its uniform
   float l, q;          // logit and draft probability of the token in the parent's row
+  int fits;            // whether it is accepted as long as no sibling was rejected
   float top, sum;      // of its own row
-  int arg;
+  int arg, pad;
 };
 struct Part {
   unsigned long long sum;
-  unsigned long long bad;
+  unsigned long long pad;
 };
-enum { kLoad = 1, kCut = 2, kDraw = 3, kEnd = 4 };
+enum { kCut, kDraw, kEnd };
 
 struct WalkShared {
   Node node[kOpMaxAccept];
@@ -192,10 +217,10 @@ struct WalkShared {
   int gone[kOpMaxAccept];              // tokens of rejected children (drafts without probabilities)
   Part part[2][kWalkCtas];             // the CTAs' sums, written by each into all
   unsigned long long warp_sum[kWalkWarps];
-  Power table[kTable];
-  unsigned long long a, w;             // A and W of the row
+  Power power[kPowers];
   float t;
-  int count, at, length, n_gone, step, next, stuck, loaded, parity;
+  int count;                           // (behind t: the two are copied together)
+  int step, at, length, n_gone, next;
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -237,42 +262,40 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool f32 = a.logits_float != 0;
   int count = node_count(a, b);
-  float t;
-  const float beta = (float)fmin(heat(a, b, &t), 1e30);
+  const Heat heat(temperature(a, b));
   if (count < 1 || count > a.n_nodes) {
     if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, count);
     count = 0;
-  } else if (!(t >= 0.f)) {
-    if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, __float_as_int(t));
+  } else if (!(heat.t >= 0.f)) {
+    if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, __float_as_int(heat.t));
     count = 0;
   }
-  if (tid == 0) sh.count = count, sh.t = t;
-  for (int i = tid; i < count; i += kWalkThreads) {
+  if (tid == 0) sh.count = count, sh.t = heat.t;
+  if (tid < count) {
+    const int i = tid;
     const long long at = (long long)b * a.n_nodes + i;
     Node x{};
+    x.first = x.next = -1;
     x.parent = i == 0 ? -1 : a.parents ? op_ld(a.parents + at) : i - 1;
+    x.token = i == 0 ? 0 : op_ld(a.tokens + at);
     x.u = op_ldf(a.uniforms + at);
     bool fine = true;
     if (!(x.u >= 0.f && x.u < 1.f)) {
       op_error(a.status, MK_ERR_INVALID, b, i, __float_as_int(x.u));
       x.u = 0.f;
       fine = false;
+    } else if (i > 0 && (x.parent < 0 || x.parent >= i)) {
+      op_error(a.status, MK_ERR_INVALID, b, i, x.parent);
+      fine = false;
+    } else if (x.token < 0 || x.token >= a.vocab) {
+      op_error(a.status, MK_ERR_INVALID, b, i, x.token);
+      fine = false;
     }
-    if (i > 0) {
-      x.token = op_ld(a.tokens + at);
-      if (x.parent < 0 || x.parent >= i) {
-        op_error(a.status, MK_ERR_INVALID, b, i, x.parent);
-        fine = false;
-      } else if (x.token < 0 || x.token >= a.vocab) {
-        op_error(a.status, MK_ERR_INVALID, b, i, x.token);
-        fine = false;
-      }
-      if (fine) {
-        x.l = load_logit(logit_row(a, b, x.parent), x.token, f32);
-        x.q = a.draft_probs ? fminf(fmaxf(op_ldf(a.draft_probs + b * a.draft_stride[0] + x.parent * a.draft_stride[1] + x.token), 0.f), 1.f) : 1.f;
-      } else {
-        x.parent = -1;
-      }
+    if (i > 0 && fine) {
+      x.l = load_logit(logit_row(a, b, x.parent), x.token, f32);
+      x.q = a.draft_probs ? fminf(fmaxf(op_ldf(a.draft_probs + b * a.draft_stride[0] + x.parent * a.draft_stride[1] + x.token), 0.f), 1.f) : 1.f;
+    } else {
+      x.parent = -1;
     }
     sh.node[i] = x;
   }
@@ -286,17 +309,17 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
       const uint4 u = op_ld16(part + j);
       const float m = __uint_as_float(u.x), s = __uint_as_float(u.y);
       if (m > top) {
-        sum *= ex2((top - m) * beta);
+        sum *= ex2((top - m) * heat.hi);
         top = m;
         arg = (int)u.z;
       }
-      sum += m == -INFINITY ? s : s * ex2((m - top) * beta);
+      sum += m == -INFINITY ? s : s * ex2((m - top) * heat.hi);
     }
     float all = top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
     if (top != all) {
-      sum = top == -INFINITY ? sum : sum * ex2((top - all) * beta);
+      sum = top == -INFINITY ? sum : sum * ex2((top - all) * heat.hi);
       arg = 0x7fffffff;
     }
 #pragma unroll
@@ -310,32 +333,50 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
       sh.node[i].arg = arg;
     }
   }
+  __syncthreads();
+  if (tid < count) {
+    // the children in order, and the test of each against its parent's whole row
+    const int up = sh.node[tid].parent;
+    int first = -1, next = -1;
+    for (int j = count - 1; j > tid; --j) {
+      const int of = sh.node[j].parent;
+      if (of == tid) first = j;
+      if (of == up) next = j;
+    }
+    bool fits = false;
+    if (up >= 0) {
+      const Node x = sh.node[tid], v = sh.node[up];
+      const Exp ex{v.top, heat.hi, heat.lo, sh.power};
+      fits = heat.t == 0.f ? x.token == v.arg && x.u * x.q < 1.f  // (p is 1 at the largest)
+                           : (double)x.u * (double)x.q * ((double)v.sum * 0x1p44) < (double)ex(x.l);
+    }
+    sh.node[tid].first = first;
+    sh.node[tid].next = up < 0 ? -1 : next;
+    sh.node[tid].fits = fits;
+  }
 }
 
-// The CTAs' sums of a pass, in all of them; their total.  (Two sets in turn: a CTA may write the next pass's sums while another
-// still reads this one's, but no CTA is two barriers ahead.)
-__device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned long long warp_sum, bool bad, int* parity, bool* any) {
+// The sum of what the warps of all CTAs hand in.  (Two sets in turn: a CTA may write the next pass's sums while another still reads
+// this one's, but no CTA is two barriers ahead.)
+__device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned long long warp_sum, int* parity) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ctas = cta_count(), rank = cta_rank();
   if (lane == 0) sh.warp_sum[warp] = warp_sum;
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   if (threadIdx.x < ctas) {
     unsigned long long mine = 0;
     for (int i = 0; i < kWalkWarps; ++i) mine += sh.warp_sum[i];
-    const uint32_t to = map_cta(&sh.part[*parity][rank], threadIdx.x);
-    put64(to, mine);
-    put64(to + 8, bad);
+    put64(map_cta(&sh.part[*parity][rank], threadIdx.x), mine);
   }
   walk_sync();
-  unsigned long long total = 0, flags = 0;
-  for (uint32_t i = 0; i < ctas; ++i) total += sh.part[*parity][i].sum, flags |= sh.part[*parity][i].bad;
-  *any = flags != 0;
+  unsigned long long total = 0;
+  for (uint32_t i = 0; i < ctas; ++i) total += sh.part[*parity][i].sum;
   *parity ^= 1;
   return total;
 }
 
-// One cluster per sequence.  Every CTA takes the same decisions from the same numbers (the first CTA's copy of the nodes, and sums
-// that each has of all), so that all of them pass the same barriers.
+// One cluster per sequence.  Every CTA's first thread walks by itself, all of them from the same numbers (the first CTA's copy of the
+// nodes, and sums that each has of all), so that they ask for the same passes and meet at the same barriers.
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ __align__(16) WalkShared sh;
@@ -347,195 +388,222 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   const bool f32 = a.logits_float != 0;
   // a piece a CTA, a part of it a warp, in whole blocks
   const int blocks = (a.vocab + kBlock - 1) / kBlock, mine = (blocks + (int)ctas - 1) / (int)ctas, per = (mine + kWalkWarps - 1) / kWalkWarps;
-  const int base = (int)rank * mine * kBlock;                                  // first element of the CTA
-  const int first = min(warp * per, mine), last = min(first + per, mine);      // blocks of this warp
-  for (int i = tid; i < kTable; i += kWalkThreads) {
-    const double y = exp2((i - 128) / 256.0);
-    sh.table[i] = Power{(unsigned long long)__double2ll_rn(y * 0x1p52), (float)y, (float)(y - (double)(float)y)};
-  }
+  const int base = (int)rank * mine * kBlock;                                       // first element of the CTA
+  const int first = min(warp * per, mine), n_blocks = min(per, mine - first);       // blocks of this warp (kWarpBlocks at most)
+  const int from = first * kBlock + 4 * lane;                                       // first element of this lane in the piece
+  for (int i = tid; i < kPowers; i += kWalkThreads) sh.power[i] = powers.v[i];
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (rank == 0) gather_nodes(p, sh, b);
   walk_sync();
   if (rank != 0) {
     if (tid == 0) {
-      const uint32_t from = map_cta(&sh.t, 0);
+      const uint32_t of = map_cta(&sh.t, 0);
       uint32_t x, y;
-      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
-      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(y) : "r"(from + 4) : "memory");
+      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(of) : "memory");
+      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(y) : "r"(of + 4) : "memory");
       sh.t = __uint_as_float(x);
       sh.count = (int)y;
     }
     __syncthreads();
-    for (int i = tid; i < 2 * sh.count; i += kWalkThreads)
+    for (int i = tid; i < 3 * sh.count; i += kWalkThreads)
       *(reinterpret_cast<uint4*>(sh.node) + i) = get128(map_cta(reinterpret_cast<const uint4*>(sh.node) + i, 0));
   }
   __syncthreads();
   const int count = sh.count;
-  const float t = sh.t;
-  const double beta = 1.4426950408889634074 / (t > 0.f ? (double)t : 1.0);
-  Exp ex;
-  ex.bh = (float)fmin(beta, 1e30);
-  ex.bl = beta < 1e30 ? (float)(beta - (double)ex.bh) : 0.f;
-  ex.table = sh.table;
-  int parity = 0, at = 0, length = 0, next = -1;
-  bool bad = count == 0;
+  const Heat heat(sh.t);
+  Exp ex{0.f, heat.hi, heat.lo, sh.power};
+  int parity = 0, at = 0, row_at = -1;
+  // of the row at `at`: A and W, and what this warp has of W
+  unsigned long long A = 0, W = 0, warp_sum = 0;
+  bool loaded = false, stuck = false;
+  float4 qs[kWarpBlocks];
+  // the first thread's: the child to test (-2: at a new node), and before the row is loaded its sum without the tokens that are gone
+  int child = -2, length = 0, n_gone = 0;
+  bool whole = true;  // no child rejected yet
+  double left = 0;
 
-  while (!bad) {
-    const Node here = sh.node[at];
-    if (tid == 0) sh.path[length] = at;
-    ++length;
-    bad = !(fabsf(here.top) < INFINITY && here.sum > 0.f);  // (a NaN in the row is a NaN in the sum)
-    if (bad) {
-      if (rank == 0 && tid == 0) op_error(a.status, MK_ERR_INVALID, b, at, __float_as_int(here.top));
-      break;
+  for (;;) {
+    if (tid == 0) {
+      int step = -1;
+      while (step < 0) {
+        if (count == 0) {
+          step = kEnd;
+          sh.next = -1;
+        } else if (child == -2) {
+          const Node& v = sh.node[at];
+          sh.path[length++] = at;
+          child = v.first;
+          n_gone = 0;
+          whole = true;
+          left = (double)v.sum * 0x1p44;
+          if (!(fabsf(v.top) < INFINITY && v.sum > 0.f)) {  // (a NaN in the row is a NaN in the sum)
+            if (rank == 0) op_error(a.status, MK_ERR_INVALID, b, at, __float_as_int(v.top));
+            step = kEnd;
+            sh.next = -1;
+          }
+        } else if (child < 0) {
+          step = kDraw;
+          if (heat.t == 0.f) {
+            step = kEnd;
+            sh.next = sh.node[at].arg;
+          }
+        } else {
+          const Node& c = sh.node[child];
+          bool taken = c.fits != 0;
+          unsigned long long y = 0;
+          if (!taken || !whole) {
+            ex.top = sh.node[at].top;
+            y = ex(c.l);
+          }
+          if (!whole && heat.t != 0.f) {
+            if (a.draft_probs) {
+              y = Cut(A)(y, c.q);
+            } else {
+              for (int g = 0; g < n_gone; ++g)
+                if (sh.gone[g] == c.token) y = 0;
+            }
+            taken = (double)c.u * (double)c.q * (a.draft_probs ? (double)W : left) < (double)y;
+          }
+          if (taken) {
+            at = child;
+            child = -2;
+          } else {
+            child = c.next;
+            whole = false;
+            if (heat.t != 0.f) {
+              if (a.draft_probs) {
+                step = kCut;
+              } else if (left > (double)y) {
+                left -= (double)y;
+                sh.gone[n_gone++] = c.token;
+              }
+            }
+          }
+        }
+      }
+      sh.step = step;
+      sh.at = at;
+      sh.n_gone = n_gone;
     }
-    const void* const row = logit_row(a, b, at);
-    const float* const draft = a.draft_probs ? a.draft_probs + b * a.draft_stride[0] + at * a.draft_stride[1] : nullptr;
-    const bool wide = is_wide(row, f32), qwide = is_wide(draft, true);
-    ex.top = here.top;
-    int n_gone = 0, taken = -1;
-    bool loaded = false, stuck = false;
-    unsigned long long A = 0, W = 0;                       // of the row once it is loaded
-    double left = (double)here.sum * 0x1p44;               // ... and before that, without the tokens that are gone
-
-    // the row's exponentials into shared memory, and their sum
-    auto load = [&]() {
-      unsigned long long sum = 0;
-      for (int k = first; k < last; ++k) {
-        const int j = base + k * kBlock + 4 * lane;
-        const float4 v = load4(row, j, a.vocab, f32, wide, -INFINITY);
-        unsigned long long y[4] = {ex(v.x), ex(v.y), ex(v.z), ex(v.w)};
-        for (int g = 0; g < n_gone; ++g) {
-          const int d = sh.gone[g] - j;
+    __syncthreads();
+    const int step = sh.step, gone = sh.n_gone, asked = sh.at;
+    __syncthreads();  // (the first thread may go on)
+    if (step == kEnd) break;
+    loaded = loaded && row_at == asked;
+    at = row_at = asked;
+    const bool draft = a.draft_probs != nullptr;
+    const float* const drow = draft ? a.draft_probs + b * a.draft_stride[0] + at * a.draft_stride[1] : nullptr;
+    // ------------------------------------------------------------ the row's exponentials into shared memory, and their sum
+    if (!loaded) {
+      const void* const row = logit_row(a, b, at);
+      const bool wide = is_wide(row, f32), qwide = is_wide(drow, true);
+      ex.top = sh.node[at].top;
+      float4 v[kWarpBlocks];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (d == i) y[i] = 0;
+      for (int k = 0; k < kWarpBlocks; ++k)
+        if (k < n_blocks) v[k] = load4(row, base + from + k * kBlock, a.vocab, f32, wide, -INFINITY);
+      unsigned long long sum = 0;
+#pragma unroll
+      for (int k = 0; k < kWarpBlocks; ++k)
+        if (k < n_blocks) {
+          unsigned long long y[4] = {ex(v[k].x), ex(v[k].y), ex(v[k].z), ex(v[k].w)};
+          for (int g = 0; g < gone; ++g) {
+            const int d = sh.gone[g] - (base + from + k * kBlock);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (d == i) y[i] = 0;
+          }
+          ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + from + k * kBlock);
+          to[0] = make_ulonglong2(y[0], y[1]);
+          to[1] = make_ulonglong2(y[2], y[3]);
+          sum += y[0] + y[1] + y[2] + y[3];
         }
-        ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + k * kBlock + 4 * lane);
-        to[0] = make_ulonglong2(y[0], y[1]);
-        to[1] = make_ulonglong2(y[2], y[3]);
-        sum += y[0] + y[1] + y[2] + y[3];
+      if (step == kCut) {  // (on their way while the sums meet)
+#pragma unroll
+        for (int k = 0; k < kWarpBlocks; ++k)
+          if (k < n_blocks) qs[k] = load4(drow, base + from + k * kBlock, a.vocab, true, qwide, 0.f);
       }
-      bool any;
-      W = exchange(sh, warp_total(sum), false, &parity, &any);
+      warp_sum = warp_total(sum);
+      A = 0;
+      W = exchange(sh, warp_sum, &parity);
       loaded = true;
-    };
-
-    for (int i = at + 1; i < count && taken < 0; ++i) {
-      const Node c = sh.node[i];
-      if (c.parent != at) continue;
-      if (t == 0.f) {  // p is 1 at the largest: a draft of anything else is rejected, and changes nothing
-        if (c.token == here.arg && (double)c.u * c.q < 1.0) taken = i;
-        continue;
-      }
-      unsigned long long y = ex(c.l);
-      if (draft) {
-        if (A) y = Cut(A)(y, c.q);
-      } else {
-        for (int g = 0; g < n_gone; ++g)
-          if (sh.gone[g] == c.token) y = 0;
-      }
-      const double whole = loaded ? (double)W : left;
-      if ((double)c.u * (double)c.q * whole < (double)y) {
-        taken = i;
-      } else if (draft) {
-        if (!loaded) load();
-        if (!stuck) {
-          const Cut cut(A + W);
-          unsigned long long sum = 0;
-          for (int k = first; k < last; ++k) {
-            const int j = k * kBlock + 4 * lane;
-            const float4 q = load4(draft, base + j, a.vocab, true, qwide, 0.f);
-            const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(e + j), hi = *reinterpret_cast<const ulonglong2*>(e + j + 2);
-            sum += cut(lo.x, q.x) + cut(lo.y, q.y) + cut(hi.x, q.z) + cut(hi.y, q.w);
-          }
-          const unsigned long long before = sh.warp_sum[warp];
-          sum = warp_total(sum);
-          bool any;
-          const unsigned long long now = exchange(sh, sum, false, &parity, &any);
-          if (now) {
-            A += W;
-            W = now;
-          } else {  // nothing is left: it stays as it was
-            stuck = true;
-            __syncthreads();
-            if (lane == 0) sh.warp_sum[warp] = before;
-          }
-        }
-      } else if (left > (double)y) {
-        left -= (double)y;
-        __syncthreads();
-        if (tid == 0) sh.gone[n_gone] = c.token;
-        ++n_gone;
-        __syncthreads();
-      }
+      stuck = false;
     }
-    if (taken >= 0) {
-      at = taken;
+    if (step == kCut) {
+      if (!stuck) {
+        const Cut cut(A + W);
+        unsigned long long sum = 0;
+#pragma unroll
+        for (int k = 0; k < kWarpBlocks; ++k)
+          if (k < n_blocks) {
+            const ulonglong2* const y = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
+            const ulonglong2 lo = y[0], hi = y[1];
+            sum += cut(lo.x, qs[k].x) + cut(lo.y, qs[k].y) + cut(hi.x, qs[k].z) + cut(hi.y, qs[k].w);
+          }
+        sum = warp_total(sum);
+        const unsigned long long now = exchange(sh, sum, &parity);
+        if (now) {
+          A += W;
+          W = now;
+          warp_sum = sum;
+        } else {
+          stuck = true;  // nothing would be left: it stays as it was
+        }
+      }
       continue;
     }
-    // the next token: the first index whose running sum passes u times the whole
-    if (t == 0.f) {
-      next = here.arg;
-      break;
-    }
-    if (!loaded) load();
-    __syncthreads();
-    bad = W == 0;
-    if (bad) break;
+    // ------------------------------------------------------------ the first index whose running sum passes u times the whole
     // (u has 24 bits: u 2^64 is exact from 2^-40 on)
     const unsigned long long goal = __umul64hi((unsigned long long)((double)sh.node[0].u * 0x1p64), W);
-    // whose piece it lies in: the parts of the last pass that counted
+    exchange(sh, warp_sum, &parity);  // (the last pass may have been one that did not count)
     unsigned long long sum = 0;
-    const Cut cut(A);
-    // sums of the CTAs before this one, from their warps' sums
-    if (tid == 0) {
-      unsigned long long own = 0;
-      for (int i = 0; i < kWalkWarps; ++i) own += sh.warp_sum[i];
-      for (uint32_t i = 0; i < ctas; ++i) put64(map_cta(&sh.part[parity][rank], i), own);
-    }
-    walk_sync();
-    for (uint32_t i = 0; i < rank; ++i) sum += sh.part[parity][i].sum;
+    for (uint32_t i = 0; i < rank; ++i) sum += sh.part[parity ^ 1][i].sum;
     for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
-    const unsigned long long end = sum + sh.warp_sum[warp];
-    if (goal >= sum && goal < end) {  // this warp's
-      for (int k = first; k < last; ++k) {
-        const int j = k * kBlock + 4 * lane;
-        unsigned long long y[4];
+    if (goal >= sum && goal < sum + warp_sum) {  // this warp's
+      const Cut cut(A);
+      bool found = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = e[j + i];
-        if (A) {
-          const float4 q = load4(draft, base + j, a.vocab, true, qwide, 0.f);
-          y[0] = cut(y[0], q.x), y[1] = cut(y[1], q.y), y[2] = cut(y[2], q.z), y[3] = cut(y[3], q.w);
-        }
-        const unsigned long long own = y[0] + y[1] + y[2] + y[3];
-        unsigned long long upto = own;
+      for (int k = 0; k < kWarpBlocks; ++k)
+        if (k < n_blocks && !found) {
+          const ulonglong2* const at4 = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
+          const ulonglong2 lo = at4[0], hi = at4[1];
+          unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
+          if (A) y[0] = cut(y[0], qs[k].x), y[1] = cut(y[1], qs[k].y), y[2] = cut(y[2], qs[k].z), y[3] = cut(y[3], qs[k].w);
+          const unsigned long long own = y[0] + y[1] + y[2] + y[3];
+          unsigned long long upto = own;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long z = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += z;
-        }
-        const unsigned found = __ballot_sync(0xffffffffu, sum + upto > goal);
-        if (found) {
-          if (lane == __ffs(found) - 1) {
-            unsigned long long s = sum + upto - own;
-            int i = 0;
-            while (i < 3 && s + y[i] <= goal) s += y[i++];
-            a.next_tokens[b] = base + j + i;
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long z = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += z;
           }
-          break;
+          const unsigned past = __ballot_sync(0xffffffffu, sum + upto > goal);
+          if (past) {
+            found = true;
+            if (lane == __ffs(past) - 1) {
+              unsigned long long s = sum + upto - own;
+              int i = 0;
+#pragma unroll
+              for (int j = 0; j < 3; ++j)
+                if (i == j && s + y[j] <= goal) s += y[j], ++i;
+              a.next_tokens[b] = base + from + k * kBlock + i;
+            }
+          } else {
+            sum += __shfl_sync(0xffffffffu, upto, 31);
+          }
         }
-        sum += __shfl_sync(0xffffffffu, upto, 31);
-      }
     }
-    next = -2;  // written
+    if (tid == 0) sh.next = -2;  // written
     break;
   }
-  __syncthreads();
   if (rank == 0) {
-    for (int i = tid; i < a.n_nodes; i += kWalkThreads) a.accepted[(long long)b * a.n_nodes + i] = i < length ? sh.path[i] : -1;
-    if (tid == 0 && next != -2) a.next_tokens[b] = next;
+    if (tid == 0) {
+      sh.length = length;
+      if (sh.next != -2) a.next_tokens[b] = sh.next;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.n_nodes; i += kWalkThreads) a.accepted[(long long)b * a.n_nodes + i] = i < sh.length ? sh.path[i] : -1;
   }
   walk_sync();  // no CTA leaves while another may write to it or read its nodes
 }
@@ -567,17 +635,14 @@ cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
                   : iter == 4 ? launch_early(row_kernel<4>, grid, kRowThreads, 0, st, p)
                               : launch_early(row_kernel<2>, grid, kRowThreads, 0, st, p);
   if (e != cudaSuccess) return e;
-  // a piece of the exponentials has to fit shared memory
-  const int ctas = p.a.vocab <= 8 * kBlock * 180 ? 8 : kWalkCtas;
-  const int blocks = (p.a.vocab + kBlock - 1) / kBlock, mine = (blocks + ctas - 1) / ctas;
-  const size_t smem = (size_t)mine * kBlock * 8;
-  static std::atomic<unsigned long long> done{0};
-  e = allow_smem(walk_kernel, 180 * kBlock * 8, done);
+  // clusters of 16 while every sequence's fits the GPU at once, and where a piece of 8 would not fit shared memory
+  const int blocks = (p.a.vocab + kBlock - 1) / kBlock;
+  const int ctas = blocks > 8 * kCtaBlocks || (blocks > 256 && (long long)p.a.batch * kWalkCtas <= p.grid) ? kWalkCtas : 8;
+  const size_t smem = (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
+  static std::atomic<unsigned long long> done{0}, done16{0};
+  e = allow_smem(walk_kernel, kCtaBlocks * kBlock * 8, done);
+  if (e == cudaSuccess && ctas > 8) e = allow_wide_clusters(walk_kernel, done16);
   if (e != cudaSuccess) return e;
-  if (ctas > 8) {
-    e = cudaFuncSetAttribute(walk_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   return launch_clusters(walk_kernel, dim3((unsigned)(p.a.batch * ctas)), ctas, kWalkThreads, smem, st, p);
 }
 
