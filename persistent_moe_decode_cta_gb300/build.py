@@ -24,7 +24,7 @@ MODULE = os.path.join(PKG, "_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["mk_kernel.cu", "mk_kernel_det.cu", "mk_kernel_umma.cu", "mk_kernel_umma_ffn.cu",
            "mk_tree_attention.cu", "mk_experts.cu", "mk_qk_rope.cu", "mk_cache_pages.cu",
-           "mk_moe.cu", "mk_verify.cu", "mk_ops.cpp", "mk_host.cpp"]
+           "mk_linear.cu", "mk_moe.cu", "mk_verify.cu", "mk_ops.cpp", "mk_host.cpp"]
 
 
 def nvcc_path() -> str:

@@ -192,7 +192,7 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& l
 
 // (EPI: one expert with every row)
 template <bool EPI>
-__device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
+__device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
   int carry = 0;
   for (int base = 0; base < E; base += nt) {
@@ -202,7 +202,7 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh) {
       int lo = 0, hi = p.a.n_rows;
       if (!EPI) expert_rows(p, e, lo, hi);
       sh.rows[e] = make_int2(lo, hi);
-      x = (hi - lo + kTileR - 1) / kTileR;
+      x = (hi - lo + tile_rows - 1) / tile_rows;
       if (hi > lo) atomicMax(&sh.most, hi - lo);
     }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(afull(a), 1);
-      mbar_init(aempty(a), 2 * 4);
+      mbar_init(aempty(a), 2 * (EPI ? 8 : 4));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -286,7 +286,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  scan_experts<EPI>(p, sh);
+  // (a float32 result: half as many rows, whose sums the epilogue keeps in registers)
+  scan_experts<EPI>(p, sh, EPI && epi.out_float ? kTileR / 2 : kTileR);
   const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
@@ -296,6 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   const uint32_t stage_bytes = kBytesW + room * kTileK * 2, stages = room == 32 ? 9 : room == 64 ? 8 : 6;
   auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, x)); };
   auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, x); };  // (one thread)
+  // The products cut what they add to below the accumulator's last bit, so that the error of a long sum grows with its length: a
+  // float32 result adds segments of 512 columns up in registers (2048 columns: 2.1e-6 of the result without, in the 2-norm).
+  const int segment = EPI && epi.out_float ? 8 : ksteps;
   const int clusters = (int)gridDim.x / 2, mine = (tiles - (int)blockIdx.x / 2 + clusters - 1) / clusters;  // tiles of this cluster
   ExpTile x;
 
@@ -337,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       const uint64_t s0 = gtime();
       while ((long long)(gtime() - s0) < 10000000ll) {}
     }
-  } else if (warp >= kExpThreads / 32) {
+  } else if (!EPI && warp >= kExpThreads / 32) {
     // ---------------------------------------------------------------- gather
     // eight threads a row (128 bytes of a stage), 16 rows at a time; the copies report themselves
     const int t128 = (int)threadIdx.x - kExpThreads, chunk = t128 & 7, row0 = t128 >> 3;
@@ -398,11 +402,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       Ring at;
       const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);  // stage 0: weights, rows
       bool ok = true;
+      uint32_t idesc = 0, na = 0;  // (na: accumulators so far, one a tile, or one a segment of its columns)
       for (; ok && (int)nt < mine; ++nt) {
-        uint32_t idesc = 0;
-        const uint32_t a = nt & 1, acc = tmem + kTileR * a;
-        if (!(ok = wait_pair1<try_wait_cluster>(aempty(a), ((nt >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
+        uint32_t a = 0, acc = 0;
         for (int ks = 0; ks < ksteps; ++ks, at.advance(stages)) {
+          if (ks % segment == 0) {
+            if (ks > 0) umma_commit_pair(afull(a)), ++na;
+            a = na & 1, acc = tmem + kTileR * a;
+            if (!(ok = wait_pair1<try_wait_cluster>(aempty(a), ((na >> 1) & 1) ^ 1, abort, p.a.status, 2))) break;
+          }
           if (!(ok = wait_pair1<try_wait_stage>(full(at.slot), at.phase, abort, p.a.status, 3))) break;
           if (p.a.rows) {
             if (!(ok = op_wait1(gathered(at.slot), at.phase, abort, p.a.status, 8))) break;
@@ -413,10 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
           const uint64_t d = d0 + at.slot * (stage_bytes / 16);
 #pragma unroll
           for (int kk = 0; kk < kTileK / 16; ++kk)
-            umma_bf16_pair(acc, d + 2 * kk, d + kBytesW / 16 + 2 * kk, idesc, ks > 0 || kk > 0);
+            umma_bf16_pair(acc, d + 2 * kk, d + kBytesW / 16 + 2 * kk, idesc, ks % segment > 0 || kk > 0);
           umma_commit_pair(empty(at.slot));
         }
-        if (ok) umma_commit_pair(afull(a));
+        if (ok) umma_commit_pair(afull(a)), ++na;
       }
     }
     __syncwarp();
@@ -432,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     // a pair gets the other's values for half of the rows.  (A wait that gives up is not followed
     // by an exit: the pair keeps meeting, and every later wait returns at once.)
     const int q = warp & 3;               // lanes 32 q .. of tensor memory
-    uint32_t nt = 0, nc = 0;
+    uint32_t nt = 0, nc = 0, na = 0;
     constexpr int kTake = GLU ? kChunk / 2 : kChunk;  // rows that this warp stores of a chunk
     const bool up = GLU && q >= 2;
     const int o = GLU ? 32 * (q & 1) : 32 * q;        // first output of this warp in the CTA's
@@ -440,7 +448,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     const bool wide = p.a.n % 8 == 0 && p.a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.a.out) & 15) == 0;
     uint16_t* const stage = reinterpret_cast<uint16_t*>(epi_g) + q * kChunk * 32;
     float* const exch_g = reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + (q & 1) * kChunk * 32;
-    for (int t = 0; tile(t, x); ++t, ++nt) {
+    if (EPI) {
+      // eight warps: two share the lanes and take 16 rows in turn.  (What they release is tensor memory alone: a release of
+      // everything would wait for the last tile's stores.)
+      const int half = (warp - 2) >> 2;
+      float* const mine_g = reinterpret_cast<float*>(epi_g) + (warp - 2) * 16 * 32;
+      for (int t = 0; tile(t, x); ++t) {
+        const int w0 = x.w0 + (int)rank * kTileW + o, width = min(32, p.a.n - w0);
+        if (epi.out_float) {
+          float sum[4][16];
+          for (int ks = 0; ks < ksteps; ks += segment, ++na) {
+            const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21) + 16 * half;
+            wait_pair<try_wait_cluster>(afull(a), (na >> 1) & 1, abort, p.a.status, 4);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (32 * c + 16 * half < x.nr) {
+                uint32_t u[16];
+                tmem_ld16(acc + 32 * c, u);
+                tmem_wait16(u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[c][i] = ks == 0 ? __uint_as_float(u[i]) : sum[c][i] + __uint_as_float(u[i]);
+              }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster_smem(map_leader(aempty(a)));
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (32 * c + 16 * half < x.nr)
+              linear_store(p.a, epi, sum[c], x.r0 + 32 * c + 16 * half, x.nr - (32 * c + 16 * half), w0, width, mine_g, lane);
+          continue;
+        }
+        const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21);
+        wait_pair<try_wait_cluster>(afull(a), (na >> 1) & 1, abort, p.a.status, 4);
+        tc_fence_after();
+        ++na;
+        uint32_t u[16];
+        tmem_ld16(acc + 16 * half, u);  // (rows beyond the tile's are other tiles' or nothing's: not stored)
+        tmem_wait16(u);
+        for (int c = 16 * half; c < x.nr; c += 32) {
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+          const bool more = c + 32 < x.nr;
+          if (more) tmem_ld16(acc + c + 32, u);
+          linear_store(p.a, epi, v, x.r0 + c, x.nr - c, w0, width, mine_g, lane);
+          if (more) tmem_wait16(u);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster_smem(map_leader(aempty(a)));
+      }
+    }
+    for (int t = 0; !EPI && tile(t, x); ++t, ++nt) {
       const uint32_t a = nt & 1;
       const uint32_t acc = tmem + kTileR * a + ((uint32_t)q << 21);
       const int w0 = x.w0 + (int)rank * (GLU ? kTileW / 2 : kTileW) + o, width = min(32, p.a.n - w0);  // (<= 0: nothing to store)
@@ -448,26 +509,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       tc_fence_after();
       uint32_t u[kChunk];
       tmem_ld32(acc, u);
-      if (EPI) {
 #pragma unroll 1
-        for (int c = 0; c < x.nr; c += kChunk) {
-          float v[kChunk];
-          tmem_wait32(u);
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(u[i]);
-          if (c + kChunk >= x.nr) {  // read: the next products may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(map_leader(aempty(a)));
-          } else {
-            tmem_ld32(acc + c + kChunk, u);
-          }
-          linear_store(p.a, epi, v, x.r0 + c, min(kChunk, x.nr - c), w0, width,
-                       reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + q * kChunk * 32, lane);
-        }
-      }
-#pragma unroll 1
-      for (int c = 0; !EPI && c < x.nr; c += kChunk, ++nc) {
+      for (int c = 0; c < x.nr; c += kChunk, ++nc) {
         float v[kTake];
         tmem_wait32(u);
         if (GLU) {
@@ -530,7 +573,7 @@ cudaError_t launch_kind(const ExpertParams& p, const CUtensorMap& tx, const CUte
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(expert_kernel<GLU, EPI>, kExpSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_early(expert_kernel<GLU, EPI>, dim3((unsigned)(p.grid / 2 * 2)), kExpThreads + (p.a.rows ? kGatherThreads : 0), kExpSmem,
+  return launch_early(expert_kernel<GLU, EPI>, dim3((unsigned)(p.grid / 2 * 2)), kExpThreads + (EPI || p.a.rows ? kGatherThreads : 0), kExpSmem,
                       st, p, tx, tx128, tw, tu, epi);
 }
 

@@ -1,0 +1,209 @@
+// Products of few rows:  out = act(x W^T + bias) + residual  where the tiles of mk_experts.cu would leave most SMs idle.
+//
+// A tile is 128 outputs (the M side of the tcgen05 products) by up to 128 rows of x (the N side, in steps of 16); its k is cut
+// into as many slices as there are SMs for, and a cluster has a tile, a CTA a slice.  Reading the weights bounds it (all of them
+// once, from every SM), and below that a chain: launch, the first copies, products, the slices' sums.  The slices meet in shared
+// memory: each CTA owns a part of the tile's rows, gets every other CTA's sums for them, adds them in the order of the slices and
+// writes its part with the epilogue: nothing but results goes to memory, and equal calls give equal bits.
+#include <algorithm>
+
+#include "mk_linear.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kSplitThreads = 192;  // producer, product issue, four epilogue warps
+constexpr int kSplitW = 128;        // outputs of a tile
+constexpr int kSplitK = 64;         // columns of a stage: one 128-byte swizzle span
+constexpr int kSplitStages = 12;
+constexpr int kSplitBytesW = kSplitW * kSplitK * 2;
+
+struct SplitShared {
+  uint32_t tmem;
+  int abort;
+  unsigned long long bars[2 * kSplitStages + 2];
+};
+constexpr int kSplitSmem = 232448 - 1024;  // (SplitShared fits the rest)
+
+__device__ __forceinline__ uint32_t split_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void split_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw) {
+  extern __shared__ uint8_t raw[];
+  __shared__ SplitShared sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = split_rank();
+  const int tile = (int)blockIdx.x / p.slices, wt = tile % p.w_tiles, rt = tile / p.w_tiles;
+  const int w0 = wt * kSplitW, r0 = rt * p.rows, rows = min(p.rows, p.m - r0);
+  const int k0 = (int)((long long)rank * p.chunks / p.slices), k1 = (int)((long long)(rank + 1) * p.chunks / p.slices);
+  const uint32_t stage_bytes = kSplitBytesW + p.box * kSplitK * 2, stages = p.stages;
+  const uint32_t sums = base + p.ring;  // [slice][owned row][kSplitW]
+  float* const sums_g = reinterpret_cast<float*>(raw + (sums - smem_u32(raw)));
+  const int own = (p.box + p.slices - 1) / p.slices;  // rows that a CTA owns of the tile
+  const uint32_t bars = smem_u32(sh.bars), done = bars + 8 * 2 * kSplitStages, got = done + 8;
+  const uint32_t part = own * kSplitW * 4;  // bytes of a slice's sums for a CTA
+  auto full = [&](uint32_t s) { return bars + 8 * s; };
+  auto empty = [&](uint32_t s) { return bars + 8 * (kSplitStages + s); };
+
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    for (uint32_t s = 0; s < stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    mbar_init(got, 1);
+    mbar_expect_tx(got, p.slices * part);
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tx : &tw)) : "memory");
+  if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
+  __syncwarp();
+  tc_fence_before();
+  split_sync();  // all CTAs have started: their shared memory may be written
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = uniform(sh.tmem);
+  volatile int* const abort = &sh.abort;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      Ring at;
+      for (int k = k0; k < k1; ++k, at.advance(stages)) {
+        if (!op_wait1(empty(at.slot), at.phase ^ 1, abort, p.status, 1)) break;
+        const uint32_t st = base + at.slot * stage_bytes;
+        mbar_expect_tx(full(at.slot), stage_bytes);
+        tma_tile(st, &tw, k * kSplitK, w0, full(at.slot));
+        tma_tile(st + kSplitBytesW, &tx, k * kSplitK, r0, full(at.slot));
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one()) {
+      Ring at;
+      bool ok = true;
+      const uint32_t idesc = umma_idesc_bf16(kSplitW, p.box);
+      const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);
+      for (int k = k0; ok && k < k1; ++k, at.advance(stages)) {
+        if (!(ok = op_wait1(full(at.slot), at.phase, abort, p.status, 2))) break;
+        tc_fence_after();
+        const uint64_t d = d0 + at.slot * (stage_bytes / 16);
+#pragma unroll
+        for (int kk = 0; kk < kSplitK / 16; ++kk) umma_bf16(tmem, d + 2 * kk, d + kSplitBytesW / 16 + 2 * kk, idesc, k > k0 || kk > 0);
+        umma_commit(empty(at.slot));
+      }
+      if (ok) umma_commit(done);
+    }
+    __syncwarp();
+  } else {
+    // this slice's sums, in order of the rows, then a copy to each CTA of what it owns: a lane has an output, a column of tensor
+    // memory is a row of x.  (The ring is free: its products have ended.  Stores of single values into the other CTAs took 6 us for
+    // 128 rows by 8 slices.)
+    op_wait(done, 0, abort, p.status, 3);
+    tc_fence_after();
+    const int q = warp & 3;
+    float* const mine = reinterpret_cast<float*>(raw + ((p.slices > 1 ? base : sums) - smem_u32(raw))) + 32 * q + lane;
+    for (int c = 0; c < rows; c += 16) {
+      uint32_t u[16];
+      tmem_ld16(tmem + c + ((uint32_t)q << 21), u);
+      tmem_wait16(u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mine[(c + i) * kSplitW] = __uint_as_float(u[i]);
+    }
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 2 && lane < p.slices && p.slices > 1) {
+      uint32_t to, bar;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(sums + rank * part), "r"(lane));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(got), "r"(lane));
+      asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                   "r"(base + lane * part), "r"(part), "r"(bar)
+                   : "memory");
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (p.slices > 1) op_wait(got, 0, abort, p.status, 4);
+  // a warp takes a row at a time, a lane four outputs
+  const int col = 4 * lane, width = min(kSplitW, p.n - w0), last = min(own, rows - (int)rank * own);
+  float b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = p.epi.bias && col + i < width ? bf16_to_f(op_ld2(p.epi.bias + w0 + col + i)) : 0.f;
+  for (int r = warp; r < last; r += kSplitThreads / 32) {
+    const long long row = r0 + (long long)rank * own + r;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 y = *reinterpret_cast<const float4*>(sums_g + r * kSplitW + col);
+    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+    for (int s = 1; s < p.slices; ++s) {
+      y = *reinterpret_cast<const float4*>(sums_g + (s * own + r) * kSplitW + col);
+      v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += b[i];
+    linear_acts(v, p.epi.act, p.epi.out_float != 0);
+    linear_put(p.epi, p.out, p.out_stride, v, row, w0 + col, width - col);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+  if (*abort) {  // an abandoned run leaves copies and products in flight: give them time to end
+    const uint64_t t0 = gtime();
+    while ((long long)(gtime() - t0) < 10000000ll) {}
+  }
+  split_sync();  // no CTA leaves before its copies have arrived
+}
+
+}  // namespace
+
+// Whether the tiles of 256 outputs by 256 rows, a pair of SMs each, would leave more than half of the pairs without one; if so the
+// split of the work.  (At 128 rows, 4096 -> 2048: 20.5 us with 8 pairs.)
+cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
+  const long long pairs = (long long)((p.n + 255) / 256) * ((p.m + 255) / 256);
+  *fits = p.m <= 1024 && pairs * 4 <= sms;
+  if (!*fits) return cudaSuccess;
+  const int r_tiles = (p.m + 127) / 128;
+  p.rows = ((p.m + r_tiles - 1) / r_tiles + 15) / 16 * 16;
+  p.box = p.rows;
+  p.w_tiles = (p.n + kSplitW - 1) / kSplitW;
+  p.r_tiles = (p.m + p.rows - 1) / p.rows;
+  p.chunks = (p.k + kSplitK - 1) / kSplitK;
+  // as many slices as keep all clusters on the GPU at once (16 tiles in 8 slices: 18 us, 15 clusters of 8 fit; in 6: @@ us)
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(split_kernel, kSplitSmem, done);
+  static std::atomic<int> known[8][64];
+  for (p.slices = std::min(8, p.chunks); e == cudaSuccess && p.slices > 1; --p.slices) {
+    int n = 0;
+    e = active_clusters(split_kernel, p.slices, kSplitThreads, kSplitSmem, known[p.slices - 1], &n);
+    if (p.w_tiles * p.r_tiles <= n) break;
+  }
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.box) p.tmem_cols *= 2;
+  const int own = (p.box + p.slices - 1) / p.slices, sums = p.slices * own * kSplitW * 4, stage = kSplitBytesW + p.box * kSplitK * 2;
+  const int per = (p.chunks + p.slices - 1) / p.slices;
+  p.stages = std::min({kSplitStages, per, (kSplitSmem - 1024 - sums) / stage});
+  p.ring = std::max(p.stages * stage, p.slices > 1 ? sums : 0);  // (the sums leave from where the stages were)
+  p.smem = 1024 + p.ring + sums;
+  return e;
+}
+
+cudaError_t launch_linear_split(const SplitParams& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
+  return launch_clusters(split_kernel, dim3((unsigned)(p.w_tiles * p.r_tiles * p.slices)), p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw);
+}
+
+}  // namespace mk

@@ -18,73 +18,78 @@ __device__ __forceinline__ float linear_act(float y) {
   const float e = EXACT ? expf(-z) : __expf(-z);
   return EXACT ? y / (1.f + e) : __fdividef(y, 1.f + e);
 }
-// ... of all of v + b.  (In registers and unrolled: one value after another, 2001 x 4096 with the tanh form took 88 us.)
+// ... of all of v.  (In registers and unrolled: one value after another through shared memory, 2001 x 4096 with the tanh form
+// took 88 us.)
 template <int ACT, bool EXACT, int N>
-__device__ __forceinline__ void linear_acts(float (&v)[N], float b) {
+__device__ __forceinline__ void linear_acts(float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = linear_act<ACT, EXACT>(v[i] + b);
+  for (int i = 0; i < N; ++i) v[i] = linear_act<ACT, EXACT>(v[i]);
 }
 template <bool EXACT, int N>
-__device__ __forceinline__ void linear_acts(float (&v)[N], float b, int act) {
+__device__ __forceinline__ void linear_acts(float (&v)[N], int act) {
   switch (act) {
-    case MK_ACT_RELU: linear_acts<MK_ACT_RELU, EXACT>(v, b); break;
-    case MK_ACT_SILU: linear_acts<MK_ACT_SILU, EXACT>(v, b); break;
-    case MK_ACT_GELU: linear_acts<MK_ACT_GELU, EXACT>(v, b); break;
-    case MK_ACT_GELU_TANH: linear_acts<MK_ACT_GELU_TANH, EXACT>(v, b); break;
-    default: linear_acts<MK_ACT_NONE, EXACT>(v, b);
+    case MK_ACT_RELU: linear_acts<MK_ACT_RELU, EXACT>(v); break;
+    case MK_ACT_SILU: linear_acts<MK_ACT_SILU, EXACT>(v); break;
+    case MK_ACT_GELU: linear_acts<MK_ACT_GELU, EXACT>(v); break;
+    case MK_ACT_GELU_TANH: linear_acts<MK_ACT_GELU_TANH, EXACT>(v); break;
   }
 }
+template <int N>
+__device__ __forceinline__ void linear_acts(float (&v)[N], int act, bool exact) {
+  if (exact)
+    linear_acts<true>(v, act);
+  else
+    linear_acts<false>(v, act);
+}
 
-// A warp's results v[i] = (row r0 + i, output w0 + lane), i < 32, `rows` and `width` of them real: bias and activation in
-// place, then through `stage` (32 x 32 floats of the warp's own) so that eight lanes write 32 outputs of a row side by side.
-__device__ __forceinline__ void linear_store(const mk_expert_args& a, const LinearEpi& epi, float (&v)[32], long long r0, int rows, int w0,
+// Four outputs of a row from column `col` on, `width` of them real (any number): residual and store.
+__device__ __forceinline__ void linear_put(const LinearEpi& epi, void* out, long long out_stride, const float (&v)[4], long long row, int col,
+                                           int width) {
+  if (width <= 0) return;
+  const uint16_t* const res = epi.residual + row * epi.residual_stride + col;
+  float y[4] = {v[0], v[1], v[2], v[3]};
+  if (epi.vec) {
+    if (epi.residual) {
+      const uint2 u = op_ld8(res);
+      const float2 lo = bf16x2_to_f2(u.x), hi = bf16x2_to_f2(u.y);
+      y[0] += lo.x, y[1] += lo.y, y[2] += hi.x, y[3] += hi.y;
+    }
+    if (epi.out_float)
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + row * out_stride + col) = make_float4(y[0], y[1], y[2], y[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + row * out_stride + col) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < width) {
+      if (epi.residual) y[i] += bf16_to_f(op_ld2(res + i));
+      if (epi.out_float)
+        static_cast<float*>(out)[row * out_stride + col + i] = y[i];
+      else
+        static_cast<uint16_t*>(out)[row * out_stride + col + i] = to_bf16(y[i]);
+    }
+}
+
+// A warp's results v[i] = (row r0 + i, output w0 + lane), i < 16, `rows` and `width` of them real: bias and activation in
+// place, then through `stage` (16 x 32 floats of the warp's own) so that eight lanes write 32 outputs of a row side by side.
+__device__ __forceinline__ void linear_store(const mk_expert_args& a, const LinearEpi& epi, float (&v)[16], long long r0, int rows, int w0,
                                              int width, float* stage, int lane) {
   if (width <= 0) return;
-  const bool wide = epi.out_float != 0;
-  const uint16_t* const res = epi.residual + r0 * epi.residual_stride + w0;
-  const int col = 4 * (lane & 7), row = lane >> 3;
-  uint2 add[8];
-  if (epi.vec && epi.residual) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (row + 4 * j < rows && col < width) add[j] = op_ld8(res + (row + 4 * j) * epi.residual_stride + col);
-  }
   const float b = epi.bias && lane < width ? bf16_to_f(op_ld2(epi.bias + w0 + lane)) : 0.f;
-  if (wide)
-    linear_acts<true>(v, b, epi.act);
-  else
-    linear_acts<false>(v, b, epi.act);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) stage[i * 32 + lane] = v[i];
+  for (int i = 0; i < 16; ++i) v[i] += b;
+  linear_acts(v, epi.act, epi.out_float != 0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = v[i];
   __syncwarp();
-  if (epi.vec) {
-    if (col < width) {
+  const int col = 4 * (lane & 7);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = row + 4 * j;
-        if (r >= rows) break;
-        float4 y = *reinterpret_cast<const float4*>(stage + r * 32 + col);
-        if (epi.residual) {
-          const float2 lo = bf16x2_to_f2(add[j].x), hi = bf16x2_to_f2(add[j].y);
-          y.x += lo.x, y.y += lo.y, y.z += hi.x, y.w += hi.y;
-        }
-        const long long at = (r0 + r) * a.out_stride + w0 + col;
-        if (wide)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-      }
-    }
-  } else if (lane < width) {
-    for (int r = 0; r < rows; ++r) {
-      float y = stage[r * 32 + lane];
-      if (epi.residual) y += bf16_to_f(op_ld2(res + r * epi.residual_stride + lane));
-      const long long at = (r0 + r) * a.out_stride + w0 + lane;
-      if (wide)
-        static_cast<float*>(a.out)[at] = y;
-      else
-        static_cast<uint16_t*>(a.out)[at] = to_bf16(y);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const int r = (lane >> 3) + 4 * j;
+    const float4 y = *reinterpret_cast<const float4*>(stage + r * 32 + col);
+    const float z[4] = {y.x, y.y, y.z, y.w};
+    if (r < rows) linear_put(epi, a.out, a.out_stride, z, r0 + r, w0 + col, width - col);
   }
   __syncwarp();
 }

@@ -427,10 +427,30 @@ int mk_linear(const mk_linear_args* a, void* stream) {
   epi.vec = a->n % 4 == 0 && a->out_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a->out) % (4 * size) == 0 &&
             (!a->residual || (a->residual_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a->residual) % 8 == 0));
   int r = num_sms(&p.grid);
+  if (!r) r = set_record(p.a.status);
   if (r) return r;
   CUtensorMap tx, tx128, tw;
   cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->m};
   cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
+  SplitParams s{};
+  s.epi = epi;
+  s.out = a->out;
+  s.out_stride = a->out_stride;
+  s.status = p.a.status;
+  s.m = a->m;
+  s.n = a->n;
+  s.k = a->k;
+  bool few = false;
+  r = cuda_error(split_shape(s, p.grid, &few), "clusters");
+  if (r) return r;
+  if (few) {
+    const cuuint32_t sxb[2] = {64, (cuuint32_t)s.box}, swb[2] = {64, 128};
+    const cuuint64_t swd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n}, sws[1] = {(cuuint64_t)a->k * 2};
+    r = encode(&tx, a->x, 2, xd, xs, sxb, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!r) r = encode(&tw, a->w, 2, swd, sws, swb, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (r) return r;
+    return cuda_error(launch_linear_split(s, tx, tw, static_cast<cudaStream_t>(stream)), "linear launch");
+  }
   cuuint32_t xb[2] = {64, 32};
   cuuint32_t xb128[2] = {64, 128};
   r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -439,7 +459,6 @@ int mk_linear(const mk_linear_args* a, void* stream) {
   cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
   cuuint32_t wb[3] = {64, 128, 1};
   if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!r) r = set_record(p.a.status);
   if (r) return r;
   return cuda_error(launch_linear_pairs(p, epi, tx, tx128, tw, static_cast<cudaStream_t>(stream)), "linear launch");
 }

@@ -77,6 +77,9 @@ __device__ __forceinline__ void op_tma_4d(uint32_t dst, const CUtensorMap* tm, i
 __device__ __forceinline__ void op_cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void op_cp8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 // arrive on the barrier (one of its expected arrivals) once this thread's copies so far have landed
 __device__ __forceinline__ void op_cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");

@@ -41,6 +41,30 @@ cudaError_t allow_wide_clusters(K* kernel, std::atomic<unsigned long long>& done
   return e;
 }
 
+// Clusters of `ctas` blocks that can run at once, one block an SM (`known`: by device, 0: not asked for yet).  Fewer than the SMs
+// divided by their size: a cluster lies within a group of SMs that share a switch.
+template <class K>
+cudaError_t active_clusters(K* kernel, int ctas, int threads, size_t smem, std::atomic<int> (&known)[64], int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+  if (*n > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*n, std::memory_order_release);
+  return e;
+}
+
 // Launch `kernel` so that its prologue may run beside the end of the kernel before it on the
 // stream (griddepcontrol.wait in the kernel is where it waits for that one).
 template <class... P, class... A>
@@ -147,6 +171,19 @@ struct LinearEpi {
   int act, out_float;
   int vec;                   // residual and out can be read and written four values at a time
 };
+// The same for few rows (mk_linear.cu).
+struct SplitParams {
+  LinearEpi epi;
+  void* out;
+  int64_t out_stride;
+  int32_t* status;
+  int m, n, k;
+  // from split_shape: row tiles of `rows` (a multiple of 16, also the copies' height), outputs' tiles, columns' chunks of 64 and how
+  // many slices they are cut into
+  int rows, box, w_tiles, r_tiles, chunks, slices, stages, tmem_cols, ring, smem;
+};
+cudaError_t split_shape(SplitParams& p, int sms, bool* fits);
+cudaError_t launch_linear_split(const SplitParams& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st);
 cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, const CUtensorMap& tx, const CUtensorMap& tx128,
                                 const CUtensorMap& tw, cudaStream_t st);
 

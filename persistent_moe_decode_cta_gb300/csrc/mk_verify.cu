@@ -22,9 +22,7 @@ constexpr int kWalkThreads = 512, kWalkWarps = kWalkThreads / 32;
 constexpr int kWalkCtas = 16;              // of a cluster at most
 constexpr int kFixed = 44;                 // fraction bits of an exponential
 constexpr int kBlock = 128;                // elements that a warp takes at a time: four a lane
-constexpr int kWarpBlocks = 12;            // ... of a row at most: in registers while they are under way
 constexpr int kCtaBlocks = 180;            // blocks whose exponentials fit a CTA's shared memory
-static_assert(kCtaBlocks <= kWarpBlocks * kWalkWarps, "");
 
 __device__ __forceinline__ float load_logit(const void* p, long long at, bool f32) {
   return f32 ? op_ldf(static_cast<const float*>(p) + at) : bf16_to_f(op_ld2(static_cast<const uint16_t*>(p) + at));
@@ -71,56 +69,90 @@ __device__ __forceinline__ float temperature(const mk_verify_args& a, int b) { r
 __device__ __forceinline__ int node_count(const mk_verify_args& a, int b) { return a.counts ? op_ld(a.counts + b) : a.n_nodes; }
 
 // -------------------------------------------------------------------------------------------- rows
+// Largest and sum of exponentials of two sets of logits, as those of their union.
+struct Peak {
+  float top, sum;
+  int arg;
+  __device__ __forceinline__ void merge(float t, float s, int a, float beta) {
+    const float all = fmaxf(top, t);
+    const float from = all == -INFINITY ? 0.f : all;  // (two empty sets)
+    sum = sum * ex2((top - from) * beta) + s * ex2((t - from) * beta);
+    arg = t > top ? a : t == top ? min(a, arg) : arg;
+    top = all;
+  }
+};
+
 // One block per piece of a row: {largest, sum of exp((l - largest) / T), index of the largest (the lowest)}.  The piece stays in
-// registers between the two.  HBM bounds it.
-template <int ITER>
+// registers between the two; threads meet once.  HBM bounds it.
+template <bool F32, int ITER>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ float s_max[kRowThreads / 32];
-  __shared__ float s_sum[kRowThreads / 32];
-  __shared__ int s_arg[kRowThreads / 32];
+  constexpr int kVec = F32 ? 4 : 8;  // elements of 16 bytes
+  __shared__ Peak s_peak[kRowThreads / 32];
   const int piece = blockIdx.x, node = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   if (node >= node_count(p.a, b)) return;
-  const bool f32 = p.a.logits_float != 0;
   const void* row = logit_row(p.a, b, node);
-  const bool wide = is_wide(row, f32);
   const float beta = Heat(temperature(p.a, b)).hi;
-  const int base = piece * (kRowThreads * 4 * ITER) + 4 * threadIdx.x;
-  float4 v[ITER];
+  const int base = piece * (kRowThreads * kVec * ITER) + kVec * threadIdx.x, n = p.a.vocab;
+  float x[ITER][kVec];
+  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+    uint4 u[ITER];
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) v[i] = load4(row, base + i * kRowThreads * 4, p.a.vocab, f32, wide, -INFINITY);
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < ITER; ++i) top = fmaxf(fmaxf(fmaxf(top, v[i].x), fmaxf(v[i].y, v[i].z)), v[i].w);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) top = fmaxf(top, s_max[i]);
-  const float from = top == -INFINITY ? 0.f : top;  // (a piece of nothing: sums of zeros)
-  float sum = 0.f;
-  int arg = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sum += ex2((x[j] - from) * beta);
-      if (x[j] == top) arg = min(arg, base + i * kRowThreads * 4 + j);
+    for (int i = 0; i < ITER; ++i) {
+      const int at = base + i * kRowThreads * kVec;
+      if (at + kVec <= n) u[i] = op_ld16(static_cast<const uint8_t*>(row) + (long long)at * (F32 ? 4 : 2));
     }
-  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    arg = min(arg, __shfl_xor_sync(0xffffffffu, arg, o));
+    for (int i = 0; i < ITER; ++i) {
+      const int at = base + i * kRowThreads * kVec;
+      if (at + kVec <= n) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (F32) {
+            x[i][j] = __uint_as_float(w[j]);
+          } else {
+            const float2 f = bf16x2_to_f2(w[j]);
+            x[i][2 * j % kVec] = f.x, x[i][(2 * j + 1) % kVec] = f.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[i][j] = at + j < n ? load_logit(row, at + j, F32) : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const int at = base + i * kRowThreads * kVec + j;
+        x[i][j] = at < n ? load_logit(row, at, F32) : -INFINITY;
+      }
   }
-  if (lane == 0) s_sum[warp] = sum, s_arg[warp] = arg;
+  Peak mine{-INFINITY, 0.f, 0x7fffffff};
+#pragma unroll
+  for (int i = 0; i < ITER; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) mine.top = fmaxf(mine.top, x[i][j]);
+  const float from = mine.top == -INFINITY ? 0.f : mine.top;
+#pragma unroll
+  for (int i = ITER - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = kVec - 1; j >= 0; --j) {
+      mine.sum += ex2((x[i][j] - from) * beta);
+      if (x[i][j] == mine.top) mine.arg = base + i * kRowThreads * kVec + j;
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    mine.merge(__shfl_xor_sync(0xffffffffu, mine.top, o), __shfl_xor_sync(0xffffffffu, mine.sum, o), __shfl_xor_sync(0xffffffffu, mine.arg, o), beta);
+  if (lane == 0) s_peak[warp] = mine;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kRowThreads / 32; ++i) sum += s_sum[i], arg = min(arg, s_arg[i]);
-    p.parts[((long long)b * p.a.n_nodes + node) * p.pieces + piece] = make_float4(top, sum, __int_as_float(arg), 0.f);
+#pragma unroll
+    for (int i = 1; i < kRowThreads / 32; ++i) mine.merge(s_peak[i].top, s_peak[i].sum, s_peak[i].arg, beta);
+    p.parts[((long long)b * p.a.n_nodes + node) * p.pieces + piece] = make_float4(mine.top, mine.sum, __int_as_float(mine.arg), 0.f);
   }
 }
 
@@ -303,34 +335,19 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   // the pieces of every row
   for (int i = warp; i < count; i += kWalkWarps) {
     const float4* part = p.parts + ((long long)b * a.n_nodes + i) * p.pieces;
-    float top = -INFINITY, sum = 0.f;
-    int arg = 0x7fffffff;
+    Peak mine{-INFINITY, 0.f, 0x7fffffff};
     for (int j = lane; j < p.pieces; j += 32) {
       const uint4 u = op_ld16(part + j);
-      const float m = __uint_as_float(u.x), s = __uint_as_float(u.y);
-      if (m > top) {
-        sum *= ex2((top - m) * heat.hi);
-        top = m;
-        arg = (int)u.z;
-      }
-      sum += m == -INFINITY ? s : s * ex2((m - top) * heat.hi);
-    }
-    float all = top;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    if (top != all) {
-      sum = top == -INFINITY ? sum : sum * ex2((top - all) * heat.hi);
-      arg = 0x7fffffff;
+      mine.merge(__uint_as_float(u.x), __uint_as_float(u.y), (int)u.z, heat.hi);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      arg = min(arg, __shfl_xor_sync(0xffffffffu, arg, o));
-    }
+    for (int o = 16; o; o >>= 1)
+      mine.merge(__shfl_xor_sync(0xffffffffu, mine.top, o), __shfl_xor_sync(0xffffffffu, mine.sum, o), __shfl_xor_sync(0xffffffffu, mine.arg, o),
+                 heat.hi);
     if (lane == 0) {
-      sh.node[i].top = all;
-      sh.node[i].sum = sum;
-      sh.node[i].arg = arg;
+      sh.node[i].top = mine.top;
+      sh.node[i].sum = mine.sum;
+      sh.node[i].arg = mine.arg;
     }
   }
   __syncthreads();
@@ -389,7 +406,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   // a piece a CTA, a part of it a warp, in whole blocks
   const int blocks = (a.vocab + kBlock - 1) / kBlock, mine = (blocks + (int)ctas - 1) / (int)ctas, per = (mine + kWalkWarps - 1) / kWalkWarps;
   const int base = (int)rank * mine * kBlock;                                       // first element of the CTA
-  const int first = min(warp * per, mine), n_blocks = min(per, mine - first);       // blocks of this warp (kWarpBlocks at most)
+  const int first = min(warp * per, mine), n_blocks = min(per, mine - first);       // blocks of this warp
   const int from = first * kBlock + 4 * lane;                                       // first element of this lane in the piece
   for (int i = tid; i < kPowers; i += kWalkThreads) sh.power[i] = powers.v[i];
   __syncthreads();
@@ -418,7 +435,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   // of the row at `at`: A and W, and what this warp has of W
   unsigned long long A = 0, W = 0, warp_sum = 0;
   bool loaded = false, stuck = false;
-  float4 qs[kWarpBlocks];
   // the first thread's: the child to test (-2: at a new node), and before the row is loaded its sum without the tokens that are gone
   int child = -2, length = 0, n_gone = 0;
   bool whole = true;  // no child rejected yet
@@ -495,35 +511,59 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     at = row_at = asked;
     const bool draft = a.draft_probs != nullptr;
     const float* const drow = draft ? a.draft_probs + b * a.draft_stride[0] + at * a.draft_stride[1] : nullptr;
+    const bool qwide = is_wide(drow, true);
     // ------------------------------------------------------------ the row's exponentials into shared memory, and their sum
     if (!loaded) {
       const void* const row = logit_row(a, b, at);
-      const bool wide = is_wide(row, f32), qwide = is_wide(drow, true);
+      const bool wide = is_wide(row, f32);
       ex.top = sh.node[at].top;
-      float4 v[kWarpBlocks];
-#pragma unroll
-      for (int k = 0; k < kWarpBlocks; ++k)
-        if (k < n_blocks) v[k] = load4(row, base + from + k * kBlock, a.vocab, f32, wide, -INFINITY);
-      unsigned long long sum = 0;
-#pragma unroll
-      for (int k = 0; k < kWarpBlocks; ++k)
-        if (k < n_blocks) {
-          unsigned long long y[4] = {ex(v[k].x), ex(v[k].y), ex(v[k].z), ex(v[k].w)};
-          for (int g = 0; g < gone; ++g) {
-            const int d = sh.gone[g] - (base + from + k * kBlock);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (d == i) y[i] = 0;
+      // (all copies first, each into the first half of what the lane turns it into: lanes wait for their own only.  Rolled loops:
+      // unrolled, the code of a pass that runs once is fetched for longer than it runs.)
+      if (wide) {
+        const int size = f32 ? 16 : 8;
+        for (int k = 0; k < n_blocks; ++k) {
+          const int j = base + from + k * kBlock;
+          const uint32_t to = smem_u32(e + from + k * kBlock);
+          const void* const src = static_cast<const uint8_t*>(row) + (long long)j * (size / 4);
+          if (j + 4 <= a.vocab) {
+            if (f32)
+              op_cp16(to, src, 16);
+            else
+              op_cp8(to, src);
           }
-          ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + from + k * kBlock);
-          to[0] = make_ulonglong2(y[0], y[1]);
-          to[1] = make_ulonglong2(y[2], y[3]);
-          sum += y[0] + y[1] + y[2] + y[3];
         }
-      if (step == kCut) {  // (on their way while the sums meet)
+      }
+      if (draft && step == kCut && qwide)  // (into L2)
+        for (int k = 0; k < n_blocks; ++k) {
+          const int j = base + from + k * kBlock;
+          if (lane % 8 == 0 && j < a.vocab) asm volatile("prefetch.global.L2 [%0];" ::"l"(drow + j) : "memory");
+        }
+      op_cp_wait_all();
+      unsigned long long sum = 0;
+#pragma unroll 1
+      for (int k = 0; k < n_blocks; ++k) {
+        const int j = base + from + k * kBlock;
+        ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + from + k * kBlock);
+        float4 v;
+        if (wide && j + 4 <= a.vocab) {
+          v = *reinterpret_cast<const float4*>(to);
+          if (!f32) {
+            const float2 lo = bf16x2_to_f2(__float_as_uint(v.x)), hi = bf16x2_to_f2(__float_as_uint(v.y));
+            v = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+        } else {
+          v = load4(row, j, a.vocab, f32, false, -INFINITY);
+        }
+        unsigned long long y[4] = {ex(v.x), ex(v.y), ex(v.z), ex(v.w)};
+        for (int g = 0; g < gone; ++g) {
+          const int d = sh.gone[g] - j;
 #pragma unroll
-        for (int k = 0; k < kWarpBlocks; ++k)
-          if (k < n_blocks) qs[k] = load4(drow, base + from + k * kBlock, a.vocab, true, qwide, 0.f);
+          for (int i = 0; i < 4; ++i)
+            if (d == i) y[i] = 0;
+        }
+        to[0] = make_ulonglong2(y[0], y[1]);
+        to[1] = make_ulonglong2(y[2], y[3]);
+        sum += y[0] + y[1] + y[2] + y[3];
       }
       warp_sum = warp_total(sum);
       A = 0;
@@ -535,13 +575,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
       if (!stuck) {
         const Cut cut(A + W);
         unsigned long long sum = 0;
+        for (int k = 0; k < n_blocks; k += 4) {
+          float4 qs[4];
 #pragma unroll
-        for (int k = 0; k < kWarpBlocks; ++k)
-          if (k < n_blocks) {
-            const ulonglong2* const y = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
-            const ulonglong2 lo = y[0], hi = y[1];
-            sum += cut(lo.x, qs[k].x) + cut(lo.y, qs[k].y) + cut(hi.x, qs[k].z) + cut(hi.y, qs[k].w);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (k + i < n_blocks) qs[i] = load4(drow, base + from + (k + i) * kBlock, a.vocab, true, qwide, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (k + i < n_blocks) {
+              const ulonglong2* const y = reinterpret_cast<const ulonglong2*>(e + from + (k + i) * kBlock);
+              const ulonglong2 lo = y[0], hi = y[1];
+              sum += cut(lo.x, qs[i].x) + cut(lo.y, qs[i].y) + cut(hi.x, qs[i].z) + cut(hi.y, qs[i].w);
+            }
+        }
         sum = warp_total(sum);
         const unsigned long long now = exchange(sh, sum, &parity);
         if (now) {
@@ -564,13 +610,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     if (goal >= sum && goal < sum + warp_sum) {  // this warp's
       const Cut cut(A);
       bool found = false;
+      for (int k0 = 0; k0 < n_blocks && !found; k0 += 4) {
+        float4 qs[4];
+        if (A) {
 #pragma unroll
-      for (int k = 0; k < kWarpBlocks; ++k)
-        if (k < n_blocks && !found) {
+          for (int i = 0; i < 4; ++i)
+            if (k0 + i < n_blocks) qs[i] = load4(drow, base + from + (k0 + i) * kBlock, a.vocab, true, qwide, 0.f);
+        }
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int k = k0 + k4;
+          if (k >= n_blocks || found) break;
           const ulonglong2* const at4 = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
           const ulonglong2 lo = at4[0], hi = at4[1];
           unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
-          if (A) y[0] = cut(y[0], qs[k].x), y[1] = cut(y[1], qs[k].y), y[2] = cut(y[2], qs[k].z), y[3] = cut(y[3], qs[k].w);
+          if (A) y[0] = cut(y[0], qs[k4].x), y[1] = cut(y[1], qs[k4].y), y[2] = cut(y[2], qs[k4].z), y[3] = cut(y[3], qs[k4].w);
           const unsigned long long own = y[0] + y[1] + y[2] + y[3];
           unsigned long long upto = own;
 #pragma unroll
@@ -593,6 +647,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
             sum += __shfl_sync(0xffffffffu, upto, 31);
           }
         }
+      }
     }
     if (tid == 0) sh.next = -2;  // written
     break;
@@ -608,15 +663,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   walk_sync();  // no CTA leaves while another may write to it or read its nodes
 }
 
-// Pieces of a row: 2048 to 8192 elements, the more the fewer rows there are
+// Loads of 16 bytes a thread: four, or eight where that leaves enough blocks to fill the GPU
 int row_iter(const mk_verify_args& a) {
-  const long long rows = (long long)a.batch * a.n_nodes;
-  for (int iter = 8; iter > 2; iter /= 2)
-    if (rows * ((a.vocab + kRowThreads * 4 * iter - 1) / (kRowThreads * 4 * iter)) >= 600) return iter;
-  return 2;
+  const int piece = kRowThreads * (a.logits_float ? 4 : 8) * 8;
+  return (long long)a.batch * a.n_nodes * ((a.vocab + piece - 1) / piece) >= 2000 ? 8 : 4;
 }
 int row_pieces(const mk_verify_args& a) {
-  const int piece = kRowThreads * 4 * row_iter(a);
+  const int piece = kRowThreads * (a.logits_float ? 4 : 8) * row_iter(a);
   return (a.vocab + piece - 1) / piece;
 }
 
@@ -630,19 +683,21 @@ cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
   p.parts = static_cast<float4*>(p.a.workspace);
   p.pieces = row_pieces(p.a);
   const dim3 grid((unsigned)p.pieces, (unsigned)p.a.n_nodes, (unsigned)p.a.batch);
-  const int iter = row_iter(p.a);
-  cudaError_t e = iter == 8   ? launch_early(row_kernel<8>, grid, kRowThreads, 0, st, p)
-                  : iter == 4 ? launch_early(row_kernel<4>, grid, kRowThreads, 0, st, p)
-                              : launch_early(row_kernel<2>, grid, kRowThreads, 0, st, p);
-  if (e != cudaSuccess) return e;
-  // clusters of 16 while every sequence's fits the GPU at once, and where a piece of 8 would not fit shared memory
-  const int blocks = (p.a.vocab + kBlock - 1) / kBlock;
-  const int ctas = blocks > 8 * kCtaBlocks || (blocks > 256 && (long long)p.a.batch * kWalkCtas <= p.grid) ? kWalkCtas : 8;
-  const size_t smem = (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
+  const bool f32 = p.a.logits_float != 0, eight = row_iter(p.a) == 8;
+  cudaError_t e = f32 ? (eight ? launch_early(row_kernel<true, 8>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<true, 4>, grid, kRowThreads, 0, st, p))
+                      : (eight ? launch_early(row_kernel<false, 8>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<false, 4>, grid, kRowThreads, 0, st, p));
   static std::atomic<unsigned long long> done{0}, done16{0};
-  e = allow_smem(walk_kernel, kCtaBlocks * kBlock * 8, done);
-  if (e == cudaSuccess && ctas > 8) e = allow_wide_clusters(walk_kernel, done16);
+  static std::atomic<int> known[64];
+  constexpr int kSmem = kCtaBlocks * kBlock * 8;
+  if (e == cudaSuccess) e = allow_smem(walk_kernel, kSmem, done);
+  if (e == cudaSuccess) e = allow_wide_clusters(walk_kernel, done16);
+  // clusters of 16 while all of them fit the GPU at once, and where a piece of 8 would not fit shared memory
+  const int blocks = (p.a.vocab + kBlock - 1) / kBlock;
+  int ctas = 8, wide = 0;
+  if (e == cudaSuccess && blocks > 256) e = active_clusters(walk_kernel, kWalkCtas, kWalkThreads, kSmem, known, &wide);
   if (e != cudaSuccess) return e;
+  if (blocks > 8 * kCtaBlocks || p.a.batch <= wide) ctas = kWalkCtas;
+  const size_t smem = (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
   return launch_clusters(walk_kernel, dim3((unsigned)(p.a.batch * ctas)), ctas, kWalkThreads, smem, st, p);
 }
 

@@ -5,11 +5,12 @@ import pytest
 
 import test_ops_sources as T
 
-NAMES = ["mk_moe.cu", "mk_verify.cu"]
+NAMES = ["mk_moe.cu", "mk_verify.cu", "mk_linear.cu"]
 
 
 def test_the_kernels_and_readers_are_found():
-    assert [[k for k, _ in T.kernels(f)] for f in NAMES] == [["router_kernel", "layer_kernel"], ["row_kernel", "walk_kernel"]]
+    assert [[k for k, _ in T.kernels(f)] for f in NAMES] == [["router_kernel", "layer_kernel"], ["row_kernel", "walk_kernel"],
+                                                          ["split_kernel"]]
     assert {"gather_nodes"} <= readers("mk_verify.cu")
 
 
@@ -18,7 +19,7 @@ def readers(name):
     text = T.source(name)
     bodies = {m.group(1): T.body(text, m.end() - 1)
               for m in re.finditer(r"__device__[^;{}()]*?\b(\w+)\s*\((?:[^()]|\([^()]*\))*\)\s*(?:const\s*)?\{", text)}
-    found = {"op_ld", "op_ld2", "op_ld8", "op_ldf", "op_ld16", "op_ld16_once", "op_cp16", "cp16", "op_error"}
+    found = {"op_ld", "op_ld2", "op_ld8", "op_ldf", "op_ld16", "op_ld16_once", "op_cp16", "op_cp8", "cp16", "op_error"}
     while True:
         more = {f for f, b in bodies.items() if f not in found and any(re.search(rf"\b{g}\s*\(", b) for g in found)}
         if not more:
