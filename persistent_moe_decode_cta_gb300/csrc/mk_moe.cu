@@ -6,7 +6,7 @@
 //
 // With few tokens every selected expert's weights are read for a handful of rows: HBM bounds it, and the products only have to
 // keep up.  Every warp has a ring of its own that it fills itself, with tensor-map copies of 8 rows by 64 columns (no barrier
-// between warps), and multiplies with m16n8k16: with 8 rows an expert a tcgen05 tile would be empty but for a sixteenth.  The
+// between warps; 128 columns of 16 rows a step), and multiplies with m16n8k16: with 8 rows an expert a tcgen05 tile would be empty but for a sixteenth.  The
 // warps split k; their parts of a result meet in shared memory and are added in the order of the warps.
 //
 // First product: a unit is 8 outputs of an expert (8 gate and 8 up rows of weights: one 16-row tile) for up to 8 NT of its
@@ -24,7 +24,7 @@ namespace {
 // ------------------------------------------------------------------------------------------ router
 // A cluster of 8 CTAs has TT tokens and an eighth of the experts a CTA.  A selection can hang on the last bits of two scores, so
 // these are sums of exact products (two bf16 factors fit fp32) with the rounding errors of the additions carried along.
-constexpr int kRouterCtas = 8, kRouterThreads = 256, kRouterWarps = kRouterThreads / 32;
+constexpr int kRouterCtas = 8, kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
 
 // (hi, lo) += v, the error of hi + v to lo; two sums at once
 __device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t v) {
@@ -54,6 +54,7 @@ __device__ __forceinline__ unsigned long long score_key(double d) {
 template <int TT>
 __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThreads) router_kernel(const __grid_constant__ MoeParams p) {
   __shared__ double s_score[kOpMaxExperts];  // of the token that this CTA selects for
+  extern __shared__ __align__(16) uint8_t raw_x[];  // the tokens' rows
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -63,29 +64,48 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && tid < 4) p.sync[tid] = 0;
-  const uint16_t* x[TT];
+  uint4* const x = reinterpret_cast<uint4*>(raw_x);
+  const int vecs = d / 8;
+  // (the first weights are on their way while the tokens' rows come in)
+  constexpr int U = TT <= 2 ? 8 : 4;
+  uint4 u[U];
+  const uint16_t* w = static_cast<const uint16_t*>(p.a.router) + (long long)min(e0 + warp, E - 1) * d;
+  auto fetch = [&](int v) {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) x[j] = static_cast<const uint16_t*>(p.a.x) + min(t0 + j, p.a.n_tokens - 1) * p.a.x_stride;
+    for (int i = 0; i < U; ++i)
+      if (v + 32 * i < vecs) u[i] = op_ld16(w + 8 * (v + 32 * i));
+  };
+  fetch(lane);
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const uint16_t* const row = static_cast<const uint16_t*>(p.a.x) + min(t0 + j, p.a.n_tokens - 1) * p.a.x_stride;
+    for (int v = tid; v < vecs; v += kRouterThreads) op_cp16(smem_u32(x + j * vecs + v), row + 8 * v, 16);
+  }
+  op_cp_wait_all();
+  __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   for (int e = e0 + warp; e < e1; e += kRouterWarps) {
-    const uint16_t* const w = static_cast<const uint16_t*>(p.a.router) + (long long)e * d;
     uint64_t hi[TT], lo[TT];
 #pragma unroll
     for (int j = 0; j < TT; ++j) hi[j] = lo[j] = 0;
-#pragma unroll(TT <= 2 ? 4 : 2)
-    for (int k = 8 * lane; k < d; k += 256) {
-      const uint4 u = op_ld16(w + k);
-      uint4 v[TT];
-#pragma unroll
-      for (int j = 0; j < TT; ++j) v[j] = op_ld16(x[j] + k);
-      const uint64_t w4[4] = {pair_of(u.x), pair_of(u.y), pair_of(u.z), pair_of(u.w)};
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        add_exact2(hi[j], lo[j], mul2(w4[0], pair_of(v[j].x)));
-        add_exact2(hi[j], lo[j], mul2(w4[1], pair_of(v[j].y)));
-        add_exact2(hi[j], lo[j], mul2(w4[2], pair_of(v[j].z)));
-        add_exact2(hi[j], lo[j], mul2(w4[3], pair_of(v[j].w)));
+    for (int v = lane; v < vecs; v += 32 * U) {
+      if (e != e0 + warp || v != lane) {
+        if (v == lane) w = static_cast<const uint16_t*>(p.a.router) + (long long)e * d;
+        fetch(v);
       }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (v + 32 * i < vecs) {
+          const uint64_t w4[4] = {pair_of(u[i].x), pair_of(u[i].y), pair_of(u[i].z), pair_of(u[i].w)};
+#pragma unroll
+          for (int j = 0; j < TT; ++j) {
+            const uint4 y = x[j * vecs + v + 32 * i];
+            add_exact2(hi[j], lo[j], mul2(w4[0], pair_of(y.x)));
+            add_exact2(hi[j], lo[j], mul2(w4[1], pair_of(y.y)));
+            add_exact2(hi[j], lo[j], mul2(w4[2], pair_of(y.z)));
+            add_exact2(hi[j], lo[j], mul2(w4[3], pair_of(y.w)));
+          }
+        }
     }
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
@@ -150,8 +170,9 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
 
 // ------------------------------------------------------------------------------------------- layer
 constexpr int kLayerThreads = 256, kLayerWarps = kLayerThreads / 32;
-constexpr int kStepK = 64;       // columns of a step: one 128-byte swizzle span
-constexpr int kTileBytes = 2048; // weights of a step: 16 rows
+constexpr int kSpan = 64;        // columns of a copy: one 128-byte swizzle span
+constexpr int kStepK = 2 * kSpan;
+constexpr int kTileBytes = 4096; // weights of a step: 16 rows, two copies of 2 KB
 constexpr int kMaxSlots = 10;    // of a warp's ring
 constexpr int kAccPitch = 20;
 
@@ -159,6 +180,7 @@ struct LayerShared {
   int off[kOpMaxExperts + 1];       // first row of every expert in the list
   int act[kOpMaxExperts];           // experts that have rows
   int tile_pre[kOpMaxExperts + 1];  // row tiles before each of them
+  int2 rows[kOpMaxExperts];         // first row of an active expert's outputs in w_down, first row of its tiles in h
   int n_act, run, next, abort;
   int warp_rows[8], warp_tiles[8], warp_act[8];
   unsigned long long bars[kLayerWarps][kMaxSlots];
@@ -169,7 +191,7 @@ struct LayerSmem {
   int warp_bytes, red, list, weight, acc, total;
   __host__ __device__ LayerSmem(int nt, bool direct, int slots, int d, int tokens, int top_k) {
     const int entries = tokens * top_k, mine = ((d + kStepK - 1) / kStepK + kLayerWarps - 1) / kLayerWarps;
-    warp_bytes = slots * kTileBytes + (slots > mine ? slots : mine) * nt * 1024;  // weights, rows
+    warp_bytes = slots * kTileBytes + (slots > mine ? slots : mine) * nt * 2048;  // weights, rows
     red = kLayerWarps * warp_bytes;
     list = red + 2 * kLayerWarps * nt * 32 * 16;  // (the token masks lie here before the first results)
     weight = list + (entries * 2 + 15) / 16 * 16;
@@ -266,6 +288,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   }
   __syncthreads();
   const int A = (int)uniform(sh.n_act), groups = f / 8;
+  if (tid < A) sh.rows[tid] = make_int2(sh.act[tid] * d, DIRECT ? tid * 8 : sh.off[sh.act[tid]]);
   for (int i = tid; i < entries; i += kLayerThreads) {
     const int t = i / K, e = i == tid ? my_id : op_ld(p.ids + i);
     const float c = i == tid ? my_weight : op_ldf(p.weights + i);
@@ -362,13 +385,15 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   };
   Down id = down_begin(), ib = id;  // weights, rows
   int ahead = 0;                    // steps of the second product whose weights are under way and whose rows are not
-  const uint32_t down_bytes = p.width * 128 + NT * 1024;
+  const uint32_t down_bytes = 2 * (p.width * 128 + NT * 1024);
 
   auto issue_weights = [&]() {
     if (elect_one()) {
       const uint32_t bar = bars + 8 * put, dst = tiles_at + put * kTileBytes;
+      const int row = sh.rows[id.a].x + id.block * p.width;
       mbar_expect_tx(bar, down_bytes);
-      tma_box(dst, &tdown, id.s * kStepK, sh.act[id.a] * d + id.block * p.width, bar);
+      tma_box(dst, &tdown, id.s * kStepK, row, bar);
+      tma_box(dst + kTileBytes / 2, &tdown, id.s * kStepK + kSpan, row, bar);
     }
     __syncwarp();
     put = put + 1 == (uint32_t)S ? 0 : put + 1;
@@ -376,9 +401,12 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     down_fit(id);
   };
   auto issue_rows = [&](uint32_t slot) {
-    if (elect_one())
-      tma_box(rows_at + slot * NT * 1024, &th, ib.s * kStepK, DIRECT ? ib.a * 8 : sh.off[sh.act[ib.a]] + (ib.tile - sh.tile_pre[ib.a]) * NT * 8,
-              bars + 8 * slot);
+    if (elect_one()) {
+      const int row = sh.rows[ib.a].y + (DIRECT ? 0 : (ib.tile - sh.tile_pre[ib.a]) * NT * 8);
+      const uint32_t dst = rows_at + slot * NT * 2048, bar = bars + 8 * slot;
+      tma_box(dst, &th, ib.s * kStepK, row, bar);
+      tma_box(dst + NT * 1024, &th, ib.s * kStepK + kSpan, row, bar);
+    }
     __syncwarp();
     ib.s += kLayerWarps;
     down_fit(ib);
@@ -393,6 +421,8 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
         mbar_expect_tx(bar, kTileBytes);
         tma_box(dst, &tgate, istep * kStepK, irow, bar);
         tma_box(dst + 1024, &tup, istep * kStepK, irow, bar);
+        tma_box(dst + kTileBytes / 2, &tgate, istep * kStepK + kSpan, irow, bar);
+        tma_box(dst + kTileBytes / 2 + 1024, &tup, istep * kStepK + kSpan, irow, bar);
       }
       __syncwarp();
       put = put + 1 == (uint32_t)S ? 0 : put + 1;
@@ -408,22 +438,25 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     }
   };
 
-  float sum[NT][4];
+  // (several sums a tile, so that the products need not wait for one another)
+  constexpr int kSets = NT == 1 ? 4 : 2;
+  float sum[kSets][NT][4];
   auto multiply = [&](uint32_t rows, int nt) {
     op_wait(bars + 8 * get.slot, get.phase, &sh.abort, p.a.status, 2);
     const uint32_t tile = tiles_at + get.slot * kTileBytes + a_at;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < 4; ++half) {
       uint32_t a[8];
-      ldsm_x4(tile + (a_x ^ (half << 6)), a[0], a[1], a[2], a[3]);
-      ldsm_x4(tile + (a_x ^ (half << 6 | 32)), a[4], a[5], a[6], a[7]);
+      const uint32_t t = tile + (half >> 1) * (kTileBytes / 2), x = a_x ^ ((half & 1) << 6);
+      ldsm_x4(t + x, a[0], a[1], a[2], a[3]);
+      ldsm_x4(t + (x ^ 32), a[4], a[5], a[6], a[7]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        if (j >= nt) break;
+        if (j > 0 && j >= nt) break;
         uint32_t b[4];
-        ldsm_x4(rows + j * 1024 + (b_at ^ (half << 6)), b[0], b[1], b[2], b[3]);
-        mma_bf16(sum[j], a[0], a[1], a[2], a[3], b[0], b[1]);
-        mma_bf16(sum[j], a[4], a[5], a[6], a[7], b[2], b[3]);
+        ldsm_x4(rows + (half >> 1) * (NT * 1024) + j * 1024 + (b_at ^ ((half & 1) << 6)), b[0], b[1], b[2], b[3]);
+        mma_bf16(sum[(2 * half) % kSets][j], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_bf16(sum[(2 * half + 1) % kSets][j], a[4], a[5], a[6], a[7], b[2], b[3]);
       }
     }
     __syncwarp();
@@ -431,7 +464,9 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   };
   auto clear = [&]() {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.f;
+    for (int k = 0; k < kSets; ++k)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sum[k][j][0] = sum[k][j][1] = sum[k][j][2] = sum[k][j][3] = 0.f;
   };
   // the warps' parts of tile j, added up (by one warp)
   auto add_up = [&](int buf, int j) {
@@ -446,24 +481,33 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   auto hand_in = [&](int buf, int nt) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      if (j < nt) red[((buf * kLayerWarps + warp) * NT + j) * 32 + lane] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
+      if (j < nt) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = sum[0][j][i] + sum[1][j][i];
+          if (kSets == 4) v[i] += sum[kSets - 2][j][i] + sum[kSets - 1][j][i];
+        }
+        red[((buf * kLayerWarps + warp) * NT + j) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+      }
     __syncthreads();
   };
   // this warp's steps of the rows of a tile (n of them from the list's first on; DIRECT: of all tokens)
   auto load_rows = [&](int first, int n) {
     uint32_t dst = rows_at;
-    for (int s = warp; s < steps_up; s += kLayerWarps, dst += NT * 1024) {
-      const int k = s * kStepK + 8 * (int)r8;
+    for (int s = warp; s < steps_up; s += kLayerWarps)
+      for (int span = 0; span < 2; ++span, dst += NT * 1024) {
+        const int k = s * kStepK + span * kSpan + 8 * (int)r8;
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) {
-        const int r = (int)m4 + 4 * i;
-        if (r < n) {
-          const int t = DIRECT ? r : list[first + r];
-          const uint16_t* const row = static_cast<const uint16_t*>(p.a.x) + t * p.a.x_stride;
-          op_cp16(dst + r * 128 + ((r8 ^ (r & 7)) << 4), k < d ? row + k : row, k < d ? 16 : 0);
+        for (int i = 0; i < 2 * NT; ++i) {
+          const int r = (int)m4 + 4 * i;
+          if (r < n) {
+            const int t = DIRECT ? r : list[first + r];
+            const uint16_t* const row = static_cast<const uint16_t*>(p.a.x) + t * p.a.x_stride;
+            op_cp16(dst + r * 128 + ((r8 ^ (r & 7)) << 4), k < d ? row + k : row, k < d ? 16 : 0);
+          }
         }
       }
-    }
     op_cp_wait_all();
     __syncwarp();
   };
@@ -485,7 +529,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
       have = cs.tile;
       clear();
       uint32_t rows = rows_at;
-      for (int s = warp; s < steps_up; s += kLayerWarps, rows += NT * 1024) {
+      for (int s = warp; s < steps_up; s += kLayerWarps, rows += NT * 2048) {
         multiply(rows, nt);
         issue_next();
       }
@@ -539,7 +583,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     }
   }
   auto take = [&](int nt) {
-    multiply(rows_at + get.slot * NT * 1024, nt);
+    multiply(rows_at + get.slot * NT * 2048, nt);
     if (id.block < blocks) {
       const uint32_t slot = put;
       issue_weights();
@@ -606,7 +650,10 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
 
 template <int TT>
 cudaError_t launch_router(const MoeParams& p, cudaStream_t st) {
-  return launch_early(router_kernel<TT>, dim3((unsigned)((p.a.n_tokens + TT - 1) / TT * kRouterCtas)), kRouterThreads, 0, st, p);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(router_kernel<TT>, TT * kMoeWidest * 2, done);
+  if (e != cudaSuccess) return e;
+  return launch_early(router_kernel<TT>, dim3((unsigned)((p.a.n_tokens + TT - 1) / TT * kRouterCtas)), kRouterThreads, (size_t)TT * p.a.d_model * 2, st, p);
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
@@ -659,7 +706,7 @@ int moe_shape(MoeParams& p) {
   const double mean = (double)entries / a.n_experts;
   p.direct = a.n_tokens <= kMoeDirect;
   p.nt = p.direct || mean <= 3 ? 1 : mean <= 10 ? 2 : 4;
-  while ((p.slots = layer_slots(a, p.nt, p.direct)) < 4 && p.nt > 1) p.nt /= 2;
+  while ((p.slots = layer_slots(a, p.nt, p.direct)) < 3 && p.nt > 1) p.nt /= 2;
   return p.slots;
 }
 

@@ -82,83 +82,95 @@ struct Peak {
   }
 };
 
-// One block per piece of a row: {largest, sum of exp((l - largest) / T), index of the largest (the lowest)}.  The piece stays in
-// registers between the two; threads meet once.  HBM bounds it.
-template <bool F32, int ITER>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ VerifyParams p) {
+// One block per piece of a row: {largest, sum of exp((l - largest) / T), index of the largest (the lowest; at temperature 0, where
+// the sum only tells whether there is a NaN)}.  HBM bounds it.  float32: four loads a thread and eight blocks an SM (batches that
+// follow one another: 14.3 us in place of 12.4 for 72 rows of 151936).  bf16, with twice the exponentials a byte: batches of two
+// loads, the next one under way while one is added up (11.7 us in place of 13.3 for 96 rows).
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads, F32 ? 8 : 6) row_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int kVec = F32 ? 4 : 8;  // elements of 16 bytes
+  constexpr int kRowLoads = F32 ? 4 : 2;
   __shared__ Peak s_peak[kRowThreads / 32];
   const int piece = blockIdx.x, node = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   if (node >= node_count(p.a, b)) return;
-  const void* row = logit_row(p.a, b, node);
-  const float beta = Heat(temperature(p.a, b)).hi;
-  const int base = piece * (kRowThreads * kVec * ITER) + kVec * threadIdx.x, n = p.a.vocab;
-  float x[ITER][kVec];
-  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0) {
-    uint4 u[ITER];
+  const uint8_t* const row = static_cast<const uint8_t*>(logit_row(p.a, b, node));
+  const Heat heat(temperature(p.a, b));
+  const float beta = heat.hi;
+  const bool greedy = heat.t == 0.f, wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+  constexpr int kBatch = kRowThreads * kVec * kRowLoads;
+  const int n = p.a.vocab, end = min(n, (piece + 1) * p.batches * kBatch);
+  int at = piece * p.batches * kBatch + kVec * threadIdx.x;
+  uint4 u[kRowLoads], next[kRowLoads];
+  auto load = [&](uint4 (&to)[kRowLoads], int from) {
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int at = base + i * kRowThreads * kVec;
-      if (at + kVec <= n) u[i] = op_ld16(static_cast<const uint8_t*>(row) + (long long)at * (F32 ? 4 : 2));
+    for (int i = 0; i < kRowLoads; ++i) {
+      const int j = from + i * kRowThreads * kVec;
+      if (wide && j + kVec <= n) to[i] = op_ld16(row + (long long)j * (F32 ? 4 : 2));
     }
+  };
+  Peak mine{-INFINITY, 0.f, 0x7fffffff};
+  if (at < end) load(u, at);
+#pragma unroll 1
+  for (; at < end; at += kBatch) {
+    if (!F32 && at + kBatch < end) load(next, at + kBatch);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int at = base + i * kRowThreads * kVec;
-      if (at + kVec <= n) {
+    for (int i = 0; i < kRowLoads; ++i) {
+      const int j = at + i * kRowThreads * kVec;
+      float x[kVec];
+      if (wide && j + kVec <= n) {
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int k = 0; k < 4; ++k) {
           if (F32) {
-            x[i][j] = __uint_as_float(w[j]);
+            x[k] = __uint_as_float(w[k]);
           } else {
-            const float2 f = bf16x2_to_f2(w[j]);
-            x[i][2 * j % kVec] = f.x, x[i][(2 * j + 1) % kVec] = f.y;
+            const float2 f = bf16x2_to_f2(w[k]);
+            x[2 * k % kVec] = f.x, x[(2 * k + 1) % kVec] = f.y;
           }
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) x[i][j] = at + j < n ? load_logit(row, at + j, F32) : -INFINITY;
+        for (int k = 0; k < kVec; ++k) x[k] = j + k < n ? load_logit(row, j + k, F32) : -INFINITY;
       }
+      float top = x[0];
+#pragma unroll
+      for (int k = 1; k < kVec; ++k) top = fmaxf(top, x[k]);
+      if (top > mine.top) {
+        mine.sum *= ex2((mine.top - top) * beta);
+        mine.top = top;
+        if (greedy) {
+#pragma unroll
+          for (int k = kVec - 1; k >= 0; --k)
+            if (x[k] == top) mine.arg = j + k;
+        }
+      }
+      const float from = mine.top == -INFINITY ? 0.f : mine.top;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) mine.sum += ex2((x[k] - from) * beta);
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const int at = base + i * kRowThreads * kVec + j;
-        x[i][j] = at < n ? load_logit(row, at, F32) : -INFINITY;
-      }
+    for (int i = 0; !F32 && i < kRowLoads; ++i) u[i] = next[i];
   }
-  Peak mine{-INFINITY, 0.f, 0x7fffffff};
-#pragma unroll
-  for (int i = 0; i < ITER; ++i)
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) mine.top = fmaxf(mine.top, x[i][j]);
-  const float from = mine.top == -INFINITY ? 0.f : mine.top;
-#pragma unroll
-  for (int i = ITER - 1; i >= 0; --i)
-#pragma unroll
-    for (int j = kVec - 1; j >= 0; --j) {
-      mine.sum += ex2((x[i][j] - from) * beta);
-      if (x[i][j] == mine.top) mine.arg = base + i * kRowThreads * kVec + j;
-    }
 #pragma unroll
   for (int o = 16; o; o >>= 1)
     mine.merge(__shfl_xor_sync(0xffffffffu, mine.top, o), __shfl_xor_sync(0xffffffffu, mine.sum, o), __shfl_xor_sync(0xffffffffu, mine.arg, o), beta);
   if (lane == 0) s_peak[warp] = mine;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
+    mine = s_peak[lane % (kRowThreads / 32)];
 #pragma unroll
-    for (int i = 1; i < kRowThreads / 32; ++i) mine.merge(s_peak[i].top, s_peak[i].sum, s_peak[i].arg, beta);
-    p.parts[((long long)b * p.a.n_nodes + node) * p.pieces + piece] = make_float4(mine.top, mine.sum, __int_as_float(mine.arg), 0.f);
+    for (int o = kRowThreads / 64; o; o >>= 1)
+      mine.merge(__shfl_xor_sync(0xffffffffu, mine.top, o), __shfl_xor_sync(0xffffffffu, mine.sum, o), __shfl_xor_sync(0xffffffffu, mine.arg, o),
+                 beta);
+    if (lane == 0) p.parts[((long long)b * p.a.n_nodes + node) * p.pieces + piece] = make_float4(mine.top, mine.sum, __int_as_float(mine.arg), 0.f);
   }
 }
 
 // ------------------------------------------------------------------------------------- exponentials
-// 2^(i/256), i = -128 .. 128, in units of 2^-52 and as a sum of two floats
-constexpr int kPowers = 257;
+// 2^(i/256), i = 0 .. 255, in units of 2^-52 and as a sum of two floats
+constexpr int kPowers = 256;
 struct __align__(16) Power {
   unsigned long long fix;
   float hi, lo;
@@ -167,9 +179,9 @@ struct Powers {
   Power v[kPowers];
   constexpr Powers() : v() {
     for (int i = 0; i < kPowers; ++i) {
-      const double x = (i - 128) / 256.0 * 0.69314718055994530942;
+      const double x = i / 256.0 * 0.69314718055994530942;
       double y = 1;
-      for (int k = 18; k > 0; --k) y = 1 + x / k * y;  // the exponential series
+      for (int k = 22; k > 0; --k) y = 1 + x / k * y;  // the exponential series
       v[i].fix = (unsigned long long)(y * 4503599627370496.0 + 0.5);
       v[i].hi = (float)y;
       v[i].lo = (float)(y - (double)v[i].hi);
@@ -178,53 +190,71 @@ struct Powers {
 };
 __device__ const Powers powers = Powers();
 
+struct U2 {
+  unsigned long long x, y;
+};
+__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+// (adding 1.5 * 2^23 rounds to an integer and leaves it in the low bits)
+constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ int low_bits(float v) { return __float_as_int(v) - 0x4b400000; }
+
+// exp((l - top) / T) in units of 2^-44 of two logits at once, for finite l <= top to 2^-41 of itself; 0 for anything else.  top: the
+// row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.)
+// One copy of the code: a cold kernel waits for its instructions longer than it runs them.
+__device__ __noinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const Power* table) {
+  const uint64_t minus = both(-1.f), l = pack2(l0, l1), b = both(bh);
+  // l - top as dh + dl, exactly; times log2(e) / T as ph + pl
+  const uint64_t dh = add2(l, both(-top)), z = fma2(l, minus, dh);
+  const uint64_t dl = fma2(add2(both(top), z), minus, fma2(fma2(z, minus, dh), minus, l));
+  const uint64_t ph = mul2(dh, b), pl = fma2(dh, both(bl), fma2(dl, b, fma2(dh, b, mul2(dh, both(-bh)))));
+  // ph = k / 256 + r, exactly
+  const uint64_t m = fma2(ph, both(256.f), both(kMagic)), r = fma2(add2(m, both(-kMagic)), both(-1.f / 256.f), ph);
+  // y = (r + pl) ln 2 as yh + yl, |y| < 2^-9; exp(y) - 1 = y + y^2 (1/2 + y/6) as eh + el
+  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654299957767e-9f;
+  const uint64_t yh = mul2(r, both(kLn2h));
+  const uint64_t yl = fma2(r, both(kLn2l), fma2(pl, both(kLn2h), fma2(r, both(kLn2h), mul2(r, both(-kLn2h)))));
+  const uint64_t s = fma2(mul2(yh, yh), fma2(yh, both(1.f / 6.f), both(0.5f)), fma2(yh, yl, yl));
+  const uint64_t eh = add2(yh, s), el = fma2(fma2(yh, minus, eh), minus, s);
+  // times the table's entry T = th + tl: T (exp(y) - 1) as wh + wl, then as an integer of 2^-52 in two steps of 22 bits
+  const float2 mf = unpack2(m), pf = unpack2(ph);
+  const int k0 = low_bits(mf.x), k1 = low_bits(mf.y);
+  const Power t0 = table[k0 & 255], t1 = table[k1 & 255];
+  const uint64_t th = pack2(t0.hi, t1.hi), tl = pack2(t0.lo, t1.lo);
+  const uint64_t wh = mul2(th, eh), wl = fma2(tl, eh, fma2(th, el, fma2(th, eh, mul2(wh, minus))));
+  const uint64_t m1 = fma2(wh, both(0x1p30f), both(kMagic)), rest = add2(fma2(add2(m1, both(-kMagic)), both(-0x1p-30f), wh), wl);
+  const float2 hi = unpack2(m1), lo = unpack2(fma2(rest, both(0x1p52f), both(kMagic)));
+  const unsigned long long v0 = t0.fix + (unsigned long long)((long long)low_bits(hi.x) * (1ll << 22) + low_bits(lo.x));
+  const unsigned long long v1 = t1.fix + (unsigned long long)((long long)low_bits(hi.y) * (1ll << 22) + low_bits(lo.y));
+  // (shifted by 52 - 44 and the whole part of k / 256, rounded)
+  return U2{pf.x >= -50.f ? ((v0 >> ((51 - kFixed - (k0 >> 8)) & 63)) + 1) >> 1 : 0ull,
+            pf.y >= -50.f ? ((v1 >> ((51 - kFixed - (k1 >> 8)) & 63)) + 1) >> 1 : 0ull};
+}
 struct Exp {
-  float top;        // the row's largest logit
-  float bh, bl;     // log2(e) / T
+  float top, bh, bl;
   const Power* table;
-  // exp((l - top) / T) in units of 2^-44, for finite l <= top, to 2^-41 of itself; 0 for anything else.
-  __device__ __forceinline__ unsigned long long operator()(float l) const {
-    // l - top as dh + dl, exactly; times log2(e) / T as ph + pl
-    const float dh = l - top, z = dh - l, dl = (l - (dh - z)) - (top + z);
-    // (every product that is used twice is rounded once: __fmul_rn is not fused into what follows)
-    const float ph = __fmul_rn(dh, bh);
-    if (!(ph >= -50.f)) return 0;
-    const float pl = fmaf(dh, bh, -ph) + fmaf(dh, bl, dl * bh);
-    // ph = n + i / 256 + r, exactly
-    const float n = rintf(ph), f = ph - n, i = rintf(f * 256.f), r = fmaf(i, -1.f / 256.f, f);
-    // y = (r + pl) ln 2 as yh + yl, |y| < 2^-9; exp(y) - 1 = y + y^2 (1/2 + y/6 + y^2/24)
-    constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654299957767e-9f;
-    const float yh = __fmul_rn(r, kLn2h), yl = fmaf(r, kLn2h, -yh) + fmaf(r, kLn2l, pl * kLn2h);
-    const float s = fmaf(yh * yh, fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f), fmaf(yh, yl, yl));
-    const float eh = yh + s, el = s - (eh - yh);
-    // times the table's entry T = th + tl: w = T (exp(y) - 1) as wh + wl, then as an integer of 2^-52 in two steps of 22 bits
-    const Power t = table[128 + (int)i];
-    const float wh = __fmul_rn(t.hi, eh), wl = fmaf(t.hi, eh, -wh) + fmaf(t.hi, el, t.lo * eh);
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer and leaves it in the low bits
-    const float m1 = fmaf(wh, 0x1p30f, kMagic), rest = fmaf(m1 - kMagic, -0x1p-30f, wh) + wl;
-    const float m2 = fmaf(rest, 0x1p52f, kMagic);
-    const int hi = __float_as_int(m1) - __float_as_int(kMagic), lo = __float_as_int(m2) - __float_as_int(kMagic);
-    const unsigned long long v = t.fix + (unsigned long long)(((long long)hi << 22) + lo);
-    const int shift = 52 - kFixed - (int)n;  // 8 .. 58
-    return (v + (1ull << (shift - 1))) >> shift;
-  }
+  __device__ __forceinline__ U2 operator()(float l0, float l1) const { return exp_fixed(l0, l1, top, bh, bl, table); }
+  __device__ __forceinline__ unsigned long long operator()(float l) const { return exp_fixed(l, l, top, bh, bl, table).x; }
 };
 
-// (E - q A)+ with A = ah + am (to 2^-48 of itself), all in units of 2^-44
+// (E - q A)+ with A = ah + am (to 2^-48 of itself), all in units of 2^-44, of two probabilities at once
 struct Cut {
   float ah, am;
   __device__ __forceinline__ explicit Cut(unsigned long long a) {
     ah = __ull2float_rn(a);
     am = (float)(long long)(a - __float2ull_rn(ah));
   }
-  __device__ __forceinline__ unsigned long long operator()(unsigned long long e, float q) const {
-    q = fminf(fmaxf(q, 0.f), 1.f);  // (NaN: 0)
-    const float th = __fmul_rn(q, ah);
-    if (!(th < 0x1p46f)) return 0;  // E is 2^44 at most
-    const float tl = fmaf(q, ah, -th) + q * am;
-    const long long left = (long long)e - (__float2ll_rn(th) + __float2ll_rn(tl));
-    return left > 0 ? (unsigned long long)left : 0ull;
+  __device__ __forceinline__ U2 operator()(unsigned long long e0, unsigned long long e1, float q0, float q1) const {
+    const uint64_t q = pack2(fminf(fmaxf(q0, 0.f), 1.f), fminf(fmaxf(q1, 0.f), 1.f));  // (NaN: 0)
+    // q A as th + tl, then as an integer in two steps of 23 bits; E is 2^44 at most
+    const uint64_t th = mul2(q, both(ah)), tl = fma2(q, both(am), fma2(q, both(ah), mul2(q, both(-ah))));
+    const uint64_t m1 = fma2(th, both(0x1p-23f), both(kMagic));
+    const uint64_t m2 = add2(add2(fma2(add2(m1, both(-kMagic)), both(-0x1p23f), th), tl), both(kMagic));
+    const float2 t = unpack2(th), hi = unpack2(m1), lo = unpack2(m2);
+    const long long y0 = (long long)e0 - ((long long)low_bits(hi.x) * (1ll << 23) + low_bits(lo.x));
+    const long long y1 = (long long)e1 - ((long long)low_bits(hi.y) * (1ll << 23) + low_bits(lo.y));
+    return U2{t.x < 0x1p44f && y0 > 0 ? (unsigned long long)y0 : 0ull, t.y < 0x1p44f && y1 > 0 ? (unsigned long long)y1 : 0ull};
   }
+  __device__ __forceinline__ unsigned long long operator()(unsigned long long e, float q) const { return (*this)(e, e, q, q).x; }
 };
 
 // -------------------------------------------------------------------------------------------- walk
@@ -453,7 +483,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           child = v.first;
           n_gone = 0;
           whole = true;
-          left = (double)v.sum * 0x1p44;
           if (!(fabsf(v.top) < INFINITY && v.sum > 0.f)) {  // (a NaN in the row is a NaN in the sum)
             if (rank == 0) op_error(a.status, MK_ERR_INVALID, b, at, __float_as_int(v.top));
             step = kEnd;
@@ -469,7 +498,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           const Node& c = sh.node[child];
           bool taken = c.fits != 0;
           unsigned long long y = 0;
-          if (!taken || !whole) {
+          if ((!taken || !whole) && heat.t != 0.f) {
+            if (whole) left = (double)sh.node[at].sum * 0x1p44;
             ex.top = sh.node[at].top;
             y = ex(c.l);
           }
@@ -554,7 +584,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
         } else {
           v = load4(row, j, a.vocab, f32, false, -INFINITY);
         }
-        unsigned long long y[4] = {ex(v.x), ex(v.y), ex(v.z), ex(v.w)};
+        const U2 lo = ex(v.x, v.y), hi = ex(v.z, v.w);
+        unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
         for (int g = 0; g < gone; ++g) {
           const int d = sh.gone[g] - j;
 #pragma unroll
@@ -585,7 +616,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
             if (k + i < n_blocks) {
               const ulonglong2* const y = reinterpret_cast<const ulonglong2*>(e + from + (k + i) * kBlock);
               const ulonglong2 lo = y[0], hi = y[1];
-              sum += cut(lo.x, qs[i].x) + cut(lo.y, qs[i].y) + cut(hi.x, qs[i].z) + cut(hi.y, qs[i].w);
+              const U2 c = cut(lo.x, lo.y, qs[i].x, qs[i].y), d = cut(hi.x, hi.y, qs[i].z, qs[i].w);
+              sum += c.x + c.y + d.x + d.y;
             }
         }
         sum = warp_total(sum);
@@ -624,7 +656,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           const ulonglong2* const at4 = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
           const ulonglong2 lo = at4[0], hi = at4[1];
           unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
-          if (A) y[0] = cut(y[0], qs[k4].x), y[1] = cut(y[1], qs[k4].y), y[2] = cut(y[2], qs[k4].z), y[3] = cut(y[3], qs[k4].w);
+          if (A) {
+            const U2 c = cut(lo.x, lo.y, qs[k4].x, qs[k4].y), d = cut(hi.x, hi.y, qs[k4].z, qs[k4].w);
+            y[0] = c.x, y[1] = c.y, y[2] = d.x, y[3] = d.y;
+          }
           const unsigned long long own = y[0] + y[1] + y[2] + y[3];
           unsigned long long upto = own;
 #pragma unroll
@@ -663,13 +698,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   walk_sync();  // no CTA leaves while another may write to it or read its nodes
 }
 
-// Loads of 16 bytes a thread: four, or eight where that leaves enough blocks to fill the GPU
-int row_iter(const mk_verify_args& a) {
-  const int piece = kRowThreads * (a.logits_float ? 4 : 8) * 8;
-  return (long long)a.batch * a.n_nodes * ((a.vocab + piece - 1) / piece) >= 2000 ? 8 : 4;
+// Elements of a batch, and batches of a piece: float32 one, bf16 as many as leave about six blocks an SM (a number of blocks, not
+// of SMs: the workspace's size goes by it)
+constexpr int kRowBatch = kRowThreads * 16;
+int row_batches(const mk_verify_args& a) {
+  if (a.logits_float) return 1;
+  const long long in_row = (a.vocab + kRowBatch - 1) / kRowBatch;
+  return (int)std::min(std::max(1ll, (long long)std::max(1, a.batch) * a.n_nodes * in_row / 900), in_row);
 }
 int row_pieces(const mk_verify_args& a) {
-  const int piece = kRowThreads * (a.logits_float ? 4 : 8) * row_iter(a);
+  const int piece = kRowBatch * row_batches(a);
   return (a.vocab + piece - 1) / piece;
 }
 
@@ -681,22 +719,29 @@ size_t verify_workspace_bytes(const mk_verify_args& a) {
 
 cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
   p.parts = static_cast<float4*>(p.a.workspace);
+  p.batches = row_batches(p.a);
   p.pieces = row_pieces(p.a);
   const dim3 grid((unsigned)p.pieces, (unsigned)p.a.n_nodes, (unsigned)p.a.batch);
-  const bool f32 = p.a.logits_float != 0, eight = row_iter(p.a) == 8;
-  cudaError_t e = f32 ? (eight ? launch_early(row_kernel<true, 8>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<true, 4>, grid, kRowThreads, 0, st, p))
-                      : (eight ? launch_early(row_kernel<false, 8>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<false, 4>, grid, kRowThreads, 0, st, p));
+  cudaError_t e = p.a.logits_float ? launch_early(row_kernel<true>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<false>, grid, kRowThreads, 0, st, p);
   static std::atomic<unsigned long long> done{0}, done16{0};
-  static std::atomic<int> known[64];
+  static std::atomic<int> known[3][64];
   constexpr int kSmem = kCtaBlocks * kBlock * 8;
   if (e == cudaSuccess) e = allow_smem(walk_kernel, kSmem, done);
   if (e == cudaSuccess) e = allow_wide_clusters(walk_kernel, done16);
-  // clusters of 16 while all of them fit the GPU at once, and where a piece of 8 would not fit shared memory
+  // the largest clusters that fit the GPU all at once (7 of 16 CTAs, 8 of 12, 13 of 10, 15 of 8), at least as many CTAs as a row's
+  // exponentials need for their shared memory
   const int blocks = (p.a.vocab + kBlock - 1) / kBlock;
-  int ctas = 8, wide = 0;
-  if (e == cudaSuccess && blocks > 256) e = active_clusters(walk_kernel, kWalkCtas, kWalkThreads, kSmem, known, &wide);
+  const int sizes[4] = {16, 12, 10, 8}, least = blocks > 8 * kCtaBlocks ? 16 : 8;
+  int ctas = least;
+  for (int i = 0; e == cudaSuccess && blocks > 256 && i < 3 && sizes[i] > least; ++i) {
+    int fit = 0;
+    e = active_clusters(walk_kernel, sizes[i], kWalkThreads, kSmem, known[i], &fit);
+    if (p.a.batch <= fit) {
+      ctas = sizes[i];
+      break;
+    }
+  }
   if (e != cudaSuccess) return e;
-  if (blocks > 8 * kCtaBlocks || p.a.batch <= wide) ctas = kWalkCtas;
   const size_t smem = (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
   return launch_clusters(walk_kernel, dim3((unsigned)(p.a.batch * ctas)), ctas, kWalkThreads, smem, st, p);
 }
