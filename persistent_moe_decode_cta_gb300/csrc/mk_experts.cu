@@ -190,7 +190,7 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& l
   if (blockIdx.x == 0 && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
 }
 
-// (EPI: one expert with every row)
+// (EPI without offsets: one expert with every row)
 template <bool EPI>
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
@@ -200,7 +200,7 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows
     int x = 0;
     if (e < E) {
       int lo = 0, hi = p.a.n_rows;
-      if (!EPI) expert_rows(p, e, lo, hi);
+      if (!EPI || p.a.offsets) expert_rows(p, e, lo, hi);
       sh.rows[e] = make_int2(lo, hi);
       x = (hi - lo + tile_rows - 1) / tile_rows;
       if (hi > lo) atomicMax(&sh.most, hi - lo);

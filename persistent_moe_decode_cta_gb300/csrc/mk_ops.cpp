@@ -151,6 +151,24 @@ bool overlap(const Rows& a, const Rows& b) {
   return !(a.width <= d && d + b.width <= a.stride);
 }
 
+// the maps of the products grouped by expert
+struct ExpertMaps {
+  CUtensorMap x, x128, w, up;
+};
+int expert_maps(const mk_expert_args& a, ExpertMaps& m) {
+  const cuuint64_t xd[2] = {(cuuint64_t)a.k, (cuuint64_t)a.n_x};
+  const cuuint64_t xs[1] = {(cuuint64_t)a.x_stride * 2};
+  const cuuint32_t xb[2] = {64, 32}, xb128[2] = {64, 128};
+  int r = encode(&m.x, a.x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = encode(&m.x128, a.x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint64_t wd[3] = {(cuuint64_t)a.k, (cuuint64_t)a.n, (cuuint64_t)a.n_experts};
+  const cuuint64_t ws[2] = {(cuuint64_t)a.k * 2, (cuuint64_t)a.n * a.k * 2};
+  const cuuint32_t wb[3] = {64, a.w_up ? 64u : 128u, 1};
+  if (!r) r = encode(&m.w, a.w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r) r = encode(&m.up, a.w_up ? a.w_up : a.w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  return r;
+}
+
 int check_moe(const mk_moe_args* a) {
   if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
   if (a->n_tokens < 0) return op_fail(MK_ERR_INVALID, "n_tokens %d < 0", a->n_tokens);
@@ -364,21 +382,11 @@ int mk_expert_product(const mk_expert_args* a, void* stream) {
   p.a = *a;
   int r = num_sms(&p.grid);
   if (r) return r;
-  CUtensorMap tx, tx128, tw, tu;
-  cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n_x};
-  cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
-  cuuint32_t xb[2] = {64, 32};
-  cuuint32_t xb128[2] = {64, 128};
-  r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!r) r = encode(&tx128, a->x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
-  cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, (cuuint64_t)a->n_experts};
-  cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
-  cuuint32_t wb[3] = {64, a->w_up ? 64u : 128u, 1};
-  if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!r) r = encode(&tu, a->w_up ? a->w_up : a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  ExpertMaps m;
+  r = expert_maps(*a, m);
   if (!r) r = set_record(p.a.status);
   if (r) return r;
-  return cuda_error(launch_experts(p, tx, tx128, tw, tu, static_cast<cudaStream_t>(stream)), "expert_product launch");
+  return cuda_error(launch_experts(p, m.x, m.x128, m.w, m.up, static_cast<cudaStream_t>(stream)), "expert_product launch");
 }
 
 int mk_linear(const mk_linear_args* a, void* stream) {
@@ -429,9 +437,6 @@ int mk_linear(const mk_linear_args* a, void* stream) {
   int r = num_sms(&p.grid);
   if (!r) r = set_record(p.a.status);
   if (r) return r;
-  CUtensorMap tx, tx128, tw;
-  cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->m};
-  cuuint64_t xs[1] = {(cuuint64_t)a->x_stride * 2};
   SplitParams s{};
   s.epi = epi;
   s.out = a->out;
@@ -444,23 +449,19 @@ int mk_linear(const mk_linear_args* a, void* stream) {
   r = cuda_error(split_shape(s, p.grid, &few), "clusters");
   if (r) return r;
   if (few) {
-    const cuuint32_t sxb[2] = {64, (cuuint32_t)s.box}, swb[2] = {64, 128};
-    const cuuint64_t swd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n}, sws[1] = {(cuuint64_t)a->k * 2};
-    r = encode(&tx, a->x, 2, xd, xs, sxb, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (!r) r = encode(&tw, a->w, 2, swd, sws, swb, CU_TENSOR_MAP_SWIZZLE_128B);
+    CUtensorMap tx, tw;
+    const cuuint64_t xd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->m}, xs[1] = {(cuuint64_t)a->x_stride * 2};
+    const cuuint64_t wd[2] = {(cuuint64_t)a->k, (cuuint64_t)a->n}, ws[1] = {(cuuint64_t)a->k * 2};
+    const cuuint32_t xb[2] = {64, (cuuint32_t)s.box}, wb[2] = {64, 128};
+    r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!r) r = encode(&tw, a->w, 2, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
     if (r) return r;
     return cuda_error(launch_linear_split(s, tx, tw, static_cast<cudaStream_t>(stream)), "linear launch");
   }
-  cuuint32_t xb[2] = {64, 32};
-  cuuint32_t xb128[2] = {64, 128};
-  r = encode(&tx, a->x, 2, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!r) r = encode(&tx128, a->x, 2, xd, xs, xb128, CU_TENSOR_MAP_SWIZZLE_128B);
-  cuuint64_t wd[3] = {(cuuint64_t)a->k, (cuuint64_t)a->n, 1};
-  cuuint64_t ws[2] = {(cuuint64_t)a->k * 2, (cuuint64_t)a->n * a->k * 2};
-  cuuint32_t wb[3] = {64, 128, 1};
-  if (!r) r = encode(&tw, a->w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+  ExpertMaps em;
+  r = expert_maps(p.a, em);
   if (r) return r;
-  return cuda_error(launch_linear_pairs(p, epi, tx, tx128, tw, static_cast<cudaStream_t>(stream)), "linear launch");
+  return cuda_error(launch_linear_pairs(p, epi, em.x, em.x128, em.w, static_cast<cudaStream_t>(stream)), "linear launch");
 }
 
 int mk_moe_layer_workspace(const mk_moe_args* a, size_t* bytes) {
@@ -508,21 +509,57 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
   p.a = *a;
   r = num_sms(&p.grid);
   if (r) return r;
-  if (!moe_shape(p)) return op_fail(MK_ERR_UNSUPPORTED, "d_model %d with %d tokens does not fit shared memory", a->d_model, a->n_tokens);
-  MoeMaps m;
-  const auto matrix = [&](CUtensorMap* tm, const void* base, long long rows, long long cols, int high) {
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)high};
-    return encode(tm, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  r = matrix(&m.gate, a->w_gate, e * f, d, 8);
-  if (!r) r = matrix(&m.up, a->w_up, e * f, d, 8);
-  if (!r) r = matrix(&m.down, a->w_down, e * d, f, p.width);
-  if (!r) r = matrix(&m.h, p.h, moe_h_rows(*a), f, 8 * p.nt);
-  if (!r) r = set_record(p.a.status);
+  moe_shape(p);
+  r = set_record(p.a.status);
   if (r) return r;
-  return cuda_error(launch_moe(p, m, static_cast<cudaStream_t>(stream)), "moe_layer launch");
+  const auto st = static_cast<cudaStream_t>(stream);
+  // (everything that can be refused is before the first launch)
+  if (p.nt) {
+    MoeMaps m;
+    const auto matrix = [&](CUtensorMap* tm, const void* base, long long rows, long long cols, int high) {
+      const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+      const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+      const cuuint32_t box[2] = {64, (cuuint32_t)high};
+      return encode(tm, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    r = matrix(&m.gate, a->w_gate, e * f, d, 8);
+    if (!r) r = matrix(&m.up, a->w_up, e * f, d, 8);
+    if (!r) r = matrix(&m.down, a->w_down, e * d, f, p.width);
+    if (!r) r = matrix(&m.h, p.h, moe_h_rows(*a), f, 8 * p.nt);
+    if (!r) r = cuda_error(launch_moe_router(p, st), "moe_layer launch");
+    if (!r) r = cuda_error(launch_moe_few(p, m, st), "moe_layer launch");
+    return r;
+  }
+  ExpertParams glu{}, down{};
+  glu.grid = down.grid = p.grid;
+  glu.a.x = a->x;
+  glu.a.w = a->w_gate;
+  glu.a.w_up = a->w_up;
+  glu.a.offsets = down.a.offsets = p.offsets;
+  glu.a.rows = p.rows;
+  glu.a.out = p.h;
+  glu.a.status = down.a.status = p.a.status;
+  glu.a.x_stride = a->x_stride;
+  glu.a.out_stride = down.a.x_stride = f;
+  glu.a.n_x = (int32_t)t;
+  glu.a.n_rows = down.a.n_x = down.a.n_rows = (int32_t)tk;
+  glu.a.n_experts = down.a.n_experts = (int32_t)e;
+  glu.a.n = down.a.k = (int32_t)f;
+  glu.a.k = down.a.n = (int32_t)d;
+  down.a.x = p.h;
+  down.a.w = a->w_down;
+  down.a.out = p.y;
+  down.a.out_stride = d;
+  LinearEpi epi{};  // (float32, as it is)
+  epi.out_float = epi.vec = 1;
+  ExpertMaps mg, md;
+  r = expert_maps(glu.a, mg);
+  if (!r) r = expert_maps(down.a, md);
+  if (!r) r = cuda_error(launch_moe_router(p, st), "moe_layer launch");
+  if (!r) r = cuda_error(launch_experts(glu, mg.x, mg.x128, mg.w, mg.up, st), "moe_layer launch");
+  if (!r) r = cuda_error(launch_linear_pairs(down, epi, md.x, md.x128, md.w, st), "moe_layer launch");
+  if (!r) r = cuda_error(launch_moe_sum(p, st), "moe_layer launch");
+  return r;
 }
 
 int mk_verify_nodes_workspace(const mk_verify_args* a, size_t* bytes) {

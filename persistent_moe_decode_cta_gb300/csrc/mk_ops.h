@@ -190,26 +190,31 @@ cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, con
 // ------------------------------------------------------------------ moe_layer
 constexpr int kMoeTokens = 256;   // tokens of one call
 constexpr int kMoeTopK = 16;
-constexpr int kMoeDirect = 8;     // up to here a tile's rows are the tokens
-constexpr int kMoeWidest = 8192;  // d_model: a tile's rows stay in shared memory
+constexpr int kMoeFew = 16;       // ... of both products in one kernel
+constexpr int kMoeWidest = 8192;  // d_model: the tokens stay in shared memory
 struct MoeParams {
   mk_moe_args a;
   int grid;          // CTAs of the products
-  int width;         // output columns of a CTA's block
-  int nt, slots;     // row tiles of a pass, slots of a warp's ring
-  bool direct;
+  int nt;            // row tiles of 8 (few tokens), or 0
+  int width, slots;  // few tokens: output columns of a CTA's block, slots of a warp's ring
+  int vec;           // residual and out can be read and written four values at a time
   int32_t* ids;      // the caller's or the workspace's
   float* weights;
-  uint16_t* h;       // [moe_h_rows][d_ff] bf16: c * silu(gate) * up
+  uint16_t* h;       // [moe_h_rows][d_ff] bf16: silu(gate) * up, of few tokens times c
   uint32_t* sync;    // counters, zeroed by the router
+  // more tokens
+  int32_t *offsets, *rows, *places;  // an expert's rows; the token of a row; the row of a token's j-th expert
+  float* y;          // [rows][d_model]
 };
 struct MoeMaps {
   CUtensorMap gate, up, down, h;
 };
 size_t moe_workspace_bytes(const mk_moe_args& a);
 long long moe_h_rows(const mk_moe_args& a);
-int moe_shape(MoeParams& p);  // fills what follows `grid`; 0: it does not fit
-cudaError_t launch_moe(const MoeParams& p, const MoeMaps& m, cudaStream_t st);
+void moe_shape(MoeParams& p);  // fills what follows `grid`
+cudaError_t launch_moe_router(const MoeParams& p, cudaStream_t st);
+cudaError_t launch_moe_few(const MoeParams& p, const MoeMaps& m, cudaStream_t st);
+cudaError_t launch_moe_sum(const MoeParams& p, cudaStream_t st);
 
 // ------------------------------------------------------------------ verify_nodes
 constexpr int kVerifyVocab = 1 << 18;

@@ -9,7 +9,7 @@ NAMES = ["mk_moe.cu", "mk_verify.cu", "mk_linear.cu"]
 
 
 def test_the_kernels_and_readers_are_found():
-    assert [[k for k, _ in T.kernels(f)] for f in NAMES] == [["router_kernel", "layer_kernel"], ["row_kernel", "walk_kernel"],
+    assert [[k for k, _ in T.kernels(f)] for f in NAMES] == [["router_kernel", "layer_kernel", "sort_kernel", "sum_kernel"], ["row_kernel", "walk_kernel"],
                                                           ["split_kernel"]]
     assert {"gather_nodes"} <= readers("mk_verify.cu")
 
