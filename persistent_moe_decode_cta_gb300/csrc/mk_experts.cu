@@ -191,7 +191,7 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& l
 }
 
 // (EPI without offsets: one expert with every row)
-template <bool EPI>
+template <int EPI>
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
   int carry = 0;
@@ -242,7 +242,8 @@ __device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& s
 
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-template <bool GLU, bool EPI>
+// EPI: 0 none, 1 with an epilogue, 2 with one and float32 results
+template <bool GLU, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGatherThreads, 1)
     expert_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ CUtensorMap tx,
                   const __grid_constant__ CUtensorMap tx128, const __grid_constant__ CUtensorMap tw,
@@ -286,8 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  // (a float32 result: half as many rows, whose sums the epilogue keeps in registers)
-  scan_experts<EPI>(p, sh, EPI && epi.out_float ? kTileR / 2 : kTileR);
+    scan_experts<EPI>(p, sh, EPI ? epi.tile_rows : kTileR);
   const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
@@ -299,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, x); };  // (one thread)
   // The products cut what they add to below the accumulator's last bit, so that the error of a long sum grows with its length: a
   // float32 result adds segments of 512 columns up in registers (2048 columns: 2.1e-6 of the result without, in the 2-norm).
-  const int segment = EPI && epi.out_float ? 8 : ksteps;
+  const int segment = EPI == 2 ? 8 : ksteps;
   const int clusters = (int)gridDim.x / 2, mine = (tiles - (int)blockIdx.x / 2 + clusters - 1) / clusters;  // tiles of this cluster
   ExpTile x;
 
@@ -455,7 +455,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       float* const mine_g = reinterpret_cast<float*>(epi_g) + (warp - 2) * 16 * 32;
       for (int t = 0; tile(t, x); ++t) {
         const int w0 = x.w0 + (int)rank * kTileW + o, width = min(32, p.a.n - w0);
-        if (epi.out_float) {
+        const float bias = epi.bias && lane < width ? bf16_to_f(op_ld2(epi.bias + w0 + lane)) : 0.f;
+        uint2 ahead[4];  // (the residual is on its way before its results are there)
+        linear_ahead(epi, ahead, x.r0 + 16 * half, x.nr - 16 * half, w0, width, lane);
+        if (EPI == 2) {
           float sum[4][16];
           for (int ks = 0; ks < ksteps; ks += segment, ++na) {
             const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21) + 16 * half;
@@ -476,8 +479,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (32 * c + 16 * half < x.nr)
-              linear_store(p.a, epi, sum[c], x.r0 + 32 * c + 16 * half, x.nr - (32 * c + 16 * half), w0, width, mine_g, lane);
+            if (32 * c + 16 * half < x.nr) {
+              const int r = 32 * c + 16 * half;
+              if (c > 0) linear_ahead(epi, ahead, x.r0 + r, x.nr - r, w0, width, lane);
+              linear_store<true>(p.a, epi, sum[c], ahead, x.r0 + r, x.nr - r, w0, width, bias, mine_g, lane);
+            }
           continue;
         }
         const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21);
@@ -492,9 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
           const bool more = c + 32 < x.nr;
+          uint2 next[4];
           if (more) tmem_ld16(acc + c + 32, u);
-          linear_store(p.a, epi, v, x.r0 + c, x.nr - c, w0, width, mine_g, lane);
+          linear_ahead(epi, next, x.r0 + c + 32, x.nr - c - 32, w0, width, lane);
+          linear_store<false>(p.a, epi, v, ahead, x.r0 + c, x.nr - c, w0, width, bias, mine_g, lane);
           if (more) tmem_wait16(u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ahead[i] = next[i];
         }
         tc_fence_before();
         __syncwarp();
@@ -567,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   }
 }
 
-template <bool GLU, bool EPI>
+template <bool GLU, int EPI>
 cudaError_t launch_kind(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                         const CUtensorMap& tu, const LinearEpi& epi, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
@@ -582,12 +592,12 @@ cudaError_t launch_kind(const ExpertParams& p, const CUtensorMap& tx, const CUte
 cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                            const CUtensorMap& tu, cudaStream_t st) {
   const LinearEpi none{};
-  return p.a.w_up ? launch_kind<true, false>(p, tx, tx128, tw, tu, none, st) : launch_kind<false, false>(p, tx, tx128, tw, tu, none, st);
+  return p.a.w_up ? launch_kind<true, 0>(p, tx, tx128, tw, tu, none, st) : launch_kind<false, 0>(p, tx, tx128, tw, tu, none, st);
 }
 
 cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, const CUtensorMap& tx, const CUtensorMap& tx128,
                                 const CUtensorMap& tw, cudaStream_t st) {
-  return launch_kind<false, true>(p, tx, tx128, tw, tw, epi, st);
+  return epi.out_float ? launch_kind<false, 2>(p, tx, tx128, tw, tw, epi, st) : launch_kind<false, 1>(p, tx, tx128, tw, tw, epi, st);
 }
 
 }  // namespace mk

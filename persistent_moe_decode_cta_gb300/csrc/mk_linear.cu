@@ -39,6 +39,7 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* tm, in
                : "memory");
 }
 
+template <bool WIDE>
 __global__ void __launch_bounds__(kSplitThreads, 1)
     split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw) {
   extern __shared__ uint8_t raw[];
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   for (int i = 0; i < 4; ++i) b[i] = p.epi.bias && col + i < width ? bf16_to_f(op_ld2(p.epi.bias + w0 + col + i)) : 0.f;
   for (int r = warp; r < last; r += kSplitThreads / 32) {
     const long long row = r0 + (long long)rank * own + r;
+    const uint2 ahead = linear_residual(p.epi, row, w0 + col, width - col);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     float4 y = *reinterpret_cast<const float4*>(sums_g + r * kSplitW + col);
     v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += b[i];
-    linear_acts(v, p.epi.act, p.epi.out_float != 0);
-    linear_put(p.epi, p.out, p.out_stride, v, row, w0 + col, width - col);
+    linear_acts<WIDE>(v, p.epi.act);
+    linear_put<WIDE>(p.epi, p.out, p.out_stride, v, ahead, row, w0 + col, width - col);
   }
   if (warp == 1) {
     tc_fence_after();
@@ -177,19 +179,22 @@ cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
   const long long pairs = (long long)((p.n + 255) / 256) * ((p.m + 255) / 256);
   *fits = p.m <= 1024 && pairs * 4 <= sms;
   if (!*fits) return cudaSuccess;
-  const int r_tiles = (p.m + 127) / 128;
+  // 64 rows a tile while every tile has an SM, else 128: of twice as many rows a CTA hands on twice the sums (128 rows, 4096 -> 2048:
+  // 11.2 us with 128, 9.0 with 64; 1024 rows 21 and 32)
+  p.w_tiles = (p.n + kSplitW - 1) / kSplitW;
+  const int most = (p.m + 63) / 64 * p.w_tiles <= sms ? 64 : 128, r_tiles = (p.m + most - 1) / most;
   p.rows = ((p.m + r_tiles - 1) / r_tiles + 15) / 16 * 16;
   p.box = p.rows;
-  p.w_tiles = (p.n + kSplitW - 1) / kSplitW;
   p.r_tiles = (p.m + p.rows - 1) / p.rows;
   p.chunks = (p.k + kSplitK - 1) / kSplitK;
-  // as many slices as keep all clusters on the GPU at once (16 tiles in 8 slices: 18 us, 15 clusters of 8 fit; in 6: @@ us)
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(split_kernel, kSplitSmem, done);
+  // as many slices as keep all clusters on the GPU at once (16 tiles in 8 slices: 18 us, 15 clusters of 8 fit; in 6: 10.4, at 128 rows a tile)
+  static std::atomic<unsigned long long> done{0}, done_wide{0};
+  cudaError_t e = allow_smem(split_kernel<false>, kSplitSmem, done);
+  if (e == cudaSuccess) e = allow_smem(split_kernel<true>, kSplitSmem, done_wide);
   static std::atomic<int> known[8][64];
   for (p.slices = std::min(8, p.chunks); e == cudaSuccess && p.slices > 1; --p.slices) {
     int n = 0;
-    e = active_clusters(split_kernel, p.slices, kSplitThreads, kSplitSmem, known[p.slices - 1], &n);
+    e = active_clusters(split_kernel<false>, p.slices, kSplitThreads, kSplitSmem, known[p.slices - 1], &n);
     if (p.w_tiles * p.r_tiles <= n) break;
   }
   p.tmem_cols = 32;
@@ -203,7 +208,9 @@ cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
 }
 
 cudaError_t launch_linear_split(const SplitParams& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
-  return launch_clusters(split_kernel, dim3((unsigned)(p.w_tiles * p.r_tiles * p.slices)), p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw);
+  const dim3 grid((unsigned)(p.w_tiles * p.r_tiles * p.slices));
+  return p.epi.out_float ? launch_clusters(split_kernel<true>, grid, p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw)
+                         : launch_clusters(split_kernel<false>, grid, p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw);
 }
 
 }  // namespace mk

@@ -557,6 +557,11 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
   pdl_wait();
   pdl_trigger();
   if (c >= d) return;
+  LinearEpi epi{};
+  epi.residual = static_cast<const uint16_t*>(p.a.residual);
+  epi.residual_stride = p.a.residual_stride;
+  epi.vec = p.vec;
+  const uint2 ahead = linear_residual(epi, t, c, d - c);
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int j = 0; j < K; ++j) {
@@ -566,11 +571,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
     y.z = fmaf(w, __uint_as_float(u.z), y.z), y.w = fmaf(w, __uint_as_float(u.w), y.w);
   }
   const float v[4] = {y.x, y.y, y.z, y.w};
-  LinearEpi epi{};
-  epi.residual = static_cast<const uint16_t*>(p.a.residual);
-  epi.residual_stride = p.a.residual_stride;
-  epi.vec = p.vec;
-  linear_put(epi, p.a.out, p.a.out_stride, v, t, c, d - c);
+  linear_put<false>(epi, p.a.out, p.a.out_stride, v, ahead, t, c, d - c);
 }
 
 // ----------------------------------------------------------------------------------------- launches

@@ -169,6 +169,22 @@ int expert_maps(const mk_expert_args& a, ExpertMaps& m) {
   return r;
 }
 
+// Rows of a tile of 256 outputs: what gives the least time over the rounds of tiles that the pairs of SMs take, where 64 columns
+// take 2 cycles a row, or as long as a pair's copies of them, 128 bytes a cycle (2001 x 4096: 2 rounds of 224 rows, 9 row tiles in
+// place of 8: @@ us, with 256 @@).  A float32 result has 128 at most, whose sums the epilogue keeps in registers.
+int pair_rows(long long m, long long n, bool wide, int sms) {
+  const long long pairs = std::max(1, sms / 2), w = (n + 255) / 256;
+  const int most = wide ? 128 : 256;
+  long long least = -1;
+  int best = most;
+  for (int r = most; r >= 64; r -= 32) {
+    const long long tiles = (m + r - 1) / r, rows = ((m + tiles - 1) / tiles + 31) / 32 * 32;
+    const long long cost = (tiles * w + pairs - 1) / pairs * std::max(2 * rows, 256 + rows);
+    if (least < 0 || cost < least) least = cost, best = r;
+  }
+  return best;
+}
+
 int check_moe(const mk_moe_args* a) {
   if (!a) return op_fail(MK_ERR_INVALID, "args is NULL");
   if (a->n_tokens < 0) return op_fail(MK_ERR_INVALID, "n_tokens %d < 0", a->n_tokens);
@@ -458,6 +474,7 @@ int mk_linear(const mk_linear_args* a, void* stream) {
     if (r) return r;
     return cuda_error(launch_linear_split(s, tx, tw, static_cast<cudaStream_t>(stream)), "linear launch");
   }
+  epi.tile_rows = pair_rows(a->m, a->n, epi.out_float, p.grid);
   ExpertMaps em;
   r = expert_maps(p.a, em);
   if (r) return r;
@@ -552,6 +569,7 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
   down.a.out_stride = d;
   LinearEpi epi{};  // (float32, as it is)
   epi.out_float = epi.vec = 1;
+  epi.tile_rows = 128;
   ExpertMaps mg, md;
   r = expert_maps(glu.a, mg);
   if (!r) r = expert_maps(down.a, md);

@@ -170,6 +170,7 @@ struct LinearEpi {
   int64_t residual_stride;
   int act, out_float;
   int vec;                   // residual and out can be read and written four values at a time
+  int tile_rows;             // of a tile, at most (a multiple of 32)
 };
 // The same for few rows (mk_linear.cu).
 struct SplitParams {
