@@ -449,24 +449,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     uint16_t* const stage = reinterpret_cast<uint16_t*>(epi_g) + q * kChunk * 32;
     float* const exch_g = reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + (q & 1) * kChunk * 32;
     if (EPI) {
-      // eight warps: two share the lanes and take 16 rows in turn.  (What they release is tensor memory alone: a release of
+      // eight warps: two share the lanes and take 16 rows in turn (three are no faster).  (What they release is tensor memory alone: a release of
       // everything would wait for the last tile's stores.)
-      const int half = (warp - 2) >> 2;
+      constexpr int kTurn = 32;
+      const int part = (warp - 2) >> 2;
       float* const mine_g = reinterpret_cast<float*>(epi_g) + (warp - 2) * 16 * 32;
       for (int t = 0; tile(t, x); ++t) {
         const int w0 = x.w0 + (int)rank * kTileW + o, width = min(32, p.a.n - w0);
         const float bias = epi.bias && lane < width ? bf16_to_f(op_ld2(epi.bias + w0 + lane)) : 0.f;
         uint2 ahead[4];  // (the residual is on its way before its results are there)
-        linear_ahead(epi, ahead, x.r0 + 16 * half, x.nr - 16 * half, w0, width, lane);
+        LinearAt at = linear_at<EPI == 2>(p.a, epi, x.r0 + 16 * part, w0, width, lane);
+        linear_ahead(epi, at, ahead, x.nr - 16 * part, width, lane);
         if (EPI == 2) {
           float sum[4][16];
           for (int ks = 0; ks < ksteps; ks += segment, ++na) {
-            const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21) + 16 * half;
+            const uint32_t a = na & 1, acc = tmem + kTileR * a + ((uint32_t)q << 21) + 16 * part;
             wait_pair<try_wait_cluster>(afull(a), (na >> 1) & 1, abort, p.a.status, 4);
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (32 * c + 16 * half < x.nr) {
+              if (32 * c + 16 * part < x.nr) {
                 uint32_t u[16];
                 tmem_ld16(acc + 32 * c, u);
                 tmem_wait16(u);
@@ -479,10 +481,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (32 * c + 16 * half < x.nr) {
-              const int r = 32 * c + 16 * half;
-              if (c > 0) linear_ahead(epi, ahead, x.r0 + r, x.nr - r, w0, width, lane);
-              linear_store<true>(p.a, epi, sum[c], ahead, x.r0 + r, x.nr - r, w0, width, bias, mine_g, lane);
+            if (32 * c + 16 * part < x.nr) {
+              const int r = 32 * c + 16 * part;
+              if (c > 0) {
+                at.out += 8 * at.out4, at.res += 8 * at.res4;
+                linear_ahead(epi, at, ahead, x.nr - r, width, lane);
+              }
+              linear_store<true>(p.a, epi, at, sum[c], ahead, x.r0 + r, x.nr - r, w0, width, bias, mine_g, lane);
             }
           continue;
         }
@@ -491,18 +496,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         tc_fence_after();
         ++na;
         uint32_t u[16];
-        tmem_ld16(acc + 16 * half, u);  // (rows beyond the tile's are other tiles' or nothing's: not stored)
+        tmem_ld16(acc + 16 * part, u);  // (rows beyond the tile's are other tiles' or nothing's: not stored)
         tmem_wait16(u);
-        for (int c = 16 * half; c < x.nr; c += 32) {
+        for (int c = 16 * part; c < x.nr; c += kTurn) {
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-          const bool more = c + 32 < x.nr;
+          const bool more = c + kTurn < x.nr;
           uint2 next[4];
-          if (more) tmem_ld16(acc + c + 32, u);
-          linear_ahead(epi, next, x.r0 + c + 32, x.nr - c - 32, w0, width, lane);
-          linear_store<false>(p.a, epi, v, ahead, x.r0 + c, x.nr - c, w0, width, bias, mine_g, lane);
+          if (more) tmem_ld16(acc + c + kTurn, u);
+          LinearAt then = at;
+          then.out += kTurn / 4 * at.out4, then.res += kTurn / 4 * at.res4;
+          linear_ahead(epi, then, next, x.nr - c - kTurn, width, lane);
+          linear_store<false>(p.a, epi, at, v, ahead, x.r0 + c, x.nr - c, w0, width, bias, mine_g, lane);
           if (more) tmem_wait16(u);
+          at = then;
 #pragma unroll
           for (int i = 0; i < 4; ++i) ahead[i] = next[i];
         }

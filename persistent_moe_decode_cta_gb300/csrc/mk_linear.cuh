@@ -86,18 +86,35 @@ __device__ __forceinline__ void linear_put(const LinearEpi& epi, void* out, long
     }
 }
 
-// A warp's results v[i] = (row r0 + i, output w0 + lane), i < 16, `rows` and `width` of them real: bias and activation in
-// place, then through `stage` (16 x 32 floats of the warp's own) so that eight lanes write 32 outputs of a row side by side.
-// ahead: the residual of the lane's four pieces, from linear_ahead.
-__device__ __forceinline__ void linear_ahead(const LinearEpi& epi, uint2 (&ahead)[4], long long r0, int rows, int w0, int width, int lane) {
-  const int col = 4 * (lane & 7), row = lane >> 3;
+// Where a lane of a warp that stores 16 rows by 32 outputs at a time has its four pieces (rows lane / 8 + 4 j, outputs 4 (lane % 8)
+// on): addresses of the first, bytes from one to the next.  `whole`: 32 outputs that can be read and written four at a time.
+struct LinearAt {
+  uint8_t* out;
+  const uint8_t* res;
+  long long out4, res4;
+  bool whole;
+};
+template <bool WIDE>
+__device__ __forceinline__ LinearAt linear_at(const mk_expert_args& a, const LinearEpi& epi, long long r0, int w0, int width, int lane) {
+  constexpr int kSize = WIDE ? 4 : 2;
+  const long long row = r0 + (lane >> 3), col = w0 + 4 * (lane & 7);
+  return LinearAt{static_cast<uint8_t*>(a.out) + (row * a.out_stride + col) * kSize,
+                  reinterpret_cast<const uint8_t*>(epi.residual + row * epi.residual_stride + col), 4 * a.out_stride * kSize,
+                  4 * epi.residual_stride * 2, epi.vec && width >= 32};
+}
+// the residual of the lane's four pieces
+__device__ __forceinline__ void linear_ahead(const LinearEpi& epi, const LinearAt& at, uint2 (&ahead)[4], int rows, int width, int lane) {
+  if (!epi.residual || !epi.vec) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    ahead[j] = row + 4 * j < rows ? linear_residual(epi, r0 + row + 4 * j, w0 + col, width - col) : make_uint2(0, 0);
+    if ((lane >> 3) + 4 * j < rows && 4 * (lane & 7) < width) ahead[j] = op_ld8(at.res + j * at.res4);
 }
+// A warp's results v[i] = (row r0 + i, output w0 + lane), i < 16, `rows` and `width` of them real: bias and activation in
+// place, then through `stage` (16 x 32 floats of the warp's own) so that eight lanes write 32 outputs of a row side by side.
 template <bool WIDE>
-__device__ __forceinline__ void linear_store(const mk_expert_args& a, const LinearEpi& epi, float (&v)[16], const uint2 (&ahead)[4],
-                                             long long r0, int rows, int w0, int width, float bias, float* stage, int lane) {
+__device__ __forceinline__ void linear_store(const mk_expert_args& a, const LinearEpi& epi, const LinearAt& at, float (&v)[16],
+                                             const uint2 (&ahead)[4], long long r0, int rows, int w0, int width, float bias, float* stage,
+                                             int lane) {
   if (width <= 0) return;
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += bias;
@@ -105,13 +122,29 @@ __device__ __forceinline__ void linear_store(const mk_expert_args& a, const Line
 #pragma unroll
   for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = v[i];
   __syncwarp();
-  const int col = 4 * (lane & 7);
+  const float4* const from = reinterpret_cast<const float4*>(stage) + lane;  // (row lane / 8, four outputs)
+  if (at.whole && rows >= 16) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = (lane >> 3) + 4 * j;
-    const float4 y = *reinterpret_cast<const float4*>(stage + r * 32 + col);
-    const float z[4] = {y.x, y.y, y.z, y.w};
-    if (r < rows) linear_put<WIDE>(epi, a.out, a.out_stride, z, ahead[j], r0 + r, w0 + col, width - col);
+    for (int j = 0; j < 4; ++j) {
+      float4 y = from[j * 32];
+      if (epi.residual) {
+        const float2 lo = bf16x2_to_f2(ahead[j].x), hi = bf16x2_to_f2(ahead[j].y);
+        y.x += lo.x, y.y += lo.y, y.z += hi.x, y.w += hi.y;
+      }
+      if (WIDE)
+        *reinterpret_cast<float4*>(at.out + j * at.out4) = y;
+      else
+        *reinterpret_cast<uint2*>(at.out + j * at.out4) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+  } else {
+    const int col = 4 * (lane & 7);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = (lane >> 3) + 4 * j;
+      const float4 y = from[j * 32];
+      const float z[4] = {y.x, y.y, y.z, y.w};
+      if (r < rows) linear_put<WIDE>(epi, a.out, a.out_stride, z, ahead[j], r0 + r, w0 + col, width - col);
+    }
   }
   __syncwarp();
 }
