@@ -223,7 +223,7 @@ struct VerifyParams {
   mk_verify_args a;
   int grid;        // SMs
   float4* parts;   // [batch][n_nodes][pieces] (largest, sum, index of the largest) of a piece of a row
-  int pieces, batches;  // of a row; of a piece
+  int pieces;      // of a row
 };
 size_t verify_workspace_bytes(const mk_verify_args& a);
 cudaError_t launch_verify(VerifyParams& p, cudaStream_t st);

@@ -17,12 +17,12 @@
 namespace mk {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowValues = 32;  // values a thread
 constexpr int kWalkThreads = 512, kWalkWarps = kWalkThreads / 32;
 constexpr int kWalkCtas = 16;              // of a cluster at most
 constexpr int kFixed = 44;                 // fraction bits of an exponential
 constexpr int kBlock = 128;                // elements that a warp takes at a time: four a lane
-constexpr int kCtaBlocks = 180;            // blocks whose exponentials fit a CTA's shared memory
+constexpr int kWalkSmem = 232448 - 8192;   // dynamic shared memory at most
 
 __device__ __forceinline__ float load_logit(const void* p, long long at, bool f32) {
   return f32 ? op_ldf(static_cast<const float*>(p) + at) : bf16_to_f(op_ld2(static_cast<const uint16_t*>(p) + at));
@@ -83,13 +83,12 @@ struct Peak {
 };
 
 // One block per piece of a row: {largest, sum of exp((l - largest) / T), index of the largest (the lowest; at temperature 0, where
-// the sum only tells whether there is a NaN)}.  HBM bounds it.  float32: four loads a thread and eight blocks an SM (batches that
-// follow one another: 14.3 us in place of 12.4 for 72 rows of 151936).  bf16, with twice the exponentials a byte: batches of two
-// loads, the next one under way while one is added up (11.7 us in place of 13.3 for 96 rows).
+// the sum only tells whether there is a NaN)}.  HBM bounds it.  32 values a thread, all of them on their way at once.  (Half as
+// many: 49 us in place of 42 for the rows of 16 trees of 32 nodes; a ring of bulk copies a warp: 52.)
 template <bool F32>
-__global__ void __launch_bounds__(kRowThreads, F32 ? 8 : 6) row_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int kVec = F32 ? 4 : 8;  // elements of 16 bytes
-  constexpr int kRowLoads = F32 ? 4 : 2;
+  constexpr int kRowLoads = kRowValues / kVec;
   __shared__ Peak s_peak[kRowThreads / 32];
   const int piece = blockIdx.x, node = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -99,59 +98,48 @@ __global__ void __launch_bounds__(kRowThreads, F32 ? 8 : 6) row_kernel(const __g
   const Heat heat(temperature(p.a, b));
   const float beta = heat.hi;
   const bool greedy = heat.t == 0.f, wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-  constexpr int kBatch = kRowThreads * kVec * kRowLoads;
-  const int n = p.a.vocab, end = min(n, (piece + 1) * p.batches * kBatch);
-  int at = piece * p.batches * kBatch + kVec * threadIdx.x;
-  uint4 u[kRowLoads], next[kRowLoads];
-  auto load = [&](uint4 (&to)[kRowLoads], int from) {
+  const int n = p.a.vocab, at = piece * kRowThreads * kRowValues + kVec * threadIdx.x;
+  uint4 u[kRowLoads];
 #pragma unroll
-    for (int i = 0; i < kRowLoads; ++i) {
-      const int j = from + i * kRowThreads * kVec;
-      if (wide && j + kVec <= n) to[i] = op_ld16(row + (long long)j * (F32 ? 4 : 2));
-    }
-  };
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int j = at + i * kRowThreads * kVec;
+    if (wide && j + kVec <= n) u[i] = op_ld16(row + (long long)j * (F32 ? 4 : 2));
+  }
   Peak mine{-INFINITY, 0.f, 0x7fffffff};
-  if (at < end) load(u, at);
-#pragma unroll 1
-  for (; at < end; at += kBatch) {
-    if (!F32 && at + kBatch < end) load(next, at + kBatch);
 #pragma unroll
-    for (int i = 0; i < kRowLoads; ++i) {
-      const int j = at + i * kRowThreads * kVec;
-      float x[kVec];
-      if (wide && j + kVec <= n) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int j = at + i * kRowThreads * kVec;
+    float x[kVec];
+    if (wide && j + kVec <= n) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (F32) {
-            x[k] = __uint_as_float(w[k]);
-          } else {
-            const float2 f = bf16x2_to_f2(w[k]);
-            x[2 * k % kVec] = f.x, x[(2 * k + 1) % kVec] = f.y;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) x[k] = j + k < n ? load_logit(row, j + k, F32) : -INFINITY;
-      }
-      float top = x[0];
-#pragma unroll
-      for (int k = 1; k < kVec; ++k) top = fmaxf(top, x[k]);
-      if (top > mine.top) {
-        mine.sum *= ex2((mine.top - top) * beta);
-        mine.top = top;
-        if (greedy) {
-#pragma unroll
-          for (int k = kVec - 1; k >= 0; --k)
-            if (x[k] == top) mine.arg = j + k;
+      for (int k = 0; k < 4; ++k) {
+        if (F32) {
+          x[k] = __uint_as_float(w[k]);
+        } else {
+          const float2 f = bf16x2_to_f2(w[k]);
+          x[2 * k % kVec] = f.x, x[(2 * k + 1) % kVec] = f.y;
         }
       }
-      const float from = mine.top == -INFINITY ? 0.f : mine.top;
+    } else {
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) mine.sum += ex2((x[k] - from) * beta);
+      for (int k = 0; k < kVec; ++k) x[k] = j + k < n ? load_logit(row, j + k, F32) : -INFINITY;
     }
+    float top = x[0];
 #pragma unroll
-    for (int i = 0; !F32 && i < kRowLoads; ++i) u[i] = next[i];
+    for (int k = 1; k < kVec; ++k) top = fmaxf(top, x[k]);
+    if (top > mine.top) {
+      mine.sum *= ex2((mine.top - top) * beta);
+      mine.top = top;
+      if (greedy) {
+#pragma unroll
+        for (int k = kVec - 1; k >= 0; --k)
+          if (x[k] == top) mine.arg = j + k;
+      }
+    }
+    const float from = mine.top == -INFINITY ? 0.f : mine.top;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) mine.sum += ex2((x[k] - from) * beta);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1)
@@ -274,9 +262,9 @@ struct Part {
 enum { kCut, kDraw, kEnd };
 
 struct WalkShared {
-  Node node[kOpMaxAccept];
-  int path[kOpMaxAccept];
-  int gone[kOpMaxAccept];              // tokens of rejected children (drafts without probabilities)
+  Node* node;                          // [n_nodes], and behind them
+  int* path;                           // [n_nodes]
+  int* gone;                           // [n_nodes] tokens of rejected children (drafts without probabilities)
   Part part[2][kWalkCtas];             // the CTAs' sums, written by each into all
   unsigned long long warp_sum[kWalkWarps];
   Power power[kPowers];
@@ -284,6 +272,8 @@ struct WalkShared {
   int count;                           // (behind t: the two are copied together)
   int step, at, length, n_gone, next;
 };
+
+__host__ __device__ constexpr int node_bytes(int n) { return (n * ((int)sizeof(Node) + 8) + 15) / 16 * 16; }
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -323,8 +313,16 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   const mk_verify_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool f32 = a.logits_float != 0;
+  // (loads that need nothing of one another first)
   int count = node_count(a, b);
   const Heat heat(temperature(a, b));
+  const long long mine_at = (long long)b * a.n_nodes + tid;
+  Node x{};
+  if (tid < a.n_nodes) {
+    x.parent = tid == 0 ? -1 : a.parents ? op_ld(a.parents + mine_at) : tid - 1;
+    x.token = tid == 0 ? 0 : op_ld(a.tokens + mine_at);
+    x.u = op_ldf(a.uniforms + mine_at);
+  }
   if (count < 1 || count > a.n_nodes) {
     if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, count);
     count = 0;
@@ -335,12 +333,6 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   if (tid == 0) sh.count = count, sh.t = heat.t;
   if (tid < count) {
     const int i = tid;
-    const long long at = (long long)b * a.n_nodes + i;
-    Node x{};
-    x.first = x.next = -1;
-    x.parent = i == 0 ? -1 : a.parents ? op_ld(a.parents + at) : i - 1;
-    x.token = i == 0 ? 0 : op_ld(a.tokens + at);
-    x.u = op_ldf(a.uniforms + at);
     bool fine = true;
     if (!(x.u >= 0.f && x.u < 1.f)) {
       op_error(a.status, MK_ERR_INVALID, b, i, __float_as_int(x.u));
@@ -359,11 +351,12 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
     } else {
       x.parent = -1;
     }
-    sh.node[i] = x;
+    Node& to = sh.node[i];  // (top, sum and arg are another warp's)
+    to.parent = x.parent, to.token = x.token, to.first = to.next = -1, to.u = x.u, to.l = x.l, to.q = x.q;
   }
-  __syncthreads();
-  // the pieces of every row
-  for (int i = warp; i < count; i += kWalkWarps) {
+  // the pieces of every row (up to 32 nodes: beside the first warp, which waits for two loads in a row above)
+  const bool beside = count <= 32;
+  for (int i = beside ? warp - 1 : warp; i >= 0 && i < count; i += beside ? kWalkWarps - 1 : kWalkWarps) {
     const float4* part = p.parts + ((long long)b * a.n_nodes + i) * p.pieces;
     Peak mine{-INFINITY, 0.f, 0x7fffffff};
     for (int j = lane; j < p.pieces; j += 32) {
@@ -425,9 +418,10 @@ __device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned 
 // One cluster per sequence.  Every CTA's first thread walks by itself, all of them from the same numbers (the first CTA's copy of the
 // nodes, and sums that each has of all), so that they ask for the same passes and meet at the same barriers.
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_constant__ VerifyParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
+  extern __shared__ __align__(128) uint8_t raw[];
   __shared__ __align__(16) WalkShared sh;
-  unsigned long long* const e = reinterpret_cast<unsigned long long*>(raw);  // the CTA's piece of the row's exponentials
+  // nodes, path, tokens gone; behind them the CTA's piece of the row's exponentials
+  unsigned long long* const e = reinterpret_cast<unsigned long long*>(raw + node_bytes(p.a.n_nodes));
   const mk_verify_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cta_rank(), ctas = cta_count();
@@ -439,6 +433,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   const int first = min(warp * per, mine), n_blocks = min(per, mine - first);       // blocks of this warp
   const int from = first * kBlock + 4 * lane;                                       // first element of this lane in the piece
   for (int i = tid; i < kPowers; i += kWalkThreads) sh.power[i] = powers.v[i];
+  if (tid == 0) {
+    sh.node = reinterpret_cast<Node*>(raw);
+    sh.path = reinterpret_cast<int*>(raw + a.n_nodes * sizeof(Node));
+    sh.gone = sh.path + a.n_nodes;
+  }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -635,7 +634,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     // ------------------------------------------------------------ the first index whose running sum passes u times the whole
     // (u has 24 bits: u 2^64 is exact from 2^-40 on)
     const unsigned long long goal = __umul64hi((unsigned long long)((double)sh.node[0].u * 0x1p64), W);
-    exchange(sh, warp_sum, &parity);  // (the last pass may have been one that did not count)
+    if (stuck) {  // (the last pass did not count)
+      exchange(sh, warp_sum, &parity);
+    }
     unsigned long long sum = 0;
     for (uint32_t i = 0; i < rank; ++i) sum += sh.part[parity ^ 1][i].sum;
     for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
@@ -695,21 +696,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     __syncthreads();
     for (int i = tid; i < a.n_nodes; i += kWalkThreads) a.accepted[(long long)b * a.n_nodes + i] = i < sh.length ? sh.path[i] : -1;
   }
-  walk_sync();  // no CTA leaves while another may write to it or read its nodes
+  // no CTA leaves while another may write to it or read its nodes: not before a barrier behind the last of that, which a pass has had
+  if (row_at < 0) walk_sync();
 }
 
-// Elements of a batch, and batches of a piece: float32 one, bf16 as many as leave about six blocks an SM (a number of blocks, not
-// of SMs: the workspace's size goes by it)
-constexpr int kRowBatch = kRowThreads * 16;
-int row_batches(const mk_verify_args& a) {
-  if (a.logits_float) return 1;
-  const long long in_row = (a.vocab + kRowBatch - 1) / kRowBatch;
-  return (int)std::min(std::max(1ll, (long long)std::max(1, a.batch) * a.n_nodes * in_row / 900), in_row);
-}
-int row_pieces(const mk_verify_args& a) {
-  const int piece = kRowBatch * row_batches(a);
-  return (a.vocab + piece - 1) / piece;
-}
+int row_pieces(const mk_verify_args& a) { return (a.vocab + kRowThreads * kRowValues - 1) / (kRowThreads * kRowValues); }
 
 }  // namespace
 
@@ -719,30 +710,33 @@ size_t verify_workspace_bytes(const mk_verify_args& a) {
 
 cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
   p.parts = static_cast<float4*>(p.a.workspace);
-  p.batches = row_batches(p.a);
   p.pieces = row_pieces(p.a);
   const dim3 grid((unsigned)p.pieces, (unsigned)p.a.n_nodes, (unsigned)p.a.batch);
-  cudaError_t e = p.a.logits_float ? launch_early(row_kernel<true>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<false>, grid, kRowThreads, 0, st, p);
   static std::atomic<unsigned long long> done{0}, done16{0};
-  static std::atomic<int> known[3][64];
-  constexpr int kSmem = kCtaBlocks * kBlock * 8;
-  if (e == cudaSuccess) e = allow_smem(walk_kernel, kSmem, done);
+  cudaError_t e = p.a.logits_float ? launch_early(row_kernel<true>, grid, kRowThreads, 0, st, p) : launch_early(row_kernel<false>, grid, kRowThreads, 0, st, p);
+  constexpr int kSizes = 8;
+  static std::atomic<int> known[kSizes][64];
+  if (e == cudaSuccess) e = allow_smem(walk_kernel, kWalkSmem, done);
   if (e == cudaSuccess) e = allow_wide_clusters(walk_kernel, done16);
-  // the largest clusters that fit the GPU all at once (7 of 16 CTAs, 8 of 12, 13 of 10, 15 of 8), at least as many CTAs as a row's
-  // exponentials need for their shared memory
-  const int blocks = (p.a.vocab + kBlock - 1) / kBlock;
-  const int sizes[4] = {16, 12, 10, 8}, least = blocks > 8 * kCtaBlocks ? 16 : 8;
-  int ctas = least;
-  for (int i = 0; e == cudaSuccess && blocks > 256 && i < 3 && sizes[i] > least; ++i) {
+  // CTAs of a cluster: a walk takes about 13 us and 1 more for every 12 blocks of a CTA's piece of the row (151936: 21 us in clusters
+  // of 8, 18 in 12).  Where the clusters do not fit the GPU all at once (7 of 16 CTAs do, 15 of 8, 23 of 6) the last ones start as
+  // the first end, which are not equally long (16 trees of 32 nodes: 95 us in clusters of 8, 107 in 6)
+  static const int sizes[kSizes] = {16, 12, 10, 8, 6, 4, 2, 1};
+  const int blocks = (p.a.vocab + kBlock - 1) / kBlock, nodes = node_bytes(p.a.n_nodes);
+  int ctas = 0;
+  double least = 0;
+  for (int i = 0; e == cudaSuccess && i < kSizes; ++i) {
+    const int piece = (blocks + sizes[i] - 1) / sizes[i];
+    if (nodes + piece * kBlock * 8 > kWalkSmem) continue;
     int fit = 0;
-    e = active_clusters(walk_kernel, sizes[i], kWalkThreads, kSmem, known[i], &fit);
-    if (p.a.batch <= fit) {
-      ctas = sizes[i];
-      break;
-    }
+    e = active_clusters(walk_kernel, sizes[i], kWalkThreads, kWalkSmem, known[i], &fit);
+    if (e != cudaSuccess || fit < 1) continue;
+    const double cost = std::max(1.0, (double)p.a.batch / fit) * (13 + piece / 12.0);
+    if (!ctas || cost < least) least = cost, ctas = sizes[i];
   }
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
+  if (!ctas) return cudaErrorInvalidConfiguration;
+  const size_t smem = nodes + (size_t)((blocks + ctas - 1) / ctas) * kBlock * 8;
   return launch_clusters(walk_kernel, dim3((unsigned)(p.a.batch * ctas)), ctas, kWalkThreads, smem, st, p);
 }
 
