@@ -22,8 +22,10 @@ namespace mk {
 namespace {
 
 // ------------------------------------------------------------------------------------------ router
-// A cluster of 8 CTAs has TT tokens and an eighth of the experts a CTA.  A selection can hang on the last bits of two scores, so
-// these are sums of exact products (two bf16 factors fit fp32) with the rounding errors of the additions carried along.
+// A cluster of 8 CTAs has TT tokens and an eighth of the experts a CTA.  A selection can hang on the last bits of two scores.  So
+// the fp32 scores come with a bound of their error, and those that lie within it of one another around the selection (one token in
+// twenty has such) are computed once more from exact products (two bf16 factors fit fp32), the errors of all additions carried
+// along.  (All scores that way: 128 tokens 19 us; every sum of four terms that way, 25.)
 constexpr int kRouterCtas = 8, kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
 
 // (hi, lo) += v, the error of hi + v to lo; two sums at once
@@ -43,6 +45,41 @@ __device__ __forceinline__ uint64_t pair_of(uint32_t bf16x2) {
   const float2 f = bf16x2_to_f2(bf16x2);
   return pack2(f.x, f.y);
 }
+// (a, b) = the two sums of all lanes together (the same in every lane: addition and its error are symmetric)
+__device__ __forceinline__ void add_lanes(uint64_t hi, uint64_t lo, float& a, float& b) {
+  const float2 h = unpack2(hi), l = unpack2(lo);
+  a = h.x, b = l.x + l.y;
+  add_exact(a, b, h.y);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+    add_exact(a, b, a2);
+    b += b2;
+  }
+}
+// w . x by a warp, to 2^-46 of the sum of the terms' sizes (the same in every lane)
+__device__ __noinline__ double exact_score(const uint16_t* w, const uint4* x, int vecs) {
+  uint64_t hi = 0, lo = 0;
+  for (int v0 = threadIdx.x & 31; v0 < vecs; v0 += 256) {
+    uint4 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (v0 + 32 * i < vecs) u[i] = op_ld16(w + 8 * (v0 + 32 * i));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (v0 + 32 * i < vecs) {
+        const uint4 y = x[v0 + 32 * i];
+        add_exact2(hi, lo, mul2(pair_of(u[i].x), pair_of(y.x)));
+        add_exact2(hi, lo, mul2(pair_of(u[i].y), pair_of(y.y)));
+        add_exact2(hi, lo, mul2(pair_of(u[i].z), pair_of(y.z)));
+        add_exact2(hi, lo, mul2(pair_of(u[i].w), pair_of(y.w)));
+      }
+  }
+  float a, b;
+  add_lanes(hi, lo, a, b);
+  // (infinities and NaN: the carried errors are NaN, the sum itself tells)
+  return fabsf(a) < INFINITY ? (double)a + (double)b : (double)a;
+}
 
 // order of scores as unsigned integers; NaN above everything, the two zeros equal
 __device__ __forceinline__ unsigned long long score_key(double d) {
@@ -51,16 +88,30 @@ __device__ __forceinline__ unsigned long long score_key(double d) {
   return v < 0 ? ~(unsigned long long)v : (unsigned long long)v | (1ull << 63);
 }
 
+struct RouterShared {
+  float2 score[kOpMaxExperts];           // of the token that this CTA selects for, and what it may be off by
+  unsigned long long key[kOpMaxExperts];
+  int rank[kOpMaxExperts];
+  uint32_t close[kOpMaxExperts / 32];    // experts whose scores are not told apart
+  float xn[kRouterWarps];                // parts of the token's square
+  float bound;                           // the score of rank K
+  int most, odd;                         // bits of the largest error; whether something is infinite or NaN
+  int chosen[kMoeTopK];
+  float value[kMoeTopK];
+};
+
 template <int TT>
 __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThreads) router_kernel(const __grid_constant__ MoeParams p) {
-  __shared__ double s_score[kOpMaxExperts];  // of the token that this CTA selects for
   extern __shared__ __align__(16) uint8_t raw_x[];  // the tokens' rows
+  __shared__ RouterShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int t0 = (int)(blockIdx.x / kRouterCtas) * TT, E = p.a.n_experts, d = p.a.d_model;
   const int per = (E + kRouterCtas - 1) / kRouterCtas, e0 = (int)rank * per, e1 = min(E, e0 + per);
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (all CTAs have started: waited for below)
+  if (tid < kOpMaxExperts / 32) sh.close[tid] = 0;
+  if (tid == 0) sh.most = sh.odd = 0;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && tid < 4) p.sync[tid] = 0;
@@ -69,7 +120,8 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
   // (the first weights are on their way while the tokens' rows come in)
   constexpr int U = TT <= 2 ? 8 : 4;
   uint4 u[U];
-  const uint16_t* w = static_cast<const uint16_t*>(p.a.router) + (long long)min(e0 + warp, E - 1) * d;
+  const uint16_t* const router = static_cast<const uint16_t*>(p.a.router);
+  const uint16_t* w = router + (long long)min(e0 + warp, E - 1) * d;
   auto fetch = [&](int v) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -85,12 +137,12 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   for (int e = e0 + warp; e < e1; e += kRouterWarps) {
-    uint64_t hi[TT], lo[TT];
+    uint64_t sum[TT], ww = 0;  // products; the row's square
 #pragma unroll
-    for (int j = 0; j < TT; ++j) hi[j] = lo[j] = 0;
+    for (int j = 0; j < TT; ++j) sum[j] = 0;
     for (int v = lane; v < vecs; v += 32 * U) {
       if (e != e0 + warp || v != lane) {
-        if (v == lane) w = static_cast<const uint16_t*>(p.a.router) + (long long)e * d;
+        if (v == lane) w = router + (long long)e * d;
         fetch(v);
       }
 #pragma unroll
@@ -98,73 +150,122 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
         if (v + 32 * i < vecs) {
           const uint64_t w4[4] = {pair_of(u[i].x), pair_of(u[i].y), pair_of(u[i].z), pair_of(u[i].w)};
 #pragma unroll
+          for (int k = 0; k < 4; ++k) ww = fma2(w4[k], w4[k], ww);
+#pragma unroll
           for (int j = 0; j < TT; ++j) {
             const uint4 y = x[j * vecs + v + 32 * i];
-            add_exact2(hi[j], lo[j], mul2(w4[0], pair_of(y.x)));
-            add_exact2(hi[j], lo[j], mul2(w4[1], pair_of(y.y)));
-            add_exact2(hi[j], lo[j], mul2(w4[2], pair_of(y.z)));
-            add_exact2(hi[j], lo[j], mul2(w4[3], pair_of(y.w)));
+            sum[j] = fma2(w4[3], pair_of(y.w), fma2(w4[2], pair_of(y.z), fma2(w4[1], pair_of(y.y), fma2(w4[0], pair_of(y.x), sum[j]))));
           }
         }
     }
+    const float2 w2 = unpack2(ww);
+    float wn = w2.x + w2.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) wn += __shfl_xor_sync(0xffffffffu, wn, o);
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-      const float2 h = unpack2(hi[j]), l = unpack2(lo[j]);
-      float a = h.x, b = l.x + l.y;
-      add_exact(a, b, h.y);
+      const float2 s2 = unpack2(sum[j]);
+      float s = s2.x + s2.y;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
-        // (the same on both sides of an exchange: addition and its error are symmetric)
-        add_exact(a, b, a2);
-        b += b2;
-      }
-      // infinities and NaN: the carried errors are NaN, the sum itself tells
-      const double s = fabsf(a) < INFINITY ? (double)a + (double)b : (double)a;
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == 0) {
         uint32_t to;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(s_score + e)), "r"(j));
-        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(__double_as_longlong(s)) : "memory");
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(sh.score + e)), "r"(j));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(s), "f"(wn) : "memory");
       }
     }
   }
+  const int t = t0 + (int)rank, K = p.a.top_k;
+  const bool mine_to_select = (int)rank < TT && t < p.a.n_tokens;
+  if (mine_to_select) {
+    float n = 0.f;
+    for (int v = tid; v < vecs; v += kRouterThreads) {
+      const uint4 y = x[rank * vecs + v];
+      const uint32_t y4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = bf16x2_to_f2(y4[k]);
+        n = fmaf(f.x, f.x, fmaf(f.y, f.y, n));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) sh.xn[warp] = n;
+  }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int t = t0 + (int)rank;
-  if (warp != 0 || (int)rank >= TT || t >= p.a.n_tokens) return;
-  constexpr int kMine = kOpMaxExperts / 32;
-  unsigned long long key[kMine];
+  if (!mine_to_select) return;
+  // A lane adds d / 64 terms (up to 4 more of a step that is not whole) to each of two sums, and 6 additions join them: each is off
+  // by 2^-24 of what it adds to at most, |w| |x| in all at most; 1.001 and 2^-120 cover the norms' own roundings and denormals.
+  float xn = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < E ? score_key(s_score[e]) : 0;  // (no score's key is 0)
+  for (int i = 0; i < kRouterWarps; ++i) xn += sh.xn[i];
+  const float unit = (d / 64 + 12) * 0x1p-24f * 1.001f * sqrtf(xn);
+  if (tid < kOpMaxExperts) {
+    const float off = tid < E ? unit * sqrtf(sh.score[tid].y) + 0x1p-120f : 0.f;
+    if (tid < E) sh.score[tid].y = off;
+    const int most = __reduce_max_sync(0xffffffffu, __float_as_int(off));  // (not negative: in the order of the bits)
+    const bool odd = tid < E && !(fabsf(sh.score[tid].x) < INFINITY && off < INFINITY);
+    if (lane == 0) atomicMax(&sh.most, most);
+    if (odd) sh.odd = 1;
   }
-  int id = 0;
-  double first = 0;
-  float mine = 0.f, total = 0.f;
-  for (int j = 0; j < p.a.top_k; ++j) {
-    unsigned long long best = key[0];
-#pragma unroll
-    for (int i = 1; i < kMine; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-    const uint32_t low = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == top ? (uint32_t)best : 0u);
-    best = (unsigned long long)top << 32 | low;
-    int where = kOpMaxExperts;
-#pragma unroll
-    for (int i = kMine - 1; i >= 0; --i)
-      if (key[i] == best) where = lane + 32 * i;
-    where = __reduce_min_sync(0xffffffffu, where);
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      if (lane + 32 * i == where) key[i] = 0;
-    const double s = s_score[where];
-    if (j == 0) first = s;
-    const float c = expf((float)(s - first));
-    total += c;
-    if (lane == j) id = where, mine = c;
+  __syncthreads();
+  // An expert's rank: how many come before it; and whether another's score is too close to tell.  (Two threads an expert, or four
+  // where there are few.)
+  const int share = kRouterThreads / kOpMaxExperts * (E <= kOpMaxExperts / 2 ? 2 : 1);
+  const int e = tid / share, part = tid % share;
+  const float2 mine = sh.score[min(e, E - 1)];
+  int n = 0, near = 0;
+#pragma unroll 4
+  for (int f = part; f < E; f += share) {
+    const float2 other = sh.score[f];
+    n += other.x > mine.x || (other.x == mine.x && f < e);
+    near |= f != e && !(fabsf(mine.x - other.x) > mine.y + other.y);
   }
-  if (lane < p.a.top_k) {
-    p.ids[t * p.a.top_k + lane] = id;
-    p.weights[t * p.a.top_k + lane] = mine / total;
+  for (int o = share / 2; o; o >>= 1) {
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+    near |= __shfl_xor_sync(0xffffffffu, near, o);
+  }
+  if (part == 0 && e < E) {
+    sh.rank[e] = n;
+    if (n == K) sh.bound = mine.x;
+  }
+  __syncthreads();
+  // Only those that may be among the first K count: not below the score of rank K by more than twice the largest error.  (Where there
+  // is no such rank, or NaN among the scores, all of them.)
+  near = near && e < E && (sh.odd || K >= E || mine.x >= sh.bound - 2.f * __int_as_float(sh.most));
+  if (near && part == 0) atomicOr(sh.close + (e >> 5), 1u << (e & 31));
+  if (__syncthreads_or(near)) {
+    for (int i = tid; i < E; i += kRouterThreads) sh.key[i] = score_key((double)sh.score[i].x);
+    __syncthreads();
+    int turn = 0;
+    for (int i0 = 0; i0 < E; i0 += 32)
+      for (uint32_t left = sh.close[i0 >> 5]; left; left &= left - 1, turn = (turn + 1) % kRouterWarps)
+        if (turn == warp) {
+          const int i = i0 + __ffs(left) - 1;
+          const double s = exact_score(router + (long long)i * d, x + rank * vecs, vecs);
+          if (lane == 0) sh.key[i] = score_key(s), sh.score[i].x = (float)s;
+        }
+    __syncthreads();
+    n = 0;
+    const unsigned long long key = sh.key[min(e, E - 1)];
+    for (int f = part; f < E; f += share) {
+      const unsigned long long other = sh.key[f];
+      n += other > key || (other == key && f < e);
+    }
+    for (int o = share / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (part == 0 && e < E) sh.rank[e] = n;
+    __syncthreads();
+  }
+  if (tid < E && sh.rank[tid] < K) {
+    sh.chosen[sh.rank[tid]] = tid;
+    sh.value[sh.rank[tid]] = sh.score[tid].x;
+  }
+  __syncthreads();
+  if (tid < K) {
+    float total = 0.f;
+    for (int j = 0; j < K; ++j) total += __expf(sh.value[j] - sh.value[0]);
+    p.ids[t * K + tid] = sh.chosen[tid];
+    p.weights[t * K + tid] = __expf(sh.value[tid] - sh.value[0]) / total;
   }
 }
 
@@ -442,7 +543,6 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   fence_proxy_async_smem();  // which also write to where x was)
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
     if (made) red_release(p.sync + 1, made);
     const uint64_t t0 = gtime();
     while (ld_acquire(p.sync + 1) != (unsigned)units)
@@ -655,7 +755,7 @@ void moe_shape(MoeParams& p) {
 }
 
 cudaError_t launch_moe_router(const MoeParams& p, cudaStream_t st) {
-  const int t = p.a.n_tokens, clusters = 2 * p.grid / kRouterCtas;
+  const int t = p.a.n_tokens, clusters = std::max(1, p.grid / kRouterCtas);  // (one CTA an SM)
   const cudaError_t e = t <= clusters       ? launch_router<1>(p, st)
                         : t <= 2 * clusters ? launch_router<2>(p, st)
                         : t <= 4 * clusters ? launch_router<4>(p, st)

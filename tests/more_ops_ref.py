@@ -66,9 +66,11 @@ def select(s, k):
 
 def moe(x, router, gate, up, down, k, residual=None):
     """(out, bound, ids, weights).  Gate and up as sums of k exact products (2^-23 of sum |x||w| each); their product with the
-    weight is rounded to bf16 (2^-8); the second sums likewise, and one rounding of the result.  A weight comes from scores that
-    are exact and an fp32 softmax: 2^-20."""
+    weight is rounded to bf16 (2^-8); the second sums likewise, and one rounding of the result.  A weight comes from fp32 scores,
+    off by (d / 64 + 12) 2^-24 |w| |x| at most, which changes it by twice that, and an fp32 softmax: 2^-20."""
     ids, c = select(scores(x, router), k)
+    off_c = 2 * (x.shape[1] / 64 + 12) * 2.0 ** -24 * float(x.double().norm(dim=1).max() * router.double().norm(dim=1).max())
+    off_c = off_c if math.isfinite(off_c) else 0.0
     x = x.double()
     t, d = x.shape
     f = gate.shape[1]
@@ -84,7 +86,7 @@ def moe(x, router, gate, up, down, k, residual=None):
         s = g * torch.sigmoid(g)
         w = c[rows, slot][:, None]
         h = w * s * u
-        dh = w * (1.1 * dg * u.abs() + s.abs() * du + dg * du) + (2.0 ** -17 + R.HALF_BF16) * h.abs()
+        dh = w * (1.1 * dg * u.abs() + s.abs() * du + dg * du) + (off_c + 2.0 ** -17 + R.HALF_BF16) * h.abs()
         out[rows] += h @ de.T
         off[rows] += dh @ de.abs().T
         size[rows] += h.abs() @ de.abs().T
