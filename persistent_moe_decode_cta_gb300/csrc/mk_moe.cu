@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   int iu = 0, is = 0, irow = 0, end = 0;  // the issuing side: unit, step, first row; end of the run
   auto unit_row = [&](int u) {
     const int a = u / groups;
-    return sh.act[a] * f + 8 * (u - a * groups);
+    return (int)uniform(sh.act[a] * f + 8 * (u - a * groups));
   };
   // Second product.  Blocks of output columns, this CTA's one after another; the warps deal out the steps of all experts.
   struct Down {
@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   const uint32_t h_at = rows_at + warp * (S * NT * 2048);
 
   auto issue_weights = [&]() {
+    const int row = (int)uniform(sh.act[id.a] * d + id.block * p.width);
     if (elect_one()) {
       const uint32_t bar = bars + 8 * put, dst = tiles_at + put * kTileBytes;
-      const int row = sh.act[id.a] * d + id.block * p.width;
       mbar_expect_tx(bar, down_bytes);
       tma_box(dst, &tdown, id.s * kStepK, row, bar);
       tma_box(dst + kTileBytes / 2, &tdown, id.s * kStepK + kSpan, row, bar);

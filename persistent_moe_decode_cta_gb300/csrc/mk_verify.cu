@@ -188,8 +188,7 @@ __device__ __forceinline__ int low_bits(float v) { return __float_as_int(v) - 0x
 
 // exp((l - top) / T) in units of 2^-44 of two logits at once, for finite l <= top to 2^-41 of itself; 0 for anything else.  top: the
 // row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.)
-// One copy of the code: a cold kernel waits for its instructions longer than it runs them.
-__device__ __noinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const Power* table) {
+__device__ __forceinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const Power* table) {
   const uint64_t minus = both(-1.f), l = pack2(l0, l1), b = both(bh);
   // l - top as dh + dl, exactly; times log2(e) / T as ph + pl
   const uint64_t dh = add2(l, both(-top)), z = fma2(l, minus, dh);
@@ -217,11 +216,15 @@ __device__ __noinline__ U2 exp_fixed(float l0, float l1, float top, float bh, fl
   return U2{pf.x >= -50.f ? ((v0 >> ((51 - kFixed - (k0 >> 8)) & 63)) + 1) >> 1 : 0ull,
             pf.y >= -50.f ? ((v1 >> ((51 - kFixed - (k1 >> 8)) & 63)) + 1) >> 1 : 0ull};
 }
+// (of single logits: one copy of the code, since a cold kernel waits for its instructions longer than it runs them)
+__device__ __noinline__ unsigned long long exp_one(float l, float top, float bh, float bl, const Power* table) {
+  return exp_fixed(l, l, top, bh, bl, table).x;
+}
 struct Exp {
   float top, bh, bl;
   const Power* table;
   __device__ __forceinline__ U2 operator()(float l0, float l1) const { return exp_fixed(l0, l1, top, bh, bl, table); }
-  __device__ __forceinline__ unsigned long long operator()(float l) const { return exp_fixed(l, l, top, bh, bl, table).x; }
+  __device__ __forceinline__ unsigned long long operator()(float l) const { return exp_one(l, top, bh, bl, table); }
 };
 
 // (E - q A)+ with A = ah + am (to 2^-48 of itself), all in units of 2^-44, of two probabilities at once
