@@ -422,7 +422,7 @@ int mk_linear(const mk_linear_args* a, void* stream) {
   const int size = a->out_float ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(a->out) % size || reinterpret_cast<uintptr_t>(a->bias) % 2 || reinterpret_cast<uintptr_t>(a->residual) % 2)
     return op_fail(MK_ERR_INVALID, "out, bias and residual must be aligned to their values");
-  if (((long long)a->m / 128 + 1) * (((long long)a->n + 255) / 256) >= 0x7fffffffll - 1024)
+  if (((long long)a->m / 64 + 1) * (((long long)a->n + 255) / 256) >= 0x7fffffffll - 1024)
     return op_fail(MK_ERR_UNSUPPORTED, "more than 2^31 tiles");
   const Rows out = rows_of(a->out, a->m, a->n, a->out_stride, size);
   if (overlap(out, rows_of(a->x, a->m, a->k, a->x_stride, 2)) || overlap(out, rows_of(a->w, a->n, a->k, a->k, 2)) ||

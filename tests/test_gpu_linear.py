@@ -152,3 +152,12 @@ def test_offsets_beyond_32_bits():
     x.copy_(R.bf16(g, 3, 128))
     w = R.bf16(g, 64, 128, std=0.1)
     R.assert_close(ops.linear(x, w), *M.linear(x, w))
+    # ... of the result and the residual, in both forms of the product
+    for n in (64, 20000):
+        stride = (1 << 31) // 2 + 20000
+        big = torch.empty(2 * stride + 20000, dtype=torch.bfloat16, device="cuda")
+        both = torch.as_strided(big, (3, n), (stride, 1))
+        both.copy_(R.bf16(g, 3, n))
+        x, w, before = R.bf16(g, 3, 64), R.bf16(g, n, 64, std=0.1), both.clone()
+        ops.linear(x, w, residual=both, out=both)
+        R.assert_close(both, *M.linear(x, w, None, None, before))

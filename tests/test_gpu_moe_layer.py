@@ -171,3 +171,9 @@ def test_many_calls_side_by_side():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     ops.check_status()
+
+
+@pytest.mark.parametrize("t", [2, 18])
+def test_weights_beyond_32_bits(t):
+    """More than 2^32 bytes in each of the experts' tensors."""
+    check(t, 40, 2, 8192, 8192)

@@ -221,3 +221,28 @@ def test_many_sequences():
     g = R.gen(77)
     logits, tokens, uniforms, parents, draft = M.tree_inputs(g, 70, 4, 20000, True, True)
     check(logits, tokens, uniforms, parents, draft)
+
+
+def test_offsets_beyond_32_bits():
+    """Sequences whose rows lie further than 2^32 bytes apart."""
+    g = R.gen(78)
+    for half in (True, False):
+        logits, tokens, uniforms, parents, draft = M.tree_inputs(g, 3, 4, 900, True, True, half=half)
+        stride = (1 << 31) // logits.element_size() + 4096
+        far = torch.as_strided(torch.empty(2 * stride + 4 * 900, dtype=logits.dtype, device="cuda"), logits.shape, (stride, 900, 1))
+        far.copy_(logits)
+        apart = (1 << 30) // 2 + 1024
+        q = torch.as_strided(torch.empty(2 * apart + 4 * 900, device="cuda"), draft.shape, (apart, 900, 1))
+        q.copy_(draft)
+        check(far, tokens, uniforms, parents, q)
+
+
+def test_a_long_chain_and_deep_tree():
+    """As many nodes as a call takes."""
+    g = R.gen(79)
+    for tree in (False, True):
+        logits, tokens, uniforms, parents, draft = M.tree_inputs(g, 2, 512, 257, tree, True, sharp=30.0)
+        uniforms[:, 1:] *= 0.3
+        check(logits, tokens, uniforms, parents, draft)
+        path = check(logits, tokens, uniforms * 0, parents, draft)   # (whatever may be drafted at all is accepted)
+        assert tree or path == [list(range(512))] * 2
