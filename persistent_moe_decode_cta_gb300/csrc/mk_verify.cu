@@ -1,11 +1,11 @@
 // Verification of drafted tokens.  A child i with token x of node v is accepted if u_i q(x) < r(x), where r = p at first and
 // r <- (r - q)+ / sum (r - q)+ after a rejection; the next token is drawn from what is left where no child is accepted.
 //
-// Two kernels.  row_kernel reads every node's logits once, in pieces, for the largest and the sum of the exponentials: all
-// that the tests of first children need beside two numbers a child.  walk_kernel has a cluster of CTAs per sequence that walks
-// from the root: an accepted child costs no more than a look at shared memory; at the first rejection in a row (or at the
-// last node) the cluster reads that row again, out of L2, and from then on keeps the row's exponentials in shared memory, a
-// piece a CTA.  The drafting model's rows are read only where one of its tokens was rejected.
+// Two kernels.  row_kernel reads the logits of every node that has children once, in pieces, for the largest and the sum of the
+// exponentials: all that the tests of first children need beside two numbers a child.  walk_kernel has a cluster of CTAs per
+// sequence that walks from the root: an accepted child costs no more than a look at shared memory; at the first rejection in a
+// row (or at the last node) the cluster reads that row, out of L2 where it has been read, and from then on keeps the row's
+// exponentials in shared memory, a piece a CTA.  The drafting model's rows are read only where one of its tokens was rejected.
 //
 // Numbers.  The drawn token is where a running sum over up to 2^18 probabilities passes u times the whole: errors of fp32 would
 // move borders enough to change one draw of a few hundred.  So the exponentials of the walk are 64-bit integers (2^-44 of the
@@ -93,7 +93,13 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const int piece = blockIdx.x, node = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  if (node >= node_count(p.a, b)) return;
+  const int count = node_count(p.a, b);
+  if (node >= count) return;
+  // a node without children: its row matters only where the walk ends there, and the walk looks at it by itself
+  bool inner = !p.a.parents && node + 1 < count;
+  if (p.a.parents)
+    for (int j = node + 1 + lane; j < min(count, p.a.n_nodes); j += 32) inner |= op_ld(p.a.parents + (long long)b * p.a.n_nodes + j) == node;
+  if (!__any_sync(0xffffffffu, inner)) return;
   const uint8_t* const row = static_cast<const uint8_t*>(logit_row(p.a, b, node));
   const Heat heat(temperature(p.a, b));
   const float beta = heat.hi;
@@ -399,8 +405,9 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   }
 }
 
-// The sum of what the warps of all CTAs hand in.  (Two sets in turn: a CTA may write the next pass's sums while another still reads
+// The sum, or the largest, of what the warps of all CTAs hand in.  (Two sets in turn: a CTA may write the next pass's sums while another still reads
 // this one's, but no CTA is two barriers ahead.)
+template <bool LARGEST = false>
 __device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned long long warp_sum, int* parity) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ctas = cta_count(), rank = cta_rank();
@@ -408,12 +415,12 @@ __device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned 
   __syncthreads();
   if (threadIdx.x < ctas) {
     unsigned long long mine = 0;
-    for (int i = 0; i < kWalkWarps; ++i) mine += sh.warp_sum[i];
+    for (int i = 0; i < kWalkWarps; ++i) mine = LARGEST ? max(mine, sh.warp_sum[i]) : mine + sh.warp_sum[i];
     put64(map_cta(&sh.part[*parity][rank], threadIdx.x), mine);
   }
   walk_sync();
   unsigned long long total = 0;
-  for (uint32_t i = 0; i < ctas; ++i) total += sh.part[*parity][i].sum;
+  for (uint32_t i = 0; i < ctas; ++i) total = LARGEST ? max(total, sh.part[*parity][i].sum) : total + sh.part[*parity][i].sum;
   *parity ^= 1;
   return total;
 }
@@ -485,14 +492,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           child = v.first;
           n_gone = 0;
           whole = true;
-          if (!(fabsf(v.top) < INFINITY && v.sum > 0.f)) {  // (a NaN in the row is a NaN in the sum)
+          // (a NaN in the row is a NaN in the sum.  Nothing is known of a row without children.)
+          if (child >= 0 && !(fabsf(v.top) < INFINITY && v.sum > 0.f)) {
             if (rank == 0) op_error(a.status, MK_ERR_INVALID, b, at, __float_as_int(v.top));
             step = kEnd;
             sh.next = -1;
           }
         } else if (child < 0) {
           step = kDraw;
-          if (heat.t == 0.f) {
+          if (heat.t == 0.f && sh.node[at].first >= 0) {
             step = kEnd;
             sh.next = sh.node[at].arg;
           }
@@ -548,7 +556,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     if (!loaded) {
       const void* const row = logit_row(a, b, at);
       const bool wide = is_wide(row, f32);
-      ex.top = sh.node[at].top;
       // (all copies first, each into the first half of what the lane turns it into: lanes wait for their own only.  Rolled loops:
       // unrolled, the code of a pass that runs once is fetched for longer than it runs.)
       if (wide) {
@@ -571,21 +578,54 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           if (lane % 8 == 0 && j < a.vocab) asm volatile("prefetch.global.L2 [%0];" ::"l"(drow + j) : "memory");
         }
       op_cp_wait_all();
+      auto logits = [&](int k) {
+        const int j = base + from + k * kBlock;
+        if (!wide || j + 4 > a.vocab) return load4(row, j, a.vocab, f32, false, -INFINITY);
+        const float4 v = *reinterpret_cast<const float4*>(e + from + k * kBlock);
+        if (f32) return v;
+        const float2 lo = bf16x2_to_f2(__float_as_uint(v.x)), hi = bf16x2_to_f2(__float_as_uint(v.y));
+        return make_float4(lo.x, lo.y, hi.x, hi.y);
+      };
+      if (sh.node[at].first < 0) {
+        // the largest logit and its index (the lowest), as one number: what is larger, and of equal ones what comes first, is larger
+        float top = -INFINITY;
+        int arg = 0;
+        bool odd = false;
+#pragma unroll 1
+        for (int k = 0; k < n_blocks; ++k) {
+          const float4 v = logits(k);
+          const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            odd |= !(x[i] < INFINITY);
+            if (x[i] > top) top = x[i], arg = base + from + k * kBlock + i;
+          }
+        }
+        const uint32_t bits = __float_as_uint(top + 0.f);  // (one zero)
+        unsigned long long key = (unsigned long long)(bits >> 31 ? ~bits : bits | 0x80000000u) << 32 | (uint32_t)~arg;
+        if (odd) key = ~0ull;  // (NaN or infinite)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+        key = exchange<true>(sh, key, &parity);
+        const uint32_t high = (uint32_t)(key >> 32);
+        top = key == ~0ull ? INFINITY : __uint_as_float(high >> 31 ? high & 0x7fffffffu : ~high);
+        ex.top = top;
+        if (!(fabsf(top) < INFINITY) || heat.t == 0.f) {
+          if (tid == 0) {
+            sh.next = fabsf(top) < INFINITY ? (int)~(uint32_t)key : -1;
+            if (rank == 0 && sh.next < 0) op_error(a.status, MK_ERR_INVALID, b, at, __float_as_int(top));
+          }
+          break;
+        }
+      } else {
+        ex.top = sh.node[at].top;
+      }
       unsigned long long sum = 0;
 #pragma unroll 1
       for (int k = 0; k < n_blocks; ++k) {
         const int j = base + from + k * kBlock;
         ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + from + k * kBlock);
-        float4 v;
-        if (wide && j + 4 <= a.vocab) {
-          v = *reinterpret_cast<const float4*>(to);
-          if (!f32) {
-            const float2 lo = bf16x2_to_f2(__float_as_uint(v.x)), hi = bf16x2_to_f2(__float_as_uint(v.y));
-            v = make_float4(lo.x, lo.y, hi.x, hi.y);
-          }
-        } else {
-          v = load4(row, j, a.vocab, f32, false, -INFINITY);
-        }
+        const float4 v = logits(k);
         const U2 lo = ex(v.x, v.y), hi = ex(v.z, v.w);
         unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
         for (int g = 0; g < gone; ++g) {
