@@ -250,3 +250,48 @@ def test_a_long_chain_and_deep_tree():
         sure[:, 0] = uniforms[:, 0]
         path = check(logits, tokens, sure, parents, draft)
         assert tree or path == [list(range(512))] * 2
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "empty"])
+def test_bad_rows_where_the_walk_ends(bad):
+    """The row of a node without children."""
+    g = R.gen(90)
+    logits, tokens, uniforms, parents, draft = M.tree_inputs(g, 3, 6, 300, False, True)
+    uniforms[:, 1:] = 0.0
+    want, drawn = M.verify(logits, tokens, uniforms, parents, draft)
+    if bad == "empty":
+        logits[1, 5] = -float("inf")
+    else:
+        logits[1, 5, 299] = float(bad)
+    for temperature in (None, torch.tensor([1.0, 0.0, 1.0], device="cuda")):
+        status = ops.new_status()
+        if temperature is not None:
+            tokens[1, 1:] = logits[1, :5].argmax(-1).to(torch.int32)
+        accepted, nxt = ops.verify_nodes(logits, tokens, uniforms, parents=parents, draft_probs=draft, temperature=temperature, status=status)
+        assert status[:3].tolist() == [B.MK_ERR_INVALID, 1, 5]
+        assert accepted.tolist() == want and want[1] == list(range(6))
+        assert int(nxt[1]) == -1 and [int(nxt[0]), int(nxt[2])] == [drawn[0], drawn[2]]
+
+
+def test_little_left_behind_a_rejection():
+    """Drafts from all but the target's own distribution: what a rejection leaves is small beside what it takes away."""
+    for seed in range(6):
+        g = R.gen(91 + seed)
+        logits, tokens, uniforms, parents, _ = M.tree_inputs(g, 4, 12, 700, True, False)
+        draft = (logits + 1e-4 * torch.randn(logits.shape, generator=g, device="cuda")).softmax(-1)
+        parents[:, 1:] = parents[:, 1:] // 2
+        tokens[:, 1::3] = logits.argmin(-1)[:, :1].to(torch.int32)      # (some that are hardly ever accepted)
+        uniforms[:, 1:] = 1 - 2.0 ** -24
+        check(logits, tokens, uniforms, parents, draft)
+
+
+def test_excluded_drafts_with_siblings():
+    """The target excludes what was drafted first: every sibling is tested against what is left."""
+    for half in (False, True):
+        g = R.gen(98)
+        logits, tokens, uniforms, parents, draft = M.tree_inputs(g, 6, 14, 2500, True, True, half=half)
+        parents[:, 1:] = (torch.arange(1, 14, device="cuda") - 1) // 4
+        for b in range(6):
+            for i in range(1, 14, 2):
+                logits[b, int(parents[b, i]), int(tokens[b, i])] = -float("inf")
+        check(logits, tokens, uniforms, parents, draft)
