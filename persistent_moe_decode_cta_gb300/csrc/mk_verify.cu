@@ -83,8 +83,9 @@ struct Peak {
 };
 
 // One block per piece of a row: {largest, sum of exp((l - largest) / T), index of the largest (the lowest; at temperature 0, where
-// the sum only tells whether there is a NaN)}.  HBM bounds it.  32 values a thread, all of them on their way at once.  (Half as
-// many: 49 us in place of 42 for the rows of 16 trees of 32 nodes; a ring of bulk copies a warp: 52.)
+// the sum only tells whether there is a NaN)}.  Its loads and instructions bound it: 4.5 TB/s and 60 % of the issue slots (161 MB in
+// 35.6 us, the rows with children of 16 trees of 32 nodes).  32 values a thread, all of them on their way at once.  (Half as many:
+// 49 us in place of 42 for all rows of those trees; a ring of bulk copies a warp: 52.)
 template <bool F32>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int kVec = F32 ? 4 : 8;  // elements of 16 bytes
@@ -105,47 +106,73 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const float beta = heat.hi;
   const bool greedy = heat.t == 0.f, wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
   const int n = p.a.vocab, at = piece * kRowThreads * kRowValues + kVec * threadIdx.x;
-  uint4 u[kRowLoads];
+  uint32_t u[kRowLoads][4];
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
     const int j = at + i * kRowThreads * kVec;
-    if (wide && j + kVec <= n) u[i] = op_ld16(row + (long long)j * (F32 ? 4 : 2));
-  }
-  Peak mine{-INFINITY, 0.f, 0x7fffffff};
-#pragma unroll
-  for (int i = 0; i < kRowLoads; ++i) {
-    const int j = at + i * kRowThreads * kVec;
-    float x[kVec];
     if (wide && j + kVec <= n) {
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      const uint4 w = op_ld16(row + (long long)j * (F32 ? 4 : 2));
+      u[i][0] = w.x, u[i][1] = w.y, u[i][2] = w.z, u[i][3] = w.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[i][k] = F32 ? 0xff800000u : 0xff80ff80u;  // (-infinity)
+    }
+  }
+  if (!wide || at + (kRowLoads - 1) * kRowThreads * kVec + kVec > n) {  // what is no whole vector, value by value
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) {
+      const int j = at + i * kRowThreads * kVec;
+      if (wide && j + kVec <= n) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (F32) {
-          x[k] = __uint_as_float(w[k]);
+          if (j + k < n) u[i][k] = __float_as_uint(load_logit(row, j + k, true));
         } else {
-          const float2 f = bf16x2_to_f2(w[k]);
-          x[2 * k % kVec] = f.x, x[(2 * k + 1) % kVec] = f.y;
+          if (j + 2 * k < n) u[i][k] = (u[i][k] & 0xffff0000u) | op_ld2(row + 2ll * (j + 2 * k));
+          if (j + 2 * k + 1 < n) u[i][k] = (u[i][k] & 0xffffu) | (uint32_t)op_ld2(row + 2ll * (j + 2 * k + 1)) << 16;
         }
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) x[k] = j + k < n ? load_logit(row, j + k, F32) : -INFINITY;
     }
-    float top = x[0];
+  }
+  // the thread's largest first (a running one, rescaled at every vector: 8 x 9 nodes 33.1 us in place of 32.0 with the walk)
+  Peak mine{-INFINITY, 0.f, 0x7fffffff};
 #pragma unroll
-    for (int k = 1; k < kVec; ++k) top = fmaxf(top, x[k]);
-    if (top > mine.top) {
-      mine.sum *= ex2((mine.top - top) * beta);
-      mine.top = top;
-      if (greedy) {
+  for (int i = 0; i < kRowLoads; ++i)
 #pragma unroll
-        for (int k = kVec - 1; k >= 0; --k)
-          if (x[k] == top) mine.arg = j + k;
+    for (int k = 0; k < 4; ++k) {
+      if (F32) {
+        mine.top = fmaxf(mine.top, __uint_as_float(u[i][k]));
+      } else {
+        const float2 f = bf16x2_to_f2(u[i][k]);
+        mine.top = fmaxf(mine.top, fmaxf(f.x, f.y));
       }
     }
-    const float from = mine.top == -INFINITY ? 0.f : mine.top;
+  const float from = mine.top == -INFINITY ? 0.f : mine.top;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) mine.sum += ex2((x[k] - from) * beta);
+  for (int i = 0; i < kRowLoads; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (F32) {
+        mine.sum += ex2((__uint_as_float(u[i][k]) - from) * beta);
+      } else {
+        const float2 f = bf16x2_to_f2(u[i][k]);
+        mine.sum += ex2((f.x - from) * beta) + ex2((f.y - from) * beta);
+      }
+    }
+  if (greedy) {
+#pragma unroll
+    for (int i = kRowLoads - 1; i >= 0; --i)
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        const int j = at + i * kRowThreads * kVec;
+        if (F32) {
+          if (__uint_as_float(u[i][k]) == mine.top) mine.arg = j + k;
+        } else {
+          const float2 f = bf16x2_to_f2(u[i][k]);
+          if (f.y == mine.top) mine.arg = j + 2 * k + 1;
+          if (f.x == mine.top) mine.arg = j + 2 * k;
+        }
+      }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1)
