@@ -79,6 +79,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // the address of the first CTA's copy of a shared variable
 __device__ __forceinline__ uint32_t map_leader(uint32_t addr) {
   uint32_t r;
@@ -190,8 +193,6 @@ __device__ __forceinline__ void expert_rows(const ExpertParams& p, int e, int& l
   if (blockIdx.x == 0 && (lo != a || hi != b)) op_error(p.a.status, MK_ERR_INVALID, e, a, b);
 }
 
-// (EPI without offsets: one expert with every row)
-template <int EPI>
 __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows) {
   const int E = p.a.n_experts, nt = (int)blockDim.x;
   int carry = 0;
@@ -199,8 +200,8 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows
     const int e = base + (int)threadIdx.x;
     int x = 0;
     if (e < E) {
-      int lo = 0, hi = p.a.n_rows;
-      if (!EPI || p.a.offsets) expert_rows(p, e, lo, hi);
+      int lo, hi;
+      expert_rows(p, e, lo, hi);
       sh.rows[e] = make_int2(lo, hi);
       x = (hi - lo + tile_rows - 1) / tile_rows;
       if (hi > lo) atomicMax(&sh.most, hi - lo);
@@ -221,11 +222,20 @@ __device__ void scan_experts(const ExpertParams& p, ExpShared& sh, int tile_rows
   }
 }
 
-// The tile that this cluster takes in turn k (false: none)
-__device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& sh, int k, int tiles, int wblocks, int wstep, ExpTile& x) {
+// The tile that this cluster takes in turn k (false: none).  `whole` > 0: one expert with every row, in so many row tiles.
+__device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& sh, int k, int tiles, int wblocks, int wstep, int whole,
+                                       ExpTile& x) {
   const int t = k * ((int)gridDim.x / 2) + (int)blockIdx.x / 2;
   if (t >= tiles) return false;
   const int rt = t / wblocks;
+  if (whole) {
+    const int per = (p.a.n_rows + whole - 1) / whole;
+    x.e = 0;
+    x.w0 = (t - rt * wblocks) * wstep;
+    x.r0 = rt * per;
+    x.nr = min(per, p.a.n_rows - x.r0);
+    return true;
+  }
   int lo = 0;
 #pragma unroll
   for (int step = kOpMaxExperts / 2; step > 0; step >>= 1)
@@ -285,23 +295,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   tc_fence_before();
   cluster_sync();  // the barriers of both CTAs are there
   tc_fence_after();
-  pdl_wait();
-  pdl_trigger();
-    scan_experts<EPI>(p, sh, EPI ? epi.tile_rows : kTileR);
   const uint32_t tmem = uniform(sh.tmem);
   constexpr int kStep = GLU ? kTileW : 2 * kTileW;
   const int wblocks = (p.a.n + kStep - 1) / kStep;
-  const int tiles = (int)uniform(sh.pre[p.a.n_experts]) * wblocks;  // (below 2^31: checked by the host)
   const int ksteps = (p.a.k + kTileK - 1) / kTileK;
-  const uint32_t most = uniform(min(sh.most, kTileR)), room = most <= 64 ? 32 : most <= 128 ? 64 : 128;  // rows of a stage
+  // One expert with every row (EPI without offsets) needs no list: its first tile is known before the wait.  (With the list the first
+  // copies left 3400 cycles behind it, 1.7 of 27 us at 2001 x 4096.)
+  const int whole = EPI && !p.a.offsets ? (p.a.n_rows + epi.tile_rows - 1) / epi.tile_rows : 0;
+  ExpTile x;
+  bool any = whole && find_tile(p, sh, 0, whole * wblocks, wblocks, kStep, whole, x);
+  pdl_wait();
+  pdl_trigger();
+  if (!whole) scan_experts(p, sh, EPI ? epi.tile_rows : kTileR);
+  const int tiles = (whole ? whole : (int)uniform(sh.pre[p.a.n_experts])) * wblocks;  // (below 2^31: checked by the host)
+  const uint32_t most = whole ? min(p.a.n_rows, epi.tile_rows) : uniform(min(sh.most, kTileR)), room = most <= 64 ? 32 : most <= 128 ? 64 : 128;  // rows of a stage
   const uint32_t stage_bytes = kBytesW + room * kTileK * 2, stages = room == 32 ? 9 : room == 64 ? 8 : 6;
-  auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, x)); };
-  auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, x); };  // (one thread)
+  auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, whole, x)); };
+  auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, whole, x); };  // (one thread)
   // The products cut what they add to below the accumulator's last bit, so that the error of a long sum grows with its length: a
   // float32 result adds segments of 512 columns up in registers (2048 columns: 2.1e-6 of the result without, in the 2-norm).
   const int segment = EPI == 2 ? 8 : ksteps;
   const int clusters = (int)gridDim.x / 2, mine = (tiles - (int)blockIdx.x / 2 + clusters - 1) / clusters;  // tiles of this cluster
-  ExpTile x;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -310,8 +324,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
       bool ok = true;
       const int half = GLU ? kTileW / 2 : kTileW;  // weight rows per copy
       const uint32_t lead = map_leader(bars);
-      // (the next tile is looked up while this one's stages are under way)
-      bool more = tile1(0, x);
+      // (the next tile is looked up while this one's stages are under way, once the ring is full)
+      const int look = min(ksteps, (int)stages) - 1;
+      bool more = whole ? any : tile1(0, x);
       for (int t = 0; ok && more; ++t) {
         const int e = x.e, n2 = (x.nr + 31) / 32 * 16;  // rows of this CTA
         const int w = x.w0 + (int)rank * half, r = x.r0 + (int)rank * n2;
@@ -331,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
             tma_pair_2d(st + kBytesW, &tx, ks * kTileK, r, bar);
             if (xrows > kBoxR) tma_pair_2d(st + kBytesW + kBoxR * kTileK * 2, &tx, ks * kTileK, r + kBoxR, bar);
           }
-          if (ks == 0) more = tile1(t + 1, x);
+          if (ks == look) more = tile1(t + 1, x);
         }
       }
     }
@@ -448,6 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
     const bool wide = p.a.n % 8 == 0 && p.a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.a.out) & 15) == 0;
     uint16_t* const stage = reinterpret_cast<uint16_t*>(epi_g) + q * kChunk * 32;
     float* const exch_g = reinterpret_cast<float*>(epi_g + 4 * kChunk * 32 * 2) + (q & 1) * kChunk * 32;
+    // Accumulators of this cluster.  The last two are not handed back: nobody waits for that, and no arrival is on its way to a CTA
+    // that has left.
+    const uint32_t mine_acc = EPI == 2 ? (uint32_t)(mine * ((ksteps + segment - 1) / segment)) : (uint32_t)mine;
     if (EPI) {
       // eight warps: two share the lanes and take 16 rows in turn (three are no faster).  (What they release is tensor memory alone: a release of
       // everything would wait for the last tile's stores.)
@@ -477,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
               }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster_smem(map_leader(aempty(a)));
+            if (lane == 0 && na + 2 < mine_acc) arrive_cluster_smem(map_leader(aempty(a)));
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -516,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster_smem(map_leader(aempty(a)));
+        if (lane == 0 && na + 1 < mine_acc) arrive_cluster_smem(map_leader(aempty(a)));  // (na counts this one)
       }
     }
     for (int t = 0; !EPI && tile(t, x); ++t, ++nt) {
@@ -546,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
         if (last) {  // read: the next products may overwrite it
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(map_leader(aempty(a)));
+          if (lane == 0 && nt + 2 < mine_acc) arrive_cluster(map_leader(aempty(a)));
         } else {
           tmem_ld32(acc + c + kChunk, u);
         }
@@ -578,7 +596,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // neither CTA leaves while the other may signal it or read its half
+  // Neither CTA leaves while the other may signal it or read its half.  All that was signalled has been waited for, so that this needs
+  // no release, which would wait for the last stores (2300 cycles); an abandoned run has not waited.
+  if (*abort)
+    cluster_sync();
+  else
+    cluster_leave();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

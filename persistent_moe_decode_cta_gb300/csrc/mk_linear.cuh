@@ -5,44 +5,75 @@
 
 namespace mk {
 
-// act(y).  EXACT: for float32 results; a bf16 result hides the 2^-20 of the approximate exponential and division.
-// The tanh form is y / (1 + exp(-2 z)), the erf form y/2 erfc(-y / sqrt 2): both keep their relative precision
-// where 1 + tanh or 1 + erf would cancel.
-// erfc(t), t >= 0, to 2^-19 of itself and 2^-22 t^2: s exp(Q(s) - t^2) with s = 1 / (1 + t/2), Q a polynomial of degree 7 through the
-// Chebyshev nodes of ln(exp(t^2) erfc(t) / s) on s = 1/16 .. 1.  (2001 x 4096 with erfcf: 45.5 us, without an activation 29.)
-__device__ __forceinline__ float erfc_fast(float t) {
-  const float s = __fdividef(1.f, fmaf(0.5f, t, 1.f));
-  float q = -0.185161319f;
-  q = fmaf(q, s, 0.741661299f);
-  q = fmaf(q, s, -0.986141772f);
-  q = fmaf(q, s, 0.338574501f);
-  q = fmaf(q, s, -0.0352274307f);
-  q = fmaf(q, s, 0.393147085f);
-  q = fmaf(q, s, 0.998619703f);
-  q = fmaf(q, s, -1.26547264f);
-  return s * __expf(fmaf(-t, t, q));
+// act(y).  The tanh form is y / (1 + exp(-2 z)), the erf form y/2 erfc(-y / sqrt 2): both keep their relative precision where
+// 1 + tanh or 1 + erf would cancel.  Far below zero the exponential overflows and the quotient is zero.
+//
+// For float32 results, with CUDA's functions:
+template <int ACT>
+__device__ __forceinline__ float act_exact(float y) {
+  if (ACT == MK_ACT_RELU) return y < 0.f ? 0.f : y;  // (NaN stays)
+  if (ACT == MK_ACT_GELU) return 0.5f * y * erfcf(-0.70710678118654752f * y);
+  const float z = ACT == MK_ACT_SILU ? y : 1.5957691216057308f * fmaf(0.044715f * y * y, y, y);
+  return y / (1.f + expf(-z));
 }
 
-template <int ACT, bool EXACT>
-__device__ __forceinline__ float linear_act(float y) {
-  if (ACT == MK_ACT_NONE) return y;
-  if (ACT == MK_ACT_RELU) return y < 0.f ? 0.f : y;  // (NaN stays)
-  if (ACT == MK_ACT_GELU) {
-    if (EXACT) return 0.5f * y * erfcf(-0.70710678118654752f * y);
-    const float half = 0.5f * y * erfc_fast(0.70710678118654752f * fabsf(y));  // (y/2 erfc(-t) = y - y/2 erfc(t))
-    return y < 0.f ? half : y - half;
-  }
-  const float z = ACT == MK_ACT_SILU ? y : 1.5957691216057308f * fmaf(0.044715f * y * y, y, y);
-  // y / (1 + exp(-z)): far below zero the exponential overflows and the quotient is zero
-  const float e = EXACT ? expf(-z) : __expf(-z);
-  return EXACT ? y / (1.f + e) : __fdividef(y, 1.f + e);
+// For bf16 results, which hide the 2^-18 of approximate exponentials and reciprocals, of two values at once.  One value at a time
+// with __expf and __fdividef, whose guards for results below the normal range cost more than the rest, a tile of 224 x 256 took
+// 8500 cycles of epilogue in place of @@.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ uint64_t splat2(float v) { return pack2(v, v); }
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  const float2 f = unpack2(v);
+  return pack2(ex2(f.x), ex2(f.y));
+}
+__device__ __forceinline__ uint64_t rcp2(uint64_t v) {
+  const float2 f = unpack2(v);
+  return pack2(rcp(f.x), rcp(f.y));
+}
+template <int ACT>
+__device__ __forceinline__ void act_pair(float& y0, float& y1) {
+  constexpr float kLog2e = 1.4426950408889634f, kTanh = -1.5957691216057308f * kLog2e;
+  const uint64_t y = pack2(y0, y1);
+  if (ACT == MK_ACT_GELU) {
+    // erfc(t), t >= 0, to 2^-19 of itself and 2^-22 t^2: s exp(Q(s) - t^2) with s = 1 / (1 + t/2), Q a polynomial of degree 7
+    // through the Chebyshev nodes of ln(exp(t^2) erfc(t) / s) on s = 1/16 .. 1.  (With erfcf 2001 x 4096 took 17 us longer.)
+    const uint64_t t = pack2(0.70710678118654752f * fabsf(y0), 0.70710678118654752f * fabsf(y1));
+    const uint64_t s = rcp2(fma2(splat2(0.5f), t, splat2(1.f)));
+    uint64_t q = splat2(-0.185161319f);
+    q = fma2(q, s, splat2(0.741661299f));
+    q = fma2(q, s, splat2(-0.986141772f));
+    q = fma2(q, s, splat2(0.338574501f));
+    q = fma2(q, s, splat2(-0.0352274307f));
+    q = fma2(q, s, splat2(0.393147085f));
+    q = fma2(q, s, splat2(0.998619703f));
+    q = fma2(q, s, splat2(-1.26547264f));
+    const uint64_t e = ex2_2(mul2(fma2(mul2(t, splat2(-1.f)), t, q), splat2(kLog2e)));
+    // (y/2 erfc(-t) = y - y/2 erfc(t); an infinite y less 0)
+    const float2 half = unpack2(mul2(mul2(pack2(fminf(y0, 1e38f), fminf(y1, 1e38f)), mul2(s, splat2(0.5f))), e));
+    y0 = y0 < 0.f ? half.x : y0 - half.x;
+    y1 = y1 < 0.f ? half.y : y1 - half.y;
+  } else {
+    const uint64_t z = ACT == MK_ACT_SILU ? splat2(-kLog2e) : fma2(mul2(y, y), splat2(0.044715f * kTanh), splat2(kTanh));
+    const float2 r = unpack2(mul2(y, rcp2(add2(ex2_2(mul2(y, z)), splat2(1.f)))));
+    y0 = r.x, y1 = r.y;
+  }
+}
+
 // ... of all of v.  (In registers and unrolled: one value after another through shared memory, 2001 x 4096 with the tanh form
 // took 88 us.)
 template <int ACT, bool EXACT, int N>
 __device__ __forceinline__ void linear_acts(float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = linear_act<ACT, EXACT>(v[i]);
+  for (int i = 0; i < N; i += EXACT || ACT == MK_ACT_RELU ? 1 : 2) {
+    if constexpr (EXACT || ACT == MK_ACT_RELU)
+      v[i] = act_exact<ACT>(v[i]);
+    else
+      act_pair<ACT>(v[i], v[i + 1]);
+  }
 }
 template <bool EXACT, int N>
 __device__ __forceinline__ void linear_acts(float (&v)[N], int act) {
