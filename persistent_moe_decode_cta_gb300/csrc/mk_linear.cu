@@ -33,6 +33,10 @@ __device__ __forceinline__ uint32_t split_rank() {
 __device__ __forceinline__ void split_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// No CTA leaves before its copies have arrived: each says when it has got its own.  (A release behind the last stores, and waited for,
+// was 1.7 of 8.5 us at 128 rows, 4096 -> 2048.)
+__device__ __forceinline__ void split_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void split_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
@@ -139,15 +143,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (p.slices > 1) op_wait(got, 0, abort, p.status, 4);
-  // a warp takes a row at a time, a lane four outputs
+  // a warp takes a row at a time, a lane four outputs; what it adds is on its way before the sums are there
   const int col = 4 * lane, width = min(kSplitW, p.n - w0), last = min(own, rows - (int)rank * own);
+  const long long row0 = r0 + (long long)rank * own;
   float b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) b[i] = p.epi.bias && col + i < width ? bf16_to_f(op_ld2(p.epi.bias + w0 + col + i)) : 0.f;
+  uint2 ahead = warp < last ? linear_residual(p.epi, row0 + warp, w0 + col, width - col) : make_uint2(0, 0);
+  if (p.slices > 1) op_wait(got, 0, abort, p.status, 4);
+  if (*abort) {  // an abandoned run leaves copies and products in flight: give them time to end
+    const uint64_t t0 = gtime();
+    while ((long long)(gtime() - t0) < 10000000ll) {}
+  }
+  __syncwarp();
+  split_arrive();
   for (int r = warp; r < last; r += kSplitThreads / 32) {
-    const long long row = r0 + (long long)rank * own + r;
-    const uint2 ahead = linear_residual(p.epi, row, w0 + col, width - col);
+    const int then = r + kSplitThreads / 32;
+    const uint2 next = then < last ? linear_residual(p.epi, row0 + then, w0 + col, width - col) : make_uint2(0, 0);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     float4 y = *reinterpret_cast<const float4*>(sums_g + r * kSplitW + col);
     v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
@@ -158,17 +170,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += b[i];
     linear_acts<WIDE>(v, p.epi.act);
-    linear_put<WIDE>(p.epi, p.out, p.out_stride, v, ahead, row, w0 + col, width - col);
+    linear_put<WIDE>(p.epi, p.out, p.out_stride, v, ahead, row0 + r, w0 + col, width - col);
+    ahead = next;
   }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
-  if (*abort) {  // an abandoned run leaves copies and products in flight: give them time to end
-    const uint64_t t0 = gtime();
-    while ((long long)(gtime() - t0) < 10000000ll) {}
-  }
-  split_sync();  // no CTA leaves before its copies have arrived
+  split_wait();
 }
 
 }  // namespace
