@@ -291,21 +291,18 @@ struct __align__(16) Node {
   float top, sum;      // of its own row
   int arg, pad;
 };
-struct Part {
-  unsigned long long sum;
-  unsigned long long pad;
-};
 enum { kCut, kDraw, kEnd };
 
 struct WalkShared {
   Node* node;                          // [n_nodes], and behind them
   int* path;                           // [n_nodes]
   int* gone;                           // [n_nodes] tokens of rejected children (drafts without probabilities)
-  Part part[2][kWalkCtas];             // the CTAs' sums, written by each into all
-  unsigned long long warp_sum[kWalkWarps];
+  unsigned long long part[2][kWalkCtas];  // the CTAs' sums, written by each into all
+  unsigned long long bars[2];          // ... and where a set says that it is whole
+  unsigned long long warp_sum[2][kWalkWarps];
   Power power[kPowers];
   float t;
-  int count;                           // (behind t: the two are copied together)
+  int count, abort;
   int step, at, length, n_gone, next;
 };
 
@@ -329,13 +326,33 @@ __device__ __forceinline__ uint32_t map_cta(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void put64(uint32_t at, unsigned long long v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+// a value into another CTA's shared memory, and its 8 bytes off what a barrier there waits for
+__device__ __forceinline__ void put_async(uint32_t at, unsigned long long v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at), "l"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ uint4 get128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ bool try_wait_sums(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// As op_wait: of a whole warp, given up after a time.  (The CTA then goes on with wrong sums, without further waits, and its call has
+// an error recorded.)
+__device__ __noinline__ void wait_sums(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  const uint64_t t0 = gtime();
+  while (!__all_sync(0xffffffffu, try_wait_sums(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort != 0)) return;
+    if (__any_sync(0xffffffffu, (long long)(gtime() - t0) > kOpWaitNs)) {
+      *abort = 1;
+      op_error(status, MK_ERR_TIMEOUT, (int)blockIdx.x, 1, (int)parity);
+      return;
+    }
+  }
 }
 
 __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
@@ -344,8 +361,9 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
   return v;
 }
 
-// What the first CTA of the cluster looks up for the whole walk.
-__device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
+// What every CTA of the cluster looks up for the whole walk.  (By one of them and copied to the others it took 1.2 us longer.)
+// `first_cta`: the one that records what is wrong.
+__device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b, bool first_cta) {
   const mk_verify_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool f32 = a.logits_float != 0;
@@ -360,10 +378,10 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
     x.u = op_ldf(a.uniforms + mine_at);
   }
   if (count < 1 || count > a.n_nodes) {
-    if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, count);
+    if (first_cta && tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, count);
     count = 0;
   } else if (!(heat.t >= 0.f)) {
-    if (tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, __float_as_int(heat.t));
+    if (first_cta && tid == 0) op_error(a.status, MK_ERR_INVALID, b, -1, __float_as_int(heat.t));
     count = 0;
   }
   if (tid == 0) sh.count = count, sh.t = heat.t;
@@ -371,14 +389,14 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
     const int i = tid;
     bool fine = true;
     if (!(x.u >= 0.f && x.u < 1.f)) {
-      op_error(a.status, MK_ERR_INVALID, b, i, __float_as_int(x.u));
+      if (first_cta) op_error(a.status, MK_ERR_INVALID, b, i, __float_as_int(x.u));
       x.u = 0.f;
       fine = false;
     } else if (i > 0 && (x.parent < 0 || x.parent >= i)) {
-      op_error(a.status, MK_ERR_INVALID, b, i, x.parent);
+      if (first_cta) op_error(a.status, MK_ERR_INVALID, b, i, x.parent);
       fine = false;
     } else if (x.token < 0 || x.token >= a.vocab) {
-      op_error(a.status, MK_ERR_INVALID, b, i, x.token);
+      if (first_cta) op_error(a.status, MK_ERR_INVALID, b, i, x.token);
       fine = false;
     }
     if (i > 0 && fine) {
@@ -432,28 +450,36 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b) {
   }
 }
 
-// The sum, or the largest, of what the warps of all CTAs hand in.  (Two sets in turn: a CTA may write the next pass's sums while another still reads
-// this one's, but no CTA is two barriers ahead.)
+// The sum, or the largest, of what the warps of all CTAs hand in, in turn `*turn`.  (Two sets in turn: a CTA may send the next pass's
+// sums while another still reads this one's, but nobody is two passes ahead, since a pass needs everybody's.)
 template <bool LARGEST = false>
-__device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned long long warp_sum, int* parity) {
+__device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned long long warp_sum, uint32_t* turn, int32_t* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ctas = cta_count(), rank = cta_rank();
-  if (lane == 0) sh.warp_sum[warp] = warp_sum;
+  const uint32_t ctas = cta_count(), set = *turn & 1, bar = smem_u32(&sh.bars[set]);
+  if (lane == 0) sh.warp_sum[set][warp] = warp_sum;
   __syncthreads();
   if (threadIdx.x < ctas) {
     unsigned long long mine = 0;
-    for (int i = 0; i < kWalkWarps; ++i) mine = LARGEST ? max(mine, sh.warp_sum[i]) : mine + sh.warp_sum[i];
-    put64(map_cta(&sh.part[*parity][rank], threadIdx.x), mine);
+#pragma unroll
+    for (int i = 0; i < kWalkWarps; ++i) mine = LARGEST ? max(mine, sh.warp_sum[set][i]) : mine + sh.warp_sum[set][i];
+    if (threadIdx.x == 0) mbar_expect_tx(bar, ctas * 8);
+    put_async(map_cta(&sh.part[set][cta_rank()], threadIdx.x), mine, map_cta(&sh.bars[set], threadIdx.x));
   }
-  walk_sync();
+  __syncwarp();
+  wait_sums(bar, *turn >> 1 & 1, &sh.abort, status);
   unsigned long long total = 0;
-  for (uint32_t i = 0; i < ctas; ++i) total = LARGEST ? max(total, sh.part[*parity][i].sum) : total + sh.part[*parity][i].sum;
-  *parity ^= 1;
+#pragma unroll
+  for (uint32_t i = 0; i < kWalkCtas; ++i) {
+    const unsigned long long v = i < ctas ? sh.part[set][i] : 0;
+    total = LARGEST ? max(total, v) : total + v;
+  }
+  ++*turn;
   return total;
 }
 
-// One cluster per sequence.  Every CTA's first thread walks by itself, all of them from the same numbers (the first CTA's copy of the
-// nodes, and sums that each has of all), so that they ask for the same passes and meet at the same barriers.
+// One cluster per sequence.  Every CTA's first thread walks by itself, all of them from the same numbers (their own copies of the
+// nodes, and sums that each has of all), so that they ask for the same passes.  The sums of a pass are sent to every CTA, whose barrier
+// counts them.  (With barriers of the cluster each meeting took 1.3 us, now @@.)
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ __align__(16) WalkShared sh;
@@ -474,30 +500,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     sh.node = reinterpret_cast<Node*>(raw);
     sh.path = reinterpret_cast<int*>(raw + a.n_nodes * sizeof(Node));
     sh.gone = sh.path + a.n_nodes;
+    sh.abort = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.bars[i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // (all CTAs have started, their barriers are there)
   pdl_wait();
   pdl_trigger();
-  if (rank == 0) gather_nodes(p, sh, b);
-  walk_sync();
-  if (rank != 0) {
-    if (tid == 0) {
-      const uint32_t of = map_cta(&sh.t, 0);
-      uint32_t x, y;
-      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(of) : "memory");
-      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(y) : "r"(of + 4) : "memory");
-      sh.t = __uint_as_float(x);
-      sh.count = (int)y;
-    }
-    __syncthreads();
-    for (int i = tid; i < 3 * sh.count; i += kWalkThreads)
-      *(reinterpret_cast<uint4*>(sh.node) + i) = get128(map_cta(reinterpret_cast<const uint4*>(sh.node) + i, 0));
-  }
+  gather_nodes(p, sh, b, rank == 0);
   __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int count = sh.count;
   const Heat heat(sh.t);
   Exp ex{0.f, heat.hi, heat.lo, sh.power};
-  int parity = 0, at = 0, row_at = -1;
+  int at = 0, row_at = -1;
+  uint32_t turn = 0;  // passes so far
   // of the row at `at`: A and W, and what this warp has of W
   unsigned long long A = 0, W = 0, warp_sum = 0;
   bool loaded = false, stuck = false;
@@ -633,7 +651,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
         if (odd) key = ~0ull;  // (NaN or infinite)
 #pragma unroll
         for (int o = 16; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-        key = exchange<true>(sh, key, &parity);
+        key = exchange<true>(sh, key, &turn, a.status);
         const uint32_t high = (uint32_t)(key >> 32);
         top = key == ~0ull ? INFINITY : __uint_as_float(high >> 31 ? high & 0x7fffffffu : ~high);
         ex.top = top;
@@ -667,7 +685,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
       }
       warp_sum = warp_total(sum);
       A = 0;
-      W = exchange(sh, warp_sum, &parity);
+      W = exchange(sh, warp_sum, &turn, a.status);
       loaded = true;
       stuck = false;
     }
@@ -690,7 +708,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
             }
         }
         sum = warp_total(sum);
-        const unsigned long long now = exchange(sh, sum, &parity);
+        const unsigned long long now = exchange(sh, sum, &turn, a.status);
         if (now) {
           A += W;
           W = now;
@@ -705,11 +723,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     // (u has 24 bits: u 2^64 is exact from 2^-40 on)
     const unsigned long long goal = __umul64hi((unsigned long long)((double)sh.node[0].u * 0x1p64), W);
     if (stuck) {  // (the last pass did not count)
-      exchange(sh, warp_sum, &parity);
+      exchange(sh, warp_sum, &turn, a.status);
     }
     unsigned long long sum = 0;
-    for (uint32_t i = 0; i < rank; ++i) sum += sh.part[parity ^ 1][i].sum;
-    for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
+    const uint32_t set = (turn - 1) & 1;  // the last pass's
+#pragma unroll
+    for (uint32_t i = 0; i < kWalkCtas; ++i) sum += i < rank ? sh.part[set][i] : 0;
+#pragma unroll
+    for (int i = 0; i < kWalkWarps; ++i) sum += i < warp ? sh.warp_sum[set][i] : 0;
     if (goal >= sum && goal < sum + warp_sum) {  // this warp's
       const Cut cut(A);
       bool found = false;
@@ -766,8 +787,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     __syncthreads();
     for (int i = tid; i < a.n_nodes; i += kWalkThreads) a.accepted[(long long)b * a.n_nodes + i] = i < sh.length ? sh.path[i] : -1;
   }
-  // no CTA leaves while another may write to it or read its nodes: not before a barrier behind the last of that, which a pass has had
-  if (row_at < 0) walk_sync();
+  // No CTA leaves while another may send to it: it has had all that was sent.  One that gave up waiting stays until the others leave.
+  if (sh.abort) walk_sync();
 }
 
 int row_pieces(const mk_verify_args& a) { return (a.vocab + kRowThreads * kRowValues - 1) / (kRowThreads * kRowValues); }
