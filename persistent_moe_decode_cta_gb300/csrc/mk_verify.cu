@@ -190,22 +190,16 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------------------------- exponentials
-// 2^(i/256), i = 0 .. 255, in units of 2^-52 and as a sum of two floats
-constexpr int kPowers = 256;
-struct __align__(16) Power {
-  unsigned long long fix;
-  float hi, lo;
-};
+// 2^(i/512), i = 0 .. 511, in units of 2^-62
+constexpr int kPowers = 512;
 struct Powers {
-  Power v[kPowers];
+  unsigned long long v[kPowers];
   constexpr Powers() : v() {
     for (int i = 0; i < kPowers; ++i) {
-      const double x = i / 256.0 * 0.69314718055994530942;
+      const double x = i / 512.0 * 0.69314718055994530942;
       double y = 1;
       for (int k = 22; k > 0; --k) y = 1 + x / k * y;  // the exponential series
-      v[i].fix = (unsigned long long)(y * 4503599627370496.0 + 0.5);
-      v[i].hi = (float)y;
-      v[i].lo = (float)(y - (double)v[i].hi);
+      v[i] = (unsigned long long)(y * 4503599627370496.0 + 0.5) << 10;
     }
   }
 };
@@ -219,43 +213,39 @@ __device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
 constexpr float kMagic = 12582912.f;
 __device__ __forceinline__ int low_bits(float v) { return __float_as_int(v) - 0x4b400000; }
 
-// exp((l - top) / T) in units of 2^-44 of two logits at once, for finite l <= top to 2^-41 of itself; 0 for anything else.  top: the
-// row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.)
-__device__ __forceinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const Power* table) {
+// exp((l - top) / T) in units of 2^-44 of two logits at once, for finite l <= top to 2^-32 of itself; 0 for anything else.  top: the
+// row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.  With
+// another 2^-9 of precision it took 1.5 times as long: 8 x 9 nodes @@ us in place of @@.)
+__device__ __forceinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const unsigned long long* table) {
   const uint64_t minus = both(-1.f), l = pack2(l0, l1), b = both(bh);
-  // l - top as dh + dl, exactly; times log2(e) / T as ph + pl
+  // l - top as dh + dl, exactly; times log2(e) / T as pl - np, np at most 46: beyond that nothing is left (nor of NaN)
   const uint64_t dh = add2(l, both(-top)), z = fma2(l, minus, dh);
   const uint64_t dl = fma2(add2(both(top), z), minus, fma2(fma2(z, minus, dh), minus, l));
-  const uint64_t ph = mul2(dh, b), pl = fma2(dh, both(bl), fma2(dl, b, fma2(dh, b, mul2(dh, both(-bh)))));
-  // ph = k / 256 + r, exactly
-  const uint64_t m = fma2(ph, both(256.f), both(kMagic)), r = fma2(add2(m, both(-kMagic)), both(-1.f / 256.f), ph);
-  // y = (r + pl) ln 2 as yh + yl, |y| < 2^-9; exp(y) - 1 = y + y^2 (1/2 + y/6) as eh + el
-  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654299957767e-9f;
-  const uint64_t yh = mul2(r, both(kLn2h));
-  const uint64_t yl = fma2(r, both(kLn2l), fma2(pl, both(kLn2h), fma2(r, both(kLn2h), mul2(r, both(-kLn2h)))));
-  const uint64_t s = fma2(mul2(yh, yh), fma2(yh, both(1.f / 6.f), both(0.5f)), fma2(yh, yl, yl));
-  const uint64_t eh = add2(yh, s), el = fma2(fma2(yh, minus, eh), minus, s);
-  // times the table's entry T = th + tl: T (exp(y) - 1) as wh + wl, then as an integer of 2^-52 in two steps of 22 bits
-  const float2 mf = unpack2(m), pf = unpack2(ph);
-  const int k0 = low_bits(mf.x), k1 = low_bits(mf.y);
-  const Power t0 = table[k0 & 255], t1 = table[k1 & 255];
-  const uint64_t th = pack2(t0.hi, t1.hi), tl = pack2(t0.lo, t1.lo);
-  const uint64_t wh = mul2(th, eh), wl = fma2(tl, eh, fma2(th, el, fma2(th, eh, mul2(wh, minus))));
-  const uint64_t m1 = fma2(wh, both(0x1p30f), both(kMagic)), rest = add2(fma2(add2(m1, both(-kMagic)), both(-0x1p-30f), wh), wl);
-  const float2 hi = unpack2(m1), lo = unpack2(fma2(rest, both(0x1p52f), both(kMagic)));
-  const unsigned long long v0 = t0.fix + (unsigned long long)((long long)low_bits(hi.x) * (1ll << 22) + low_bits(lo.x));
-  const unsigned long long v1 = t1.fix + (unsigned long long)((long long)low_bits(hi.y) * (1ll << 22) + low_bits(lo.y));
-  // (shifted by 52 - 44 and the whole part of k / 256, rounded)
-  return U2{pf.x >= -50.f ? ((v0 >> ((51 - kFixed - (k0 >> 8)) & 63)) + 1) >> 1 : 0ull,
-            pf.y >= -50.f ? ((v1 >> ((51 - kFixed - (k1 >> 8)) & 63)) + 1) >> 1 : 0ull};
+  const float2 n2 = unpack2(mul2(dh, both(-bh)));
+  const uint64_t np = pack2(fminf(n2.x, 46.f), fminf(n2.y, 46.f)), pl = fma2(dh, both(bl), fma2(dl, b, fma2(dh, b, np)));
+  // -np = k / 512 - nr, exactly; y = 1024 (pl - nr) ln 2, |y| < 0.69; e = 1024 (exp(y / 1024) - 1) by its series
+  constexpr float kLn2 = 1024 * 0.693147182464599609375f;
+  const uint64_t m = fma2(np, both(-512.f), both(kMagic)), nr = fma2(add2(m, both(-kMagic)), both(1.f / 512.f), np);
+  const uint64_t y = fma2(nr, both(-kLn2), mul2(pl, both(kLn2)));
+  const uint64_t e = fma2(mul2(y, y), fma2(y, both(0x1p-20f / 6), both(0x1p-11f)), y);
+  // the table's entry t plus t e, the latter as an integer of 2^-40
+  const float2 mf = unpack2(m);
+  const uint32_t k0 = __float_as_uint(mf.x), k1 = __float_as_uint(mf.y);  // k + 0x4b400000
+  const unsigned long long t0 = table[k0 & 511], t1 = table[k1 & 511];
+  const float2 w = unpack2(mul2(pack2((float)(uint32_t)(t0 >> 32), (float)(uint32_t)(t1 >> 32)), e));
+  const unsigned long long v0 = t0 + (unsigned long long)((long long)__float2int_rn(w.x) * (1ll << 22));
+  const unsigned long long v1 = t1 + (unsigned long long)((long long)__float2int_rn(w.y) * (1ll << 22));
+  // (shifted by 62 - 44 and the whole part of k / 512, rounded)
+  constexpr uint32_t kShift = 61 - kFixed + (0x4b400000u >> 9);
+  return U2{((v0 >> (kShift - (k0 >> 9) & 63)) + 1) >> 1, ((v1 >> (kShift - (k1 >> 9) & 63)) + 1) >> 1};
 }
 // (of single logits: one copy of the code, since a cold kernel waits for its instructions longer than it runs them)
-__device__ __noinline__ unsigned long long exp_one(float l, float top, float bh, float bl, const Power* table) {
+__device__ __noinline__ unsigned long long exp_one(float l, float top, float bh, float bl, const unsigned long long* table) {
   return exp_fixed(l, l, top, bh, bl, table).x;
 }
 struct Exp {
   float top, bh, bl;
-  const Power* table;
+  const unsigned long long* table;
   __device__ __forceinline__ U2 operator()(float l0, float l1) const { return exp_fixed(l0, l1, top, bh, bl, table); }
   __device__ __forceinline__ unsigned long long operator()(float l) const { return exp_one(l, top, bh, bl, table); }
 };
@@ -300,7 +290,7 @@ struct WalkShared {
   unsigned long long part[2][kWalkCtas];  // the CTAs' sums, written by each into all
   unsigned long long bars[2];          // ... and where a set says that it is whole
   unsigned long long warp_sum[2][kWalkWarps];
-  Power power[kPowers];
+  unsigned long long power[kPowers];
   float t;
   int count, abort;
   int step, at, length, n_gone, next;
@@ -432,6 +422,7 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b, bool 
     // the children in order, and the test of each against its parent's whole row
     const int up = sh.node[tid].parent;
     int first = -1, next = -1;
+#pragma unroll 8
     for (int j = count - 1; j > tid; --j) {
       const int of = sh.node[j].parent;
       if (of == tid) first = j;
@@ -601,8 +592,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     if (!loaded) {
       const void* const row = logit_row(a, b, at);
       const bool wide = is_wide(row, f32);
-      // (all copies first, each into the first half of what the lane turns it into: lanes wait for their own only.  Rolled loops:
-      // unrolled, the code of a pass that runs once is fetched for longer than it runs.)
+      // (all copies first, each into the first half of what the lane turns it into: lanes wait for their own only, for the second
+      // half of them behind the first half's exponentials.  Rolled loops: unrolled, the code of a pass that runs once is fetched for
+      // longer than it runs.)
+      const int half = (n_blocks + 1) / 2;
       if (wide) {
         const int size = f32 ? 16 : 8;
         for (int k = 0; k < n_blocks; ++k) {
@@ -615,6 +608,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
             else
               op_cp8(to, src);
           }
+          if (k + 1 == half) asm volatile("cp.async.commit_group;" ::: "memory");
         }
       }
       if (draft && step == kCut && qwide)  // (into L2)
@@ -622,7 +616,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           const int j = base + from + k * kBlock;
           if (lane % 8 == 0 && j < a.vocab) asm volatile("prefetch.global.L2 [%0];" ::"l"(drow + j) : "memory");
         }
-      op_cp_wait_all();
       auto logits = [&](int k) {
         const int j = base + from + k * kBlock;
         if (!wide || j + 4 > a.vocab) return load4(row, j, a.vocab, f32, false, -INFINITY);
@@ -636,6 +629,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
         float top = -INFINITY;
         int arg = 0;
         bool odd = false;
+        op_cp_wait_all();
 #pragma unroll 1
         for (int k = 0; k < n_blocks; ++k) {
           const float4 v = logits(k);
@@ -664,10 +658,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
         }
       } else {
         ex.top = sh.node[at].top;
+        // (the last group is open: the copies of the second half)
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
       }
       unsigned long long sum = 0;
 #pragma unroll 1
       for (int k = 0; k < n_blocks; ++k) {
+        if (k == half) op_cp_wait_all();
         const int j = base + from + k * kBlock;
         ulonglong2* const to = reinterpret_cast<ulonglong2*>(e + from + k * kBlock);
         const float4 v = logits(k);
