@@ -9,7 +9,7 @@
 //
 // Numbers.  The drawn token is where a running sum over up to 2^18 probabilities passes u times the whole: errors of fp32 would
 // move borders enough to change one draw of a few hundred.  So the exponentials of the walk are 64-bit integers (2^-44 of the
-// largest), exponentiated in pairs of floats, and their sums are exact: neither order nor split matters.  With R the integers
+// largest, right to 2^-32 of themselves), and their sums are exact: neither order nor split matters.  With R the integers
 // left and W their sum, r = R / W, and a rejection leaves (R - q W)+: in terms of the row's exponentials E
 // R = (E - q A)+ where A grows by W with every rejection; E is kept and A is one number.
 #include "mk_ops.cuh"
@@ -214,8 +214,9 @@ constexpr float kMagic = 12582912.f;
 __device__ __forceinline__ int low_bits(float v) { return __float_as_int(v) - 0x4b400000; }
 
 // exp((l - top) / T) in units of 2^-44 of two logits at once, for finite l <= top to 2^-32 of itself; 0 for anything else.  top: the
-// row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.  With
-// another 2^-9 of precision it took 1.5 times as long: 8 x 9 nodes @@ us in place of @@.)
+// row's largest logit; bh + bl: log2(e) / T.  (With packed operations, which are rounded one by one, whatever follows them.  To 2^-41
+// it took 1.5 times the instructions: 8 x 9 nodes 30.4 us with that and a row's copies in one piece, 28.3 with this and two halves.
+// What is off is a random 2^-35.5 in the mean: of 10^6 draws from 2^17 tokens it moves about one.)
 __device__ __forceinline__ U2 exp_fixed(float l0, float l1, float top, float bh, float bl, const unsigned long long* table) {
   const uint64_t minus = both(-1.f), l = pack2(l0, l1), b = both(bh);
   // l - top as dh + dl, exactly; times log2(e) / T as pl - np, np at most 46: beyond that nothing is left (nor of NaN)
@@ -470,7 +471,8 @@ __device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned 
 
 // One cluster per sequence.  Every CTA's first thread walks by itself, all of them from the same numbers (their own copies of the
 // nodes, and sums that each has of all), so that they ask for the same passes.  The sums of a pass are sent to every CTA, whose barrier
-// counts them.  (With barriers of the cluster each meeting took 1.3 us, now @@.)
+// counts them.  (With barriers of the cluster in their
+// place, and one CTA's nodes copied to the others, 8 x 9 nodes took 32.1 us, without 30.4.)
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ __align__(16) WalkShared sh;
