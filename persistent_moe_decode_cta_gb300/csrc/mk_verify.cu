@@ -809,9 +809,10 @@ cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
   static std::atomic<int> known[kSizes][64];
   if (e == cudaSuccess) e = allow_smem(walk_kernel, kWalkSmem, done);
   if (e == cudaSuccess) e = allow_wide_clusters(walk_kernel, done16);
-  // CTAs of a cluster: a walk takes about 13 us and 1 more for every 12 blocks of a CTA's piece of the row (151936: 21 us in clusters
-  // of 8, 18 in 12).  Where the clusters do not fit the GPU all at once (7 of 16 CTAs do, 15 of 8, 23 of 6) the last ones start as
-  // the first end, which are not equally long (16 trees of 32 nodes: 95 us in clusters of 8, 107 in 6)
+  // CTAs of a cluster: a walk with one pass over a row takes about 10 us and 1 more for every 12.5 blocks of a CTA's piece of it (8 x 9
+  // nodes of 151936: 37.5 us in clusters of 6, 32.1 in 8, 29.3 in 10, 28.1 in 12).  Where the clusters do not fit the GPU all at
+  // once (7 of 16 CTAs do, 8 of 12, 15 of 8, 23 of 6) the last ones start as the first end, which are not equally long (16 trees of
+  // 32 nodes: 73.3 us in clusters of 8, 81.9 in 6)
   static const int sizes[kSizes] = {16, 12, 10, 8, 6, 4, 2, 1};
   const int blocks = (p.a.vocab + kBlock - 1) / kBlock, nodes = node_bytes(p.a.n_nodes);
   int ctas = 0;
@@ -822,7 +823,7 @@ cudaError_t launch_verify(VerifyParams& p, cudaStream_t st) {
     int fit = 0;
     e = active_clusters(walk_kernel, sizes[i], kWalkThreads, kWalkSmem, known[i], &fit);
     if (e != cudaSuccess || fit < 1) continue;
-    const double cost = std::max(1.0, (double)p.a.batch / fit) * (13 + piece / 12.0);
+    const double cost = std::max(1.0, (double)p.a.batch / fit) * (10 + piece / 12.5);
     if (!ctas || cost < least) least = cost, ctas = sizes[i];
   }
   if (e != cudaSuccess) return e;
