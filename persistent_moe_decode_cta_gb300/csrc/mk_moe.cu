@@ -261,11 +261,15 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
     sh.value[sh.rank[tid]] = sh.score[tid].x;
   }
   __syncthreads();
-  if (tid < K) {
-    float total = 0.f;
-    for (int j = 0; j < K; ++j) total += __expf(sh.value[j] - sh.value[0]);
-    p.ids[t * K + tid] = sh.chosen[tid];
-    p.weights[t * K + tid] = __expf(sh.value[tid] - sh.value[0]) / total;
+  if (warp == 0) {
+    const float mine = lane < K ? __expf(sh.value[lane] - sh.value[0]) : 0.f;
+    float total = mine;
+#pragma unroll
+    for (int o = kMoeTopK / 2; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane < K) {
+      p.ids[t * K + lane] = sh.chosen[lane];
+      p.weights[t * K + lane] = mine / total;
+    }
   }
 }
 
@@ -563,6 +567,11 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   for (int block = blockIdx.x; block < blocks; block += runs) {
     const int c0 = block * p.width, wide = min(p.width, d - c0), n = A * steps_down;
     clear();
+    // (a value a thread: the residual is on its way before its sum is there)
+    const int c = tid & 15, t = tid >> 4;
+    const bool mine = tid < NT * 128 && t < T && c < wide;
+    const uint16_t* const residual = static_cast<const uint16_t*>(p.a.residual);
+    const float ahead_y = mine && residual ? bf16_to_f(op_ld2(residual + t * p.a.residual_stride + c0 + c)) : 0.f;
     for (int s = warp; s < n; s += kLayerWarps) {
       multiply(h_at + get.slot * (NT * 2048));
       if (id.block < blocks) {
@@ -574,16 +583,14 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
 #pragma unroll
     for (int j = 0; j < NT; ++j) red[(warp * NT + j) * 32 + lane] = make_float4(total(j, 0), total(j, 1), total(j, 2), total(j, 3));
     __syncthreads();
-    // the warps' parts, in their order: a value a thread
-    for (int i = tid; i < NT * 128; i += kLayerThreads) {
-      const int c = i & 15, t = i >> 4, j = t >> 3, from = (c & 7) * 4 + ((t & 7) >> 1), part = (t & 1) + 2 * (c >> 3);
-      if (t < T && c < wide) {
-        float y = 0.f;
+    // the warps' parts, in their order
+    if (mine) {
+      const int j = t >> 3, from = (c & 7) * 4 + ((t & 7) >> 1), part = (t & 1) + 2 * (c >> 3);
+      float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kLayerWarps; ++w) y += reinterpret_cast<const float*>(red + (w * NT + j) * 32 + from)[part];
-        if (p.a.residual) y += bf16_to_f(op_ld2(static_cast<const uint16_t*>(p.a.residual) + t * p.a.residual_stride + c0 + c));
-        static_cast<uint16_t*>(p.a.out)[t * p.a.out_stride + c0 + c] = to_bf16(y);
-      }
+      for (int w = 0; w < kLayerWarps; ++w) y += reinterpret_cast<const float*>(red + (w * NT + j) * 32 + from)[part];
+      if (residual) y += ahead_y;
+      static_cast<uint16_t*>(p.a.out)[t * p.a.out_stride + c0 + c] = to_bf16(y);
     }
     __syncthreads();
   }
