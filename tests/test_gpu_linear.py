@@ -161,3 +161,26 @@ def test_offsets_beyond_32_bits():
         x, w, before = R.bf16(g, 3, 64), R.bf16(g, n, 64, std=0.1), both.clone()
         ops.linear(x, w, residual=both, out=both)
         R.assert_close(both, *M.linear(x, w, None, None, before))
+
+
+@pytest.mark.parametrize("act", M.ACTS)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("m", [2, 300])
+def test_activations_at_the_ends_of_the_range(m, act, wide):
+    """What the formula gives for infinite, NaN and huge sums: an infinite sum stays, a product of zero and infinity is a NaN."""
+    ends = [float("inf"), -float("inf"), float("nan"), 3e38, -3e38, 1e30, -1e30, 1e13, -1e13, 40.0, -40.0, 0.0, -0.0, 1e-38, -1e-38]
+    n = 8 * len(ends)
+    b = torch.tensor(ends, device="cuda").repeat(8).to(torch.bfloat16)
+    x = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda")
+    got = ops.linear(x, w, bias=b, activation=act, dtype=torch.float32 if wide else torch.bfloat16).double()
+    y = b.double().expand(m, n)
+    want, rel, _ = M.activation(y, act)
+    assert torch.equal(got.isnan(), want.isnan())
+    some = want.isinf()
+    assert torch.equal(got[some], want[some])
+    rest = ~want.isnan() & ~some
+    rel = torch.as_tensor(rel, device="cuda").expand_as(want)[rest]
+    step = 2.0 ** -24 if wide else 2.0 ** -8
+    # (a value below the smallest normal one may be zero)
+    assert ((got[rest] - want[rest]).abs() <= want[rest].abs() * (step + rel) + 2.0 ** -126).all()
