@@ -22,11 +22,11 @@ namespace mk {
 namespace {
 
 // ------------------------------------------------------------------------------------------ router
-// A cluster of 8 CTAs has TT tokens and an eighth of the experts a CTA.  A selection can hang on the last bits of two scores.  So
-// the fp32 scores come with a bound of their error, and those that lie within it of one another around the selection (one token in
+// A cluster of CTAS has TT tokens and its share of the experts a CTA (MANY: more than 64 experts).  A selection can hang on the last
+// bits of two scores.  So the fp32 scores come with a bound of their error, and those that lie within it of one another around the selection (one token in
 // twenty has such) are computed once more from exact products (two bf16 factors fit fp32), the errors of all additions carried
 // along.  (All scores that way: 128 tokens 19 us; every sum of four terms that way, 25.)
-constexpr int kRouterCtas = 8, kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
+constexpr int kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
 
 // (hi, lo) += v, the error of hi + v to lo; two sums at once
 __device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t v) {
@@ -90,6 +90,8 @@ __device__ __forceinline__ unsigned long long score_key(double d) {
 
 struct RouterShared {
   float2 score[kOpMaxExperts];           // of the token that this CTA selects for, and what it may be off by
+  float4 flat[kOpMaxExperts / 4];        // the scores alone; -infinity beyond the last
+  float best[kMoeTopK + 1];              // ... of the first ranks, in their order
   unsigned long long key[kOpMaxExperts];
   int rank[kOpMaxExperts];
   uint32_t close[kOpMaxExperts / 32];    // experts whose scores are not told apart
@@ -100,15 +102,15 @@ struct RouterShared {
   float value[kMoeTopK];
 };
 
-template <int TT>
-__global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThreads) router_kernel(const __grid_constant__ MoeParams p) {
+template <int TT, int CTAS, bool MANY>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kRouterThreads) router_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ __align__(16) uint8_t raw_x[];  // the tokens' rows
   __shared__ RouterShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const int t0 = (int)(blockIdx.x / kRouterCtas) * TT, E = p.a.n_experts, d = p.a.d_model;
-  const int per = (E + kRouterCtas - 1) / kRouterCtas, e0 = (int)rank * per, e1 = min(E, e0 + per);
+  const int t0 = (int)(blockIdx.x / CTAS) * TT, E = p.a.n_experts, d = p.a.d_model;
+  const int per = (E + CTAS - 1) / CTAS, e0 = (int)rank * per, e1 = min(E, e0 + per);
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (all CTAs have started: waited for below)
   if (tid < kOpMaxExperts / 32) sh.close[tid] = 0;
   if (tid == 0) sh.most = sh.odd = 0;
@@ -204,57 +206,82 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
     const float off = tid < E ? unit * sqrtf(sh.score[tid].y) + 0x1p-120f : 0.f;
     if (tid < E) sh.score[tid].y = off;
     const int most = __reduce_max_sync(0xffffffffu, __float_as_int(off));  // (not negative: in the order of the bits)
+    if (MANY) {
+      reinterpret_cast<float*>(sh.flat)[tid] = tid < E ? sh.score[tid].x : -INFINITY;
+      if (tid <= K) sh.best[tid] = NAN;
+    }
     const bool odd = tid < E && !(fabsf(sh.score[tid].x) < INFINITY && off < INFINITY);
     if (lane == 0) atomicMax(&sh.most, most);
     if (odd) sh.odd = 1;
   }
   __syncthreads();
-  // An expert's rank: how many come before it; and whether another's score is too close to tell.  (Two threads an expert, or four
-  // where there are few.)
+  // An expert's rank: how many come before it.  (Two threads an expert, or four where there are few.)
   const int share = kRouterThreads / kOpMaxExperts * (E <= kOpMaxExperts / 2 ? 2 : 1);
   const int e = tid / share, part = tid % share;
   const float2 mine = sh.score[min(e, E - 1)];
-  int n = 0, near = 0;
+  int n = 0;
+  bool unsure = true;
+  if (MANY) {
+    // The larger scores are counted first.  That is it where neighbours among the first ranks lie further apart than two
+    // scores can be off together.  (Equal ones leave a rank without a score, a NaN here.  128 experts, 4 tokens: 57.1 us without
+    // this, 56.1; 32 experts, 1 token: 12.4 without, 12.8.)
 #pragma unroll 4
-  for (int f = part; f < E; f += share) {
-    const float2 other = sh.score[f];
-    n += other.x > mine.x || (other.x == mine.x && f < e);
-    near |= f != e && !(fabsf(mine.x - other.x) > mine.y + other.y);
-  }
-  for (int o = share / 2; o; o >>= 1) {
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-    near |= __shfl_xor_sync(0xffffffffu, near, o);
-  }
-  if (part == 0 && e < E) {
-    sh.rank[e] = n;
-    if (n == K) sh.bound = mine.x;
-  }
-  __syncthreads();
-  // Only those that may be among the first K count: not below the score of rank K by more than twice the largest error.  (Where there
-  // is no such rank, or NaN among the scores, all of them.)
-  near = near && e < E && (sh.odd || K >= E || mine.x >= sh.bound - 2.f * __int_as_float(sh.most));
-  if (near && part == 0) atomicOr(sh.close + (e >> 5), 1u << (e & 31));
-  if (__syncthreads_or(near)) {
-    for (int i = tid; i < E; i += kRouterThreads) sh.key[i] = score_key((double)sh.score[i].x);
-    __syncthreads();
-    int turn = 0;
-    for (int i0 = 0; i0 < E; i0 += 32)
-      for (uint32_t left = sh.close[i0 >> 5]; left; left &= left - 1, turn = (turn + 1) % kRouterWarps)
-        if (turn == warp) {
-          const int i = i0 + __ffs(left) - 1;
-          const double s = exact_score(router + (long long)i * d, x + rank * vecs, vecs);
-          if (lane == 0) sh.key[i] = score_key(s), sh.score[i].x = (float)s;
-        }
-    __syncthreads();
-    n = 0;
-    const unsigned long long key = sh.key[min(e, E - 1)];
-    for (int f = part; f < E; f += share) {
-      const unsigned long long other = sh.key[f];
-      n += other > key || (other == key && f < e);
+    for (int f = part; 4 * f < E; f += share) {
+      const float4 other = sh.flat[f];
+      n += (other.x > mine.x) + (other.y > mine.x) + (other.z > mine.x) + (other.w > mine.x);
     }
     for (int o = share / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (part == 0 && e < E) sh.rank[e] = n;
+    if (part == 0 && e < E) {
+      sh.rank[e] = n;
+      if (n <= K) sh.best[n] = mine.x;
+    }
     __syncthreads();
+    unsure = __syncthreads_or(sh.odd || (tid < K && tid + 1 < E && !(sh.best[tid] - sh.best[tid + 1] > 2.f * __int_as_float(sh.most))));
+  }
+  if (unsure) {  // every pair with its own errors
+    int near = 0;
+    n = 0;
+#pragma unroll 4
+    for (int f = part; f < E; f += share) {
+      const float2 other = sh.score[f];
+      n += other.x > mine.x || (other.x == mine.x && f < e);
+      near |= f != e && !(fabsf(mine.x - other.x) > mine.y + other.y);
+    }
+    for (int o = share / 2; o; o >>= 1) {
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+      near |= __shfl_xor_sync(0xffffffffu, near, o);
+    }
+    if (part == 0 && e < E) {
+      sh.rank[e] = n;
+      if (n == K) sh.bound = mine.x;
+    }
+    __syncthreads();
+    // Only those that may be among the first K count: not below the score of rank K by more than twice the largest error.  (Where
+    // there is no such rank, or NaN among the scores, all of them.)
+    near = near && e < E && (sh.odd || K >= E || mine.x >= sh.bound - 2.f * __int_as_float(sh.most));
+    if (near && part == 0) atomicOr(sh.close + (e >> 5), 1u << (e & 31));
+    if (__syncthreads_or(near)) {
+      for (int i = tid; i < E; i += kRouterThreads) sh.key[i] = score_key((double)sh.score[i].x);
+      __syncthreads();
+      int turn = 0;
+      for (int i0 = 0; i0 < E; i0 += 32)
+        for (uint32_t left = sh.close[i0 >> 5]; left; left &= left - 1, turn = (turn + 1) % kRouterWarps)
+          if (turn == warp) {
+            const int i = i0 + __ffs(left) - 1;
+            const double s = exact_score(router + (long long)i * d, x + rank * vecs, vecs);
+            if (lane == 0) sh.key[i] = score_key(s), sh.score[i].x = (float)s;
+          }
+      __syncthreads();
+      n = 0;
+      const unsigned long long key = sh.key[min(e, E - 1)];
+      for (int f = part; f < E; f += share) {
+        const unsigned long long other = sh.key[f];
+        n += other > key || (other == key && f < e);
+      }
+      for (int o = share / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (part == 0 && e < E) sh.rank[e] = n;
+      __syncthreads();
+    }
   }
   if (tid < E && sh.rank[tid] < K) {
     sh.chosen[sh.rank[tid]] = tid;
@@ -682,12 +709,21 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
 }
 
 // ----------------------------------------------------------------------------------------- launches
-template <int TT>
+template <int TT, int CTAS, bool MANY>
 cudaError_t launch_router(const MoeParams& p, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(router_kernel<TT>, TT * kMoeWidest * 2, done);
+  static std::atomic<unsigned long long> done{0}, done_wide{0};
+  cudaError_t e = allow_smem(router_kernel<TT, CTAS, MANY>, TT * kMoeWidest * 2, done);
+  if (e == cudaSuccess && CTAS > 8) e = allow_wide_clusters(router_kernel<TT, CTAS, MANY>, done_wide);
   if (e != cudaSuccess) return e;
-  return launch_early(router_kernel<TT>, dim3((unsigned)((p.a.n_tokens + TT - 1) / TT * kRouterCtas)), kRouterThreads, (size_t)TT * p.a.d_model * 2, st, p);
+  return launch_early(router_kernel<TT, CTAS, MANY>, dim3((unsigned)((p.a.n_tokens + TT - 1) / TT * CTAS)), kRouterThreads, (size_t)TT * p.a.d_model * 2, st, p);
+}
+
+template <bool MANY>
+cudaError_t launch_router(const MoeParams& p, int tt, cudaStream_t st) {
+  return tt == 1   ? launch_router<1, 8, MANY>(p, st)
+         : tt == 2 ? launch_router<2, 8, MANY>(p, st)
+         : tt == 4 ? launch_router<4, 8, MANY>(p, st)
+                   : launch_router<8, 8, MANY>(p, st);
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
@@ -764,11 +800,13 @@ void moe_shape(MoeParams& p) {
 }
 
 cudaError_t launch_moe_router(const MoeParams& p, cudaStream_t st) {
-  const int t = p.a.n_tokens, clusters = std::max(1, p.grid / kRouterCtas);  // (one CTA an SM)
-  const cudaError_t e = t <= clusters       ? launch_router<1>(p, st)
-                        : t <= 2 * clusters ? launch_router<2>(p, st)
-                        : t <= 4 * clusters ? launch_router<4>(p, st)
-                                            : launch_router<8>(p, st);
+  // As few tokens a cluster as keep it at one CTA an SM.  For hardly any tokens a cluster of 16 where its CTAs still have 32 KB of
+  // weights each (1 token, 128 x 2048: 23.8 us in place of 24.2; 32 x 1024: 13.2 and 12.8).
+  const int t = p.a.n_tokens, clusters = std::max(1, p.grid / 8);
+  const bool wide = t <= 4 && (long long)p.a.n_experts * p.a.d_model * 2 >= 16 * 32768;
+  const int tt = t <= clusters ? 1 : t <= 2 * clusters ? 2 : t <= 4 * clusters ? 4 : 8;
+  const cudaError_t e = p.a.n_experts > 64 ? wide ? launch_router<1, 16, true>(p, st) : launch_router<true>(p, tt, st)
+                                           : wide ? launch_router<1, 16, false>(p, st) : launch_router<false>(p, tt, st);
   if (e != cudaSuccess || p.nt) return e;
   return launch_early(sort_kernel, dim3(1), kSortThreads, 0, st, p);
 }
