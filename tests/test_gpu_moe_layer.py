@@ -177,3 +177,55 @@ def test_many_calls_side_by_side():
 def test_weights_beyond_32_bits(t):
     """More than 2^32 bytes in each of the experts' tensors."""
     check(t, 40, 2, 8192, 8192)
+
+
+@pytest.mark.parametrize("t,d", [(1, 2048), (4, 2048), (6, 256), (50, 256), (200, 72)])
+@pytest.mark.parametrize("e,k", [(65, 4), (128, 8), (256, 16)])
+def test_equal_scores_among_many_experts(t, d, e, k):
+    """Ties inside the selection, at its border and behind it, and nothing but ties."""
+    def inside(x, router):
+        router[40] = router[3]
+        router[e - 1] = router[10]
+    check(t, e, k, d, 16, spoil=inside)
+
+    def border(x, router):
+        router[k // 2:] = router[k // 2]
+    check(t, e, k, d, 16, spoil=border)
+
+    def nothing(x, router):
+        router[:] = 0
+    check(t, e, k, d, 16, spoil=nothing)
+
+
+def test_many_scores_that_differ_in_their_last_bits():
+    """As above with 100 experts: the selected five lie within 2^-30 of the terms' sizes of one another, the others far below."""
+    d = 512
+    x = torch.ones(3, d, dtype=torch.bfloat16, device="cuda")
+    x[:, 1::2] = -1
+    x[:, -1] = 0
+    router = torch.zeros(100, d, dtype=torch.bfloat16, device="cuda")
+    router[:] = torch.linspace(100, 200, d // 2, device="cuda").repeat_interleave(2).to(torch.bfloat16)   # (pairs cancel)
+    router[:, -1] = 0
+    router[:, -2] = -5
+    for i, e in enumerate([7, 31, 64, 65, 99]):
+        router[e, -2] = 2.0 ** -14 * (1 + (2 * i) % 5)
+    g = R.gen(18)
+    _, gate, up, down = weights(g, 100, d, 64)
+    ids = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+    ops.moe_layer(x, router, gate, up, down, 4, ids=ids)
+    want, _ = M.select(M.scores(x, router), 4)
+    assert torch.equal(ids.long(), want) and want[0].tolist() == [64, 99, 31, 65]   # (5, 4, 3 and 2 of 1, 3, 5, 2, 4)
+
+
+def test_many_scores_that_are_not_finite():
+    g = R.gen(19)
+    x, (router, gate, up, down) = R.bf16(g, 5, 64), weights(g, 90, 64, 32)
+    x[1, 3] = float("nan")
+    x[2, 4] = float("inf")
+    router[80, 5] = float("inf")           # (one expert's scores, of any sign, for every token)
+    ids = torch.zeros(5, 3, dtype=torch.int32, device="cuda")
+    ops.moe_layer(x, router, gate, up, down, 3, ids=ids)
+    assert ids.min() >= 0 and ids.max() < 90 and all(len(set(r)) == 3 for r in ids.tolist())
+    fine = [0, 3, 4]
+    want, _ = M.select(M.scores(x, router)[fine], 3)
+    assert torch.equal(ids[fine].long(), want)
