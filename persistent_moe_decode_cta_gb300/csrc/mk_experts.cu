@@ -244,7 +244,9 @@ __device__ __noinline__ bool find_tile(const ExpertParams& p, const ExpShared& s
   x.w0 = (t - rt * wblocks) * wstep;
   // the expert's rows in equal tiles
   const int2 r = sh.rows[lo];
-  const int mine = sh.pre[lo + 1] - sh.pre[lo], per = mine == 1 ? r.y - r.x : (r.y - r.x + mine - 1) / mine;
+  const int mine = sh.pre[lo + 1] - sh.pre[lo];
+  int per = mine == 1 ? r.y - r.x : (r.y - r.x + mine - 1) / mine;
+  if (p.pairs) per += per & 1;  // (a tile's rows are an even number at most)
   x.r0 = r.x + (rt - sh.pre[lo]) * per;
   x.nr = min(per, r.y - x.r0);
   return true;
@@ -501,6 +503,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
           for (int c = 0; c < 4; ++c)
             if (32 * c + 16 * part < x.nr) {
               const int r = 32 * c + 16 * part;
+              if (p.pairs) {  // eight rows from sixteen
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = i < 8 ? sum[c][2 * i & 15] + sum[c][(2 * i + 1) & 15] : 0.f;
+                linear_store<true>(p.a, epi, at, v, ahead, (x.r0 + r) / 2, min(8, (x.nr - r) / 2), w0, width, bias, mine_g, lane);
+                continue;
+              }
               if (c > 0) {
                 at.out += 8 * at.out4, at.res += 8 * at.res4;
                 linear_ahead(epi, at, ahead, x.nr - r, width, lane);
@@ -577,20 +586,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
             v[i] = up ? silu(y) * v[i] : silu(v[i]) * y;
           }
         }
+        const int r0 = c + (up ? kTake : 0), rows = min(kTake, x.nr - r0);
+        uint16_t* out = static_cast<uint16_t*>(p.a.out) + (x.r0 + r0) * p.a.out_stride + w0;
+        auto store = [&]() {
+          __syncwarp();
+          if (wide) {
+            if (8 * (lane & 3) < width)
+              for (int r = lane >> 2; r < rows; r += 8)
+                *reinterpret_cast<uint4*>(out + r * p.a.out_stride + 8 * (lane & 3)) =
+                    *reinterpret_cast<const uint4*>(stage + r * 32 + 8 * (lane & 3));
+          } else if (lane < width) {
+            for (int r = 0; r < rows; ++r) out[r * p.a.out_stride + lane] = stage[r * 32 + lane];
+          }
+          __syncwarp();
+        };
 #pragma unroll
         for (int i = 0; i < kTake; ++i) stage[i * 32 + lane] = to_bf16(v[i]);
-        __syncwarp();
-        const int r0 = c + (up ? kTake : 0), rows = min(kTake, x.nr - r0);
-        uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (x.r0 + r0) * p.a.out_stride + w0;
-        if (wide) {
-          if (8 * (lane & 3) < width)
-            for (int r = lane >> 2; r < rows; r += 8)
-              *reinterpret_cast<uint4*>(out + r * p.a.out_stride + 8 * (lane & 3)) =
-                  *reinterpret_cast<const uint4*>(stage + r * 32 + 8 * (lane & 3));
-        } else if (lane < width) {
-          for (int r = 0; r < rows; ++r) out[r * p.a.out_stride + lane] = stage[r * 32 + lane];
+        store();
+        if (GLU && p.rest) {
+          out += p.rest;
+#pragma unroll
+          for (int i = 0; i < kTake; ++i) stage[i * 32 + lane] = bf16_rest(v[i]);
+          store();
         }
-        __syncwarp();
       }
     }
   }

@@ -1,6 +1,6 @@
 // The routed layer of a few tokens:  out = residual + sum_j c_j Wd[id_j] (silu(Wg[id_j] x) * (Wu[id_j] x)).
 //
-// router_kernel: scores, selection, weights.  Then, for up to 16 tokens, layer_kernel: both products in one kernel, one CTA per
+// router_kernel: scores, selection, weights.  Then, for up to 8 tokens, layer_kernel: both products in one kernel, one CTA per
 // SM, with the first product's results handed over inside it so that the second one's weights are under way while the last
 // results of the first are added up.  For more tokens the products of mk_experts.cu, between sort_kernel and sum_kernel.
 //
@@ -15,6 +15,7 @@
 // yet to start.  Second product: a CTA has up to 16 output columns and goes through all experts with them, the warps taking steps
 // in turn; their sums meet at the end, in the order of the warps, and no partial results leave the CTA.
 #include <algorithm>
+#include <type_traits>
 
 #include "mk_linear.cuh"
 
@@ -305,6 +306,7 @@ constexpr int kLayerThreads = 256, kLayerWarps = kLayerThreads / 32;
 constexpr int kSpan = 64;         // columns of a copy: one 128-byte swizzle span
 constexpr int kStepK = 2 * kSpan;
 constexpr int kTileBytes = 4096;  // weights of a step: 16 rows, two copies of 2 KB
+constexpr int kGroupBytes = 2048;  // ... and of eight rows of x or h
 constexpr int kMaxSlots = 8;      // of a warp's ring
 
 struct LayerShared {
@@ -317,12 +319,12 @@ struct LayerShared {
 // offsets in dynamic shared memory; the same on host and device
 struct LayerSmem {
   int rows, red, weight, total;
-  __host__ __device__ LayerSmem(int nt, int slots, int d, int entries) {
+  __host__ __device__ LayerSmem(int groups, int slots, int d, int entries) {
     rows = kLayerWarps * slots * kTileBytes;  // behind the weights' rings: x, and later the rings for rows of h
-    const int x = (d + kStepK - 1) / kStepK * nt * 2048, h = kLayerWarps * slots * nt * 2048;
+    const int x = (d + kStepK - 1) / kStepK * kGroupBytes, h = kLayerWarps * slots * groups * kGroupBytes;
     red = rows + (x > h ? x : h);
-    weight = red + kLayerWarps * nt * 32 * 16;
-    total = weight + entries * nt * 8 * 4 + 1024;
+    weight = red + kLayerWarps * 32 * 16;
+    total = weight + entries * 8 * 4 + 1024;
   }
 };
 
@@ -332,11 +334,15 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int
                : "memory");
 }
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+template <int N>
+using Number = std::integral_constant<int, N>;
 __device__ __forceinline__ float moe_silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-// Up to 8 NT tokens.  A tile's rows are the tokens, all of them for every expert, with zeros in h for those that have not selected
-// it: x is laid out once, and the second product adds its experts up in registers.
-template <int NT>
+// Up to 8 tokens.  A tile's rows are the tokens, all of them for every expert, with zeros in h for those that have not selected it: x
+// is laid out once, and the second product adds its experts up in registers.  h is kept as a sum of two bf16 values: rounded to one, it
+// would be off by as much as the result's own rounding (outputs 1.41 times as far off in the 2-norm).  Up to 4 tokens the second
+// values take the other four of eight rows (GROUPS 1), else eight more (2).
+template <int GROUPS>
 __global__ void __launch_bounds__(kLayerThreads, 1)
     layer_kernel(const __grid_constant__ MoeParams p, const __grid_constant__ CUtensorMap tgate, const __grid_constant__ CUtensorMap tup,
                  const __grid_constant__ CUtensorMap tdown, const __grid_constant__ CUtensorMap th) {
@@ -344,7 +350,8 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   __shared__ LayerShared sh;
   const int tid = threadIdx.x, warp = (int)uniform(threadIdx.x >> 5), lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int T = p.a.n_tokens, K = p.a.top_k, d = p.a.d_model, f = p.a.d_ff, entries = T * K, S = p.slots;
-  const LayerSmem at(NT, S, d, entries);
+  constexpr int kRest = GROUPS == 1 ? 4 : 8;  // rows from a token's first part of h to its second
+  const LayerSmem at(GROUPS, S, d, entries);
   const uint32_t base = (smem_u32(raw_) + 1023u) & ~1023u;
   uint8_t* const raw = raw_ + (base - smem_u32(raw_));
   float4* const red = reinterpret_cast<float4*>(raw + at.red);
@@ -363,7 +370,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
   }
   if (tid < kOpMaxExperts / 32) sh.mask[tid] = 0;
-  for (int i = tid; i < entries * NT * 8; i += kLayerThreads) weight[i] = -1.f;
+  for (int i = tid; i < entries * 8; i += kLayerThreads) weight[i] = -1.f;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -377,11 +384,11 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   }
   const int steps_up = (d + kStepK - 1) / kStepK, steps_down = (f + kStepK - 1) / kStepK;
   const uint32_t tiles_at = base + warp * (S * kTileBytes), rows_at = base + at.rows;
-  for (int i = tid; i < steps_up * NT * 128; i += kLayerThreads) {  // 16 bytes each: [step][span][row][8], swizzled
-    const int c = i & 7, r = (i >> 3) & (8 * NT - 1), span = i / (64 * NT), k = span * kSpan + 8 * c;
+  for (int i = tid; i < steps_up * 128; i += kLayerThreads) {  // 16 bytes each: [step][span][row][8], swizzled
+    const int c = i & 7, r = (i >> 3) & 7, span = i / 64, k = span * kSpan + 8 * c;
     if (r < T) {
       const uint16_t* const row = static_cast<const uint16_t*>(p.a.x) + r * p.a.x_stride;
-      op_cp16(rows_at + (span * NT * 8 + r) * 128 + ((c ^ (r & 7)) << 4), k < d ? row + k : row, k < d ? 16 : 0);
+      op_cp16(rows_at + (span * 8 + r) * 128 + ((c ^ r) << 4), k < d ? row + k : row, k < d ? 16 : 0);
     }
   }
   if (tid < entries) atomicOr(sh.mask + (my_id >> 5), 1u << (my_id & 31));
@@ -396,7 +403,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     if ((sh.mask[tid >> 5] >> (tid & 31)) & 1) sh.act[a] = tid;
     if (tid == p.a.n_experts - 1) sh.n_act = a + ((sh.mask[tid >> 5] >> (tid & 31)) & 1);
   }
-  if (tid < entries) weight[place(my_id) * (8 * NT) + tid / K] = my_weight;
+  if (tid < entries) weight[place(my_id) * 8 + tid / K] = my_weight;
   __syncthreads();
   const int A = (int)uniform(sh.n_act), groups = f / 8, units = A * groups, runs = (int)gridDim.x;
 
@@ -433,8 +440,8 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   if (id.block < blocks) down_fit(id);
   ib = id;
   int ahead = 0;  // steps of the second product whose weights are under way and whose rows are not
-  const uint32_t down_bytes = 2 * (p.width * 128 + NT * 1024);
-  const uint32_t h_at = rows_at + warp * (S * NT * 2048);
+  const uint32_t down_bytes = 2 * p.width * 128 + GROUPS * kGroupBytes;
+  const uint32_t h_at = rows_at + warp * (S * GROUPS * kGroupBytes);
 
   auto issue_weights = [&]() {
     const int row = (int)uniform(sh.act[id.a] * d + id.block * p.width);
@@ -451,9 +458,9 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   };
   auto issue_rows = [&](uint32_t slot) {
     if (elect_one()) {
-      const uint32_t dst = h_at + slot * (NT * 2048), bar = bars + 8 * slot;
-      tma_box(dst, &th, ib.s * kStepK, ib.a * (8 * NT), bar);
-      tma_box(dst + NT * 1024, &th, ib.s * kStepK + kSpan, ib.a * (8 * NT), bar);
+      const uint32_t dst = h_at + slot * (GROUPS * kGroupBytes), bar = bars + 8 * slot;
+      tma_box(dst, &th, ib.s * kStepK, ib.a * (8 * GROUPS), bar);
+      tma_box(dst + GROUPS * kGroupBytes / 2, &th, ib.s * kStepK + kSpan, ib.a * (8 * GROUPS), bar);
     }
     __syncwarp();
     ib.s += kLayerWarps;
@@ -493,15 +500,15 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
   };
 
   // (several sums a tile, so that the products need not wait for one another)
-  constexpr int kSets = NT == 1 ? 4 : 2;
-  float sum[kSets][NT][4];
+  constexpr int kSets = 4;
+  float sum[kSets][4];
   auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < kSets; ++k)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sum[k][j][0] = sum[k][j][1] = sum[k][j][2] = sum[k][j][3] = 0.f;
+    for (int k = 0; k < kSets; ++k) sum[k][0] = sum[k][1] = sum[k][2] = sum[k][3] = 0.f;
   };
-  auto multiply = [&](uint32_t rows) {
+  // one step with eight rows of x, or GROUPS times eight rows of h
+  auto multiply = [&](uint32_t rows, auto groups) {
+    constexpr int kGroups = decltype(groups)::value;
     op_wait(bars + 8 * get.slot, get.phase, &sh.abort, p.a.status, 2);
     const uint32_t tile = a_at + get.slot * kTileBytes;
 #pragma unroll
@@ -511,21 +518,17 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
       ldsm_x4(t + x, a[0], a[1], a[2], a[3]);
       ldsm_x4(t + (x ^ 32), a[4], a[5], a[6], a[7]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < kGroups; ++j) {
         uint32_t b[4];
-        ldsm_x4(rows + (half >> 1) * (NT * 1024) + j * 1024 + (b_at ^ ((half & 1) << 6)), b[0], b[1], b[2], b[3]);
-        mma_bf16(sum[(2 * half) % kSets][j], a[0], a[1], a[2], a[3], b[0], b[1]);
-        mma_bf16(sum[(2 * half + 1) % kSets][j], a[4], a[5], a[6], a[7], b[2], b[3]);
+        ldsm_x4(rows + (half >> 1) * (kGroups * kGroupBytes / 2) + j * 1024 + (b_at ^ ((half & 1) << 6)), b[0], b[1], b[2], b[3]);
+        mma_bf16(sum[(2 * half) % kSets], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_bf16(sum[(2 * half + 1) % kSets], a[4], a[5], a[6], a[7], b[2], b[3]);
       }
     }
     __syncwarp();
     get.advance(S);
   };
-  auto total = [&](int j, int i) {
-    float v = sum[0][j][i] + sum[1][j][i];
-    if (kSets == 4) v += sum[kSets - 2][j][i] + sum[kSets - 1][j][i];
-    return v;
-  };
+  auto total = [&](int i) { return (sum[0][i] + sum[1][i]) + (sum[2][i] + sum[3][i]); };
 
   unsigned made = 0;
   bool first = true;
@@ -544,21 +547,21 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     for (int u = u0 + warp; u < u1; u += kLayerWarps) {
       clear();
       for (int s = 0; s < steps_up; ++s) {
-        multiply(rows_at + s * (NT * 2048));
+        multiply(rows_at + s * kGroupBytes, Number<1>());
         issue_next();
       }
       const int a = u / groups, col = 8 * (u - a * groups) + g;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = 8 * j + 2 * q + i;
-          if (t < T) {
-            // (c < 0: the token has not selected the expert, and its product does not count, whatever it is)
-            const float c = weight[a * (8 * NT) + t], y = c * (moe_silu(total(j, i)) * total(j, i + 2));
-            p.h[(long long)(a * (8 * NT) + t) * f + col] = c < 0.f ? (uint16_t)0 : to_bf16(y);
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * q + i;
+        if (t < T) {
+          // (c < 0: the token has not selected the expert, and its product does not count, whatever it is)
+          const float c = weight[a * 8 + t], y = c * (moe_silu(total(i)) * total(i + 2));
+          uint16_t* const h = p.h + (long long)(a * (8 * GROUPS) + t) * f + col;
+          h[0] = c < 0.f ? (uint16_t)0 : to_bf16(y);
+          h[(long long)kRest * f] = c < 0.f ? (uint16_t)0 : bf16_rest(y);
         }
+      }
     }
     made += (unsigned)(u1 - u0);
     // (until the claim is known there may be weights to fetch, but nothing says which)
@@ -596,26 +599,28 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     clear();
     // (a value a thread: the residual is on its way before its sum is there)
     const int c = tid & 15, t = tid >> 4;
-    const bool mine = tid < NT * 128 && t < T && c < wide;
+    const bool mine = tid < 128 && t < T && c < wide;
     const uint16_t* const residual = static_cast<const uint16_t*>(p.a.residual);
     const float ahead_y = mine && residual ? bf16_to_f(op_ld2(residual + t * p.a.residual_stride + c0 + c)) : 0.f;
     for (int s = warp; s < n; s += kLayerWarps) {
-      multiply(h_at + get.slot * (NT * 2048));
+      multiply(h_at + get.slot * (GROUPS * kGroupBytes), Number<GROUPS>());
       if (id.block < blocks) {
         const uint32_t slot = put;
         issue_weights();
         issue_rows(slot);
       }
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[(warp * NT + j) * 32 + lane] = make_float4(total(j, 0), total(j, 1), total(j, 2), total(j, 3));
+    red[warp * 32 + lane] = make_float4(total(0), total(1), total(2), total(3));
     __syncthreads();
     // the warps' parts, in their order
     if (mine) {
-      const int j = t >> 3, from = (c & 7) * 4 + ((t & 7) >> 1), part = (t & 1) + 2 * (c >> 3);
+      const int from = (c & 7) * 4 + (t >> 1), part = (t & 1) + 2 * (c >> 3);
       float y = 0.f;
 #pragma unroll
-      for (int w = 0; w < kLayerWarps; ++w) y += reinterpret_cast<const float*>(red + (w * NT + j) * 32 + from)[part];
+      for (int w = 0; w < kLayerWarps; ++w) {
+        y += reinterpret_cast<const float*>(red + w * 32 + from)[part];
+        if (GROUPS == 1) y += reinterpret_cast<const float*>(red + w * 32 + from + kRest / 2)[part];
+      }
       if (residual) y += ahead_y;
       static_cast<uint16_t*>(p.a.out)[t * p.a.out_stride + c0 + c] = to_bf16(y);
     }
@@ -669,8 +674,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   if (tid < kOpMaxExperts) {
     for (int w = 0; w < warp; ++w) before += sums[w];
     off[tid] = before - n;
-    if (tid < p.a.n_experts) p.offsets[tid + 1] = before;
-    if (tid == 0) p.offsets[0] = 0;
+    if (tid < p.a.n_experts) p.offsets[tid + 1] = before, p.offsets_h[tid + 1] = 2 * before;
+    if (tid == 0) p.offsets[0] = p.offsets_h[0] = 0;
   }
   __syncthreads();
 #pragma unroll
@@ -731,40 +736,41 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 constexpr int kMostSmem = 232448 - ((int)sizeof(LayerShared) + 127) / 128 * 128;
 
 // slots of a warp's ring that fit: as many as there is room for
-int layer_slots(const mk_moe_args& a, int nt) {
+int layer_slots(const mk_moe_args& a, int groups) {
   for (int s = kMaxSlots; s >= 2; --s)
-    if (LayerSmem(nt, s, a.d_model, a.n_tokens * a.top_k).total <= kMostSmem) return s;
+    if (LayerSmem(groups, s, a.d_model, a.n_tokens * a.top_k).total <= kMostSmem) return s;
   return 0;
 }
 
-template <int NT>
+template <int GROUPS>
 cudaError_t launch_layer(const MoeParams& p, const MoeMaps& m, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(layer_kernel<NT>, kMostSmem, done);
+  const cudaError_t e = allow_smem(layer_kernel<GROUPS>, kMostSmem, done);
   if (e != cudaSuccess) return e;
-  const int smem = LayerSmem(NT, p.slots, p.a.d_model, p.a.n_tokens * p.a.top_k).total;
-  return launch_early(layer_kernel<NT>, dim3((unsigned)p.grid), kLayerThreads, (size_t)smem, st, p, m.gate, m.up, m.down, m.h);
+  const int smem = LayerSmem(GROUPS, p.slots, p.a.d_model, p.a.n_tokens * p.a.top_k).total;
+  return launch_early(layer_kernel<GROUPS>, dim3((unsigned)p.grid), kLayerThreads, (size_t)smem, st, p, m.gate, m.up, m.down, m.h);
 }
 
 }  // namespace
 
-// Row tiles of the kernel for few tokens, 0: the products of mk_experts.cu.  Up to 16 tokens the one kernel, whose tiles waste the
-// fewest products (d_model 2048, 64 of 1024 columns, 8 a token; us of the one kernel / sort, products and sum: 1 token 26.3 / 34.8,
-// 4 57.4 / 71.5, 8 88 / 102, 9 108.7 / 109.5, 12 121 / 128, 16 141 / 147; of a small layer 1 13.5 / 22.3, 16 30.4 / 36.3).
-int moe_tiles(const mk_moe_args& a) {
-  const int nt = a.n_tokens <= 8 ? 1 : a.n_tokens <= kMoeFew ? 2 : 0;
-  return nt && a.n_tokens * a.top_k <= kLayerThreads && layer_slots(a, nt) >= 3 ? nt : 0;
+// Groups of eight rows of h for a kernel of few tokens, 0: the products of mk_experts.cu.  Up to 8 tokens the one kernel, whose tiles
+// waste the fewest products (2048 wide, 128 experts of 768, 8 a token; us of the one kernel / sort, products and sum: 1 token 23.9 / 34.8,
+// 4 55.8 / 71.5, 5 73.2 / 75.2, 8 93.5 / 100.1, 16, with 32 rows of h, 167 / 146; of 32 experts of 1024 x 512 1 12.5 / 22.3, 5
+// 23.0 / 28.2, 8 25.4 / 33.5).
+int moe_groups(const mk_moe_args& a) {
+  const int groups = a.n_tokens <= 4 ? 1 : a.n_tokens <= kMoeFew ? 2 : 0;
+  return groups && a.n_tokens * a.top_k <= kLayerThreads && layer_slots(a, groups) >= 3 ? groups : 0;
 }
 
 long long moe_h_rows(const mk_moe_args& a) {
-  const long long entries = (long long)a.n_tokens * a.top_k, nt = moe_tiles(a);
-  return nt ? 8 * nt * std::min<long long>(a.n_experts, entries) : entries;
+  const long long entries = (long long)a.n_tokens * a.top_k, groups = moe_groups(a);
+  return groups ? 8 * groups * std::min<long long>(a.n_experts, entries) : 2 * entries;
 }
 
 size_t moe_workspace_bytes(const mk_moe_args& a) {
   const size_t entries = (size_t)a.n_tokens * a.top_k;
   size_t n = 16 + 2 * align16(entries * 4) + align16((size_t)moe_h_rows(a) * a.d_ff * 2);
-  if (!moe_tiles(a)) n += 2 * align16(entries * 4) + align16((size_t)(a.n_experts + 1) * 4) + entries * a.d_model * 4;
+  if (!moe_groups(a)) n += 2 * align16(entries * 4) + 2 * align16((size_t)(a.n_experts + 1) * 4) + entries * a.d_model * 4;
   return n;
 }
 
@@ -777,15 +783,15 @@ void moe_shape(MoeParams& p) {
     at += align16(bytes);
     return here;
   };
-  p.nt = moe_tiles(a);
+  p.groups = moe_groups(a);
   p.sync = reinterpret_cast<uint32_t*>(take(16));
   int32_t* const ids = reinterpret_cast<int32_t*>(take(entries * 4));
   float* const weights = reinterpret_cast<float*>(take(entries * 4));
   p.ids = a.ids ? a.ids : ids;
   p.weights = a.weights ? a.weights : weights;
   p.h = reinterpret_cast<uint16_t*>(take((size_t)moe_h_rows(a) * a.d_ff * 2));
-  if (p.nt) {
-    p.slots = layer_slots(a, p.nt);
+  if (p.groups) {
+    p.slots = layer_slots(a, p.groups);
     // output columns: 16 at most, in blocks of equal width over all CTAs
     const int rounds = (a.d_model + 16 * p.grid - 1) / (16 * p.grid);
     p.width = (a.d_model + rounds * p.grid - 1) / (rounds * p.grid);
@@ -793,6 +799,7 @@ void moe_shape(MoeParams& p) {
     p.rows = reinterpret_cast<int32_t*>(take(entries * 4));
     p.places = reinterpret_cast<int32_t*>(take(entries * 4));
     p.offsets = reinterpret_cast<int32_t*>(take((size_t)(a.n_experts + 1) * 4));
+    p.offsets_h = reinterpret_cast<int32_t*>(take((size_t)(a.n_experts + 1) * 4));
     p.y = reinterpret_cast<float*>(at);
   }
   p.vec = a.out_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % 8 == 0 &&
@@ -807,12 +814,12 @@ cudaError_t launch_moe_router(const MoeParams& p, cudaStream_t st) {
   const int tt = t <= clusters ? 1 : t <= 2 * clusters ? 2 : t <= 4 * clusters ? 4 : 8;
   const cudaError_t e = p.a.n_experts > 64 ? wide ? launch_router<1, 16, true>(p, st) : launch_router<true>(p, tt, st)
                                            : wide ? launch_router<1, 16, false>(p, st) : launch_router<false>(p, tt, st);
-  if (e != cudaSuccess || p.nt) return e;
+  if (e != cudaSuccess || p.groups) return e;
   return launch_early(sort_kernel, dim3(1), kSortThreads, 0, st, p);
 }
 
 cudaError_t launch_moe_few(const MoeParams& p, const MoeMaps& m, cudaStream_t st) {
-  return p.nt == 1 ? launch_layer<1>(p, m, st) : launch_layer<2>(p, m, st);
+  return p.groups == 1 ? launch_layer<1>(p, m, st) : launch_layer<2>(p, m, st);
 }
 
 cudaError_t launch_moe_sum(const MoeParams& p, cudaStream_t st) {

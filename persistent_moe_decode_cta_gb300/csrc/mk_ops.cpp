@@ -531,7 +531,7 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
   if (r) return r;
   const auto st = static_cast<cudaStream_t>(stream);
   // (everything that can be refused is before the first launch)
-  if (p.nt) {
+  if (p.groups) {
     MoeMaps m;
     const auto matrix = [&](CUtensorMap* tm, const void* base, long long rows, long long cols, int high) {
       const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -542,7 +542,7 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
     r = matrix(&m.gate, a->w_gate, e * f, d, 8);
     if (!r) r = matrix(&m.up, a->w_up, e * f, d, 8);
     if (!r) r = matrix(&m.down, a->w_down, e * d, f, p.width);
-    if (!r) r = matrix(&m.h, p.h, moe_h_rows(*a), f, 8 * p.nt);
+    if (!r) r = matrix(&m.h, p.h, moe_h_rows(*a), f, 8 * p.groups);
     if (!r) r = cuda_error(launch_moe_router(p, st), "moe_layer launch");
     if (!r) r = cuda_error(launch_moe_few(p, m, st), "moe_layer launch");
     return r;
@@ -552,14 +552,19 @@ int mk_moe_layer(const mk_moe_args* a, void* stream) {
   glu.a.x = a->x;
   glu.a.w = a->w_gate;
   glu.a.w_up = a->w_up;
-  glu.a.offsets = down.a.offsets = p.offsets;
+  glu.a.offsets = p.offsets;
+  down.a.offsets = p.offsets_h;
+  glu.rest = f;  // (h: a row and what its rounding left, one behind the other)
+  down.pairs = 1;
   glu.a.rows = p.rows;
   glu.a.out = p.h;
   glu.a.status = down.a.status = p.a.status;
   glu.a.x_stride = a->x_stride;
-  glu.a.out_stride = down.a.x_stride = f;
+  glu.a.out_stride = 2 * f;
+  down.a.x_stride = f;
   glu.a.n_x = (int32_t)t;
-  glu.a.n_rows = down.a.n_x = down.a.n_rows = (int32_t)tk;
+  glu.a.n_rows = (int32_t)tk;
+  down.a.n_x = down.a.n_rows = (int32_t)(2 * tk);
   glu.a.n_experts = down.a.n_experts = (int32_t)e;
   glu.a.n = down.a.k = (int32_t)f;
   glu.a.k = down.a.n = (int32_t)d;

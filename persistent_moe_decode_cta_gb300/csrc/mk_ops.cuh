@@ -177,6 +177,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// what a rounding to bf16 leaves, as another bf16 (0 where that is no number)
+__device__ __forceinline__ uint16_t bf16_rest(float v) {
+  const float rest = v - bf16_to_f(to_bf16(v));
+  return fabsf(rest) < INFINITY ? to_bf16(rest) : (uint16_t)0;
+}
+
 // 2^x on the special-function unit (2 ulp; -inf gives 0)
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -158,6 +158,10 @@ cudaError_t launch_commit(const CommitParams& p, cudaStream_t st);
 struct ExpertParams {
   mk_expert_args a;
   int grid;
+  // Results as sums of two bf16 rows: where the second part of each lies, in elements behind the first (0: one rounded row), and
+  // whether the rows of x come in such pairs, whose products are added.
+  int64_t rest;
+  int pairs;
 };
 cudaError_t launch_experts(const ExpertParams& p, const CUtensorMap& tx, const CUtensorMap& tx128, const CUtensorMap& tw,
                            const CUtensorMap& tu, cudaStream_t st);
@@ -191,20 +195,20 @@ cudaError_t launch_linear_pairs(const ExpertParams& p, const LinearEpi& epi, con
 // ------------------------------------------------------------------ moe_layer
 constexpr int kMoeTokens = 256;   // tokens of one call
 constexpr int kMoeTopK = 16;
-constexpr int kMoeFew = 16;       // ... of both products in one kernel
+constexpr int kMoeFew = 8;        // ... of both products in one kernel
 constexpr int kMoeWidest = 8192;  // d_model: the tokens stay in shared memory
 struct MoeParams {
   mk_moe_args a;
   int grid;          // CTAs of the products
-  int nt;            // row tiles of 8 (few tokens), or 0
+  int groups;        // few tokens: groups of eight rows of h an expert, else 0
   int width, slots;  // few tokens: output columns of a CTA's block, slots of a warp's ring
   int vec;           // residual and out can be read and written four values at a time
   int32_t* ids;      // the caller's or the workspace's
   float* weights;
-  uint16_t* h;       // [moe_h_rows][d_ff] bf16: silu(gate) * up, of few tokens times c
+  uint16_t* h;       // [moe_h_rows][d_ff] bf16: silu(gate) * up, of few tokens times c, as sums of two values
   uint32_t* sync;    // counters, zeroed by the router
   // more tokens
-  int32_t *offsets, *rows, *places;  // an expert's rows; the token of a row; the row of a token's j-th expert
+  int32_t *offsets, *offsets_h, *rows, *places;  // an expert's rows, and of h, two each; the token of a row; the row of a token's j-th expert
   float* y;          // [rows][d_model]
 };
 struct MoeMaps {

@@ -229,3 +229,16 @@ def test_many_scores_that_are_not_finite():
     fine = [0, 3, 4]
     want, _ = M.select(M.scores(x, router)[fine], 3)
     assert torch.equal(ids[fine].long(), want)
+
+
+@pytest.mark.parametrize("t", [1, 4, 5, 8, 9, 40, 200])
+@pytest.mark.parametrize("e,k,d,f", [(8, 2, 256, 128), (32, 4, 1024, 512)])
+def test_one_rounding_of_the_result(t, e, k, d, f):
+    """In the 2-norm the result is off by its own rounding: what the products add (the inner results, kept to 2^-17, the weights to
+    2^-20, sums of up to 1024 terms in fp32) is below 2^-12.  An inner result in one bf16 value would be as much as the rounding."""
+    g = R.gen(20 + t)
+    x, (router, gate, up, down) = R.bf16(g, t, d), weights(g, e, d, f)
+    got = ops.moe_layer(x, router, gate, up, down, k).double()
+    want = M.moe(x, router, gate, up, down, k)[0]
+    rounding = (want.to(torch.bfloat16).double() - want).norm()
+    assert float((got - want).norm()) <= float(rounding + 2.0 ** -12 * want.norm())
