@@ -403,8 +403,8 @@ int mk_plan_dry(const mk_config* cfg, int batch, int n_sms, int32_t* tasks_out,
  * (mk_tree_attention), multiply by the routed experts' matrices (mk_expert_product), then
  * keep the accepted path (mk_commit_nodes); mk_copy_pages copies pages for a fork.  mk_linear
  * has the projections and the LM head, mk_moe_layer the routed layer of a few tokens as a whole,
- * and mk_verify_nodes decides which drafted tokens are accepted.  The pages have no counterpart to them.  They need no handle and read plain (unpacked) bf16
- * tensors.
+ * and mk_verify_nodes decides which drafted tokens are accepted.  The pages have no counterpart to
+ * them.  They need no handle and read plain (unpacked) bf16 tensors.
  *
  * Conventions beside the ones above:
  *   - Every pointer is a device address on the current device unless it is called a HOST

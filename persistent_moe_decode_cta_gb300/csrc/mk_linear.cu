@@ -5,6 +5,10 @@
 // once, from every SM), and below that a chain: launch, the first copies, products, the slices' sums.  The slices meet in shared
 // memory: each CTA owns a part of the tile's rows, gets every other CTA's sums for them, adds them in the order of the slices and
 // writes its part with the epilogue: nothing but results goes to memory, and equal calls give equal bits.
+//
+// Measured in a graph: 5 rows, 1024 -> 1536 3.3 us, 128 rows, 4096 -> 2048 with a residual 7.8 us (of them weights stream for 2.5, at 7
+// TB/s; 0.6 until the first are there, 0.4 for the last products and reading the sums, 0.7 the exchange, ~1 the epilogue, the rest
+// launch, setup and the end); 2048 x 4096: 1 row 6.4 us, 64 7.9, 256 11.8, 1024 21.4.
 #include <algorithm>
 
 #include "mk_linear.cuh"

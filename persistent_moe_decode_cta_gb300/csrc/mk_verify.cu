@@ -12,6 +12,10 @@
 // largest, right to 2^-32 of themselves), and their sums are exact: neither order nor split matters.  With R the integers
 // left and W their sum, r = R / W, and a rejection leaves (R - q W)+: in terms of the row's exponentials E
 // R = (E - q A)+ where A grows by W with every rejection; E is kept and A is one number.
+//
+// Measured in a graph (float32, 151936 tokens): 8 chains of 9 nodes 28 us, of them the rows 9 (39 MB), the rest the longest walk's chain:
+// nodes 2.5, steps 1 to 2, the row out of L2 and its exponentials 4 to 5, every meeting of the cluster 0.5, a cut 2, the draw 0.5;
+// 16 trees of 32 nodes 73 us (rows 33, 161 MB); bf16, 8 trees of 16 22 us; 5 nodes of 32000 tokens 12 us.
 #include "mk_ops.cuh"
 
 namespace mk {
