@@ -308,12 +308,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads + kGathe
   // copies left 3400 cycles behind it, 1.7 of 27 us at 2001 x 4096.)
   const int whole = EPI && !p.a.offsets ? (p.a.n_rows + epi.tile_rows - 1) / epi.tile_rows : 0;
   ExpTile x;
-  bool any = whole && find_tile(p, sh, 0, whole * wblocks, wblocks, kStep, whole, x);
+  const bool any = whole && find_tile(p, sh, 0, whole * wblocks, wblocks, kStep, whole, x);
   pdl_wait();
   pdl_trigger();
   if (!whole) scan_experts(p, sh, EPI ? epi.tile_rows : kTileR);
   const int tiles = (whole ? whole : (int)uniform(sh.pre[p.a.n_experts])) * wblocks;  // (below 2^31: checked by the host)
-  const uint32_t most = whole ? min(p.a.n_rows, epi.tile_rows) : uniform(min(sh.most, kTileR)), room = most <= 64 ? 32 : most <= 128 ? 64 : 128;  // rows of a stage
+  const uint32_t most = whole ? min(p.a.n_rows, epi.tile_rows) : uniform(min(sh.most, kTileR));
+  const uint32_t room = most <= 64 ? 32 : most <= 128 ? 64 : 128;  // rows of a stage
   const uint32_t stage_bytes = kBytesW + room * kTileK * 2, stages = room == 32 ? 9 : room == 64 ? 8 : 6;
   auto tile = [&](int k, ExpTile& x) -> bool { return uniform(find_tile(p, sh, k, tiles, wblocks, kStep, whole, x)); };
   auto tile1 = [&](int k, ExpTile& x) -> bool { return find_tile(p, sh, k, tiles, wblocks, kStep, whole, x); };  // (one thread)
