@@ -11,7 +11,8 @@
 // move borders enough to change one draw of a few hundred.  So the exponentials of the walk are 64-bit integers (2^-44 of the
 // largest, right to 2^-32 of themselves), and their sums are exact: neither order nor split matters.  With R the integers
 // left and W their sum, r = R / W, and a rejection leaves (R - q W)+: in terms of the row's exponentials E
-// R = (E - q A)+ where A grows by W with every rejection; E is kept and A is one number.
+// R = (E - q A)+ where A grows by W with every rejection; E is kept and A is one number, a double: W is up to 2^62 (2^18 tokens as
+// likely as the largest), and 511 siblings can be rejected in one row.
 //
 // Measured in a graph (float32, 151936 tokens): 8 chains of 9 nodes 28 us, of them the rows 9 (39 MB), the rest the longest walk's chain:
 // nodes 2.5, steps 1 to 2, the row out of L2 and its exponentials 4 to 5, every meeting of the cluster 0.5, a cut 2, the draw 0.5;
@@ -258,10 +259,7 @@ struct Exp {
 // (E - q A)+ with A = ah + am (to 2^-48 of itself), all in units of 2^-44, of two probabilities at once
 struct Cut {
   float ah, am;
-  __device__ __forceinline__ explicit Cut(unsigned long long a) {
-    ah = __ull2float_rn(a);
-    am = (float)(long long)(a - __float2ull_rn(ah));
-  }
+  __device__ __forceinline__ explicit Cut(double a) : ah((float)a), am((float)(a - (double)ah)) {}
   __device__ __forceinline__ U2 operator()(unsigned long long e0, unsigned long long e1, float q0, float q1) const {
     const uint64_t q = pack2(fminf(fmaxf(q0, 0.f), 1.f), fminf(fmaxf(q1, 0.f), 1.f));  // (NaN: 0)
     // q A as th + tl, then as an integer in two steps of 23 bits; E is 2^44 at most
@@ -514,7 +512,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   int at = 0, row_at = -1;
   uint32_t turn = 0;  // passes so far
   // of the row at `at`: A and W, and what this warp has of W
-  unsigned long long A = 0, W = 0, warp_sum = 0;
+  double A = 0;
+  unsigned long long W = 0, warp_sum = 0;
   bool loaded = false, stuck = false;
   // the first thread's: the child to test (-2: at a new node), and before the row is loaded its sum without the tokens that are gone
   int child = -2, length = 0, n_gone = 0;
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     }
     if (step == kCut) {
       if (!stuck) {
-        const Cut cut(A + W);
+        const Cut cut(A + (double)W);
         unsigned long long sum = 0;
         for (int k = 0; k < n_blocks; k += 4) {
           float4 qs[4];
@@ -714,7 +713,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
         sum = warp_total(sum);
         const unsigned long long now = exchange(sh, sum, &turn, a.status);
         if (now) {
-          A += W;
+          A += (double)W;
           W = now;
           warp_sum = sum;
         } else {
@@ -740,7 +739,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
       bool found = false;
       for (int k0 = 0; k0 < n_blocks && !found; k0 += 4) {
         float4 qs[4];
-        if (A) {
+        if (A > 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (k0 + i < n_blocks) qs[i] = load4(drow, base + from + (k0 + i) * kBlock, a.vocab, true, qwide, 0.f);
@@ -752,7 +751,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           const ulonglong2* const at4 = reinterpret_cast<const ulonglong2*>(e + from + k * kBlock);
           const ulonglong2 lo = at4[0], hi = at4[1];
           unsigned long long y[4] = {lo.x, lo.y, hi.x, hi.y};
-          if (A) {
+          if (A > 0) {
             const U2 c = cut(lo.x, lo.y, qs[k4].x, qs[k4].y), d = cut(hi.x, hi.y, qs[k4].z, qs[k4].w);
             y[0] = c.x, y[1] = c.y, y[2] = d.x, y[3] = d.y;
           }

@@ -295,3 +295,31 @@ def test_excluded_drafts_with_siblings():
             for i in range(1, 14, 2):
                 logits[b, int(parents[b, i]), int(tokens[b, i])] = -float("inf")
         check(logits, tokens, uniforms, parents, draft)
+
+
+@pytest.mark.parametrize("v,spread,heat,n", [(262144, 0.0, 1.0, 24), (151936, 2.5, 20.0, 32), (100003, 2.5, 100.0, 32)])
+def test_many_rejections_on_a_flat_row(v, spread, heat, n):
+    """One child after another is cut out of a row of hundreds of thousands of tokens of about the same size: what is cut adds up to
+    many times the whole, and what an earlier rejection has taken stays away, however many there were."""
+    b = 16
+    g = R.gen(110)
+    line = spread * torch.randn(b, v, generator=g, device="cuda")
+    # what was drafted lies in one half of the tokens, with more than the target gives them there
+    half = torch.rand(b, v, generator=g, device="cuda") < 0.5
+    q = torch.where(half, torch.rand(b, v, generator=g, device="cuda") + 0.5, 0.0)
+    q = q / q.sum(-1, keepdim=True)
+    row = torch.arange(b, device="cuda")
+    counts = n - row.to(torch.int32)
+    parents = torch.zeros(b, n, dtype=torch.int32, device="cuda")
+    tokens = q.argmax(-1, keepdim=True).to(torch.int32).repeat(1, n)
+    uniforms = torch.rand(b, n, generator=g, device="cuda")
+    uniforms[:, 1:] = 1 - 2.0 ** -24
+    # (the last child of every fourth sequence is a token of the other half with little of the draft)
+    other = (~half).float().argmax(-1)
+    tokens[row[::4], counts[::4].long() - 1] = other[::4].to(torch.int32)
+    q[row[::4], other[::4]] = 1e-12
+    logits, draft = (torch.zeros(b, n, v, device="cuda") for _ in range(2))
+    logits[:] = line[:, None]
+    draft[:] = q[:, None]
+    path = check(logits, tokens, uniforms, parents, draft, torch.full((b,), heat, device="cuda"), counts)
+    assert [p[1] for p in path] == [int(counts[i]) - 1 if i % 4 == 0 else -1 for i in range(b)]
