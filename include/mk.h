@@ -647,8 +647,8 @@ int mk_moe_layer_workspace(const mk_moe_args* args, size_t* bytes);
  *   next_tokens  int32 [batch]; neither output overlaps an input
  *   workspace mk_verify_nodes_workspace(..) bytes, 16-byte aligned, not shared with a call that may run at
  *             the same time; its contents do not matter
- * The sums that a token is drawn from are exact sums of 64-bit integers (each probability to 2^-32 of itself or 2^-44 of
- * the largest; one below 2^-45 of that is 0), so neither the split of the work nor the order changes a result.
+ * Verdicts and draws go by exact sums of 64-bit integers (each probability to 2^-32 of itself or 2^-44 of the largest; one
+ * below 2^-45 of that is 0), so neither the split of the work nor the order changes a result.
  * vocab in 1..262144, n_nodes in 1..512 (as mk_commit_nodes).  A row of p without a finite largest logit or with a NaN, a count,
  * parent, token, temperature or uniform out of its range is recorded (MK_ERR_INVALID; sequence, node, value); such a child is
  * passed over, a sequence whose count, temperature or p is bad ends there with next_tokens[b] = -1. */

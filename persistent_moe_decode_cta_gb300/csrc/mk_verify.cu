@@ -6,10 +6,12 @@
 // sequence that walks from the root: an accepted child costs no more than a look at shared memory; at the first rejection in a
 // row (or at the last node) the cluster reads that row, out of L2 where it has been read, and from then on keeps the row's
 // exponentials in shared memory, a piece a CTA.  The drafting model's rows are read only where one of its tokens was rejected.
+// Siblings of proposed tokens (no probabilities) need no row, only what the rejected ones had.
 //
 // Numbers.  The drawn token is where a running sum over up to 2^18 probabilities passes u times the whole: errors of fp32 would
 // move borders enough to change one draw of a few hundred.  So the exponentials of the walk are 64-bit integers (2^-44 of the
-// largest, right to 2^-32 of themselves), and their sums are exact: neither order nor split matters.  With R the integers
+// largest, right to 2^-32 of themselves), and their sums are exact: neither order nor split matters.  A verdict is one of those
+// numbers too: where the fp32 sum of row_kernel, to 2^-15, does not tell, the row is added up first.  With R the integers
 // left and W their sum, r = R / W, and a rejection leaves (R - q W)+: in terms of the row's exponentials E
 // R = (E - q A)+ where A grows by W with every rejection; E is kept and A is one number, a double: W is up to 2^62 (2^18 tokens as
 // likely as the largest), and 511 siblings can be rejected in one row.
@@ -280,11 +282,25 @@ struct __align__(16) Node {
   int first, next;     // its first child, its parent's next child; -1: none
   float u;             // its uniform
   float l, q;          // logit and draft probability of the token in the parent's row
-  int fits;            // whether it is accepted as long as no sibling was rejected
+  int fits;            // whether it is accepted as long as no sibling was rejected: a verdict
   float top, sum;      // of its own row
   int arg, pad;
 };
-enum { kCut, kDraw, kEnd };
+enum { kCut, kDraw, kWhole, kEnd };
+
+// Whether a child is accepted, u q left < y, where `left`, what there is of the parent's row, is off by `off` at most; kUnsure: that
+// does not tell.
+enum { kNo, kYes, kUnsure };
+// What is off by where `left` comes from row_kernel's sum, relative to that.  The sum: an exponent (l - top) / T log2(e) by 5 2^-24 of
+// itself (one that matters among 2^18 tokens is 18 at most: 2^-18), the exponentials by 2^-22 a dozen times (themselves and from maximum to
+// maximum: 2^-18), 50 additions by 2^-24 each (2^-18); then half a dozen roundings of the test itself: less than
+constexpr float kSumOff = 0x1p-15f;
+template <class T>
+__device__ __forceinline__ int verdict(T uq, T left, T off, T y) {
+  const T border = uq * left;
+  return fabs(border - y) < uq * off ? kUnsure : border < y ? kYes : kNo;
+}
+__device__ __forceinline__ float unit(unsigned long long y) { return (float)y * 0x1p-44f; }
 
 struct WalkShared {
   Node* node;                          // [n_nodes], and behind them
@@ -431,12 +447,12 @@ __device__ void gather_nodes(const VerifyParams& p, WalkShared& sh, int b, bool 
       if (of == tid) first = j;
       if (of == up) next = j;
     }
-    bool fits = false;
+    int fits = kNo;
     if (up >= 0) {
       const Node x = sh.node[tid], v = sh.node[up];
       const Exp ex{v.top, heat.hi, heat.lo, sh.power};
-      fits = heat.t == 0.f ? x.token == v.arg && x.u * x.q < 1.f  // (p is 1 at the largest)
-                           : (double)x.u * (double)x.q * ((double)v.sum * 0x1p44) < (double)ex(x.l);
+      fits = heat.t == 0.f ? (x.token == v.arg && x.u * x.q < 1.f ? kYes : kNo)  // (p is 1 at the largest)
+                           : verdict(x.u * x.q, v.sum, v.sum * kSumOff, unit(ex(x.l)));
     }
     sh.node[tid].first = first;
     sh.node[tid].next = up < 0 ? -1 : next;
@@ -515,10 +531,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
   double A = 0;
   unsigned long long W = 0, warp_sum = 0;
   bool loaded = false, stuck = false;
-  // the first thread's: the child to test (-2: at a new node), and before the row is loaded its sum without the tokens that are gone
+  // the first thread's: the child to test (-2: at a new node), the proposed tokens that are gone and what they had
   int child = -2, length = 0, n_gone = 0;
+  unsigned long long gone_sum = 0;
   bool whole = true;  // no child rejected yet
-  double left = 0;
 
   for (;;) {
     if (tid == 0) {
@@ -532,6 +548,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           sh.path[length++] = at;
           child = v.first;
           n_gone = 0;
+          gone_sum = 0;
           whole = true;
           // (a NaN in the row is a NaN in the sum.  Nothing is known of a row without children.)
           if (child >= 0 && !(fabsf(v.top) < INFINITY && v.sum > 0.f)) {
@@ -547,36 +564,41 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
           }
         } else {
           const Node& c = sh.node[child];
-          bool taken = c.fits != 0;
-          unsigned long long y = 0;
-          if ((!taken || !whole) && heat.t != 0.f) {
-            if (whole) left = (double)sh.node[at].sum * 0x1p44;
+          const bool proposed = heat.t != 0.f && !a.draft_probs;
+          int taken = whole || heat.t == 0.f ? c.fits : kUnsure;
+          if (taken == kUnsure || (proposed && taken == kNo)) {
             ex.top = sh.node[at].top;
-            y = ex(c.l);
-          }
-          if (!whole && heat.t != 0.f) {
+            unsigned long long y = ex(c.l);
             if (a.draft_probs) {
-              y = Cut(A)(y, c.q);
+              if (!whole) y = Cut(A)(y, c.q);
             } else {
               for (int g = 0; g < n_gone; ++g)
                 if (sh.gone[g] == c.token) y = 0;
             }
-            taken = (double)c.u * (double)c.q * (a.draft_probs ? (double)W : left) < (double)y;
+            bool more;  // whether anything but this token is left
+            if (loaded && row_at == at) {
+              taken = verdict((double)c.u * (double)c.q, (double)(W - gone_sum), 0.0, (double)y);
+              more = W - gone_sum > y;
+            } else {  // (in doubles: 8 trees of 16 nodes 23.3 us in place of 21.7)
+              const float all = sh.node[at].sum, off = all * kSumOff, left = all - unit(gone_sum);
+              taken = verdict(c.u * c.q, left, off, unit(y));
+              more = left - unit(y) > off;
+              if (proposed && taken == kNo && !more) taken = kUnsure;
+            }
+            if (proposed && taken == kNo && y > 0 && more) {
+              gone_sum += y;
+              sh.gone[n_gone++] = c.token;
+            }
           }
-          if (taken) {
+          if (taken == kUnsure) {
+            step = kWhole;
+          } else if (taken == kYes) {
             at = child;
             child = -2;
           } else {
             child = c.next;
             whole = false;
-            if (heat.t != 0.f) {
-              if (a.draft_probs) {
-                step = kCut;
-              } else if (left > (double)y) {
-                left -= (double)y;
-                sh.gone[n_gone++] = c.token;
-              }
-            }
+            if (heat.t != 0.f && a.draft_probs) step = kCut;
           }
         }
       }
@@ -585,10 +607,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
       sh.n_gone = n_gone;
     }
     __syncthreads();
-    const int step = sh.step, gone = sh.n_gone, asked = sh.at;
+    const int step = sh.step, gone = step == kDraw ? sh.n_gone : 0, asked = sh.at;
     __syncthreads();  // (the first thread may go on)
     if (step == kEnd) break;
-    loaded = loaded && row_at == asked;
+    loaded = loaded && row_at == asked && gone == 0;  // (once more without the tokens that are gone)
     at = row_at = asked;
     const bool draft = a.draft_probs != nullptr;
     const float* const drow = draft ? a.draft_probs + b * a.draft_stride[0] + at * a.draft_stride[1] : nullptr;
@@ -692,6 +714,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
       loaded = true;
       stuck = false;
     }
+    if (step == kWhole) continue;
     if (step == kCut) {
       if (!stuck) {
         const Cut cut(A + (double)W);
@@ -724,6 +747,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const __grid_cons
     }
     // ------------------------------------------------------------ the first index whose running sum passes u times the whole
     // (u has 24 bits: u 2^64 is exact from 2^-40 on)
+    if (W == 0) {  // (a wait was given up: something is left of every row)
+      if (tid == 0) sh.next = -1;
+      break;
+    }
     const unsigned long long goal = __umul64hi((unsigned long long)((double)sh.node[0].u * 0x1p64), W);
     if (stuck) {  // (the last pass did not count)
       exchange(sh, warp_sum, &turn, a.status);

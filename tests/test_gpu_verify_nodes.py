@@ -323,3 +323,79 @@ def test_many_rejections_on_a_flat_row(v, spread, heat, n):
     draft[:] = q[:, None]
     path = check(logits, tokens, uniforms, parents, draft, torch.full((b,), heat, device="cuda"), counts)
     assert [p[1] for p in path] == [int(counts[i]) - 1 if i % 4 == 0 else -1 for i in range(b)]
+
+
+@pytest.mark.parametrize("some", [2, 3, 4])
+def test_proposed_tokens_that_are_all_there_is(some):
+    """Logits masked to a few tokens, all of them proposed, and uniforms that reject one after another: the last one is all that is left,
+    and accepted.  Whatever happens, the next token is written."""
+    b, v, n = 400, 37, some + 2
+    g = R.gen(120 + some)
+    place = torch.rand(b, v, generator=g, device="cuda").argsort(-1)[:, :some]
+    logits = torch.full((b, n, v), -float("inf"), device="cuda")
+    size = torch.cumsum(0.5 + 6 * torch.rand(b, some, generator=g, device="cuda"), -1).neg()
+    logits.scatter_(2, place[:, None].expand(b, n, some), size[:, None].expand(b, n, some))
+    tokens = torch.zeros(b, n, dtype=torch.int32, device="cuda")
+    tokens[:, 1:some + 1] = place
+    tokens[:, some + 1] = place[:, 0]
+    parents = torch.zeros(b, n, dtype=torch.int32, device="cuda")
+    uniforms = 1 - 2.0 ** -24 * torch.randint(1, 5, (b, n), generator=g, device="cuda")
+    uniforms[:, 0] = torch.rand(b, generator=g, device="cuda")
+    uniforms = uniforms.float()
+    status = ops.new_status()
+    drawn = torch.full((b,), -5, dtype=torch.int32, device="cuda")
+    accepted, _ = ops.verify_nodes(logits, tokens, uniforms, parents=parents, next_tokens=drawn, status=status)
+    ops.check_status(status)
+    path, nxt = M.verify(logits, tokens, uniforms, parents)
+    assert accepted.tolist() == path and drawn.tolist() == nxt
+    assert sum(p[1] == some for p in path) > b // 4      # (rejections up to the last)
+
+
+def test_two_tokens_of_which_one_is_left():
+    """Two tokens, the likely one rejected: the other one's probability is 1."""
+    logits = torch.tensor([0.0, -5.0625], device="cuda").expand(1, 3, 2).contiguous()
+    tokens = torch.tensor([[0, 0, 1]], dtype=torch.int32, device="cuda")
+    parents = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    uniforms = torch.tensor([[0.3, 0.9995, 0.999997]], device="cuda")
+    assert check(logits, tokens, uniforms, parents) == [[0, 2, -1]]
+
+
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("half,v", [(False, 151936), (True, 151936), (False, 900)])
+def test_verdicts_at_their_border(half, v, probs):
+    """Uniforms next to p / q on either side, 2^-26 of it away at least (probabilities are right to 2^-32), of a first child and of a
+    sibling behind a rejection."""
+    b, n = 64, 3
+    g = R.gen(130)
+    logits, tokens, uniforms, parents, draft = M.tree_inputs(g, b, n, v, True, True, sharp=8.0, half=half)
+    parents[:, 1:] = 0
+    heat = 0.6 + torch.rand(b, generator=g, device="cuda")
+    heat[::4] = 1.0
+    p = torch.softmax(logits[:, 0].double() / heat.double()[:, None], -1)
+    likely = p.topk(3, -1).indices
+    row = torch.arange(b, device="cuda")
+    tokens[:, 1], tokens[:, 2] = likely[:, 1], likely[:, 2]
+    # (probabilities of the draft that leave the border inside (0, 1))
+    at = p[row, likely[:, 1]] * (1 + 2 * torch.rand(b, generator=g, device="cuda"))
+    draft[row, 0, likely[:, 1]] = at.clamp(max=1).float()
+    # (... and some of the target's left at the sibling)
+    draft[row, 0, likely[:, 2]] = (p[row, likely[:, 2]] * (0.1 + 0.7 * torch.rand(b, generator=g, device="cuda"))).float()
+    q = draft[:, 0].double() if probs else torch.nn.functional.one_hot(likely[:, 1], v).double()
+
+    def beside(border, below):
+        u = (border * (1 - 2.0 ** -26 if below else 1 + 2.0 ** -26)).float()
+        off = torch.nextafter(u, torch.full_like(u, 0.0 if below else 1.0))
+        right = u.double() <= border * (1 - 2.0 ** -26) if below else u.double() >= border * (1 + 2.0 ** -26)
+        return torch.where(right, u, off).clamp(max=1 - 2.0 ** -24)
+
+    first = p[row, likely[:, 1]] / q[row, likely[:, 1]]
+    rest = (p - q).clamp(min=0)
+    rest = rest / rest.sum(-1, keepdim=True)
+    second = rest[row, likely[:, 2]] / (draft[row, 0, likely[:, 2]].double() if probs else 1.0)
+    for below in (True, False):
+        uniforms[:, 1] = beside(first, below)
+        path = check(logits, tokens, uniforms, parents, draft if probs else None, heat)
+        assert (sum(x[1] == 1 for x in path) > b // 2) == below
+        uniforms[:, 1] = 1 - 2.0 ** -24            # (rejected, where it can be)
+        uniforms[:, 2] = beside(second, below)
+        check(logits, tokens, uniforms, parents, draft if probs else None, heat)
