@@ -577,7 +577,8 @@ int mk_expert_product(const mk_expert_args* args, void* stream);
  *             be the residual itself (same address, stride and type); it overlaps nothing else
  *   activation  MK_ACT_NONE, _RELU, _SILU (y / (1 + exp(-y))), _GELU (y/2 (1 + erf(y / sqrt 2))) or
  *             _GELU_TANH (y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))))
- * fp32 accumulation in a fixed order (equal calls give equal bits), one rounding. */
+ * fp32 accumulation in a fixed order (equal calls give equal bits), of float32 results in sums of 512 columns at most that are added up
+ * (the products' own sums are not rounded but cut at the last bit), one rounding. */
 enum { MK_ACT_NONE = 0, MK_ACT_RELU = 1, MK_ACT_SILU = 2, MK_ACT_GELU = 3, MK_ACT_GELU_TANH = 4 };
 typedef struct mk_linear_args {
   const void* x;

@@ -18,14 +18,21 @@ namespace {
 
 constexpr int kSplitThreads = 192;  // producer, product issue, four epilogue warps
 constexpr int kSplitW = 128;        // outputs of a tile
+constexpr int kSplitRows = 128;     // ... and rows at most
 constexpr int kSplitK = 64;         // columns of a stage: one 128-byte swizzle span
 constexpr int kSplitStages = 12;
 constexpr int kSplitBytesW = kSplitW * kSplitK * 2;
+// Stages of an accumulator of float32 results.  The products drop what lies below its last bit, so that a sum is off by more the longer it
+// is (2-norm: 512 columns 4.7e-7, 2048 2.1e-6, 16384 1.9e-5): sums of 512 columns are added up in registers, from two accumulators in
+// turn.  A kernel of its own (LONG), which it slows down (float32, 4096 -> 2048: 64 rows 6.1 -> 6.6 us, 128 7.7 ->
+// 8.3, 512 14.9 -> 17.1, 1024 20.6 -> 21.4; with the sums in shared memory 6.8, 8.3, 17.0, 21.6).
+constexpr int kSegment = 8;
+constexpr int kAccCols = 128;  // from one to the other
 
 struct SplitShared {
   uint32_t tmem;
   int abort;
-  unsigned long long bars[2 * kSplitStages + 2];
+  unsigned long long bars[2 * kSplitStages + 5];
 };
 constexpr int kSplitSmem = 232448 - 1024;  // (SplitShared fits the rest)
 
@@ -47,7 +54,7 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* tm, in
                : "memory");
 }
 
-template <bool WIDE>
+template <bool WIDE, bool LONG>
 __global__ void __launch_bounds__(kSplitThreads, 1)
     split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw) {
   extern __shared__ uint8_t raw[];
@@ -62,10 +69,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const uint32_t sums = base + p.ring;  // [slice][owned row][kSplitW]
   float* const sums_g = reinterpret_cast<float*>(raw + (sums - smem_u32(raw)));
   const int own = (p.box + p.slices - 1) / p.slices;  // rows that a CTA owns of the tile
-  const uint32_t bars = smem_u32(sh.bars), done = bars + 8 * 2 * kSplitStages, got = done + 8;
+  const uint32_t bars = smem_u32(sh.bars), got = bars + 8 * 2 * kSplitStages;
   const uint32_t part = own * kSplitW * 4;  // bytes of a slice's sums for a CTA
   auto full = [&](uint32_t s) { return bars + 8 * s; };
   auto empty = [&](uint32_t s) { return bars + 8 * (kSplitStages + s); };
+  auto done = [&](uint32_t a) { return got + 8 + 8 * a; };    // an accumulator is whole
+  auto taken = [&](uint32_t a) { return got + 24 + 8 * a; };  // ... and has been read
 
   if (threadIdx.x == 0) {
     sh.abort = 0;
@@ -73,7 +82,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(done, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(done(a), 1);
+      mbar_init(taken(a), 4);
+    }
     mbar_init(got, 1);
     mbar_expect_tx(got, p.slices * part);
     fence_proxy_async_smem();
@@ -108,30 +120,70 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       const uint32_t idesc = umma_idesc_bf16(kSplitW, p.box);
       const uint64_t d0 = umma_sdesc_sw(base, 16, 1024, 128);
       for (int k = k0; ok && k < k1; ++k, at.advance(stages)) {
+        const uint32_t n = LONG ? (uint32_t)(k - k0) / kSegment : 0;  // accumulators before this one
+        const bool first = k == k0 || (LONG && (k - k0) % kSegment == 0);
+        if (LONG && first && k > k0) {
+          umma_commit(done((n - 1) & 1));
+          if (!(ok = op_wait1(taken(n & 1), (n >> 1 & 1) ^ 1, abort, p.status, 5))) break;
+        }
         if (!(ok = op_wait1(full(at.slot), at.phase, abort, p.status, 2))) break;
         tc_fence_after();
         const uint64_t d = d0 + at.slot * (stage_bytes / 16);
 #pragma unroll
-        for (int kk = 0; kk < kSplitK / 16; ++kk) umma_bf16(tmem, d + 2 * kk, d + kSplitBytesW / 16 + 2 * kk, idesc, k > k0 || kk > 0);
+        for (int kk = 0; kk < kSplitK / 16; ++kk)
+          umma_bf16(tmem + (n & 1) * kAccCols, d + 2 * kk, d + kSplitBytesW / 16 + 2 * kk, idesc, !first || kk > 0);
         umma_commit(empty(at.slot));
       }
-      if (ok) umma_commit(done);
+      if (ok) umma_commit(done(LONG ? (uint32_t)(k1 - 1 - k0) / kSegment & 1 : 0));
     }
     __syncwarp();
   } else {
     // this slice's sums, in order of the rows, then a copy to each CTA of what it owns: a lane has an output, a column of tensor
     // memory is a row of x.  (The ring is free: its products have ended.  Stores of single values into the other CTAs took 6 us for
     // 128 rows by 8 slices.)
-    op_wait(done, 0, abort, p.status, 3);
-    tc_fence_after();
     const int q = warp & 3;
     float* const mine = reinterpret_cast<float*>(raw + ((p.slices > 1 ? base : sums) - smem_u32(raw))) + 32 * q + lane;
-    for (int c = 0; c < rows; c += 16) {
-      uint32_t u[16];
-      tmem_ld16(tmem + c + ((uint32_t)q << 21), u);
-      tmem_wait16(u);
+    if (LONG) {
+      constexpr int kParts = kSplitRows / 16;
+      float sum[kParts][16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mine[(c + i) * kSplitW] = __uint_as_float(u[i]);
+      for (int c = 0; c < kParts; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[c][i] = 0.f;
+      const int segments = (k1 - k0 + kSegment - 1) / kSegment;
+#pragma unroll 1
+      for (int s = 0; s < segments; ++s) {
+        op_wait(done(s & 1), s >> 1 & 1, abort, p.status, 3);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kParts; ++c)
+          if (16 * c < rows) {
+            uint32_t u[16];
+            tmem_ld16(tmem + (s & 1) * kAccCols + 16 * c + ((uint32_t)q << 21), u);
+            tmem_wait16(u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c][i] += __uint_as_float(u[i]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && s + 2 < segments) mbar_arrive(taken(s & 1));
+      }
+#pragma unroll
+      for (int c = 0; c < kParts; ++c)
+        if (16 * c < rows) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(16 * c + i) * kSplitW] = sum[c][i];
+        }
+    } else {
+      op_wait(done(0), 0, abort, p.status, 3);
+      tc_fence_after();
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t u[16];
+        tmem_ld16(tmem + c + ((uint32_t)q << 21), u);
+        tmem_wait16(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mine[(c + i) * kSplitW] = __uint_as_float(u[i]);
+      }
     }
     fence_proxy_async_smem();
     asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -195,25 +247,27 @@ cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
   // 64 rows a tile while every tile has an SM, else 128: of twice as many rows a CTA hands on twice the sums (128 rows, 4096 -> 2048:
   // 11.2 us with 128, 9.0 with 64; 1024 rows 21 and 32)
   p.w_tiles = (p.n + kSplitW - 1) / kSplitW;
-  const int most = (p.m + 63) / 64 * p.w_tiles <= sms ? 64 : 128, r_tiles = (p.m + most - 1) / most;
+  const int most = (p.m + 63) / 64 * p.w_tiles <= sms ? 64 : kSplitRows, r_tiles = (p.m + most - 1) / most;
   p.rows = ((p.m + r_tiles - 1) / r_tiles + 15) / 16 * 16;
   p.box = p.rows;
   p.r_tiles = (p.m + p.rows - 1) / p.rows;
   p.chunks = (p.k + kSplitK - 1) / kSplitK;
   // as many slices as keep all clusters on the GPU at once (16 tiles in 8 slices: 18 us, 15 clusters of 8 fit; in 6: 10.4, at 128 rows a tile)
-  static std::atomic<unsigned long long> done{0}, done_wide{0};
-  cudaError_t e = allow_smem(split_kernel<false>, kSplitSmem, done);
-  if (e == cudaSuccess) e = allow_smem(split_kernel<true>, kSplitSmem, done_wide);
+  static std::atomic<unsigned long long> done{0}, done_wide{0}, done_long{0};
+  cudaError_t e = allow_smem(split_kernel<false, false>, kSplitSmem, done);
+  if (e == cudaSuccess) e = allow_smem(split_kernel<true, false>, kSplitSmem, done_wide);
+  if (e == cudaSuccess) e = allow_smem(split_kernel<true, true>, kSplitSmem, done_long);
   static std::atomic<int> known[8][64];
   for (p.slices = std::min(8, p.chunks); e == cudaSuccess && p.slices > 1; --p.slices) {
     int n = 0;
-    e = active_clusters(split_kernel<false>, p.slices, kSplitThreads, kSplitSmem, known[p.slices - 1], &n);
+    e = active_clusters(split_kernel<false, false>, p.slices, kSplitThreads, kSplitSmem, known[p.slices - 1], &n);
     if (p.w_tiles * p.r_tiles <= n) break;
   }
-  p.tmem_cols = 32;
-  while (p.tmem_cols < p.box) p.tmem_cols *= 2;
   const int own = (p.box + p.slices - 1) / p.slices, sums = p.slices * own * kSplitW * 4, stage = kSplitBytesW + p.box * kSplitK * 2;
   const int per = (p.chunks + p.slices - 1) / p.slices;
+  p.long_sums = p.epi.out_float && per > kSegment;
+  p.tmem_cols = p.long_sums ? 2 * kAccCols : 32;
+  while (p.tmem_cols < p.box) p.tmem_cols *= 2;
   p.stages = std::min({kSplitStages, per, (kSplitSmem - 1024 - sums) / stage});
   p.ring = std::max(p.stages * stage, p.slices > 1 ? sums : 0);  // (the sums leave from where the stages were)
   p.smem = 1024 + p.ring + sums;
@@ -222,8 +276,8 @@ cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
 
 cudaError_t launch_linear_split(const SplitParams& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
   const dim3 grid((unsigned)(p.w_tiles * p.r_tiles * p.slices));
-  return p.epi.out_float ? launch_clusters(split_kernel<true>, grid, p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw)
-                         : launch_clusters(split_kernel<false>, grid, p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw);
+  const auto launch = [&](auto* kernel) { return launch_clusters(kernel, grid, p.slices, kSplitThreads, (size_t)p.smem, st, p, tx, tw); };
+  return p.long_sums ? launch(split_kernel<true, true>) : p.epi.out_float ? launch(split_kernel<true, false>) : launch(split_kernel<false, false>);
 }
 
 }  // namespace mk

@@ -186,6 +186,7 @@ struct SplitParams {
   // from split_shape: row tiles of `rows` (a multiple of 16, also the copies' height), outputs' tiles, columns' chunks of 64 and how
   // many slices they are cut into
   int rows, box, w_tiles, r_tiles, chunks, slices, stages, tmem_cols, ring, smem;
+  int long_sums;  // float32 results of more than 512 columns a slice
 };
 cudaError_t split_shape(SplitParams& p, int sms, bool* fits);
 cudaError_t launch_linear_split(const SplitParams& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st);

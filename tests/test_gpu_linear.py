@@ -184,3 +184,16 @@ def test_activations_at_the_ends_of_the_range(m, act, wide):
     step = 2.0 ** -24 if wide else 2.0 ** -8
     # (a value below the smallest normal one may be zero)
     assert ((got[rest] - want[rest]).abs() <= want[rest].abs() * (step + rel) + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1024, 2048, 4096), (512, 2048, 4096), (1000, 1500, 4104), (1024, 2048, 16384), (130, 250, 16384), (1, 700, 16384),
+                                   (9, 2048, 24576), (40, 100, 1024), (72, 30000, 4096)])
+def test_long_sums_of_float32_results(m, n, k):
+    """In the 2-norm, whatever the length and whichever kernel has the product: the products' accumulator drops what lies below its last
+    bit, half a step (2^-24) of the sum so far in the mean, at every 16 columns.  Segments of 512 columns (32 additions, of sums that are
+    two thirds of the last one in the mean, mantissas 0.7 of a step) make that 9e-7 at most; joining them adds 2^-25 each, at random."""
+    g = R.gen(k + m)
+    x, w = R.bf16(g, m, k), R.bf16(g, n, k, std=k ** -0.5)
+    got = ops.linear(x, w, dtype=torch.float32).double()
+    want = x.double() @ w.double().T
+    assert float((got - want).norm() / want.norm()) <= 1e-6
