@@ -342,6 +342,29 @@ template <int N>
 using Number = std::integral_constant<int, N>;
 __device__ __forceinline__ float moe_silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
+// w . h by a warp (the same in every lane), h in its two parts.  For results that are not finite, one at a time: the tiles multiply rows
+// of tokens that have not selected an expert, which are zeros, with its weights, and both parts of h, of which one may be zero, and zero
+// times infinity is a NaN that the formula does not have.  (What is a NaN stays one: no need to go on.)
+__device__ __noinline__ float plain_product(const uint16_t* w, const uint16_t* h, const uint16_t* rest, int f) {
+  float y = 0.f;
+  for (int i0 = 0; i0 < f; i0 += 256) {
+    const int i = i0 + 8 * (threadIdx.x & 31);
+    if (i < f) {
+      const uint4 a = op_ld16(w + i), b = op_ld16(h + i), c = op_ld16(rest + i);
+      const uint32_t a4[4] = {a.x, a.y, a.z, a.w}, b4[4] = {b.x, b.y, b.z, b.w}, c4[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = bf16x2_to_f2(a4[k]), u = bf16x2_to_f2(b4[k]), v = bf16x2_to_f2(c4[k]);
+        y = fmaf(x.y, u.y + v.y, fmaf(x.x, u.x + v.x, y));
+      }
+    }
+    if (__any_sync(0xffffffffu, y != y)) return NAN;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+  return y;
+}
+
 // Up to 8 tokens.  A tile's rows are the tokens, all of them for every expert, with zeros in h for those that have not selected it: x
 // is laid out once, and the second product adds its experts up in registers.  h is kept as a sum of two bf16 values: rounded to one, it
 // would be off by as much as the result's own rounding (outputs 1.41 times as far off in the 2-norm).  Up to 4 tokens the second
@@ -617,14 +640,26 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     red[warp * 32 + lane] = make_float4(total(0), total(1), total(2), total(3));
     __syncthreads();
     // the warps' parts, in their order
+    float y = 0.f;
     if (mine) {
       const int from = (c & 7) * 4 + (t >> 1), part = (t & 1) + 2 * (c >> 3);
-      float y = 0.f;
 #pragma unroll
       for (int w = 0; w < kLayerWarps; ++w) {
         y += reinterpret_cast<const float*>(red + w * 32 + from)[part];
         if (GROUPS == 1) y += reinterpret_cast<const float*>(red + w * 32 + from + kRest / 2)[part];
       }
+    }
+    for (unsigned odd = __ballot_sync(0xffffffffu, !(fabsf(y) < INFINITY)); odd; odd &= odd - 1) {  // the token's own experts alone
+      const int i = 32 * warp + __ffs(odd) - 1, ti = i >> 4, ci = c0 + (i & 15);
+      float z = 0.f;
+      for (int a = 0; a < A && z == z; ++a)
+        if (!(weight[a * 8 + ti] < 0.f)) {
+          const uint16_t* const h = p.h + (long long)(a * (8 * GROUPS) + ti) * f;
+          z += plain_product(static_cast<const uint16_t*>(p.a.w_down) + ((long long)sh.act[a] * d + ci) * f, h, h + (long long)kRest * f, f);
+        }
+      if (tid == i) y = z;
+    }
+    if (mine) {
       if (residual) y += ahead_y;
       static_cast<uint16_t*>(p.a.out)[t * p.a.out_stride + c0 + c] = to_bf16(y);
     }
@@ -694,26 +729,55 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   }
 }
 
+// The four sums of every lane in `odd` once more, from the rows of h (a cold path, so that it takes no registers of the other).
+__device__ __noinline__ float4 plain_sums(const MoeParams& p, int t, int c, unsigned odd, float4 y) {
+  const int K = p.a.top_k, d = p.a.d_model, f = p.a.d_ff;
+  for (; odd; odd &= odd - 1) {
+    const int from = __ffs(odd) - 1, c0 = __shfl_sync(0xffffffffu, c, from);
+    float v[4];
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float z = 0.f;
+      for (int j = 0; j < K && z == z; ++j) {
+        const uint16_t* const h = p.h + (long long)op_ld(p.places + t * K + j) * (2 * f);
+        const uint16_t* const w = static_cast<const uint16_t*>(p.a.w_down) + ((long long)op_ld(p.ids + t * K + j) * d + c0 + i) * f;
+        z = fmaf(op_ldf(p.weights + t * K + j), plain_product(w, h, h + f, f), z);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i == k) v[k] = z;
+    }
+    if ((threadIdx.x & 31) == from) y = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  return y;
+}
+
 // out[t] = residual[t] + sum_j c_j y[place of (t, j)], four columns a thread
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ MoeParams p) {
   const int t = blockIdx.x, c = 4 * (blockIdx.y * kSumThreads + threadIdx.x), K = p.a.top_k, d = p.a.d_model;
   pdl_wait();
   pdl_trigger();
-  if (c >= d) return;
   LinearEpi epi{};
   epi.residual = static_cast<const uint16_t*>(p.a.residual);
   epi.residual_stride = p.a.residual_stride;
   epi.vec = p.vec;
   const uint2 ahead = linear_residual(epi, t, c, d - c);
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < d) {
 #pragma unroll 4
-  for (int j = 0; j < K; ++j) {
-    const float w = op_ldf(p.weights + t * K + j);
-    const uint4 u = op_ld16(p.y + (long long)op_ld(p.places + t * K + j) * d + c);
-    y.x = fmaf(w, __uint_as_float(u.x), y.x), y.y = fmaf(w, __uint_as_float(u.y), y.y);
-    y.z = fmaf(w, __uint_as_float(u.z), y.z), y.w = fmaf(w, __uint_as_float(u.w), y.w);
+    for (int j = 0; j < K; ++j) {
+      const float w = op_ldf(p.weights + t * K + j);
+      const uint4 u = op_ld16(p.y + (long long)op_ld(p.places + t * K + j) * d + c);
+      v[0] = fmaf(w, __uint_as_float(u.x), v[0]), v[1] = fmaf(w, __uint_as_float(u.y), v[1]);
+      v[2] = fmaf(w, __uint_as_float(u.z), v[2]), v[3] = fmaf(w, __uint_as_float(u.w), v[3]);
+    }
   }
-  const float v[4] = {y.x, y.y, y.z, y.w};
+  const bool fine = fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY;
+  const unsigned odd = __ballot_sync(0xffffffffu, !fine);
+  if (odd) {
+    const float4 y = plain_sums(p, t, c, odd, make_float4(v[0], v[1], v[2], v[3]));
+    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+  }
   linear_put<false>(epi, p.a.out, p.a.out_stride, v, ahead, t, c, d - c);
 }
 

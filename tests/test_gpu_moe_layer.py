@@ -242,3 +242,24 @@ def test_one_rounding_of_the_result(t, e, k, d, f):
     want = M.moe(x, router, gate, up, down, k)[0]
     rounding = (want.to(torch.bfloat16).double() - want).norm()
     assert float((got - want).norm()) <= float(rounding + 2.0 ** -12 * want.norm())
+
+
+@pytest.mark.parametrize("t", [1, 2, 4, 5, 8, 9, 40, 200])
+@pytest.mark.parametrize("e,k,d,f", [(8, 2, 256, 128), (20, 3, 72, 200)])
+def test_weights_that_are_not_finite_stay_with_the_tokens_that_chose_them(t, e, k, d, f):
+    """Infinities and a NaN in the second matrix of some experts: the outputs of tokens that have not selected those are as ever, those of
+    the others what the formula gives."""
+    g = R.gen(30 + t)
+    x, (router, gate, up, down) = R.bf16(g, t, d), weights(g, e, d, f)
+    router[2], router[1] = 0.5 * router[2], 0.0
+    down[1, 3, 5], down[1, 60, 9] = float("inf"), float("nan")
+    down[2, 7, f - 1], down[2, 8] = -float("inf"), float("inf")
+    down[4, 7, 0] = float("inf")
+    r = R.bf16(g, t, d)
+    got_ids = torch.zeros(t, k, dtype=torch.int32, device="cuda")
+    for res in (None, r):
+        want, bound, ids, _ = M.moe(x, router, gate, up, down, k, res)
+        y = ops.moe_layer(x, router, gate, up, down, k, residual=res, ids=got_ids)
+        assert torch.equal(got_ids.long(), ids)
+        R.assert_close(y, want, bound, f"{t} tokens")
+        assert torch.equal(y.view(torch.int16), ops.moe_layer(x, router, gate, up, down, k, residual=res).view(torch.int16))
