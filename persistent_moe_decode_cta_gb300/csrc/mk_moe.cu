@@ -202,13 +202,15 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kRouterThreads) r
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (!mine_to_select) return;
   // A lane adds d / 64 terms (up to 4 more of a step that is not whole) to each of two sums, and 6 additions join them: each is off
-  // by 2^-24 of what it adds to at most, |w| |x| in all at most; 1.001 and 2^-120 cover the norms' own roundings and denormals.
+  // by 2^-24 of what it adds to at most, |w| |x| in all at most.  Squares below the least float are lost from the norms, each of up to
+  // 8192 by 2^-149 at most: kLost; 1.001 covers the norms' roundings, 2^-120 what the products lose in the same way.
+  constexpr float kLost = 0x1p-136f;
   float xn = 0.f;
 #pragma unroll
   for (int i = 0; i < kRouterWarps; ++i) xn += sh.xn[i];
-  const float unit = (d / 64 + 12) * 0x1p-24f * 1.001f * sqrtf(xn);
+  const float unit = (d / 64 + 12) * 0x1p-24f * 1.001f * sqrtf(xn + kLost);
   if (tid < kOpMaxExperts) {
-    const float off = tid < E ? unit * sqrtf(sh.score[tid].y) + 0x1p-120f : 0.f;
+    const float off = tid < E ? unit * sqrtf(sh.score[tid].y + kLost) + 0x1p-120f : 0.f;
     if (tid < E) sh.score[tid].y = off;
     const int most = __reduce_max_sync(0xffffffffu, __float_as_int(off));  // (not negative: in the order of the bits)
     if (MANY) {

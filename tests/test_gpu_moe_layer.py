@@ -263,3 +263,24 @@ def test_weights_that_are_not_finite_stay_with_the_tokens_that_chose_them(t, e, 
         assert torch.equal(got_ids.long(), ids)
         R.assert_close(y, want, bound, f"{t} tokens")
         assert torch.equal(y.view(torch.int16), ops.moe_layer(x, router, gate, up, down, k, residual=res).view(torch.int16))
+
+
+@pytest.mark.parametrize("e,k,d", [(8, 2, 512), (60, 4, 1024), (100, 8, 2048), (256, 16, 512)])
+@pytest.mark.parametrize("x_size,router_size", [(0, 0), (-76, 0), (-76, 13), (-100, 10), (0, -76), (13, -90), (-60, -50)])
+def test_equal_scores_of_any_size(e, k, d, x_size, router_size):
+    """Rows of the router that are one another's permutations and tokens of equal values: all scores are equal, sums in fp32 are not, however
+    small the squares of what they are sums of.  Ties go to the lowest experts."""
+    g = R.gen(40)
+    line = torch.randn(d, generator=g, device="cuda") * 2.0 ** torch.randint(-10, 11, (d,), generator=g, device="cuda")
+    line = torch.where(line.abs() < 2.0 ** -10, 1.0, line)            # (sums of 32 bits or so, no term below 2^-120)
+    order = torch.rand(e, d, generator=g, device="cuda").argsort(-1)
+    router = (line.to(torch.bfloat16).float()[order] * 2.0 ** router_size).to(torch.bfloat16)
+    x = torch.full((5, d), 2.0 ** x_size, dtype=torch.bfloat16, device="cuda")
+    x[1] *= -1.5
+    x[3] = 0
+    _, gate, up, down = weights(g, e, d, 16)
+    ids = torch.full((5, k), -1, dtype=torch.int32, device="cuda")
+    share = torch.zeros(5, k, device="cuda")
+    ops.moe_layer(x, router, gate, up, down, k, ids=ids, weights=share)
+    assert torch.equal(ids, torch.arange(k, dtype=torch.int32, device="cuda").expand(5, k))
+    assert float((share - 1 / k).abs().max()) <= 2.0 ** -20 / k      # (exponentials of 0, a sum of k and a quotient)
