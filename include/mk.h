@@ -643,7 +643,7 @@ int mk_moe_layer_workspace(const mk_moe_args* args, size_t* bytes);
  *   draft_probs  float32 [batch][n_nodes][vocab], strides likewise, values in [0, 1] (others are clamped), or NULL
  *   tokens, parents  int32 [batch][n_nodes]; parents NULL: a chain.  parents[b][0] and tokens[b][0] are not read
  *   uniforms  float32 [batch][n_nodes] in [0, 1)
- *   temperature  float32 [batch], >= 0, or NULL (1)
+ *   temperature  float32 [batch], >= 0, or NULL (1); beside 0, what lies outside 1e-30..1e30 counts as the nearer end
  *   counts    int32 [batch]: nodes of each sequence, in 1..n_nodes, or NULL (n_nodes for all)
  *   accepted  int32 [batch][n_nodes]: the accepted nodes, 0 first, then -1 (mk_commit_nodes' argument)
  *   next_tokens  int32 [batch]; neither output overlaps an input

@@ -8,7 +8,8 @@
 //
 // Measured in a graph: 5 rows, 1024 -> 1536 3.3 us, 128 rows, 4096 -> 2048 with a residual 7.8 us (of them weights stream for 2.5, at 7
 // TB/s; 0.6 until the first are there, 0.4 for the last products and reading the sums, 0.7 the exchange, ~1 the epilogue, the rest
-// launch, setup and the end); 2048 x 4096: 1 row 6.4 us, 64 7.9, 256 11.8, 1024 21.4.
+// launch, setup and the end); 4096 -> 2048 without: 1 row 5.8 us, 64 7.3, 256 11.0, 512 15.1, 1024 20.8, the last two in one slice: the tiles'
+// copies out of L2 bound them, 13 TB/s (with a quarter of the products 2 to 7 % less).
 #include <algorithm>
 
 #include "mk_linear.cuh"
@@ -24,8 +25,8 @@ constexpr int kSplitStages = 12;
 constexpr int kSplitBytesW = kSplitW * kSplitK * 2;
 // Stages of an accumulator of float32 results.  The products drop what lies below its last bit, so that a sum is off by more the longer it
 // is (2-norm: 512 columns 4.7e-7, 2048 2.1e-6, 16384 1.9e-5): sums of 512 columns are added up in registers, from two accumulators in
-// turn.  A kernel of its own (LONG), which it slows down (float32, 4096 -> 2048: 64 rows 6.1 -> 6.6 us, 128 7.7 ->
-// 8.3, 512 14.9 -> 17.1, 1024 20.6 -> 21.4; with the sums in shared memory 6.8, 8.3, 17.0, 21.6).
+// turn.  A kernel of its own (LONG), which it slows down (float32, 4096 -> 2048: 64 rows 7.3 -> 7.7 us, 128 8.2 ->
+// 8.7, 512 15.1 -> 17.3, 1024 20.8 -> 21.5; with the sums in shared memory the same to 1 %).
 constexpr int kSegment = 8;
 constexpr int kAccCols = 128;  // from one to the other
 
@@ -239,7 +240,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 }  // namespace
 
 // Whether the tiles of 256 outputs by 256 rows, a pair of SMs each, would leave more than half of the pairs without one; if so the
-// split of the work.  (At 128 rows, 4096 -> 2048: 20.5 us with 8 pairs.)
+// split of the work.  (us of this / of the pairs, 4096 -> 2048: 1 row 5.8 / 15.0, 128 8.2 / 15.4, 256 11.0 / 15.4, 512 15.1 / 16.2, 768
+// 20.3 / 17.3, 1024 20.8 / 17.9; 2048 -> 4096: 128 8.8 / 9.8, 256 10.3 / 10.4, 512 14.3 / 11.7; 1024 -> 1024: 128 4.9 / 6.5, 512
+// 7.0 / 6.7, 1024 7.6 / 7.4.  The rule gives up to a fifth away above 256 to 600 rows, where pairs have tiles of 64 to 128 rows.)
 cudaError_t split_shape(SplitParams& p, int sms, bool* fits) {
   const long long pairs = (long long)((p.n + 255) / 256) * ((p.m + 255) / 256);
   *fits = p.m <= 1024 && pairs * 4 <= sms;

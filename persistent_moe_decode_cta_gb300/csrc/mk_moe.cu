@@ -16,8 +16,8 @@
 // in turn; their sums meet at the end, in the order of the warps, and no partial results leave the CTA.
 //
 // Measured in a graph (2048 wide, 128 experts of 768, 8 a token): 1 token 23.9 us (76 MB; a chain: router 4, start and list 2.5, the
-// first product 8, handover 2, the second 4, the rest launches), 4 55.8, 8 93.5 (5.2 TB/s), 16 145, 128 219 us (router 9, sort 3,
-// products 124 and 70, sum 5; 5.5 TB/s); 32 experts of 1024 x 512, 4 a token: 1 token 12.5 us.
+// first product 8, handover 2, the second 4, the rest launches), 4 55.8, 8 90 (5.4 TB/s), 16 142, 128 217 us (router 9, sort 3,
+// products 124 and 70, sum 5; 5.6 TB/s); 32 experts of 1024 x 512, 4 a token: 1 token 12.5 us, 8 26, 9 35, 64 40.
 #include <algorithm>
 #include <type_traits>
 
@@ -826,7 +826,7 @@ cudaError_t launch_layer(const MoeParams& p, const MoeMaps& m, cudaStream_t st) 
 // Groups of eight rows of h for a kernel of few tokens, 0: the products of mk_experts.cu.  Up to 8 tokens the one kernel, whose tiles
 // waste the fewest products (2048 wide, 128 experts of 768, 8 a token; us of the one kernel / sort, products and sum: 1 token 23.9 / 34.8,
 // 4 55.8 / 71.5, 5 73.2 / 75.2, 8 93.5 / 100.1, 16, with 32 rows of h, 167 / 146; of 32 experts of 1024 x 512 1 12.5 / 22.3, 5
-// 23.0 / 28.2, 8 25.4 / 33.5).
+// 23.0 / 28.2, 8 25.4 / 33.5; 9 to 16 of those in one kernel have not been measured, in several 9 take 34.9, 16 37.2).
 int moe_groups(const mk_moe_args& a) {
   const int groups = a.n_tokens <= 4 ? 1 : a.n_tokens <= kMoeFew ? 2 : 0;
   return groups && a.n_tokens * a.top_k <= kLayerThreads && layer_slots(a, groups) >= 3 ? groups : 0;
