@@ -350,8 +350,8 @@ __device__ __forceinline__ bool try_wait_sums(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// As op_wait: of a whole warp, given up after a time.  (The CTA then goes on with wrong sums, without further waits, and its call has
-// an error recorded.)
+// As op_wait: of a whole warp, given up after a time.  (The CTA then goes on with wrong sums, without further waits and without sending
+// its own, so that the others give up too, and its call has an error recorded.)
 __device__ __noinline__ void wait_sums(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const uint64_t t0 = gtime();
   while (!__all_sync(0xffffffffu, try_wait_sums(bar, parity))) {
@@ -468,7 +468,7 @@ __device__ __forceinline__ unsigned long long exchange(WalkShared& sh, unsigned 
   const uint32_t ctas = cta_count(), set = *turn & 1, bar = smem_u32(&sh.bars[set]);
   if (lane == 0) sh.warp_sum[set][warp] = warp_sum;
   __syncthreads();
-  if (threadIdx.x < ctas) {
+  if (threadIdx.x < ctas && !*static_cast<volatile int*>(&sh.abort)) {  // (one that gave up a wait may walk on when the others have left)
     unsigned long long mine = 0;
 #pragma unroll
     for (int i = 0; i < kWalkWarps; ++i) mine = LARGEST ? max(mine, sh.warp_sum[set][i]) : mine + sh.warp_sum[set][i];

@@ -45,3 +45,13 @@ def test_launches_ask_the_device_for_its_sms(name):
 @pytest.mark.parametrize("name", NAMES + ["mk_linear.cuh"])
 def test_global_memory_is_not_read_through_the_read_only_path(name):
     assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", T.source(name))
+
+
+def test_a_cta_that_gave_up_a_wait_sends_no_more():
+    """The other CTAs of a walk leave once they have had all that was sent for their own passes: one whose sums are wrong may walk longer than
+    they do, and must not write to where they were."""
+    text = T.source("mk_verify.cu")
+    exchange = T.body(text, text.index("exchange(WalkShared& sh"))
+    sends = [exchange[:m.start()] for m in re.finditer(r"\bput_async\s*\(", exchange)]
+    assert len(sends) == 1 and len(re.findall(r"\bput_async\s*\(", text)) == 2      # (the function and its one call)
+    assert re.search(r"if\s*\([^{;]*!\s*[^{;]*\bsh\.abort[^{;]*\)\s*\{[^}]*$", sends[0]), "sent whether a wait was given up or not"
