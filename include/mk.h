@@ -604,9 +604,10 @@ int mk_linear(const mk_linear_args* args, void* stream);
  *   workspace mk_moe_layer_workspace(..) bytes, 16-byte aligned, not shared with a call that may run at
  *             the same time; its contents do not matter
  * The selection is that of the formula: scores that fp32 sums do not tell apart are computed to 2^-46 of the sum of their
- * terms' sizes (or 2^-136: a term below 2^-133 loses bits).  A NaN score counts as the largest.  The product of gate and up (times c, up to 8 tokens) is kept as a sum of two bf16
- * values, to 2^-17 of itself, everything else is fp32 until the one rounding of out.  A weight or token that is infinite or NaN reaches
- * the outputs of the tokens that have selected the expert, or of the token, alone.  The sums have a fixed order: equal calls give equal bits.
+ * terms' sizes (or 2^-136: a term below 2^-133 loses bits).  A NaN score counts as the largest.  The product of gate and up
+ * (times c, up to 8 tokens) is kept as a sum of two bf16 values, to 2^-17 of itself, everything else is fp32 until the one
+ * rounding of out.  A weight or token that is infinite or NaN reaches the outputs of the tokens that have selected the expert,
+ * or of the token, alone.  The sums have a fixed order: equal calls give equal bits.
  * n_experts in 1..256, top_k in 1..min(16, n_experts), d_model up to 8192, d_ff up to 65536. */
 typedef struct mk_moe_args {
   const void* x;
